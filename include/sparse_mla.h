@@ -318,13 +318,251 @@ SMLA_API smla_status sparse_mla_fwd_no_alloc(const void *q, const void *kv_cache
                                              smla_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The serving step around the forward: page maps, rotary tables and rotations,
+ * a block-scaled 8-bit cache and attention over it. The pool is paged as for
+ * the forward: block `j` of a request holds its tokens [j * block_size,
+ * (j + 1) * block_size), block_table[b, j] names the pool block, and a slot is
+ * block * block_size + offset. block_size is 16, 32, 64 or 128 here.
+ * ---------------------------------------------------------------------------
+ *
+ * Block tables and slot maps of one step, from the requests' lengths, on the
+ * device. With need_b = ceil(max(seq_lens[b], 0) / block_size):
+ *   - request b takes max(0, need_b - held_b) new blocks and gives back
+ *     max(0, held_b - need_b) (all of them when it has ended: seq_lens[b] = 0);
+ *   - free blocks are a ring: free_ring[(head + i) % ring_size], i < count, with
+ *     (head, count) = ring_state. The batch's k-th new block (requests in
+ *     order, then blocks in order) is the ring's k-th; given-back blocks (in
+ *     the same order) go behind its end, for later calls;
+ *   - token i of request b's query_lens[b] new tokens (clamped to
+ *     [0, seq_lens[b]]; its last ones) is flat token query_start[b] + i, at
+ *     position p = seq_lens[b] - query_lens[b] + i, with slot
+ *     block_table[b, p / block_size] * block_size + p % block_size.
+ * If a request needs more than table_width blocks, or the ring holds fewer than
+ * the batch needs, nothing is taken or given back (tables, ring, held counts
+ * and ring state keep their values), counts[3] is the number of blocks lacking
+ * and tokens in blocks not held get slot -1: the caller can free requests and
+ * call again.
+ *
+ * seq_lens, query_lens   device, int32 [B].
+ * blocks_held            device, int32 [B]: blocks each request has in its row.
+ * blocks_held_out        device, int32 [B], written; may be blocks_held.
+ * block_table            device, int32 [B, table_width], row stride
+ *                        table_stride; entries [held, need) of a row written.
+ *                        Entries past a row's blocks keep what they hold.
+ * free_ring              device, int32 [ring_size], ring_size >= every block of
+ *                        the pool (so that what is taken and what is given back
+ *                        never meet); entries behind the ring's end written.
+ * ring_state             device, int32 [2] (head, count).
+ * ring_state_out         device, int32 [2], written; may be ring_state.
+ * query_start            device, int32 [B + 1], written: exclusive sums.
+ * positions              device, int64 [num_tokens], written (0 past the last
+ *                        token: a padded step's rows stay valid positions).
+ * slot_mapping           device, int64 [num_tokens], written (-1 past it).
+ * token_request          device, int32 [num_tokens] or NULL, written (-1 past it).
+ * counts                 device, int32 [4], written: tokens, blocks taken, given
+ *                        back, lacking (each at most 2^31 - 1).
+ * workspace              device, smla_build_block_tables_workspace_size(B)
+ *                        bytes, 16-byte aligned; need not be initialised.
+ *                        Calls that overlap in time must not share it.
+ */
+SMLA_API size_t smla_build_block_tables_workspace_size(int B);
+SMLA_API smla_status smla_build_block_tables(const int32_t *seq_lens, const int32_t *query_lens,
+                                             const int32_t *blocks_held, int32_t *blocks_held_out, int B,
+                                             int block_size, int32_t *block_table, int64_t table_stride,
+                                             int table_width, int32_t *free_ring, int ring_size,
+                                             const int32_t *ring_state, int32_t *ring_state_out,
+                                             int32_t *query_start, int64_t *positions, int64_t *slot_mapping,
+                                             int32_t *token_request, int64_t num_tokens, int32_t *counts,
+                                             void *workspace, size_t workspace_bytes, smla_stream_t stream);
+
+/* How smla_rope_cos_sin_cache scales the frequencies base^(-2i / rot_dim) for
+ * contexts longer than those a model was trained on:
+ *   LINEAR : divided by factor (positions interpolated).
+ *   NTK    : base replaced by base * factor^(rot_dim / (rot_dim - 2)).
+ *   YARN   : pairs that turn more than beta_fast times over
+ *            original_max_position stay, those that turn less than beta_slow
+ *            times are divided by factor, a linear ramp over the pair index
+ *            between: with c(n) = rot_dim ln(original_max_position / (2 pi n)) /
+ *            (2 ln base), lo = max(floor(c(beta_fast)), 0), hi =
+ *            min(ceil(c(beta_slow)), rot_dim - 1), the ramp of pair i is
+ *            clamp((i - lo) / max(hi - lo, 0.001), 0, 1). */
+typedef enum {
+    SMLA_ROPE_NONE = 0,
+    SMLA_ROPE_LINEAR = 1,
+    SMLA_ROPE_NTK = 2,
+    SMLA_ROPE_YARN = 3
+} smla_rope_scaling;
+
+/*
+ * The rotary table that smla_rope and smla_fused_qk_rope_cache read: row r
+ * holds, for position p = first_position + r and pairs i < n = rot_dim / 2,
+ * m cos(p f_i) in column i and m sin(p f_i) in column n + i, in binary32. The
+ * angle is carried as a 64-bit fraction of a turn, so it is as exact at
+ * position 2^31 as at 1 (the frequencies are rounded to binary64 once).
+ *
+ * table              device, float [num_positions, rot_dim], 4-byte aligned, written.
+ * num_positions, first_position  >= 0, first_position + num_positions <= 2^31.
+ * rot_dim            even, 2..256 (NTK: at least 4).
+ * base               > 1 and finite.
+ * scaling            smla_rope_scaling; factor >= 1 (ignored for NONE);
+ *                    original_max_position >= 1, beta_fast > beta_slow > 0 (YARN).
+ * attention_factor   m; 0 = the scaling's own: 0.1 ln(factor) + 1 for YARN, else 1.
+ */
+SMLA_API smla_status smla_rope_cos_sin_cache(float *table, int64_t num_positions, int64_t first_position,
+                                             int rot_dim, double base, int scaling, double factor,
+                                             int64_t original_max_position, double beta_fast, double beta_slow,
+                                             double attention_factor, smla_stream_t stream);
+
+/* Element type of smla_rope's tensors. */
+typedef enum {
+    SMLA_BF16 = 0,
+    SMLA_F16 = 1,
+    SMLA_F32 = 2
+} smla_dtype;
+
+/*
+ * Rotary positions on part of each head, for a query and (optionally) a key
+ * tensor in one launch. For token t, head h, p = positions[t] and pairs
+ * i < n = rot_dim / 2 of the columns [rot_offset, rot_offset + rot_dim):
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * pair i being elements (i, n + i) (is_neox != 0) or (2i, 2i + 1), cos and sin
+ * from row p of cos_sin_cache. In binary32, each product and the difference or
+ * sum rounded (as smla_fused_qk_rope_cache), then rounded once to the type.
+ * inverse != 0 turns by the opposite angle: the transpose, which is also the
+ * gradient of the forward rotation. Other columns are copied.
+ *
+ * q, k            device, [T, H, D] and [T, H_k, D] of `dtype`, element strides
+ *                 (t, h), last dimension contiguous. k (and k_out) NULL with
+ *                 H_k = 0: q alone.
+ * q_out, k_out    device, the same shapes, strides of their own. An output may
+ *                 be its input (then with the same strides: rotated in place);
+ *                 otherwise it must not overlap an input.
+ * positions       device, int64 [T].
+ * cos_sin_cache   device, float [max_position, rot_dim], 4-byte aligned.
+ * rot_dim even, 2..256, rot_offset >= 0, rot_offset + rot_dim <= D <= 65536.
+ * A token whose position is outside [0, max_position) is not written and sets
+ * bit 4 of smla_device_error.
+ */
+typedef struct smla_rope_params {
+    size_t size; /* sizeof(smla_rope_params) */
+    int dtype;
+    const void *q;
+    int64_t q_stride_t, q_stride_h;
+    void *q_out;
+    int64_t q_out_stride_t, q_out_stride_h;
+    const void *k;
+    int64_t k_stride_t, k_stride_h;
+    void *k_out;
+    int64_t k_out_stride_t, k_out_stride_h;
+    const int64_t *positions;
+    const float *cos_sin_cache;
+    int64_t max_position;
+    int T, H, H_k, D, rot_dim, rot_offset, is_neox, inverse;
+    smla_stream_t stream;
+} smla_rope_params;
+
+SMLA_API smla_status smla_rope(const smla_rope_params *params);
+
+/*
+ * The block-scaled 8-bit cache: keys and values of H_kv heads in two pools
+ * k_cache, v_cache, uint8 [num_blocks, H_kv, block_size, D] of E4M3 codes, each
+ * (block, head) with its own scale in k_scale, v_scale, float [num_blocks,
+ * H_kv]: value = code * scale.
+ *
+ * smla_kv8_append writes the rows of T new tokens at their slots. A run is a
+ * maximal stretch of consecutive tokens t whose slots lie in one block. For each
+ * run, head and cache, with amax the largest finite |x| of the run's rows there
+ * and s_new = max(amax / 448, 2^-60) (1.0 if amax is 0), in binary32:
+ *   - if the run's smallest offset o is above 0, the block holds o older tokens:
+ *     scale = max(old scale, s_new), and when it grew their codes become
+ *     E4M3_RNE(code * old / scale); otherwise scale = s_new;
+ *   - the run's codes are E4M3_RNE_satfinite(x / scale) (infinities saturate,
+ *     NaN is the NaN code).
+ * A negative slot skips its token (and ends a run); a slot >= num_blocks *
+ * block_size writes nothing and sets bit 8 of smla_device_error. The new tokens
+ * of a block must be one run with distinct slots (as smla_build_block_tables
+ * lays them out): two runs of one call in one block race on its scale.
+ *
+ * k, v          device, bf16 [T, H_kv, D], element strides (t, h) multiples of
+ *               8, 16-byte aligned, last dimension contiguous.
+ * slot_mapping  device, int64 [T].
+ * caches 16-byte aligned, scales 4-byte aligned. D is 64 or 128.
+ */
+SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v,
+                                     int64_t v_stride_t, int64_t v_stride_h, const int64_t *slot_mapping, int T,
+                                     int H_kv, int D, int block_size, void *k_cache, void *v_cache, float *k_scale,
+                                     float *v_scale, int64_t num_blocks, smla_stream_t stream);
+
+/*
+ * Attention over the block-scaled cache, for prompts, chunks of prompts and
+ * single tokens. Request b's new tokens are the flat tokens [query_start[b],
+ * query_start[b + 1]); its token i has position p = seq_lens[b] - (its number of
+ * new tokens) + i. For query head h, which reads kv head h / (H / H_kv):
+ *   s_j  = scale * q[t, h] . K_j over the visible positions j: j <= p, j <
+ *          seq_lens[b], and j > p - window when window > 0;
+ *   out[t, h] = sum_j softmax(s)_j V_j (bf16), lse[t, h] = ln sum_j exp(s_j).
+ * With sinks, e^{sinks[h]} joins the denominator and the lse. A row that sees
+ * nothing gives out = 0 and lse = -inf (sinks[h] with sinks). Positions whose
+ * block_table entry is outside [0, num_blocks) are not read and see no one;
+ * nothing beyond seq_lens[b] is read. q keeps its bf16 values (dots in 16 bits
+ * or in two 8-bit parts of it, sums in binary32), softmax weights are rounded to
+ * binary16. The scales of one request's blocks of a head must be positive and
+ * lie within a factor of 2^100 (smla_kv8_append gives at least 2^-60).
+ *
+ * q             device, bf16 [T, H, D], element strides (t, h) multiples of 8,
+ *               16-byte aligned, last dimension contiguous; D is 64 or 128.
+ * block_table   device, int32 [B, table_width], row stride table_stride;
+ *               seq_lens above table_width * block_size are cut to that.
+ * seq_lens      device, int32 [B]. query_start device, int32 [B + 1], ascending,
+ *               within [0, T]; rows of q at or past query_start[B] are not read
+ *               and their out and lse not written.
+ * max_query_len a bound of the requests' new tokens: it chooses the kernel (a
+ *               streaming kernel that splits the requests' tokens evenly over
+ *               the SMs, or one with 128 query rows to a tile). A request with
+ *               more is still computed in full.
+ * out           device, bf16 [T, H, D] contiguous, 16-byte aligned; must not
+ *               overlap q. lse device, float [T, H] or NULL.
+ * sinks         device, float [H] or NULL, in the units of scale * q . k.
+ * workspace     device, >= smla_kv8_attn_workspace_size(...) bytes (for the
+ *               current device), 256-byte aligned, need not be initialised.
+ *               Calls that overlap in time must not share it.
+ * H a multiple of H_kv; B >= 0, T >= 0 (0: a no-op); 0 <= window.
+ */
+typedef struct smla_kv8_attn_params {
+    size_t size; /* sizeof(smla_kv8_attn_params) */
+    const void *q;
+    int64_t q_stride_t, q_stride_h;
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    int64_t num_blocks;
+    const int32_t *block_table;
+    int64_t table_stride;
+    int table_width;
+    const int32_t *seq_lens, *query_start;
+    int B, T, H, H_kv, D, block_size, max_query_len, window;
+    float scale;
+    const float *sinks;
+    void *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    smla_stream_t stream;
+} smla_kv8_attn_params;
+
+/* (size_t)-1 on invalid arguments or a failed device query. */
+SMLA_API size_t smla_kv8_attn_workspace_size(int B, int T, int H, int H_kv, int D, int max_query_len);
+SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *params);
+
+/*
  * Error word of the device-side checks (0 = none). The tcgen05 kernels wait on
  * the tensor core and on their own warps with a time limit (about 2 s); a wait
  * that gives up sets a bit here (1 = an awaited barrier never completed,
  * 2 = the copies or MMAs in flight did not drain), abandons the call's
  * arithmetic, frees its tensor memory and returns, leaving the context usable.
- * smla_fused_qk_rope_cache sets 4 for a position outside [0, max_position) and
- * 8 for a slot >= num_slots. Synchronous (copies the word from the device):
+ * smla_fused_qk_rope_cache and smla_rope set 4 for a position outside
+ * [0, max_position); smla_fused_qk_rope_cache and smla_kv8_append set 8 for a
+ * slot past the pool. Synchronous (copies the word from the device):
  * unlike every other entry point it waits for the device, since the word is
  * read on the host. reset != 0 clears it.
  */

@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -71,12 +71,34 @@ SIGNATURES = {
                                   _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int,
                                   _c.c_int, _c.c_void_p], _c.c_int),
     "smla_last_error_string": ([], _c.c_char_p),
+    "smla_build_block_tables_workspace_size": ([_c.c_int], _c.c_size_t),
+    "smla_build_block_tables": ([_c.c_void_p] * 4 + [_c.c_int, _c.c_int, _c.c_void_p, _c.c_int64, _c.c_int,
+                                _c.c_void_p, _c.c_int] + [_c.c_void_p] * 6 + [_c.c_int64, _c.c_void_p, _c.c_void_p,
+                                _c.c_size_t, _c.c_void_p], _c.c_int),
+    "smla_rope_cos_sin_cache": ([_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int, _c.c_double, _c.c_int, _c.c_double,
+                                 _c.c_int64, _c.c_double, _c.c_double, _c.c_double, _c.c_void_p], _c.c_int),
+    "smla_rope": ([_c.c_void_p], _c.c_int),
+    "smla_kv8_append": ([_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p,
+                         _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                         _c.c_int64, _c.c_void_p], _c.c_int),
+    "smla_kv8_attn_workspace_size": ([_c.c_int] * 6, _c.c_size_t),
+    "smla_kv8_attn_fwd": ([_c.c_void_p], _c.c_int),
     "sparse_mla_fwd_no_alloc": ([_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p,
                                  _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int64, _c.c_int,
                                  _c.c_float, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_int,
                                  _c.c_void_p], _c.c_int),
 }
 
+
+SMLA_BF16 = 0
+SMLA_F16 = 1
+SMLA_F32 = 2
+_DTYPE = {torch.bfloat16: SMLA_BF16, torch.float16: SMLA_F16, torch.float32: SMLA_F32}
+SMLA_ROPE_NONE = 0
+SMLA_ROPE_LINEAR = 1
+SMLA_ROPE_NTK = 2
+SMLA_ROPE_YARN = 3
+_ROPE = {"none": SMLA_ROPE_NONE, "linear": SMLA_ROPE_LINEAR, "ntk": SMLA_ROPE_NTK, "yarn": SMLA_ROPE_YARN}
 
 
 class SmlaFwdParams(ctypes.Structure):
@@ -88,6 +110,30 @@ class SmlaFwdParams(ctypes.Structure):
                 ("sinks", _c.c_void_p), ("out", _c.c_void_p), ("lse", _c.c_void_p), ("workspace", _c.c_void_p),
                 ("workspace_bytes", _c.c_size_t), ("num_splits", _c.c_int), ("stream", _c.c_void_p),
                 ("kernel", _c.c_int)]
+
+
+class SmlaRopeParams(ctypes.Structure):
+    """smla_rope_params of include/sparse_mla.h."""
+    _fields_ = [("size", _c.c_size_t), ("dtype", _c.c_int), ("q", _c.c_void_p), ("q_stride_t", _c.c_int64),
+                ("q_stride_h", _c.c_int64), ("q_out", _c.c_void_p), ("q_out_stride_t", _c.c_int64),
+                ("q_out_stride_h", _c.c_int64), ("k", _c.c_void_p), ("k_stride_t", _c.c_int64),
+                ("k_stride_h", _c.c_int64), ("k_out", _c.c_void_p), ("k_out_stride_t", _c.c_int64),
+                ("k_out_stride_h", _c.c_int64), ("positions", _c.c_void_p), ("cos_sin_cache", _c.c_void_p),
+                ("max_position", _c.c_int64), ("T", _c.c_int), ("H", _c.c_int), ("H_k", _c.c_int), ("D", _c.c_int),
+                ("rot_dim", _c.c_int), ("rot_offset", _c.c_int), ("is_neox", _c.c_int), ("inverse", _c.c_int),
+                ("stream", _c.c_void_p)]
+
+
+class SmlaKv8AttnParams(ctypes.Structure):
+    """smla_kv8_attn_params of include/sparse_mla.h."""
+    _fields_ = [("size", _c.c_size_t), ("q", _c.c_void_p), ("q_stride_t", _c.c_int64), ("q_stride_h", _c.c_int64),
+                ("k_cache", _c.c_void_p), ("v_cache", _c.c_void_p), ("k_scale", _c.c_void_p),
+                ("v_scale", _c.c_void_p), ("num_blocks", _c.c_int64), ("block_table", _c.c_void_p),
+                ("table_stride", _c.c_int64), ("table_width", _c.c_int), ("seq_lens", _c.c_void_p),
+                ("query_start", _c.c_void_p), ("B", _c.c_int), ("T", _c.c_int), ("H", _c.c_int), ("H_kv", _c.c_int),
+                ("D", _c.c_int), ("block_size", _c.c_int), ("max_query_len", _c.c_int), ("window", _c.c_int),
+                ("scale", _c.c_float), ("sinks", _c.c_void_p), ("out", _c.c_void_p), ("lse", _c.c_void_p),
+                ("workspace", _c.c_void_p), ("workspace_bytes", _c.c_size_t), ("stream", _c.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -474,3 +520,324 @@ def build_fp8_cache(kv_source: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
     slots = torch.arange(kv_source.shape[0], dtype=torch.int64, device=kv_source.device)
     smla_fp8_cache_write(kv_source, slots, scale, cache, stream=stream)
     return cache, scale
+
+
+# ---- the serving step around the forward: page maps, rotary positions, the block-scaled 8-bit cache
+
+class _Launch:
+    """Runs a call on the tensors' device and on its stream, with that stream
+    current, so that what the call allocates belongs to it. `handle` is the
+    stream's handle."""
+
+    __slots__ = ("handle", "_device", "_stream")
+
+    def __init__(self, device: torch.device, stream):
+        self._device = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self._stream = None
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self._stream = torch.cuda.stream(stream)
+            self.handle = int(stream.cuda_stream)
+        else:
+            self.handle = None
+
+    def __enter__(self):
+        if self._device is not None:
+            self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        else:
+            self.handle = int(torch.cuda.current_stream().cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._device is not None:
+            self._device.__exit__(*exc)
+
+
+def _same_device(first: torch.Tensor, **others):
+    for name, x in others.items():
+        if x is not None and x.device != first.device:
+            raise ValueError("%s is on %s, the other tensors on %s" % (name, x.device, first.device))
+
+
+def _rows(x: torch.Tensor, name: str, dtype, ndim: int):
+    """A CUDA tensor whose last dimension is contiguous (other strides free)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if x.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, x.dtype))
+    if x.dim() != ndim:
+        raise ValueError("%s must have %d dims, got shape %s" % (name, ndim, tuple(x.shape)))
+    if x.stride(-1) != 1 and x.shape[-1] > 1 and x.numel() > 0:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    if not x.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+
+
+def _out(x: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    if x is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(x, name, dtype, len(shape))
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(x.shape)))
+    return x
+
+
+class BlockTables(NamedTuple):
+    """What smla_build_block_tables returns (device tensors)."""
+    query_start: torch.Tensor    # int32 [B + 1]
+    positions: torch.Tensor      # int64 [num_tokens]
+    slot_mapping: torch.Tensor   # int64 [num_tokens], -1 past the last token
+    token_request: torch.Tensor  # int32 [num_tokens], -1 past the last token
+    counts: torch.Tensor         # int32 [4]: tokens, blocks taken, blocks given back, blocks lacking
+    blocks_held: torch.Tensor    # int32 [B]
+    ring_state: torch.Tensor     # int32 [2]: head, count
+
+
+def smla_build_block_tables(seq_lens: torch.Tensor, query_lens: torch.Tensor, blocks_held: torch.Tensor,
+                            block_table: torch.Tensor, free_ring: torch.Tensor, ring_state: torch.Tensor, *,
+                            block_size: int, num_tokens: Optional[int] = None,
+                            blocks_held_out: Optional[torch.Tensor] = None,
+                            ring_state_out: Optional[torch.Tensor] = None, query_start: Optional[torch.Tensor] = None,
+                            positions: Optional[torch.Tensor] = None, slot_mapping: Optional[torch.Tensor] = None,
+                            token_request: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> BlockTables:
+    """Block tables and slot maps of one step from the requests' lengths, all on
+    the device (include/sparse_mla.h). seq_lens, query_lens, blocks_held int32
+    [B]; block_table int32 [B, width] (rows may be strided; its new entries are
+    written); free_ring int32, at least as long as the pool, and ring_state
+    int32 [2] = (head, count). blocks_held and ring_state are updated in place
+    unless *_out is given. num_tokens: entries of the token maps (taken from
+    positions when that is given; needed otherwise), those past the last token
+    padded. Nothing is taken when blocks lack: counts[3] says how many."""
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    B = seq_lens.shape[0]
+    for name, x in (("query_lens", query_lens), ("blocks_held", blocks_held)):
+        _need(x, name, torch.int32, 1)
+        if x.shape[0] != B:
+            raise ValueError("%s must be [B] = [%d]" % (name, B))
+    _rows(block_table, "block_table", torch.int32, 2)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table has %d rows, seq_lens %d" % (block_table.shape[0], B))
+    width = block_table.shape[1]
+    row_stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
+    if row_stride < width:
+        raise ValueError("block_table rows overlap")
+    _need(free_ring, "free_ring", torch.int32, 1)
+    _need(ring_state, "ring_state", torch.int32, 1)
+    if ring_state.shape[0] != 2:
+        raise ValueError("ring_state must be [2]: head, count")
+    if num_tokens is None:
+        if positions is None:
+            raise ValueError("num_tokens or positions is needed")
+        num_tokens = positions.shape[0]
+    dev = seq_lens.device
+    _same_device(seq_lens, query_lens=query_lens, blocks_held=blocks_held, block_table=block_table,
+                 free_ring=free_ring, ring_state=ring_state, blocks_held_out=blocks_held_out,
+                 ring_state_out=ring_state_out, query_start=query_start, positions=positions,
+                 slot_mapping=slot_mapping, token_request=token_request, counts=counts, workspace=workspace)
+    with _Launch(dev, stream) as on:
+        held = blocks_held if blocks_held_out is None else _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
+        state = ring_state if ring_state_out is None else _out(ring_state_out, "ring_state_out", (2,), torch.int32, dev)
+        query_start = _out(query_start, "query_start", (B + 1,), torch.int32, dev)
+        positions = _out(positions, "positions", (num_tokens,), torch.int64, dev)
+        slot_mapping = _out(slot_mapping, "slot_mapping", (num_tokens,), torch.int64, dev)
+        token_request = _out(token_request, "token_request", (num_tokens,), torch.int32, dev)
+        counts = _out(counts, "counts", (4,), torch.int32, dev)
+        if workspace is None:
+            workspace = torch.empty(int(lib().smla_build_block_tables_workspace_size(B)), dtype=torch.uint8, device=dev)
+        _check(lib().smla_build_block_tables(
+            _ptr(seq_lens), _ptr(query_lens), _ptr(blocks_held), _ptr(held), B, int(block_size), _ptr(block_table),
+            row_stride, width, _ptr(free_ring), free_ring.shape[0], _ptr(ring_state), _ptr(state), _ptr(query_start),
+            _ptr(positions), _ptr(slot_mapping), _ptr(token_request), num_tokens, _ptr(counts), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), on.handle), "smla_build_block_tables")
+    return BlockTables(query_start, positions, slot_mapping, token_request, counts, held, state)
+
+
+def smla_rope_cos_sin_cache(num_positions: int, rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
+                            factor: float = 1.0, original_max_position: int = 0, beta_fast: float = 32.0,
+                            beta_slow: float = 1.0, attention_factor: Optional[float] = None, first_position: int = 0,
+                            out: Optional[torch.Tensor] = None, device=None, stream=None) -> torch.Tensor:
+    """The rotary table [num_positions, rot_dim] (fp32: rot_dim / 2 cosines, then
+    as many sines) that smla_rope and smla_fused_qk_rope_cache (rot_dim 64) read.
+    scaling: "none", "linear", "ntk" or "yarn" (which needs
+    original_max_position); attention_factor multiplies the values (None: the
+    scaling's own)."""
+    if scaling not in _ROPE:
+        raise ValueError("scaling must be one of %s" % sorted(_ROPE))
+    if attention_factor is not None and not attention_factor > 0:
+        raise ValueError("attention_factor must be positive")
+    if out is not None:
+        _need(out, "out", torch.float32, 2)
+        if tuple(out.shape) != (num_positions, rot_dim):
+            raise ValueError("out must have shape %s, got %s" % ((num_positions, rot_dim), tuple(out.shape)))
+        dev = out.device
+    else:
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError("device must be a CUDA device")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+    with _Launch(dev, stream) as on:
+        if out is None:
+            out = torch.empty((num_positions, rot_dim), dtype=torch.float32, device=dev)
+        _check(lib().smla_rope_cos_sin_cache(_ptr(out), int(num_positions), int(first_position), int(rot_dim),
+                                             float(base), _ROPE[scaling], float(factor), int(original_max_position),
+                                             float(beta_fast), float(beta_slow), float(attention_factor or 0.0),
+                                             on.handle), "smla_rope_cos_sin_cache")
+    return out
+
+
+def smla_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, cos_sin_cache: torch.Tensor, *,
+              rot_offset: int = 0, is_neox: bool = True, inverse: bool = False, q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None,
+              stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary positions on columns [rot_offset, rot_offset + rot_dim) of each head
+    of q [T, H, D] and k [T, H_k, D] (or None), rot_dim being cos_sin_cache's
+    width; the other columns are copied. bf16, fp16 or fp32; rows may be strided.
+    Halves (is_neox) or interleaved pairs; inverse turns back (the forward
+    rotation's gradient). q_out / k_out may be q / k: rotated in place."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
+        raise TypeError("q must be a bf16, fp16 or fp32 tensor")
+    _rows(q, "q", q.dtype, 3)
+    T, H, D = q.shape
+    if k is not None:
+        _rows(k, "k", q.dtype, 3)
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("k must be [T, H_k, D] = [%d, *, %d], got %s" % (T, D, tuple(k.shape)))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _need(positions, "positions", torch.int64, 1)
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [T] = [%d]" % T)
+    _need(cos_sin_cache, "cos_sin_cache", torch.float32, 2)
+    _same_device(q, k=k, positions=positions, cos_sin_cache=cos_sin_cache, q_out=q_out, k_out=k_out)
+    with _Launch(q.device, stream) as on:
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
+        for name, x, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if x is not None:
+                _rows(x, name, q.dtype, 3)
+                if x.shape != like.shape:
+                    raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(x.shape)))
+        ks = (None, 0, 0, None, 0, 0) if k is None else (k.data_ptr(), k.stride(0), k.stride(1), k_out.data_ptr(),
+                                                         k_out.stride(0), k_out.stride(1))
+        p = SmlaRopeParams(ctypes.sizeof(SmlaRopeParams), _DTYPE[q.dtype], q.data_ptr(), q.stride(0), q.stride(1),
+                           q_out.data_ptr(), q_out.stride(0), q_out.stride(1), *ks, positions.data_ptr(),
+                           cos_sin_cache.data_ptr(), cos_sin_cache.shape[0], T, H, 0 if k is None else k.shape[1], D,
+                           cos_sin_cache.shape[1], int(rot_offset), 1 if is_neox else 0, 1 if inverse else 0,
+                           on.handle)
+        _check(lib().smla_rope(ctypes.byref(p)), "smla_rope")
+    return q_out, k_out
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
+    for name, x in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(x, torch.Tensor) or x.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError("%s must be E4M3 codes (uint8 / float8_e4m3fn)" % name)
+        _need(x, name, x.dtype, 4)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache is %s, v_cache %s" % (tuple(k_cache.shape), tuple(v_cache.shape)))
+    num_blocks, H_kv, block_size, D = k_cache.shape
+    for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(x, name, torch.float32, 2)
+        if tuple(x.shape) != (num_blocks, H_kv):
+            raise ValueError("%s must be [num_blocks, H_kv] = [%d, %d]" % (name, num_blocks, H_kv))
+    return num_blocks, H_kv, block_size, D
+
+
+def smla_kv8_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, stream=None):
+    """Writes bf16 rows k, v [T, H_kv, D] (may be strided) at their slots of the
+    block-scaled cache: k_cache, v_cache [num_blocks, H_kv, block_size, D] E4M3
+    codes, k_scale, v_scale fp32 [num_blocks, H_kv]. A block's scale grows with
+    its largest value and its older codes follow. Returns (k_cache, v_cache)."""
+    num_blocks, H_kv, block_size, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    _strided(k, "k", 3)
+    _strided(v, "v", 3)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, H_kv, D) or tuple(v.shape) != (T, H_kv, D):
+        raise ValueError("k and v must be [T, %d, %d], got %s and %s" % (H_kv, D, tuple(k.shape), tuple(v.shape)))
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must be [T] = [%d]" % T)
+    _same_device(k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    with _Launch(k.device, stream) as on:
+        _check(lib().smla_kv8_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+                                     slot_mapping.data_ptr(), T, H_kv, D, block_size, k_cache.data_ptr(),
+                                     v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), num_blocks,
+                                     on.handle), "smla_kv8_append")
+    return k_cache, v_cache
+
+
+def smla_kv8_attn_workspace_size(B: int, T: int, H: int, H_kv: int, D: int, max_query_len: int) -> int:
+    n = lib().smla_kv8_attn_workspace_size(B, T, H, H_kv, D, max_query_len)
+    if n == ctypes.c_size_t(-1).value:
+        raise SmlaError(SMLA_ERR_BAD_SHAPE, "smla_kv8_attn_workspace_size")
+    return int(n)
+
+
+def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                      v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      query_start: torch.Tensor, scale: float, *, max_query_len: int, window: int = 0,
+                      sinks: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal attention of each request's last tokens over its pages of the
+    block-scaled cache: out [T, H, D] (bf16) and lse [T, H] (fp32).
+
+    q bf16 [T, H, D] (rows may be strided); the caches and scales as for
+    smla_kv8_append, H a multiple of H_kv; block_table int32 [B, width] (rows
+    may be strided); seq_lens int32 [B]; query_start int32 [B + 1] (rows of q
+    past query_start[B] are left alone); max_query_len: a bound of the requests'
+    tokens in q; window > 0: each token sees its last `window` positions; sinks
+    fp32 [H]: logits that join the denominator."""
+    num_blocks, H_kv, block_size, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    _strided(q, "q", 3)
+    T, H, Dq = q.shape
+    if Dq != D or H % H_kv != 0 or H == 0:
+        raise ValueError("q is %s, the cache has %d heads of %d columns" % (tuple(q.shape), H_kv, D))
+    _rows(block_table, "block_table", torch.int32, 2)
+    B, width = block_table.shape
+    row_stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(query_start, "query_start", torch.int32, 1)
+    if seq_lens.shape[0] != B or query_start.shape[0] != B + 1:
+        raise ValueError("seq_lens must be [B], query_start [B + 1], B = %d" % B)
+    if sinks is not None:
+        _need(sinks, "sinks", torch.float32, 1)
+        if sinks.shape[0] != H:
+            raise ValueError("sinks must be [H]")
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
+                 seq_lens=seq_lens, query_start=query_start, sinks=sinks, out=out, lse=lse, workspace=workspace)
+    with _Launch(q.device, stream) as on:
+        out = _out(out, "out", (T, H, D), torch.bfloat16, q.device)
+        if lse is not None or return_lse:
+            lse = _out(lse, "lse", (T, H), torch.float32, q.device)
+        if workspace is None:
+            # of the stream's own pool, so calls in flight and captured graphs never share one
+            workspace = torch.empty(smla_kv8_attn_workspace_size(B, T, H, H_kv, D, int(max_query_len)),
+                                    dtype=torch.uint8, device=q.device)
+        p = SmlaKv8AttnParams(ctypes.sizeof(SmlaKv8AttnParams), q.data_ptr(), q.stride(0), q.stride(1),
+                              k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                              num_blocks, block_table.data_ptr(), row_stride, width, seq_lens.data_ptr(),
+                              query_start.data_ptr(), B, T, H, H_kv, D, block_size, int(max_query_len), int(window),
+                              float(scale), _ptr(sinks), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), on.handle)
+        _check(lib().smla_kv8_attn_fwd(ctypes.byref(p)), "smla_kv8_attn_fwd")
+    return out, lse
+
+
+def new_kv8_cache(num_blocks: int, H_kv: int, block_size: int, D: int, device="cuda"):
+    """An empty block-scaled cache: (k_cache, v_cache, k_scale, v_scale)."""
+    shape = (num_blocks, H_kv, block_size, D)
+    return (torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device),
+            torch.ones((num_blocks, H_kv), dtype=torch.float32, device=device),
+            torch.ones((num_blocks, H_kv), dtype=torch.float32, device=device))

@@ -13,6 +13,13 @@ namespace {
 
 thread_local cudaError_t t_last_cuda_error = cudaSuccess;
 
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sm_count[kMaxDevices];
+
+} // namespace
+
+namespace smla {
+
 // Record a CUDA error for smla_last_error_string and map it to a status.
 smla_status cuda_status(cudaError_t e)
 {
@@ -21,9 +28,6 @@ smla_status cuda_status(cudaError_t e)
     t_last_cuda_error = e;
     return SMLA_ERR_CUDA;
 }
-
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_sm_count[kMaxDevices];
 
 // SM count of the current device (cached per device).
 cudaError_t current_sm_count(int *out)
@@ -48,6 +52,13 @@ cudaError_t current_sm_count(int *out)
     *out = n;
     return cudaSuccess;
 }
+
+} // namespace smla
+
+namespace {
+
+using smla::cuda_status;
+using smla::current_sm_count;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -243,7 +254,7 @@ SMLA_API const char *smla_status_string(int status)
     }
 }
 
-SMLA_API int smla_version(void) { return (1 << 16) | 1; }
+SMLA_API int smla_version(void) { return (1 << 16) | 2; }
 
 SMLA_API const char *smla_last_error_string(void)
 {
@@ -451,7 +462,7 @@ SMLA_API smla_status smla_device_error(int *code, int reset)
 {
     if (code == nullptr)
         return SMLA_ERR_NULL_POINTER;
-    int c16 = 0, cw = 0, cp = 0, cg = 0, cl = 0;
+    int c16 = 0, cw = 0, cp = 0, cg = 0, cl = 0, cr = 0, ca = 0;
     if (const cudaError_t e = smla::read_umma_error(&c16, reset != 0); e != cudaSuccess)
         return cuda_status(e);
     if (const cudaError_t e = smla::read_lean_error(&cl, reset != 0); e != cudaSuccess)
@@ -462,7 +473,11 @@ SMLA_API smla_status smla_device_error(int *code, int reset)
         return cuda_status(e);
     if (const cudaError_t e = smla::read_producer_error(&cp, reset != 0); e != cudaSuccess)
         return cuda_status(e);
-    *code = c16 | cw | cp | cg | cl;
+    if (const cudaError_t e = smla::read_rope_error(&cr, reset != 0); e != cudaSuccess)
+        return cuda_status(e);
+    if (const cudaError_t e = smla::read_append_error(&ca, reset != 0); e != cudaSuccess)
+        return cuda_status(e);
+    *code = c16 | cw | cp | cg | cl | cr | ca;
     return SMLA_OK;
 }
 

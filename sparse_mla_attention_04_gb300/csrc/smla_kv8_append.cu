@@ -1,0 +1,234 @@
+// The write of the block-scaled 8-bit cache (sm_103a): E4M3 codes with one
+// scale per (block, kv head), kept right as blocks fill.
+//
+// A warp takes one run (the new tokens of one block) of one head of K or V: it
+// finds the run's largest |x|, settles the block's scale, requantizes the
+// block's older codes when the scale grew, and writes the run's codes. Nothing
+// is shared between warps, so there are no atomics and no barrier. A run of up
+// to kHeld 16-byte rows a lane stays in registers between the two passes; what
+// is beyond is read again (from L2). Bound: 2 bytes read and 1 written per
+// element.
+#include "smla_device.cuh"
+#include "smla_internal.h"
+
+#include <algorithm>
+
+namespace smla {
+
+__device__ int g_append_error = 0; // bit 8: a slot out of range
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kHeld = 32;
+constexpr float kMinScale = 0x1p-60f;
+
+__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b)); // a NaN loses
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+
+// max(m, |x|) over a vector, pairwise. kFinite: infinities left out.
+template <bool kFinite>
+__device__ __forceinline__ uint32_t amax8(uint32_t m, const uint4 &v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a = w[i] & 0x7FFF7FFFu;
+        if (kFinite) {
+            if ((a & 0x7FFFu) >= 0x7F80u)
+                a &= 0x7FFF0000u;
+            if ((a >> 16) >= 0x7F80u)
+                a &= 0xFFFFu;
+        }
+        m = amax2(m, a);
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint2 quant8(const uint4 v, float s, const E4m3Recip &inv)
+{
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    const float2 f0 = __bfloat1622float2(p[0]), f1 = __bfloat1622float2(p[1]);
+    const float2 f2 = __bfloat1622float2(p[2]), f3 = __bfloat1622float2(p[3]);
+    return make_uint2(quant4_e4m3(f0.x, f0.y, f1.x, f1.y, s, inv), quant4_e4m3(f2.x, f2.y, f3.x, f3.y, s, inv));
+}
+
+// Four older codes under a grown scale: E4M3(code * old / now), each operation rounded in binary32.
+__device__ __forceinline__ uint32_t requant4(uint32_t w, float old, float now)
+{
+    uint32_t lo, hi;
+    e4m3x4_to_f16x4(w, lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const float2 qa = make_float2(__fdiv_rn(__fmul_rn(a.x, old), now), __fdiv_rn(__fmul_rn(a.y, old), now));
+    const float2 qb = make_float2(__fdiv_rn(__fmul_rn(b.x, old), now), __fdiv_rn(__fmul_rn(b.y, old), now));
+    const uint32_t ca = __nv_cvt_float2_to_fp8x2(qa, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t cb = __nv_cvt_float2_to_fp8x2(qb, __NV_SATFINITE, __NV_E4M3);
+    return (ca & 0xFFFFu) | (cb << 16);
+}
+
+__device__ __forceinline__ float warp_amax(uint32_t m)
+{
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&m));
+    return warp_max(fmaxf(f.x, f.y));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8AppendArgs a)
+{
+    constexpr int kLanes = D / 8;        // lanes of one row
+    constexpr int kRows = 32 / kLanes;   // rows of one warp-wide access
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int which = (int)(item % (2 * a.H_kv));
+    const int64_t t0 = item / (2 * a.H_kv) * a.window;
+    if (t0 >= a.T)
+        return;
+    const int h = which >> 1;
+    const bool isv = which & 1;
+    const __nv_bfloat16 *src = isv ? a.v + h * a.v_sh : a.k + h * a.k_sh;
+    const int64_t st = isv ? a.v_st : a.k_st;
+    uint8_t *cache = isv ? a.v_cache : a.k_cache;
+    float *scales = isv ? a.v_scale : a.k_scale;
+    const int bs = 1 << a.block_shift;
+    const int64_t slots = a.num_blocks << a.block_shift;
+
+    // lane l holds the block of token t0 - 1 + l: a run begins where it changes
+    int64_t blk = -1;
+    {
+        const int64_t t = t0 - 1 + lane;
+        if (lane <= a.window && t >= 0 && t < a.T) {
+            const int64_t s = a.slot_mapping[t];
+            if (s >= slots) {
+                if (which == 0 && lane > 0)
+                    atomicOr(&g_append_error, 8);
+            } else if (s >= 0) {
+                blk = s >> a.block_shift;
+            }
+        }
+    }
+    const int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
+    unsigned begins = __ballot_sync(0xffffffffu, lane > 0 && blk >= 0 && blk != before);
+    while (begins) {
+        const int l0 = __ffs(begins) - 1;
+        begins &= begins - 1;
+        const int64_t run0 = t0 - 1 + l0;
+        const int64_t block = __shfl_sync(0xffffffffu, blk, l0);
+        // the run's length and smallest offset
+        int64_t n = 0;
+        int low = bs;
+        while (true) {
+            const int64_t t = run0 + n + lane;
+            const int64_t s = t < a.T ? a.slot_mapping[t] : -1;
+            const bool in = s >= 0 && s < slots && (s >> a.block_shift) == block;
+            const unsigned out = __ballot_sync(0xffffffffu, !in);
+            const int take = out ? __ffs(out) - 1 : 32;
+            if (lane < take)
+                low = min(low, (int)(s & (bs - 1)));
+            n += take;
+            if (take < 32)
+                break;
+        }
+        low = __reduce_min_sync(0xffffffffu, low);
+
+        const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+        const __nv_bfloat16 *rows = src + run0 * st + col;
+        uint4 held[kHeld];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            if (i * kRows >= n)
+                break;
+            const int r = i * kRows + sub;
+            held[i] = r < n ? *reinterpret_cast<const uint4 *>(rows + r * st) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            if (i * kRows >= n)
+                break;
+            m = amax8<false>(m, held[i]);
+        }
+        for (int64_t r = kHeld * kRows + sub; r < n; r += kRows)
+            m = amax8<false>(m, *reinterpret_cast<const uint4 *>(rows + r * st));
+        float amax = warp_amax(m);
+        if (isinf(amax)) { // an infinity among the rows: the largest finite value counts
+            m = 0;
+            for (int64_t r = sub; r < n; r += kRows)
+                m = amax8<true>(m, *reinterpret_cast<const uint4 *>(rows + r * st));
+            amax = warp_amax(m);
+        }
+        float now = amax == 0.f ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), kMinScale);
+        uint8_t *dst = cache + (((block * a.H_kv + h) << a.block_shift)) * D;
+        float *cell = scales + block * a.H_kv + h;
+        if (low > 0) {
+            const float old = *cell;
+            if (now > old) {
+                for (int i = lane * 16; i < low * D; i += 512) {
+                    uint4 w = *reinterpret_cast<const uint4 *>(dst + i);
+                    w.x = requant4(w.x, old, now);
+                    w.y = requant4(w.y, old, now);
+                    w.z = requant4(w.z, old, now);
+                    w.w = requant4(w.w, old, now);
+                    *reinterpret_cast<uint4 *>(dst + i) = w;
+                }
+            } else {
+                now = old;
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            *cell = now;
+        const E4m3Recip inv = e4m3_recip(now);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            if (i * kRows >= n)
+                break;
+            const int r = i * kRows + sub;
+            if (r < n) {
+                const int off = (int)(a.slot_mapping[run0 + r] & (bs - 1));
+                *reinterpret_cast<uint2 *>(dst + off * D + col) = quant8(held[i], now, inv);
+            }
+        }
+        for (int64_t r = kHeld * kRows + sub; r < n; r += kRows) {
+            const int off = (int)(a.slot_mapping[run0 + r] & (bs - 1));
+            *reinterpret_cast<uint2 *>(dst + off * D + col) =
+                quant8(*reinterpret_cast<const uint4 *>(rows + r * st), now, inv);
+        }
+    }
+}
+
+} // namespace
+
+cudaError_t launch_kv8_append(const Kv8AppendArgs &args, int D, int sm_count, cudaStream_t stream)
+{
+    Kv8AppendArgs a = args;
+    // one token to a warp while that gives each SM at most 128 warps (a decode
+    // step's runs are one token long); beyond, 8 tokens: of a prompt's warps
+    // only those at a block's start have a run
+    a.window = (int64_t)a.T * a.H_kv * 2 <= (int64_t)sm_count * 128 ? 1 : 8;
+    const int64_t items = ((int64_t)a.T + a.window - 1) / a.window * a.H_kv * 2;
+    const int64_t blocks = (items + kWarps - 1) / kWarps;
+    if (blocks > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    if (D == 128)
+        kv8_append_kernel<128><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(a);
+    else
+        kv8_append_kernel<64><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t read_append_error(int *out, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_append_error, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_append_error, &zero, sizeof(int));
+    }
+    return e;
+}
+
+} // namespace smla

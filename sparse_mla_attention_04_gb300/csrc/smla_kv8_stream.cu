@@ -1,0 +1,708 @@
+// Attention over the block-scaled 8-bit cache for few query rows (decode,
+// sm_103a): every code of K and V crosses the bus once, at HBM's rate.
+//
+// The work is cut evenly, whatever the lengths: a unit is (request, chunk of
+// R = 8 kTiles query rows, kv head), its length in steps of 16 positions plus a
+// constant for its start and end; the units laid end to end are divided into
+// equal parts, one per block of a grid that fills the GPU once. A block walks
+// its part; a unit that lies in it whole is finished there, one that several
+// blocks share leaves partial sums that a second kernel (launched behind, its
+// start overlapped) joins in a fixed order. Nothing depends on the host
+// knowing the lengths, so a captured call follows them.
+//
+// In a block the four warps take a unit's steps in turn, each with its own
+// softmax state and its own asynchronous copies: nothing is waited for between
+// warps until a unit ends. Each lane copies (16-byte cp.async) just the bytes
+// it will use itself, so its part of the ring in shared memory is an extension
+// of its registers: no barrier, no bank conflict.
+//
+// Arithmetic: S^T = K Q^T and O^T = V^T P^T by warp-level m16n8k16 products in
+// binary16 with binary32 sums: the tokens (for S) and the value columns (for O)
+// fill the 16 rows, 8 query rows the columns, which wastes nothing for the 4 to
+// 16 query heads of a kv head. Codes expand to binary16 exactly. The order of
+// a product's inner index is free, so it is chosen for the loads: a lane's 16
+// bytes of a K row are four k-steps of its fragment, and its 16 bytes of four
+// V rows are its whole V^T fragment. q is scaled by a power of two so that
+// binary16 holds its bf16 values exactly down to 2^-28 of the row's largest.
+// The block scales: K's multiplies the logits, V's is folded into the exponent,
+// p' = 2^(s + log2(vs) - m), so p' <= 2^8 needs no other range, and the
+// denominator adds p' / vs. The reference m moves only when a logit passes it
+// by 8 (then p' would pass 2^8): one vote a step instead of a reduction.
+#include "smla_kv8.cuh"
+#include "smla_umma.cuh"
+
+namespace smla {
+namespace {
+
+using namespace kv8;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 4;
+constexpr int kUnitCost = 4;  // a unit's start and end, in steps
+constexpr int kMinPart = 12;  // a block's part, in steps, before more blocks share the work
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+// Bytes of the NaN code (0x7F or 0xFF) as 0x80 in the same byte.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// The units of one request and the cost of each.
+struct Units {
+    int steps; // of 16 positions
+    long long count, cost;
+};
+
+template <int R>
+__device__ __forceinline__ Units units_of(const Kv8AttnArgs &a, const Request &r)
+{
+    Units u;
+    u.steps = max(1, (r.len - r.begin + 15) >> 4);
+    u.count = (((long long)r.qlen * a.G + R - 1) / R) * a.H_kv;
+    u.cost = u.steps + kUnitCost;
+    return u;
+}
+
+template <int D, int NT> struct Layout {
+    static constexpr int R = 8 * NT;
+    static constexpr int kStageBytes = 16 * 2 * D;              // one step's K and V
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kMerge = kWarps * R * D * 4;           // the warps' value sums at a unit's end
+    static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kNanWords = R * D / 32;
+    static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 16 + kNanWords * 4;
+};
+
+// The workspace: total units; for each unit {first block, last block, request,
+// index in the request}; then a head and a tail partial of each block.
+struct Part {
+    int *header;
+    int4 *dir;
+    float2 *ml;   // [2 blocks][R]
+    float *o;     // [2 blocks][R][D]
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(const Kv8AttnArgs a, const Part part)
+{
+    using L = Layout<D, NT>;
+    constexpr int R = L::R;
+    constexpr int kH = D / 64;      // 16-byte pieces of a lane's K row
+    constexpr int kV = D / 8;       // bytes of a lane's V row
+    constexpr int kM = D / 16;      // 16-row tiles of the value columns
+    extern __shared__ __align__(16) uint8_t smem[];
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kBig);
+    float4 *s_meta = reinterpret_cast<float4 *>(smem + L::kBig + kWarps * R * 8);
+    uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 16);
+    __shared__ long long s_sum[kThreads];
+    __shared__ long long s_base;
+    __shared__ int s_b;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    umma::grid_launch_dependents();
+
+    // the total cost, and this block's part [lo, hi)
+    const int per = (a.B + kThreads - 1) / kThreads;
+    {
+        long long mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < a.B) {
+                const Units u = units_of<R>(a, request(a, b));
+                mine += u.count * u.cost;
+            }
+        }
+        s_sum[tid] = mine;
+    }
+    __syncthreads();
+    long long total = 0, before = 0;
+    for (int i = 0; i < kThreads; ++i) {
+        if (i == tid)
+            before = total;
+        total += s_sum[i];
+    }
+    const long long blocks = max(1ll, min((long long)gridDim.x, (total + kMinPart - 1) / kMinPart));
+    if (blockIdx.x == 0) { // the number of units, for the joining kernel
+        long long n = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < a.B)
+                n += units_of<R>(a, request(a, b)).count;
+        }
+        __syncthreads();
+        s_sum[tid] = n;
+        __syncthreads();
+        if (tid == 0) {
+            long long all = 0;
+            for (int i = 0; i < kThreads; ++i)
+                all += s_sum[i];
+            *part.header = (int)all;
+        }
+    }
+    if (blockIdx.x >= blocks || total == 0)
+        return;
+    const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
+    if (lo >= hi)
+        return;
+    // the request that holds cost lo: found by the thread whose requests do
+    {
+        long long mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < a.B) {
+                const Units u = units_of<R>(a, request(a, b));
+                const long long c = u.count * u.cost;
+                if (lo >= before + mine && lo < before + mine + c) {
+                    s_b = b;
+                    s_base = before + mine;
+                }
+                mine += c;
+            }
+        }
+    }
+    __syncthreads();
+    int b = s_b;
+    long long base = s_base; // cost at which request b begins
+    // units before request b: the index of its first in the directory
+    long long unit0 = 0;
+    {
+        long long n = 0;
+        for (int i = tid; i < b; i += kThreads)
+            n += units_of<R>(a, request(a, i)).count;
+        __syncthreads();
+        s_sum[tid] = n;
+        __syncthreads();
+        for (int i = 0; i < kThreads; ++i)
+            unit0 += s_sum[i];
+    }
+
+    const float scale_log2 = a.scale * kLog2e;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStageBytes;
+    float4 *meta = s_meta + warp * kStages;
+
+    long long at = lo;
+    while (at < hi) {
+        Request rq = request(a, b);
+        Units un = units_of<R>(a, rq);
+        while (at >= base + un.count * un.cost) { // requests without tokens have no units
+            base += un.count * un.cost;
+            unit0 += un.count;
+            ++b;
+            rq = request(a, b);
+            un = units_of<R>(a, rq);
+        }
+        const long long ui = (at - base) / un.cost;
+        const long long ubase = base + ui * un.cost;
+        const long long uend = min(hi, ubase + un.cost);
+        const int s0 = (int)max(0ll, at - ubase - kUnitCost), s1 = (int)max(0ll, uend - ubase - kUnitCost);
+        at = uend;
+        if (s0 >= s1)
+            continue;
+        const bool whole = s0 == 0 && s1 == un.steps;
+        if (s0 == 0 && tid == 0) {
+            // blocks that hold the unit's first and last step
+            const long long x0 = ubase + kUnitCost, x1 = ubase + un.cost - 1;
+            const int c0 = (int)(((x0 + 1) * blocks - 1) / total), c1 = (int)(((x1 + 1) * blocks - 1) / total);
+            part.dir[unit0 + ui] = make_int4(c0, c1, b, (int)ui);
+        }
+        const int h = (int)(ui % a.H_kv);
+        const int row0 = (int)(ui / a.H_kv) * R;
+        const int rows = min(R, rq.qlen * a.G - row0);
+        // the chunk's tokens and what its rows see
+        const int p_first = rq.pos(row0 / a.G), p_last = rq.pos((row0 + rows - 1) / a.G);
+        const int kv_end = min(rq.len, p_last + 1);                                    // beyond: seen by none
+        const int kv_begin = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+        const int all_from = a.window > 0 ? p_last - a.window + 1 : 0;                 // [all_from, p_first]: seen by all
+        const bool many = p_first != p_last;
+
+        // this lane's part of Q: fragment column g of each tile, and the factors of its columns 2 t4, 2 t4 + 1
+        uint32_t qf[NT][4 * kH][2];
+        float qscale[NT];
+        int pos[NT][2];
+        float cscale[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            uint4 v[kH][2];
+            float amax = 0.f;
+            const int rr = row0 + r;
+            const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(a.q) +
+                                      (int64_t)(rq.q0 + (r < rows ? rr / a.G : 0)) * a.q_st +
+                                      (int64_t)(h * a.G + (r < rows ? rr % a.G : 0)) * a.q_sh;
+#pragma unroll
+            for (int hh = 0; hh < kH; ++hh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    v[hh][e] = r < rows ? *reinterpret_cast<const uint4 *>(qr + hh * 64 + t4 * 16 + e * 8)
+                                        : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v[hh][e].x, v[hh][e].y, v[hh][e].z, v[hh][e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // q times 2^(14 - e), e the exponent of the largest: below 2^15 in binary16
+            const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
+            const float up = __uint_as_float((uint32_t)(127 + 14 - min(e, 127)) << 23);
+            qscale[nt] = __uint_as_float((uint32_t)(127 + min(e, 127) - 14) << 23);
+#pragma unroll
+            for (int hh = 0; hh < kH; ++hh)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint4 &x = v[hh][w >> 1];
+                    const uint32_t lo2 = (w & 1) ? x.z : x.x, hi2 = (w & 1) ? x.w : x.y;
+                    const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&lo2));
+                    const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi2));
+                    qf[nt][hh * 4 + w][0] = pack_f16x2(f0.x * up, f0.y * up);
+                    qf[nt][hh * 4 + w][1] = pack_f16x2(f1.x * up, f1.y * up);
+                }
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+                cscale[nt][e2] = __shfl_sync(0xffffffffu, qscale[nt], 4 * (2 * t4 + e2));
+                const int rc = nt * 8 + 2 * t4 + e2;
+                pos[nt][e2] = rc < rows ? rq.pos((row0 + rc) / a.G) : -1;
+            }
+        }
+
+        float o[kM][NT][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[i][nt][e] = 0.f;
+        }
+        if (many) {
+            for (int i = tid; i < L::kNanWords; i += kThreads)
+                s_nan[i] = 0;
+            __syncthreads();
+        }
+
+        // the lane's table entries: entry first + lane, its scales
+        const int32_t *row = a.block_table + b * a.table_stride;
+        int first = -(1 << 30);
+        int e_blk = -1;
+        float e_ks = 0.f, e_vs = 1.f;
+        const int tok_a = 4 * (g >> 1) + (g & 1); // the tokens of the lane's two K rows: tok_a, tok_a + 2
+
+        auto issue = [&](int s, int stage) {
+            if (s < s1) {
+                const int tb = rq.begin + s * 16;
+                const int e = tb >> a.block_shift;
+                if (e - first >= 32 || e < first) {
+                    first = e;
+                    const int x = e + lane;
+                    e_blk = x < a.table_width && ((long long)x << a.block_shift) < rq.len ? row[x] : -1;
+                    if (e_blk >= 0 && e_blk < a.num_blocks) {
+                        e_ks = a.k_scale[(int64_t)e_blk * a.H_kv + h];
+                        e_vs = a.v_scale[(int64_t)e_blk * a.H_kv + h];
+                    } else {
+                        e_blk = -1;
+                        e_ks = 0.f;
+                        e_vs = 1.f;
+                    }
+                }
+                const int blk = __shfl_sync(0xffffffffu, e_blk, e - first);
+                const float ks = __shfl_sync(0xffffffffu, e_ks, e - first);
+                const float vs = __shfl_sync(0xffffffffu, e_vs, e - first);
+                if (lane == 0)
+                    meta[stage] = make_float4(ks * scale_log2, lg2_approx(vs), __frcp_rn(vs), blk >= 0 ? 1.f : 0.f);
+                const int64_t off = (((int64_t)max(blk, 0) * a.H_kv + h) << a.block_shift) + (tb & (a.block_size - 1));
+                const uint8_t *kp = a.k_cache + off * D + t4 * 16;
+                const uint8_t *vp = a.v_cache + off * D + g * kV;
+                const uint32_t dst = ring + stage * L::kStageBytes;
+                auto in = [&](int tok) { return blk >= 0 && tb + tok < kv_end && tb + tok >= kv_begin; };
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int hh = 0; hh < kH; ++hh) {
+                        const int tok = tok_a + 2 * x;
+                        const bool ok = in(tok);
+                        cp_async_16(dst + ((x * kH + hh) * 32 + lane) * 16, kp + (ok ? tok : 0) * D + hh * 64, ok ? 16 : 0);
+                    }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int tok = 4 * t4 + x;
+                    const bool ok = in(tok);
+                    const uint32_t d = dst + 16 * D + (x * 32 + lane) * kV;
+                    if (D == 128)
+                        cp_async_16(d, vp + (ok ? tok : 0) * D, ok ? 16 : 0);
+                    else
+                        cp_async_8(d, vp + (ok ? tok : 0) * D, ok ? 8 : 0);
+                }
+            }
+            cp_async_commit();
+        };
+
+        const int n_mine = (s1 - s0 - warp + kWarps - 1) / kWarps; // steps s0 + warp + 4 k
+        for (int k = 0; k < kStages - 1; ++k)
+            issue(s0 + warp + k * kWarps, k);
+        for (int k = 0; k < n_mine; ++k) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp(); // lane 0's scales
+            const int stage = k % kStages;
+            const int s = s0 + warp + k * kWarps;
+            const int tb = rq.begin + s * 16;
+            const float4 mt = meta[stage];
+            const uint32_t src = ring + stage * L::kStageBytes;
+
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+            for (int hh = 0; hh < kH; ++hh) {
+                const uint4 ka = lds128(src + (hh * 32 + lane) * 16), kb = lds128(src + ((kH + hh) * 32 + lane) * 16);
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t f[4];
+                    e4m3x4_to_f16x4(wa[w], f[0], f[2]);
+                    e4m3x4_to_f16x4(wb[w], f[1], f[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16_16816(sc[nt], f, qf[nt][hh * 4 + w][0], qf[nt][hh * 4 + w][1]);
+                }
+            }
+            uint32_t vw[4][kV / 4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (D == 128) {
+                    const uint4 v = lds128(src + 16 * D + (x * 32 + lane) * kV);
+                    vw[x][0] = v.x;
+                    vw[x][1] = v.y;
+                    vw[x][(kV / 4) - 2] = v.z;
+                    vw[x][(kV / 4) - 1] = v.w;
+                } else {
+                    const uint2 v = lds64(src + 16 * D + (x * 32 + lane) * kV);
+                    vw[x][0] = v.x;
+                    vw[x][1] = v.y;
+                }
+            }
+            // the ring's next stage is issued here: the stage it overwrites was read in the last turn
+            issue(s0 + warp + (k + kStages - 1) * kWarps, (k + kStages - 1) % kStages);
+
+            const bool clear = mt.w != 0.f && tb + 15 <= p_first && tb >= all_from && tb + 15 < rq.len && rows == R;
+            bool raise = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = sc[nt][e] * (mt.x * cscale[nt][e & 1]) + mt.y;
+                    if (!clear) {
+                        const int j = tb + tok_a + (e & 2);
+                        const int p = pos[nt][e & 1];
+                        if (!(mt.w != 0.f && j <= p && j < rq.len && (a.window <= 0 || j > p - a.window)))
+                            x = -INFINITY;
+                    }
+                    sc[nt][e] = x;
+                    raise |= x > m[nt][e & 1] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        const float now = fmaxf(m[nt][e], x);
+                        const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - now);
+                        m[nt][e] = now;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) {
+                            o[i][nt][e] *= f;
+                            o[i][nt][e + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                const float p0 = ex2_approx(sc[nt][0] - m0), p1 = ex2_approx(sc[nt][1] - m1);
+                const float p2 = ex2_approx(sc[nt][2] - m0), p3 = ex2_approx(sc[nt][3] - m1);
+                l[nt][0] += (p0 + p2) * mt.z;
+                l[nt][1] += (p1 + p3) * mt.z;
+                pf[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                pf[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+            }
+            // A NaN code of V at a position that some rows see and others do not
+            // must not reach the others through 0 * NaN: it is taken out and
+            // noted for the rows that see it.
+            if (many && !clear) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = tb + 4 * t4 + x;
+#pragma unroll
+                    for (int w = 0; w < kV / 4; ++w) {
+                        const uint32_t bad = nan_bytes(vw[x][w]);
+                        if (bad) {
+                            for (int y = 0; y < 4; ++y)
+                                if (bad >> (8 * y + 7) & 1) {
+                                    const int d = kV * g + 4 * w + y;
+                                    for (int r = 0; r < rows; ++r) {
+                                        const int p = rq.pos((row0 + r) / a.G);
+                                        if (j <= p && j < rq.len && (a.window <= 0 || j > p - a.window))
+                                            atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
+                                    }
+                                }
+                            vw[x][w] &= ~((bad >> 7) * 0xFFu);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kM; ++i) {
+                // value columns kV g + 2 i (row g of the tile) and + 1 (row g + 8)
+                const int w = i >> 1;
+                uint32_t f[4];
+                const uint32_t sel = (i & 1) ? 0x7362 : 0x5140;
+                e4m3x4_to_f16x4(__byte_perm(vw[0][w], vw[1][w], sel), f[0], f[1]);
+                e4m3x4_to_f16x4(__byte_perm(vw[2][w], vw[3][w], sel), f[2], f[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16_16816(o[i][nt], f, pf[nt][0], pf[nt][1]);
+            }
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+
+        // the unit's end: the four warps' sums are joined through shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                if (g == 0)
+                    s_ml[warp * R + nt * 8 + 2 * t4 + e] = make_float2(m[nt][e], l[nt][e]);
+            }
+        __syncthreads(); // every warp is done with the ring
+        float *so = reinterpret_cast<float *>(smem);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float *dst = so + (warp * R + nt * 8 + 2 * t4 + e) * D + kV * g;
+#pragma unroll
+                for (int i = 0; i < kM; i += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * i) =
+                        make_float4(o[i][nt][e], o[i][nt][e + 2], o[i + 1][nt][e], o[i + 1][nt][e + 2]);
+            }
+        __syncthreads();
+        for (int x = tid; x < rows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+            float2 ml[kWarps];
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                ml[w] = s_ml[w * R + r];
+                top = fmaxf(top, ml[w].x);
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                // a warp that saw nothing has m = -inf; its sums are 0, or NaN from a NaN logit
+                const float f = ml[w].x == -INFINITY ? 1.f : ex2_approx(ml[w].x - top);
+                const float4 v = *reinterpret_cast<const float4 *>(so + (w * R + r) * D + d);
+                sum += ml[w].y * f;
+                acc.x += v.x * f;
+                acc.y += v.y * f;
+                acc.z += v.z * f;
+                acc.w += v.w * f;
+            }
+            if (many) {
+                const uint32_t bits = s_nan[(r * D + d) >> 5] >> (d & 31);
+                acc.x = (bits & 1) ? NAN : acc.x;
+                acc.y = (bits & 2) ? NAN : acc.y;
+                acc.z = (bits & 4) ? NAN : acc.z;
+                acc.w = (bits & 8) ? NAN : acc.w;
+            }
+            if (whole) {
+                const int64_t t = rq.q0 + (row0 + r) / a.G;
+                const int head = h * a.G + (row0 + r) % a.G;
+                float lse;
+                const float f = finish_row(top, sum, a.sinks, head, &lse);
+                uint2 out2 = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + d) = out2;
+                if (a.lse && d == 0)
+                    a.lse[t * a.H + head] = lse;
+            } else {
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
+                *reinterpret_cast<float4 *>(part.o + (slot * R + r) * D + d) = acc;
+                if (d == 0)
+                    part.ml[slot * R + r] = make_float2(top, sum);
+            }
+        }
+        __syncthreads(); // the ring and the sums are free again
+    }
+}
+
+// Joins the partial sums of the units that several blocks share: a warp to a
+// row, the blocks in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) kv8_join_kernel(const Kv8AttnArgs a, const Part part)
+{
+    constexpr int R = 8 * NT;
+    constexpr int kD = D / 32; // columns of a lane
+    umma::grid_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x >= *part.header)
+        return;
+    const int4 u = part.dir[blockIdx.x];
+    if (u.x == u.y)
+        return;
+    const Request rq = request(a, u.z);
+    const int h = u.w % a.H_kv, row0 = u.w / a.H_kv * R;
+    const int rows = min(R, rq.qlen * a.G - row0);
+    for (int r = warp; r < rows; r += 8) {
+        float m = -INFINITY, l = 0.f;
+        for (int c = u.x + lane; c <= u.y; c += 32)
+            m = fmaxf(m, part.ml[(2 * (int64_t)c + (c == u.x)) * R + r].x);
+        m = warp_max(m);
+        float acc[kD];
+#pragma unroll
+        for (int i = 0; i < kD; ++i)
+            acc[i] = 0.f;
+#pragma unroll 4
+        for (int c = u.x; c <= u.y; ++c) {
+            const int64_t slot = (2 * (int64_t)c + (c == u.x)) * R + r;
+            const float2 ml = part.ml[slot];
+            const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+            l += ml.y * f;
+            const float *src = part.o + slot * D + lane * kD;
+            if (D == 128) {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                acc[0] += v.x * f;
+                acc[1] += v.y * f;
+                acc[kD - 2] += v.z * f;
+                acc[kD - 1] += v.w * f;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                acc[0] += v.x * f;
+                acc[1] += v.y * f;
+            }
+        }
+        const int64_t t = rq.q0 + (row0 + r) / a.G;
+        const int head = h * a.G + (row0 + r) % a.G;
+        float lse;
+        const float f = finish_row(m, l, a.sinks, head, &lse);
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
+#pragma unroll
+        for (int i = 0; i < kD; i += 2)
+            *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
+        if (a.lse && lane == 0)
+            a.lse[t * a.H + head] = lse;
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int blocks_of(int NT, int sm_count) { return sm_count * (NT == 1 ? 3 : 2); }
+
+struct Sizes {
+    size_t dir, ml, o, total;
+    int64_t units;
+};
+
+Sizes sizes(int64_t B, int64_t T, int H, int H_kv, int D, int NT, int sm_count)
+{
+    const int R = 8 * NT;
+    Sizes s;
+    s.units = (T * (H / H_kv) / R + B) * H_kv; // each request's last chunk may be short
+    const size_t slots = 2 * (size_t)blocks_of(NT, sm_count);
+    s.dir = 256;
+    s.ml = up256(s.dir + (size_t)s.units * sizeof(int4));
+    s.o = up256(s.ml + slots * R * sizeof(float2));
+    s.total = s.o + slots * R * D * sizeof(float);
+    return s;
+}
+
+template <int D, int NT>
+cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
+{
+    using L = Layout<D, NT>;
+    const Sizes sz = sizes(a.B, a.T, a.H, a.H_kv, D, NT, sm_count);
+    if (sz.units > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const Part part{reinterpret_cast<int *>(ws), reinterpret_cast<int4 *>(ws + sz.dir),
+                    reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o)};
+    cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    kv8_stream_kernel<D, NT><<<blocks_of(NT, sm_count), kThreads, L::kSmem, stream>>>(a, part);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    // behind it, its start overlapped (it waits for the first kernel's end)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sz.units);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, NT>, a, part);
+}
+
+// Query rows to a unit: 8, or 16 where the requests' rows fill more than 8.
+int tiles_for(int G, int max_query_len) { return (int64_t)G * max_query_len > 8 ? 2 : 1; }
+
+} // namespace
+
+size_t kv8_stream_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sm_count)
+{
+    return sizes(B, T, H, H_kv, D, tiles_for(H / H_kv, max_query_len), sm_count).total;
+}
+
+cudaError_t launch_kv8_stream(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count,
+                              cudaStream_t stream)
+{
+    const int nt = tiles_for(a.G, max_query_len);
+    if (D == 128)
+        return nt == 1 ? launch<128, 1>(a, workspace, sm_count, stream) : launch<128, 2>(a, workspace, sm_count, stream);
+    return nt == 1 ? launch<64, 1>(a, workspace, sm_count, stream) : launch<64, 2>(a, workspace, sm_count, stream);
+}
+
+} // namespace smla
