@@ -1,0 +1,684 @@
+// Attention over the block-scaled 8-bit cache for many query rows (prompts and
+// chunks of prompts, sm_103a): 128 query rows to a tile, both products on the
+// tensor cores (tcgen05), scores and sums in tensor memory.
+//
+// A CTA takes 128 rows (token, head of the kv head's group) of one request and
+// kv head and walks over the visible positions in tiles of 128. Two CTAs share
+// an SM: one's softmax runs while the other's products do, so each CTA's own
+// chain stays simple: scores, softmax, values, scores, ... Its warps:
+//   0-3  softmax, a row to a thread; the epilogue
+//   4-7  producers: K codes by cp.async, V codes to registers and, expanded to
+//        binary16, to shared memory; the blocks' scales
+//   8    one thread issues the tensor-core products
+//
+// S = Q K^T runs on the cache's codes as they are. q's bf16 values are carried
+// exactly by two E4M3 parts: scaled by a power of two to below 2^8, hi = E4M3(q)
+// and lo = E4M3(q - hi) hold the 8 significant bits of every element down to
+// 2^-9 of the row's largest (smaller ones to 2^-17 of it); two fp8 products
+// take the time of one in 16 bits and need no expansion of K.
+// O += P V takes P in binary16 from tensor memory (where it overlays S) and V
+// expanded exactly to binary16: 8-bit weights would lose half of their bits.
+// The block scales enter as in the streaming kernel: K's multiplies the logits,
+// V's is folded into the exponent, p' = 2^(s + log2(vs) - m), and the
+// denominator adds p' / vs. A row's reference m moves, and its O is rescaled,
+// only when a logit passes it by 8 (p' <= 2^8 is far inside binary16).
+//
+// Shared memory: every operand in 8-row x 16-byte core matrices, written so
+// that eight lanes fill one (no bank conflict). Copies beyond the visible
+// positions, and of blocks outside the pool, are zero-filled and read nothing.
+#include "smla_kv8.cuh"
+#include "smla_umma.cuh"
+
+#include <algorithm>
+
+namespace smla {
+
+__device__ int g_kv8_error = 0; // 1: a bounded wait gave up; 2: products in flight did not drain
+
+namespace {
+
+using namespace kv8;
+using namespace umma;
+
+constexpr int kRows = 128;
+constexpr int kTile = 128;
+constexpr int kSoftmaxThreads = 128, kProducerThreads = 128;
+constexpr int kThreads = kSoftmaxThreads + kProducerThreads + 32;
+constexpr float kSlack = 8.0f;
+constexpr int kMaxSplits = 8;
+
+template <int D> struct Shape {
+    static constexpr int kQBytes = kRows * D;       // one part of Q, or one tile of K codes
+    static constexpr int kVBytes = kTile * D * 2;   // a tile of V in binary16
+    static constexpr int kRowAtoms = D / 16 * 128;  // 8 rows of K (or Q): D / 16 core matrices
+    static constexpr int kVAtoms = D / 8 * 128;     // 8 rows of V
+    static constexpr int kQ = 0;                    // hi, lo
+    static constexpr int kK = 2 * kQBytes;          // two stages
+    static constexpr int kV = kK + 2 * kQBytes;
+    static constexpr int kScales = kV + kVBytes;    // 4 stages x 8 groups x {c, log2 vs, 1 / vs}
+    static constexpr int kBars = kScales + 4 * 8 * 12;
+    static constexpr int kMisc = kBars + 10 * 8;
+    static constexpr int kSmem = kMisc + 64;
+    static constexpr int kNanWords = kRows * D / 32;
+    static constexpr uint32_t kTmem = 256;          // S (P over its first half) and O
+    static constexpr uint32_t kO = 128;
+    static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
+    static constexpr uint32_t kIdescO = idesc(128, D, 0, 0, 0, 1);
+};
+
+struct Part {
+    float2 *ml; // [items][splits][128]
+    float *o;   // [items][splits][128][D]
+    int splits;
+};
+
+// A tile's item: request, chunk of rows, kv head.
+struct Item {
+    int b, chunk, h;
+};
+
+// Items are numbered request by request; request b's first number is
+// floor(q0 G / 128) + b, which leaves room for its ceil(rows / 128) chunks
+// without a running sum. Returns false for a number that no chunk has.
+__device__ __forceinline__ bool find_item(const Kv8AttnArgs &a, int n, Item *it)
+{
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const int q0 = min(max(a.query_start[mid], 0), a.T);
+        if ((int)((long long)q0 * a.G / kRows) + mid <= n)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const Request r = request(a, lo);
+    it->b = lo;
+    it->chunk = n - ((int)((long long)r.q0 * a.G / kRows) + lo);
+    return it->chunk >= 0 && (long long)it->chunk * kRows < (long long)r.qlen * a.G;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// Four floats below 2^8 as E4M3 codes of hi and of the rest lo.
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo)
+{
+    const uint32_t h0 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t h1 = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    hi = (h0 & 0xFFFFu) | (h1 << 16);
+    uint32_t f0, f1;
+    e4m3x4_to_f16x4(hi, f0, f1);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f0));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&f1));
+    const uint32_t l0 = __nv_cvt_float2_to_fp8x2(make_float2(a - x.x, b - x.y), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t l1 = __nv_cvt_float2_to_fp8x2(make_float2(c - y.x, d - y.y), __NV_SATFINITE, __NV_E4M3);
+    lo = (l0 & 0xFFFFu) | (l1 << 16);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs a, const Part part)
+{
+    using S = Shape<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t s_nan[S::kNanWords];
+    __shared__ int s_any_nan;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t bars = base + S::kBars;
+    // K landed / free (two stages), scores ready, P ready, V ready, values done, drained
+    const uint32_t k_full = bars, k_empty = bars + 16, s_full = bars + 32, p_full = bars + 40, v_full = bars + 48,
+                   v_empty = bars + 56, drained = bars + 64;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
+
+    // the longest rows first: a causal prompt's last chunks
+    Item it;
+    const int n_item = (int)((gridDim.x - 1 - blockIdx.x) / a.H_kv);
+    it.h = (int)((gridDim.x - 1 - blockIdx.x) % a.H_kv);
+    if (!find_item(a, n_item, &it))
+        return;
+    const Request rq = request(a, it.b);
+    const int row0 = it.chunk * kRows;
+    const int rows = min(kRows, rq.qlen * a.G - row0);
+    const int p_first = rq.pos(row0 / a.G), p_last = rq.pos((row0 + rows - 1) / a.G);
+    const int kv_end = min(rq.len, p_last + 1);                                       // beyond: seen by none
+    const int kv_begin = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+    const int all_from = a.window > 0 ? p_last - a.window + 1 : 0;                    // [all_from, p_first]: seen by all
+    const int tb0 = kv_begin & ~15;
+    const int tiles_all = kv_end > tb0 ? (kv_end - tb0 + kTile - 1) / kTile : 0;
+    const int split = blockIdx.y;
+    const int t_begin = (int)((long long)tiles_all * split / part.splits);
+    const int t_end = (int)((long long)tiles_all * (split + 1) / part.splits);
+    const int n = t_end - t_begin;
+    const bool many = p_first != p_last;
+
+    if (n <= 0) { // nothing to see here
+        if (tid < rows) {
+            const int64_t t = rq.q0 + (row0 + tid) / a.G;
+            const int head = it.h * a.G + (row0 + tid) % a.G;
+            if (part.splits > 1) {
+                part.ml[(((int64_t)n_item * a.H_kv + it.h) * part.splits + split) * kRows + tid] = make_float2(-INFINITY, 0.f);
+            } else {
+                float lse;
+                finish_row(-INFINITY, 0.f, a.sinks, head, &lse);
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D);
+                for (int i = 0; i < D / 8; ++i)
+                    dst[i] = make_uint4(0, 0, 0, 0);
+                if (a.lse)
+                    a.lse[t * a.H + head] = lse;
+            }
+        }
+        return;
+    }
+
+    if (tid == 0) {
+        s_any_nan = 0;
+        mbar_init(k_full, kProducerThreads);
+        mbar_init(k_full + 8, kProducerThreads);
+        mbar_init(k_empty, 1);
+        mbar_init(k_empty + 8, 1);
+        mbar_init(s_full, 1);
+        mbar_init(p_full, kSoftmaxThreads);
+        mbar_init(v_full, kProducerThreads);
+        mbar_init(v_empty, 1);
+        mbar_init(drained, 1);
+        mbar_init_fence();
+    }
+    if (many)
+        for (int i = tid; i < S::kNanWords; i += kThreads)
+            s_nan[i] = 0;
+    if (warp == 8)
+        alloc(smem_u32(tmem_slot), S::kTmem);
+    const float scale_log2 = fabsf(a.scale) * kLog2e; // the sign goes into q
+
+    float qs = 0.f;
+    if (tid < kSoftmaxThreads) {
+        // this thread's row of Q, in two E4M3 parts
+        const int r = tid;
+        const bool live = r < rows;
+        const int rr = row0 + (live ? r : 0);
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                           (int64_t)(rq.q0 + rr / a.G) * a.q_st +
+                                                           (int64_t)(it.h * a.G + rr % a.G) * a.q_sh);
+        float amax = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        }
+        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 127);
+        float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+        qs = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + e - 7) << 23); // an infinite q has no finite logit
+        up = a.scale < 0.f ? -up : up;
+        const uint32_t dst = base + S::kQ + (r >> 3) * S::kRowAtoms + (r & 7) * 16;
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+                const uint4 v = live ? src[2 * i + e2] : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * x]));
+                    const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * x + 1]));
+                    split4(f0.x * up, f0.y * up, f1.x * up, f1.y * up, hi[2 * e2 + x], lo[2 * e2 + x]);
+                }
+            }
+            sts128(dst + i * 128, hi[0], hi[1], hi[2], hi[3]);
+            sts128(dst + S::kQBytes + i * 128, lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_smem();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    // a bounded wait, by whole warps (or by the one thread of warp 8)
+    auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
+        if (!ok && lane == 0)
+            atomicOr(&g_kv8_error, 1);
+        return ok;
+    };
+
+    if (warp < 4) {
+        // ---------------------------------------------------------------- softmax
+        const int r = tid;
+        const int pos = r < rows ? rq.pos((row0 + r) / a.G) : -1;
+        const int pos_lo = a.window > 0 ? pos - a.window + 1 : 0;
+        const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
+        const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < n; ++j) {
+            // the scales of this tile's blocks come with its K; then its scores
+            if (!wait_warp(k_full + (j & 1) * 8, (j >> 1) & 1) || !wait_warp(s_full, j & 1))
+                break;
+            fence_after_sync();
+            const int tb = tb0 + (t_begin + j) * kTile;
+            const float *sc = scales + (j & 3) * 24;
+            const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
+            // the row's largest logit
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32];
+                ld32(my + c * 32, x);
+                wait_ld();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float big = -INFINITY;
+                    if (clear) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            big = fmaxf(big, __uint_as_float(x[g * 16 + i]));
+                    } else {
+                        const int t = tb + c * 32 + g * 16;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            big = (t + i <= pos && t + i >= pos_lo) ? fmaxf(big, __uint_as_float(x[g * 16 + i])) : big;
+                    }
+                    const int gi = c * 2 + g;
+                    top = fmaxf(top, big == -INFINITY ? big : fmaf(big, sc[gi] * qs, sc[8 + gi]));
+                }
+            }
+            const bool raise = top > m + kSlack;
+            if (__any_sync(0xffffffffu, raise)) {
+                // O is at rest: the scores just read were issued after its last product was done
+                const float f = !raise ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - top));
+                m = raise ? top : m;
+                l *= f;
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t x[32];
+                        ld32(my + S::kO + c * 32, x);
+                        wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                        st32(my + S::kO + c * 32, x);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            // logits beyond 2^20: s - m is taken from the rounded logit, as m was, or the
+            // rounding of m alone could pass any bound of p'
+            const bool plain = clear && !__any_sync(0xffffffffu, fabsf(ref) > 0x1p20f);
+            // the weights, over the scores they come from: a chunk's columns were read before they are written
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32], p[16];
+                ld32(my + c * 32, x);
+                wait_ld();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int gi = c * 2 + g;
+                    const float k0 = sc[gi] * qs, b0 = sc[8 + gi] - ref;
+                    const int t = tb + c * 32 + g * 16;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float p0, p1;
+                        if (plain) {
+                            p0 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i]), k0, b0));
+                            p1 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i + 1]), k0, b0));
+                        } else {
+                            p0 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i]), k0, sc[8 + gi]) - ref);
+                            p1 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i + 1]), k0, sc[8 + gi]) - ref);
+                            p0 = (t + i <= pos && t + i >= pos_lo) ? p0 : 0.f;
+                            p1 = (t + i + 1 <= pos && t + i + 1 >= pos_lo) ? p1 : 0.f;
+                        }
+                        sum += p0 + p1;
+                        p[g * 8 + i / 2] = pack_f16x2(p0, p1);
+                    }
+                    l = fmaf(sum, sc[16 + gi], l);
+                }
+                st16(my + c * 16, p);
+            }
+            wait_st();
+            fence_before_sync();
+            mbar_arrive(p_full);
+        }
+        if (ok && wait_warp(v_full, (n - 1) & 1) && wait_warp(v_empty, (n - 1) & 1)) {
+            fence_after_sync();
+            const bool live = r < rows;
+            const int rr = row0 + (live ? r : 0);
+            const int64_t t = rq.q0 + rr / a.G;
+            const int head = it.h * a.G + rr % a.G;
+            const int64_t slot = (((int64_t)n_item * a.H_kv + it.h) * part.splits + split) * kRows + r;
+            const bool nans = many && s_any_nan;
+            float lse = 0.f, f = 1.f;
+            if (part.splits == 1)
+                f = finish_row(m, l, a.sinks, head, &lse);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                ld32(my + S::kO + c * 32, x);
+                wait_ld();
+                if (nans) {
+                    const uint32_t bits = s_nan[(r * D + c * 32) >> 5];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = (bits >> i & 1) ? 0x7FC00000u : x[i];
+                }
+                if (!live)
+                    continue;
+                if (part.splits == 1) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + c * 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(x[i * 8 + 2 * e]) * f, __uint_as_float(x[i * 8 + 2 * e + 1]) * f);
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(part.o + slot * D + c * 32);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                }
+            }
+            if (live) {
+                if (part.splits > 1)
+                    part.ml[slot] = make_float2(m, l);
+                else if (a.lse)
+                    a.lse[t * a.H + head] = lse;
+            }
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- producers
+        constexpr int kC = D / 64; // 16-byte pieces of a row to a lane
+        const int pw = warp - 4;
+        const int sub = lane & 7, piece = lane >> 3; // rows pw * 32 + sub + 8 k, pieces piece + 4 c
+        const int32_t *table = a.block_table + it.b * a.table_stride;
+        float *scales = reinterpret_cast<float *>(smem + S::kScales);
+        int blk[2];
+        float ks = 0.f, vs = 1.f; // lanes 0 and 1: the scales of the warp's two groups of 16 positions
+        uint4 vr[4][kC];
+        auto load_blocks = [&](int j) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int t = tb0 + (t_begin + j) * kTile + pw * 32 + 16 * x;
+                const int e = t >> a.block_shift;
+                int v = t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
+                blk[x] = v >= 0 && v < a.num_blocks ? v : -1;
+            }
+        };
+        auto offset = [&](int j, int k, bool *in) {
+            const int t = tb0 + (t_begin + j) * kTile + pw * 32 + sub + 8 * k;
+            const int v = blk[k >> 1];
+            *in = v >= 0 && t < kv_end && t >= kv_begin;
+            return *in ? (((((int64_t)v * a.H_kv + it.h) << a.block_shift) + (t & (a.block_size - 1))) * D) : 0;
+        };
+        auto issue_k = [&](int j) {
+            const uint32_t dst = base + S::kK + (j & 1) * S::kQBytes + pw * 4 * S::kRowAtoms + sub * 16 + piece * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bool in;
+                const uint8_t *src = a.k_cache + offset(j, k, &in) + piece * 16;
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    cp_async_16(dst + k * S::kRowAtoms + c * 512, src + c * 64, in ? 16 : 0);
+            }
+            cp_async_commit();
+            if (lane < 2) {
+                const int v = lane ? blk[1] : blk[0];
+                ks = v >= 0 ? __ldg(a.k_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
+                vs = v >= 0 ? __ldg(a.v_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
+            }
+        };
+        auto load_v = [&](int j) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bool in;
+                const uint8_t *src = a.v_cache + offset(j, k, &in) + piece * 16;
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    vr[k][c] = in ? *reinterpret_cast<const uint4 *>(src + c * 64) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        load_blocks(0);
+        issue_k(0);
+        load_v(0);
+        if (n > 1)
+            load_blocks(1);
+        for (int j = 0; j < n; ++j) {
+            cp_async_wait<0>();
+            if (lane < 2) {
+                // a group outside the pool (or past the end): logits of -inf
+                float *sc = scales + (j & 3) * 24 + pw * 2 + lane;
+                sc[0] = ks * scale_log2;
+                sc[8] = vs > 0.f ? lg2_approx(vs) : -INFINITY;
+                sc[16] = vs > 0.f ? __frcp_rn(vs) : 1.f;
+            }
+            fence_async_smem();
+            mbar_arrive(k_full + (j & 1) * 8);
+            if (j + 1 < n) {
+                if (j > 0 && !wait_warp(k_empty + ((j + 1) & 1) * 8, ((j - 1) >> 1) & 1))
+                    break;
+                issue_k(j + 1);
+            }
+            if (j > 0 && !wait_warp(v_empty, (j - 1) & 1))
+                break;
+            const int tb = tb0 + (t_begin + j) * kTile;
+            if (many && !(tb + kTile - 1 <= p_first && tb >= all_from)) {
+                // A NaN code at a position that some rows see and others do not must not
+                // reach the others through 0 * NaN: it is taken out and noted for the
+                // rows that see it.
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int c = 0; c < kC; ++c) {
+                        uint32_t w[4] = {vr[k][c].x, vr[k][c].y, vr[k][c].z, vr[k][c].w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t bad = nan_bytes(w[y]);
+                            if (bad) {
+                                const int t = tb + pw * 32 + sub + 8 * k;
+                                for (int z = 0; z < 4; ++z)
+                                    if (bad >> (8 * z + 7) & 1) {
+                                        const int d = (piece + 4 * c) * 16 + 4 * y + z;
+                                        for (int r = 0; r < rows; ++r) {
+                                            const int p = rq.pos((row0 + r) / a.G);
+                                            if (t <= p && (a.window <= 0 || t > p - a.window))
+                                                atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
+                                        }
+                                    }
+                                s_any_nan = 1;
+                                w[y] &= ~((bad >> 7) * 0xFFu);
+                            }
+                        }
+                        vr[k][c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+            }
+            const uint32_t dst = base + S::kV + pw * 4 * S::kVAtoms + sub * 16 + piece * 256;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    uint32_t f[8];
+                    e4m3x4_to_f16x4(vr[k][c].x, f[0], f[1]);
+                    e4m3x4_to_f16x4(vr[k][c].y, f[2], f[3]);
+                    e4m3x4_to_f16x4(vr[k][c].z, f[4], f[5]);
+                    e4m3x4_to_f16x4(vr[k][c].w, f[6], f[7]);
+                    sts128(dst + k * S::kVAtoms + c * 1024, f[0], f[1], f[2], f[3]);
+                    sts128(dst + k * S::kVAtoms + c * 1024 + 128, f[4], f[5], f[6], f[7]);
+                }
+            fence_async_smem();
+            mbar_arrive(v_full);
+            if (j + 1 < n)
+                load_v(j + 1);
+            if (j + 2 < n)
+                load_blocks(j + 2);
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+    } else if (lane == 0) {
+        // ---------------------------------------------------------------- products
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && mbar_wait(bar, parity);
+            if (!ok)
+                atomicOr(&g_kv8_error, 1);
+            return ok;
+        };
+        const uint64_t q_hi = desc(base + S::kQ, 128, S::kRowAtoms);
+        const uint64_t q_lo = desc(base + S::kQ + S::kQBytes, 128, S::kRowAtoms);
+        const uint64_t v_d = desc(base + S::kV, S::kVAtoms, 128);
+        for (int j = 0; j < n; ++j) {
+            // P overlays S: the last product of P is done before scores are written there
+            if (!wait(k_full + (j & 1) * 8, (j >> 1) & 1) || (j > 0 && !wait(v_empty, (j - 1) & 1)))
+                break;
+            fence_after_sync();
+            const uint64_t k_d = desc(base + S::kK + (j & 1) * S::kQBytes, 128, S::kRowAtoms);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) // 32 columns: two core matrices of 128 bytes
+                mma_f8(tmem, q_hi + kk * 16, k_d + kk * 16, S::kIdescS, kk > 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+                mma_f8(tmem, q_lo + kk * 16, k_d + kk * 16, S::kIdescS, 1);
+            commit(s_full);
+            commit(k_empty + (j & 1) * 8);
+            if (!wait(v_full, j & 1) || !wait(p_full, j & 1))
+                break;
+            fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk) // 16 positions: 8 columns of P, two atoms of V
+                mma_f16_ts(tmem + S::kO, tmem + kk * 8, v_d + (uint64_t)(kk * 2 * S::kVAtoms / 16), S::kIdescO, j > 0 || kk > 0);
+            commit(v_empty);
+        }
+        if (!ok) { // what was issued ends before its memory is given back
+            commit(drained);
+            if (!mbar_wait(drained, 0))
+                atomicOr(&g_kv8_error, 2);
+        }
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 8)
+        dealloc(tmem, S::kTmem);
+}
+
+// Joins the splits of each item's rows, a warp to a row.
+template <int D>
+__global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a, const Part part)
+{
+    constexpr int kD = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Item it;
+    const int n_item = (int)(blockIdx.x / a.H_kv);
+    it.h = (int)(blockIdx.x % a.H_kv);
+    if (!find_item(a, n_item, &it))
+        return;
+    const Request rq = request(a, it.b);
+    const int row0 = it.chunk * kRows;
+    const int rows = min(kRows, rq.qlen * a.G - row0);
+    const int64_t slot0 = ((int64_t)n_item * a.H_kv + it.h) * part.splits * kRows;
+    for (int r = warp + 8 * blockIdx.y; r < rows; r += 8 * gridDim.y) {
+        float2 ml[kMaxSplits];
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+            if (s < part.splits) {
+                ml[s] = part.ml[slot0 + s * kRows + r];
+                m = fmaxf(m, ml[s].x);
+            }
+        float acc[kD];
+#pragma unroll
+        for (int i = 0; i < kD; ++i)
+            acc[i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+            if (s < part.splits && !(ml[s].x == -INFINITY && ml[s].y == 0.f)) { // nothing seen: no sums were written
+                const float f = ml[s].x == -INFINITY ? 1.f : ex2_approx(ml[s].x - m);
+                l += ml[s].y * f;
+                const float *src = part.o + (slot0 + s * kRows + r) * D + lane * kD;
+#pragma unroll
+                for (int i = 0; i < kD; i += 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + i);
+                    acc[i] += v.x * f;
+                    acc[i + 1] += v.y * f;
+                }
+            }
+        const int64_t t = rq.q0 + (row0 + r) / a.G;
+        const int head = it.h * a.G + (row0 + r) % a.G;
+        float lse;
+        const float f = finish_row(m, l, a.sinks, head, &lse);
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
+#pragma unroll
+        for (int i = 0; i < kD; i += 2)
+            *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
+        if (a.lse && lane == 0)
+            a.lse[t * a.H + head] = lse;
+    }
+}
+
+int64_t items_of(int B, int T, int G) { return (int64_t)T * G / kRows + B; }
+
+// Splits of a request's positions: while the items are fewer than three to
+// each CTA slot, so that ragged lengths even out.
+int splits_of(int B, int T, int H, int H_kv, int sm_count)
+{
+    const int64_t items = items_of(B, T, H / H_kv) * H_kv, slots = 2 * (int64_t)std::max(sm_count, 1);
+    return (int)std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, 3 * slots / std::max<int64_t>(items, 1)));
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int D>
+cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
+{
+    const int64_t items = items_of(a.B, a.T, a.G) * a.H_kv;
+    Part part;
+    part.splits = splits_of(a.B, a.T, a.G * a.H_kv, a.H_kv, sm_count);
+    const size_t slots = (size_t)items * part.splits * kRows;
+    part.ml = static_cast<float2 *>(workspace);
+    part.o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(slots * sizeof(float2)));
+    cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(a, part);
+    if ((e = cudaGetLastError()) != cudaSuccess || part.splits == 1)
+        return e;
+    kv8_tile_join_kernel<D><<<dim3((unsigned)items, 4), 256, 0, stream>>>(a, part);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int sm_count)
+{
+    const int splits = splits_of(B, T, H, H_kv, sm_count);
+    if (splits == 1)
+        return 256;
+    const size_t slots = (size_t)items_of(B, T, H / H_kv) * H_kv * splits * kRows;
+    return up256(slots * sizeof(float2)) + slots * D * sizeof(float);
+}
+
+cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, void *workspace, int sm_count, cudaStream_t stream)
+{
+    return D == 128 ? launch<128>(a, workspace, sm_count, stream) : launch<64>(a, workspace, sm_count, stream);
+}
+
+cudaError_t read_kv8_error(int *out, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_kv8_error, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_kv8_error, &zero, sizeof(int));
+    }
+    return e;
+}
+
+} // namespace smla

@@ -35,6 +35,15 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // workspace of smla_build_block_tables: the ring state, then the plan of each request
 size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + up256((size_t)B * sizeof(int32_t)); }
 
+// Rows of a request that the streaming kernel takes in one unit; more go to the tile kernel.
+bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) * max_query_len <= 16; }
+
+size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sms)
+{
+    return few_rows(H, H_kv, max_query_len) ? smla::kv8_stream_workspace(B, T, H, H_kv, D, max_query_len, sms)
+                                            : smla::kv8_tile_workspace(B, T, H, H_kv, D, sms);
+}
+
 smla_status check_kv8_shape(int B, int T, int H, int H_kv, int D, int max_query_len)
 {
     if (B < 0 || T < 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || D <= 0 || max_query_len < 0)
@@ -289,7 +298,7 @@ SMLA_API size_t smla_kv8_attn_workspace_size(int B, int T, int H, int H_kv, int 
     int sms = 0;
     if (check_kv8_shape(B, T, H, H_kv, D, max_query_len) != SMLA_OK || current_sm_count(&sms) != cudaSuccess)
         return (size_t)-1;
-    return smla::kv8_stream_workspace(B, T, H, H_kv, D, max_query_len, sms);
+    return kv8_workspace(B, T, H, H_kv, D, max_query_len, sms);
 }
 
 SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
@@ -320,7 +329,7 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms); e != cudaSuccess)
         return cuda_status(e);
-    if (p->workspace_bytes < smla::kv8_stream_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len, sms))
+    if (p->workspace_bytes < kv8_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len, sms))
         return SMLA_ERR_WORKSPACE_TOO_SMALL;
     smla::Kv8AttnArgs a;
     a.q = p->q;
@@ -348,6 +357,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     a.sinks = p->sinks;
     a.out = p->out;
     a.lse = p->lse;
+    if (!few_rows(p->H, p->H_kv, p->max_query_len))
+        return cuda_status(smla::launch_kv8_tile(a, p->D, p->workspace, sms, reinterpret_cast<cudaStream_t>(p->stream)));
     return cuda_status(smla::launch_kv8_stream(a, p->D, p->max_query_len, p->workspace, sms,
                                                reinterpret_cast<cudaStream_t>(p->stream)));
 }
