@@ -527,7 +527,8 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
  * workspace     device, >= smla_kv8_attn_workspace_size(...) bytes (for the
  *               current device), 256-byte aligned, need not be initialised.
  *               Calls that overlap in time must not share it.
- * H a multiple of H_kv; B >= 0, T >= 0 (0: a no-op); 0 <= window.
+ * H a multiple of H_kv; B >= 0, T >= 0 (0: a no-op); 0 <= window;
+ * num_blocks * H_kv and table_width * block_size below 2^31.
  */
 typedef struct smla_kv8_attn_params {
     size_t size; /* sizeof(smla_kv8_attn_params) */

@@ -7,9 +7,10 @@
 // an SM: one's softmax runs while the other's products do, so each CTA's own
 // chain stays simple: scores, softmax, values, scores, ... Its warps:
 //   0-3  softmax, a row to a thread; the epilogue
-//   4-7  producers: K codes by cp.async, V codes to registers and, expanded to
-//        binary16, to shared memory; the blocks' scales
-//   8    one thread issues the tensor-core products
+//   4-5  V: codes to registers and, expanded to binary16, to shared memory
+//   6    K: the blocks' codes by TMA as they lie in the cache; the blocks' scales
+//   7    one thread issues the tensor-core products
+// (eight warps, so that both CTAs' threads have 128 registers).
 //
 // S = Q K^T runs on the cache's codes as they are. q's bf16 values are carried
 // exactly by two E4M3 parts: scaled by a power of two to below 2^8, hi = E4M3(q)
@@ -23,9 +24,10 @@
 // denominator adds p' / vs. A row's reference m moves, and its O is rescaled,
 // only when a logit passes it by 8 (p' <= 2^8 is far inside binary16).
 //
-// Shared memory: every operand in 8-row x 16-byte core matrices, written so
-// that eight lanes fill one (no bank conflict). Copies beyond the visible
-// positions, and of blocks outside the pool, are zero-filled and read nothing.
+// Shared memory: K in TMA's swizzled rows; Q and V in 8-row x 16-byte core
+// matrices, written so that eight lanes fill one (no bank conflict). Blocks
+// outside the pool and V beyond the visible positions are zero-filled and not
+// read.
 #include "smla_kv8.cuh"
 #include "smla_umma.cuh"
 
@@ -42,24 +44,25 @@ using namespace umma;
 
 constexpr int kRows = 128;
 constexpr int kTile = 128;
-constexpr int kSoftmaxThreads = 128, kProducerThreads = 128;
-constexpr int kThreads = kSoftmaxThreads + kProducerThreads + 32;
+constexpr int kSoftmaxThreads = 128, kVThreads = 64;
+constexpr int kThreads = 256;
 constexpr float kSlack = 8.0f;
 constexpr int kMaxSplits = 8;
 
 template <int D> struct Shape {
     static constexpr int kQBytes = kRows * D;       // one part of Q, or one tile of K codes
     static constexpr int kVBytes = kTile * D * 2;   // a tile of V in binary16
-    static constexpr int kRowAtoms = D / 16 * 128;  // 8 rows of K (or Q): D / 16 core matrices
+    static constexpr int kQAtoms = D / 16 * 128;    // 8 rows of Q: D / 16 core matrices
     static constexpr int kVAtoms = D / 8 * 128;     // 8 rows of V
-    static constexpr int kQ = 0;                    // hi, lo
-    static constexpr int kK = 2 * kQBytes;          // two stages
-    static constexpr int kV = kK + 2 * kQBytes;
+    static constexpr int kK = 0;                    // two stages
+    static constexpr int kQ = 2 * kQBytes;          // hi, lo
+    static constexpr int kV = kQ + 2 * kQBytes;
     static constexpr int kScales = kV + kVBytes;    // 4 stages x 8 groups x {c, log2 vs, 1 / vs}
     static constexpr int kBars = kScales + 4 * 8 * 12;
     static constexpr int kMisc = kBars + 10 * 8;
-    static constexpr int kSmem = kMisc + 64;
+    static constexpr int kNan = kMisc + 16;         // a bit for each (row, column)
     static constexpr int kNanWords = kRows * D / 32;
+    static constexpr int kSmem = kNan + kNanWords * 4 + 1024; // the base is rounded up to 1024
     static constexpr uint32_t kTmem = 256;          // S (P over its first half) and O
     static constexpr uint32_t kO = 128;
     static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
@@ -119,13 +122,151 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
     lo = (l0 & 0xFFFFu) | (l1 << 16);
 }
 
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c)); // a NaN loses, as with fmaxf
+    return r;
+}
+
+// Waits for this thread's tensor-memory loads; x holds what they brought only after it.
+__device__ __forceinline__ void wait_ld16(uint32_t (&x)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                   "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+}
+
+// The largest logit of 16 scores of one row. sc: the group's factor of K,
+// sc[8]: log2 of its value scale. kClear: every position is seen; else position
+// t + i is when pos_lo <= t + i <= pos.
+template <bool kClear>
+__device__ __forceinline__ float group_max(const uint32_t (&x)[16], const float *sc, float qs, int t, int pos, int pos_lo)
+{
+    float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = __uint_as_float(x[i + e]);
+            if (!kClear)
+                y[e] = (t + i + e <= pos && t + i + e >= pos_lo) ? y[e] : -INFINITY;
+        }
+        b0 = max3(b0, y[0], y[1]);
+        b1 = max3(b1, y[2], y[3]);
+    }
+    b0 = fmaxf(b0, b1);
+    const float s = fmaf(b0, sc[0] * qs, sc[8]);
+    // (a masked group has no logit; -inf times a factor of 0 would be NaN)
+    return !kClear && b0 == -INFINITY ? b0 : s;
+}
+
+// The largest logit of a row's 128 scores (the thread's lane of tensor memory);
+// a group's load is in flight while the one before is looked at.
+template <bool kClear>
+__device__ __forceinline__ float row_max(uint32_t my, const float *sc, float qs, int t0, int pos, int pos_lo)
+{
+    float top = -INFINITY;
+    uint32_t a[16], b[16];
+    ld16(my, a);
+    wait_ld16(a);
+#pragma unroll 1
+    for (int g = 0; g < 8; g += 2) {
+        ld16(my + g * 16 + 16, b);
+        top = fmaxf(top, group_max<kClear>(a, sc + g, qs, t0 + g * 16, pos, pos_lo));
+        wait_ld16(b);
+        if (g < 6)
+            ld16(my + g * 16 + 32, a);
+        top = fmaxf(top, group_max<kClear>(b, sc + g + 1, qs, t0 + g * 16 + 16, pos, pos_lo));
+        wait_ld16(a);
+    }
+    return top;
+}
+
+// The weights 2^(s + log2(vs) - ref) of 16 scores, in binary16, written over
+// scores that were read before; their sum divided by vs is added to l. sc[16]:
+// 1 / vs. kPlain: every position is seen and |ref| is small.
+template <bool kPlain>
+__device__ __forceinline__ float group_weights(const uint32_t (&x)[16], uint32_t dst, const float *sc, float qs, float ref,
+                                               float l, int t, int pos, int pos_lo)
+{
+    uint32_t p[8];
+    const float k0 = sc[0] * qs, b0 = sc[8] - ref;
+    const uint64_t kk = pair(k0, k0), bb = pair(b0, b0);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+        float p0, p1;
+        if (kPlain) {
+            unpair(fma2(pair(x0, x1), kk, bb), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+        } else {
+            p0 = ex2_approx(fmaf(x0, k0, sc[8]) - ref);
+            p1 = ex2_approx(fmaf(x1, k0, sc[8]) - ref);
+            p0 = (t + i <= pos && t + i >= pos_lo) ? p0 : 0.f;
+            p1 = (t + i + 1 <= pos && t + i + 1 >= pos_lo) ? p1 : 0.f;
+        }
+        sum = add2(sum, pair(p0, p1));
+        p[i / 2] = pack_f16x2(p0, p1);
+    }
+    st8(dst, p);
+    float s0, s1;
+    unpair(sum, s0, s1);
+    return fmaf(s0 + s1, sc[16], l);
+}
+
+template <bool kPlain>
+__device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float qs, float ref, float l, int t0, int pos,
+                                             int pos_lo)
+{
+    uint32_t a[16], b[16];
+    ld16(my, a);
+    wait_ld16(a);
+#pragma unroll 1
+    for (int g = 0; g < 8; g += 2) {
+        ld16(my + g * 16 + 16, b);
+        l = group_weights<kPlain>(a, my + g * 8, sc + g, qs, ref, l, t0 + g * 16, pos, pos_lo);
+        wait_ld16(b);
+        if (g < 6)
+            ld16(my + g * 16 + 32, a);
+        l = group_weights<kPlain>(b, my + g * 8 + 8, sc + g + 1, qs, ref, l, t0 + g * 16 + 16, pos, pos_lo);
+        wait_ld16(a);
+    }
+    return l;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs a, const Part part)
+__global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map, const Kv8AttnArgs a,
+                                                               const Part part)
 {
     using S = Shape<D>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t s_nan[S::kNanWords];
-    __shared__ int s_any_nan;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+    uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + S::kNan);
+    int *s_any_nan = reinterpret_cast<int *>(smem + S::kMisc + 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = smem_u32(smem);
     const uint32_t bars = base + S::kBars;
@@ -147,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
     const int kv_end = min(rq.len, p_last + 1);                                       // beyond: seen by none
     const int kv_begin = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
     const int all_from = a.window > 0 ? p_last - a.window + 1 : 0;                    // [all_from, p_first]: seen by all
-    const int tb0 = kv_begin & ~15;
+    const int tb0 = kv_begin & ~(kTile - 1); // so that the blocks lie whole in the tiles
     const int tiles_all = kv_end > tb0 ? (kv_end - tb0 + kTile - 1) / kTile : 0;
     const int split = blockIdx.y;
     const int t_begin = (int)((long long)tiles_all * split / part.splits);
@@ -175,14 +316,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
     }
 
     if (tid == 0) {
-        s_any_nan = 0;
-        mbar_init(k_full, kProducerThreads);
-        mbar_init(k_full + 8, kProducerThreads);
+        *s_any_nan = 0;
+        mbar_init(k_full, 2); // the copies' bytes; the scales
+        mbar_init(k_full + 8, 2);
         mbar_init(k_empty, 1);
         mbar_init(k_empty + 8, 1);
         mbar_init(s_full, 1);
         mbar_init(p_full, kSoftmaxThreads);
-        mbar_init(v_full, kProducerThreads);
+        mbar_init(v_full, kVThreads);
         mbar_init(v_empty, 1);
         mbar_init(drained, 1);
         mbar_init_fence();
@@ -190,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
     if (many)
         for (int i = tid; i < S::kNanWords; i += kThreads)
             s_nan[i] = 0;
-    if (warp == 8)
+    if (warp == 7)
         alloc(smem_u32(tmem_slot), S::kTmem);
     const float scale_log2 = fabsf(a.scale) * kLog2e; // the sign goes into q
 
@@ -218,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
         float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
         qs = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + e - 7) << 23); // an infinite q has no finite logit
         up = a.scale < 0.f ? -up : up;
-        const uint32_t dst = base + S::kQ + (r >> 3) * S::kRowAtoms + (r & 7) * 16;
+        const uint32_t dst = base + S::kQ + (r >> 3) * S::kQAtoms + (r & 7) * 16;
 #pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {
             uint32_t hi[4], lo[4];
@@ -243,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
-    // a bounded wait, by whole warps (or by the one thread of warp 8)
+    // a bounded wait, by whole warps (or by the one thread of warp 7)
     auto wait_warp = [&](uint32_t bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
         if (!ok && lane == 0)
@@ -267,30 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
             const int tb = tb0 + (t_begin + j) * kTile;
             const float *sc = scales + (j & 3) * 24;
             const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
-            // the row's largest logit
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32];
-                ld32(my + c * 32, x);
-                wait_ld();
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float big = -INFINITY;
-                    if (clear) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            big = fmaxf(big, __uint_as_float(x[g * 16 + i]));
-                    } else {
-                        const int t = tb + c * 32 + g * 16;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            big = (t + i <= pos && t + i >= pos_lo) ? fmaxf(big, __uint_as_float(x[g * 16 + i])) : big;
-                    }
-                    const int gi = c * 2 + g;
-                    top = fmaxf(top, big == -INFINITY ? big : fmaf(big, sc[gi] * qs, sc[8 + gi]));
-                }
-            }
+            const float top = clear ? row_max<true>(my, sc, qs, 0, 0, 0) : row_max<false>(my, sc, qs, tb, pos, pos_lo);
             const bool raise = top > m + kSlack;
             if (__any_sync(0xffffffffu, raise)) {
                 // O is at rest: the scores just read were issued after its last product was done
@@ -311,44 +429,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            // logits beyond 2^20: s - m is taken from the rounded logit, as m was, or the
-            // rounding of m alone could pass any bound of p'
+            // beyond 2^20, s - m is taken from the rounded logit, as m was, or the rounding
+            // of m alone could pass any bound of p'
             const bool plain = clear && !__any_sync(0xffffffffu, fabsf(ref) > 0x1p20f);
-            // the weights, over the scores they come from: a chunk's columns were read before they are written
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32], p[16];
-                ld32(my + c * 32, x);
-                wait_ld();
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int gi = c * 2 + g;
-                    const float k0 = sc[gi] * qs, b0 = sc[8 + gi] - ref;
-                    const int t = tb + c * 32 + g * 16;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float p0, p1;
-                        if (plain) {
-                            p0 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i]), k0, b0));
-                            p1 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i + 1]), k0, b0));
-                        } else {
-                            p0 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i]), k0, sc[8 + gi]) - ref);
-                            p1 = ex2_approx(fmaf(__uint_as_float(x[g * 16 + i + 1]), k0, sc[8 + gi]) - ref);
-                            p0 = (t + i <= pos && t + i >= pos_lo) ? p0 : 0.f;
-                            p1 = (t + i + 1 <= pos && t + i + 1 >= pos_lo) ? p1 : 0.f;
-                        }
-                        sum += p0 + p1;
-                        p[g * 8 + i / 2] = pack_f16x2(p0, p1);
-                    }
-                    l = fmaf(sum, sc[16 + gi], l);
-                }
-                st16(my + c * 16, p);
-            }
+            l = plain ? row_weights<true>(my, sc, qs, ref, l, 0, 0, 0) : row_weights<false>(my, sc, qs, ref, l, tb, pos, pos_lo);
             wait_st();
             fence_before_sync();
             mbar_arrive(p_full);
         }
+        // (V's last arrival carries the notes of NaN codes)
         if (ok && wait_warp(v_full, (n - 1) & 1) && wait_warp(v_empty, (n - 1) & 1)) {
             fence_after_sync();
             const bool live = r < rows;
@@ -356,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
             const int64_t t = rq.q0 + rr / a.G;
             const int head = it.h * a.G + rr % a.G;
             const int64_t slot = (((int64_t)n_item * a.H_kv + it.h) * part.splits + split) * kRows + r;
-            const bool nans = many && s_any_nan;
+            const bool nans = many && *s_any_nan;
             float lse = 0.f, f = 1.f;
             if (part.splits == 1)
                 f = finish_row(m, l, a.sinks, head, &lse);
@@ -397,79 +486,40 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
                     a.lse[t * a.H + head] = lse;
             }
         }
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- producers
-        constexpr int kC = D / 64; // 16-byte pieces of a row to a lane
-        const int pw = warp - 4;
-        const int sub = lane & 7, piece = lane >> 3; // rows pw * 32 + sub + 8 k, pieces piece + 4 c
+    } else if (warp < 6) {
+        // ---------------------------------------------------------------- V
+        constexpr int kC = D / 64;                   // 16-byte pieces of a row to a lane
+        const int vw = warp - 4;
+        const int sub = lane & 7, piece = lane >> 3; // rows vw * 64 + sub + 8 k, pieces piece + 4 c
         const int32_t *table = a.block_table + it.b * a.table_stride;
-        float *scales = reinterpret_cast<float *>(smem + S::kScales);
-        int blk[2];
-        float ks = 0.f, vs = 1.f; // lanes 0 and 1: the scales of the warp's two groups of 16 positions
-        uint4 vr[4][kC];
+        int raw[4]; // table entries of the warp's four groups of 16 positions
+        uint4 vr[8][kC];
         auto load_blocks = [&](int j) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = tb0 + (t_begin + j) * kTile + pw * 32 + 16 * x;
+            for (int x = 0; x < 4; ++x) {
+                const int t = tb0 + (t_begin + j) * kTile + vw * 64 + 16 * x;
                 const int e = t >> a.block_shift;
-                int v = t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
-                blk[x] = v >= 0 && v < a.num_blocks ? v : -1;
-            }
-        };
-        auto offset = [&](int j, int k, bool *in) {
-            const int t = tb0 + (t_begin + j) * kTile + pw * 32 + sub + 8 * k;
-            const int v = blk[k >> 1];
-            *in = v >= 0 && t < kv_end && t >= kv_begin;
-            return *in ? (((((int64_t)v * a.H_kv + it.h) << a.block_shift) + (t & (a.block_size - 1))) * D) : 0;
-        };
-        auto issue_k = [&](int j) {
-            const uint32_t dst = base + S::kK + (j & 1) * S::kQBytes + pw * 4 * S::kRowAtoms + sub * 16 + piece * 128;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                bool in;
-                const uint8_t *src = a.k_cache + offset(j, k, &in) + piece * 16;
-#pragma unroll
-                for (int c = 0; c < kC; ++c)
-                    cp_async_16(dst + k * S::kRowAtoms + c * 512, src + c * 64, in ? 16 : 0);
-            }
-            cp_async_commit();
-            if (lane < 2) {
-                const int v = lane ? blk[1] : blk[0];
-                ks = v >= 0 ? __ldg(a.k_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
-                vs = v >= 0 ? __ldg(a.v_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
+                raw[x] = t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
             }
         };
         auto load_v = [&](int j) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                bool in;
-                const uint8_t *src = a.v_cache + offset(j, k, &in) + piece * 16;
+            for (int k = 0; k < 8; ++k) {
+                const int t = tb0 + (t_begin + j) * kTile + vw * 64 + sub + 8 * k;
+                const int v = raw[k >> 1];
+                const bool in = v >= 0 && v < a.num_blocks && t < kv_end && t >= kv_begin;
+                const uint8_t *src = a.v_cache + piece * 16 +
+                                     ((((int64_t)v * a.H_kv + it.h) << a.block_shift) + (t & (a.block_size - 1))) * D;
 #pragma unroll
                 for (int c = 0; c < kC; ++c)
-                    vr[k][c] = in ? *reinterpret_cast<const uint4 *>(src + c * 64) : make_uint4(0, 0, 0, 0);
+                    vr[k][c] = in ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0, 0, 0, 0);
             }
         };
         load_blocks(0);
-        issue_k(0);
         load_v(0);
         if (n > 1)
             load_blocks(1);
         for (int j = 0; j < n; ++j) {
-            cp_async_wait<0>();
-            if (lane < 2) {
-                // a group outside the pool (or past the end): logits of -inf
-                float *sc = scales + (j & 3) * 24 + pw * 2 + lane;
-                sc[0] = ks * scale_log2;
-                sc[8] = vs > 0.f ? lg2_approx(vs) : -INFINITY;
-                sc[16] = vs > 0.f ? __frcp_rn(vs) : 1.f;
-            }
-            fence_async_smem();
-            mbar_arrive(k_full + (j & 1) * 8);
-            if (j + 1 < n) {
-                if (j > 0 && !wait_warp(k_empty + ((j + 1) & 1) * 8, ((j - 1) >> 1) & 1))
-                    break;
-                issue_k(j + 1);
-            }
             if (j > 0 && !wait_warp(v_empty, (j - 1) & 1))
                 break;
             const int tb = tb0 + (t_begin + j) * kTile;
@@ -478,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
                 // reach the others through 0 * NaN: it is taken out and noted for the
                 // rows that see it.
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 8; ++k)
 #pragma unroll
                     for (int c = 0; c < kC; ++c) {
                         uint32_t w[4] = {vr[k][c].x, vr[k][c].y, vr[k][c].z, vr[k][c].w};
@@ -486,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
                         for (int y = 0; y < 4; ++y) {
                             const uint32_t bad = nan_bytes(w[y]);
                             if (bad) {
-                                const int t = tb + pw * 32 + sub + 8 * k;
+                                const int t = tb + vw * 64 + sub + 8 * k;
                                 for (int z = 0; z < 4; ++z)
                                     if (bad >> (8 * z + 7) & 1) {
                                         const int d = (piece + 4 * c) * 16 + 4 * y + z;
@@ -496,16 +546,16 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
                                                 atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
                                         }
                                     }
-                                s_any_nan = 1;
+                                *s_any_nan = 1;
                                 w[y] &= ~((bad >> 7) * 0xFFu);
                             }
                         }
                         vr[k][c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
             }
-            const uint32_t dst = base + S::kV + pw * 4 * S::kVAtoms + sub * 16 + piece * 256;
+            const uint32_t dst = base + S::kV + vw * 8 * S::kVAtoms + sub * 16 + piece * 256;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 8; ++k)
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
                     uint32_t f[8];
@@ -523,7 +573,49 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
             if (j + 2 < n)
                 load_blocks(j + 2);
         }
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
+    } else if (warp == 6) {
+        // ---------------------------------------------------------------- K and the scales
+        const int32_t *table = a.block_table + it.b * a.table_stride;
+        const int pages = kTile >> a.block_shift;
+        float *scales = reinterpret_cast<float *>(smem + S::kScales);
+        auto entry = [&](int j) { // lane g < 8: the table entry of group g
+            const int t = tb0 + (t_begin + j) * kTile + 16 * (lane & 7);
+            const int e = t >> a.block_shift;
+            return t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
+        };
+        int raw = entry(0), issued = 0;
+        for (int j = 0; j < n; ++j) {
+            const int v = raw >= 0 && raw < a.num_blocks ? raw : -1;
+            if (j + 1 < n)
+                raw = entry(j + 1);
+            if (j > 1 && !wait_warp(k_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
+                break;
+            const uint32_t full = k_full + (j & 1) * 8;
+            if (lane == 0)
+                mbar_arrive_expect_tx(full, S::kQBytes);
+            __syncwarp();
+            const int page = __shfl_sync(0xffffffffu, v, (lane << a.block_shift >> 4) & 7);
+            if (lane < pages) // a block outside the pool: rows outside the map, which fills zeros and reads nothing
+                tma_load_3d(base + S::kK + (j & 1) * S::kQBytes + (lane << a.block_shift) * D, &k_map, 0,
+                            page >= 0 ? 0 : a.block_size, page >= 0 ? page * a.H_kv + it.h : 0, full);
+            issued = j + 1;
+            if (lane < 8) {
+                // a group outside the pool (or past the end): logits of -inf
+                const float ks = v >= 0 ? __ldg(a.k_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
+                const float vs = v >= 0 ? __ldg(a.v_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
+                float *sc = scales + (j & 3) * 24 + lane;
+                sc[0] = ks * scale_log2;
+                sc[8] = v >= 0 ? lg2_approx(vs) : -INFINITY;
+                sc[16] = v >= 0 ? __frcp_rn(vs) : 1.f;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(full);
+        }
+        // no copy outlives the block, also where a wait gave up
+        for (int j = max(0, issued - 2); j < issued; ++j)
+            if (!mbar_wait(k_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
+                atomicOr(&g_kv8_error, 2);
     } else if (lane == 0) {
         // ---------------------------------------------------------------- products
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -532,21 +624,22 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
                 atomicOr(&g_kv8_error, 1);
             return ok;
         };
-        const uint64_t q_hi = desc(base + S::kQ, 128, S::kRowAtoms);
-        const uint64_t q_lo = desc(base + S::kQ + S::kQBytes, 128, S::kRowAtoms);
+        const uint64_t q_hi = desc(base + S::kQ, 128, S::kQAtoms);
+        const uint64_t q_lo = desc(base + S::kQ + S::kQBytes, 128, S::kQAtoms);
         const uint64_t v_d = desc(base + S::kV, S::kVAtoms, 128);
         for (int j = 0; j < n; ++j) {
             // P overlays S: the last product of P is done before scores are written there
             if (!wait(k_full + (j & 1) * 8, (j >> 1) & 1) || (j > 0 && !wait(v_empty, (j - 1) & 1)))
                 break;
             fence_after_sync();
-            const uint64_t k_d = desc(base + S::kK + (j & 1) * S::kQBytes, 128, S::kRowAtoms);
+            const uint32_t k_s = base + S::kK + (j & 1) * S::kQBytes;
+            const uint64_t k_d = D == 128 ? desc_sw128(k_s, 16, 1024) : desc_sw64(k_s, 16, 512);
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) // 32 columns: two core matrices of 128 bytes
-                mma_f8(tmem, q_hi + kk * 16, k_d + kk * 16, S::kIdescS, kk > 0);
+            for (int kk = 0; kk < D / 32; ++kk) // 32 columns: two core matrices of Q, 32 bytes of a row of K
+                mma_f8(tmem, q_hi + kk * 16, k_d + kk * 2, S::kIdescS, kk > 0);
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8(tmem, q_lo + kk * 16, k_d + kk * 16, S::kIdescS, 1);
+                mma_f8(tmem, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
             commit(s_full);
             commit(k_empty + (j & 1) * 8);
             if (!wait(v_full, j & 1) || !wait(p_full, j & 1))
@@ -566,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const Kv8AttnArgs
     __syncwarp();
     fence_before_sync();
     __syncthreads();
-    if (warp == 8)
+    if (warp == 7)
         dealloc(tmem, S::kTmem);
 }
 
@@ -648,7 +741,21 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
     if (e != cudaSuccess)
         return e;
-    kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(a, part);
+    // K as blocks of [block_size, D] bytes, the rows swizzled as they land
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr)
+        return cudaErrorNotSupported;
+    CUtensorMap k_map;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.block_size, (cuuint64_t)std::max<int64_t>(1, a.num_blocks * a.H_kv)};
+    const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * a.block_size};
+    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)a.block_size, 1}, step[3] = {1, 1, 1};
+    // (of an empty pool nothing is read: any aligned address will do)
+    void *pool = a.num_blocks > 0 ? const_cast<uint8_t *>(a.k_cache) : const_cast<void *>(a.q);
+    if (encode(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(k_map, a, part);
     if ((e = cudaGetLastError()) != cudaSuccess || part.splits == 1)
         return e;
     kv8_tile_join_kernel<D><<<dim3((unsigned)items, 4), 256, 0, stream>>>(a, part);

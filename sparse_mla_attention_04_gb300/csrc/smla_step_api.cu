@@ -312,7 +312,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     if (p->num_blocks < 0 || p->table_width < 0 || p->table_stride < p->table_width || p->window < 0 ||
         p->q_stride_t < 0 || p->q_stride_h < 0 || !std::isfinite(p->scale))
         return SMLA_ERR_BAD_SHAPE;
-    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > INT_MAX - 256)
+    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > INT_MAX - 256 ||
+        p->num_blocks > INT_MAX / p->H_kv)
         return SMLA_ERR_UNSUPPORTED;
     if (p->T == 0 || p->B == 0)
         return SMLA_OK;
