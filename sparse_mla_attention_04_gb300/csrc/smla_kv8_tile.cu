@@ -7,10 +7,12 @@
 // an SM: one's softmax runs while the other's products do, so each CTA's own
 // chain stays simple: scores, softmax, values, scores, ... Its warps:
 //   0-3  softmax, a row to a thread; the epilogue
-//   4-5  V: codes to registers and, expanded to binary16, to shared memory
-//   6    K: the blocks' codes by TMA as they lie in the cache; the blocks' scales
+//   4-5  V's codes, expanded to binary16
+//   6    the blocks' codes by TMA as they lie in the cache; the blocks' scales
 //   7    one thread issues the tensor-core products
-// (eight warps, so that both CTAs' threads have 128 registers).
+// (eight warps, so that both CTAs' threads have 128 registers). Their loops are
+// kept short, not unrolled: all run at once, and with long straight code each
+// instruction was fetched again every tile (8 to 20 cycles an instruction).
 //
 // S = Q K^T runs on the cache's codes as they are. q's bf16 values are carried
 // exactly by two E4M3 parts: scaled by a power of two to below 2^8, hi = E4M3(q)
@@ -24,10 +26,9 @@
 // denominator adds p' / vs. A row's reference m moves, and its O is rescaled,
 // only when a logit passes it by 8 (p' <= 2^8 is far inside binary16).
 //
-// Shared memory: K in TMA's swizzled rows; Q and V in 8-row x 16-byte core
-// matrices, written so that eight lanes fill one (no bank conflict). Blocks
-// outside the pool and V beyond the visible positions are zero-filled and not
-// read.
+// Shared memory: the codes in TMA's swizzled rows; Q and the expanded V in 8-row
+// x 16-byte core matrices, written so that eight lanes fill one (no bank
+// conflict). Blocks outside the pool are zero-filled and not read.
 #include "smla_kv8.cuh"
 #include "smla_umma.cuh"
 
@@ -50,23 +51,23 @@ constexpr float kSlack = 8.0f;
 constexpr int kMaxSplits = 8;
 
 template <int D> struct Shape {
-    static constexpr int kQBytes = kRows * D;       // one part of Q, or one tile of K codes
+    static constexpr int kQBytes = kRows * D;       // one part of Q, or one tile of codes
     static constexpr int kVBytes = kTile * D * 2;   // a tile of V in binary16
     static constexpr int kQAtoms = D / 16 * 128;    // 8 rows of Q: D / 16 core matrices
     static constexpr int kVAtoms = D / 8 * 128;     // 8 rows of V
     static constexpr int kK = 0;                    // two stages
-    static constexpr int kQ = 2 * kQBytes;          // hi, lo
+    static constexpr int kCodes = 2 * kQBytes;      // V as it comes
+    static constexpr int kQ = 3 * kQBytes;          // hi, lo
     static constexpr int kV = kQ + 2 * kQBytes;
     static constexpr int kScales = kV + kVBytes;    // 4 stages x 8 groups x {c, log2 vs, 1 / vs}
     static constexpr int kBars = kScales + 4 * 8 * 12;
-    static constexpr int kMisc = kBars + 10 * 8;
-    static constexpr int kNan = kMisc + 16;         // a bit for each (row, column)
-    static constexpr int kNanWords = kRows * D / 32;
-    static constexpr int kSmem = kNan + kNanWords * 4 + 1024; // the base is rounded up to 1024
+    static constexpr int kMisc = kBars + 12 * 8;
+    static constexpr int kSmem = kMisc + 16;
     static constexpr uint32_t kTmem = 256;          // S (P over its first half) and O
     static constexpr uint32_t kO = 128;
     static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
     static constexpr uint32_t kIdescO = idesc(128, D, 0, 0, 0, 1);
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
 struct Part {
@@ -150,129 +151,163 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 }
 
 // Waits for this thread's tensor-memory loads; x holds what they brought only after it.
-__device__ __forceinline__ void wait_ld16(uint32_t (&x)[16])
+__device__ __forceinline__ void wait_ld32(uint32_t (&x)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                  : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
-                   "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+                   "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]),
+                   "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]), "+r"(x[23]),
+                   "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27])::"memory");
+    asm volatile("" : "+r"(x[28]), "+r"(x[29]), "+r"(x[30]), "+r"(x[31])::"memory");
 }
 
-// The largest logit of 16 scores of one row. sc: the group's factor of K,
-// sc[8]: log2 of its value scale. kClear: every position is seen; else position
-// t + i is when pos_lo <= t + i <= pos.
-template <bool kClear>
-__device__ __forceinline__ float group_max(const uint32_t (&x)[16], const float *sc, float qs, int t, int pos, int pos_lo)
-{
-    float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[e] = __uint_as_float(x[i + e]);
-            if (!kClear)
-                y[e] = (t + i + e <= pos && t + i + e >= pos_lo) ? y[e] : -INFINITY;
-        }
-        b0 = max3(b0, y[0], y[1]);
-        b1 = max3(b1, y[2], y[3]);
-    }
-    b0 = fmaxf(b0, b1);
-    const float s = fmaf(b0, sc[0] * qs, sc[8]);
-    // (a masked group has no logit; -inf times a factor of 0 would be NaN)
-    return !kClear && b0 == -INFINITY ? b0 : s;
-}
+// What the rows of a tile see of 32 positions.
+struct Sight {
+    int p_first, p_last, all_from, kv_begin; // the tile's: see the kernel
+    int pos, pos_lo;                         // this row: pos_lo <= t <= pos
+    __device__ bool all(int t) const { return t + 31 <= p_first && t >= all_from; }
+    __device__ bool none(int t) const { return t > p_last || t + 31 < kv_begin; }
+    __device__ bool sees(int t) const { return t <= pos && t >= pos_lo; }
+};
 
-// The largest logit of a row's 128 scores (the thread's lane of tensor memory);
-// a group's load is in flight while the one before is looked at.
-template <bool kClear>
-__device__ __forceinline__ float row_max(uint32_t my, const float *sc, float qs, int t0, int pos, int pos_lo)
+// The largest logit of a row's 128 scores (the thread's lane of tensor memory).
+// sc: the factors of the 8 groups of 16, then log2 of their value scales.
+__device__ __forceinline__ float row_max(uint32_t my, const float *sc, float qs, int t0, const Sight &see)
 {
     float top = -INFINITY;
-    uint32_t a[16], b[16];
-    ld16(my, a);
-    wait_ld16(a);
 #pragma unroll 1
-    for (int g = 0; g < 8; g += 2) {
-        ld16(my + g * 16 + 16, b);
-        top = fmaxf(top, group_max<kClear>(a, sc + g, qs, t0 + g * 16, pos, pos_lo));
-        wait_ld16(b);
-        if (g < 6)
-            ld16(my + g * 16 + 32, a);
-        top = fmaxf(top, group_max<kClear>(b, sc + g + 1, qs, t0 + g * 16 + 16, pos, pos_lo));
-        wait_ld16(a);
+    for (int c = 0; c < 4; ++c) {
+        const int t = t0 + c * 32;
+        if (see.none(t))
+            continue;
+        uint32_t x[32];
+        ld32(my + c * 32, x);
+        const float2 f = *reinterpret_cast<const float2 *>(sc + 2 * c), v = *reinterpret_cast<const float2 *>(sc + 8 + 2 * c);
+        wait_ld32(x);
+        if (!see.all(t)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                x[i] = see.sees(t + i) ? x[i] : 0xFF800000u; // -inf
+        }
+        float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            b0 = max3(b0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            b1 = max3(b1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+            b2 = max3(b2, __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
+            b3 = max3(b3, __uint_as_float(x[18 + i]), __uint_as_float(x[19 + i]));
+        }
+        b0 = fmaxf(b0, b1);
+        b2 = fmaxf(b2, b3);
+        // (a masked group has no logit; -inf times a factor of 0 would be NaN)
+        top = fmaxf(top, b0 == -INFINITY ? b0 : fmaf(b0, f.x * qs, v.x));
+        top = fmaxf(top, b2 == -INFINITY ? b2 : fmaf(b2, f.y * qs, v.y));
     }
     return top;
 }
 
-// The weights 2^(s + log2(vs) - ref) of 16 scores, in binary16, written over
-// scores that were read before; their sum divided by vs is added to l. sc[16]:
-// 1 / vs. kPlain: every position is seen and |ref| is small.
-template <bool kPlain>
-__device__ __forceinline__ float group_weights(const uint32_t (&x)[16], uint32_t dst, const float *sc, float qs, float ref,
-                                               float l, int t, int pos, int pos_lo)
+// A row's 128 weights 2^(s + log2(vs) - ref), in binary16, over the scores they
+// come from (a chunk's columns are read before they are written); returns l
+// with their sum, each group's divided by vs (sc[16]: 1 / vs), added.
+// small: |ref| is below 2^20.
+__device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float qs, float ref, float l, int t0,
+                                             const Sight &see, bool small)
 {
-    uint32_t p[8];
-    const float k0 = sc[0] * qs, b0 = sc[8] - ref;
-    const uint64_t kk = pair(k0, k0), bb = pair(b0, b0);
-    uint64_t sum = 0;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
-        float p0, p1;
-        if (kPlain) {
-            unpair(fma2(pair(x0, x1), kk, bb), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-        } else {
-            p0 = ex2_approx(fmaf(x0, k0, sc[8]) - ref);
-            p1 = ex2_approx(fmaf(x1, k0, sc[8]) - ref);
-            p0 = (t + i <= pos && t + i >= pos_lo) ? p0 : 0.f;
-            p1 = (t + i + 1 <= pos && t + i + 1 >= pos_lo) ? p1 : 0.f;
-        }
-        sum = add2(sum, pair(p0, p1));
-        p[i / 2] = pack_f16x2(p0, p1);
-    }
-    st8(dst, p);
-    float s0, s1;
-    unpair(sum, s0, s1);
-    return fmaf(s0 + s1, sc[16], l);
-}
-
-template <bool kPlain>
-__device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float qs, float ref, float l, int t0, int pos,
-                                             int pos_lo)
-{
-    uint32_t a[16], b[16];
-    ld16(my, a);
-    wait_ld16(a);
 #pragma unroll 1
-    for (int g = 0; g < 8; g += 2) {
-        ld16(my + g * 16 + 16, b);
-        l = group_weights<kPlain>(a, my + g * 8, sc + g, qs, ref, l, t0 + g * 16, pos, pos_lo);
-        wait_ld16(b);
-        if (g < 6)
-            ld16(my + g * 16 + 32, a);
-        l = group_weights<kPlain>(b, my + g * 8 + 8, sc + g + 1, qs, ref, l, t0 + g * 16 + 16, pos, pos_lo);
-        wait_ld16(a);
+    for (int c = 0; c < 4; ++c) {
+        const int t = t0 + c * 32;
+        uint32_t p[16];
+        if (see.none(t)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                p[i] = 0;
+            st16(my + c * 16, p);
+            continue;
+        }
+        uint32_t x[32];
+        ld32(my + c * 32, x);
+        const float2 f = *reinterpret_cast<const float2 *>(sc + 2 * c), v = *reinterpret_cast<const float2 *>(sc + 8 + 2 * c),
+                     w = *reinterpret_cast<const float2 *>(sc + 16 + 2 * c);
+        const float k0 = f.x * qs, k1 = f.y * qs;
+        wait_ld32(x);
+        if (small && see.all(t)) {
+            const float b0 = v.x - ref, b1 = v.y - ref;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float e0, e1;
+                unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), i < 16 ? pair(k0, k0) : pair(k1, k1),
+                            i < 16 ? pair(b0, b0) : pair(b1, b1)),
+                       e0, e1);
+                x[i] = __float_as_uint(e0);
+                x[i + 1] = __float_as_uint(e1);
+            }
+        } else {
+            // beyond 2^20, s - m is taken from the rounded logit, as m was, or the rounding of m
+            // alone could pass any bound of p'
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                x[i] = see.sees(t + i) ? __float_as_uint(fmaf(__uint_as_float(x[i]), i < 16 ? k0 : k1, i < 16 ? v.x : v.y) - ref)
+                                       : 0xFF800000u;
+        }
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float p0 = ex2_approx(__uint_as_float(x[i])), p1 = ex2_approx(__uint_as_float(x[i + 1]));
+            sum[i >> 4] = add2(sum[i >> 4], pair(p0, p1));
+            p[i / 2] = pack_f16x2(p0, p1);
+        }
+        st16(my + c * 16, p);
+        float s0, s1, s2, s3;
+        unpair(sum[0], s0, s1);
+        unpair(sum[1], s2, s3);
+        l = fmaf(s0 + s1, w.x, l);
+        l = fmaf(s2 + s3, w.y, l);
     }
     return l;
 }
 
+// Which of the 32 value columns from 32 c on hold a NaN code at a position that
+// the row sees, in the tiles where some rows see positions that others do not
+// (there the codes were taken out, so that 0 * NaN does not reach the others).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map, const Kv8AttnArgs a,
-                                                               const Part part)
+__device__ __noinline__ uint32_t nan_columns(const Kv8AttnArgs &a, const Item &it, const Sight &see, int tb0, int t_begin, int n,
+                                             int c)
+{
+    uint32_t bits = 0;
+    for (int t = max(see.pos_lo, tb0 + t_begin * kTile); t <= see.pos && t < tb0 + (t_begin + n) * kTile; ++t) {
+        const int tile = t & ~(kTile - 1); // (tb0 is a multiple of it)
+        if (tile + kTile - 1 <= see.p_first && tile >= see.all_from)
+            continue;
+        const int e = t >> a.block_shift;
+        const int v = e < a.table_width ? a.block_table[it.b * a.table_stride + e] : -1;
+        if (v < 0 || v >= a.num_blocks)
+            continue;
+        const uint8_t *row = a.v_cache + ((((int64_t)v * a.H_kv + it.h) << a.block_shift) + (t & (a.block_size - 1))) * D + c * 32;
+        for (int i = 0; i < 32; ++i)
+            bits |= (row[i] & 0x7F) == 0x7F ? 1u << i : 0u;
+    }
+    return bits;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
+                                                               const __grid_constant__ CUtensorMap v_map,
+                                                               const Kv8AttnArgs a, const Part part)
 {
     using S = Shape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-    uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + S::kNan);
+    extern __shared__ __align__(1024) uint8_t smem[]; // (the swizzle goes by address)
     int *s_any_nan = reinterpret_cast<int *>(smem + S::kMisc + 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = smem_u32(smem);
+    if (base & 1023u) { // a layout that the swizzle does not fit
+        if (tid == 0)
+            atomicOr(&g_kv8_error, 1);
+        return;
+    }
     const uint32_t bars = base + S::kBars;
-    // K landed / free (two stages), scores ready, P ready, V ready, values done, drained
+    // K landed / free (two stages), scores ready, P ready, V ready, values done, drained, V's codes landed / free
     const uint32_t k_full = bars, k_empty = bars + 16, s_full = bars + 32, p_full = bars + 40, v_full = bars + 48,
-                   v_empty = bars + 56, drained = bars + 64;
+                   v_empty = bars + 56, drained = bars + 64, c_full = bars + 72, c_empty = bars + 80;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     // the longest rows first: a causal prompt's last chunks
@@ -326,11 +361,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         mbar_init(v_full, kVThreads);
         mbar_init(v_empty, 1);
         mbar_init(drained, 1);
+        mbar_init(c_full, 1);
+        mbar_init(c_empty, kVThreads);
         mbar_init_fence();
     }
-    if (many)
-        for (int i = tid; i < S::kNanWords; i += kThreads)
-            s_nan[i] = 0;
     if (warp == 7)
         alloc(smem_u32(tmem_slot), S::kTmem);
     const float scale_log2 = fabsf(a.scale) * kLog2e; // the sign goes into q
@@ -396,10 +430,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         // ---------------------------------------------------------------- softmax
         const int r = tid;
         const int pos = r < rows ? rq.pos((row0 + r) / a.G) : -1;
-        const int pos_lo = a.window > 0 ? pos - a.window + 1 : 0;
+        const Sight see{p_first, p_last, all_from, kv_begin, pos, a.window > 0 ? pos - a.window + 1 : 0};
         const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
         float m = -INFINITY, l = 0.f;
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
             // the scales of this tile's blocks come with its K; then its scores
             if (!wait_warp(k_full + (j & 1) * 8, (j >> 1) & 1) || !wait_warp(s_full, j & 1))
@@ -407,8 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             fence_after_sync();
             const int tb = tb0 + (t_begin + j) * kTile;
             const float *sc = scales + (j & 3) * 24;
-            const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
-            const float top = clear ? row_max<true>(my, sc, qs, 0, 0, 0) : row_max<false>(my, sc, qs, tb, pos, pos_lo);
+            const float top = row_max(my, sc, qs, tb, see);
             const bool raise = top > m + kSlack;
             if (__any_sync(0xffffffffu, raise)) {
                 // O is at rest: the scores just read were issued after its last product was done
@@ -416,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 m = raise ? top : m;
                 l *= f;
                 if (j > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t x[32];
                         ld32(my + S::kO + c * 32, x);
-                        wait_ld();
+                        wait_ld32(x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
@@ -429,10 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            // beyond 2^20, s - m is taken from the rounded logit, as m was, or the rounding
-            // of m alone could pass any bound of p'
-            const bool plain = clear && !__any_sync(0xffffffffu, fabsf(ref) > 0x1p20f);
-            l = plain ? row_weights<true>(my, sc, qs, ref, l, 0, 0, 0) : row_weights<false>(my, sc, qs, ref, l, tb, pos, pos_lo);
+            l = row_weights(my, sc, qs, ref, l, tb, see, !__any_sync(0xffffffffu, fabsf(ref) > 0x1p20f));
             wait_st();
             fence_before_sync();
             mbar_arrive(p_full);
@@ -449,13 +480,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             float lse = 0.f, f = 1.f;
             if (part.splits == 1)
                 f = finish_row(m, l, a.sinks, head, &lse);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
                 ld32(my + S::kO + c * 32, x);
-                wait_ld();
+                wait_ld32(x);
                 if (nans) {
-                    const uint32_t bits = s_nan[(r * D + c * 32) >> 5];
+                    const uint32_t bits = live ? nan_columns<D>(a, it, see, tb0, t_begin, n, c) : 0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         x[i] = (bits >> i & 1) ? 0x7FC00000u : x[i];
@@ -488,116 +519,81 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         }
     } else if (warp < 6) {
         // ---------------------------------------------------------------- V
-        constexpr int kC = D / 64;                   // 16-byte pieces of a row to a lane
-        const int vw = warp - 4;
-        const int sub = lane & 7, piece = lane >> 3; // rows vw * 64 + sub + 8 k, pieces piece + 4 c
-        const int32_t *table = a.block_table + it.b * a.table_stride;
-        int raw[4]; // table entries of the warp's four groups of 16 positions
-        uint4 vr[8][kC];
-        auto load_blocks = [&](int j) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int t = tb0 + (t_begin + j) * kTile + vw * 64 + 16 * x;
-                const int e = t >> a.block_shift;
-                raw[x] = t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
-            }
-        };
-        auto load_v = [&](int j) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int t = tb0 + (t_begin + j) * kTile + vw * 64 + sub + 8 * k;
-                const int v = raw[k >> 1];
-                const bool in = v >= 0 && v < a.num_blocks && t < kv_end && t >= kv_begin;
-                const uint8_t *src = a.v_cache + piece * 16 +
-                                     ((((int64_t)v * a.H_kv + it.h) << a.block_shift) + (t & (a.block_size - 1))) * D;
-#pragma unroll
-                for (int c = 0; c < kC; ++c)
-                    vr[k][c] = in ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        load_blocks(0);
-        load_v(0);
-        if (n > 1)
-            load_blocks(1);
+        const int row_in = (warp - 4) * 64 + (lane & 7), piece = lane >> 3; // rows row_in + 8 k, pieces piece + 4 c
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            if (j > 0 && !wait_warp(v_empty, (j - 1) & 1))
+            if (!wait_warp(c_full, j & 1) || (j > 0 && !wait_warp(v_empty, (j - 1) & 1)))
                 break;
             const int tb = tb0 + (t_begin + j) * kTile;
-            if (many && !(tb + kTile - 1 <= p_first && tb >= all_from)) {
-                // A NaN code at a position that some rows see and others do not must not
-                // reach the others through 0 * NaN: it is taken out and noted for the
-                // rows that see it.
+            const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
+#pragma unroll 2
+            for (int k = 0; k < 8; ++k) {
+                const int r = row_in + 8 * k;
+                const bool in = tb + r < kv_end && tb + r >= kv_begin; // else whatever the block holds there
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-#pragma unroll
-                    for (int c = 0; c < kC; ++c) {
-                        uint32_t w[4] = {vr[k][c].x, vr[k][c].y, vr[k][c].z, vr[k][c].w};
+                for (int c = 0; c < D / 64; ++c) {
+                    const int chunk = piece + 4 * c;
+                    const uint32_t src = base + S::kCodes + r * D + (D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) * 16;
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(src));
+                    if (!clear) {
+                        // A NaN code at a position that some rows see and others do not must not
+                        // reach the others through 0 * NaN: it is taken out, and the rows that
+                        // see it look for it at their end.
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            const uint32_t bad = nan_bytes(w[y]);
+                            w[y] = in ? w[y] : 0;
+                            const uint32_t bad = many ? nan_bytes(w[y]) : 0;
                             if (bad) {
-                                const int t = tb + vw * 64 + sub + 8 * k;
-                                for (int z = 0; z < 4; ++z)
-                                    if (bad >> (8 * z + 7) & 1) {
-                                        const int d = (piece + 4 * c) * 16 + 4 * y + z;
-                                        for (int r = 0; r < rows; ++r) {
-                                            const int p = rq.pos((row0 + r) / a.G);
-                                            if (t <= p && (a.window <= 0 || t > p - a.window))
-                                                atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
-                                        }
-                                    }
                                 *s_any_nan = 1;
                                 w[y] &= ~((bad >> 7) * 0xFFu);
                             }
                         }
-                        vr[k][c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-            }
-            const uint32_t dst = base + S::kV + vw * 8 * S::kVAtoms + sub * 16 + piece * 256;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int c = 0; c < kC; ++c) {
                     uint32_t f[8];
-                    e4m3x4_to_f16x4(vr[k][c].x, f[0], f[1]);
-                    e4m3x4_to_f16x4(vr[k][c].y, f[2], f[3]);
-                    e4m3x4_to_f16x4(vr[k][c].z, f[4], f[5]);
-                    e4m3x4_to_f16x4(vr[k][c].w, f[6], f[7]);
-                    sts128(dst + k * S::kVAtoms + c * 1024, f[0], f[1], f[2], f[3]);
-                    sts128(dst + k * S::kVAtoms + c * 1024 + 128, f[4], f[5], f[6], f[7]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        e4m3x4_to_f16x4(w[y], f[2 * y], f[2 * y + 1]);
+                    const uint32_t dst = base + S::kV + (r >> 3) * S::kVAtoms + (r & 7) * 16 + chunk * 256;
+                    sts128(dst, f[0], f[1], f[2], f[3]);
+                    sts128(dst + 128, f[4], f[5], f[6], f[7]);
                 }
+            }
+            mbar_arrive(c_empty);
             fence_async_smem();
             mbar_arrive(v_full);
-            if (j + 1 < n)
-                load_v(j + 1);
-            if (j + 2 < n)
-                load_blocks(j + 2);
         }
     } else if (warp == 6) {
-        // ---------------------------------------------------------------- K and the scales
+        // ---------------------------------------------------------------- the cache's codes and scales
         const int32_t *table = a.block_table + it.b * a.table_stride;
         const int pages = kTile >> a.block_shift;
         float *scales = reinterpret_cast<float *>(smem + S::kScales);
-        auto entry = [&](int j) { // lane g < 8: the table entry of group g
+        auto entry = [&](int j) { // lanes g and g + 16: the table entry of group g < 8
             const int t = tb0 + (t_begin + j) * kTile + 16 * (lane & 7);
             const int e = t >> a.block_shift;
             return t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
         };
-        int raw = entry(0), issued = 0;
+        int raw = entry(0), issued = 0, v_issued = 0;
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int v = raw >= 0 && raw < a.num_blocks ? raw : -1;
             if (j + 1 < n)
                 raw = entry(j + 1);
+            // lanes p and 16 + p: block p of the tile, for K and for V
+            const int page = __shfl_sync(0xffffffffu, v, ((lane & 15) << a.block_shift >> 4) & 7);
+            // a block outside the pool: rows outside the map, which fills zeros and reads nothing
+            const int y = page >= 0 ? 0 : a.block_size, z = page >= 0 ? page * a.H_kv + it.h : 0;
+            const uint32_t at = ((lane & 15) << a.block_shift) * D;
             if (j > 1 && !wait_warp(k_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
                 break;
             const uint32_t full = k_full + (j & 1) * 8;
             if (lane == 0)
                 mbar_arrive_expect_tx(full, S::kQBytes);
             __syncwarp();
-            const int page = __shfl_sync(0xffffffffu, v, (lane << a.block_shift >> 4) & 7);
-            if (lane < pages) // a block outside the pool: rows outside the map, which fills zeros and reads nothing
-                tma_load_3d(base + S::kK + (j & 1) * S::kQBytes + (lane << a.block_shift) * D, &k_map, 0,
-                            page >= 0 ? 0 : a.block_size, page >= 0 ? page * a.H_kv + it.h : 0, full);
+            if (lane < pages)
+                tma_load_3d(base + S::kK + (j & 1) * S::kQBytes + at, &k_map, 0, y, z, full);
             issued = j + 1;
             if (lane < 8) {
                 // a group outside the pool (or past the end): logits of -inf
@@ -611,11 +607,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(full);
+            if (j > 0 && !wait_warp(c_empty, (j - 1) & 1))
+                break;
+            if (lane == 0)
+                mbar_arrive_expect_tx(c_full, S::kQBytes);
+            __syncwarp();
+            if (lane >= 16 && lane - 16 < pages)
+                tma_load_3d(base + S::kCodes + at, &v_map, 0, y, z, c_full);
+            v_issued = j + 1;
         }
         // no copy outlives the block, also where a wait gave up
         for (int j = max(0, issued - 2); j < issued; ++j)
             if (!mbar_wait(k_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
+        if (v_issued > 0 && !mbar_wait(c_full, (v_issued - 1) & 1) && lane == 0)
+            atomicOr(&g_kv8_error, 2);
     } else if (lane == 0) {
         // ---------------------------------------------------------------- products
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -741,21 +747,23 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
     if (e != cudaSuccess)
         return e;
-    // K as blocks of [block_size, D] bytes, the rows swizzled as they land
+    // the codes as blocks of [block_size, D] bytes, the rows swizzled as they land
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr)
         return cudaErrorNotSupported;
-    CUtensorMap k_map;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.block_size, (cuuint64_t)std::max<int64_t>(1, a.num_blocks * a.H_kv)};
     const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * a.block_size};
     const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)a.block_size, 1}, step[3] = {1, 1, 1};
-    // (of an empty pool nothing is read: any aligned address will do)
-    void *pool = a.num_blocks > 0 ? const_cast<uint8_t *>(a.k_cache) : const_cast<void *>(a.q);
-    if (encode(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(k_map, a, part);
+    CUtensorMap maps[2];
+    for (int i = 0; i < 2; ++i) {
+        // (of an empty pool nothing is read: any aligned address will do)
+        void *pool = a.num_blocks > 0 ? const_cast<uint8_t *>(i ? a.v_cache : a.k_cache) : const_cast<void *>(a.q);
+        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess || part.splits == 1)
         return e;
     kv8_tile_join_kernel<D><<<dim3((unsigned)items, 4), 256, 0, stream>>>(a, part);
