@@ -3,9 +3,10 @@
 // tensor cores (tcgen05), scores and sums in tensor memory.
 //
 // A CTA takes 128 rows (token, head of the kv head's group) of one request and
-// kv head and walks over the visible positions in tiles of 128. Two CTAs share
-// an SM: one's softmax runs while the other's products do, so each CTA's own
-// chain stays simple: scores, softmax, values, scores, ... Its warps:
+// kv head and walks over the visible positions in tiles of 64. Scores have two
+// buffers in tensor memory: while a tile's softmax runs, the next one's scores
+// are computed; two CTAs share an SM, so that the tensor cores have the other's
+// products meanwhile. Warps of a CTA:
 //   0-3  softmax, a row to a thread; the epilogue
 //   4-5  V's codes, expanded to binary16
 //   6    the blocks' codes by TMA as they lie in the cache; the blocks' scales
@@ -23,8 +24,10 @@
 // expanded exactly to binary16: 8-bit weights would lose half of their bits.
 // The block scales enter as in the streaming kernel: K's multiplies the logits,
 // V's is folded into the exponent, p' = 2^(s + log2(vs) - m), and the
-// denominator adds p' / vs. A row's reference m moves, and its O is rescaled,
-// only when a logit passes it by 8 (p' <= 2^8 is far inside binary16).
+// denominator adds p' / vs. A row's reference m moves, and what was added up
+// so far is rescaled, only when a logit passes it by 15 (p' <= 2^15 is inside
+// binary16, whose precision is relative): the scores are read once, with no
+// pass for the maximum before.
 //
 // Shared memory: the codes in TMA's swizzled rows; Q and the expanded V in 8-row
 // x 16-byte core matrices, written so that eight lanes fill one (no bank
@@ -44,27 +47,28 @@ using namespace kv8;
 using namespace umma;
 
 constexpr int kRows = 128;
-constexpr int kTile = 128;
+constexpr int kTile = 64;
 constexpr int kSoftmaxThreads = 128, kVThreads = 64;
 constexpr int kThreads = 256;
-constexpr float kSlack = 8.0f;
+constexpr float kSlack = 15.0f;
 constexpr int kMaxSplits = 8;
 
 template <int D> struct Shape {
-    static constexpr int kQBytes = kRows * D;       // one part of Q, or one tile of codes
+    static constexpr int kQBytes = kRows * D;       // one part of Q
+    static constexpr int kTileBytes = kTile * D;    // one tile of codes
     static constexpr int kVBytes = kTile * D * 2;   // a tile of V in binary16
     static constexpr int kQAtoms = D / 16 * 128;    // 8 rows of Q: D / 16 core matrices
     static constexpr int kVAtoms = D / 8 * 128;     // 8 rows of V
-    static constexpr int kK = 0;                    // two stages
-    static constexpr int kCodes = 2 * kQBytes;      // V as it comes
-    static constexpr int kQ = 3 * kQBytes;          // hi, lo
-    static constexpr int kV = kQ + 2 * kQBytes;
-    static constexpr int kScales = kV + kVBytes;    // 4 stages x 8 groups x {c, log2 vs, 1 / vs}
-    static constexpr int kBars = kScales + 4 * 8 * 12;
-    static constexpr int kMisc = kBars + 12 * 8;
+    static constexpr int kK = 0;                    // four stages
+    static constexpr int kCodes = 4 * kTileBytes;   // V as it comes, two stages
+    static constexpr int kQ = 6 * kTileBytes;       // hi, lo
+    static constexpr int kV = kQ + 2 * kQBytes;     // two stages
+    static constexpr int kScales = kV + 2 * kVBytes; // 8 stages x 4 groups x {c, log2 vs, 1 / vs}
+    static constexpr int kBars = kScales + 8 * 4 * 12;
+    static constexpr int kMisc = kBars + 32 * 8;
     static constexpr int kSmem = kMisc + 16;
-    static constexpr uint32_t kTmem = 256;          // S (P over its first half) and O
-    static constexpr uint32_t kO = 128;
+    static constexpr uint32_t kTmem = 256;          // two S (P over each one's first half) and O
+    static constexpr uint32_t kO = 2 * kTile;
     static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
     static constexpr uint32_t kIdescO = idesc(128, D, 0, 0, 0, 1);
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
@@ -161,6 +165,13 @@ __device__ __forceinline__ void wait_ld32(uint32_t (&x)[32])
     asm volatile("" : "+r"(x[28]), "+r"(x[29]), "+r"(x[30]), "+r"(x[31])::"memory");
 }
 
+__device__ __forceinline__ void wait_ld16(uint32_t (&x)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                   "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+}
+
 // What the rows of a tile see of 32 positions.
 struct Sight {
     int p_first, p_last, all_from, kv_begin; // the tile's: see the kernel
@@ -170,51 +181,23 @@ struct Sight {
     __device__ bool sees(int t) const { return t <= pos && t >= pos_lo; }
 };
 
-// The largest logit of a row's 128 scores (the thread's lane of tensor memory).
-// sc: the factors of the 8 groups of 16, then log2 of their value scales.
-__device__ __forceinline__ float row_max(uint32_t my, const float *sc, float qs, int t0, const Sight &see)
-{
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-        const int t = t0 + c * 32;
-        if (see.none(t))
-            continue;
-        uint32_t x[32];
-        ld32(my + c * 32, x);
-        const float2 f = *reinterpret_cast<const float2 *>(sc + 2 * c), v = *reinterpret_cast<const float2 *>(sc + 8 + 2 * c);
-        wait_ld32(x);
-        if (!see.all(t)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                x[i] = see.sees(t + i) ? x[i] : 0xFF800000u; // -inf
-        }
-        float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            b0 = max3(b0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            b1 = max3(b1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-            b2 = max3(b2, __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
-            b3 = max3(b3, __uint_as_float(x[18 + i]), __uint_as_float(x[19 + i]));
-        }
-        b0 = fmaxf(b0, b1);
-        b2 = fmaxf(b2, b3);
-        // (a masked group has no logit; -inf times a factor of 0 would be NaN)
-        top = fmaxf(top, b0 == -INFINITY ? b0 : fmaf(b0, f.x * qs, v.x));
-        top = fmaxf(top, b2 == -INFINITY ? b2 : fmaf(b2, f.y * qs, v.y));
-    }
-    return top;
-}
+// A row's running sums.
+struct Row {
+    float m, l; // reference (log2 units), denominator relative to it
+};
 
-// A row's 128 weights 2^(s + log2(vs) - ref), in binary16, over the scores they
-// come from (a chunk's columns are read before they are written); returns l
-// with their sum, each group's divided by vs (sc[16]: 1 / vs), added.
-// small: |ref| is below 2^20.
-__device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float qs, float ref, float l, int t0,
-                                             const Sight &see, bool small)
+// One row's 64 scores (the thread's lane of tensor memory at my) become weights
+// 2^(s + log2(vs) - m) in binary16, over the scores they come from (a chunk's
+// columns are read before they are written); their sum, each group's divided by
+// vs, joins l. sc: the factors of the 4 groups of 16, log2 of their value
+// scales, 1 / vs. settle() is called, by the whole warp, before O is rescaled:
+// false where its wait gave up. o_cols: O's columns (0 before the first product).
+template <typename Settle>
+__device__ __forceinline__ bool row_tile(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row &row, int t0,
+                                         const Sight &see, Settle settle)
 {
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kTile / 32; ++c) {
         const int t = t0 + c * 32;
         uint32_t p[16];
         if (see.none(t)) {
@@ -226,11 +209,14 @@ __device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float
         }
         uint32_t x[32];
         ld32(my + c * 32, x);
-        const float2 f = *reinterpret_cast<const float2 *>(sc + 2 * c), v = *reinterpret_cast<const float2 *>(sc + 8 + 2 * c),
-                     w = *reinterpret_cast<const float2 *>(sc + 16 + 2 * c);
+        const float2 f = *reinterpret_cast<const float2 *>(sc + 2 * c), v = *reinterpret_cast<const float2 *>(sc + 4 + 2 * c),
+                     w = *reinterpret_cast<const float2 *>(sc + 8 + 2 * c);
         const float k0 = f.x * qs, k1 = f.y * qs;
+        const float ref = row.m == -INFINITY ? 0.f : row.m;
         wait_ld32(x);
-        if (small && see.all(t)) {
+        float now; // the reference that would make the chunk's largest weight 1
+        float top = -INFINITY, top1 = -INFINITY;
+        if (fabsf(ref) <= 0x1p20f && see.all(t)) {
             const float b0 = v.x - ref, b1 = v.y - ref;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -240,14 +226,59 @@ __device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float
                        e0, e1);
                 x[i] = __float_as_uint(e0);
                 x[i + 1] = __float_as_uint(e1);
+                if (i < 16)
+                    top = max3(top, e0, e1);
+                else
+                    top1 = max3(top1, e0, e1);
             }
+            top = fmaxf(top, top1);
+            now = ref + top;
         } else {
-            // beyond 2^20, s - m is taken from the rounded logit, as m was, or the rounding of m
-            // alone could pass any bound of p'
+            // Also beyond 2^20, where the difference is taken from the rounded logit, as the
+            // reference is: the rounding of m alone could pass any bound of the weights.
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float s = see.sees(t + i) ? fmaf(__uint_as_float(x[i]), i < 16 ? k0 : k1, i < 16 ? v.x : v.y) : -INFINITY;
+                x[i] = __float_as_uint(s - ref);
+                top = fmaxf(top, s);
+            }
+            now = top;
+            top -= ref;
+        }
+        const bool raise = row.m == -INFINITY ? top > -INFINITY : top > kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+            // the row's sums so far, its weights of this tile and its O under the new reference
+            const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - now)) : 1.f;
+            const float d = raise ? now - ref : 0.f;
+            row.m = raise ? now : row.m;
+            row.l *= g;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                x[i] = see.sees(t + i) ? __float_as_uint(fmaf(__uint_as_float(x[i]), i < 16 ? k0 : k1, i < 16 ? v.x : v.y) - ref)
-                                       : 0xFF800000u;
+                x[i] = __float_as_uint(__uint_as_float(x[i]) - d);
+            wait_st();
+            if (c > 0) {
+                ld16(my, p);
+                wait_ld16(p);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&p[i]));
+                    p[i] = pack_f16x2(h.x * g, h.y * g);
+                }
+                st16(my, p);
+            }
+            if (o_cols > 0) {
+                if (!settle())
+                    return false;
+#pragma unroll 1
+                for (int o = 0; o < o_cols; o += 16) {
+                    ld16(my_o + o, p);
+                    wait_ld16(p);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        p[i] = __float_as_uint(__uint_as_float(p[i]) * g);
+                    st16(my_o + o, p);
+                }
+            }
         }
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -260,10 +291,10 @@ __device__ __forceinline__ float row_weights(uint32_t my, const float *sc, float
         float s0, s1, s2, s3;
         unpair(sum[0], s0, s1);
         unpair(sum[1], s2, s3);
-        l = fmaf(s0 + s1, w.x, l);
-        l = fmaf(s2 + s3, w.y, l);
+        row.l = fmaf(s0 + s1, w.x, row.l);
+        row.l = fmaf(s2 + s3, w.y, row.l);
     }
-    return l;
+    return true;
 }
 
 // Which of the 32 value columns from 32 c on hold a NaN code at a position that
@@ -305,9 +336,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         return;
     }
     const uint32_t bars = base + S::kBars;
-    // K landed / free (two stages), scores ready, P ready, V ready, values done, drained, V's codes landed / free
-    const uint32_t k_full = bars, k_empty = bars + 16, s_full = bars + 32, p_full = bars + 40, v_full = bars + 48,
-                   v_empty = bars + 56, drained = bars + 64, c_full = bars + 72, c_empty = bars + 80;
+    // K landed / free (four stages); V's codes landed / free, scores ready, P ready, V ready, values done (two
+    // stages each); scales written (eight stages); drained
+    const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, s_full = bars + 96,
+                   p_full = bars + 112, v_full = bars + 128, v_empty = bars + 144, sc_full = bars + 160, drained = bars + 224;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     // the longest rows first: a causal prompt's last chunks
@@ -352,17 +384,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
 
     if (tid == 0) {
         *s_any_nan = 0;
-        mbar_init(k_full, 2); // the copies' bytes; the scales
-        mbar_init(k_full + 8, 2);
-        mbar_init(k_empty, 1);
-        mbar_init(k_empty + 8, 1);
-        mbar_init(s_full, 1);
-        mbar_init(p_full, kSoftmaxThreads);
-        mbar_init(v_full, kVThreads);
-        mbar_init(v_empty, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(c_full + 8 * i, 1);
+            mbar_init(c_empty + 8 * i, kVThreads);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, kSoftmaxThreads);
+            mbar_init(v_full + 8 * i, kVThreads);
+            mbar_init(v_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 8; ++i)
+            mbar_init(sc_full + 8 * i, 1);
         mbar_init(drained, 1);
-        mbar_init(c_full, 1);
-        mbar_init(c_empty, kVThreads);
         mbar_init_fence();
     }
     if (warp == 7)
@@ -433,43 +469,30 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         const Sight see{p_first, p_last, all_from, kv_begin, pos, a.window > 0 ? pos - a.window + 1 : 0};
         const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
-        float m = -INFINITY, l = 0.f;
+        Row sums{-INFINITY, 0.f};
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            // the scales of this tile's blocks come with its K; then its scores
-            if (!wait_warp(k_full + (j & 1) * 8, (j >> 1) & 1) || !wait_warp(s_full, j & 1))
+            // the scales of this tile's blocks, its scores
+            if (!wait_warp(sc_full + (j & 7) * 8, (j >> 3) & 1) || !wait_warp(s_full + (j & 1) * 8, (j >> 1) & 1))
                 break;
             fence_after_sync();
-            const int tb = tb0 + (t_begin + j) * kTile;
-            const float *sc = scales + (j & 3) * 24;
-            const float top = row_max(my, sc, qs, tb, see);
-            const bool raise = top > m + kSlack;
-            if (__any_sync(0xffffffffu, raise)) {
-                // O is at rest: the scores just read were issued after its last product was done
-                const float f = !raise ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - top));
-                m = raise ? top : m;
-                l *= f;
-                if (j > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t x[32];
-                        ld32(my + S::kO + c * 32, x);
-                        wait_ld32(x);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                        st32(my + S::kO + c * 32, x);
-                    }
-                }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-            l = row_weights(my, sc, qs, ref, l, tb, see, !__any_sync(0xffffffffu, fabsf(ref) > 0x1p20f));
+            // O is at rest once the last tile's product is done: the next one waits for this tile's weights
+            const auto settle = [&] {
+                const bool done = wait_warp(v_empty + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1);
+                fence_after_sync();
+                return done;
+            };
+            if (!row_tile(my + (j & 1) * kTile, my + S::kO, j > 0 ? D : 0, scales + (j & 7) * 12, qs, sums,
+                          tb0 + (t_begin + j) * kTile, see, settle))
+                break;
             wait_st();
             fence_before_sync();
-            mbar_arrive(p_full);
+            mbar_arrive(p_full + (j & 1) * 8);
         }
+        const float m = sums.m, l = sums.l;
         // (V's last arrival carries the notes of NaN codes)
-        if (ok && wait_warp(v_full, (n - 1) & 1) && wait_warp(v_empty, (n - 1) & 1)) {
+        if (ok && wait_warp(v_full + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1) &&
+            wait_warp(v_empty + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1)) {
             fence_after_sync();
             const bool live = r < rows;
             const int rr = row0 + (live ? r : 0);
@@ -519,21 +542,22 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         }
     } else if (warp < 6) {
         // ---------------------------------------------------------------- V
-        const int row_in = (warp - 4) * 64 + (lane & 7), piece = lane >> 3; // rows row_in + 8 k, pieces piece + 4 c
+        const int row_in = (warp - 4) * (kTile / 2) + (lane & 7), piece = lane >> 3; // rows row_in + 8 k, pieces piece + 4 c
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            if (!wait_warp(c_full, j & 1) || (j > 0 && !wait_warp(v_empty, (j - 1) & 1)))
+            const int stage = j & 1;
+            if (!wait_warp(c_full + stage * 8, (j >> 1) & 1) || (j > 1 && !wait_warp(v_empty + stage * 8, ((j >> 1) - 1) & 1)))
                 break;
             const int tb = tb0 + (t_begin + j) * kTile;
             const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
 #pragma unroll 2
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kTile / 16; ++k) {
                 const int r = row_in + 8 * k;
                 const bool in = tb + r < kv_end && tb + r >= kv_begin; // else whatever the block holds there
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     const int chunk = piece + 4 * c;
-                    const uint32_t src = base + S::kCodes + r * D + (D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) * 16;
+                    const uint32_t src = base + S::kCodes + stage * S::kTileBytes + r * D + (D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) * 16;
                     uint32_t w[4];
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
                                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -556,22 +580,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         e4m3x4_to_f16x4(w[y], f[2 * y], f[2 * y + 1]);
-                    const uint32_t dst = base + S::kV + (r >> 3) * S::kVAtoms + (r & 7) * 16 + chunk * 256;
+                    const uint32_t dst = base + S::kV + stage * S::kVBytes + (r >> 3) * S::kVAtoms + (r & 7) * 16 + chunk * 256;
                     sts128(dst, f[0], f[1], f[2], f[3]);
                     sts128(dst + 128, f[4], f[5], f[6], f[7]);
                 }
             }
-            mbar_arrive(c_empty);
+            mbar_arrive(c_empty + stage * 8);
             fence_async_smem();
-            mbar_arrive(v_full);
+            mbar_arrive(v_full + stage * 8);
         }
     } else if (warp == 6) {
         // ---------------------------------------------------------------- the cache's codes and scales
         const int32_t *table = a.block_table + it.b * a.table_stride;
-        const int pages = kTile >> a.block_shift;
+        const int rows_in = min(kTile, a.block_size); // of a block in a tile
+        const int pages = kTile / rows_in;
         float *scales = reinterpret_cast<float *>(smem + S::kScales);
-        auto entry = [&](int j) { // lanes g and g + 16: the table entry of group g < 8
-            const int t = tb0 + (t_begin + j) * kTile + 16 * (lane & 7);
+        auto entry = [&](int j) { // lane: the table entry of group lane & 3 (16 positions)
+            const int t = tb0 + (t_begin + j) * kTile + 16 * (lane & 3);
             const int e = t >> a.block_shift;
             return t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
         };
@@ -582,46 +607,47 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             if (j + 1 < n)
                 raw = entry(j + 1);
             // lanes p and 16 + p: block p of the tile, for K and for V
-            const int page = __shfl_sync(0xffffffffu, v, ((lane & 15) << a.block_shift >> 4) & 7);
+            const int page = __shfl_sync(0xffffffffu, v, ((lane & 15) * rows_in >> 4) & 3);
             // a block outside the pool: rows outside the map, which fills zeros and reads nothing
-            const int y = page >= 0 ? 0 : a.block_size, z = page >= 0 ? page * a.H_kv + it.h : 0;
-            const uint32_t at = ((lane & 15) << a.block_shift) * D;
-            if (j > 1 && !wait_warp(k_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
+            const int y = page >= 0 ? (tb0 + (t_begin + j) * kTile) & (a.block_size - 1) : a.block_size;
+            const int z = page >= 0 ? page * a.H_kv + it.h : 0;
+            const uint32_t at = (lane & 15) * rows_in * D;
+            if (j > 3 && !wait_warp(k_empty + (j & 3) * 8, ((j >> 2) - 1) & 1))
                 break;
-            const uint32_t full = k_full + (j & 1) * 8;
             if (lane == 0)
-                mbar_arrive_expect_tx(full, S::kQBytes);
+                mbar_arrive_expect_tx(k_full + (j & 3) * 8, S::kTileBytes);
             __syncwarp();
             if (lane < pages)
-                tma_load_3d(base + S::kK + (j & 1) * S::kQBytes + at, &k_map, 0, y, z, full);
+                tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, k_full + (j & 3) * 8);
             issued = j + 1;
-            if (lane < 8) {
+            if (lane < 4) {
                 // a group outside the pool (or past the end): logits of -inf
                 const float ks = v >= 0 ? __ldg(a.k_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
                 const float vs = v >= 0 ? __ldg(a.v_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
-                float *sc = scales + (j & 3) * 24 + lane;
+                float *sc = scales + (j & 7) * 12 + lane;
                 sc[0] = ks * scale_log2;
-                sc[8] = v >= 0 ? lg2_approx(vs) : -INFINITY;
-                sc[16] = v >= 0 ? __frcp_rn(vs) : 1.f;
+                sc[4] = v >= 0 ? lg2_approx(vs) : -INFINITY;
+                sc[8] = v >= 0 ? __frcp_rn(vs) : 1.f;
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(full);
-            if (j > 0 && !wait_warp(c_empty, (j - 1) & 1))
+                mbar_arrive(sc_full + (j & 7) * 8);
+            if (j > 1 && !wait_warp(c_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
                 break;
             if (lane == 0)
-                mbar_arrive_expect_tx(c_full, S::kQBytes);
+                mbar_arrive_expect_tx(c_full + (j & 1) * 8, S::kTileBytes);
             __syncwarp();
             if (lane >= 16 && lane - 16 < pages)
-                tma_load_3d(base + S::kCodes + at, &v_map, 0, y, z, c_full);
+                tma_load_3d(base + S::kCodes + (j & 1) * S::kTileBytes + at, &v_map, 0, y, z, c_full + (j & 1) * 8);
             v_issued = j + 1;
         }
         // no copy outlives the block, also where a wait gave up
-        for (int j = max(0, issued - 2); j < issued; ++j)
-            if (!mbar_wait(k_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
+        for (int j = max(0, issued - 4); j < issued; ++j)
+            if (!mbar_wait(k_full + (j & 3) * 8, (j >> 2) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
-        if (v_issued > 0 && !mbar_wait(c_full, (v_issued - 1) & 1) && lane == 0)
-            atomicOr(&g_kv8_error, 2);
+        for (int j = max(0, v_issued - 2); j < v_issued; ++j)
+            if (!mbar_wait(c_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
+                atomicOr(&g_kv8_error, 2);
     } else if (lane == 0) {
         // ---------------------------------------------------------------- products
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -632,29 +658,39 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         };
         const uint64_t q_hi = desc(base + S::kQ, 128, S::kQAtoms);
         const uint64_t q_lo = desc(base + S::kQ + S::kQBytes, 128, S::kQAtoms);
-        const uint64_t v_d = desc(base + S::kV, S::kVAtoms, 128);
-        for (int j = 0; j < n; ++j) {
-            // P overlays S: the last product of P is done before scores are written there
-            if (!wait(k_full + (j & 1) * 8, (j >> 1) & 1) || (j > 0 && !wait(v_empty, (j - 1) & 1)))
-                break;
+        const auto scores = [&](int j) {
+            if (!wait(k_full + (j & 3) * 8, (j >> 2) & 1))
+                return false;
             fence_after_sync();
-            const uint32_t k_s = base + S::kK + (j & 1) * S::kQBytes;
+            const uint32_t k_s = base + S::kK + (j & 3) * S::kTileBytes;
             const uint64_t k_d = D == 128 ? desc_sw128(k_s, 16, 1024) : desc_sw64(k_s, 16, 512);
+            const uint32_t dst = tmem + (j & 1) * kTile;
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) // 32 columns: two core matrices of Q, 32 bytes of a row of K
-                mma_f8(tmem, q_hi + kk * 16, k_d + kk * 2, S::kIdescS, kk > 0);
+                mma_f8(dst, q_hi + kk * 16, k_d + kk * 2, S::kIdescS, kk > 0);
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8(tmem, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
-            commit(s_full);
-            commit(k_empty + (j & 1) * 8);
-            if (!wait(v_full, j & 1) || !wait(p_full, j & 1))
+                mma_f8(dst, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
+            commit(s_full + (j & 1) * 8);
+            commit(k_empty + (j & 3) * 8);
+            return true;
+        };
+        bool go = scores(0) && (n == 1 || scores(1));
+#pragma unroll 1
+        for (int j = 0; go && j < n; ++j) {
+            const int stage = j & 1, phase = (j >> 1) & 1;
+            if (!wait(v_full + stage * 8, phase) || !wait(p_full + stage * 8, phase))
                 break;
             fence_after_sync();
+            const uint64_t v_d = desc(base + S::kV + stage * S::kVBytes, S::kVAtoms, 128);
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk) // 16 positions: 8 columns of P, two atoms of V
-                mma_f16_ts(tmem + S::kO, tmem + kk * 8, v_d + (uint64_t)(kk * 2 * S::kVAtoms / 16), S::kIdescO, j > 0 || kk > 0);
-            commit(v_empty);
+                mma_f16_ts(tmem + S::kO, tmem + stage * kTile + kk * 8, v_d + (uint64_t)(kk * 2 * S::kVAtoms / 16), S::kIdescO,
+                           j > 0 || kk > 0);
+            commit(v_empty + stage * 8);
+            // P lies over its scores: those of two tiles on go there when its product is done
+            if (j + 2 < n && (!wait(v_empty + stage * 8, phase) || !scores(j + 2)))
+                break;
         }
         if (!ok) { // what was issued ends before its memory is given back
             commit(drained);
@@ -753,7 +789,7 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
         return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.block_size, (cuuint64_t)std::max<int64_t>(1, a.num_blocks * a.H_kv)};
     const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * a.block_size};
-    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)a.block_size, 1}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(a.block_size, kTile), 1}, step[3] = {1, 1, 1};
     CUtensorMap maps[2];
     for (int i = 0; i < 2; ++i) {
         // (of an empty pool nothing is read: any aligned address will do)
