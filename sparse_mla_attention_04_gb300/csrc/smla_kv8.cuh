@@ -21,7 +21,7 @@ __device__ __forceinline__ float lg2_approx(float x)
 struct Request {
     int q0, qlen; // its first flat token and how many
     int len;      // positions [0, len) exist
-    int begin;    // positions below it (a multiple of 16) are seen by none of its tokens
+    int begin;    // positions below it (a multiple of 32) are seen by none of its tokens
     __device__ int pos(int i) const { return len - qlen + i; } // may be negative: sees nothing
 };
 
@@ -35,7 +35,7 @@ __device__ __forceinline__ Request request(const Kv8AttnArgs &a, int b)
     r.len = (int)min((long long)max(a.seq_lens[b], 0), (long long)a.table_width << a.block_shift);
     r.begin = 0;
     if (a.window > 0)
-        r.begin = (int)max(0ll, (long long)r.len - r.qlen - a.window + 1) & ~15;
+        r.begin = (int)max(0ll, (long long)r.len - r.qlen - a.window + 1) & ~31;
     return r;
 }
 

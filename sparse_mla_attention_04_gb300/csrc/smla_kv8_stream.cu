@@ -2,7 +2,7 @@
 // sm_103a): every code of K and V crosses the bus once, at HBM's rate.
 //
 // The work is cut evenly, whatever the lengths: a unit is (request, chunk of
-// R = 8 kTiles query rows, kv head), its length in steps of 16 positions plus a
+// R = 8 kTiles query rows, kv head), its length in steps of 32 positions plus a
 // constant for its start and end; the units laid end to end are divided into
 // equal parts, one per block of a grid that fills the GPU once. A block walks
 // its part; a unit that lies in it whole is finished there, one that several
@@ -38,9 +38,10 @@ using namespace kv8;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
-constexpr int kUnitCost = 4;  // a unit's start and end, in steps
-constexpr int kMinPart = 12;  // a block's part, in steps, before more blocks share the work
+constexpr int kStep = 32;     // positions a warp takes at a time
+constexpr int kStages = 2;
+constexpr int kUnitCost = 2;  // a unit's start and end, in steps
+constexpr int kMinPart = 6;   // a block's part, in steps, before more blocks share the work
 constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src, uint32_t src_bytes)
@@ -76,7 +77,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7
 
 // The units of one request and the cost of each.
 struct Units {
-    int steps; // of 16 positions
+    int steps; // of kStep positions
     long long count, cost;
 };
 
@@ -84,7 +85,7 @@ template <int R>
 __device__ __forceinline__ Units units_of(const Kv8AttnArgs &a, const Request &r)
 {
     Units u;
-    u.steps = max(1, (r.len - r.begin + 15) >> 4);
+    u.steps = max(1, (r.len - r.begin + kStep - 1) / kStep);
     u.count = (((long long)r.qlen * a.G + R - 1) / R) * a.H_kv;
     u.cost = u.steps + kUnitCost;
     return u;
@@ -92,12 +93,13 @@ __device__ __forceinline__ Units units_of(const Kv8AttnArgs &a, const Request &r
 
 template <int D, int NT> struct Layout {
     static constexpr int R = 8 * NT;
-    static constexpr int kStageBytes = 16 * 2 * D;              // one step's K and V
+    static constexpr int kHalf = 16 * 2 * D;                    // K and V of 16 positions
+    static constexpr int kStageBytes = kStep / 16 * kHalf;      // one step
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kMerge = kWarps * R * D * 4;           // the warps' value sums at a unit's end
     static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
     static constexpr int kNanWords = R * D / 32;
-    static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 16 + kNanWords * 4;
+    static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 32 + kNanWords * 4;
 };
 
 // The workspace: total units; for each unit {first block, last block, request,
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
     extern __shared__ __align__(16) uint8_t smem[];
     float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kBig);
     float4 *s_meta = reinterpret_cast<float4 *>(smem + L::kBig + kWarps * R * 8);
-    uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 16);
+    uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 32);
     __shared__ long long s_sum[kThreads];
     __shared__ long long s_base;
     __shared__ int s_b;
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
 
     const float scale_log2 = a.scale * kLog2e;
     const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStageBytes;
-    float4 *meta = s_meta + warp * kStages;
+    float4 *meta = s_meta + warp * kStages * 2;
 
     long long at = lo;
     while (at < hi) {
@@ -313,132 +315,150 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             __syncthreads();
         }
 
-        // the lane's table entries: entry first + lane, its scales
+        // the lane's table entry, first + lane: its block (-1: none), the factor of its logits, log2 and
+        // inverse of its value scale (a block outside the pool: logits of -inf, nothing is read)
         const int32_t *row = a.block_table + b * a.table_stride;
         int first = -(1 << 30);
         int e_blk = -1;
-        float e_ks = 0.f, e_vs = 1.f;
+        float e_c = 0.f, e_lv = -INFINITY, e_iv = 1.f;
         const int tok_a = 4 * (g >> 1) + (g & 1); // the tokens of the lane's two K rows: tok_a, tok_a + 2
 
         auto issue = [&](int s, int stage) {
             if (s < s1) {
-                const int tb = rq.begin + s * 16;
+                const int tb = rq.begin + s * kStep;
                 const int e = tb >> a.block_shift;
-                if (e - first >= 32 || e < first) {
+                if (e - first >= 31 || e < first) {
                     first = e;
                     const int x = e + lane;
                     e_blk = x < a.table_width && ((long long)x << a.block_shift) < rq.len ? row[x] : -1;
+                    e_c = 0.f;
+                    e_lv = -INFINITY;
+                    e_iv = 1.f;
                     if (e_blk >= 0 && e_blk < a.num_blocks) {
-                        e_ks = a.k_scale[(int64_t)e_blk * a.H_kv + h];
-                        e_vs = a.v_scale[(int64_t)e_blk * a.H_kv + h];
+                        const float vs = a.v_scale[(int64_t)e_blk * a.H_kv + h];
+                        e_c = a.k_scale[(int64_t)e_blk * a.H_kv + h] * scale_log2;
+                        e_lv = lg2_approx(vs);
+                        e_iv = __frcp_rn(vs);
                     } else {
                         e_blk = -1;
-                        e_ks = 0.f;
-                        e_vs = 1.f;
                     }
                 }
-                const int blk = __shfl_sync(0xffffffffu, e_blk, e - first);
-                const float ks = __shfl_sync(0xffffffffu, e_ks, e - first);
-                const float vs = __shfl_sync(0xffffffffu, e_vs, e - first);
-                if (lane == 0)
-                    meta[stage] = make_float4(ks * scale_log2, lg2_approx(vs), __frcp_rn(vs), blk >= 0 ? 1.f : 0.f);
-                const int64_t off = (((int64_t)max(blk, 0) * a.H_kv + h) << a.block_shift) + (tb & (a.block_size - 1));
-                const uint8_t *kp = a.k_cache + off * D + t4 * 16;
-                const uint8_t *vp = a.v_cache + off * D + g * kV;
-                const uint32_t dst = ring + stage * L::kStageBytes;
-                auto in = [&](int tok) { return blk >= 0 && tb + tok < kv_end && tb + tok >= kv_begin; };
+                const bool inside = tb >= kv_begin && tb + kStep <= kv_end;
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < kStep / 16; ++x) {
+                    const int ex = ((tb + 16 * x) >> a.block_shift) - first;
+                    const int blk = __shfl_sync(0xffffffffu, e_blk, ex);
+                    const float c = __shfl_sync(0xffffffffu, e_c, ex), lv = __shfl_sync(0xffffffffu, e_lv, ex),
+                                iv = __shfl_sync(0xffffffffu, e_iv, ex);
+                    if (lane == 0)
+                        meta[stage * 2 + x] = make_float4(c, lv, iv, 0.f);
+                    const int64_t off = ((((int64_t)max(blk, 0) * a.H_kv + h) << a.block_shift) + ((tb + 16 * x) & (a.block_size - 1))) * D;
+                    const uint8_t *kp = a.k_cache + off + tok_a * D + t4 * 16, *vp = a.v_cache + off + 4 * t4 * D + g * kV;
+                    const uint32_t dk = ring + stage * L::kStageBytes + x * L::kHalf + lane * 16,
+                                   dv = ring + stage * L::kStageBytes + x * L::kHalf + 16 * D + lane * kV;
+                    if (inside && blk >= 0) {
 #pragma unroll
-                    for (int hh = 0; hh < kH; ++hh) {
-                        const int tok = tok_a + 2 * x;
-                        const bool ok = in(tok);
-                        cp_async_16(dst + ((x * kH + hh) * 32 + lane) * 16, kp + (ok ? tok : 0) * D + hh * 64, ok ? 16 : 0);
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int hh = 0; hh < kH; ++hh)
+                                cp_async_16(dk + (y * kH + hh) * 512, kp + 2 * y * D + hh * 64, 16);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            if (D == 128)
+                                cp_async_16(dv + y * 32 * kV, vp + y * D, 16);
+                            else
+                                cp_async_8(dv + y * 32 * kV, vp + y * D, 8);
+                        }
+                    } else {
+                        // at the ends of what is seen: zeros where nothing is read
+                        auto in = [&](int tok) { return blk >= 0 && tb + 16 * x + tok < kv_end && tb + 16 * x + tok >= kv_begin; };
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int hh = 0; hh < kH; ++hh) {
+                                const bool ok = in(tok_a + 2 * y);
+                                cp_async_16(dk + (y * kH + hh) * 512, ok ? kp + 2 * y * D + hh * 64 : a.k_cache, ok ? 16 : 0);
+                            }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const bool ok = in(4 * t4 + y);
+                            if (D == 128)
+                                cp_async_16(dv + y * 32 * kV, ok ? vp + y * D : a.v_cache, ok ? 16 : 0);
+                            else
+                                cp_async_8(dv + y * 32 * kV, ok ? vp + y * D : a.v_cache, ok ? 8 : 0);
+                        }
                     }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int tok = 4 * t4 + x;
-                    const bool ok = in(tok);
-                    const uint32_t d = dst + 16 * D + (x * 32 + lane) * kV;
-                    if (D == 128)
-                        cp_async_16(d, vp + (ok ? tok : 0) * D, ok ? 16 : 0);
-                    else
-                        cp_async_8(d, vp + (ok ? tok : 0) * D, ok ? 8 : 0);
                 }
             }
             cp_async_commit();
         };
 
         const int n_mine = (s1 - s0 - warp + kWarps - 1) / kWarps; // steps s0 + warp + 4 k
-        for (int k = 0; k < kStages - 1; ++k)
+        for (int k = 0; k < kStages; ++k)
             issue(s0 + warp + k * kWarps, k);
         for (int k = 0; k < n_mine; ++k) {
-            cp_async_wait<kStages - 2>();
+            cp_async_wait<kStages - 1>();
             __syncwarp(); // lane 0's scales
             const int stage = k % kStages;
             const int s = s0 + warp + k * kWarps;
-            const int tb = rq.begin + s * 16;
-            const float4 mt = meta[stage];
+            const int tb = rq.begin + s * kStep;
             const uint32_t src = ring + stage * L::kStageBytes;
 
-            float sc[NT][4];
+            float sc[2][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+            for (int x = 0; x < 2; ++x) {
+                float odd[NT][4]; // every other k-step: two chains of products
 #pragma unroll
-            for (int hh = 0; hh < kH; ++hh) {
-                const uint4 ka = lds128(src + (hh * 32 + lane) * 16), kb = lds128(src + ((kH + hh) * 32 + lane) * 16);
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t f[4];
-                    e4m3x4_to_f16x4(wa[w], f[0], f[2]);
-                    e4m3x4_to_f16x4(wb[w], f[1], f[3]);
+                    for (int e = 0; e < 4; ++e)
+                        sc[x][nt][e] = odd[nt][e] = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16_16816(sc[nt], f, qf[nt][hh * 4 + w][0], qf[nt][hh * 4 + w][1]);
+                for (int hh = 0; hh < kH; ++hh) {
+                    const uint4 ka = lds128(src + x * L::kHalf + (hh * 32 + lane) * 16),
+                                kb = lds128(src + x * L::kHalf + ((kH + hh) * 32 + lane) * 16);
+                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t f[4];
+                        e4m3x4_to_f16x4(wa[w], f[0], f[2]);
+                        e4m3x4_to_f16x4(wb[w], f[1], f[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16_16816(w & 1 ? odd[nt] : sc[x][nt], f, qf[nt][hh * 4 + w][0], qf[nt][hh * 4 + w][1]);
+                    }
                 }
-            }
-            uint32_t vw[4][kV / 4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (D == 128) {
-                    const uint4 v = lds128(src + 16 * D + (x * 32 + lane) * kV);
-                    vw[x][0] = v.x;
-                    vw[x][1] = v.y;
-                    vw[x][(kV / 4) - 2] = v.z;
-                    vw[x][(kV / 4) - 1] = v.w;
-                } else {
-                    const uint2 v = lds64(src + 16 * D + (x * 32 + lane) * kV);
-                    vw[x][0] = v.x;
-                    vw[x][1] = v.y;
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[x][nt][e] += odd[nt][e];
             }
-            // the ring's next stage is issued here: the stage it overwrites was read in the last turn
-            issue(s0 + warp + (k + kStages - 1) * kWarps, (k + kStages - 1) % kStages);
-
-            const bool clear = mt.w != 0.f && tb + 15 <= p_first && tb >= all_from && tb + 15 < rq.len && rows == R;
+            const float4 mt[2] = {meta[stage * 2], meta[stage * 2 + 1]};
+            const bool clear = tb + kStep - 1 <= p_first && tb >= all_from && rows == R;
             bool raise = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = sc[nt][e] * (mt.x * cscale[nt][e & 1]) + mt.y;
-                    if (!clear) {
-                        const int j = tb + tok_a + (e & 2);
-                        const int p = pos[nt][e & 1];
-                        if (!(mt.w != 0.f && j <= p && j < rq.len && (a.window <= 0 || j > p - a.window)))
-                            x = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y = fmaf(sc[x][nt][e], mt[x].x * cscale[nt][e & 1], mt[x].y);
+                        if (!clear) {
+                            const int j = tb + 16 * x + tok_a + (e & 2);
+                            const int p = pos[nt][e & 1];
+                            if (!(j <= p && (a.window <= 0 || j > p - a.window)))
+                                y = -INFINITY;
+                        }
+                        sc[x][nt][e] = y;
+                        raise |= y > m[nt][e & 1] + kSlack;
                     }
-                    sc[nt][e] = x;
-                    raise |= x > m[nt][e & 1] + kSlack;
-                }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
+                        float x = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -453,54 +473,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                         }
                     }
             }
-            uint32_t pf[NT][2];
+            uint32_t pf[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-                const float p0 = ex2_approx(sc[nt][0] - m0), p1 = ex2_approx(sc[nt][1] - m1);
-                const float p2 = ex2_approx(sc[nt][2] - m0), p3 = ex2_approx(sc[nt][3] - m1);
-                l[nt][0] += (p0 + p2) * mt.z;
-                l[nt][1] += (p1 + p3) * mt.z;
-                pf[nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
-                pf[nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
-            }
-            // A NaN code of V at a position that some rows see and others do not
-            // must not reach the others through 0 * NaN: it is taken out and
-            // noted for the rows that see it.
-            if (many && !clear) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int j = tb + 4 * t4 + x;
-#pragma unroll
-                    for (int w = 0; w < kV / 4; ++w) {
-                        const uint32_t bad = nan_bytes(vw[x][w]);
-                        if (bad) {
-                            for (int y = 0; y < 4; ++y)
-                                if (bad >> (8 * y + 7) & 1) {
-                                    const int d = kV * g + 4 * w + y;
-                                    for (int r = 0; r < rows; ++r) {
-                                        const int p = rq.pos((row0 + r) / a.G);
-                                        if (j <= p && j < rq.len && (a.window <= 0 || j > p - a.window))
-                                            atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
-                                    }
-                                }
-                            vw[x][w] &= ~((bad >> 7) * 0xFFu);
-                        }
-                    }
+                for (int x = 0; x < 2; ++x) {
+                    const float p0 = ex2_approx(sc[x][nt][0] - m0), p1 = ex2_approx(sc[x][nt][1] - m1);
+                    const float p2 = ex2_approx(sc[x][nt][2] - m0), p3 = ex2_approx(sc[x][nt][3] - m1);
+                    l[nt][0] += (p0 + p2) * mt[x].z;
+                    l[nt][1] += (p1 + p3) * mt[x].z;
+                    pf[x][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                    pf[x][nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kM; ++i) {
-                // value columns kV g + 2 i (row g of the tile) and + 1 (row g + 8)
-                const int w = i >> 1;
-                uint32_t f[4];
-                const uint32_t sel = (i & 1) ? 0x7362 : 0x5140;
-                e4m3x4_to_f16x4(__byte_perm(vw[0][w], vw[1][w], sel), f[0], f[1]);
-                e4m3x4_to_f16x4(__byte_perm(vw[2][w], vw[3][w], sel), f[2], f[3]);
+            for (int x = 0; x < 2; ++x) {
+                uint32_t vw[4][kV / 4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16_16816(o[i][nt], f, pf[nt][0], pf[nt][1]);
+                for (int y = 0; y < 4; ++y) {
+                    if (D == 128) {
+                        const uint4 v = lds128(src + x * L::kHalf + 16 * D + (y * 32 + lane) * kV);
+                        vw[y][0] = v.x;
+                        vw[y][1] = v.y;
+                        vw[y][(kV / 4) - 2] = v.z;
+                        vw[y][(kV / 4) - 1] = v.w;
+                    } else {
+                        const uint2 v = lds64(src + x * L::kHalf + 16 * D + (y * 32 + lane) * kV);
+                        vw[y][0] = v.x;
+                        vw[y][1] = v.y;
+                    }
+                }
+                // A NaN code of V at a position that some rows see and others do not
+                // must not reach the others through 0 * NaN: it is taken out and
+                // noted for the rows that see it.
+                if (many && !clear) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int j = tb + 16 * x + 4 * t4 + y;
+#pragma unroll
+                        for (int w = 0; w < kV / 4; ++w) {
+                            const uint32_t bad = nan_bytes(vw[y][w]);
+                            if (bad) {
+                                for (int z = 0; z < 4; ++z)
+                                    if (bad >> (8 * z + 7) & 1) {
+                                        const int d = kV * g + 4 * w + z;
+                                        for (int r = 0; r < rows; ++r) {
+                                            const int p = rq.pos((row0 + r) / a.G);
+                                            if (j <= p && (a.window <= 0 || j > p - a.window))
+                                                atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
+                                        }
+                                    }
+                                vw[y][w] &= ~((bad >> 7) * 0xFFu);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kM; ++i) {
+                    // value columns kV g + 2 i (row g of the tile) and + 1 (row g + 8)
+                    const int w = i >> 1;
+                    uint32_t f[4];
+                    const uint32_t sel = (i & 1) ? 0x7362 : 0x5140;
+                    e4m3x4_to_f16x4(__byte_perm(vw[0][w], vw[1][w], sel), f[0], f[1]);
+                    e4m3x4_to_f16x4(__byte_perm(vw[2][w], vw[3][w], sel), f[2], f[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16_16816(o[i][nt], f, pf[x][nt][0], pf[x][nt][1]);
+                }
             }
+            // the stage is free: each lane has used what it copied, all have read the scales
+            __syncwarp();
+            issue(s0 + warp + (k + kStages) * kWarps, stage);
         }
         asm volatile("cp.async.wait_all;\n" ::: "memory");
 
