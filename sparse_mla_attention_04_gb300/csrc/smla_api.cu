@@ -462,7 +462,7 @@ SMLA_API smla_status smla_device_error(int *code, int reset)
 {
     if (code == nullptr)
         return SMLA_ERR_NULL_POINTER;
-    int c16 = 0, cw = 0, cp = 0, cg = 0, cl = 0, cr = 0, ca = 0, ck = 0;
+    int c16 = 0, cw = 0, cp = 0, cg = 0, cl = 0, cr = 0, ca = 0, ck = 0, cs = 0;
     if (const cudaError_t e = smla::read_umma_error(&c16, reset != 0); e != cudaSuccess)
         return cuda_status(e);
     if (const cudaError_t e = smla::read_lean_error(&cl, reset != 0); e != cudaSuccess)
@@ -479,7 +479,9 @@ SMLA_API smla_status smla_device_error(int *code, int reset)
         return cuda_status(e);
     if (const cudaError_t e = smla::read_kv8_error(&ck, reset != 0); e != cudaSuccess)
         return cuda_status(e);
-    *code = c16 | cw | cp | cg | cl | cr | ca | ck;
+    if (const cudaError_t e = smla::read_kv8_stream_error(&cs, reset != 0); e != cudaSuccess)
+        return cuda_status(e);
+    *code = c16 | cw | cp | cg | cl | cr | ca | ck | cs;
     return SMLA_OK;
 }
 

@@ -39,6 +39,73 @@ __device__ __forceinline__ Request request(const Kv8AttnArgs &a, int b)
     return r;
 }
 
+// q's rows as two E4M3 parts: the power of two that brings a row below 2^8, and
+// its inverse (NaN for a row with an infinity, which has no finite logit).
+__device__ __forceinline__ void split_scale(float amax, float &up, float &down)
+{
+    const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 127);
+    up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+    down = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + e - 7) << 23);
+}
+
+// The largest |x| of eight bf16 values (NaN loses).
+__device__ __forceinline__ float amax8(const uint4 &v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+    return m;
+}
+
+// Eight bf16 values times `up` as E4M3 codes: hi = E4M3(x) and lo = E4M3(x - hi).
+__device__ __forceinline__ void split8(const uint4 &v, float up, uint32_t (&hi)[2], uint32_t (&lo)[2])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * i]));
+        float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * i + 1]));
+        a = make_float2(a.x * up, a.y * up);
+        b = make_float2(b.x * up, b.y * up);
+        hi[i] = (__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) & 0xFFFFu) |
+                ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
+        uint32_t f0, f1;
+        e4m3x4_to_f16x4(hi[i], f0, f1);
+        const float2 ha = __half22float2(*reinterpret_cast<const __half2 *>(&f0));
+        const float2 hb = __half22float2(*reinterpret_cast<const __half2 *>(&f1));
+        lo[i] = (__nv_cvt_float2_to_fp8x2(make_float2(a.x - ha.x, a.y - ha.y), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu) |
+                ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(b.x - hb.x, b.y - hb.y), __NV_SATFINITE, __NV_E4M3) << 16);
+    }
+}
+
+// Tensor maps of the two caches as blocks of [block_size, D] codes, copied
+// min(block_size, most_rows) rows at a time into swizzled rows of D bytes. False
+// where the driver has no encoder or refuses. (Of an empty pool nothing is read:
+// any aligned address will do.)
+inline bool kv8_tensor_maps(const Kv8AttnArgs &a, int D, int most_rows, CUtensorMap (&maps)[2])
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr)
+        return false;
+    const int64_t blocks = a.num_blocks * a.H_kv;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.block_size, (cuuint64_t)(blocks > 0 ? blocks : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * a.block_size};
+    const cuuint32_t rows = (cuuint32_t)(a.block_size < most_rows ? a.block_size : most_rows);
+    const cuuint32_t box[3] = {(cuuint32_t)D, rows, 1}, step[3] = {1, 1, 1};
+    for (int i = 0; i < 2; ++i) {
+        void *pool = blocks > 0 ? const_cast<uint8_t *>(i ? a.v_cache : a.k_cache) : const_cast<void *>(a.q);
+        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    return true;
+}
+
 // The final values of a row from its sums: m the reference (log2 units), l the
 // softmax denominator relative to it. Returns the factor for the value sums.
 __device__ __forceinline__ float finish_row(float m, float l, const float *sinks, int head, float *lse)

@@ -11,19 +11,23 @@
 // knowing the lengths, so a captured call follows them.
 //
 // In a block the four warps take a unit's steps in turn, each with its own
-// softmax state and its own asynchronous copies: nothing is waited for between
-// warps until a unit ends. Each lane copies (16-byte cp.async) just the bytes
-// it will use itself, so its part of the ring in shared memory is an extension
-// of its registers: no barrier, no bank conflict.
+// softmax state and its own ring of TMA copies: nothing is waited for between
+// warps until a unit ends. Copies land in TMA's swizzled rows, and the order of
+// a step's positions in the products is chosen so that eight lanes' 16-byte
+// reads of K and of V both fall on different banks.
 //
-// Arithmetic: S^T = K Q^T and O^T = V^T P^T by warp-level m16n8k16 products in
-// binary16 with binary32 sums: the tokens (for S) and the value columns (for O)
-// fill the 16 rows, 8 query rows the columns, which wastes nothing for the 4 to
-// 16 query heads of a kv head. Codes expand to binary16 exactly. The order of
-// a product's inner index is free, so it is chosen for the loads: a lane's 16
-// bytes of a K row are four k-steps of its fragment, and its 16 bytes of four
-// V rows are its whole V^T fragment. q is scaled by a power of two so that
-// binary16 holds its bf16 values exactly down to 2^-28 of the row's largest.
+// Arithmetic: S^T = K Q^T and O^T = V^T P^T by warp-level products with binary32
+// sums: the tokens (for S) and the value columns (for O) fill the 16 rows, 8
+// query rows the columns, which wastes nothing for the 4 to 16 query heads of a
+// kv head. S runs on the cache's codes as they are (m16n8k32): q's bf16 values
+// are carried by two E4M3 parts, exactly down to 2^-9 of the row's largest
+// (smaller ones to 2^-17 of it), and two such products take the time of one in
+// binary16 (4.4 against 8.7 cycles each) without expanding K. V's codes are
+// expanded to binary16, exactly, as are not the weights: 8-bit parts of a weight
+// lose those far below the largest, of which a long context has many. The order
+// of a product's inner index is free, so it is chosen for the loads: a lane's 16
+// bytes of a K row are two k-steps of its fragment, and its 16 bytes of four V
+// rows are its whole V^T fragment.
 // The block scales: K's multiplies the logits, V's is folded into the exponent,
 // p' = 2^(s + log2(vs) - m), so p' <= 2^8 needs no other range, and the
 // denominator adds p' / vs. The reference m moves only when a logit passes it
@@ -32,6 +36,9 @@
 #include "smla_umma.cuh"
 
 namespace smla {
+
+__device__ int g_kv8_stream_error = 0; // 1: a bounded wait gave up; 2: copies in flight did not land
+
 namespace {
 
 using namespace kv8;
@@ -43,11 +50,6 @@ constexpr int kStages = 2;
 constexpr int kUnitCost = 2;  // a unit's start and end, in steps
 constexpr int kMinPart = 6;   // a block's part, in steps, before more blocks share the work
 constexpr float kSlack = 8.0f;
-
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void *src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
 {
@@ -93,13 +95,13 @@ __device__ __forceinline__ Units units_of(const Kv8AttnArgs &a, const Request &r
 
 template <int D, int NT> struct Layout {
     static constexpr int R = 8 * NT;
-    static constexpr int kHalf = 16 * 2 * D;                    // K and V of 16 positions
-    static constexpr int kStageBytes = kStep / 16 * kHalf;      // one step
+    static constexpr int kSide = kStep * D;                     // K (or V) of one step
+    static constexpr int kStageBytes = 2 * kSide;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kMerge = kWarps * R * D * 4;           // the warps' value sums at a unit's end
     static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
     static constexpr int kNanWords = R * D / 32;
-    static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 32 + kNanWords * 4;
+    static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 32 + kNanWords * 4 + kWarps * kStages * 8;
 };
 
 // The workspace: total units; for each unit {first block, last block, request,
@@ -112,18 +114,20 @@ struct Part {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(const Kv8AttnArgs a, const Part part)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(const __grid_constant__ CUtensorMap k_map,
+                                                                                const __grid_constant__ CUtensorMap v_map,
+                                                                                const Kv8AttnArgs a, const Part part)
 {
     using L = Layout<D, NT>;
     constexpr int R = L::R;
     constexpr int kH = D / 64;      // 16-byte pieces of a lane's K row
     constexpr int kV = D / 8;       // bytes of a lane's V row
     constexpr int kM = D / 16;      // 16-row tiles of the value columns
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kBig);
     float4 *s_meta = reinterpret_cast<float4 *>(smem + L::kBig + kWarps * R * 8);
     uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 32);
-    __shared__ long long s_sum[kThreads];
+    long long *s_sum = reinterpret_cast<long long *>(smem); // before the ring is used
     __shared__ long long s_base;
     __shared__ int s_b;
 
@@ -206,7 +210,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             unit0 += s_sum[i];
     }
 
+    umma::fence_async_smem();
+    __syncthreads(); // the sums were read: the ring is free for copies
     const float scale_log2 = a.scale * kLog2e;
+    const uint32_t full = smem_u32(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 32 + L::kNanWords * 4) + warp * kStages * 8;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i)
+            umma::mbar_init(full + 8 * i, 1);
+        umma::mbar_init_fence();
+    }
+    __syncwarp();
+    uint32_t phases = 0; // bit i: the parity that stage i's next copies complete
+    bool ok = (smem_u32(smem) & 1023u) == 0; // (the swizzle goes by address)
+    if (!ok && tid == 0)
+        atomicOr(&g_kv8_stream_error, 1);
+    const int rows_in = min(kStep, a.block_size), pages = kStep / rows_in; // of a block in a step; blocks of a step
     const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStageBytes;
     float4 *meta = s_meta + warp * kStages * 2;
 
@@ -246,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         const bool many = p_first != p_last;
 
         // this lane's part of Q: fragment column g of each tile, and the factors of its columns 2 t4, 2 t4 + 1
-        uint32_t qf[NT][4 * kH][2];
+        uint32_t qf[NT][2 * kH][2][2]; // k-step, part (hi, lo), register
         float qscale[NT];
         int pos[NT][2];
         float cscale[NT][2];
@@ -265,30 +283,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                 for (int e = 0; e < 2; ++e) {
                     v[hh][e] = r < rows ? *reinterpret_cast<const uint4 *>(qr + hh * 64 + t4 * 16 + e * 8)
                                         : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[4] = {v[hh][e].x, v[hh][e].y, v[hh][e].z, v[hh][e].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
+                    amax = fmaxf(amax, amax8(v[hh][e]));
                 }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // q times 2^(14 - e), e the exponent of the largest: below 2^15 in binary16
-            const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
-            const float up = __uint_as_float((uint32_t)(127 + 14 - min(e, 127)) << 23);
-            qscale[nt] = __uint_as_float((uint32_t)(127 + min(e, 127) - 14) << 23);
+            float up;
+            split_scale(amax, up, qscale[nt]);
 #pragma unroll
             for (int hh = 0; hh < kH; ++hh)
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint4 &x = v[hh][w >> 1];
-                    const uint32_t lo2 = (w & 1) ? x.z : x.x, hi2 = (w & 1) ? x.w : x.y;
-                    const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&lo2));
-                    const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&hi2));
-                    qf[nt][hh * 4 + w][0] = pack_f16x2(f0.x * up, f0.y * up);
-                    qf[nt][hh * 4 + w][1] = pack_f16x2(f1.x * up, f1.y * up);
-                }
+                for (int e = 0; e < 2; ++e)
+                    split8(v[hh][e], up, qf[nt][hh * 2 + e][0], qf[nt][hh * 2 + e][1]);
 #pragma unroll
             for (int e2 = 0; e2 < 2; ++e2) {
                 cscale[nt][e2] = __shfl_sync(0xffffffffu, qscale[nt], 4 * (2 * t4 + e2));
@@ -321,7 +326,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         int first = -(1 << 30);
         int e_blk = -1;
         float e_c = 0.f, e_lv = -INFINITY, e_iv = 1.f;
-        const int tok_a = 4 * (g >> 1) + (g & 1); // the tokens of the lane's two K rows: tok_a, tok_a + 2
+        // Position 8 i + tau(j) of a step is number j of its i-th eight: tau(2 t + e) = (2 t ^ 4 e) | e. The
+        // rows of lanes g = 2 t and 2 t + 1 (K) then differ in bit 2, those of the four t (V) in bits 1 and
+        // 2, so that with the swizzle eight lanes read eight different 16-byte columns.
+        const int tau_g = ((g & 6) ^ (4 * (g & 1))) | (g & 1);
+        const int tau_t[2] = {2 * t4, (2 * t4 ^ 4) | 1};
 
         auto issue = [&](int s, int stage) {
             if (s < s1) {
@@ -343,63 +352,40 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                         e_blk = -1;
                     }
                 }
-                const bool inside = tb >= kv_begin && tb + kStep <= kv_end;
+                if (lane == 0)
+                    umma::mbar_arrive_expect_tx(full + 8 * stage, L::kStageBytes);
 #pragma unroll
-                for (int x = 0; x < kStep / 16; ++x) {
+                for (int x = 0; x < 2; ++x) {
                     const int ex = ((tb + 16 * x) >> a.block_shift) - first;
-                    const int blk = __shfl_sync(0xffffffffu, e_blk, ex);
                     const float c = __shfl_sync(0xffffffffu, e_c, ex), lv = __shfl_sync(0xffffffffu, e_lv, ex),
                                 iv = __shfl_sync(0xffffffffu, e_iv, ex);
                     if (lane == 0)
                         meta[stage * 2 + x] = make_float4(c, lv, iv, 0.f);
-                    const int64_t off = ((((int64_t)max(blk, 0) * a.H_kv + h) << a.block_shift) + ((tb + 16 * x) & (a.block_size - 1))) * D;
-                    const uint8_t *kp = a.k_cache + off + tok_a * D + t4 * 16, *vp = a.v_cache + off + 4 * t4 * D + g * kV;
-                    const uint32_t dk = ring + stage * L::kStageBytes + x * L::kHalf + lane * 16,
-                                   dv = ring + stage * L::kStageBytes + x * L::kHalf + 16 * D + lane * kV;
-                    if (inside && blk >= 0) {
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-#pragma unroll
-                            for (int hh = 0; hh < kH; ++hh)
-                                cp_async_16(dk + (y * kH + hh) * 512, kp + 2 * y * D + hh * 64, 16);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            if (D == 128)
-                                cp_async_16(dv + y * 32 * kV, vp + y * D, 16);
-                            else
-                                cp_async_8(dv + y * 32 * kV, vp + y * D, 8);
-                        }
-                    } else {
-                        // at the ends of what is seen: zeros where nothing is read
-                        auto in = [&](int tok) { return blk >= 0 && tb + 16 * x + tok < kv_end && tb + 16 * x + tok >= kv_begin; };
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-#pragma unroll
-                            for (int hh = 0; hh < kH; ++hh) {
-                                const bool ok = in(tok_a + 2 * y);
-                                cp_async_16(dk + (y * kH + hh) * 512, ok ? kp + 2 * y * D + hh * 64 : a.k_cache, ok ? 16 : 0);
-                            }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const bool ok = in(4 * t4 + y);
-                            if (D == 128)
-                                cp_async_16(dv + y * 32 * kV, ok ? vp + y * D : a.v_cache, ok ? 16 : 0);
-                            else
-                                cp_async_8(dv + y * 32 * kV, ok ? vp + y * D : a.v_cache, ok ? 8 : 0);
-                        }
-                    }
                 }
+                __syncwarp();
+                // lanes p and 16 + p: block p of the step, for K and for V. A block outside the pool: rows
+                // outside the map, which fills zeros and reads nothing.
+                const int p = lane & 15;
+                const int blk = __shfl_sync(0xffffffffu, e_blk, ((tb + (p < pages ? p : 0) * rows_in) >> a.block_shift) - first);
+                if (p < pages)
+                    umma::tma_load_3d(ring + stage * L::kStageBytes + (lane >> 4) * L::kSide + p * rows_in * D,
+                                      lane < 16 ? &k_map : &v_map, 0, blk >= 0 ? tb & (a.block_size - 1) : a.block_size,
+                                      blk >= 0 ? blk * a.H_kv + h : 0, full + 8 * stage);
             }
-            cp_async_commit();
         };
 
         const int n_mine = (s1 - s0 - warp + kWarps - 1) / kWarps; // steps s0 + warp + 4 k
-        for (int k = 0; k < kStages; ++k)
+        for (int k = 0; ok && k < kStages; ++k)
             issue(s0 + warp + k * kWarps, k);
-        for (int k = 0; k < n_mine; ++k) {
-            cp_async_wait<kStages - 1>();
-            __syncwarp(); // lane 0's scales
+        for (int k = 0; ok && k < n_mine; ++k) {
             const int stage = k % kStages;
+            ok = __all_sync(0xffffffffu, umma::mbar_wait(full + 8 * stage, phases >> stage & 1));
+            if (!ok) {
+                if (lane == 0)
+                    atomicOr(&g_kv8_stream_error, 1);
+                break;
+            }
+            phases ^= 1u << stage;
             const int s = s0 + warp + k * kWarps;
             const int tb = rq.begin + s * kStep;
             const uint32_t src = ring + stage * L::kStageBytes;
@@ -407,25 +393,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             float sc[2][NT][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float odd[NT][4]; // every other k-step: two chains of products
+                float odd[NT][4]; // the low parts: two chains of products
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sc[x][nt][e] = odd[nt][e] = 0.f;
+                const int ra = 16 * x + tau_g; // the lane's rows: ra, ra + 8
 #pragma unroll
                 for (int hh = 0; hh < kH; ++hh) {
-                    const uint4 ka = lds128(src + x * L::kHalf + (hh * 32 + lane) * 16),
-                                kb = lds128(src + x * L::kHalf + ((kH + hh) * 32 + lane) * 16);
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                    const uint32_t col = D == 128 ? ((t4 + 4 * hh) ^ (ra & 7)) * 16 : (t4 ^ ((ra >> 1) & 3)) * 16;
+                    const uint4 ka = lds128(src + ra * D + col), kb = lds128(src + (ra + 8) * D + col);
+                    const uint32_t f0[4] = {ka.x, kb.x, ka.y, kb.y}, f1[4] = {ka.z, kb.z, ka.w, kb.w};
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t f[4];
-                        e4m3x4_to_f16x4(wa[w], f[0], f[2]);
-                        e4m3x4_to_f16x4(wb[w], f[1], f[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16_16816(w & 1 ? odd[nt] : sc[x][nt], f, qf[nt][hh * 4 + w][0], qf[nt][hh * 4 + w][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_e4m3_16832(sc[x][nt], f0, qf[nt][2 * hh][0][0], qf[nt][2 * hh][0][1]);
+                        mma_e4m3_16832(odd[nt], f0, qf[nt][2 * hh][1][0], qf[nt][2 * hh][1][1]);
+                        mma_e4m3_16832(sc[x][nt], f1, qf[nt][2 * hh + 1][0][0], qf[nt][2 * hh + 1][0][1]);
+                        mma_e4m3_16832(odd[nt], f1, qf[nt][2 * hh + 1][1][0], qf[nt][2 * hh + 1][1][1]);
                     }
                 }
 #pragma unroll
@@ -445,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                     for (int e = 0; e < 4; ++e) {
                         float y = fmaf(sc[x][nt][e], mt[x].x * cscale[nt][e & 1], mt[x].y);
                         if (!clear) {
-                            const int j = tb + 16 * x + tok_a + (e & 2);
+                            const int j = tb + 16 * x + tau_g + 4 * (e & 2);
                             const int p = pos[nt][e & 1];
                             if (!(j <= p && (a.window <= 0 || j > p - a.window)))
                                 y = -INFINITY;
@@ -492,17 +477,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                 uint32_t vw[4][kV / 4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
+                    const int r = 16 * x + 8 * (y >> 1) + tau_t[y & 1];
                     if (D == 128) {
-                        const uint4 v = lds128(src + x * L::kHalf + 16 * D + (y * 32 + lane) * kV);
+                        const uint4 v = lds128(src + L::kSide + r * D + ((g ^ (r & 7)) << 4));
                         vw[y][0] = v.x;
                         vw[y][1] = v.y;
                         vw[y][(kV / 4) - 2] = v.z;
                         vw[y][(kV / 4) - 1] = v.w;
                     } else {
-                        const uint2 v = lds64(src + x * L::kHalf + 16 * D + (y * 32 + lane) * kV);
+                        const uint2 v = lds64(src + L::kSide + r * D + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
                         vw[y][0] = v.x;
                         vw[y][1] = v.y;
                     }
+                    // where no row sees the position the block may hold anything
+                    if (!clear && !(tb + r < kv_end && tb + r >= kv_begin))
+#pragma unroll
+                        for (int w = 0; w < kV / 4; ++w)
+                            vw[y][w] = 0;
                 }
                 // A NaN code of V at a position that some rows see and others do not
                 // must not reach the others through 0 * NaN: it is taken out and
@@ -510,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                 if (many && !clear) {
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const int j = tb + 16 * x + 4 * t4 + y;
+                        const int j = tb + 16 * x + 8 * (y >> 1) + tau_t[y & 1];
 #pragma unroll
                         for (int w = 0; w < kV / 4; ++w) {
                             const uint32_t bad = nan_bytes(vw[y][w]);
@@ -542,12 +533,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                         mma_f16_16816(o[i][nt], f, pf[x][nt][0], pf[x][nt][1]);
                 }
             }
-            // the stage is free: each lane has used what it copied, all have read the scales
+            // the stage is free: every lane has used what it read of it
             __syncwarp();
             issue(s0 + warp + (k + kStages) * kWarps, stage);
         }
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-
         // the unit's end: the four warps' sums are joined through shared memory
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -617,8 +606,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                     part.ml[slot * R + r] = make_float2(top, sum);
             }
         }
-        __syncthreads(); // the ring and the sums are free again
+        // the ring and the sums are free again; what was written there is done before the next copies land
+        umma::fence_async_smem();
+        __syncthreads();
     }
+    // no copy outlives the block, also where a wait gave up
+    if (!ok)
+        for (int i = 0; i < kStages; ++i)
+            if (!umma::mbar_wait(full + 8 * i, phases >> i & 1) && lane == 0)
+                atomicOr(&g_kv8_stream_error, 2);
 }
 
 // Joins the partial sums of the units that several blocks share: a warp to a
@@ -714,7 +710,10 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess)
         return e;
-    kv8_stream_kernel<D, NT><<<blocks_of(NT, sm_count), kThreads, L::kSmem, stream>>>(a, part);
+    CUtensorMap maps[2];
+    if (!kv8_tensor_maps(a, D, kStep, maps))
+        return cudaErrorInvalidValue;
+    kv8_stream_kernel<D, NT><<<blocks_of(NT, sm_count), kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     // behind it, its start overlapped (it waits for the first kernel's end)
@@ -747,6 +746,16 @@ cudaError_t launch_kv8_stream(const Kv8AttnArgs &a, int D, int max_query_len, vo
     if (D == 128)
         return nt == 1 ? launch<128, 1>(a, workspace, sm_count, stream) : launch<128, 2>(a, workspace, sm_count, stream);
     return nt == 1 ? launch<64, 1>(a, workspace, sm_count, stream) : launch<64, 2>(a, workspace, sm_count, stream);
+}
+
+cudaError_t read_kv8_stream_error(int *out, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_kv8_stream_error, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_kv8_stream_error, &zero, sizeof(int));
+    }
+    return e;
 }
 
 } // namespace smla

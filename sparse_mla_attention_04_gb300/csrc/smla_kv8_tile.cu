@@ -112,21 +112,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// Four floats below 2^8 as E4M3 codes of hi and of the rest lo.
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo)
-{
-    const uint32_t h0 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t h1 = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    hi = (h0 & 0xFFFFu) | (h1 << 16);
-    uint32_t f0, f1;
-    e4m3x4_to_f16x4(hi, f0, f1);
-    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f0));
-    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&f1));
-    const uint32_t l0 = __nv_cvt_float2_to_fp8x2(make_float2(a - x.x, b - x.y), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t l1 = __nv_cvt_float2_to_fp8x2(make_float2(c - y.x, d - y.y), __NV_SATFINITE, __NV_E4M3);
-    lo = (l0 & 0xFFFFu) | (l1 << 16);
-}
-
 // Two binary32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(float a, float b)
 {
@@ -416,36 +401,20 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                                                            (int64_t)(it.h * a.G + rr % a.G) * a.q_sh);
         float amax = 0.f;
 #pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-        }
-        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 127);
-        float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-        qs = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + e - 7) << 23); // an infinite q has no finite logit
+        for (int i = 0; i < D / 8; ++i)
+            amax = fmaxf(amax, live ? amax8(src[i]) : 0.f);
+        float up;
+        split_scale(amax, up, qs);
         up = a.scale < 0.f ? -up : up;
         const uint32_t dst = base + S::kQ + (r >> 3) * S::kQAtoms + (r & 7) * 16;
 #pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {
-            uint32_t hi[4], lo[4];
+            uint32_t hi[2][2], lo[2][2];
 #pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {
-                const uint4 v = live ? src[2 * i + e2] : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * x]));
-                    const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * x + 1]));
-                    split4(f0.x * up, f0.y * up, f1.x * up, f1.y * up, hi[2 * e2 + x], lo[2 * e2 + x]);
-                }
-            }
-            sts128(dst + i * 128, hi[0], hi[1], hi[2], hi[3]);
-            sts128(dst + S::kQBytes + i * 128, lo[0], lo[1], lo[2], lo[3]);
+            for (int e = 0; e < 2; ++e)
+                split8(live ? src[2 * i + e] : make_uint4(0, 0, 0, 0), up, hi[e], lo[e]);
+            sts128(dst + i * 128, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
+            sts128(dst + S::kQBytes + i * 128, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
         }
         fence_async_smem();
     }
@@ -783,22 +752,9 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
     if (e != cudaSuccess)
         return e;
-    // the codes as blocks of [block_size, D] bytes, the rows swizzled as they land
-    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-    if (encode == nullptr)
-        return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.block_size, (cuuint64_t)std::max<int64_t>(1, a.num_blocks * a.H_kv)};
-    const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * a.block_size};
-    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(a.block_size, kTile), 1}, step[3] = {1, 1, 1};
     CUtensorMap maps[2];
-    for (int i = 0; i < 2; ++i) {
-        // (of an empty pool nothing is read: any aligned address will do)
-        void *pool = a.num_blocks > 0 ? const_cast<uint8_t *>(i ? a.v_cache : a.k_cache) : const_cast<void *>(a.q);
-        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, step,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-    }
+    if (!kv8_tensor_maps(a, D, kTile, maps))
+        return cudaErrorInvalidValue;
     kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess || part.splits == 1)
         return e;
