@@ -127,91 +127,74 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
     float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kBig);
     float4 *s_meta = reinterpret_cast<float4 *>(smem + L::kBig + kWarps * R * 8);
     uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 32);
-    long long *s_sum = reinterpret_cast<long long *>(smem); // before the ring is used
-    __shared__ long long s_base;
-    __shared__ int s_b;
+    // The block's place in the work, kept here and not in registers while a unit is worked on.
+    __shared__ struct {
+        long long at, hi, total; // cost: where the block is, where its part ends, the whole
+        long long base, unit0;   // cost and units before request b
+        int b, blocks;
+        long long warp_cost[kWarps], warp_count[kWarps];
+    } s_walk;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     umma::grid_launch_dependents();
 
-    // the total cost, and this block's part [lo, hi)
-    const int per = (a.B + kThreads - 1) / kThreads;
+    // The total cost and this block's part of it: each thread adds up its requests, the block scans the sums, and
+    // the thread whose requests hold the part's begin finds the request.
     {
-        long long mine = 0;
+        const int per = (a.B + kThreads - 1) / kThreads;
+        long long cost = 0, count = 0;
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
             if (b < a.B) {
                 const Units u = units_of<R>(a, request(a, b));
-                mine += u.count * u.cost;
+                cost += u.count * u.cost;
+                count += u.count;
             }
         }
-        s_sum[tid] = mine;
-    }
-    __syncthreads();
-    long long total = 0, before = 0;
-    for (int i = 0; i < kThreads; ++i) {
-        if (i == tid)
-            before = total;
-        total += s_sum[i];
-    }
-    const long long blocks = max(1ll, min((long long)gridDim.x, (total + kMinPart - 1) / kMinPart));
-    if (blockIdx.x == 0) { // the number of units, for the joining kernel
-        long long n = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < a.B)
-                n += units_of<R>(a, request(a, b)).count;
+        long long cost_to = cost, count_to = count; // inclusive
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, cost_to, d), y = __shfl_up_sync(0xffffffffu, count_to, d);
+            cost_to += lane >= d ? x : 0;
+            count_to += lane >= d ? y : 0;
+        }
+        if (lane == 31) {
+            s_walk.warp_cost[warp] = cost_to;
+            s_walk.warp_count[warp] = count_to;
         }
         __syncthreads();
-        s_sum[tid] = n;
-        __syncthreads();
-        if (tid == 0) {
-            long long all = 0;
-            for (int i = 0; i < kThreads; ++i)
-                all += s_sum[i];
-            *part.header = (int)all;
+        long long total = 0, units = 0, cost0 = cost_to - cost, count0 = count_to - count;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            cost0 += w < warp ? s_walk.warp_cost[w] : 0;
+            count0 += w < warp ? s_walk.warp_count[w] : 0;
+            total += s_walk.warp_cost[w];
+            units += s_walk.warp_count[w];
         }
-    }
-    if (blockIdx.x >= blocks || total == 0)
-        return;
-    const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
-    if (lo >= hi)
-        return;
-    // the request that holds cost lo: found by the thread whose requests do
-    {
-        long long mine = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < a.B) {
-                const Units u = units_of<R>(a, request(a, b));
-                const long long c = u.count * u.cost;
-                if (lo >= before + mine && lo < before + mine + c) {
-                    s_b = b;
-                    s_base = before + mine;
-                }
-                mine += c;
+        if (blockIdx.x == 0 && tid == 0)
+            *part.header = (int)units; // for the joining kernel
+        const long long blocks = max(1ll, min((long long)gridDim.x, (total + kMinPart - 1) / kMinPart));
+        const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
+        if (blockIdx.x >= blocks || lo >= hi)
+            return;
+        if (lo >= cost0 && lo < cost0 + cost) {
+            int b = tid * per;
+            Units u = units_of<R>(a, request(a, b));
+            while (lo >= cost0 + u.count * u.cost) {
+                cost0 += u.count * u.cost;
+                count0 += u.count;
+                u = units_of<R>(a, request(a, ++b));
             }
+            s_walk.at = lo;
+            s_walk.hi = hi;
+            s_walk.total = total;
+            s_walk.base = cost0;
+            s_walk.unit0 = count0;
+            s_walk.b = b;
+            s_walk.blocks = (int)blocks;
         }
     }
-    __syncthreads();
-    int b = s_b;
-    long long base = s_base; // cost at which request b begins
-    // units before request b: the index of its first in the directory
-    long long unit0 = 0;
-    {
-        long long n = 0;
-        for (int i = tid; i < b; i += kThreads)
-            n += units_of<R>(a, request(a, i)).count;
-        __syncthreads();
-        s_sum[tid] = n;
-        __syncthreads();
-        for (int i = 0; i < kThreads; ++i)
-            unit0 += s_sum[i];
-    }
-
-    umma::fence_async_smem();
-    __syncthreads(); // the sums were read: the ring is free for copies
     const float scale_log2 = a.scale * kLog2e;
     const uint32_t full = smem_u32(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 32 + L::kNanWords * 4) + warp * kStages * 8;
     if (lane == 0) {
@@ -228,8 +211,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
     const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStageBytes;
     float4 *meta = s_meta + warp * kStages * 2;
 
-    long long at = lo;
-    while (at < hi) {
+    __syncthreads();
+    while (s_walk.at < s_walk.hi) {
+        long long at = s_walk.at, base = s_walk.base, unit0 = s_walk.unit0;
+        int b = s_walk.b;
         Request rq = request(a, b);
         Units un = units_of<R>(a, rq);
         while (at >= base + un.count * un.cost) { // requests without tokens have no units
@@ -241,16 +226,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         }
         const long long ui = (at - base) / un.cost;
         const long long ubase = base + ui * un.cost;
-        const long long uend = min(hi, ubase + un.cost);
+        const long long uend = min(s_walk.hi, ubase + un.cost);
         const int s0 = (int)max(0ll, at - ubase - kUnitCost), s1 = (int)max(0ll, uend - ubase - kUnitCost);
-        at = uend;
-        if (s0 >= s1)
+        __syncthreads(); // all have read the place
+        if (tid == 0) {
+            s_walk.at = uend;
+            s_walk.base = base;
+            s_walk.unit0 = unit0;
+            s_walk.b = b;
+        }
+        if (s0 >= s1) {
+            __syncthreads();
             continue;
+        }
         const bool whole = s0 == 0 && s1 == un.steps;
         if (s0 == 0 && tid == 0) {
             // blocks that hold the unit's first and last step
-            const long long x0 = ubase + kUnitCost, x1 = ubase + un.cost - 1;
-            const int c0 = (int)(((x0 + 1) * blocks - 1) / total), c1 = (int)(((x1 + 1) * blocks - 1) / total);
+            const long long x0 = ubase + kUnitCost, x1 = ubase + un.cost - 1, total = s_walk.total;
+            const int c0 = (int)(((x0 + 1) * s_walk.blocks - 1) / total), c1 = (int)(((x1 + 1) * s_walk.blocks - 1) / total);
             part.dir[unit0 + ui] = make_int4(c0, c1, b, (int)ui);
         }
         const int h = (int)(ui % a.H_kv);
@@ -262,6 +255,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         const int kv_begin = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
         const int all_from = a.window > 0 ? p_last - a.window + 1 : 0;                 // [all_from, p_first]: seen by all
         const bool many = p_first != p_last;
+
+        // the lane's table entry, first + lane: its block (-1: none), the factor of its logits, log2 and
+        // inverse of its value scale (a block outside the pool: logits of -inf, nothing is read)
+        const int32_t *row = a.block_table + b * a.table_stride;
+        int first = -(1 << 30);
+        int e_blk = -1;
+        float e_c = 0.f, e_lv = -INFINITY, e_iv = 1.f;
+        // Position 8 i + tau(j) of a step is number j of its i-th eight: tau(2 t + e) = (2 t ^ 4 e) | e. The
+        // rows of lanes g = 2 t and 2 t + 1 (K) then differ in bit 2, those of the four t (V) in bits 1 and
+        // 2, so that with the swizzle eight lanes read eight different 16-byte columns.
+        const int tau_g = ((g & 6) ^ (4 * (g & 1))) | (g & 1);
+        const int tau_t[2] = {2 * t4, (2 * t4 ^ 4) | 1};
+
+        auto issue = [&](int s, int stage) {
+            if (s < s1) {
+                const int tb = rq.begin + s * kStep;
+                const int e = tb >> a.block_shift;
+                if (e - first >= 31 || e < first) {
+                    first = e;
+                    const int x = e + lane;
+                    e_blk = x < a.table_width && ((long long)x << a.block_shift) < rq.len ? row[x] : -1;
+                    e_c = 0.f;
+                    e_lv = -INFINITY;
+                    e_iv = 1.f;
+                    if (e_blk >= 0 && e_blk < a.num_blocks) {
+                        const float vs = a.v_scale[(int64_t)e_blk * a.H_kv + h];
+                        e_c = a.k_scale[(int64_t)e_blk * a.H_kv + h] * scale_log2;
+                        e_lv = lg2_approx(vs);
+                        e_iv = __frcp_rn(vs);
+                    } else {
+                        e_blk = -1;
+                    }
+                }
+                if (lane == 0)
+                    umma::mbar_arrive_expect_tx(full + 8 * stage, L::kStageBytes);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int ex = ((tb + 16 * x) >> a.block_shift) - first;
+                    const float c = __shfl_sync(0xffffffffu, e_c, ex), lv = __shfl_sync(0xffffffffu, e_lv, ex),
+                                iv = __shfl_sync(0xffffffffu, e_iv, ex);
+                    if (lane == 0)
+                        meta[stage * 2 + x] = make_float4(c, lv, iv, 0.f);
+                }
+                __syncwarp();
+                // lanes p and 16 + p: block p of the step, for K and for V. A block outside the pool: rows
+                // outside the map, which fills zeros and reads nothing.
+                const int p = lane & 15;
+                const int blk = __shfl_sync(0xffffffffu, e_blk, ((tb + (p < pages ? p : 0) * rows_in) >> a.block_shift) - first);
+                if (p < pages)
+                    umma::tma_load_3d(ring + stage * L::kStageBytes + (lane >> 4) * L::kSide + p * rows_in * D,
+                                      lane < 16 ? &k_map : &v_map, 0, blk >= 0 ? tb & (a.block_size - 1) : a.block_size,
+                                      blk >= 0 ? blk * a.H_kv + h : 0, full + 8 * stage);
+            }
+        };
+
+        for (int k = 0; ok && k < kStages; ++k)
+            issue(s0 + warp + k * kWarps, k);
 
         // this lane's part of Q: fragment column g of each tile, and the factors of its columns 2 t4, 2 t4 + 1
         uint32_t qf[NT][2 * kH][2][2]; // k-step, part (hi, lo), register
@@ -320,63 +370,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             __syncthreads();
         }
 
-        // the lane's table entry, first + lane: its block (-1: none), the factor of its logits, log2 and
-        // inverse of its value scale (a block outside the pool: logits of -inf, nothing is read)
-        const int32_t *row = a.block_table + b * a.table_stride;
-        int first = -(1 << 30);
-        int e_blk = -1;
-        float e_c = 0.f, e_lv = -INFINITY, e_iv = 1.f;
-        // Position 8 i + tau(j) of a step is number j of its i-th eight: tau(2 t + e) = (2 t ^ 4 e) | e. The
-        // rows of lanes g = 2 t and 2 t + 1 (K) then differ in bit 2, those of the four t (V) in bits 1 and
-        // 2, so that with the swizzle eight lanes read eight different 16-byte columns.
-        const int tau_g = ((g & 6) ^ (4 * (g & 1))) | (g & 1);
-        const int tau_t[2] = {2 * t4, (2 * t4 ^ 4) | 1};
-
-        auto issue = [&](int s, int stage) {
-            if (s < s1) {
-                const int tb = rq.begin + s * kStep;
-                const int e = tb >> a.block_shift;
-                if (e - first >= 31 || e < first) {
-                    first = e;
-                    const int x = e + lane;
-                    e_blk = x < a.table_width && ((long long)x << a.block_shift) < rq.len ? row[x] : -1;
-                    e_c = 0.f;
-                    e_lv = -INFINITY;
-                    e_iv = 1.f;
-                    if (e_blk >= 0 && e_blk < a.num_blocks) {
-                        const float vs = a.v_scale[(int64_t)e_blk * a.H_kv + h];
-                        e_c = a.k_scale[(int64_t)e_blk * a.H_kv + h] * scale_log2;
-                        e_lv = lg2_approx(vs);
-                        e_iv = __frcp_rn(vs);
-                    } else {
-                        e_blk = -1;
-                    }
-                }
-                if (lane == 0)
-                    umma::mbar_arrive_expect_tx(full + 8 * stage, L::kStageBytes);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int ex = ((tb + 16 * x) >> a.block_shift) - first;
-                    const float c = __shfl_sync(0xffffffffu, e_c, ex), lv = __shfl_sync(0xffffffffu, e_lv, ex),
-                                iv = __shfl_sync(0xffffffffu, e_iv, ex);
-                    if (lane == 0)
-                        meta[stage * 2 + x] = make_float4(c, lv, iv, 0.f);
-                }
-                __syncwarp();
-                // lanes p and 16 + p: block p of the step, for K and for V. A block outside the pool: rows
-                // outside the map, which fills zeros and reads nothing.
-                const int p = lane & 15;
-                const int blk = __shfl_sync(0xffffffffu, e_blk, ((tb + (p < pages ? p : 0) * rows_in) >> a.block_shift) - first);
-                if (p < pages)
-                    umma::tma_load_3d(ring + stage * L::kStageBytes + (lane >> 4) * L::kSide + p * rows_in * D,
-                                      lane < 16 ? &k_map : &v_map, 0, blk >= 0 ? tb & (a.block_size - 1) : a.block_size,
-                                      blk >= 0 ? blk * a.H_kv + h : 0, full + 8 * stage);
-            }
-        };
-
         const int n_mine = (s1 - s0 - warp + kWarps - 1) / kWarps; // steps s0 + warp + 4 k
-        for (int k = 0; ok && k < kStages; ++k)
-            issue(s0 + warp + k * kWarps, k);
         for (int k = 0; ok && k < n_mine; ++k) {
             const int stage = k % kStages;
             ok = __all_sync(0xffffffffu, umma::mbar_wait(full + 8 * stage, phases >> stage & 1));
