@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional, Tuple
 
@@ -524,6 +525,7 @@ def build_fp8_cache(kv_source: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
 
 # ---- the serving step around the forward: page maps, rotary positions, the block-scaled 8-bit cache
 
+
 class _Launch:
     """Runs a call on the tensors' device and on its stream, with that stream
     current, so that what the call allocates belongs to it. `handle` is the
@@ -534,13 +536,12 @@ class _Launch:
     def __init__(self, device: torch.device, stream):
         self._device = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
         self._stream = None
+        self.handle = None
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
             self._stream = torch.cuda.stream(stream)
             self.handle = int(stream.cuda_stream)
-        else:
-            self.handle = None
 
     def __enter__(self):
         if self._device is not None:
@@ -549,7 +550,7 @@ class _Launch:
             self._stream.__enter__()
         else:
             self.handle = int(torch.cuda.current_stream().cuda_stream)
-        return self
+        return self.handle
 
     def __exit__(self, *exc):
         if self._stream is not None:
@@ -558,13 +559,50 @@ class _Launch:
             self._device.__exit__(*exc)
 
 
-def _same_device(first: torch.Tensor, **others):
-    for name, x in others.items():
-        if x is not None and x.device != first.device:
-            raise ValueError("%s is on %s, the other tensors on %s" % (name, x.device, first.device))
+class _Here:
+    """As _Launch for the usual call: the tensors are on the current device and no
+    stream is given. One for each device, kept: such a call costs a few
+    microseconds in all."""
+
+    __slots__ = ("_index",)
+
+    def __init__(self, index: int):
+        self._index = index
+
+    def __enter__(self):
+        return _raw_stream(self._index)
+
+    def __exit__(self, *exc):
+        return None
 
 
-def _rows(x: torch.Tensor, name: str, dtype, ndim: int):
+def _raw_stream(index: int) -> int:
+    return int(torch.cuda.current_stream(index).cuda_stream)
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+_here = {}
+
+
+def _on(device: torch.device, stream):
+    if stream is not None or device.index != torch.cuda.current_device():
+        return _Launch(device, stream)
+    on = _here.get(device.index)
+    if on is None:
+        on = _here[device.index] = _Here(device.index)
+    return on
+
+
+def _fits(x, name: str, dtype, ndim: int, device: torch.device):
+    """_need, and on `device`."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.dim() == ndim and x.device == device
+            and x.is_contiguous()):
+        _need(x, name, dtype, ndim)
+        raise ValueError("%s is on %s, the other tensors on %s" % (name, x.device, device))
+
+
+def _rows(x: torch.Tensor, name: str, dtype, ndim: int, device: Optional[torch.device] = None):
     """A CUDA tensor whose last dimension is contiguous (other strides free)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -576,15 +614,27 @@ def _rows(x: torch.Tensor, name: str, dtype, ndim: int):
         raise ValueError("%s must be contiguous in its last dimension" % name)
     if not x.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    if device is not None and x.device != device:
+        raise ValueError("%s is on %s, the other tensors on %s" % (name, x.device, device))
 
 
 def _out(x: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
     if x is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(x, name, dtype, len(shape))
-    if tuple(x.shape) != tuple(shape):
+    _fits(x, name, dtype, len(shape), device)
+    if x.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(x.shape)))
     return x
+
+
+def _workspace(x: Optional[torch.Tensor], need: int, device: torch.device):
+    """The caller's workspace, or one of the current stream's pool (so that calls in
+    flight and captured graphs never share one), and its size."""
+    if x is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if not x.is_contiguous() or x.device != device:
+        raise ValueError("workspace must be contiguous and on %s" % device)
+    return x, x.numel() * x.element_size()
 
 
 class BlockTables(NamedTuple):
@@ -615,32 +665,31 @@ def smla_build_block_tables(seq_lens: torch.Tensor, query_lens: torch.Tensor, bl
     positions when that is given; needed otherwise), those past the last token
     padded. Nothing is taken when blocks lack: counts[3] says how many."""
     _need(seq_lens, "seq_lens", torch.int32, 1)
+    dev = seq_lens.device
     B = seq_lens.shape[0]
-    for name, x in (("query_lens", query_lens), ("blocks_held", blocks_held)):
-        _need(x, name, torch.int32, 1)
-        if x.shape[0] != B:
-            raise ValueError("%s must be [B] = [%d]" % (name, B))
-    _rows(block_table, "block_table", torch.int32, 2)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table has %d rows, seq_lens %d" % (block_table.shape[0], B))
-    width = block_table.shape[1]
-    row_stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
+    _fits(query_lens, "query_lens", torch.int32, 1, dev)
+    _fits(blocks_held, "blocks_held", torch.int32, 1, dev)
+    if query_lens.shape[0] != B or blocks_held.shape[0] != B:
+        raise ValueError("query_lens and blocks_held must be [B] = [%d]" % B)
+    _rows(block_table, "block_table", torch.int32, 2, dev)
+    rows, width = block_table.shape
+    if rows != B:
+        raise ValueError("block_table has %d rows, seq_lens %d" % (rows, B))
+    row_stride = block_table.stride(0)
     if row_stride < width:
-        raise ValueError("block_table rows overlap")
-    _need(free_ring, "free_ring", torch.int32, 1)
-    _need(ring_state, "ring_state", torch.int32, 1)
+        if B > 1:
+            raise ValueError("block_table rows overlap")
+        row_stride = width
+    _fits(free_ring, "free_ring", torch.int32, 1, dev)
+    _fits(ring_state, "ring_state", torch.int32, 1, dev)
     if ring_state.shape[0] != 2:
         raise ValueError("ring_state must be [2]: head, count")
     if num_tokens is None:
         if positions is None:
             raise ValueError("num_tokens or positions is needed")
         num_tokens = positions.shape[0]
-    dev = seq_lens.device
-    _same_device(seq_lens, query_lens=query_lens, blocks_held=blocks_held, block_table=block_table,
-                 free_ring=free_ring, ring_state=ring_state, blocks_held_out=blocks_held_out,
-                 ring_state_out=ring_state_out, query_start=query_start, positions=positions,
-                 slot_mapping=slot_mapping, token_request=token_request, counts=counts, workspace=workspace)
-    with _Launch(dev, stream) as on:
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
         held = blocks_held if blocks_held_out is None else _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
         state = ring_state if ring_state_out is None else _out(ring_state_out, "ring_state_out", (2,), torch.int32, dev)
         query_start = _out(query_start, "query_start", (B + 1,), torch.int32, dev)
@@ -648,14 +697,22 @@ def smla_build_block_tables(seq_lens: torch.Tensor, query_lens: torch.Tensor, bl
         slot_mapping = _out(slot_mapping, "slot_mapping", (num_tokens,), torch.int64, dev)
         token_request = _out(token_request, "token_request", (num_tokens,), torch.int32, dev)
         counts = _out(counts, "counts", (4,), torch.int32, dev)
-        if workspace is None:
-            workspace = torch.empty(int(lib().smla_build_block_tables_workspace_size(B)), dtype=torch.uint8, device=dev)
-        _check(lib().smla_build_block_tables(
-            _ptr(seq_lens), _ptr(query_lens), _ptr(blocks_held), _ptr(held), B, int(block_size), _ptr(block_table),
-            row_stride, width, _ptr(free_ring), free_ring.shape[0], _ptr(ring_state), _ptr(state), _ptr(query_start),
-            _ptr(positions), _ptr(slot_mapping), _ptr(token_request), num_tokens, _ptr(counts), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), on.handle), "smla_build_block_tables")
+        need = _sizes.get(("tables", B))
+        if need is None:
+            need = _sizes[("tables", B)] = int(L.smla_build_block_tables_workspace_size(B))
+        workspace, ws_bytes = _workspace(workspace, need, dev)
+        st = L.smla_build_block_tables(
+            seq_lens.data_ptr(), query_lens.data_ptr(), blocks_held.data_ptr(), held.data_ptr(), B, block_size,
+            block_table.data_ptr(), row_stride, width, free_ring.data_ptr(), free_ring.shape[0], ring_state.data_ptr(),
+            state.data_ptr(), query_start.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
+            token_request.data_ptr(), num_tokens, counts.data_ptr(), workspace.data_ptr(), ws_bytes, handle)
+    if st:
+        _check(st, "smla_build_block_tables")
     return BlockTables(query_start, positions, slot_mapping, token_request, counts, held, state)
+
+
+# workspace bytes by the sizes they follow from (and the device, whose SM count they follow too)
+_sizes = {}
 
 
 def smla_rope_cos_sin_cache(num_positions: int, rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
@@ -682,14 +739,21 @@ def smla_rope_cos_sin_cache(num_positions: int, rot_dim: int, *, base: float = 1
             raise ValueError("device must be a CUDA device")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-    with _Launch(dev, stream) as on:
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
         if out is None:
             out = torch.empty((num_positions, rot_dim), dtype=torch.float32, device=dev)
-        _check(lib().smla_rope_cos_sin_cache(_ptr(out), int(num_positions), int(first_position), int(rot_dim),
-                                             float(base), _ROPE[scaling], float(factor), int(original_max_position),
-                                             float(beta_fast), float(beta_slow), float(attention_factor or 0.0),
-                                             on.handle), "smla_rope_cos_sin_cache")
+        st = L.smla_rope_cos_sin_cache(out.data_ptr(), num_positions, first_position, rot_dim, base, _ROPE[scaling],
+                                       factor, original_max_position, beta_fast, beta_slow, attention_factor or 0.0,
+                                       handle)
+    if st:
+        _check(st, "smla_rope_cos_sin_cache")
     return out
+
+
+# the C structures, packed (native sizes and alignment) instead of built field by field
+_ROPE_PARAMS = struct.Struct("@NiPqqPqqPqqPqqPPqiiiiiiiiP")
+_KV8_ATTN_PARAMS = struct.Struct("@NPqqPPPPqPqiPPiiiiiiiifPPPPNP")
 
 
 def smla_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, cos_sin_cache: torch.Tensor, *,
@@ -703,37 +767,45 @@ def smla_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
     rotation's gradient). q_out / k_out may be q / k: rotated in place."""
     if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
         raise TypeError("q must be a bf16, fp16 or fp32 tensor")
-    _rows(q, "q", q.dtype, 3)
+    dtype, dev = q.dtype, q.device
+    _rows(q, "q", dtype, 3)
     T, H, D = q.shape
     if k is not None:
-        _rows(k, "k", q.dtype, 3)
+        _rows(k, "k", dtype, 3, dev)
         if k.shape[0] != T or k.shape[2] != D:
             raise ValueError("k must be [T, H_k, D] = [%d, *, %d], got %s" % (T, D, tuple(k.shape)))
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _need(positions, "positions", torch.int64, 1)
+    _fits(positions, "positions", torch.int64, 1, dev)
     if positions.shape[0] != T:
         raise ValueError("positions must be [T] = [%d]" % T)
-    _need(cos_sin_cache, "cos_sin_cache", torch.float32, 2)
-    _same_device(q, k=k, positions=positions, cos_sin_cache=cos_sin_cache, q_out=q_out, k_out=k_out)
-    with _Launch(q.device, stream) as on:
+    _fits(cos_sin_cache, "cos_sin_cache", torch.float32, 2, dev)
+    for name, x, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if x is not None and x is not like:
+            _rows(x, name, dtype, 3, dev)
+            if x.shape != like.shape:
+                raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(x.shape)))
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
         if q_out is None:
-            q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
-        for name, x, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-            if x is not None:
-                _rows(x, name, q.dtype, 3)
-                if x.shape != like.shape:
-                    raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(x.shape)))
-        ks = (None, 0, 0, None, 0, 0) if k is None else (k.data_ptr(), k.stride(0), k.stride(1), k_out.data_ptr(),
-                                                         k_out.stride(0), k_out.stride(1))
-        p = SmlaRopeParams(ctypes.sizeof(SmlaRopeParams), _DTYPE[q.dtype], q.data_ptr(), q.stride(0), q.stride(1),
-                           q_out.data_ptr(), q_out.stride(0), q_out.stride(1), *ks, positions.data_ptr(),
-                           cos_sin_cache.data_ptr(), cos_sin_cache.shape[0], T, H, 0 if k is None else k.shape[1], D,
-                           cos_sin_cache.shape[1], int(rot_offset), 1 if is_neox else 0, 1 if inverse else 0,
-                           on.handle)
-        _check(lib().smla_rope(ctypes.byref(p)), "smla_rope")
+            q_out = torch.empty((T, H, D), dtype=dtype, device=dev)
+        qs, os = q.stride(), q_out.stride()
+        if k is None:
+            ks = (0, 0, 0, 0, 0, 0)
+            Hk = 0
+        else:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+            Hk = k.shape[1]
+            a, b = k.stride(), k_out.stride()
+            ks = (k.data_ptr(), a[0], a[1], k_out.data_ptr(), b[0], b[1])
+        P, rot = cos_sin_cache.shape
+        st = L.smla_rope(_ROPE_PARAMS.pack(
+            _ROPE_PARAMS.size, _DTYPE[dtype], q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os[0], os[1], *ks,
+            positions.data_ptr(), cos_sin_cache.data_ptr(), P, T, H, Hk, D, rot, rot_offset, 1 if is_neox else 0,
+            1 if inverse else 0, handle))
+    if st:
+        _check(st, "smla_rope")
     return q_out, k_out
 
 
@@ -741,15 +813,17 @@ def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
     for name, x in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(x, torch.Tensor) or x.dtype not in (torch.uint8, torch.float8_e4m3fn):
             raise TypeError("%s must be E4M3 codes (uint8 / float8_e4m3fn)" % name)
-        _need(x, name, x.dtype, 4)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache is %s, v_cache %s" % (tuple(k_cache.shape), tuple(v_cache.shape)))
-    num_blocks, H_kv, block_size, D = k_cache.shape
-    for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(x, name, torch.float32, 2)
-        if tuple(x.shape) != (num_blocks, H_kv):
-            raise ValueError("%s must be [num_blocks, H_kv] = [%d, %d]" % (name, num_blocks, H_kv))
-    return num_blocks, H_kv, block_size, D
+    _need(k_cache, "k_cache", k_cache.dtype, 4)
+    dev = k_cache.device
+    _fits(v_cache, "v_cache", v_cache.dtype, 4, dev)
+    shape = k_cache.shape
+    if shape != v_cache.shape:
+        raise ValueError("k_cache is %s, v_cache %s" % (tuple(shape), tuple(v_cache.shape)))
+    _fits(k_scale, "k_scale", torch.float32, 2, dev)
+    _fits(v_scale, "v_scale", torch.float32, 2, dev)
+    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("k_scale and v_scale must be [num_blocks, H_kv] = %s" % (tuple(shape[:2]),))
+    return shape
 
 
 def smla_kv8_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -759,24 +833,28 @@ def smla_kv8_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor
     codes, k_scale, v_scale fp32 [num_blocks, H_kv]. A block's scale grows with
     its largest value and its older codes follow. Returns (k_cache, v_cache)."""
     num_blocks, H_kv, block_size, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    _strided(k, "k", 3)
-    _strided(v, "v", 3)
+    dev = k_cache.device
+    _rows(k, "k", torch.bfloat16, 3, dev)
+    _rows(v, "v", torch.bfloat16, 3, dev)
     T = k.shape[0]
-    if tuple(k.shape) != (T, H_kv, D) or tuple(v.shape) != (T, H_kv, D):
+    if k.shape != (T, H_kv, D) or v.shape != (T, H_kv, D):
         raise ValueError("k and v must be [T, %d, %d], got %s and %s" % (H_kv, D, tuple(k.shape), tuple(v.shape)))
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    _fits(slot_mapping, "slot_mapping", torch.int64, 1, dev)
     if slot_mapping.shape[0] != T:
         raise ValueError("slot_mapping must be [T] = [%d]" % T)
-    _same_device(k, v=v, slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    with _Launch(k.device, stream) as on:
-        _check(lib().smla_kv8_append(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-                                     slot_mapping.data_ptr(), T, H_kv, D, block_size, k_cache.data_ptr(),
-                                     v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), num_blocks,
-                                     on.handle), "smla_kv8_append")
+    ks, vs = k.stride(), v.stride()
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
+        st = L.smla_kv8_append(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slot_mapping.data_ptr(), T,
+                               H_kv, D, block_size, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                               v_scale.data_ptr(), num_blocks, handle)
+    if st:
+        _check(st, "smla_kv8_append")
     return k_cache, v_cache
 
 
 def smla_kv8_attn_workspace_size(B: int, T: int, H: int, H_kv: int, D: int, max_query_len: int) -> int:
+    """Workspace bytes of smla_kv8_attn_fwd on the current device."""
     n = lib().smla_kv8_attn_workspace_size(B, T, H, H_kv, D, max_query_len)
     if n == ctypes.c_size_t(-1).value:
         raise SmlaError(SMLA_ERR_BAD_SHAPE, "smla_kv8_attn_workspace_size")
@@ -800,38 +878,43 @@ def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     tokens in q; window > 0: each token sees its last `window` positions; sinks
     fp32 [H]: logits that join the denominator."""
     num_blocks, H_kv, block_size, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
-    _strided(q, "q", 3)
+    dev = k_cache.device
+    _rows(q, "q", torch.bfloat16, 3, dev)
     T, H, Dq = q.shape
-    if Dq != D or H % H_kv != 0 or H == 0:
+    if Dq != D or H_kv == 0 or H % H_kv != 0 or H == 0:
         raise ValueError("q is %s, the cache has %d heads of %d columns" % (tuple(q.shape), H_kv, D))
-    _rows(block_table, "block_table", torch.int32, 2)
+    _rows(block_table, "block_table", torch.int32, 2, dev)
     B, width = block_table.shape
-    row_stride = block_table.stride(0) if B > 1 else max(width, block_table.stride(0))
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(query_start, "query_start", torch.int32, 1)
+    row_stride = block_table.stride(0)
+    if B <= 1 and row_stride < width:
+        row_stride = width
+    _fits(seq_lens, "seq_lens", torch.int32, 1, dev)
+    _fits(query_start, "query_start", torch.int32, 1, dev)
     if seq_lens.shape[0] != B or query_start.shape[0] != B + 1:
         raise ValueError("seq_lens must be [B], query_start [B + 1], B = %d" % B)
     if sinks is not None:
-        _need(sinks, "sinks", torch.float32, 1)
+        _fits(sinks, "sinks", torch.float32, 1, dev)
         if sinks.shape[0] != H:
             raise ValueError("sinks must be [H]")
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
-                 seq_lens=seq_lens, query_start=query_start, sinks=sinks, out=out, lse=lse, workspace=workspace)
-    with _Launch(q.device, stream) as on:
-        out = _out(out, "out", (T, H, D), torch.bfloat16, q.device)
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
+        out = _out(out, "out", (T, H, D), torch.bfloat16, dev)
         if lse is not None or return_lse:
-            lse = _out(lse, "lse", (T, H), torch.float32, q.device)
-        if workspace is None:
-            # of the stream's own pool, so calls in flight and captured graphs never share one
-            workspace = torch.empty(smla_kv8_attn_workspace_size(B, T, H, H_kv, D, int(max_query_len)),
-                                    dtype=torch.uint8, device=q.device)
-        p = SmlaKv8AttnParams(ctypes.sizeof(SmlaKv8AttnParams), q.data_ptr(), q.stride(0), q.stride(1),
-                              k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                              num_blocks, block_table.data_ptr(), row_stride, width, seq_lens.data_ptr(),
-                              query_start.data_ptr(), B, T, H, H_kv, D, block_size, int(max_query_len), int(window),
-                              float(scale), _ptr(sinks), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), on.handle)
-        _check(lib().smla_kv8_attn_fwd(ctypes.byref(p)), "smla_kv8_attn_fwd")
+            lse = _out(lse, "lse", (T, H), torch.float32, dev)
+        sizes = (dev.index, B, T, H, H_kv, D, max_query_len)
+        need = _sizes.get(sizes)
+        if need is None:
+            need = _sizes[sizes] = smla_kv8_attn_workspace_size(B, T, H, H_kv, D, max_query_len)
+        workspace, ws_bytes = _workspace(workspace, need, dev)
+        qs = q.stride()
+        st = L.smla_kv8_attn_fwd(_KV8_ATTN_PARAMS.pack(
+            _KV8_ATTN_PARAMS.size, q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), num_blocks, block_table.data_ptr(), row_stride, width,
+            seq_lens.data_ptr(), query_start.data_ptr(), B, T, H, H_kv, D, block_size, max_query_len, window, scale,
+            0 if sinks is None else sinks.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), ws_bytes, handle))
+    if st:
+        _check(st, "smla_kv8_attn_fwd")
     return out, lse
 
 

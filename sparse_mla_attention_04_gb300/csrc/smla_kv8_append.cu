@@ -1,13 +1,13 @@
 // The write of the block-scaled 8-bit cache (sm_103a): E4M3 codes with one
 // scale per (block, kv head), kept right as blocks fill.
 //
-// A warp takes one run (the new tokens of one block) of one head of K or V: it
-// finds the run's largest |x|, settles the block's scale, requantizes the
-// block's older codes when the scale grew, and writes the run's codes. Nothing
-// is shared between warps, so there are no atomics and no barrier. A run of up
-// to kHeld 16-byte rows a lane stays in registers between the two passes; what
-// is beyond is read again (from L2). Bound: 2 bytes read and 1 written per
-// element.
+// A team of one or four warps takes one run (the new tokens of one block) of one
+// head of K or V: it finds the run's largest |x|, settles the block's scale,
+// requantizes the block's older codes when the scale grew, and writes the run's
+// codes. Nothing is shared between teams, so there are no atomics on data. What a
+// lane reads of a run (kHeld 16-byte pieces) stays in registers between the two
+// passes; what is beyond is read again (from L2). Bound: 2 bytes read and 1
+// written per element.
 #include "smla_device.cuh"
 #include "smla_internal.h"
 
@@ -19,8 +19,8 @@ __device__ int g_append_error = 0; // bit 8: a slot out of range
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kHeld = 32;
+constexpr int kThreads = 128;
+constexpr int kHeld = 8;
 constexpr float kMinScale = 0x1p-60f;
 
 __device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b)
@@ -77,17 +77,19 @@ __device__ __forceinline__ float warp_amax(uint32_t m)
     return warp_max(fmaxf(f.x, f.y));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8AppendArgs a)
+template <int D, int kTeam> // kTeam: warps of a team
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArgs a)
 {
-    constexpr int kLanes = D / 8;        // lanes of one row
-    constexpr int kRows = 32 / kLanes;   // rows of one warp-wide access
+    constexpr int kLanes = D / 8;                  // lanes of one row
+    constexpr int kRows = 32 * kTeam / kLanes;     // rows of one team-wide access
+    __shared__ uint32_t s_amax[kThreads / 32];
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int tid = threadIdx.x % (32 * kTeam);    // in the team
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32 / kTeam) + threadIdx.x / (32 * kTeam);
     const int which = (int)(item % (2 * a.H_kv));
     const int64_t t0 = item / (2 * a.H_kv) * a.window;
     if (t0 >= a.T)
-        return;
+        return; // (a team of four is a block: all of it returns)
     const int h = which >> 1;
     const bool isv = which & 1;
     const __nv_bfloat16 *src = isv ? a.v + h * a.v_sh : a.k + h * a.k_sh;
@@ -96,78 +98,100 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
     float *scales = isv ? a.v_scale : a.k_scale;
     const int bs = 1 << a.block_shift;
     const int64_t slots = a.num_blocks << a.block_shift;
-
-    // lane l holds the block of token t0 - 1 + l: a run begins where it changes
-    int64_t blk = -1;
-    {
-        const int64_t t = t0 - 1 + lane;
-        if (lane <= a.window && t >= 0 && t < a.T) {
-            const int64_t s = a.slot_mapping[t];
-            if (s >= slots) {
-                if (which == 0 && lane > 0)
-                    atomicOr(&g_append_error, 8);
-            } else if (s >= 0) {
-                blk = s >> a.block_shift;
-            }
+    // the largest over the team
+    auto team_max = [&](uint32_t m) {
+        float f = warp_amax(m);
+        if (kTeam > 1) {
+            __syncthreads();
+            if (lane == 0)
+                s_amax[threadIdx.x >> 5] = __float_as_uint(f);
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kTeam; ++w)
+                f = fmaxf(f, __uint_as_float(s_amax[w]));
         }
-    }
-    const int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
-    unsigned begins = __ballot_sync(0xffffffffu, lane > 0 && blk >= 0 && blk != before);
+        return f;
+    };
+
+    // lane l holds the block of token t0 + l: a run begins where it changes
+    auto block_of = [&](int64_t t, bool report) -> int64_t {
+        if (t < 0 || t >= a.T)
+            return -1;
+        const int64_t s = a.slot_mapping[t];
+        if (s >= slots && report)
+            atomicOr(&g_append_error, 8);
+        return s >= 0 && s < slots ? s >> a.block_shift : -1;
+    };
+    const int64_t blk = lane < a.window ? block_of(t0 + lane, which == 0) : -1;
+    int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
+    if (lane == 0)
+        before = block_of(t0 - 1, false);
+    unsigned begins = __ballot_sync(0xffffffffu, blk >= 0 && blk != before);
     while (begins) {
         const int l0 = __ffs(begins) - 1;
         begins &= begins - 1;
-        const int64_t run0 = t0 - 1 + l0;
+        const int64_t run0 = t0 + l0;
         const int64_t block = __shfl_sync(0xffffffffu, blk, l0);
-        // the run's length and smallest offset
+        float *cell = scales + block * a.H_kv + h;
+        const float old = *cell;
+        // the run's length, its smallest offset, and whether its slots follow one another
         int64_t n = 0;
         int low = bs;
+        bool dense = true;
+        const int off0 = (int)(a.slot_mapping[run0] & (bs - 1));
         while (true) {
-            const int64_t t = run0 + n + lane;
-            const int64_t s = t < a.T ? a.slot_mapping[t] : -1;
-            const bool in = s >= 0 && s < slots && (s >> a.block_shift) == block;
-            const unsigned out = __ballot_sync(0xffffffffu, !in);
-            const int take = out ? __ffs(out) - 1 : 32;
-            if (lane < take)
-                low = min(low, (int)(s & (bs - 1)));
-            n += take;
-            if (take < 32)
+            int64_t s[4];
+            int took = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t t = run0 + n + 32 * k + lane;
+                s[k] = t < a.T ? a.slot_mapping[t] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = took == 32 * k && s[k] >= 0 && s[k] < slots && (s[k] >> a.block_shift) == block;
+                const unsigned out = __ballot_sync(0xffffffffu, !in);
+                const int take = out ? __ffs(out) - 1 : 32;
+                if (lane < take) {
+                    const int off = (int)(s[k] & (bs - 1));
+                    low = min(low, off);
+                    dense = dense && off == off0 + n + 32 * k + lane;
+                }
+                took += take;
+            }
+            n += took;
+            if (took < 128)
                 break;
         }
         low = __reduce_min_sync(0xffffffffu, low);
+        dense = __all_sync(0xffffffffu, dense);
 
-        const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+        const int sub = tid / kLanes, col = (tid % kLanes) * 8;
         const __nv_bfloat16 *rows = src + run0 * st + col;
         uint4 held[kHeld];
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            if (i * kRows >= n)
-                break;
-            const int r = i * kRows + sub;
+            const int64_t r = i * kRows + sub;
             held[i] = r < n ? *reinterpret_cast<const uint4 *>(rows + r * st) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            if (i * kRows >= n)
-                break;
+        for (int i = 0; i < kHeld; ++i)
             m = amax8<false>(m, held[i]);
-        }
         for (int64_t r = kHeld * kRows + sub; r < n; r += kRows)
             m = amax8<false>(m, *reinterpret_cast<const uint4 *>(rows + r * st));
-        float amax = warp_amax(m);
+        float amax = team_max(m);
         if (isinf(amax)) { // an infinity among the rows: the largest finite value counts
             m = 0;
             for (int64_t r = sub; r < n; r += kRows)
                 m = amax8<true>(m, *reinterpret_cast<const uint4 *>(rows + r * st));
-            amax = warp_amax(m);
+            amax = team_max(m);
         }
         float now = amax == 0.f ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), kMinScale);
         uint8_t *dst = cache + (((block * a.H_kv + h) << a.block_shift)) * D;
-        float *cell = scales + block * a.H_kv + h;
         if (low > 0) {
-            const float old = *cell;
             if (now > old) {
-                for (int i = lane * 16; i < low * D; i += 512) {
+                for (int i = tid * 16; i < low * D; i += 512 * kTeam) {
                     uint4 w = *reinterpret_cast<const uint4 *>(dst + i);
                     w.x = requant4(w.x, old, now);
                     w.y = requant4(w.y, old, now);
@@ -179,26 +203,36 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
                 now = old;
             }
         }
+        // (every thread of the team has read the old scale: it passed the team's maximum, or is in the one warp)
         __syncwarp();
-        if (lane == 0)
+        if (tid == 0)
             *cell = now;
         const E4m3Recip inv = e4m3_recip(now);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            if (i * kRows >= n)
-                break;
-            const int r = i * kRows + sub;
+            const int64_t r = i * kRows + sub;
             if (r < n) {
-                const int off = (int)(a.slot_mapping[run0 + r] & (bs - 1));
+                const int off = dense ? off0 + (int)r : (int)(a.slot_mapping[run0 + r] & (bs - 1));
                 *reinterpret_cast<uint2 *>(dst + off * D + col) = quant8(held[i], now, inv);
             }
         }
         for (int64_t r = kHeld * kRows + sub; r < n; r += kRows) {
-            const int off = (int)(a.slot_mapping[run0 + r] & (bs - 1));
+            const int off = dense ? off0 + (int)r : (int)(a.slot_mapping[run0 + r] & (bs - 1));
             *reinterpret_cast<uint2 *>(dst + off * D + col) =
                 quant8(*reinterpret_cast<const uint4 *>(rows + r * st), now, inv);
         }
     }
+}
+
+template <int D, int kTeam>
+cudaError_t launch(const Kv8AppendArgs &a, cudaStream_t stream)
+{
+    const int64_t items = ((int64_t)a.T + a.window - 1) / a.window * a.H_kv * 2;
+    const int64_t blocks = (items * kTeam * 32 + kThreads - 1) / kThreads;
+    if (blocks > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    kv8_append_kernel<D, kTeam><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 } // namespace
@@ -206,19 +240,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const Kv8Append
 cudaError_t launch_kv8_append(const Kv8AppendArgs &args, int D, int sm_count, cudaStream_t stream)
 {
     Kv8AppendArgs a = args;
-    // one token to a warp while that gives each SM at most 128 warps (a decode
-    // step's runs are one token long); beyond, 8 tokens: of a prompt's warps
-    // only those at a block's start have a run
-    a.window = (int64_t)a.T * a.H_kv * 2 <= (int64_t)sm_count * 128 ? 1 : 8;
-    const int64_t items = ((int64_t)a.T + a.window - 1) / a.window * a.H_kv * 2;
-    const int64_t blocks = (items + kWarps - 1) / kWarps;
-    if (blocks > 0x7FFFFFFF)
-        return cudaErrorInvalidValue;
-    if (D == 128)
-        kv8_append_kernel<128><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(a);
-    else
-        kv8_append_kernel<64><<<(unsigned)blocks, kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    // a warp to each token while that gives each SM at most 128 warps (a decode
+    // step's runs are one token long); beyond, four warps to 32 tokens, whose runs
+    // are long in a prompt
+    if ((int64_t)a.T * a.H_kv * 2 <= (int64_t)sm_count * 128) {
+        a.window = 1;
+        return D == 128 ? launch<128, 1>(a, stream) : launch<64, 1>(a, stream);
+    }
+    a.window = 32;
+    return D == 128 ? launch<128, 4>(a, stream) : launch<64, 4>(a, stream);
 }
 
 cudaError_t read_append_error(int *out, bool reset)

@@ -3,12 +3,14 @@
 //
 // The work is cut evenly, whatever the lengths: a unit is (request, chunk of
 // R = 8 kTiles query rows, kv head), its length in steps of 32 positions plus a
-// constant for its start and end; the units laid end to end are divided into
-// equal parts, one per block of a grid that fills the GPU once. A block walks
-// its part; a unit that lies in it whole is finished there, one that several
-// blocks share leaves partial sums that a second kernel (launched behind, its
-// start overlapped) joins in a fixed order. Nothing depends on the host
-// knowing the lengths, so a captured call follows them.
+// constant for its start and end; the units laid end to end are cut into parts,
+// one per block: equal ones that fill the GPU once with eleven twelfths of the
+// work, then as many small ones for the blocks that are done first (SMs differ by
+// 15% in what they get through). A block walks its part; a unit that lies in
+// it whole is finished there, one that several blocks share leaves partial sums
+// that a second kernel (launched behind, its start overlapped) joins in a fixed
+// order. Nothing depends on the host knowing the lengths, so a captured call
+// follows them; the division depends on nothing else, so results do not vary.
 //
 // In a block the four warps take a unit's steps in turn, each with its own
 // softmax state and its own ring of TMA copies: nothing is waited for between
@@ -34,6 +36,8 @@
 // by 8 (then p' would pass 2^8): one vote a step instead of a reduction.
 #include "smla_kv8.cuh"
 #include "smla_umma.cuh"
+
+#include <algorithm>
 
 namespace smla {
 
@@ -93,6 +97,38 @@ __device__ __forceinline__ Units units_of(const Kv8AttnArgs &a, const Request &r
     return u;
 }
 
+// How the total cost is cut: `big` equal parts of the first big_total, then
+// `small` equal ones.
+constexpr int kSmallPerBig = 1;
+struct Division {
+    long long total, big_total;
+    int big, small;
+
+    // fill: the blocks that the GPU holds; grid: those launched (fill, or with the small parts too)
+    __device__ static Division of(long long total, int fill, int grid)
+    {
+        Division d{total, total, 0, 0};
+        const long long parts = max(1ll, (total + kMinPart - 1) / kMinPart);
+        d.big = (int)min((long long)fill, parts);
+        // small parts of a twelfth of a block's share, where that is work enough for one
+        if (grid > fill && total / 12 >= (long long)2 * kMinPart * fill) {
+            d.small = grid - fill;
+            d.big_total = total - total / 12 * kSmallPerBig;
+        }
+        return d;
+    }
+    __device__ long long begin(int i) const
+    {
+        return i <= big ? big_total * i / big : big_total + (total - big_total) * (i - big) / small;
+    }
+    // the part that holds cost x
+    __device__ int part(long long x) const
+    {
+        return x < big_total ? (int)(((x + 1) * big - 1) / big_total)
+                             : big + (int)(((x - big_total + 1) * small - 1) / (total - big_total));
+    }
+};
+
 template <int D, int NT> struct Layout {
     static constexpr int R = 8 * NT;
     static constexpr int kSide = kStep * D;                     // K (or V) of one step
@@ -111,6 +147,7 @@ struct Part {
     int4 *dir;
     float2 *ml;   // [2 blocks][R]
     float *o;     // [2 blocks][R][D]
+    int fill;     // blocks that the GPU holds at a time
 };
 
 template <int D, int NT>
@@ -129,9 +166,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
     uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + L::kBig + kWarps * R * 8 + kWarps * kStages * 32);
     // The block's place in the work, kept here and not in registers while a unit is worked on.
     __shared__ struct {
-        long long at, hi, total; // cost: where the block is, where its part ends, the whole
-        long long base, unit0;   // cost and units before request b
-        int b, blocks;
+        long long at, hi;      // cost: where the block is, where its part ends
+        long long base, unit0; // cost and units before request b
+        int b;
+        Division cut;
         long long warp_cost[kWarps], warp_count[kWarps];
     } s_walk;
 
@@ -174,9 +212,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         }
         if (blockIdx.x == 0 && tid == 0)
             *part.header = (int)units; // for the joining kernel
-        const long long blocks = max(1ll, min((long long)gridDim.x, (total + kMinPart - 1) / kMinPart));
-        const long long lo = total * blockIdx.x / blocks, hi = total * (blockIdx.x + 1) / blocks;
-        if (blockIdx.x >= blocks || lo >= hi)
+        const Division cut = Division::of(total, part.fill, gridDim.x);
+        if ((int)blockIdx.x >= cut.big + cut.small)
+            return;
+        const long long lo = cut.begin(blockIdx.x), hi = cut.begin(blockIdx.x + 1);
+        if (lo >= hi)
             return;
         if (lo >= cost0 && lo < cost0 + cost) {
             int b = tid * per;
@@ -188,11 +228,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             }
             s_walk.at = lo;
             s_walk.hi = hi;
-            s_walk.total = total;
             s_walk.base = cost0;
             s_walk.unit0 = count0;
             s_walk.b = b;
-            s_walk.blocks = (int)blocks;
+            s_walk.cut = cut;
         }
     }
     const float scale_log2 = a.scale * kLog2e;
@@ -242,8 +281,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         const bool whole = s0 == 0 && s1 == un.steps;
         if (s0 == 0 && tid == 0) {
             // blocks that hold the unit's first and last step
-            const long long x0 = ubase + kUnitCost, x1 = ubase + un.cost - 1, total = s_walk.total;
-            const int c0 = (int)(((x0 + 1) * s_walk.blocks - 1) / total), c1 = (int)(((x1 + 1) * s_walk.blocks - 1) / total);
+            const int c0 = s_walk.cut.part(ubase + kUnitCost), c1 = s_walk.cut.part(ubase + un.cost - 1);
             part.dir[unit0 + ui] = make_int4(c0, c1, b, (int)ui);
         }
         const int h = (int)(ui % a.H_kv);
@@ -611,13 +649,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                 atomicOr(&g_kv8_stream_error, 2);
 }
 
-// Joins the partial sums of the units that several blocks share: a warp to a
-// row, the blocks in order.
+// Joins the partial sums of the units that several blocks share: a block to a
+// row, its warps take the parts in turn, and their sums are added in order.
+constexpr int kJoinWarps = 4;
 template <int D, int NT>
-__global__ void __launch_bounds__(256) kv8_join_kernel(const Kv8AttnArgs a, const Part part)
+__global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8AttnArgs a, const Part part)
 {
     constexpr int R = 8 * NT;
     constexpr int kD = D / 32; // columns of a lane
+    __shared__ float s_acc[kJoinWarps][D];
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     umma::grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if ((int)blockIdx.x >= *part.header)
@@ -626,52 +667,72 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const Kv8AttnArgs a, cons
     if (u.x == u.y)
         return;
     const Request rq = request(a, u.z);
-    const int h = u.w % a.H_kv, row0 = u.w / a.H_kv * R;
-    const int rows = min(R, rq.qlen * a.G - row0);
-    for (int r = warp; r < rows; r += 8) {
-        float m = -INFINITY, l = 0.f;
-        for (int c = u.x + lane; c <= u.y; c += 32)
-            m = fmaxf(m, part.ml[(2 * (int64_t)c + (c == u.x)) * R + r].x);
-        m = warp_max(m);
-        float acc[kD];
+    const int h = u.w % a.H_kv, row0 = u.w / a.H_kv * R, r = blockIdx.y;
+    if (r >= min(R, rq.qlen * a.G - row0))
+        return;
+    float m = -INFINITY, l = 0.f;
+    for (int c = u.x + threadIdx.x; c <= u.y; c += kJoinWarps * 32)
+        m = fmaxf(m, part.ml[(2 * (int64_t)c + (c == u.x)) * R + r].x);
+    m = warp_max(m);
+    if (lane == 0)
+        s_m[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+        m = fmaxf(m, s_m[w]);
+    float acc[kD];
+#pragma unroll
+    for (int i = 0; i < kD; ++i)
+        acc[i] = 0.f;
+#pragma unroll 4
+    for (int c = u.x + warp; c <= u.y; c += kJoinWarps) {
+        const int64_t slot = (2 * (int64_t)c + (c == u.x)) * R + r;
+        const float2 ml = part.ml[slot];
+        const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+        l += ml.y * f;
+        const float *src = part.o + slot * D + lane * kD;
+        if (D == 128) {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            acc[0] += v.x * f;
+            acc[1] += v.y * f;
+            acc[kD - 2] += v.z * f;
+            acc[kD - 1] += v.w * f;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            acc[0] += v.x * f;
+            acc[1] += v.y * f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kD; ++i)
+        s_acc[warp][lane * kD + i] = acc[i];
+    if (lane == 0)
+        s_l[warp] = l;
+    __syncthreads();
+    if (warp != 0)
+        return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+        l += s_l[w];
 #pragma unroll
         for (int i = 0; i < kD; ++i)
-            acc[i] = 0.f;
-#pragma unroll 4
-        for (int c = u.x; c <= u.y; ++c) {
-            const int64_t slot = (2 * (int64_t)c + (c == u.x)) * R + r;
-            const float2 ml = part.ml[slot];
-            const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
-            l += ml.y * f;
-            const float *src = part.o + slot * D + lane * kD;
-            if (D == 128) {
-                const float4 v = *reinterpret_cast<const float4 *>(src);
-                acc[0] += v.x * f;
-                acc[1] += v.y * f;
-                acc[kD - 2] += v.z * f;
-                acc[kD - 1] += v.w * f;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(src);
-                acc[0] += v.x * f;
-                acc[1] += v.y * f;
-            }
-        }
-        const int64_t t = rq.q0 + (row0 + r) / a.G;
-        const int head = h * a.G + (row0 + r) % a.G;
-        float lse;
-        const float f = finish_row(m, l, a.sinks, head, &lse);
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
-#pragma unroll
-        for (int i = 0; i < kD; i += 2)
-            *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
-        if (a.lse && lane == 0)
-            a.lse[t * a.H + head] = lse;
+            acc[i] += s_acc[w][lane * kD + i];
     }
+    const int64_t t = rq.q0 + (row0 + r) / a.G;
+    const int head = h * a.G + (row0 + r) % a.G;
+    float lse;
+    const float f = finish_row(m, l, a.sinks, head, &lse);
+    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
+#pragma unroll
+    for (int i = 0; i < kD; i += 2)
+        *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
+    if (a.lse && lane == 0)
+        a.lse[t * a.H + head] = lse;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-int blocks_of(int NT, int sm_count) { return sm_count * (NT == 1 ? 3 : 2); }
+int fill_of(int NT, int sm_count) { return sm_count * (NT == 1 ? 3 : 2); }
 
 struct Sizes {
     size_t dir, ml, o, total;
@@ -683,7 +744,7 @@ Sizes sizes(int64_t B, int64_t T, int H, int H_kv, int D, int NT, int sm_count)
     const int R = 8 * NT;
     Sizes s;
     s.units = (T * (H / H_kv) / R + B) * H_kv; // each request's last chunk may be short
-    const size_t slots = 2 * (size_t)blocks_of(NT, sm_count);
+    const size_t slots = 2 * (size_t)fill_of(NT, sm_count) * (1 + kSmallPerBig);
     s.dir = 256;
     s.ml = up256(s.dir + (size_t)s.units * sizeof(int4));
     s.o = up256(s.ml + slots * R * sizeof(float2));
@@ -700,20 +761,27 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
         return cudaErrorInvalidValue;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Part part{reinterpret_cast<int *>(ws), reinterpret_cast<int4 *>(ws + sz.dir),
-                    reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o)};
+                    reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o),
+                    fill_of(NT, sm_count)};
     cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kStep, maps))
         return cudaErrorInvalidValue;
-    kv8_stream_kernel<D, NT><<<blocks_of(NT, sm_count), kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
+    // the most work that there can be decides the grid: blocks without a part end at once, but not for nothing
+    const double most = (double)sz.units * ((double)a.table_width * a.block_size / kStep + kUnitCost + 1);
+    const int fill = part.fill;
+    int grid = fill * (1 + kSmallPerBig);
+    if (most < 24.0 * kMinPart * fill) // no small parts
+        grid = most < (double)fill * kMinPart ? std::max(1, (int)(most / kMinPart) + 1) : fill;
+    kv8_stream_kernel<D, NT><<<grid, kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     // behind it, its start overlapped (it waits for the first kernel's end)
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)sz.units);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)sz.units, 8 * NT);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

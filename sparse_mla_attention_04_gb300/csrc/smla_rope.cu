@@ -12,29 +12,67 @@ __device__ int g_rope_error = 0; // bit 4: a position out of range
 
 namespace {
 
+// Sine and cosine of a 64-bit fraction of a turn (its high 32 bits: 2^-32 of a
+// turn is 1.5e-9 radians, a fortieth of binary32's step at 1). The nearest
+// quarter turn leaves an angle of at most pi/4, for which the Taylor series to
+// x^9 and x^10 are off by less than 2e-9; the quarter then swaps and negates.
+__device__ __forceinline__ void sincos_turn(unsigned hi, float &s, float &c)
+{
+    const unsigned q = (hi + 0x20000000u) >> 30;
+    const float x = (float)(int)(hi - (q << 30)) * 1.4629180792671596e-9f; // 2 pi 2^-32
+    const float y = x * x;
+    float sn = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
+    sn = fmaf(sn, y, 8.3333333e-3f);
+    sn = fmaf(sn, y, -1.6666667e-1f);
+    sn = fmaf(sn * y, x, x);
+    float cs = fmaf(y, -2.7557319e-7f, 2.4801587e-5f);
+    cs = fmaf(cs, y, -1.3888889e-3f);
+    cs = fmaf(cs, y, 4.1666667e-2f);
+    cs = fmaf(cs, y, -0.5f);
+    cs = fmaf(cs, y, 1.0f);
+    const float a = q & 1 ? cs : sn, b = q & 1 ? sn : cs;
+    s = q & 2 ? -a : a;
+    c = (q + 1) & 2 ? -b : b;
+}
+
 // The table. frac[i] is pair i's frequency as a fraction of a turn, times 2^64:
 // position * frac modulo 2^64 is then the angle modulo one turn, with no
 // rounding at all however far the position, in integer arithmetic (binary64
-// would run at 1/64 of the binary32 rate here). The signed high part, times
-// 2^-63, is the angle in half turns in [-1, 1), which sinpi / cospi take.
-// Bound: 4 bytes written per value.
+// would run at 1/64 of the binary32 rate here). A thread keeps its kVec pairs
+// and walks down the rows, adding a constant to each angle. Bound: 4 bytes
+// written per value.
+template <int kVec>
 __global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ table, int64_t rows, int64_t first,
                                                          const RopeFrequencies f)
 {
-    // a thread keeps its pair and walks down the rows
-    const int n = f.pairs;
-    const int per = blockDim.x / n; // rows a block writes at a time
-    const int i = threadIdx.x % n, r0 = threadIdx.x / n;
+    const int n = f.pairs, lanes = n / kVec;
+    const int per = blockDim.x / lanes; // rows a block writes at a time
+    const int i = threadIdx.x % lanes * kVec, r0 = threadIdx.x / lanes;
     if (r0 >= per)
         return;
-    const unsigned long long step = f.frac[i];
-    for (int64_t r = (int64_t)blockIdx.x * per + r0; r < rows; r += (int64_t)gridDim.x * per) {
-        const long long a = (long long)((unsigned long long)(first + r) * step);
-        float s, c;
-        sincospif((float)a * 0x1p-63f, &s, &c);
-        float *row = table + r * 2 * n;
-        row[i] = c * f.factor;
-        row[n + i] = s * f.factor;
+    const int64_t stride = (int64_t)gridDim.x * per;
+    int64_t r = (int64_t)blockIdx.x * per + r0;
+    unsigned long long at[kVec], step[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        at[e] = (unsigned long long)(first + r) * f.frac[i + e];
+        step[e] = (unsigned long long)stride * f.frac[i + e];
+    }
+#pragma unroll 2
+    for (; r < rows; r += stride) {
+        struct alignas(4 * kVec) {
+            float v[kVec];
+        } c, s;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            sincos_turn((unsigned)(at[e] >> 32), s.v[e], c.v[e]);
+            c.v[e] *= f.factor;
+            s.v[e] *= f.factor;
+            at[e] += step[e];
+        }
+        float *row = table + r * 2 * n + i;
+        *reinterpret_cast<decltype(c) *>(row) = c;
+        *reinterpret_cast<decltype(s) *>(row + n) = s;
     }
 }
 
@@ -67,6 +105,7 @@ template <typename E, int kVec> struct alignas(sizeof(E) * kVec) Pack {
 // threadIdx.x is the unit, threadIdx.y the first head, blockIdx.x the token.
 // Both elements of a pair are read before either is written, by the one thread
 // that has them: in-place calls are safe. Bound: bytes in and out.
+constexpr int kBatch = 4;
 template <typename E, int kVec, bool kNeox>
 __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a)
 {
@@ -107,35 +146,50 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a)
             s[e] = __ldg(row + n + p0 + e);
             s[e] = a.inverse ? -s[e] : s[e];
         }
-        for (int h = blockIdx.y * blockDim.y + threadIdx.y; h < heads; h += hstep) {
-            const bool isq = h < a.H;
-            const E *src = static_cast<const E *>(isq ? a.q : a.k) + (isq ? t * a.q_st + h * a.q_sh : t * a.k_st + (h - a.H) * a.k_sh) + a.rot_offset;
-            E *dst = static_cast<E *>(isq ? a.q_out : a.k_out) + (isq ? t * a.qo_st + h * a.qo_sh : t * a.ko_st + (h - a.H) * a.ko_sh) + a.rot_offset;
-            if (kNeox) {
-                const Pack<E, kVec> x = *reinterpret_cast<const Pack<E, kVec> *>(src + p0);
-                const Pack<E, kVec> y = *reinterpret_cast<const Pack<E, kVec> *>(src + n + p0);
+        // kBatch heads at a time: their loads are in flight together
+        for (int h0 = blockIdx.y * blockDim.y + threadIdx.y; h0 < heads; h0 += kBatch * hstep) {
+            Pack<E, kVec> x[kBatch], y[kBatch];
+            E *out[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int h = h0 + k * hstep;
+                if (h < heads) {
+                    const bool isq = h < a.H;
+                    const E *src = static_cast<const E *>(isq ? a.q : a.k) + (isq ? t * a.q_st + h * a.q_sh : t * a.k_st + (h - a.H) * a.k_sh) + a.rot_offset;
+                    out[k] = static_cast<E *>(isq ? a.q_out : a.k_out) + (isq ? t * a.qo_st + h * a.qo_sh : t * a.ko_st + (h - a.H) * a.ko_sh) + a.rot_offset;
+                    if (kNeox) {
+                        x[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + p0);
+                        y[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + n + p0);
+                    } else {
+                        x[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + 2 * p0);
+                        if (kVec == 1)
+                            y[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + 2 * p0 + 1);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (h0 + k * hstep >= heads)
+                    break;
+                E *dst = out[k];
                 Pack<E, kVec> xo, yo;
+                if (kNeox || kVec == 1) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    xo.e[e] = from_f<E>(rot_a(to_f(x.e[e]), to_f(y.e[e]), c[e], s[e]));
-                    yo.e[e] = from_f<E>(rot_b(to_f(x.e[e]), to_f(y.e[e]), c[e], s[e]));
-                }
-                *reinterpret_cast<Pack<E, kVec> *>(dst + p0) = xo;
-                *reinterpret_cast<Pack<E, kVec> *>(dst + n + p0) = yo;
-            } else if (kVec > 1) {
-                const Pack<E, kVec> x = *reinterpret_cast<const Pack<E, kVec> *>(src + 2 * p0);
-                Pack<E, kVec> o;
+                    for (int e = 0; e < kVec; ++e) {
+                        xo.e[e] = from_f<E>(rot_a(to_f(x[k].e[e]), to_f(y[k].e[e]), c[e % kPairs], s[e % kPairs]));
+                        yo.e[e] = from_f<E>(rot_b(to_f(x[k].e[e]), to_f(y[k].e[e]), c[e % kPairs], s[e % kPairs]));
+                    }
+                    *reinterpret_cast<Pack<E, kVec> *>(dst + (kNeox ? p0 : 2 * p0)) = xo;
+                    *reinterpret_cast<Pack<E, kVec> *>(dst + (kNeox ? n + p0 : 2 * p0 + 1)) = yo;
+                } else {
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e) {
-                    const float xa = to_f(x.e[(2 * e) % kVec]), xb = to_f(x.e[(2 * e + 1) % kVec]);
-                    o.e[(2 * e) % kVec] = from_f<E>(rot_a(xa, xb, c[e], s[e]));
-                    o.e[(2 * e + 1) % kVec] = from_f<E>(rot_b(xa, xb, c[e], s[e]));
+                    for (int e = 0; e < kPairs; ++e) {
+                        const float xa = to_f(x[k].e[(2 * e) % kVec]), xb = to_f(x[k].e[(2 * e + 1) % kVec]);
+                        xo.e[(2 * e) % kVec] = from_f<E>(rot_a(xa, xb, c[e], s[e]));
+                        xo.e[(2 * e + 1) % kVec] = from_f<E>(rot_b(xa, xb, c[e], s[e]));
+                    }
+                    *reinterpret_cast<Pack<E, kVec> *>(dst + 2 * p0) = xo;
                 }
-                *reinterpret_cast<Pack<E, kVec> *>(dst + 2 * p0) = o;
-            } else {
-                const float xa = to_f(src[2 * p0]), xb = to_f(src[2 * p0 + 1]);
-                dst[2 * p0] = from_f<E>(rot_a(xa, xb, c[0], s[0]));
-                dst[2 * p0 + 1] = from_f<E>(rot_b(xa, xb, c[0], s[0]));
             }
         }
     }
@@ -149,7 +203,11 @@ cudaError_t launch_vec(const RopeArgs &a, int sm_count, cudaStream_t stream)
     const int units = (a.neox ? n : a.rot_dim) / kV + (a.D - a.rot_dim) / kVec;
     const int x = std::min(units, 256);
     const int heads = a.H + a.H_k;
-    const int y = std::max(1, std::min(256 / x, heads));
+    // a thread's batches should come out even: 40 heads over 16 threads' rows would leave the last half idle
+    int y = std::max(1, std::min(128 / x, heads));
+    const int64_t rounds = (heads + (int64_t)y * kBatch - 1) / ((int64_t)y * kBatch);
+    if (rounds == 1)
+        y = std::max(1, std::min(y, (heads + kBatch - 1) / kBatch));
     // few tokens: their heads are spread over blocks until the SMs have two each
     int64_t groups = (heads + y - 1) / y;
     groups = std::min<int64_t>(groups, std::max<int64_t>(1, (int64_t)2 * sm_count / a.T));
@@ -183,9 +241,14 @@ cudaError_t launch_rope_table(float *table, int64_t rows, int64_t first, const R
 {
     if (rows == 0)
         return cudaSuccess;
-    const int per = 256 / f.pairs;
+    // four pairs to a thread (16-byte stores) where the rows allow it
+    const bool vec = f.pairs % 4 == 0 && reinterpret_cast<uintptr_t>(table) % 16 == 0;
+    const int per = 256 / (vec ? f.pairs / 4 : f.pairs);
     const int64_t blocks = std::min<int64_t>((rows + per - 1) / per, (int64_t)std::max(sm_count, 1) * 8);
-    rope_table_kernel<<<(unsigned)blocks, 256, 0, stream>>>(table, rows, first, f);
+    if (vec)
+        rope_table_kernel<4><<<(unsigned)blocks, 256, 0, stream>>>(table, rows, first, f);
+    else
+        rope_table_kernel<1><<<(unsigned)blocks, 256, 0, stream>>>(table, rows, first, f);
     return cudaGetLastError();
 }
 

@@ -3,11 +3,12 @@
 // given back), then independent fills of tokens and table entries.
 //
 // Work and bound: 12 bytes read per request, 20 written per token. A decode
-// step is a few kilobytes, so it is one launch of one block, whose scan and
-// fill meet in block barriers; past kOneBlockTokens tokens the fill is a second
-// launch over the whole GPU and the plan passes through the workspace. No
-// entry that one thread writes is read by another within the fill: a token
-// whose block is new takes it from the ring, as the table's writer does.
+// step is a few kilobytes, so it is one launch of one block (a thread to a
+// request, the plan in shared memory); with more than kOneBlockTokens tokens or
+// kThreads requests the fill is a second launch over the whole GPU and the plan
+// passes through the workspace. No entry that one thread writes is read by
+// another within the fill: a token whose block is new takes it from the ring, as
+// the table's writer does.
 #include "smla_device.cuh"
 #include "smla_internal.h"
 
@@ -19,6 +20,8 @@ namespace {
 constexpr int kThreads = 1024;
 // Above this many tokens the fill runs on the whole GPU.
 constexpr int kOneBlockTokens = 4096;
+// Up to this many requests a block of the whole-GPU fill searches a copy of the starts in shared memory.
+constexpr int kSharedStarts = 4096;
 
 struct Sums {
     long long q, take, give;
@@ -124,24 +127,92 @@ __device__ __forceinline__ void fill_blocks(const TablesArgs &a, int b, int4 p, 
         a.free_ring[((long long)head + count + give + j - p.z) % a.ring_size] = row[j];
 }
 
-// The scan, by one block. With `fill`, the fill too. The inputs are all read
-// before the outputs that may be the same buffers (held counts, ring state)
-// are written.
-template <bool kFill>
+__device__ __forceinline__ void pad_token(const TablesArgs &a, int64_t t)
+{
+    a.positions[t] = 0;
+    a.slot_mapping[t] = -1;
+    if (a.token_request)
+        a.token_request[t] = -1;
+}
+
+__device__ __forceinline__ int2 ring_state(const TablesArgs &a)
+{
+    const int h = a.ring_state[0] % a.ring_size;
+    return make_int2(h < 0 ? h + a.ring_size : h, min(max(a.ring_state[1], 0), a.ring_size));
+}
+
+__device__ __forceinline__ void finish_scan(const TablesArgs &a, const Sums &all, long long lacking, int head, int count)
+{
+    const bool ok = lacking == 0;
+    a.query_start[a.B] = clamp31(all.q);
+    a.counts[0] = clamp31(all.q);
+    a.counts[1] = ok ? clamp31(all.take) : 0;
+    a.counts[2] = ok ? clamp31(all.give) : 0;
+    a.counts[3] = clamp31(lacking);
+    a.ring_state_out[0] = ok ? (int)((head + all.take) % a.ring_size) : head;
+    a.ring_state_out[1] = ok ? (int)min(count - all.take + all.give, (long long)a.ring_size) : count;
+}
+
+// Scan and fill by one block, a thread to a request (B <= kThreads). The
+// inputs are all read before the outputs that may be the same buffers (held
+// counts, ring state) are written.
+__global__ void __launch_bounds__(kThreads) tables_small_kernel(const TablesArgs a)
+{
+    __shared__ Sums warp_sums[32];
+    __shared__ int4 s_plan[kThreads];
+    __shared__ int s_start[kThreads + 1], s_give[kThreads];
+    __shared__ int s_wide;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int2 ring = ring_state(a);
+    const int head = ring.x, count = ring.y;
+    Request r{0, 0, 0, 0};
+    if (tid < a.B)
+        r = request(a, tid);
+    if (tid == 0)
+        s_wide = 0;
+    const Sums v{r.q, max(r.need - r.held, 0), max(r.held - r.need, 0)};
+    Sums all;
+    const Sums x = block_exclusive(v, &all, warp_sums);
+    if (r.need > a.table_width)
+        atomicAdd(&s_wide, min(r.need - a.table_width, INT_MAX / kThreads)); // (whole numbers: any order)
+    __syncthreads();
+    const long long lacking = s_wide + max(all.take - count, 0ll);
+    const bool ok = lacking == 0;
+    if (tid < a.B) {
+        const int after = ok ? r.need : r.held;
+        s_start[tid] = clamp31(x.q);
+        s_plan[tid] = make_int4(clamp31(x.take), r.held, after, r.len);
+        s_give[tid] = clamp31(x.give);
+        a.query_start[tid] = s_start[tid];
+        a.blocks_held_out[tid] = after;
+    }
+    if (tid == 0) {
+        s_start[a.B] = clamp31(all.q);
+        finish_scan(a, all, lacking, head, count);
+    }
+    __syncthreads();
+    for (int64_t t = tid; t < a.num_tokens; t += kThreads) {
+        if (t < all.q) {
+            const int b = find_request(s_start, 0, a.B - 1, t);
+            fill_token(a, t, b, s_start[b], s_plan[b], s_start[b + 1] - s_start[b], head);
+        } else {
+            pad_token(a, t);
+        }
+    }
+    if (ok && all.take + all.give > 0)
+        for (int b = warp; b < a.B; b += kThreads / 32)
+            fill_blocks(a, b, s_plan[b], s_give[b], head, count, lane);
+}
+
+// The scan alone, for any number of requests: one block, its plan to the workspace.
 __global__ void __launch_bounds__(kThreads) tables_scan_kernel(const TablesArgs a)
 {
     __shared__ Sums warp_sums[32];
-    __shared__ int s_state[2];
     const int tid = threadIdx.x;
-    if (tid == 0) {
-        const int h = a.ring_state[0] % a.ring_size;
-        s_state[0] = h < 0 ? h + a.ring_size : h;
-        s_state[1] = min(max(a.ring_state[1], 0), a.ring_size);
-    }
+    const int2 ring = ring_state(a);
+    const int head = ring.x, count = ring.y;
     Sums all{0, 0, 0};
     long long lacking = 0;
-    // first pass: what the batch takes in all (with up to kThreads requests
-    // the second pass's numbers are the first's)
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         Sums v{0, 0, 0};
@@ -152,17 +223,13 @@ __global__ void __launch_bounds__(kThreads) tables_scan_kernel(const TablesArgs 
             wide = max(r.need - a.table_width, 0);
         }
         Sums total;
-        const Sums x{v.q, v.take, v.give};
-        (void)block_exclusive(x, &total, warp_sums);
+        (void)block_exclusive(v, &total, warp_sums);
         all = add(all, total);
-        Sums w{wide, 0, 0};
         if (__syncthreads_or(wide)) {
-            (void)block_exclusive(w, &total, warp_sums);
+            (void)block_exclusive(Sums{wide, 0, 0}, &total, warp_sums);
             lacking += total.q;
         }
     }
-    __syncthreads();
-    const int head = s_state[0], count = s_state[1];
     lacking += max(all.take - count, 0ll);
     const bool ok = lacking == 0;
     Sums carry{0, 0, 0};
@@ -186,46 +253,26 @@ __global__ void __launch_bounds__(kThreads) tables_scan_kernel(const TablesArgs 
         carry = add(carry, total);
     }
     if (tid == 0) {
-        a.query_start[a.B] = clamp31(all.q);
-        a.counts[0] = clamp31(all.q);
-        a.counts[1] = ok ? clamp31(all.take) : 0;
-        a.counts[2] = ok ? clamp31(all.give) : 0;
-        a.counts[3] = clamp31(lacking);
-        a.ring_state_out[0] = ok ? (int)((head + all.take) % a.ring_size) : head;
-        a.ring_state_out[1] = ok ? (int)min(count - all.take + all.give, (long long)a.ring_size) : count;
-        if (!kFill) {
-            a.state[0] = head;
-            a.state[1] = count;
-        }
-    }
-    if (kFill) {
-        __syncthreads();
-        const int lane = tid & 31, warp = tid >> 5;
-        // tokens read old table entries and the ring; blocks that were given
-        // back are only written over ring places that hold none
-        for (int64_t t = tid; t < a.num_tokens; t += kThreads) {
-            if (t < all.q) {
-                const int b = find_request(a.query_start, 0, a.B - 1, t);
-                const int start = a.query_start[b];
-                fill_token(a, t, b, start, a.plan[b], a.query_start[b + 1] - start, head);
-            } else {
-                a.positions[t] = 0;
-                a.slot_mapping[t] = -1;
-                if (a.token_request)
-                    a.token_request[t] = -1;
-            }
-        }
-        if (all.take + all.give > 0 && ok)
-            for (int b = warp; b < a.B; b += kThreads / 32)
-                fill_blocks(a, b, a.plan[b], a.give_start[b], head, count, lane);
+        a.state[0] = head;
+        a.state[1] = count;
+        finish_scan(a, all, lacking, head, count);
     }
 }
 
 // The fill over the whole GPU: a warp takes 64 consecutive tokens (finds the
 // requests of the first and the last, between which its lanes search), then
 // one request's blocks.
+template <bool kShared>
 __global__ void __launch_bounds__(256) tables_fill_kernel(const TablesArgs a)
 {
+    __shared__ int s_start[kShared ? kSharedStarts + 1 : 1];
+    const int32_t *start_of = a.query_start;
+    if (kShared) {
+        for (int i = threadIdx.x; i <= a.B; i += blockDim.x)
+            s_start[i] = a.query_start[i];
+        __syncthreads();
+        start_of = s_start;
+    }
     const int lane = threadIdx.x & 31;
     const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -235,11 +282,8 @@ __global__ void __launch_bounds__(256) tables_fill_kernel(const TablesArgs a)
         const int64_t t0 = g * 64;
         int lo = 0, hi = 0;
         if (t0 < total) {
-            lo = find_request(a.query_start, 0, a.B - 1, t0);
-            hi = find_request(a.query_start, lo, min(a.B - 1, lo + 64), min(t0 + 63, total - 1));
-            // more than 64 requests further on (empty ones between): search them all
-            if (hi == lo + 64)
-                hi = a.B - 1;
+            lo = find_request(start_of, 0, a.B - 1, t0);
+            hi = find_request(start_of, lo, a.B - 1, min(t0 + 63, total - 1));
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -247,14 +291,10 @@ __global__ void __launch_bounds__(256) tables_fill_kernel(const TablesArgs a)
             if (t >= a.num_tokens)
                 break;
             if (t < total) {
-                const int b = find_request(a.query_start, lo, hi, t);
-                const int start = a.query_start[b];
-                fill_token(a, t, b, start, a.plan[b], a.query_start[b + 1] - start, head);
+                const int b = find_request(start_of, lo, hi, t);
+                fill_token(a, t, b, start_of[b], a.plan[b], start_of[b + 1] - start_of[b], head);
             } else {
-                a.positions[t] = 0;
-                a.slot_mapping[t] = -1;
-                if (a.token_request)
-                    a.token_request[t] = -1;
+                pad_token(a, t);
             }
         }
     }
@@ -268,16 +308,20 @@ __global__ void __launch_bounds__(256) tables_fill_kernel(const TablesArgs a)
 
 cudaError_t launch_block_tables(const TablesArgs &a, int sm_count, cudaStream_t stream)
 {
-    if (a.num_tokens <= kOneBlockTokens) {
-        tables_scan_kernel<true><<<1, kThreads, 0, stream>>>(a);
+    if (a.num_tokens <= kOneBlockTokens && a.B <= kThreads) {
+        tables_small_kernel<<<1, kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    tables_scan_kernel<false><<<1, kThreads, 0, stream>>>(a);
+    tables_scan_kernel<<<1, kThreads, 0, stream>>>(a);
     if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess)
         return e;
     const int64_t blocks = (a.num_tokens / 64 + 7) / 8 + 1;
     const int64_t most = (int64_t)(sm_count > 0 ? sm_count : 1) * 8;
-    tables_fill_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(a);
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    if (a.B <= kSharedStarts)
+        tables_fill_kernel<true><<<grid, 256, 0, stream>>>(a);
+    else
+        tables_fill_kernel<false><<<grid, 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

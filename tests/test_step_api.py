@@ -148,3 +148,13 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         b._kv8_cache(torch.zeros(4, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2, 16, 64, dtype=torch.uint8),
                      torch.ones(4, 2), torch.ones(4, 2))   # not on a GPU
+
+
+def test_packed_structures_match_the_headers():
+    """The packed layouts have the C structures' size and field offsets."""
+    for packed, st in ((b._ROPE_PARAMS, b.SmlaRopeParams), (b._KV8_ATTN_PARAMS, b.SmlaKv8AttnParams)):
+        assert packed.size == ctypes.sizeof(st)
+        n = len(st._fields_)
+        values = [i + 1 for i in range(n)]
+        got = st.from_buffer_copy(packed.pack(*values))
+        assert [getattr(got, name) for name, _ in st._fields_] == values
