@@ -487,7 +487,8 @@ SMLA_API smla_status smla_rope(const smla_rope_params *params);
  * k, v          device, bf16 [T, H_kv, D], element strides (t, h) multiples of
  *               8, 16-byte aligned, last dimension contiguous.
  * slot_mapping  device, int64 [T].
- * caches 16-byte aligned, scales 4-byte aligned. D is 64 or 128.
+ * caches 16-byte aligned, scales 4-byte aligned. D is 64 or 128; num_blocks
+ * below 2^31.
  */
 SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v,
                                      int64_t v_stride_t, int64_t v_stride_h, const int64_t *slot_mapping, int T,

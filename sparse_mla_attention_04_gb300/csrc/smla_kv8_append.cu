@@ -49,16 +49,53 @@ __device__ __forceinline__ uint32_t amax8(uint32_t m, const uint4 &v)
     return m;
 }
 
-__device__ __forceinline__ uint2 quant8(const uint4 v, float s, const E4m3Recip &inv)
+// The codes of eight quotients by division: out of line, for the few vectors
+// that need it (its code would be most of the kernel's).
+__device__ __noinline__ uint2 divide8(const uint4 v, float s)
 {
-    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&v);
-    const float2 f0 = __bfloat1622float2(p[0]), f1 = __bfloat1622float2(p[1]);
-    const float2 f2 = __bfloat1622float2(p[2]), f3 = __bfloat1622float2(p[3]);
-    return make_uint2(quant4_e4m3(f0.x, f0.y, f1.x, f1.y, s, inv), quant4_e4m3(f2.x, f2.y, f3.x, f3.y, s, inv));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+        c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s)), __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2((c[0] & 0xFFFFu) | (c[1] << 16), (c[2] & 0xFFFFu) | (c[3] << 16));
+}
+
+// Two products in one instruction.
+__device__ __forceinline__ float2 mul2(float x, float y, float f)
+{
+    uint64_t a, b, r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(a) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %1};\n" : "=l"(b) : "f"(f));
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+
+// Eight bf16 values as codes of x / s (binary32 division): found by the two
+// products that bracket each quotient (see quant4_e4m3), divided where they differ.
+__device__ __forceinline__ uint2 quant8(const uint4 v, float s, const E4m3Recip &r)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __uint_as_float(w[i] << 16), y = __uint_as_float(w[i] & 0xFFFF0000u);
+        lo[i] = __nv_cvt_float2_to_fp8x2(mul2(x, y, r.lo), __NV_SATFINITE, __NV_E4M3);
+        hi[i] = __nv_cvt_float2_to_fp8x2(mul2(x, y, r.hi), __NV_SATFINITE, __NV_E4M3);
+    }
+    const uint2 a = make_uint2(__byte_perm(lo[0], lo[1], 0x5410), __byte_perm(lo[2], lo[3], 0x5410));
+    const uint2 b = make_uint2(__byte_perm(hi[0], hi[1], 0x5410), __byte_perm(hi[2], hi[3], 0x5410));
+    if (!r.ok || a.x != b.x || a.y != b.y)
+        return divide8(v, s);
+    return a;
 }
 
 // Four older codes under a grown scale: E4M3(code * old / now), each operation rounded in binary32.
-__device__ __forceinline__ uint32_t requant4(uint32_t w, float old, float now)
+__device__ __noinline__ uint32_t requant4(uint32_t w, float old, float now)
 {
     uint32_t lo, hi;
     e4m3x4_to_f16x4(w, lo, hi);
@@ -78,16 +115,16 @@ __device__ __forceinline__ float warp_amax(uint32_t m)
 }
 
 template <int D, int kTeam> // kTeam: warps of a team
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArgs a)
+__global__ void __launch_bounds__(kThreads, kTeam == 4 ? 8 : 4) kv8_append_kernel(const Kv8AppendArgs a)
 {
     constexpr int kLanes = D / 8;                  // lanes of one row
     constexpr int kRows = 32 * kTeam / kLanes;     // rows of one team-wide access
     __shared__ uint32_t s_amax[kThreads / 32];
     const int lane = threadIdx.x & 31;
     const int tid = threadIdx.x % (32 * kTeam);    // in the team
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / 32 / kTeam) + threadIdx.x / (32 * kTeam);
-    const int which = (int)(item % (2 * a.H_kv));
-    const int64_t t0 = item / (2 * a.H_kv) * a.window;
+    const int item = (int)(blockIdx.x * (kThreads / 32 / kTeam) + threadIdx.x / (32 * kTeam));
+    const int which = item % (2 * a.H_kv);
+    const int t0 = item / (2 * a.H_kv) * a.window;
     if (t0 >= a.T)
         return; // (a team of four is a block: all of it returns)
     const int h = which >> 1;
@@ -113,113 +150,133 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
         return f;
     };
 
-    // lane l holds the block of token t0 + l: a run begins where it changes
-    auto block_of = [&](int64_t t, bool report) -> int64_t {
+    // a run begins where the block changes; lane l looks at tokens t0 + l, t0 + 32 + l, ... of the window
+    auto block_of = [&](int t, bool report) -> int {
         if (t < 0 || t >= a.T)
             return -1;
         const int64_t s = a.slot_mapping[t];
         if (s >= slots && report)
             atomicOr(&g_append_error, 8);
-        return s >= 0 && s < slots ? s >> a.block_shift : -1;
+        return s >= 0 && s < slots ? (int)(s >> a.block_shift) : -1;
     };
-    const int64_t blk = lane < a.window ? block_of(t0 + lane, which == 0) : -1;
-    int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
-    if (lane == 0)
-        before = block_of(t0 - 1, false);
-    unsigned begins = __ballot_sync(0xffffffffu, blk >= 0 && blk != before);
-    while (begins) {
-        const int l0 = __ffs(begins) - 1;
-        begins &= begins - 1;
-        const int64_t run0 = t0 + l0;
-        const int64_t block = __shfl_sync(0xffffffffu, blk, l0);
-        float *cell = scales + block * a.H_kv + h;
-        const float old = *cell;
-        // the run's length, its smallest offset, and whether its slots follow one another
-        int64_t n = 0;
-        int low = bs;
-        bool dense = true;
-        const int off0 = (int)(a.slot_mapping[run0] & (bs - 1));
-        while (true) {
-            int64_t s[4];
-            int took = 0;
+    int last = block_of(t0 - 1, false); // of the token before
+    for (int w0 = 0; w0 < a.window; w0 += 32) {
+        const int blk = w0 + lane < a.window ? block_of(t0 + w0 + lane, which == 0) : -1;
+        int before = __shfl_up_sync(0xffffffffu, blk, 1);
+        before = lane == 0 ? last : before;
+        last = __shfl_sync(0xffffffffu, blk, 31);
+        unsigned begins = __ballot_sync(0xffffffffu, blk >= 0 && blk != before);
+        while (begins) {
+            const int l0 = __ffs(begins) - 1;
+            begins &= begins - 1;
+            const int run0 = t0 + w0 + l0;
+            const int block = __shfl_sync(0xffffffffu, blk, l0);
+            float *cell = scales + (int64_t)block * a.H_kv + h;
+            const float old = *cell;
+            const int64_t first_slot = (int64_t)block << a.block_shift;
+            const int64_t *run_slots = a.slot_mapping + run0;
+            const int off0 = (int)(run_slots[0] - first_slot);
+            const int sub = tid / kLanes, col = (tid % kLanes) * 8;
+            const __nv_bfloat16 *rows = src + (int64_t)run0 * st + col + sub * st;
+            const int64_t step = kRows * st;
+            // A team of four asks for what a run that fills its block has before the run's
+            // length is known: mostly it does.
+            const int room = min(bs - off0, a.T - run0);
+            uint4 held[kHeld];
+            if (kTeam > 1) {
+                const __nv_bfloat16 *p = rows;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t t = run0 + n + 32 * k + lane;
-                s[k] = t < a.T ? a.slot_mapping[t] : -1;
+                for (int i = 0; i < kHeld; ++i, p += step)
+                    held[i] = i * kRows + sub < room ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
             }
+            // the run's length, its smallest offset, and whether its slots follow one another
+            int n = 0, low = bs;
+            bool dense = true;
+            while (true) {
+                int off[4], took = 0; // offsets in the block: outside [0, bs) for another block's slots
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bool in = took == 32 * k && s[k] >= 0 && s[k] < slots && (s[k] >> a.block_shift) == block;
-                const unsigned out = __ballot_sync(0xffffffffu, !in);
-                const int take = out ? __ffs(out) - 1 : 32;
-                if (lane < take) {
-                    const int off = (int)(s[k] & (bs - 1));
-                    low = min(low, off);
-                    dense = dense && off == off0 + n + 32 * k + lane;
+                for (int k = 0; k < 4; ++k) {
+                    const int i = n + 32 * k + lane;
+                    const int64_t d = i < a.T - run0 ? run_slots[i] - first_slot : -1;
+                    off[k] = d >= 0 && d < bs ? (int)d : -1;
                 }
-                took += take;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned out = __ballot_sync(0xffffffffu, off[k] < 0);
+                    const int take = took < 32 * k ? 0 : out ? __ffs(out) - 1 : 32;
+                    if (lane < take) {
+                        low = min(low, off[k]);
+                        dense = dense && off[k] == off0 + n + 32 * k + lane;
+                    }
+                    took += take;
+                }
+                n += took;
+                if (took < 128)
+                    break;
             }
-            n += took;
-            if (took < 128)
-                break;
-        }
-        low = __reduce_min_sync(0xffffffffu, low);
-        dense = __all_sync(0xffffffffu, dense);
+            low = __reduce_min_sync(0xffffffffu, low);
+            dense = __all_sync(0xffffffffu, dense);
 
-        const int sub = tid / kLanes, col = (tid % kLanes) * 8;
-        const __nv_bfloat16 *rows = src + run0 * st + col;
-        uint4 held[kHeld];
-        uint32_t m = 0;
+            uint32_t m = 0;
+            if (kTeam == 1 || n > room) {
+                const __nv_bfloat16 *p = rows;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t r = i * kRows + sub;
-            held[i] = r < n ? *reinterpret_cast<const uint4 *>(rows + r * st) : make_uint4(0, 0, 0, 0);
-        }
+                for (int i = 0; i < kHeld; ++i, p += step)
+                    held[i] = i * kRows + sub < n ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+            } else if (n < room) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            m = amax8<false>(m, held[i]);
-        for (int64_t r = kHeld * kRows + sub; r < n; r += kRows)
-            m = amax8<false>(m, *reinterpret_cast<const uint4 *>(rows + r * st));
-        float amax = team_max(m);
-        if (isinf(amax)) { // an infinity among the rows: the largest finite value counts
-            m = 0;
-            for (int64_t r = sub; r < n; r += kRows)
-                m = amax8<true>(m, *reinterpret_cast<const uint4 *>(rows + r * st));
-            amax = team_max(m);
-        }
-        float now = amax == 0.f ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), kMinScale);
-        uint8_t *dst = cache + (((block * a.H_kv + h) << a.block_shift)) * D;
-        if (low > 0) {
-            if (now > old) {
-                for (int i = tid * 16; i < low * D; i += 512 * kTeam) {
-                    uint4 w = *reinterpret_cast<const uint4 *>(dst + i);
-                    w.x = requant4(w.x, old, now);
-                    w.y = requant4(w.y, old, now);
-                    w.z = requant4(w.z, old, now);
-                    w.w = requant4(w.w, old, now);
-                    *reinterpret_cast<uint4 *>(dst + i) = w;
+                for (int i = 0; i < kHeld; ++i)
+                    held[i] = i * kRows + sub < n ? held[i] : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                m = amax8<false>(m, held[i]);
+            for (int r = kHeld * kRows + sub; r < n; r += kRows)
+                m = amax8<false>(m, *reinterpret_cast<const uint4 *>(rows + (int64_t)(r - sub) * st));
+            float amax = team_max(m);
+            if (isinf(amax)) { // an infinity among the rows: the largest finite value counts
+                m = 0;
+                for (int r = sub; r < n; r += kRows)
+                    m = amax8<true>(m, *reinterpret_cast<const uint4 *>(rows + (int64_t)(r - sub) * st));
+                amax = team_max(m);
+            }
+            float now = amax == 0.f ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), kMinScale);
+            uint8_t *dst = cache + ((((int64_t)block * a.H_kv + h) << a.block_shift)) * D;
+            if (low > 0) {
+                if (now > old) {
+                    for (int i = tid * 16; i < low * D; i += 512 * kTeam) {
+                        uint4 w = *reinterpret_cast<const uint4 *>(dst + i);
+                        w.x = requant4(w.x, old, now);
+                        w.y = requant4(w.y, old, now);
+                        w.z = requant4(w.z, old, now);
+                        w.w = requant4(w.w, old, now);
+                        *reinterpret_cast<uint4 *>(dst + i) = w;
+                    }
+                } else {
+                    now = old;
                 }
-            } else {
-                now = old;
             }
-        }
-        // (every thread of the team has read the old scale: it passed the team's maximum, or is in the one warp)
-        __syncwarp();
-        if (tid == 0)
-            *cell = now;
-        const E4m3Recip inv = e4m3_recip(now);
+            // (every thread of the team has read the old scale: it passed the team's maximum, or is in the one warp)
+            __syncwarp();
+            if (tid == 0)
+                *cell = now;
+            const E4m3Recip inv = e4m3_recip(now);
+            dst += col;
+            if (dense) {
+                uint8_t *p = dst + (off0 + sub) * D;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int64_t r = i * kRows + sub;
-            if (r < n) {
-                const int off = dense ? off0 + (int)r : (int)(a.slot_mapping[run0 + r] & (bs - 1));
-                *reinterpret_cast<uint2 *>(dst + off * D + col) = quant8(held[i], now, inv);
+                for (int i = 0; i < kHeld; ++i)
+                    if (i * kRows + sub < n)
+                        *reinterpret_cast<uint2 *>(p + i * kRows * D) = quant8(held[i], now, inv);
+            } else {
+#pragma unroll 1
+                for (int r = sub; r < min(n, kHeld * kRows); r += kRows)
+                    *reinterpret_cast<uint2 *>(dst + (int)(run_slots[r] - first_slot) * D) =
+                        quant8(*reinterpret_cast<const uint4 *>(rows + (int64_t)(r - sub) * st), now, inv);
             }
-        }
-        for (int64_t r = kHeld * kRows + sub; r < n; r += kRows) {
-            const int off = dense ? off0 + (int)r : (int)(a.slot_mapping[run0 + r] & (bs - 1));
-            *reinterpret_cast<uint2 *>(dst + off * D + col) =
-                quant8(*reinterpret_cast<const uint4 *>(rows + r * st), now, inv);
+            for (int r = kHeld * kRows + sub; r < n; r += kRows)
+                *reinterpret_cast<uint2 *>(dst + (int)(run_slots[r] - first_slot) * D) =
+                    quant8(*reinterpret_cast<const uint4 *>(rows + (int64_t)(r - sub) * st), now, inv);
         }
     }
 }
@@ -229,7 +286,7 @@ cudaError_t launch(const Kv8AppendArgs &a, cudaStream_t stream)
 {
     const int64_t items = ((int64_t)a.T + a.window - 1) / a.window * a.H_kv * 2;
     const int64_t blocks = (items * kTeam * 32 + kThreads - 1) / kThreads;
-    if (blocks > 0x7FFFFFFF)
+    if (items > 0x7FFFFF00 || blocks > 0x7FFFFFFF)
         return cudaErrorInvalidValue;
     kv8_append_kernel<D, kTeam><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
@@ -241,13 +298,13 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs &args, int D, int sm_count, cu
 {
     Kv8AppendArgs a = args;
     // a warp to each token while that gives each SM at most 128 warps (a decode
-    // step's runs are one token long); beyond, four warps to 32 tokens, whose runs
-    // are long in a prompt
+    // step's runs are one token long); beyond, four warps to a block's worth of
+    // tokens, of which a prompt has one run or two
     if ((int64_t)a.T * a.H_kv * 2 <= (int64_t)sm_count * 128) {
         a.window = 1;
         return D == 128 ? launch<128, 1>(a, stream) : launch<64, 1>(a, stream);
     }
-    a.window = 32;
+    a.window = 1 << a.block_shift;
     return D == 128 ? launch<128, 4>(a, stream) : launch<64, 4>(a, stream);
 }
 

@@ -101,96 +101,125 @@ template <typename E, int kVec> struct alignas(sizeof(E) * kVec) Pack {
 // A unit is what one thread turns or copies of one head: with halves, kVec
 // elements of each half (kVec pairs); interleaved, kVec elements (kVec / 2
 // pairs; two for kVec = 1); or kVec plain columns. A thread keeps its unit, so
-// its cosines and sines are loaded once, and walks over the heads of q, then k.
-// threadIdx.x is the unit, threadIdx.y the first head, blockIdx.x the token.
-// Both elements of a pair are read before either is written, by the one thread
-// that has them: in-place calls are safe. Bound: bytes in and out.
-constexpr int kBatch = 4;
-template <typename E, int kVec, bool kNeox>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a)
+// its cosines and sines are loaded once, and walks over the heads of q, then k,
+// a batch (64 bytes) at a time. threadIdx.x is the unit, threadIdx.y the first
+// head, blockIdx.x and threadIdx.z the token. The first batch's elements are
+// asked for before the position is known. Both elements of a pair are read before either is written,
+// by the one thread that has them: in-place calls are safe. Bound: bytes in and
+// out.
+template <int kVec, bool kNeox> constexpr int kBatch = kNeox || kVec == 1 ? 2 : 4;
+
+// kPairs consecutive floats of a table row, by 16 bytes where they are aligned.
+template <int kPairs>
+__device__ __forceinline__ void load_angles(const float *p, float (&v)[kPairs])
 {
-    constexpr int kV = kNeox || kVec > 1 ? kVec : 2; // elements of a rotated unit (of each half with kNeox)
-    const int64_t t = blockIdx.x;
-    const int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.max_position) {
-        if (threadIdx.x == 0 && threadIdx.y == 0 && blockIdx.y == 0)
-            atomicOr(&g_rope_error, 4);
-        return;
+    if (kPairs % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+        for (int e = 0; e < kPairs / 4; ++e) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + e);
+            v[4 * e] = f.x;
+            v[(4 * e + 1) % kPairs] = f.y;
+            v[(4 * e + 2) % kPairs] = f.z;
+            v[(4 * e + 3) % kPairs] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e)
+            v[e] = __ldg(p + e);
     }
+}
+
+template <typename E, int kVec, bool kNeox>
+__global__ void __launch_bounds__(256, 4) rope_kernel(const RopeArgs a)
+{
+    using P = Pack<E, kVec>;
+    constexpr int kB = kBatch<kVec, kNeox>;
+    constexpr bool kTwo = kNeox || kVec == 1;          // a unit's pairs lie in two accesses
+    constexpr int kPairs = kTwo ? kVec : kVec / 2;
+    const int64_t t = (int64_t)blockIdx.x * blockDim.z + threadIdx.z;
+    if (t >= a.T)
+        return;
+    const int64_t pos = a.positions[t];
     const int n = a.rot_dim / 2;
-    const int turned = kNeox ? n / kV : a.rot_dim / kV;
+    const int turned = n / kPairs;
     const int units = turned + (a.D - a.rot_dim) / kVec;
-    const float *row = a.cos_sin + pos * a.rot_dim;
-    const int heads = a.H + a.H_k;
-    const int hstep = blockDim.y * gridDim.y;
+    const int h_first = blockIdx.y * blockDim.y + threadIdx.y, hstep = blockDim.y * gridDim.y;
     for (int u = threadIdx.x; u < units; u += blockDim.x) {
-        if (u >= turned) {
-            int col = (u - turned) * kVec; // plain column, the rotated ones left out
-            if (col >= a.rot_offset)
-                col += a.rot_dim;
-            for (int h = blockIdx.y * blockDim.y + threadIdx.y; h < heads; h += hstep) {
-                const bool isq = h < a.H;
-                const E *src = static_cast<const E *>(isq ? a.q : a.k) + (isq ? t * a.q_st + h * a.q_sh : t * a.k_st + (h - a.H) * a.k_sh);
-                E *dst = static_cast<E *>(isq ? a.q_out : a.k_out) + (isq ? t * a.qo_st + h * a.qo_sh : t * a.ko_st + (h - a.H) * a.ko_sh);
-                if (src != dst)
-                    *reinterpret_cast<Pack<E, kVec> *>(dst + col) = *reinterpret_cast<const Pack<E, kVec> *>(src + col);
-            }
-            continue;
+        const bool turns = u < turned;
+        // the unit's columns: c0 and, of pairs in two accesses, c0 + apart
+        const int apart = kNeox ? n : 1;
+        int c0;
+        if (!turns) {
+            c0 = (u - turned) * kVec;
+            c0 += c0 >= a.rot_offset ? a.rot_dim : 0;
+        } else {
+            c0 = a.rot_offset + u * (kNeox || !kTwo ? kVec : 2);
         }
-        constexpr int kPairs = kNeox ? kV : kV / 2;
         float c[kPairs], s[kPairs];
-        const int p0 = u * kPairs;
+        bool first = true;
+        // q's heads, then k's, as one row of heads
+        int h = h_first;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            const int count = side ? a.H_k : a.H;
+            const int64_t sh = side ? a.k_sh : a.q_sh, oh = side ? a.ko_sh : a.qo_sh;
+            const E *src = static_cast<const E *>(side ? a.k : a.q) + t * (side ? a.k_st : a.q_st) + c0 + h * sh;
+            E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * (side ? a.ko_st : a.qo_st) + c0 + h * oh;
+            const int64_t src_step = hstep * sh, dst_step = hstep * oh;
+#pragma unroll 1
+            for (; h < count; h += kB * hstep, src += kB * src_step, dst += kB * dst_step) {
+                P x[kB], y[kTwo ? kB : 1];
 #pragma unroll
-        for (int e = 0; e < kPairs; ++e) {
-            c[e] = __ldg(row + p0 + e);
-            s[e] = __ldg(row + n + p0 + e);
-            s[e] = a.inverse ? -s[e] : s[e];
-        }
-        // kBatch heads at a time: their loads are in flight together
-        for (int h0 = blockIdx.y * blockDim.y + threadIdx.y; h0 < heads; h0 += kBatch * hstep) {
-            Pack<E, kVec> x[kBatch], y[kBatch];
-            E *out[kBatch];
+                for (int i = 0; i < kB; ++i)
+                    if (h + i * hstep < count) {
+                        x[i] = *reinterpret_cast<const P *>(src + i * src_step);
+                        if (kTwo && turns)
+                            y[kTwo ? i : 0] = *reinterpret_cast<const P *>(src + i * src_step + apart);
+                    }
+                if (first) {
+                    first = false;
+                    if (pos < 0 || pos >= a.max_position) {
+                        if (threadIdx.x == 0 && threadIdx.y == 0 && blockIdx.y == 0)
+                            atomicOr(&g_rope_error, 4);
+                        return;
+                    }
+                    if (turns) {
+                        const float *row = a.cos_sin + pos * a.rot_dim + u * kPairs;
+                        load_angles<kPairs>(row, c);
+                        load_angles<kPairs>(row + n, s);
+                        if (a.inverse)
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int h = h0 + k * hstep;
-                if (h < heads) {
-                    const bool isq = h < a.H;
-                    const E *src = static_cast<const E *>(isq ? a.q : a.k) + (isq ? t * a.q_st + h * a.q_sh : t * a.k_st + (h - a.H) * a.k_sh) + a.rot_offset;
-                    out[k] = static_cast<E *>(isq ? a.q_out : a.k_out) + (isq ? t * a.qo_st + h * a.qo_sh : t * a.ko_st + (h - a.H) * a.ko_sh) + a.rot_offset;
-                    if (kNeox) {
-                        x[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + p0);
-                        y[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + n + p0);
-                    } else {
-                        x[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + 2 * p0);
-                        if (kVec == 1)
-                            y[k] = *reinterpret_cast<const Pack<E, kVec> *>(src + 2 * p0 + 1);
+                            for (int e = 0; e < kPairs; ++e)
+                                s[e] = -s[e];
                     }
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (h0 + k * hstep >= heads)
-                    break;
-                E *dst = out[k];
-                Pack<E, kVec> xo, yo;
-                if (kNeox || kVec == 1) {
+                for (int i = 0; i < kB; ++i) {
+                    if (h + i * hstep >= count)
+                        break;
+                    if (turns && kTwo) {
+                        P yo;
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        xo.e[e] = from_f<E>(rot_a(to_f(x[k].e[e]), to_f(y[k].e[e]), c[e % kPairs], s[e % kPairs]));
-                        yo.e[e] = from_f<E>(rot_b(to_f(x[k].e[e]), to_f(y[k].e[e]), c[e % kPairs], s[e % kPairs]));
+                        for (int e = 0; e < kVec; ++e) {
+                            const float xa = to_f(x[i].e[e]), xb = to_f(y[kTwo ? i : 0].e[e]);
+                            x[i].e[e] = from_f<E>(rot_a(xa, xb, c[e % kPairs], s[e % kPairs]));
+                            yo.e[e] = from_f<E>(rot_b(xa, xb, c[e % kPairs], s[e % kPairs]));
+                        }
+                        *reinterpret_cast<P *>(dst + i * dst_step + apart) = yo;
+                    } else if (turns) {
+#pragma unroll
+                        for (int e = 0; e < kPairs; ++e) {
+                            const float xa = to_f(x[i].e[(2 * e) % kVec]), xb = to_f(x[i].e[(2 * e + 1) % kVec]);
+                            x[i].e[(2 * e) % kVec] = from_f<E>(rot_a(xa, xb, c[e], s[e]));
+                            x[i].e[(2 * e + 1) % kVec] = from_f<E>(rot_b(xa, xb, c[e], s[e]));
+                        }
                     }
-                    *reinterpret_cast<Pack<E, kVec> *>(dst + (kNeox ? p0 : 2 * p0)) = xo;
-                    *reinterpret_cast<Pack<E, kVec> *>(dst + (kNeox ? n + p0 : 2 * p0 + 1)) = yo;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kPairs; ++e) {
-                        const float xa = to_f(x[k].e[(2 * e) % kVec]), xb = to_f(x[k].e[(2 * e + 1) % kVec]);
-                        xo.e[(2 * e) % kVec] = from_f<E>(rot_a(xa, xb, c[e], s[e]));
-                        xo.e[(2 * e + 1) % kVec] = from_f<E>(rot_b(xa, xb, c[e], s[e]));
-                    }
-                    *reinterpret_cast<Pack<E, kVec> *>(dst + 2 * p0) = xo;
+                    *reinterpret_cast<P *>(dst + i * dst_step) = x[i];
                 }
             }
+            // the next side's first head of this thread: the batches above pass heads beyond the end
+            if (side == 0)
+                h = h_first >= a.H ? h_first - a.H : (hstep - (a.H - h_first) % hstep) % hstep;
         }
     }
 }
@@ -198,20 +227,22 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a)
 template <typename E, int kVec>
 cudaError_t launch_vec(const RopeArgs &a, int sm_count, cudaStream_t stream)
 {
-    const int n = a.rot_dim / 2;
-    const int kV = a.neox || kVec > 1 ? kVec : 2;
-    const int units = (a.neox ? n : a.rot_dim) / kV + (a.D - a.rot_dim) / kVec;
+    const int batch = a.neox || kVec == 1 ? 2 : 4;
+    const int units = a.rot_dim / 2 / (a.neox || kVec == 1 ? kVec : kVec / 2) + (a.D - a.rot_dim) / kVec;
     const int x = std::min(units, 256);
     const int heads = a.H + a.H_k;
-    // a thread's batches should come out even: 40 heads over 16 threads' rows would leave the last half idle
-    int y = std::max(1, std::min(128 / x, heads));
-    const int64_t rounds = (heads + (int64_t)y * kBatch - 1) / ((int64_t)y * kBatch);
-    if (rounds == 1)
-        y = std::max(1, std::min(y, (heads + kBatch - 1) / kBatch));
-    // few tokens: their heads are spread over blocks until the SMs have two each
-    int64_t groups = (heads + y - 1) / y;
-    groups = std::min<int64_t>(groups, std::max<int64_t>(1, (int64_t)2 * sm_count / a.T));
-    const dim3 grid((unsigned)a.T, (unsigned)std::min<int64_t>(groups, 65535)), block(x, y);
+    // Many tokens: three batches of heads to a thread, so that the positions' and angles' latency is paid once for
+    // them, and as many tokens as fill a block. Few tokens: their heads are spread over threads and blocks until the
+    // SMs have eight blocks each.
+    int y = std::max(1, std::min(256 / x, (heads + 3 * batch - 1) / (3 * batch)));
+    int z = std::min(64, 256 / (x * y));
+    int64_t groups = 1;
+    if ((int64_t)a.T * x * y < (int64_t)sm_count * 2048) {
+        z = 1;
+        y = std::max(1, std::min(std::min(128 / x, 64), (heads + batch - 1) / batch));
+        groups = std::min<int64_t>((heads + y - 1) / y, std::max<int64_t>(1, (int64_t)8 * sm_count / a.T));
+    }
+    const dim3 grid((unsigned)((a.T + z - 1) / z), (unsigned)std::min<int64_t>(groups, 65535)), block(x, y, z);
     if (a.neox)
         rope_kernel<E, kVec, true><<<grid, block, 0, stream>>>(a);
     else

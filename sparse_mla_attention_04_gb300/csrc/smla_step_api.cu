@@ -255,10 +255,9 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
                                      int H_kv, int D, int block_size, void *k_cache, void *v_cache, float *k_scale,
                                      float *v_scale, int64_t num_blocks, smla_stream_t stream)
 {
-    if (T < 0 || H_kv <= 0 || num_blocks < 0 || k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0 ||
-        num_blocks > INT64_MAX / 128)
+    if (T < 0 || H_kv <= 0 || num_blocks < 0 || k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0)
         return SMLA_ERR_BAD_SHAPE;
-    if ((D != 64 && D != 128) || block_shift(block_size) < 0)
+    if ((D != 64 && D != 128) || block_shift(block_size) < 0 || num_blocks > INT_MAX || H_kv > INT_MAX / 2)
         return SMLA_ERR_UNSUPPORTED;
     if (T == 0)
         return SMLA_OK;

@@ -11,6 +11,7 @@
 // the table's writer does.
 #include "smla_device.cuh"
 #include "smla_internal.h"
+#include "smla_umma.cuh"
 
 #include <climits>
 
@@ -82,24 +83,25 @@ __device__ __forceinline__ Request request(const TablesArgs &a, int b)
 
 __device__ __forceinline__ int clamp31(long long v) { return (int)min(v, (long long)INT_MAX); }
 
-__device__ __forceinline__ int ring_at(const TablesArgs &a, int head, long long i)
+// Places of the ring, i and head below 2^31 (32-bit remainders: 64-bit ones took most of a step's time).
+__device__ __forceinline__ unsigned ring_place(const TablesArgs &a, unsigned head, unsigned i)
 {
-    return a.free_ring[(head + i) % a.ring_size];
+    return (head + i) % (unsigned)a.ring_size;
 }
+__device__ __forceinline__ int ring_at(const TablesArgs &a, int head, int i) { return a.free_ring[ring_place(a, head, i)]; }
 
-// One token's position, slot and request. plan[b] = {first taken block of the
+// One token's position and slot. p: the request's plan {first taken block of the
 // batch, held blocks, blocks after the call, length}.
-__device__ __forceinline__ void fill_token(const TablesArgs &a, int64_t t, int b, int start, int4 p, int q, int head)
+__device__ __forceinline__ void token(const TablesArgs &a, int64_t t, int start, int4 p, int q, int head, int b, int64_t &pos,
+                                      int64_t &slot)
 {
-    const int pos = p.w - q + (int)(t - start);
-    const int j = pos >> a.block_shift;
+    const int at = p.w - q + (int)(t - start);
+    const int j = at >> a.block_shift;
     int block = -1;
     if (j < p.z)
         block = j < p.y ? a.block_table[b * a.table_stride + j] : ring_at(a, head, p.x + j - p.y);
-    a.positions[t] = pos;
-    a.slot_mapping[t] = block < 0 ? -1 : (int64_t)block * a.block_size + (pos & (a.block_size - 1));
-    if (a.token_request)
-        a.token_request[t] = b;
+    pos = at;
+    slot = block < 0 ? -1 : (int64_t)block * a.block_size + (at & (a.block_size - 1));
 }
 
 // The request of token t: the last b in [lo, hi] with start[b] <= t (empty
@@ -116,23 +118,25 @@ __device__ __forceinline__ int find_request(const int32_t *start, int lo, int hi
     return lo;
 }
 
-// Table entries and the ring's end: a warp to a request. `give` is the first
-// given-back block's place behind the ring's end.
+// Table entries and the ring's end: a warp to a request, four entries of a lane
+// in flight. `give` is the first given-back block's place behind the ring's end.
 __device__ __forceinline__ void fill_blocks(const TablesArgs &a, int b, int4 p, int give, int head, int count, int lane)
 {
     int32_t *row = a.block_table + b * a.table_stride;
+#pragma unroll 4
     for (int j = p.y + lane; j < p.z; j += 32)
         row[j] = ring_at(a, head, p.x + j - p.y);
-    for (int j = p.z + lane; j < p.y; j += 32)
-        a.free_ring[((long long)head + count + give + j - p.z) % a.ring_size] = row[j];
-}
-
-__device__ __forceinline__ void pad_token(const TablesArgs &a, int64_t t)
-{
-    a.positions[t] = 0;
-    a.slot_mapping[t] = -1;
-    if (a.token_request)
-        a.token_request[t] = -1;
+    const unsigned end = ring_place(a, head, count);
+    for (int j = p.z + lane; j < p.y; j += 128) {
+        int v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[k] = j + 32 * k < p.y ? row[j + 32 * k] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + 32 * k < p.y)
+                a.free_ring[ring_place(a, end, give + j + 32 * k - p.z)] = v[k];
+    }
 }
 
 __device__ __forceinline__ int2 ring_state(const TablesArgs &a)
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) tables_small_kernel(const TablesArgs
     __shared__ int4 s_plan[kThreads];
     __shared__ int s_start[kThreads + 1], s_give[kThreads];
     __shared__ int s_wide;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int2 ring = ring_state(a);
     const int head = ring.x, count = ring.y;
     Request r{0, 0, 0, 0};
@@ -194,14 +198,41 @@ __global__ void __launch_bounds__(kThreads) tables_small_kernel(const TablesArgs
     for (int64_t t = tid; t < a.num_tokens; t += kThreads) {
         if (t < all.q) {
             const int b = find_request(s_start, 0, a.B - 1, t);
-            fill_token(a, t, b, s_start[b], s_plan[b], s_start[b + 1] - s_start[b], head);
+            int64_t pos, slot;
+            token(a, t, s_start[b], s_plan[b], s_start[b + 1] - s_start[b], head, b, pos, slot);
+            a.positions[t] = pos;
+            a.slot_mapping[t] = slot;
+            if (a.token_request)
+                a.token_request[t] = b;
         } else {
-            pad_token(a, t);
+            a.positions[t] = 0;
+            a.slot_mapping[t] = -1;
+            if (a.token_request)
+                a.token_request[t] = -1;
         }
     }
-    if (ok && all.take + all.give > 0)
-        for (int b = warp; b < a.B; b += kThreads / 32)
-            fill_blocks(a, b, s_plan[b], s_give[b], head, count, lane);
+    if (!ok)
+        return;
+    // entries that change, one to a thread: those taken, then those given back
+    const unsigned end = ring_place(a, head, count);
+    for (int64_t i = tid; i < all.take + all.give; i += kThreads) {
+        const bool takes = i < all.take;
+        const int x = (int)(takes ? i : i - all.take);
+        int lo = 0, hi = a.B - 1; // the last request whose first entry is not behind x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((takes ? s_plan[mid].x : s_give[mid]) <= x)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int4 p = s_plan[lo];
+        int32_t *row = a.block_table + lo * a.table_stride;
+        if (takes)
+            row[p.y + x - p.x] = ring_at(a, head, x);
+        else
+            a.free_ring[ring_place(a, end, x)] = row[p.z + x - s_give[lo]];
+    }
 }
 
 // The scan alone, for any number of requests: one block, its plan to the workspace.
@@ -211,19 +242,21 @@ __global__ void __launch_bounds__(kThreads) tables_scan_kernel(const TablesArgs 
     const int tid = threadIdx.x;
     const int2 ring = ring_state(a);
     const int head = ring.x, count = ring.y;
-    Sums all{0, 0, 0};
+    umma::grid_launch_dependents();
+    Sums all{0, 0, 0}, mine{0, 0, 0}; // (with one round, the second pass has its sums from the first)
+    Request r{0, 0, 0, 0};
     long long lacking = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         Sums v{0, 0, 0};
         int wide = 0;
         if (b < a.B) {
-            const Request r = request(a, b);
+            r = request(a, b);
             v = {r.q, max(r.need - r.held, 0), max(r.held - r.need, 0)};
             wide = max(r.need - a.table_width, 0);
         }
         Sums total;
-        (void)block_exclusive(v, &total, warp_sums);
+        mine = block_exclusive(v, &total, warp_sums);
         all = add(all, total);
         if (__syncthreads_or(wide)) {
             (void)block_exclusive(Sums{wide, 0, 0}, &total, warp_sums);
@@ -235,14 +268,16 @@ __global__ void __launch_bounds__(kThreads) tables_scan_kernel(const TablesArgs 
     Sums carry{0, 0, 0};
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
-        Sums v{0, 0, 0};
-        Request r{0, 0, 0, 0};
-        if (b < a.B) {
-            r = request(a, b);
-            v = {r.q, max(r.need - r.held, 0), max(r.held - r.need, 0)};
+        Sums x = mine;
+        if (a.B > kThreads) {
+            Sums v{0, 0, 0}, total;
+            if (b < a.B) {
+                r = request(a, b);
+                v = {r.q, max(r.need - r.held, 0), max(r.held - r.need, 0)};
+            }
+            x = add(carry, block_exclusive(v, &total, warp_sums));
+            carry = add(carry, total);
         }
-        Sums total;
-        const Sums x = add(carry, block_exclusive(v, &total, warp_sums));
         if (b < a.B) {
             const int after = ok ? r.need : r.held;
             a.query_start[b] = clamp31(x.q);
@@ -250,7 +285,6 @@ __global__ void __launch_bounds__(kThreads) tables_scan_kernel(const TablesArgs 
             a.give_start[b] = clamp31(x.give);
             a.blocks_held_out[b] = after;
         }
-        carry = add(carry, total);
     }
     if (tid == 0) {
         a.state[0] = head;
@@ -266,6 +300,7 @@ template <bool kShared>
 __global__ void __launch_bounds__(256) tables_fill_kernel(const TablesArgs a)
 {
     __shared__ int s_start[kShared ? kSharedStarts + 1 : 1];
+    umma::grid_wait(); // the scan is done
     const int32_t *start_of = a.query_start;
     if (kShared) {
         for (int i = threadIdx.x; i <= a.B; i += blockDim.x)
@@ -285,16 +320,29 @@ __global__ void __launch_bounds__(256) tables_fill_kernel(const TablesArgs a)
             lo = find_request(start_of, 0, a.B - 1, t0);
             hi = find_request(start_of, lo, a.B - 1, min(t0 + 63, total - 1));
         }
+        // both of a lane's tokens' loads are in flight before either is written
+        int64_t pos[2], slot[2];
+        int req[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int64_t t = t0 + k * 32 + lane;
-            if (t >= a.num_tokens)
-                break;
-            if (t < total) {
-                const int b = find_request(start_of, lo, hi, t);
-                fill_token(a, t, b, start_of[b], a.plan[b], start_of[b + 1] - start_of[b], head);
-            } else {
-                pad_token(a, t);
+            pos[k] = 0;
+            slot[k] = -1;
+            req[k] = -1;
+            if (t < total && t < a.num_tokens) {
+                req[k] = find_request(start_of, lo, hi, t);
+                token(a, t, start_of[req[k]], a.plan[req[k]], start_of[req[k] + 1] - start_of[req[k]], head, req[k], pos[k],
+                      slot[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t t = t0 + k * 32 + lane;
+            if (t < a.num_tokens) {
+                a.positions[t] = pos[k];
+                a.slot_mapping[t] = slot[k];
+                if (a.token_request)
+                    a.token_request[t] = req[k];
             }
         }
     }
@@ -317,12 +365,17 @@ cudaError_t launch_block_tables(const TablesArgs &a, int sm_count, cudaStream_t 
         return e;
     const int64_t blocks = (a.num_tokens / 64 + 7) / 8 + 1;
     const int64_t most = (int64_t)(sm_count > 0 ? sm_count : 1) * 8;
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-    if (a.B <= kSharedStarts)
-        tables_fill_kernel<true><<<grid, 256, 0, stream>>>(a);
-    else
-        tables_fill_kernel<false><<<grid, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    // behind the scan, its start overlapped
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, a.B <= kSharedStarts ? tables_fill_kernel<true> : tables_fill_kernel<false>, a);
 }
 
 } // namespace smla
