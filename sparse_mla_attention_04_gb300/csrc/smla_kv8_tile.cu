@@ -51,7 +51,9 @@ constexpr int kTile = 64;
 constexpr int kSoftmaxThreads = 128, kVThreads = 64;
 constexpr int kThreads = 256;
 constexpr float kSlack = 15.0f;
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 16; // of an item's positions
+constexpr int kWaves = 2;      // an item is split where it is more than this part of a CTA slot's share
+constexpr int kMinSplit = 16;  // tiles of a split, at least
 
 template <int D> struct Shape {
     static constexpr int kQBytes = kRows * D;       // one part of Q
@@ -74,10 +76,16 @@ template <int D> struct Shape {
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
-struct Part {
-    float2 *ml; // [items][splits][128]
-    float *o;   // [items][splits][128][D]
-    int splits;
+// The plan of a call, in the workspace: how many entries and how many split items
+// there are; the entries {item, split | splits << 16, first partial}, the longest
+// first; the split items {item, splits, first partial}; their partial sums.
+struct Plan {
+    int *header;
+    int4 *entries;
+    int4 *splits;
+    float2 *ml; // [partials][H_kv][128]
+    float *o;   // [partials][H_kv][128][D]
+    int n_items;
 };
 
 // A tile's item: request, chunk of rows, kv head.
@@ -103,6 +111,129 @@ __device__ __forceinline__ bool find_item(const Kv8AttnArgs &a, int n, Item *it)
     it->b = lo;
     it->chunk = n - ((int)((long long)r.q0 * a.G / kRows) + lo);
     return it->chunk >= 0 && (long long)it->chunk * kRows < (long long)r.qlen * a.G;
+}
+
+// What an item's rows see.
+struct Span {
+    int row0, rows, p_first, p_last;
+    int kv_begin, kv_end; // beyond: seen by none
+    int all_from;         // [all_from, p_first]: seen by all
+    int tb0, tiles;       // tiles of kTile positions from tb0 on (a multiple of kTile: blocks lie whole in the tiles)
+};
+
+__device__ __forceinline__ Span span_of(const Kv8AttnArgs &a, const Request &rq, int chunk)
+{
+    Span s;
+    s.row0 = chunk * kRows;
+    s.rows = min(kRows, rq.qlen * a.G - s.row0);
+    s.p_first = rq.pos(s.row0 / a.G);
+    s.p_last = rq.pos((s.row0 + s.rows - 1) / a.G);
+    s.kv_end = min(rq.len, s.p_last + 1);
+    s.kv_begin = a.window > 0 ? max(0, s.p_first - a.window + 1) : 0;
+    s.all_from = a.window > 0 ? s.p_last - a.window + 1 : 0;
+    s.tb0 = s.kv_begin & ~(kTile - 1);
+    s.tiles = s.kv_end > s.tb0 ? (s.kv_end - s.tb0 + kTile - 1) / kTile : 0;
+    return s;
+}
+
+// Plans a call, by one block: items that are longer than their part of a CTA
+// slot's share are split, and the entries are sorted by length (64 classes), so
+// that ragged requests fill the GPU evenly whatever their order. Where an entry
+// or a partial stands does not change what is computed from it. The first
+// kPlanned items of a thread stay in registers.
+constexpr int kPlanThreads = 1024, kPlanned = 4;
+__global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8AttnArgs a, const Plan plan, int slots)
+{
+    __shared__ long long s_total;
+    __shared__ int s_most, s_hist[64], s_parts, s_split_items;
+    grid_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) {
+        s_total = 0;
+        s_most = 0;
+        s_parts = 0;
+        s_split_items = 0;
+    }
+    if (tid < 64)
+        s_hist[tid] = 0;
+    __syncthreads();
+    auto tiles_of = [&](int n) { // -1: no such item
+        Item it;
+        return find_item(a, n, &it) ? span_of(a, request(a, it.b), it.chunk).tiles : -1;
+    };
+    int kept[kPlanned];
+    long long sum = 0;
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanned; ++i) {
+        const int n = tid + i * kPlanThreads;
+        kept[i] = n < plan.n_items ? tiles_of(n) : -1;
+        sum += max(kept[i], 0);
+        most = max(most, kept[i]);
+    }
+    for (int n = tid + kPlanned * kPlanThreads; n < plan.n_items; n += kPlanThreads) {
+        const int tiles = tiles_of(n);
+        sum += max(tiles, 0);
+        most = max(most, tiles);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        atomicAdd(reinterpret_cast<unsigned long long *>(&s_total), (unsigned long long)sum);
+        atomicMax(&s_most, most);
+    }
+    __syncthreads();
+    const int target = (int)max((long long)kMinSplit, (s_total * a.H_kv + (long long)kWaves * slots - 1) / ((long long)kWaves * slots));
+    const int longest = max(1, min(s_most, target));
+    auto splits = [&](int tiles) { return min(kMaxSplits, max(1, (tiles + target - 1) / target)); };
+    auto bucket = [&](int tiles) { return 63 - min(63, (int)((long long)(tiles / splits(tiles)) * 63 / longest)); };
+    auto count = [&](int tiles) {
+        if (tiles >= 0)
+            atomicAdd(&s_hist[bucket(tiles)], splits(tiles));
+    };
+#pragma unroll
+    for (int i = 0; i < kPlanned; ++i)
+        count(kept[i]);
+    for (int n = tid + kPlanned * kPlanThreads; n < plan.n_items; n += kPlanThreads)
+        count(tiles_of(n));
+    __syncthreads();
+    if (tid < 32) { // the classes' first places
+        const int x0 = s_hist[2 * lane], x1 = s_hist[2 * lane + 1];
+        int to = x0 + x1;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, to, d);
+            to += lane >= d ? y : 0;
+        }
+        s_hist[2 * lane] = to - x0 - x1;
+        s_hist[2 * lane + 1] = to - x1;
+        if (lane == 31)
+            plan.header[0] = to;
+    }
+    __syncthreads();
+    auto place = [&](int n, int tiles) {
+        if (tiles < 0)
+            return;
+        const int ns = splits(tiles);
+        const int at = atomicAdd(&s_hist[bucket(tiles)], ns);
+        int first = 0;
+        if (ns > 1) {
+            first = atomicAdd(&s_parts, ns);
+            plan.splits[atomicAdd(&s_split_items, 1)] = make_int4(n, ns, first, 0);
+        }
+        for (int i = 0; i < ns; ++i)
+            plan.entries[at + i] = make_int4(n, i | ns << 16, first, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kPlanned; ++i)
+        place(tid + i * kPlanThreads, kept[i]);
+    for (int n = tid + kPlanned * kPlanThreads; n < plan.n_items; n += kPlanThreads)
+        place(n, tiles_of(n));
+    __syncthreads();
+    if (tid == 0)
+        plan.header[1] = s_split_items;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
@@ -308,7 +439,7 @@ __device__ __noinline__ uint32_t nan_columns(const Kv8AttnArgs &a, const Item &i
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                const __grid_constant__ CUtensorMap v_map,
-                                                               const Kv8AttnArgs a, const Part part)
+                                                               const Kv8AttnArgs a, const Plan plan)
 {
     using S = Shape<D>;
     extern __shared__ __align__(1024) uint8_t smem[]; // (the swizzle goes by address)
@@ -327,24 +458,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                    p_full = bars + 112, v_full = bars + 128, v_empty = bars + 144, sc_full = bars + 160, drained = bars + 224;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
-    // the longest rows first: a causal prompt's last chunks
+    grid_wait(); // the plan
     Item it;
-    const int n_item = (int)((gridDim.x - 1 - blockIdx.x) / a.H_kv);
-    it.h = (int)((gridDim.x - 1 - blockIdx.x) % a.H_kv);
-    if (!find_item(a, n_item, &it))
+    const int n_entry = (int)(blockIdx.x / a.H_kv);
+    const int4 entry = plan.entries[n_entry]; // (inside the workspace, whatever it holds)
+    if (n_entry >= plan.header[0])
         return;
+    const int split = entry.y & 0xFFFF, splits = entry.y >> 16;
+    if (!find_item(a, entry.x, &it))
+        return;
+    it.h = (int)(blockIdx.x % a.H_kv);
+    const int64_t slot0 = ((int64_t)(entry.z + split) * a.H_kv + it.h) * kRows; // (of a split item)
     const Request rq = request(a, it.b);
-    const int row0 = it.chunk * kRows;
-    const int rows = min(kRows, rq.qlen * a.G - row0);
-    const int p_first = rq.pos(row0 / a.G), p_last = rq.pos((row0 + rows - 1) / a.G);
-    const int kv_end = min(rq.len, p_last + 1);                                       // beyond: seen by none
-    const int kv_begin = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
-    const int all_from = a.window > 0 ? p_last - a.window + 1 : 0;                    // [all_from, p_first]: seen by all
-    const int tb0 = kv_begin & ~(kTile - 1); // so that the blocks lie whole in the tiles
-    const int tiles_all = kv_end > tb0 ? (kv_end - tb0 + kTile - 1) / kTile : 0;
-    const int split = blockIdx.y;
-    const int t_begin = (int)((long long)tiles_all * split / part.splits);
-    const int t_end = (int)((long long)tiles_all * (split + 1) / part.splits);
+    const Span sp = span_of(a, rq, it.chunk);
+    const int row0 = sp.row0, rows = sp.rows, p_first = sp.p_first, p_last = sp.p_last, kv_begin = sp.kv_begin,
+              kv_end = sp.kv_end, all_from = sp.all_from, tb0 = sp.tb0;
+    const int t_begin = (int)((long long)sp.tiles * split / splits);
+    const int t_end = (int)((long long)sp.tiles * (split + 1) / splits);
     const int n = t_end - t_begin;
     const bool many = p_first != p_last;
 
@@ -352,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         if (tid < rows) {
             const int64_t t = rq.q0 + (row0 + tid) / a.G;
             const int head = it.h * a.G + (row0 + tid) % a.G;
-            if (part.splits > 1) {
-                part.ml[(((int64_t)n_item * a.H_kv + it.h) * part.splits + split) * kRows + tid] = make_float2(-INFINITY, 0.f);
+            if (splits > 1) {
+                plan.ml[slot0 + tid] = make_float2(-INFINITY, 0.f);
             } else {
                 float lse;
                 finish_row(-INFINITY, 0.f, a.sinks, head, &lse);
@@ -467,10 +597,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             const int rr = row0 + (live ? r : 0);
             const int64_t t = rq.q0 + rr / a.G;
             const int head = it.h * a.G + rr % a.G;
-            const int64_t slot = (((int64_t)n_item * a.H_kv + it.h) * part.splits + split) * kRows + r;
+            const int64_t slot = slot0 + r;
             const bool nans = many && *s_any_nan;
             float lse = 0.f, f = 1.f;
-            if (part.splits == 1)
+            if (splits == 1)
                 f = finish_row(m, l, a.sinks, head, &lse);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -485,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 }
                 if (!live)
                     continue;
-                if (part.splits == 1) {
+                if (splits == 1) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + c * 32);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -496,15 +626,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                         dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(part.o + slot * D + c * 32);
+                    uint4 *dst = reinterpret_cast<uint4 *>(plan.o + slot * D + c * 32);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                 }
             }
             if (live) {
-                if (part.splits > 1)
-                    part.ml[slot] = make_float2(m, l);
+                if (splits > 1)
+                    plan.ml[slot] = make_float2(m, l);
                 else if (a.lse)
                     a.lse[t * a.H + head] = lse;
             }
@@ -674,40 +804,42 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         dealloc(tmem, S::kTmem);
 }
 
-// Joins the splits of each item's rows, a warp to a row.
+// Joins the splits of the split items' rows, a warp to a row; the blocks share
+// out quarters of the items.
 template <int D>
-__global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a, const Part part)
+__global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a, const Plan plan)
 {
     constexpr int kD = D / 32;
+    grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Item it;
-    const int n_item = (int)(blockIdx.x / a.H_kv);
-    it.h = (int)(blockIdx.x % a.H_kv);
-    if (!find_item(a, n_item, &it))
-        return;
-    const Request rq = request(a, it.b);
-    const int row0 = it.chunk * kRows;
-    const int rows = min(kRows, rq.qlen * a.G - row0);
-    const int64_t slot0 = ((int64_t)n_item * a.H_kv + it.h) * part.splits * kRows;
-    for (int r = warp + 8 * blockIdx.y; r < rows; r += 8 * gridDim.y) {
-        float2 ml[kMaxSplits];
-        float m = -INFINITY, l = 0.f;
+    const long long work = (long long)plan.header[1] * a.H_kv * 4;
+    for (long long x = blockIdx.x; x < work; x += gridDim.x) {
+        const int4 info = plan.splits[x / 4 / a.H_kv];
+        Item it;
+        if (!find_item(a, info.x, &it))
+            continue;
+        it.h = (int)(x / 4 % a.H_kv);
+        const int splits = info.y;
+        const Request rq = request(a, it.b);
+        const int row0 = it.chunk * kRows;
+        const int rows = min(kRows, rq.qlen * a.G - row0);
+        for (int r = warp + 8 * (int)(x & 3); r < rows; r += 32) {
+            auto slot = [&](int s) { return ((int64_t)(info.z + s) * a.H_kv + it.h) * kRows + r; };
+            const float2 mine = lane < splits ? plan.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+            const float m = warp_max(mine.x);
+            const float f_mine = mine.x == -INFINITY ? 1.f : ex2_approx(mine.x - m);
+            float acc[kD], l = 0.f;
 #pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-            if (s < part.splits) {
-                ml[s] = part.ml[slot0 + s * kRows + r];
-                m = fmaxf(m, ml[s].x);
-            }
-        float acc[kD];
-#pragma unroll
-        for (int i = 0; i < kD; ++i)
-            acc[i] = 0.f;
-#pragma unroll
-        for (int s = 0; s < kMaxSplits; ++s)
-            if (s < part.splits && !(ml[s].x == -INFINITY && ml[s].y == 0.f)) { // nothing seen: no sums were written
-                const float f = ml[s].x == -INFINITY ? 1.f : ex2_approx(ml[s].x - m);
-                l += ml[s].y * f;
-                const float *src = part.o + (slot0 + s * kRows + r) * D + lane * kD;
+            for (int i = 0; i < kD; ++i)
+                acc[i] = 0.f;
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s) {
+                const float sm = __shfl_sync(0xffffffffu, mine.x, s), sl = __shfl_sync(0xffffffffu, mine.y, s),
+                            f = __shfl_sync(0xffffffffu, f_mine, s);
+                if (sm == -INFINITY && sl == 0.f) // nothing seen: no sums were written
+                    continue;
+                l += sl * f;
+                const float *src = plan.o + slot(s) * D + lane * kD;
 #pragma unroll
                 for (int i = 0; i < kD; i += 2) {
                     const float2 v = *reinterpret_cast<const float2 *>(src + i);
@@ -715,62 +847,92 @@ __global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a,
                     acc[i + 1] += v.y * f;
                 }
             }
-        const int64_t t = rq.q0 + (row0 + r) / a.G;
-        const int head = it.h * a.G + (row0 + r) % a.G;
-        float lse;
-        const float f = finish_row(m, l, a.sinks, head, &lse);
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
+            const int64_t t = rq.q0 + (row0 + r) / a.G;
+            const int head = it.h * a.G + (row0 + r) % a.G;
+            float lse;
+            const float f = finish_row(m, l, a.sinks, head, &lse);
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
 #pragma unroll
-        for (int i = 0; i < kD; i += 2)
-            *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
-        if (a.lse && lane == 0)
-            a.lse[t * a.H + head] = lse;
+            for (int i = 0; i < kD; i += 2)
+                *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
+            if (a.lse && lane == 0)
+                a.lse[t * a.H + head] = lse;
+        }
     }
 }
 
-int64_t items_of(int B, int T, int G) { return (int64_t)T * G / kRows + B; }
-
-// Splits of a request's positions: while the items are fewer than three to
-// each CTA slot, so that ragged lengths even out.
-int splits_of(int B, int T, int H, int H_kv, int sm_count)
-{
-    const int64_t items = items_of(B, T, H / H_kv) * H_kv, slots = 2 * (int64_t)std::max(sm_count, 1);
-    return (int)std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, 3 * slots / std::max<int64_t>(items, 1)));
-}
+struct Sizes {
+    int64_t items, entries, partials; // entries and partials: for each kv head
+    size_t entries_at, splits_at, ml_at, o_at, total;
+};
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Items: each request's last chunk may be short. Entries: an item, and one more
+// for each whole part of the shares that its length holds. Split items: no more
+// than there are parts; their partials at most twice as many.
+Sizes sizes_of(int64_t B, int64_t T, int G, int H_kv, int D, int sm_count)
+{
+    Sizes z;
+    const int64_t parts = (int64_t)kWaves * 2 * std::max(sm_count, 1) / H_kv + 1;
+    z.items = T * G / kRows + B;
+    z.entries = z.items + parts;
+    z.partials = 2 * parts;
+    z.entries_at = 256;
+    z.splits_at = up256(z.entries_at + (size_t)z.entries * sizeof(int4));
+    z.ml_at = up256(z.splits_at + (size_t)parts * sizeof(int4));
+    z.o_at = up256(z.ml_at + (size_t)z.partials * H_kv * kRows * sizeof(float2));
+    z.total = z.o_at + (size_t)z.partials * H_kv * kRows * D * sizeof(float);
+    return z;
+}
+
+// A launch behind the last one, its start overlapped (the kernel waits for the last one's end itself).
+template <typename... Args, typename... Given>
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, const Given &...given)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, given...);
+}
 
 template <int D>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
-    const int64_t items = items_of(a.B, a.T, a.G) * a.H_kv;
-    Part part;
-    part.splits = splits_of(a.B, a.T, a.G * a.H_kv, a.H_kv, sm_count);
-    const size_t slots = (size_t)items * part.splits * kRows;
-    part.ml = static_cast<float2 *>(workspace);
-    part.o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256(slots * sizeof(float2)));
+    const Sizes z = sizes_of(a.B, a.T, a.G, a.H_kv, D, sm_count);
+    if (z.entries * a.H_kv > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const Plan plan{reinterpret_cast<int *>(ws), reinterpret_cast<int4 *>(ws + z.entries_at), reinterpret_cast<int4 *>(ws + z.splits_at),
+                    reinterpret_cast<float2 *>(ws + z.ml_at), reinterpret_cast<float *>(ws + z.o_at), (int)z.items};
     cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kTile, maps))
         return cudaErrorInvalidValue;
-    kv8_tile_kernel<D><<<dim3((unsigned)items, part.splits), kThreads, Shape<D>::kSmem, stream>>>(maps[0], maps[1], a, part);
-    if ((e = cudaGetLastError()) != cudaSuccess || part.splits == 1)
+    kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, 2 * sm_count);
+    if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    kv8_tile_join_kernel<D><<<dim3((unsigned)items, 4), 256, 0, stream>>>(a, part);
-    return cudaGetLastError();
+    e = launch_behind(kv8_tile_kernel<D>, dim3((unsigned)(z.entries * a.H_kv)), kThreads, Shape<D>::kSmem, stream, maps[0], maps[1],
+                      a, plan);
+    if (e != cudaSuccess)
+        return e;
+    return launch_behind(kv8_tile_join_kernel<D>, dim3((unsigned)(4 * sm_count)), 256, 0, stream, a, plan);
 }
 
 } // namespace
 
 size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int sm_count)
 {
-    const int splits = splits_of(B, T, H, H_kv, sm_count);
-    if (splits == 1)
-        return 256;
-    const size_t slots = (size_t)items_of(B, T, H / H_kv) * H_kv * splits * kRows;
-    return up256(slots * sizeof(float2)) + slots * D * sizeof(float);
+    return sizes_of(B, T, H / H_kv, H_kv, D, sm_count).total;
 }
 
 cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, void *workspace, int sm_count, cudaStream_t stream)
