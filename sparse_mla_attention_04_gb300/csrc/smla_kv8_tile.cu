@@ -78,7 +78,7 @@ template <int D> struct Shape {
 
 // The plan of a call, in the workspace: how many entries and how many split items
 // there are; the entries {item, split | splits << 16, first partial}, the longest
-// first; the split items {item, splits, first partial}; their partial sums.
+// first; the split items {request, chunk, splits, first partial}; their partial sums.
 struct Plan {
     int *header;
     int4 *entries;
@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8At
         int first = 0;
         if (ns > 1) {
             first = atomicAdd(&s_parts, ns);
-            plan.splits[atomicAdd(&s_split_items, 1)] = make_int4(n, ns, first, 0);
+            Item it;
+            (void)find_item(a, n, &it);
+            plan.splits[atomicAdd(&s_split_items, 1)] = make_int4(it.b, it.chunk, ns, first);
         }
         for (int i = 0; i < ns; ++i)
             plan.entries[at + i] = make_int4(n, i | ns << 16, first, 0);
@@ -239,6 +241,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8At
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
@@ -290,10 +299,9 @@ __device__ __forceinline__ void wait_ld16(uint32_t (&x)[16])
 
 // What the rows of a tile see of 32 positions.
 struct Sight {
-    int p_first, p_last, all_from, kv_begin; // the tile's: see the kernel
-    int pos, pos_lo;                         // this row: pos_lo <= t <= pos
+    int p_first, all_from; // the tile's: see Span
+    int pos, pos_lo;       // this row: pos_lo <= t <= pos
     __device__ bool all(int t) const { return t + 31 <= p_first && t >= all_from; }
-    __device__ bool none(int t) const { return t > p_last || t + 31 < kv_begin; }
     __device__ bool sees(int t) const { return t <= pos && t >= pos_lo; }
 };
 
@@ -303,114 +311,109 @@ struct Row {
 };
 
 // One row's 64 scores (the thread's lane of tensor memory at my) become weights
-// 2^(s + log2(vs) - m) in binary16, over the scores they come from (a chunk's
-// columns are read before they are written); their sum, each group's divided by
-// vs, joins l. sc: the factors of the 4 groups of 16, log2 of their value
-// scales, 1 / vs. settle() is called, by the whole warp, before O is rescaled:
-// false where its wait gave up. o_cols: O's columns (0 before the first product).
+// 2^(s + log2(vs) - m) in binary16, over the scores they come from; their sum,
+// each group's divided by vs, joins l. sc: the factors of the 4 groups of 16,
+// log2 of their value scales, 1 / vs. settle() is called, by the whole warp,
+// before O is rescaled: false where its wait gave up. o_cols: O's columns (0
+// before the first product).
 template <typename Settle>
 __device__ __forceinline__ bool row_tile(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row &row, int t0,
                                          const Sight &see, Settle settle)
 {
+    uint32_t x[64];
+    ld32(my, *reinterpret_cast<uint32_t(*)[32]>(x));
+    ld32(my + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+    const float4 f = *reinterpret_cast<const float4 *>(sc), v = *reinterpret_cast<const float4 *>(sc + 4);
+    const float k[4] = {f.x * qs, f.y * qs, f.z * qs, f.w * qs}, vs[4] = {v.x, v.y, v.z, v.w};
+    const float ref = row.m == -INFINITY ? 0.f : row.m;
+    wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x));
+    wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
+    float now; // the reference that would make the tile's largest weight 1
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (fabsf(ref) <= 0x1p20f && see.all(t0) && see.all(t0 + 32)) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+            float e0, e1;
+            const float b = vs[i >> 4] - ref;
+            unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pair(k[i >> 4], k[i >> 4]), pair(b, b)), e0, e1);
+            x[i] = __float_as_uint(e0);
+            x[i + 1] = __float_as_uint(e1);
+            top[i >> 4] = max3(top[i >> 4], e0, e1);
+        }
+        top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        now = ref + top[0];
+    } else {
+        // Also beyond 2^20, where the difference is taken from the rounded logit, as the
+        // reference is: the rounding of m alone could pass any bound of the weights.
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            const float s = see.sees(t0 + i) ? fmaf(__uint_as_float(x[i]), k[i >> 4], vs[i >> 4]) : -INFINITY;
+            x[i] = __float_as_uint(s - ref);
+            top[i >> 4] = fmaxf(top[i >> 4], s);
+        }
+        now = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        top[0] = now - ref;
+    }
+    const bool raise = row.m == -INFINITY ? top[0] > -INFINITY : top[0] > kSlack;
+    if (__any_sync(0xffffffffu, raise)) {
+        // the row's sums so far and its O under the new reference
+        const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - now)) : 1.f;
+        const float d = raise ? now - ref : 0.f;
+        row.m = raise ? now : row.m;
+        row.l *= g;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+            x[i] = __float_as_uint(__uint_as_float(x[i]) - d);
+        if (o_cols > 0) {
+            if (!settle())
+                return false;
 #pragma unroll 1
-    for (int c = 0; c < kTile / 32; ++c) {
-        const int t = t0 + c * 32;
-        uint32_t p[16];
-        if (see.none(t)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                p[i] = 0;
-            st16(my + c * 16, p);
-            continue;
-        }
-        uint32_t x[32];
-        ld32(my + c * 32, x);
-        const float2 f = *reinterpret_cast<const float2 *>(sc + 2 * c), v = *reinterpret_cast<const float2 *>(sc + 4 + 2 * c),
-                     w = *reinterpret_cast<const float2 *>(sc + 8 + 2 * c);
-        const float k0 = f.x * qs, k1 = f.y * qs;
-        const float ref = row.m == -INFINITY ? 0.f : row.m;
-        wait_ld32(x);
-        float now; // the reference that would make the chunk's largest weight 1
-        float top = -INFINITY, top1 = -INFINITY;
-        if (fabsf(ref) <= 0x1p20f && see.all(t)) {
-            const float b0 = v.x - ref, b1 = v.y - ref;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float e0, e1;
-                unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), i < 16 ? pair(k0, k0) : pair(k1, k1),
-                            i < 16 ? pair(b0, b0) : pair(b1, b1)),
-                       e0, e1);
-                x[i] = __float_as_uint(e0);
-                x[i + 1] = __float_as_uint(e1);
-                if (i < 16)
-                    top = max3(top, e0, e1);
-                else
-                    top1 = max3(top1, e0, e1);
-            }
-            top = fmaxf(top, top1);
-            now = ref + top;
-        } else {
-            // Also beyond 2^20, where the difference is taken from the rounded logit, as the
-            // reference is: the rounding of m alone could pass any bound of the weights.
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float s = see.sees(t + i) ? fmaf(__uint_as_float(x[i]), i < 16 ? k0 : k1, i < 16 ? v.x : v.y) : -INFINITY;
-                x[i] = __float_as_uint(s - ref);
-                top = fmaxf(top, s);
-            }
-            now = top;
-            top -= ref;
-        }
-        const bool raise = row.m == -INFINITY ? top > -INFINITY : top > kSlack;
-        if (__any_sync(0xffffffffu, raise)) {
-            // the row's sums so far, its weights of this tile and its O under the new reference
-            const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - now)) : 1.f;
-            const float d = raise ? now - ref : 0.f;
-            row.m = raise ? now : row.m;
-            row.l *= g;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                x[i] = __float_as_uint(__uint_as_float(x[i]) - d);
-            wait_st();
-            if (c > 0) {
-                ld16(my, p);
+            for (int o = 0; o < o_cols; o += 16) {
+                uint32_t p[16];
+                ld16(my_o + o, p);
                 wait_ld16(p);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&p[i]));
-                    p[i] = pack_f16x2(h.x * g, h.y * g);
-                }
-                st16(my, p);
-            }
-            if (o_cols > 0) {
-                if (!settle())
-                    return false;
-#pragma unroll 1
-                for (int o = 0; o < o_cols; o += 16) {
-                    ld16(my_o + o, p);
-                    wait_ld16(p);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        p[i] = __float_as_uint(__uint_as_float(p[i]) * g);
-                    st16(my_o + o, p);
-                }
+                for (int i = 0; i < 16; ++i)
+                    p[i] = __float_as_uint(__uint_as_float(p[i]) * g);
+                st16(my_o + o, p);
             }
         }
-        uint64_t sum[2] = {0, 0};
+    }
+    const float4 w = *reinterpret_cast<const float4 *>(sc + 8);
+    const float iv[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float p0 = ex2_approx(__uint_as_float(x[i])), p1 = ex2_approx(__uint_as_float(x[i + 1]));
-            sum[i >> 4] = add2(sum[i >> 4], pair(p0, p1));
+    for (int c = 0; c < 4; ++c) {
+        uint32_t p[8];
+        uint64_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float p0 = ex2_approx(__uint_as_float(x[c * 16 + i])), p1 = ex2_approx(__uint_as_float(x[c * 16 + i + 1]));
+            sum = add2(sum, pair(p0, p1));
             p[i / 2] = pack_f16x2(p0, p1);
         }
-        st16(my + c * 16, p);
-        float s0, s1, s2, s3;
-        unpair(sum[0], s0, s1);
-        unpair(sum[1], s2, s3);
-        row.l = fmaf(s0 + s1, w.x, row.l);
-        row.l = fmaf(s2 + s3, w.y, row.l);
+        st8(my + c * 8, p);
+        float s0, s1;
+        unpair(sum, s0, s1);
+        row.l = fmaf(s0 + s1, iv[c], row.l);
     }
     return true;
+}
+
+// V's codes of a position in a tile that not every row sees whole: nothing where
+// no row sees it (the block holds anything there); and a NaN code that some rows
+// see and others do not must not reach the others through 0 * NaN: it is taken
+// out, and the rows that see it look for it at their end.
+__device__ __noinline__ void visible_codes(uint32_t (&w)[4], bool in, bool many, int *any_nan)
+{
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        w[y] = in ? w[y] : 0;
+        const uint32_t bad = many ? nan_bytes(w[y]) : 0;
+        if (bad) {
+            *any_nan = 1;
+            w[y] &= ~((bad >> 7) * 0xFFu);
+        }
+    }
 }
 
 // Which of the 32 value columns from 32 c on hold a NaN code at a position that
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         // ---------------------------------------------------------------- softmax
         const int r = tid;
         const int pos = r < rows ? rq.pos((row0 + r) / a.G) : -1;
-        const Sight see{p_first, p_last, all_from, kv_begin, pos, a.window > 0 ? pos - a.window + 1 : 0};
+        const Sight see{p_first, all_from, pos, a.window > 0 ? pos - a.window + 1 : 0};
         const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
         Row sums{-INFINITY, 0.f};
@@ -642,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
     } else if (warp < 6) {
         // ---------------------------------------------------------------- V
         const int row_in = (warp - 4) * (kTile / 2) + (lane & 7), piece = lane >> 3; // rows row_in + 8 k, pieces piece + 4 c
+        const int turn = D == 128 ? lane & 7 : (lane >> 1) & 3;                      // the swizzle of the lane's rows
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int stage = j & 1;
@@ -649,39 +653,22 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 break;
             const int tb = tb0 + (t_begin + j) * kTile;
             const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
-#pragma unroll 2
+            const uint32_t src = base + S::kCodes + stage * S::kTileBytes + row_in * D;
+            const uint32_t dst = base + S::kV + stage * S::kVBytes + (row_in >> 3) * S::kVAtoms + (lane & 7) * 16 + piece * 256;
+#pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
-                const int r = row_in + 8 * k;
-                const bool in = tb + r < kv_end && tb + r >= kv_begin; // else whatever the block holds there
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    const int chunk = piece + 4 * c;
-                    const uint32_t src = base + S::kCodes + stage * S::kTileBytes + r * D + (D == 128 ? chunk ^ (r & 7) : chunk ^ ((r >> 1) & 3)) * 16;
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(src));
-                    if (!clear) {
-                        // A NaN code at a position that some rows see and others do not must not
-                        // reach the others through 0 * NaN: it is taken out, and the rows that
-                        // see it look for it at their end.
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            w[y] = in ? w[y] : 0;
-                            const uint32_t bad = many ? nan_bytes(w[y]) : 0;
-                            if (bad) {
-                                *s_any_nan = 1;
-                                w[y] &= ~((bad >> 7) * 0xFFu);
-                            }
-                        }
-                    }
+                    const uint4 q = lds128(src + k * 8 * D + (((piece + 4 * c) ^ turn) << 4));
+                    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    if (!clear)
+                        visible_codes(w, tb + row_in + 8 * k < kv_end && tb + row_in + 8 * k >= kv_begin, many, s_any_nan);
                     uint32_t f[8];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         e4m3x4_to_f16x4(w[y], f[2 * y], f[2 * y + 1]);
-                    const uint32_t dst = base + S::kV + stage * S::kVBytes + (r >> 3) * S::kVAtoms + (r & 7) * 16 + chunk * 256;
-                    sts128(dst, f[0], f[1], f[2], f[3]);
-                    sts128(dst + 128, f[4], f[5], f[6], f[7]);
+                    sts128(dst + k * S::kVAtoms + c * 1024, f[0], f[1], f[2], f[3]);
+                    sts128(dst + k * S::kVAtoms + c * 1024 + 128, f[4], f[5], f[6], f[7]);
                 }
             }
             mbar_arrive(c_empty + stage * 8);
@@ -805,50 +792,49 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
 }
 
 // Joins the splits of the split items' rows, a warp to a row; the blocks share
-// out quarters of the items.
+// out the items by eight rows.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a, const Plan plan)
 {
     constexpr int kD = D / 32;
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long work = (long long)plan.header[1] * a.H_kv * 4;
-    for (long long x = blockIdx.x; x < work; x += gridDim.x) {
-        const int4 info = plan.splits[x / 4 / a.H_kv];
-        Item it;
-        if (!find_item(a, info.x, &it))
-            continue;
-        it.h = (int)(x / 4 % a.H_kv);
-        const int splits = info.y;
-        const Request rq = request(a, it.b);
-        const int row0 = it.chunk * kRows;
+    const int work = plan.header[1] * a.H_kv * 16; // (partials are fewer than 2^31 / 128)
+    for (int x = blockIdx.x; x < work; x += gridDim.x) {
+        const int4 info = plan.splits[x / 16 / a.H_kv];
+        const int splits = info.z, h = x / 16 % a.H_kv;
+        const Request rq = request(a, info.x);
+        const int row0 = info.y * kRows;
         const int rows = min(kRows, rq.qlen * a.G - row0);
-        for (int r = warp + 8 * (int)(x & 3); r < rows; r += 32) {
-            auto slot = [&](int s) { return ((int64_t)(info.z + s) * a.H_kv + it.h) * kRows + r; };
+        const int r = warp + 8 * (int)(x & 15);
+        if (r < rows) {
+            auto slot = [&](int s) { return ((int64_t)(info.w + s) * a.H_kv + h) * kRows + r; };
             const float2 mine = lane < splits ? plan.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
             const float m = warp_max(mine.x);
             const float f_mine = mine.x == -INFINITY ? 1.f : ex2_approx(mine.x - m);
+            // nothing seen: no sums were written
+            const unsigned seen = __ballot_sync(0xffffffffu, lane < splits && !(mine.x == -INFINITY && mine.y == 0.f));
             float acc[kD], l = 0.f;
 #pragma unroll
             for (int i = 0; i < kD; ++i)
                 acc[i] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
             for (int s = 0; s < splits; ++s) {
-                const float sm = __shfl_sync(0xffffffffu, mine.x, s), sl = __shfl_sync(0xffffffffu, mine.y, s),
-                            f = __shfl_sync(0xffffffffu, f_mine, s);
-                if (sm == -INFINITY && sl == 0.f) // nothing seen: no sums were written
-                    continue;
-                l += sl * f;
-                const float *src = plan.o + slot(s) * D + lane * kD;
+                float2 v[kD / 2];
+                const float2 *src = reinterpret_cast<const float2 *>(plan.o + slot(s) * D + lane * kD);
 #pragma unroll
-                for (int i = 0; i < kD; i += 2) {
-                    const float2 v = *reinterpret_cast<const float2 *>(src + i);
-                    acc[i] += v.x * f;
-                    acc[i + 1] += v.y * f;
+                for (int i = 0; i < kD / 2; ++i)
+                    v[i] = seen >> s & 1 ? src[i] : make_float2(0.f, 0.f);
+                const float sl = __shfl_sync(0xffffffffu, mine.y, s), f = __shfl_sync(0xffffffffu, f_mine, s);
+                l += sl * f;
+#pragma unroll
+                for (int i = 0; i < kD / 2; ++i) {
+                    acc[2 * i] += v[i].x * f;
+                    acc[2 * i + 1] += v[i].y * f;
                 }
             }
             const int64_t t = rq.q0 + (row0 + r) / a.G;
-            const int head = it.h * a.G + (row0 + r) % a.G;
+            const int head = h * a.G + (row0 + r) % a.G;
             float lse;
             const float f = finish_row(m, l, a.sinks, head, &lse);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
@@ -925,7 +911,7 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
                       a, plan);
     if (e != cudaSuccess)
         return e;
-    return launch_behind(kv8_tile_join_kernel<D>, dim3((unsigned)(4 * sm_count)), 256, 0, stream, a, plan);
+    return launch_behind(kv8_tile_join_kernel<D>, dim3((unsigned)(16 * sm_count)), 256, 0, stream, a, plan);
 }
 
 } // namespace
