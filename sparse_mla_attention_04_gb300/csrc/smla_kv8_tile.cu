@@ -10,7 +10,7 @@
 //   0-3  softmax, a row to a thread; the epilogue
 //   4-5  V's codes, expanded to binary16
 //   6    the blocks' codes by TMA as they lie in the cache; the blocks' scales
-//   7    one thread issues the tensor-core products
+//   7    issues the tensor-core products
 // (eight warps, so that both CTAs' threads have 128 registers). Their loops are
 // kept short, not unrolled: all run at once, and with long straight code each
 // instruction was fetched again every tile (8 to 20 cycles an instruction).
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     bool ok = true;
-    // a bounded wait, by whole warps (or by the one thread of warp 7)
+    // a bounded wait, by whole warps
     auto wait_warp = [&](uint32_t bar, uint32_t parity) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
         if (!ok && lane == 0)
@@ -734,53 +734,55 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         for (int j = max(0, v_issued - 2); j < v_issued; ++j)
             if (!mbar_wait(c_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
-    } else if (lane == 0) {
+    } else {
         // ---------------------------------------------------------------- products
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = ok && mbar_wait(bar, parity);
-            if (!ok)
-                atomicOr(&g_kv8_error, 1);
-            return ok;
-        };
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t q_hi = desc(base + S::kQ, 128, S::kQAtoms);
         const uint64_t q_lo = desc(base + S::kQ + S::kQBytes, 128, S::kQAtoms);
         const auto scores = [&](int j) {
-            if (!wait(k_full + (j & 3) * 8, (j >> 2) & 1))
+            if (!wait_warp(k_full + (j & 3) * 8, (j >> 2) & 1))
                 return false;
             fence_after_sync();
             const uint32_t k_s = base + S::kK + (j & 3) * S::kTileBytes;
             const uint64_t k_d = D == 128 ? desc_sw128(k_s, 16, 1024) : desc_sw64(k_s, 16, 512);
-            const uint32_t dst = tmem + (j & 1) * kTile;
+            const uint32_t dst = tm + (j & 1) * kTile;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) // 32 columns: two core matrices of Q, 32 bytes of a row of K
-                mma_f8(dst, q_hi + kk * 16, k_d + kk * 2, S::kIdescS, kk > 0);
+                for (int kk = 0; kk < D / 32; ++kk) // 32 columns: two core matrices of Q, 32 bytes of a row of K
+                    mma_f8(dst, q_hi + kk * 16, k_d + kk * 2, S::kIdescS, kk > 0);
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8(dst, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
-            commit(s_full + (j & 1) * 8);
-            commit(k_empty + (j & 3) * 8);
+                for (int kk = 0; kk < D / 32; ++kk)
+                    mma_f8(dst, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
+                commit(s_full + (j & 1) * 8);
+                commit(k_empty + (j & 3) * 8);
+            }
+            __syncwarp();
             return true;
         };
         bool go = scores(0) && (n == 1 || scores(1));
 #pragma unroll 1
         for (int j = 0; go && j < n; ++j) {
             const int stage = j & 1, phase = (j >> 1) & 1;
-            if (!wait(v_full + stage * 8, phase) || !wait(p_full + stage * 8, phase))
+            if (!wait_warp(v_full + stage * 8, phase) || !wait_warp(p_full + stage * 8, phase))
                 break;
             fence_after_sync();
             const uint64_t v_d = desc(base + S::kV + stage * S::kVBytes, S::kVAtoms, 128);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk) // 16 positions: 8 columns of P, two atoms of V
-                mma_f16_ts(tmem + S::kO, tmem + stage * kTile + kk * 8, v_d + (uint64_t)(kk * 2 * S::kVAtoms / 16), S::kIdescO,
-                           j > 0 || kk > 0);
-            commit(v_empty + stage * 8);
+                for (int kk = 0; kk < kTile / 16; ++kk) // 16 positions: 8 columns of P, two atoms of V
+                    mma_f16_ts(tm + S::kO, tm + stage * kTile + kk * 8, v_d + (uint64_t)(kk * 2 * S::kVAtoms / 16), S::kIdescO,
+                               j > 0 || kk > 0);
+                commit(v_empty + stage * 8);
+            }
+            __syncwarp();
             // P lies over its scores: those of two tiles on go there when its product is done
-            if (j + 2 < n && (!wait(v_empty + stage * 8, phase) || !scores(j + 2)))
+            if (j + 2 < n && (!wait_warp(v_empty + stage * 8, phase) || !scores(j + 2)))
                 break;
         }
         if (!ok) { // what was issued ends before its memory is given back
-            commit(drained);
-            if (!mbar_wait(drained, 0))
+            if (elect_one())
+                commit(drained);
+            if (!mbar_wait(drained, 0) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
         }
     }

@@ -77,6 +77,16 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
                  "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
+// True in one lane of a converged warp. With it the code around stays uniform, so
+// that descriptors are computed in uniform registers, which tcgen05 instructions
+// take; under a branch on the lane each operand is moved there first.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // Arrive once on the mbarrier at shared-memory offset `mbar` of every CTA of
 // the cluster in `cta_mask` when every tcgen05 op issued so far by this
 // thread is done.
