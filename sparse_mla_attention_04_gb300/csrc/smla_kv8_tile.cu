@@ -686,12 +686,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             const int e = t >> a.block_shift;
             return t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
         };
-        int raw = entry(0), issued = 0, v_issued = 0;
+        auto in_pool = [&](int e) { return e >= 0 && e < a.num_blocks ? e : -1; };
+        auto scale_of = [&](const float *p, int v) { return v >= 0 ? __ldg(p + (int64_t)v * a.H_kv + it.h) : 0.f; };
+        // the table is read two tiles ahead, the scales one: neither's latency is waited for
+        int v_next = in_pool(entry(0)), raw = n > 1 ? entry(1) : -1, issued = 0, v_issued = 0;
+        float ks_next = scale_of(a.k_scale, v_next), vs_next = scale_of(a.v_scale, v_next);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            const int v = raw >= 0 && raw < a.num_blocks ? raw : -1;
-            if (j + 1 < n)
-                raw = entry(j + 1);
+            const int v = v_next;
+            const float ks = ks_next, vs = vs_next;
+            if (j + 1 < n) {
+                v_next = in_pool(raw);
+                ks_next = scale_of(a.k_scale, v_next);
+                vs_next = scale_of(a.v_scale, v_next);
+                raw = j + 2 < n ? entry(j + 2) : -1;
+            }
             // lanes p and 16 + p: block p of the tile, for K and for V
             const int page = __shfl_sync(0xffffffffu, v, ((lane & 15) * rows_in >> 4) & 3);
             // a block outside the pool: rows outside the map, which fills zeros and reads nothing
@@ -708,8 +717,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             issued = j + 1;
             if (lane < 4) {
                 // a group outside the pool (or past the end): logits of -inf
-                const float ks = v >= 0 ? __ldg(a.k_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
-                const float vs = v >= 0 ? __ldg(a.v_scale + (int64_t)v * a.H_kv + it.h) : 0.f;
                 float *sc = scales + (j & 7) * 12 + lane;
                 sc[0] = ks * scale_log2;
                 sc[4] = v >= 0 ? lg2_approx(vs) : -INFINITY;
