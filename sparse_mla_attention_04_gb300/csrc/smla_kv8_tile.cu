@@ -655,12 +655,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
             const uint32_t src = base + S::kCodes + stage * S::kTileBytes + row_in * D;
             const uint32_t dst = base + S::kV + stage * S::kVBytes + (row_in >> 3) * S::kVAtoms + (lane & 7) * 16 + piece * 256;
+            uint4 q[kTile / 16][D / 64]; // all of them on their way before the first is used
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    q[k][c] = lds128(src + k * 8 * D + (((piece + 4 * c) ^ turn) << 4));
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    const uint4 q = lds128(src + k * 8 * D + (((piece + 4 * c) ^ turn) << 4));
-                    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                    uint32_t w[4] = {q[k][c].x, q[k][c].y, q[k][c].z, q[k][c].w};
                     if (!clear)
                         visible_codes(w, tb + row_in + 8 * k < kv_end && tb + row_in + 8 * k >= kv_begin, many, s_any_nan);
                     uint32_t f[8];
