@@ -686,28 +686,31 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         const int rows_in = min(kTile, a.block_size); // of a block in a tile
         const int pages = kTile / rows_in;
         float *scales = reinterpret_cast<float *>(smem + S::kScales);
-        auto entry = [&](int j) { // lane: the table entry of group lane & 3 (16 positions)
-            const int t = tb0 + (t_begin + j) * kTile + 16 * (lane & 3);
+        // Lane l looks after group l % 4 (16 positions) of tile l / 4 of eight: the table is read two eights
+        // ahead, the scales one, so that no latency is waited for (tile by tile this warp held up the rest).
+        auto entry = [&](int eight) {
+            const int t = tb0 + (t_begin + 8 * eight + (lane >> 2)) * kTile + 16 * (lane & 3);
             const int e = t >> a.block_shift;
             return t < kv_end && e < a.table_width ? __ldg(table + e) : -1;
         };
         auto in_pool = [&](int e) { return e >= 0 && e < a.num_blocks ? e : -1; };
         auto scale_of = [&](const float *p, int v) { return v >= 0 ? __ldg(p + (int64_t)v * a.H_kv + it.h) : 0.f; };
-        // the table is read two tiles ahead, the scales one: neither's latency is waited for
-        int v_next = in_pool(entry(0)), raw = n > 1 ? entry(1) : -1, issued = 0, v_issued = 0;
-        float ks_next = scale_of(a.k_scale, v_next), vs_next = scale_of(a.v_scale, v_next);
+        int v = in_pool(entry(0)), v_next = in_pool(entry(1)), raw = entry(2), issued = 0, v_issued = 0;
+        float ks = scale_of(a.k_scale, v), vs = scale_of(a.v_scale, v), ks_next = scale_of(a.k_scale, v_next),
+              vs_next = scale_of(a.v_scale, v_next);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            const int v = v_next;
-            const float ks = ks_next, vs = vs_next;
-            if (j + 1 < n) {
+            if ((j & 7) == 0 && j > 0) {
+                v = v_next;
+                ks = ks_next;
+                vs = vs_next;
                 v_next = in_pool(raw);
                 ks_next = scale_of(a.k_scale, v_next);
                 vs_next = scale_of(a.v_scale, v_next);
-                raw = j + 2 < n ? entry(j + 2) : -1;
+                raw = entry((j >> 3) + 2);
             }
             // lanes p and 16 + p: block p of the tile, for K and for V
-            const int page = __shfl_sync(0xffffffffu, v, ((lane & 15) * rows_in >> 4) & 3);
+            const int page = __shfl_sync(0xffffffffu, v, (j & 7) * 4 + (((lane & 15) * rows_in >> 4) & 3));
             // a block outside the pool: rows outside the map, which fills zeros and reads nothing
             const int y = page >= 0 ? (tb0 + (t_begin + j) * kTile) & (a.block_size - 1) : a.block_size;
             const int z = page >= 0 ? page * a.H_kv + it.h : 0;
@@ -720,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             if (lane < pages)
                 tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, k_full + (j & 3) * 8);
             issued = j + 1;
-            if (lane < 4) {
+            if (lane >> 2 == (j & 7)) {
                 // a group outside the pool (or past the end): logits of -inf
-                float *sc = scales + (j & 7) * 12 + lane;
+                float *sc = scales + (j & 7) * 12 + (lane & 3);
                 sc[0] = ks * scale_log2;
                 sc[4] = v >= 0 ? lg2_approx(vs) : -INFINITY;
                 sc[8] = v >= 0 ? __frcp_rn(vs) : 1.f;
