@@ -1,7 +1,7 @@
 // C ABI of libsparse_mla.so: argument checks on the host, the split plan, and
 // dispatch to the kernels. Declared and documented in include/sparse_mla.h.
 #include "../../include/sparse_mla.h"
-#include "smla_internal.h"
+#include "smla_step.h"
 
 #include <cuda_runtime.h>
 

@@ -2,10 +2,40 @@
 #pragma once
 
 #include "smla_device.cuh"
-#include "smla_internal.h"
+#include "smla_step.h"
+#include "smla_umma.cuh"
 
 namespace smla {
 namespace kv8 {
+
+// The 64-byte swizzled layout (CU_TENSOR_MAP_SWIZZLE_64B), K-major: rows of
+// 64 B in atoms of 8 rows (512 B), the 16-byte chunk index (0..3) XORed with
+// half the row index in the atom; SBO = distance between atoms.
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return umma::desc(saddr, lbo, sbo) | (4ull << 61);
+}
+
+// True in one lane of a converged warp. With it the code around stays uniform, so
+// that descriptors are computed in uniform registers, which tcgen05 instructions
+// take; under a branch on the lane each operand is moved there first.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// TMA tile load of the box at (x, y, z) of a 3-D tensor map into shared memory at
+// dst (in the map's swizzle), bytes counted on mbar; out-of-range parts of the box
+// are filled with zeros.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+                 "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(mbar)
+                 : "memory");
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

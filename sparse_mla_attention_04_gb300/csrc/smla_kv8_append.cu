@@ -9,7 +9,7 @@
 // passes; what is beyond is read again (from L2). Bound: 2 bytes read and 1
 // written per element.
 #include "smla_device.cuh"
-#include "smla_internal.h"
+#include "smla_step.h"
 
 #include <algorithm>
 

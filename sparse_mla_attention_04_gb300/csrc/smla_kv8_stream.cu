@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                 const int p = lane & 15;
                 const int blk = __shfl_sync(0xffffffffu, e_blk, ((tb + (p < pages ? p : 0) * rows_in) >> a.block_shift) - first);
                 if (p < pages)
-                    umma::tma_load_3d(ring + stage * L::kStageBytes + (lane >> 4) * L::kSide + p * rows_in * D,
+                    tma_load_3d(ring + stage * L::kStageBytes + (lane >> 4) * L::kSide + p * rows_in * D,
                                       lane < 16 ? &k_map : &v_map, 0, blk >= 0 ? tb & (a.block_size - 1) : a.block_size,
                                       blk >= 0 ? blk * a.H_kv + h : 0, full + 8 * stage);
             }

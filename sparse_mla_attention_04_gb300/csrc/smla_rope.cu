@@ -1,7 +1,7 @@
 // Rotary positions (sm_103a): the cos/sin table of a scaled frequency set, and
 // the rotation of part of each head.
 #include "smla_device.cuh"
-#include "smla_internal.h"
+#include "smla_step.h"
 
 #include <algorithm>
 #include <climits>

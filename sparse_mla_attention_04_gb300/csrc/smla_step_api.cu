@@ -1,7 +1,7 @@
 // C ABI of the serving-step operators (block tables, rotary, the block-scaled
 // cache's write and attention): argument checks on the host, then the launch.
 // Declared and documented in include/sparse_mla.h.
-#include "smla_internal.h"
+#include "smla_step.h"
 
 #include <climits>
 #include <cmath>

@@ -10,7 +10,7 @@
 // another within the fill: a token whose block is new takes it from the ring, as
 // the table's writer does.
 #include "smla_device.cuh"
-#include "smla_internal.h"
+#include "smla_step.h"
 #include "smla_umma.cuh"
 
 #include <climits>

@@ -36,14 +36,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
     return desc(saddr, lbo, sbo) | (2ull << 61);
 }
 
-// The 64-byte swizzled layout (CU_TENSOR_MAP_SWIZZLE_64B), K-major: rows of
-// 64 B in atoms of 8 rows (512 B), the 16-byte chunk index (0..3) XORed with
-// half the row index in the atom; SBO = distance between atoms.
-__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo)
-{
-    return desc(saddr, lbo, sbo) | (4ull << 61);
-}
-
 // Instruction descriptor: fp32 accumulate; fmt 0/1 = f16/bf16 (kind::f16) or
 // 0 = e4m3 (kind::f8f6f4); major 0 = K-major, 1 = MN-major.
 __host__ __device__ constexpr uint32_t idesc(int M, int N, int afmt, int bfmt, int amaj, int bmaj)
@@ -75,16 +67,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
     asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
                  "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-// True in one lane of a converged warp. With it the code around stays uniform, so
-// that descriptors are computed in uniform registers, which tcgen05 instructions
-// take; under a branch on the lane each operand is moved there first.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
 }
 
 // Arrive once on the mbarrier at shared-memory offset `mbar` of every CTA of
@@ -238,15 +220,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int 
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
                  "l"(tmap), "r"(x), "r"(y), "r"(mbar)
-                 : "memory");
-}
-
-// The same for the box at (x, y, z) of a 3-D tensor map.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z, uint32_t mbar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
-                 "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(mbar)
                  : "memory");
 }
 
