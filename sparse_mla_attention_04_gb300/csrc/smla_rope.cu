@@ -93,9 +93,17 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __
 template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ float from_f(float x) { return x; }
 
-// kVec elements moved as one access.
-template <typename E, int kVec> struct alignas(sizeof(E) * kVec) Pack {
-    E e[kVec];
+// kVec elements moved as one access: as one word, whose elements are looked at in
+// place (a structure of elements would be copied element by element).
+template <int kBytes> struct Word;
+template <> struct Word<16> { using type = uint4; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<2> { using type = uint16_t; };
+template <typename E, int kVec> struct Pack {
+    typename Word<sizeof(E) * kVec>::type w;
+    __device__ __forceinline__ void load(const E *p) { w = *reinterpret_cast<const decltype(w) *>(p); }
+    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<decltype(w) *>(p) = w; }
+    __device__ __forceinline__ E &at(int i) { return reinterpret_cast<E *>(&w)[i]; }
 };
 
 // A unit is what one thread turns or copies of one head: with halves, kVec
@@ -172,9 +180,9 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const RopeArgs a)
 #pragma unroll
                 for (int i = 0; i < kB; ++i)
                     if (h + i * hstep < count) {
-                        x[i] = *reinterpret_cast<const P *>(src + i * src_step);
+                        x[i].load(src + i * src_step);
                         if (kTwo && turns)
-                            y[kTwo ? i : 0] = *reinterpret_cast<const P *>(src + i * src_step + apart);
+                            y[kTwo ? i : 0].load(src + i * src_step + apart);
                     }
                 if (first) {
                     first = false;
@@ -201,20 +209,20 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(const RopeArgs a)
                         P yo;
 #pragma unroll
                         for (int e = 0; e < kVec; ++e) {
-                            const float xa = to_f(x[i].e[e]), xb = to_f(y[kTwo ? i : 0].e[e]);
-                            x[i].e[e] = from_f<E>(rot_a(xa, xb, c[e % kPairs], s[e % kPairs]));
-                            yo.e[e] = from_f<E>(rot_b(xa, xb, c[e % kPairs], s[e % kPairs]));
+                            const float xa = to_f(x[i].at(e)), xb = to_f(y[kTwo ? i : 0].at(e));
+                            x[i].at(e) = from_f<E>(rot_a(xa, xb, c[e % kPairs], s[e % kPairs]));
+                            yo.at(e) = from_f<E>(rot_b(xa, xb, c[e % kPairs], s[e % kPairs]));
                         }
-                        *reinterpret_cast<P *>(dst + i * dst_step + apart) = yo;
+                        yo.store(dst + i * dst_step + apart);
                     } else if (turns) {
 #pragma unroll
                         for (int e = 0; e < kPairs; ++e) {
-                            const float xa = to_f(x[i].e[(2 * e) % kVec]), xb = to_f(x[i].e[(2 * e + 1) % kVec]);
-                            x[i].e[(2 * e) % kVec] = from_f<E>(rot_a(xa, xb, c[e], s[e]));
-                            x[i].e[(2 * e + 1) % kVec] = from_f<E>(rot_b(xa, xb, c[e], s[e]));
+                            const float xa = to_f(x[i].at((2 * e) % kVec)), xb = to_f(x[i].at((2 * e + 1) % kVec));
+                            x[i].at((2 * e) % kVec) = from_f<E>(rot_a(xa, xb, c[e], s[e]));
+                            x[i].at((2 * e + 1) % kVec) = from_f<E>(rot_b(xa, xb, c[e], s[e]));
                         }
                     }
-                    *reinterpret_cast<P *>(dst + i * dst_step) = x[i];
+                    x[i].store(dst + i * dst_step);
                 }
             }
             // the next side's first head of this thread: the batches above pass heads beyond the end
