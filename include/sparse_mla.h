@@ -437,7 +437,8 @@ typedef enum {
  *                 H_k = 0: q alone.
  * q_out, k_out    device, the same shapes, strides of their own. An output may
  *                 be its input (then with the same strides: rotated in place);
- *                 otherwise it must not overlap an input.
+ *                 otherwise it must not overlap an input. Its rows must not
+ *                 overlap: st >= (H - 1) sh + D or sh >= (T - 1) st + D.
  * positions       device, int64 [T].
  * cos_sin_cache   device, float [max_position, rot_dim], 4-byte aligned.
  * rot_dim even, 2..256, rot_offset >= 0, rot_offset + rot_dim <= D <= 65536.
@@ -508,8 +509,9 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
  * block_table entry is outside [0, num_blocks) are not read and see no one;
  * nothing beyond seq_lens[b] is read. q keeps its bf16 values (dots in 16 bits
  * or in two 8-bit parts of it, sums in binary32), softmax weights are rounded to
- * binary16. The scales of one request's blocks of a head must be positive and
- * lie within a factor of 2^100 (smla_kv8_append gives at least 2^-60).
+ * binary16. Scales are read of the blocks that a token of the request sees; of
+ * one request and head they must be positive, at least 2^-60 (as
+ * smla_kv8_append gives them) and within a factor of 2^100.
  *
  * q             device, bf16 [T, H, D], element strides (t, h) multiples of 8,
  *               16-byte aligned, last dimension contiguous; D is 64 or 128.
@@ -529,7 +531,7 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
  *               current device), 256-byte aligned, need not be initialised.
  *               Calls that overlap in time must not share it.
  * H a multiple of H_kv; B >= 0, T >= 0 (0: a no-op); 0 <= window;
- * num_blocks * H_kv and table_width * block_size below 2^31.
+ * num_blocks * H_kv below 2^31, table_width * block_size at most 2^30.
  */
 typedef struct smla_kv8_attn_params {
     size_t size; /* sizeof(smla_kv8_attn_params) */
@@ -564,7 +566,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *params);
  * arithmetic, frees its tensor memory and returns, leaving the context usable.
  * smla_fused_qk_rope_cache and smla_rope set 4 for a position outside
  * [0, max_position); smla_fused_qk_rope_cache and smla_kv8_append set 8 for a
- * slot past the pool. Synchronous (copies the word from the device):
+ * slot past the pool. smla_kv8_attn_fwd's waits for its copies and products have
+ * the same limit and bits. Synchronous (copies the word from the device):
  * unlike every other entry point it waits for the device, since the word is
  * read on the host. reset != 0 clears it.
  */

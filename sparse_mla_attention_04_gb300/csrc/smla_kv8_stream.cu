@@ -140,10 +140,11 @@ template <int D, int NT> struct Layout {
     static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 32 + kNanWords * 4 + kWarps * kStages * 8;
 };
 
-// The workspace: total units; for each unit {first block, last block, request,
-// index in the request}; then a head and a tail partial of each block.
+// The workspace: for each block the unit that it begins and others end, {last
+// block (-1: none), request, index in the request}; then a head and a tail
+// partial of each block. Its size follows from the GPU alone, so nothing that the
+// lengths hold leads outside it.
 struct Part {
-    int *header;
     int4 *dir;
     float2 *ml;   // [2 blocks][R]
     float *o;     // [2 blocks][R][D]
@@ -167,51 +168,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
     // The block's place in the work, kept here and not in registers while a unit is worked on.
     __shared__ struct {
         long long at, hi;      // cost: where the block is, where its part ends
-        long long base, unit0; // cost and units before request b
+        long long base;        // cost before request b
         int b;
         Division cut;
-        long long warp_cost[kWarps], warp_count[kWarps];
+        long long warp_cost[kWarps];
     } s_walk;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     umma::grid_launch_dependents();
 
+    if (tid == 0)
+        part.dir[blockIdx.x] = make_int4(-1, 0, 0, 0);
     // The total cost and this block's part of it: each thread adds up its requests, the block scans the sums, and
     // the thread whose requests hold the part's begin finds the request.
     {
         const int per = (a.B + kThreads - 1) / kThreads;
-        long long cost = 0, count = 0;
+        long long cost = 0;
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
             if (b < a.B) {
                 const Units u = units_of<R>(a, request(a, b));
                 cost += u.count * u.cost;
-                count += u.count;
             }
         }
-        long long cost_to = cost, count_to = count; // inclusive
+        long long cost_to = cost; // inclusive
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, cost_to, d), y = __shfl_up_sync(0xffffffffu, count_to, d);
+            const long long x = __shfl_up_sync(0xffffffffu, cost_to, d);
             cost_to += lane >= d ? x : 0;
-            count_to += lane >= d ? y : 0;
         }
-        if (lane == 31) {
+        if (lane == 31)
             s_walk.warp_cost[warp] = cost_to;
-            s_walk.warp_count[warp] = count_to;
-        }
         __syncthreads();
-        long long total = 0, units = 0, cost0 = cost_to - cost, count0 = count_to - count;
+        long long total = 0, cost0 = cost_to - cost;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             cost0 += w < warp ? s_walk.warp_cost[w] : 0;
-            count0 += w < warp ? s_walk.warp_count[w] : 0;
             total += s_walk.warp_cost[w];
-            units += s_walk.warp_count[w];
         }
-        if (blockIdx.x == 0 && tid == 0)
-            *part.header = (int)units; // for the joining kernel
         const Division cut = Division::of(total, part.fill, gridDim.x);
         if ((int)blockIdx.x >= cut.big + cut.small)
             return;
@@ -223,13 +218,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             Units u = units_of<R>(a, request(a, b));
             while (lo >= cost0 + u.count * u.cost) {
                 cost0 += u.count * u.cost;
-                count0 += u.count;
                 u = units_of<R>(a, request(a, ++b));
             }
             s_walk.at = lo;
             s_walk.hi = hi;
             s_walk.base = cost0;
-            s_walk.unit0 = count0;
             s_walk.b = b;
             s_walk.cut = cut;
         }
@@ -252,13 +245,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
 
     __syncthreads();
     while (s_walk.at < s_walk.hi) {
-        long long at = s_walk.at, base = s_walk.base, unit0 = s_walk.unit0;
+        long long at = s_walk.at, base = s_walk.base;
         int b = s_walk.b;
         Request rq = request(a, b);
         Units un = units_of<R>(a, rq);
         while (at >= base + un.count * un.cost) { // requests without tokens have no units
             base += un.count * un.cost;
-            unit0 += un.count;
             ++b;
             rq = request(a, b);
             un = units_of<R>(a, rq);
@@ -271,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         if (tid == 0) {
             s_walk.at = uend;
             s_walk.base = base;
-            s_walk.unit0 = unit0;
             s_walk.b = b;
         }
         if (s0 >= s1) {
@@ -279,11 +270,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             continue;
         }
         const bool whole = s0 == 0 && s1 == un.steps;
-        if (s0 == 0 && tid == 0) {
-            // blocks that hold the unit's first and last step
-            const int c0 = s_walk.cut.part(ubase + kUnitCost), c1 = s_walk.cut.part(ubase + un.cost - 1);
-            part.dir[unit0 + ui] = make_int4(c0, c1, b, (int)ui);
-        }
+        if (s0 == 0 && !whole && tid == 0) // (the same thread as above)
+            part.dir[blockIdx.x] = make_int4(s_walk.cut.part(ubase + un.cost - 1), b, (int)ui, 0);
         const int h = (int)(ui % a.H_kv);
         const int row0 = (int)(ui / a.H_kv) * R;
         const int rows = min(R, rq.qlen * a.G - row0);
@@ -333,8 +321,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                     const int ex = ((tb + 16 * x) >> a.block_shift) - first;
                     const float c = __shfl_sync(0xffffffffu, e_c, ex), lv = __shfl_sync(0xffffffffu, e_lv, ex),
                                 iv = __shfl_sync(0xffffffffu, e_iv, ex);
+                    // of 16 positions that no row sees (below the window, where a block may have gone to
+                    // another request) the scales are not used: a bad one would reach the sums as 0 * NaN
+                    const bool seen = tb + 16 * x + 15 >= kv_begin;
                     if (lane == 0)
-                        meta[stage * 2 + x] = make_float4(c, lv, iv, 0.f);
+                        meta[stage * 2 + x] = seen ? make_float4(c, lv, iv, 0.f) : make_float4(0.f, -INFINITY, 1.f, 0.f);
                 }
                 __syncwarp();
                 // lanes p and 16 + p: block p of the step, for K and for V. A block outside the pool: rows
@@ -661,18 +652,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     umma::grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if ((int)blockIdx.x >= *part.header)
-        return;
     const int4 u = part.dir[blockIdx.x];
-    if (u.x == u.y)
+    const int c0 = blockIdx.x, c1 = u.x;
+    if (c1 <= c0)
         return;
-    const Request rq = request(a, u.z);
-    const int h = u.w % a.H_kv, row0 = u.w / a.H_kv * R, r = blockIdx.y;
+    const Request rq = request(a, u.y);
+    const int h = u.z % a.H_kv, row0 = u.z / a.H_kv * R, r = blockIdx.y;
     if (r >= min(R, rq.qlen * a.G - row0))
         return;
     float m = -INFINITY, l = 0.f;
-    for (int c = u.x + threadIdx.x; c <= u.y; c += kJoinWarps * 32)
-        m = fmaxf(m, part.ml[(2 * (int64_t)c + (c == u.x)) * R + r].x);
+    for (int c = c0 + threadIdx.x; c <= c1; c += kJoinWarps * 32)
+        m = fmaxf(m, part.ml[(2 * (int64_t)c + (c == c0)) * R + r].x);
     m = warp_max(m);
     if (lane == 0)
         s_m[warp] = m;
@@ -685,8 +675,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
     for (int i = 0; i < kD; ++i)
         acc[i] = 0.f;
 #pragma unroll 4
-    for (int c = u.x + warp; c <= u.y; c += kJoinWarps) {
-        const int64_t slot = (2 * (int64_t)c + (c == u.x)) * R + r;
+    for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+        const int64_t slot = (2 * (int64_t)c + (c == c0)) * R + r;
         const float2 ml = part.ml[slot];
         const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
         l += ml.y * f;
@@ -735,20 +725,17 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int fill_of(int NT, int sm_count) { return sm_count * (NT == 1 ? 3 : 2); }
 
 struct Sizes {
-    size_t dir, ml, o, total;
-    int64_t units;
+    size_t ml, o, total;
 };
 
-Sizes sizes(int64_t B, int64_t T, int H, int H_kv, int D, int NT, int sm_count)
+Sizes sizes(int D, int NT, int sm_count)
 {
     const int R = 8 * NT;
+    const size_t blocks = (size_t)fill_of(NT, sm_count) * (1 + kSmallPerBig);
     Sizes s;
-    s.units = (T * (H / H_kv) / R + B) * H_kv; // each request's last chunk may be short
-    const size_t slots = 2 * (size_t)fill_of(NT, sm_count) * (1 + kSmallPerBig);
-    s.dir = 256;
-    s.ml = up256(s.dir + (size_t)s.units * sizeof(int4));
-    s.o = up256(s.ml + slots * R * sizeof(float2));
-    s.total = s.o + slots * R * D * sizeof(float);
+    s.ml = up256(blocks * sizeof(int4));
+    s.o = up256(s.ml + 2 * blocks * R * sizeof(float2));
+    s.total = s.o + 2 * blocks * R * D * sizeof(float);
     return s;
 }
 
@@ -756,12 +743,9 @@ template <int D, int NT>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
     using L = Layout<D, NT>;
-    const Sizes sz = sizes(a.B, a.T, a.H, a.H_kv, D, NT, sm_count);
-    if (sz.units > 0x7FFFFFFF)
-        return cudaErrorInvalidValue;
+    const Sizes sz = sizes(D, NT, sm_count);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const Part part{reinterpret_cast<int *>(ws), reinterpret_cast<int4 *>(ws + sz.dir),
-                    reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o),
+    const Part part{reinterpret_cast<int4 *>(ws), reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o),
                     fill_of(NT, sm_count)};
     cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess)
@@ -770,7 +754,8 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     if (!kv8_tensor_maps(a, D, kStep, maps))
         return cudaErrorInvalidValue;
     // the most work that there can be decides the grid: blocks without a part end at once, but not for nothing
-    const double most = (double)sz.units * ((double)a.table_width * a.block_size / kStep + kUnitCost + 1);
+    const double units = ((double)a.T * a.G / (8 * NT) + a.B) * a.H_kv; // each request's last chunk may be short
+    const double most = units * ((double)a.table_width * a.block_size / kStep + kUnitCost + 1);
     const int fill = part.fill;
     int grid = fill * (1 + kSmallPerBig);
     if (most < 24.0 * kMinPart * fill) // no small parts
@@ -778,9 +763,11 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     kv8_stream_kernel<D, NT><<<grid, kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
+    if (grid == 1)
+        return cudaSuccess; // (every unit is whole)
     // behind it, its start overlapped (it waits for the first kernel's end)
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)sz.units, 8 * NT);
+    cfg.gridDim = dim3((unsigned)grid, 8 * NT);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -796,9 +783,9 @@ int tiles_for(int G, int max_query_len) { return (int64_t)G * max_query_len > 8 
 
 } // namespace
 
-size_t kv8_stream_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sm_count)
+size_t kv8_stream_workspace(int G, int D, int max_query_len, int sm_count)
 {
-    return sizes(B, T, H, H_kv, D, tiles_for(H / H_kv, max_query_len), sm_count).total;
+    return sizes(D, tiles_for(G, max_query_len), sm_count).total;
 }
 
 cudaError_t launch_kv8_stream(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count,

@@ -724,11 +724,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, k_full + (j & 3) * 8);
             issued = j + 1;
             if (lane >> 2 == (j & 7)) {
-                // a group outside the pool (or past the end): logits of -inf
+                // a group outside the pool, past the end, or below what any row sees (where the block may have
+                // gone to another request: a bad scale would reach the sums as 0 * NaN): logits of -inf
                 float *sc = scales + (j & 7) * 12 + (lane & 3);
-                sc[0] = ks * scale_log2;
-                sc[4] = v >= 0 ? lg2_approx(vs) : -INFINITY;
-                sc[8] = v >= 0 ? __frcp_rn(vs) : 1.f;
+                const bool seen = v >= 0 && tb0 + (t_begin + j) * kTile + 16 * (lane & 3) + 15 >= kv_begin;
+                sc[0] = seen ? ks * scale_log2 : 0.f;
+                sc[4] = seen ? lg2_approx(vs) : -INFINITY;
+                sc[8] = seen ? __frcp_rn(vs) : 1.f;
             }
             __syncwarp();
             if (lane == 0)

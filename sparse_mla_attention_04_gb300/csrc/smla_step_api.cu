@@ -40,7 +40,7 @@ bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) *
 
 size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sms)
 {
-    return few_rows(H, H_kv, max_query_len) ? smla::kv8_stream_workspace(B, T, H, H_kv, D, max_query_len, sms)
+    return few_rows(H, H_kv, max_query_len) ? smla::kv8_stream_workspace(H / H_kv, D, max_query_len, sms)
                                             : smla::kv8_tile_workspace(B, T, H, H_kv, D, sms);
 }
 
@@ -209,9 +209,12 @@ SMLA_API smla_status smla_rope(const smla_rope_params *p)
     if ((p->H > 0 && p->q == p->q_out && (p->q_stride_t != p->q_out_stride_t || p->q_stride_h != p->q_out_stride_h)) ||
         (p->H_k > 0 && p->k == p->k_out && (p->k_stride_t != p->k_out_stride_t || p->k_stride_h != p->k_out_stride_h)))
         return SMLA_ERR_BAD_SHAPE;
-    // two rows on one place would be written by several threads
+    // Rows over one another would be written by several threads: heads lie within a token's row, or tokens within a
+    // head's (any other order of rows apart is refused with those that overlap).
     const auto overlapping = [&](int heads, int64_t st, int64_t sh) {
-        return (heads > 1 && sh < p->D) || (p->T > 1 && st == 0);
+        if ((heads > 1 && sh < p->D) || (p->T > 1 && st < p->D))
+            return true;
+        return heads > 1 && p->T > 1 && st < (heads - 1) * sh + p->D && sh < (p->T - 1) * st + p->D;
     };
     if ((p->H > 0 && overlapping(p->H, p->q_out_stride_t, p->q_out_stride_h)) ||
         (p->H_k > 0 && overlapping(p->H_k, p->k_out_stride_t, p->k_out_stride_h)))
@@ -257,13 +260,18 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
 {
     if (T < 0 || H_kv <= 0 || num_blocks < 0 || k_stride_t < 0 || k_stride_h < 0 || v_stride_t < 0 || v_stride_h < 0)
         return SMLA_ERR_BAD_SHAPE;
-    if ((D != 64 && D != 128) || block_shift(block_size) < 0 || num_blocks > INT_MAX || H_kv > INT_MAX / 2)
+    if ((D != 64 && D != 128) || block_shift(block_size) < 0 || num_blocks > INT_MAX || H_kv > INT_MAX / 2 ||
+        T > INT_MAX - 128)
         return SMLA_ERR_UNSUPPORTED;
     if (T == 0)
         return SMLA_OK;
     if (k == nullptr || v == nullptr || slot_mapping == nullptr || k_cache == nullptr || v_cache == nullptr ||
         k_scale == nullptr || v_scale == nullptr)
         return SMLA_ERR_NULL_POINTER;
+    if (T == 1) // of one row no stride is used
+        k_stride_t = v_stride_t = 0;
+    if (H_kv == 1)
+        k_stride_h = v_stride_h = 0;
     if (k_stride_t % 8 != 0 || k_stride_h % 8 != 0 || v_stride_t % 8 != 0 || v_stride_h % 8 != 0 || !aligned(k, 16) ||
         !aligned(v, 16) || !aligned(slot_mapping, 8) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4))
@@ -311,7 +319,7 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     if (p->num_blocks < 0 || p->table_width < 0 || p->table_stride < p->table_width || p->window < 0 ||
         p->q_stride_t < 0 || p->q_stride_h < 0 || !std::isfinite(p->scale))
         return SMLA_ERR_BAD_SHAPE;
-    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > INT_MAX - 256 ||
+    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > 1 << 30 ||
         p->num_blocks > INT_MAX / p->H_kv)
         return SMLA_ERR_UNSUPPORTED;
     if (p->T == 0 || p->B == 0)
@@ -321,7 +329,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
         (p->num_blocks > 0 && (p->k_cache == nullptr || p->v_cache == nullptr || p->k_scale == nullptr || p->v_scale == nullptr)) ||
         p->workspace == nullptr)
         return SMLA_ERR_NULL_POINTER;
-    if (p->q_stride_t % 8 != 0 || p->q_stride_h % 8 != 0 || !aligned(p->q, 16) || !aligned(p->out, 16) ||
+    const int64_t q_st = p->T > 1 ? p->q_stride_t : 0, q_sh = p->H > 1 ? p->q_stride_h : 0; // (of one row none is used)
+    if (q_st % 8 != 0 || q_sh % 8 != 0 || !aligned(p->q, 16) || !aligned(p->out, 16) ||
         !aligned(p->k_cache, 16) || !aligned(p->v_cache, 16) || !aligned(p->k_scale, 4) || !aligned(p->v_scale, 4) ||
         !aligned(p->block_table, 4) || !aligned(p->seq_lens, 4) || !aligned(p->query_start, 4) || !aligned(p->lse, 4) ||
         !aligned(p->sinks, 4) || !aligned(p->workspace, 256))
@@ -333,8 +342,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
         return SMLA_ERR_WORKSPACE_TOO_SMALL;
     smla::Kv8AttnArgs a;
     a.q = p->q;
-    a.q_st = p->q_stride_t;
-    a.q_sh = p->q_stride_h;
+    a.q_st = q_st;
+    a.q_sh = q_sh;
     a.k_cache = static_cast<const uint8_t *>(p->k_cache);
     a.v_cache = static_cast<const uint8_t *>(p->v_cache);
     a.k_scale = p->k_scale;
@@ -352,7 +361,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     a.G = p->H / p->H_kv;
     a.block_size = p->block_size;
     a.block_shift = block_shift(p->block_size);
-    a.window = p->window;
+    // a window of all positions that the table has is none, and sums with others stay in 31 bits
+    a.window = p->window < (int64_t)p->table_width << a.block_shift ? p->window : 0;
     a.scale = p->scale;
     a.sinks = p->sinks;
     a.out = p->out;

@@ -426,3 +426,93 @@ def test_refuses_overlapping_shapes():
     with pytest.raises(ValueError):
         binding.smla_kv8_append(d["q"], d["q"], torch.zeros(1, dtype=torch.int64, device=DEV), d["kc"], d["vc"], d["ks"],
                                 d["vs"])
+
+
+@pytest.mark.parametrize("ql", [[1, 1, 1], [40, 1, 20]])
+@pytest.mark.parametrize("bad", [math.nan, 0.0, math.inf])
+def test_pages_below_the_window_may_be_gone(ql, bad):
+    """Blocks that no token sees any more (a window moved on) hold anything, their scales too."""
+    p = _problem(8, 2, 128, 16, [300, 170, 95], ql, seed=18)
+    window = 37
+    for b, n in enumerate((300, 170, 95)):
+        first = max(0, n - ql[b] - window + 1)                 # the lowest position that a token sees
+        for j in range(first // 16):
+            blk = int(p["table"][b, j])
+            p["ks"][blk], p["vs"][blk] = bad, bad
+            p["kc"][blk], p["vc"][blk] = 0x7F, 0x7F
+    out, lse = _run(p, window)
+    for b, n in enumerate((300, 170, 95)):                     # the reference multiplies what it masks
+        for j in range(max(0, n - ql[b] - window + 1) // 16):
+            blk = int(p["table"][b, j])
+            p["ks"][blk], p["vs"][blk] = 1.0, 1.0
+            p["kc"][blk], p["vc"][blk] = 0, 0
+    _check(p, (out, lse), window)
+
+
+@pytest.mark.parametrize("ql", [[1, 1], [30, 90]])
+def test_an_empty_pool_and_a_table_without_width(ql):
+    """Nothing is there to see: out 0, lse -inf (the sink with sinks)."""
+    T, H, D = sum(ql), 4, 64
+    q = torch.randn((T, H, D), device=DEV).to(torch.bfloat16)
+    start = torch.tensor([0, ql[0], T], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([100, 120], dtype=torch.int32, device=DEV)
+    sinks = torch.linspace(-1.0, 2.0, H, device=DEV)
+    for nb, width in ((0, 4), (5, 0), (0, 0)):
+        kc, vc, ks, vs = binding.new_kv8_cache(nb, 2, 32, D, device=DEV)
+        table = torch.zeros((2, width), dtype=torch.int32, device=DEV)
+        for s in (None, sinks):
+            out, lse = binding.smla_kv8_attn_fwd(q, kc, vc, ks, vs, table, lens, start, 0.1, max_query_len=max(ql), sinks=s)
+            assert bool((out == 0).all())
+            want = torch.full((T, H), -math.inf, device=DEV) if s is None else s.expand(T, H)
+            assert torch.allclose(lse, want, rtol=2.0 ** -18, atol=2.0 ** -18)
+    assert binding.smla_device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("ql", [[1, 1], [60, 70]])
+def test_lengths_beyond_the_table_and_the_widest_windows(ql):
+    """seq_lens are cut to the table; a window of everything is none."""
+    p = _problem(8, 2, 64, 16, [96, 64], ql, seed=19)
+    width = 6
+    cut = dict(p, table=p["table"][:, :width].contiguous())
+    cut["table"][1, 4:] = -1
+    long = dict(cut, lens=torch.tensor([2 ** 31 - 1, 64], dtype=torch.int32))
+    got = _run(long, 2 ** 31 - 1)
+    _check(dict(cut, lens=torch.tensor([96, 64], dtype=torch.int32)), got)
+
+
+@pytest.mark.parametrize("ql", [1, 150])
+def test_starts_that_overlap_stay_within_the_buffers(ql):
+    """Requests that name the same tokens again (an error of the caller): some result in
+    their rows, the other rows and everything outside as they were."""
+    p = _problem(8, 2, 128, 64, [200] * 6, [ql] * 6, seed=20, pad=2)
+    T = 6 * ql
+    p["start"] = torch.tensor([0, T, 0, T, 0, T, 0], dtype=torch.int32)
+    out = torch.full((T + 2, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    need = binding.smla_kv8_attn_workspace_size(6, T + 2, 8, 2, 128, ql)
+    room = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    _run(p, out=out, workspace=room[:need])
+    torch.cuda.synchronize()
+    assert bool((out[T:] == 3.0).all()) and bool((room[need:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("ql", [[1, 1, 1], [70, 130, 1]])
+def test_strides_of_single_rows_and_of_own_workspaces(ql):
+    """H = 1 with any head stride; a workspace of the caller, used again and again."""
+    p = _problem(1, 1, 64, 32, [90, 150, 31], ql, seed=21)
+    T = sum(ql)
+    flat = torch.zeros((T, 64 + 8), dtype=torch.bfloat16, device=DEV)
+    flat[:, :64] = p["q"].to(DEV)[:, 0]
+    q = flat.as_strided((T, 1, 64), (72, 3, 1))
+    room = torch.full((binding.smla_kv8_attn_workspace_size(3, T, 1, 1, 64, max(ql)),), 0xFF, dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        _check(p, _run(p, q=q, workspace=room))
+
+
+def test_append_of_nothing_and_of_one_head():
+    hk, D, bs, nb = 1, 128, 16, 3
+    codes, scales = _fresh(nb, hk, bs, D, 9)
+    _append_both(torch.empty((0, hk, D), dtype=torch.bfloat16, device=DEV), torch.empty((0, hk, D), dtype=torch.bfloat16, device=DEV),
+                 torch.empty(0, dtype=torch.int64), codes, scales)
+    rows = torch.randn((5, D), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    k = rows.as_strided((5, 1, D), (D, 7, 1))
+    _append_both(k, k, torch.arange(3, 8), codes, scales)

@@ -158,3 +158,30 @@ def test_packed_structures_match_the_headers():
         values = [i + 1 for i in range(n)]
         got = st.from_buffer_copy(packed.pack(*values))
         assert [getattr(got, name) for name, _ in st._fields_] == values
+
+
+def test_row_strides_that_no_row_uses_and_rows_over_one_another(L):
+    """Strides of a single token or head are free; output rows of a rotation must lie apart."""
+    def rope(st, sh, positions=P, T=4, H=8):
+        a = dict(size=ctypes.sizeof(b.SmlaRopeParams), dtype=0, q=P, q_stride_t=4096, q_stride_h=128, q_out=2 * P,
+                 q_out_stride_t=st, q_out_stride_h=sh, k=None, k_stride_t=0, k_stride_h=0, k_out=None, k_out_stride_t=0,
+                 k_out_stride_h=0, positions=positions, cos_sin_cache=P, max_position=100, T=T, H=H, H_k=0, D=128,
+                 rot_dim=64, rot_offset=0, is_neox=1, inverse=0, stream=None)
+        return L.smla_rope(ctypes.byref(b.SmlaRopeParams(*[a[n] for n, _ in b.SmlaRopeParams._fields_])))
+
+    for st, sh in ((128, 128), (64, 1024), (0, 128), (256, 192), (1000, 128)):
+        assert rope(st, sh) == b.SMLA_ERR_BAD_SHAPE, (st, sh)
+    # heads within a token, tokens within a head: refused for the positions' address only
+    for st, sh in ((1024, 128), (4096, 130), (128, 512)):
+        assert rope(st, sh, P + 4) == b.SMLA_ERR_MISALIGNED, (st, sh)
+
+    def append(**kw):
+        a = dict(k=P, kt=1024, kh=128, v=P, vt=1024, vh=128, slots=P + 4, T=4, H=8, D=128, bs=64, kc=P, vc=P, ks=P, vs=P,
+                 nb=10)
+        a.update(kw)
+        return L.smla_kv8_append(*[a[n] for n in ("k", "kt", "kh", "v", "vt", "vh", "slots", "T", "H", "D", "bs",
+                                                  "kc", "vc", "ks", "vs", "nb")], None)
+
+    assert append(T=(1 << 31) - 1) == b.SMLA_ERR_UNSUPPORTED
+    for kw in (dict(T=1, kt=1021, vt=3), dict(H=1, kh=5, vh=7)):
+        assert append(**kw) == b.SMLA_ERR_MISALIGNED       # (the slots' address)
