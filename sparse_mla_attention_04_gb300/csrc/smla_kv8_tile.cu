@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
     }
     const uint32_t bars = base + S::kBars;
     // K landed / free (four stages); V's codes landed / free, scores ready, P ready, V ready, values done (two
-    // stages each); scales written (eight stages); drained
+    // stages each); scales written (eight stages); drained; Q written
     const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, s_full = bars + 96,
-                   p_full = bars + 112, v_full = bars + 128, v_empty = bars + 144, sc_full = bars + 160, drained = bars + 224;
+                   p_full = bars + 112, v_full = bars + 128, v_empty = bars + 144, sc_full = bars + 160, drained = bars + 224, q_full = bars + 232;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     grid_wait(); // the plan
@@ -517,40 +517,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         for (int i = 0; i < 8; ++i)
             mbar_init(sc_full + 8 * i, 1);
         mbar_init(drained, 1);
+        mbar_init(q_full, kSoftmaxThreads);
         mbar_init_fence();
     }
     if (warp == 7)
         alloc(smem_u32(tmem_slot), S::kTmem);
     const float scale_log2 = fabsf(a.scale) * kLog2e; // the sign goes into q
 
-    float qs = 0.f;
-    if (tid < kSoftmaxThreads) {
-        // this thread's row of Q, in two E4M3 parts
-        const int r = tid;
-        const bool live = r < rows;
-        const int rr = row0 + (live ? r : 0);
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                           (int64_t)(rq.q0 + rr / a.G) * a.q_st +
-                                                           (int64_t)(it.h * a.G + rr % a.G) * a.q_sh);
-        float amax = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i)
-            amax = fmaxf(amax, live ? amax8(src[i]) : 0.f);
-        float up;
-        split_scale(amax, up, qs);
-        up = a.scale < 0.f ? -up : up;
-        const uint32_t dst = base + S::kQ + (r >> 3) * S::kQAtoms + (r & 7) * 16;
-#pragma unroll 2
-        for (int i = 0; i < D / 16; ++i) {
-            uint32_t hi[2][2], lo[2][2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                split8(live ? src[2 * i + e] : make_uint4(0, 0, 0, 0), up, hi[e], lo[e]);
-            sts128(dst + i * 128, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
-            sts128(dst + S::kQBytes + i * 128, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
-        }
-        fence_async_smem();
-    }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -566,7 +539,35 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
 
     if (warp < 4) {
         // ---------------------------------------------------------------- softmax
+        // this thread's row of Q, in two E4M3 parts; meanwhile the first codes come
         const int r = tid;
+        float qs;
+        {
+            const bool live = r < rows;
+            const int rr = row0 + (live ? r : 0);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                               (int64_t)(rq.q0 + rr / a.G) * a.q_st +
+                                                               (int64_t)(it.h * a.G + rr % a.G) * a.q_sh);
+            float amax = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < D / 8; ++i)
+                amax = fmaxf(amax, live ? amax8(src[i]) : 0.f);
+            float up;
+            split_scale(amax, up, qs);
+            up = a.scale < 0.f ? -up : up;
+            const uint32_t dst = base + S::kQ + (r >> 3) * S::kQAtoms + (r & 7) * 16;
+#pragma unroll 2
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t hi[2][2], lo[2][2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    split8(live ? src[2 * i + e] : make_uint4(0, 0, 0, 0), up, hi[e], lo[e]);
+                sts128(dst + i * 128, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
+                sts128(dst + S::kQBytes + i * 128, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
+            }
+            fence_async_smem();
+            mbar_arrive(q_full);
+        }
         const int pos = r < rows ? rq.pos((row0 + r) / a.G) : -1;
         const Sight see{p_first, all_from, pos, a.window > 0 ? pos - a.window + 1 : 0};
         const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
@@ -776,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             __syncwarp();
             return true;
         };
-        bool go = scores(0) && (n == 1 || scores(1));
+        bool go = wait_warp(q_full, 0) && scores(0) && (n == 1 || scores(1));
 #pragma unroll 1
         for (int j = 0; go && j < n; ++j) {
             const int stage = j & 1, phase = (j >> 1) & 1;
