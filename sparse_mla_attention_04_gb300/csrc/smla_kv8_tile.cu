@@ -46,34 +46,36 @@ namespace {
 using namespace kv8;
 using namespace umma;
 
-constexpr int kRows = 128;
+constexpr int kRows = 128;  // of a row tile
 constexpr int kTile = 64;
-constexpr int kSoftmaxThreads = 128, kVThreads = 64;
-constexpr int kThreads = 256;
 constexpr float kSlack = 15.0f;
 constexpr int kMaxSplits = 16; // of an item's positions
 constexpr int kWaves = 2;      // an item is split where it is more than this part of a CTA slot's share
 constexpr int kMinSplit = 16;  // tiles of a split, at least
 
-template <int D> struct Shape {
-    static constexpr int kQBytes = kRows * D;       // one part of Q
+template <int D, int NR> struct Shape {
+    static constexpr int kItemRows = NR * kRows;
+    static constexpr int kVWarps = 2 * NR;
+    static constexpr int kV0 = 4 * NR, kLoader = kV0 + kVWarps, kMma = kLoader + 1; // the roles' first warps
+    static constexpr int kThreads = (kMma + NR) * 32;
+    static constexpr int kQBytes = kRows * D;       // one part of a row tile's Q
     static constexpr int kTileBytes = kTile * D;    // one tile of codes
     static constexpr int kVBytes = kTile * D * 2;   // a tile of V in binary16
     static constexpr int kQAtoms = D / 16 * 128;    // 8 rows of Q: D / 16 core matrices
     static constexpr int kVAtoms = D / 8 * 128;     // 8 rows of V
     static constexpr int kK = 0;                    // four stages
     static constexpr int kCodes = 4 * kTileBytes;   // V as it comes, two stages
-    static constexpr int kQ = 6 * kTileBytes;       // hi, lo
-    static constexpr int kV = kQ + 2 * kQBytes;     // two stages
+    static constexpr int kQ = 6 * kTileBytes;       // of each row tile: hi, lo
+    static constexpr int kV = kQ + NR * 2 * kQBytes; // two stages
     static constexpr int kScales = kV + 2 * kVBytes; // 8 stages x 4 groups x {c, log2 vs, 1 / vs}
     static constexpr int kBars = kScales + 8 * 4 * 12;
-    static constexpr int kMisc = kBars + 32 * 8;
+    static constexpr int kMisc = kBars + 40 * 8;
     static constexpr int kSmem = kMisc + 16;
-    static constexpr uint32_t kTmem = 256;          // two S (P over each one's first half) and O
+    static constexpr uint32_t kTmem = 256;          // of a row tile: two S (P over each one's first half) and O
     static constexpr uint32_t kO = 2 * kTile;
     static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
     static constexpr uint32_t kIdescO = idesc(128, D, 0, 0, 0, 1);
-    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
+    static_assert(NR == 2 || 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
 // The plan of a call, in the workspace: how many entries and how many split items
@@ -83,9 +85,9 @@ struct Plan {
     int *header;
     int4 *entries;
     int4 *splits;
-    float2 *ml; // [partials][H_kv][128]
-    float *o;   // [partials][H_kv][128][D]
-    int n_items;
+    float2 *ml; // [partials][H_kv][item_rows]
+    float *o;   // [partials][H_kv][item_rows][D]
+    int n_items, item_rows;
 };
 
 // A tile's item: request, chunk of rows, kv head.
@@ -94,23 +96,23 @@ struct Item {
 };
 
 // Items are numbered request by request; request b's first number is
-// floor(q0 G / 128) + b, which leaves room for its ceil(rows / 128) chunks
-// without a running sum. Returns false for a number that no chunk has.
-__device__ __forceinline__ bool find_item(const Kv8AttnArgs &a, int n, Item *it)
+// floor(q0 G / item_rows) + b, which leaves room for its ceil(rows / item_rows)
+// chunks without a running sum. Returns false for a number that no chunk has.
+__device__ __forceinline__ bool find_item(const Kv8AttnArgs &a, int item_rows, int n, Item *it)
 {
     int lo = 0, hi = a.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         const int q0 = min(max(a.query_start[mid], 0), a.T);
-        if ((int)((long long)q0 * a.G / kRows) + mid <= n)
+        if ((int)((long long)q0 * a.G / item_rows) + mid <= n)
             lo = mid;
         else
             hi = mid - 1;
     }
     const Request r = request(a, lo);
     it->b = lo;
-    it->chunk = n - ((int)((long long)r.q0 * a.G / kRows) + lo);
-    return it->chunk >= 0 && (long long)it->chunk * kRows < (long long)r.qlen * a.G;
+    it->chunk = n - ((int)((long long)r.q0 * a.G / item_rows) + lo);
+    return it->chunk >= 0 && (long long)it->chunk * item_rows < (long long)r.qlen * a.G;
 }
 
 // What an item's rows see.
@@ -121,11 +123,11 @@ struct Span {
     int tb0, tiles;       // tiles of kTile positions from tb0 on (a multiple of kTile: blocks lie whole in the tiles)
 };
 
-__device__ __forceinline__ Span span_of(const Kv8AttnArgs &a, const Request &rq, int chunk)
+__device__ __forceinline__ Span span_of(const Kv8AttnArgs &a, int item_rows, const Request &rq, int chunk)
 {
     Span s;
-    s.row0 = chunk * kRows;
-    s.rows = min(kRows, rq.qlen * a.G - s.row0);
+    s.row0 = chunk * item_rows;
+    s.rows = min(item_rows, rq.qlen * a.G - s.row0);
     s.p_first = rq.pos(s.row0 / a.G);
     s.p_last = rq.pos((s.row0 + s.rows - 1) / a.G);
     s.kv_end = min(rq.len, s.p_last + 1);
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8At
     __syncthreads();
     auto tiles_of = [&](int n) { // -1: no such item
         Item it;
-        return find_item(a, n, &it) ? span_of(a, request(a, it.b), it.chunk).tiles : -1;
+        return find_item(a, plan.item_rows, n, &it) ? span_of(a, plan.item_rows, request(a, it.b), it.chunk).tiles : -1;
     };
     int kept[kPlanned];
     long long sum = 0;
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8At
         if (ns > 1) {
             first = atomicAdd(&s_parts, ns);
             Item it;
-            (void)find_item(a, n, &it);
+            (void)find_item(a, plan.item_rows, n, &it);
             plan.splits[atomicAdd(&s_split_items, 1)] = make_int4(it.b, it.chunk, ns, first);
         }
         for (int i = 0; i < ns; ++i)
@@ -439,12 +441,12 @@ __device__ __noinline__ uint32_t nan_columns(const Kv8AttnArgs &a, const Item &i
     return bits;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
+template <int D, int NR>
+__global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                const __grid_constant__ CUtensorMap v_map,
                                                                const Kv8AttnArgs a, const Plan plan)
 {
-    using S = Shape<D>;
+    using S = Shape<D, NR>;
     extern __shared__ __align__(1024) uint8_t smem[]; // (the swizzle goes by address)
     int *s_any_nan = reinterpret_cast<int *>(smem + S::kMisc + 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -455,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         return;
     }
     const uint32_t bars = base + S::kBars;
-    // K landed / free (four stages); V's codes landed / free, scores ready, P ready, V ready, values done (two
-    // stages each); scales written (eight stages); drained; Q written
-    const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, s_full = bars + 96,
-                   p_full = bars + 112, v_full = bars + 128, v_empty = bars + 144, sc_full = bars + 160, drained = bars + 224, q_full = bars + 232;
+    // K landed / free (four stages); V's codes landed / free, V ready (two stages); scales written (eight stages);
+    // drained (each row tile); Q written; of each row tile, two stages: scores ready, P ready, values done
+    const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, v_full = bars + 96,
+                   sc_full = bars + 112, drained = bars + 176, q_full = bars + 192, s_full = bars + 200, p_full = bars + 232,
+                   v_empty = bars + 264;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     grid_wait(); // the plan
@@ -468,18 +471,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
     if (n_entry >= plan.header[0])
         return;
     const int split = entry.y & 0xFFFF, splits = entry.y >> 16;
-    if (!find_item(a, entry.x, &it))
+    if (!find_item(a, S::kItemRows, entry.x, &it))
         return;
     it.h = (int)(blockIdx.x % a.H_kv);
-    const int64_t slot0 = ((int64_t)(entry.z + split) * a.H_kv + it.h) * kRows; // (of a split item)
+    const int64_t slot0 = ((int64_t)(entry.z + split) * a.H_kv + it.h) * S::kItemRows; // (of a split item)
     const Request rq = request(a, it.b);
-    const Span sp = span_of(a, rq, it.chunk);
+    const Span sp = span_of(a, S::kItemRows, rq, it.chunk);
     const int row0 = sp.row0, rows = sp.rows, p_first = sp.p_first, p_last = sp.p_last, kv_begin = sp.kv_begin,
               kv_end = sp.kv_end, all_from = sp.all_from, tb0 = sp.tb0;
     const int t_begin = (int)((long long)sp.tiles * split / splits);
     const int t_end = (int)((long long)sp.tiles * (split + 1) / splits);
     const int n = t_end - t_begin;
     const bool many = p_first != p_last;
+    const int live_tiles = NR == 1 || rows <= kRows ? 1 : 2; // (a row tile without rows does nothing)
 
     if (n <= 0) { // nothing to see here
         if (tid < rows) {
@@ -504,24 +508,26 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         *s_any_nan = 0;
         for (int i = 0; i < 4; ++i) {
             mbar_init(k_full + 8 * i, 1);
-            mbar_init(k_empty + 8 * i, 1);
+            mbar_init(k_empty + 8 * i, live_tiles);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(c_full + 8 * i, 1);
-            mbar_init(c_empty + 8 * i, kVThreads);
+            mbar_init(c_empty + 8 * i, S::kVWarps * 32);
+            mbar_init(v_full + 8 * i, S::kVWarps * 32);
+            mbar_init(drained + 8 * i, 1);
+        }
+        for (int i = 0; i < 2 * NR; ++i) {
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, kSoftmaxThreads);
-            mbar_init(v_full + 8 * i, kVThreads);
+            mbar_init(p_full + 8 * i, kRows);
             mbar_init(v_empty + 8 * i, 1);
         }
         for (int i = 0; i < 8; ++i)
             mbar_init(sc_full + 8 * i, 1);
-        mbar_init(drained, 1);
-        mbar_init(q_full, kSoftmaxThreads);
+        mbar_init(q_full, live_tiles * kRows);
         mbar_init_fence();
     }
-    if (warp == 7)
-        alloc(smem_u32(tmem_slot), S::kTmem);
+    if (warp == S::kMma)
+        alloc(smem_u32(tmem_slot), NR * S::kTmem);
     const float scale_log2 = fabsf(a.scale) * kLog2e; // the sign goes into q
 
     fence_before_sync();
@@ -537,7 +543,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         return ok;
     };
 
-    if (warp < 4) {
+    if (warp < S::kV0) {
+        const int tile = warp >> 2; // of rows
+        if (tile < live_tiles) {
         // ---------------------------------------------------------------- softmax
         // this thread's row of Q, in two E4M3 parts; meanwhile the first codes come
         const int r = tid;
@@ -555,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             float up;
             split_scale(amax, up, qs);
             up = a.scale < 0.f ? -up : up;
-            const uint32_t dst = base + S::kQ + (r >> 3) * S::kQAtoms + (r & 7) * 16;
+            const uint32_t dst = base + S::kQ + tile * 2 * S::kQBytes + ((r & 127) >> 3) * S::kQAtoms + (r & 7) * 16;
 #pragma unroll 2
             for (int i = 0; i < D / 16; ++i) {
                 uint32_t hi[2][2], lo[2][2];
@@ -570,18 +578,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         }
         const int pos = r < rows ? rq.pos((row0 + r) / a.G) : -1;
         const Sight see{p_first, all_from, pos, a.window > 0 ? pos - a.window + 1 : 0};
-        const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t my = tmem + tile * S::kTmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_ready = s_full + tile * 16, p_ready = p_full + tile * 16, o_done = v_empty + tile * 16;
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
         Row sums{-INFINITY, 0.f};
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             // the scales of this tile's blocks, its scores
-            if (!wait_warp(sc_full + (j & 7) * 8, (j >> 3) & 1) || !wait_warp(s_full + (j & 1) * 8, (j >> 1) & 1))
+            if (!wait_warp(sc_full + (j & 7) * 8, (j >> 3) & 1) || !wait_warp(s_ready + (j & 1) * 8, (j >> 1) & 1))
                 break;
             fence_after_sync();
             // O is at rest once the last tile's product is done: the next one waits for this tile's weights
             const auto settle = [&] {
-                const bool done = wait_warp(v_empty + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1);
+                const bool done = wait_warp(o_done + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1);
                 fence_after_sync();
                 return done;
             };
@@ -590,12 +599,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 break;
             wait_st();
             fence_before_sync();
-            mbar_arrive(p_full + (j & 1) * 8);
+            mbar_arrive(p_ready + (j & 1) * 8);
         }
         const float m = sums.m, l = sums.l;
         // (V's last arrival carries the notes of NaN codes)
         if (ok && wait_warp(v_full + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1) &&
-            wait_warp(v_empty + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1)) {
+            wait_warp(o_done + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1)) {
             fence_after_sync();
             const bool live = r < rows;
             const int rr = row0 + (live ? r : 0);
@@ -643,27 +652,31 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                     a.lse[t * a.H + head] = lse;
             }
         }
-    } else if (warp < 6) {
+        }
+    } else if (warp < S::kLoader) {
         // ---------------------------------------------------------------- V
-        const int row_in = (warp - 4) * (kTile / 2) + (lane & 7), piece = lane >> 3; // rows row_in + 8 k, pieces piece + 4 c
+        constexpr int kTurns = kTile / S::kVWarps / 8;
+        const int row_in = (warp - S::kV0) * kTurns * 8 + (lane & 7), piece = lane >> 3; // rows row_in + 8 k, pieces piece + 4 c
         const int turn = D == 128 ? lane & 7 : (lane >> 1) & 3;                      // the swizzle of the lane's rows
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int stage = j & 1;
-            if (!wait_warp(c_full + stage * 8, (j >> 1) & 1) || (j > 1 && !wait_warp(v_empty + stage * 8, ((j >> 1) - 1) & 1)))
+            if (!wait_warp(c_full + stage * 8, (j >> 1) & 1) ||
+                (j > 1 && (!wait_warp(v_empty + stage * 8, ((j >> 1) - 1) & 1) ||
+                           (live_tiles > 1 && !wait_warp(v_empty + 16 + stage * 8, ((j >> 1) - 1) & 1)))))
                 break;
             const int tb = tb0 + (t_begin + j) * kTile;
             const bool clear = tb + kTile - 1 <= p_first && tb >= all_from;
             const uint32_t src = base + S::kCodes + stage * S::kTileBytes + row_in * D;
             const uint32_t dst = base + S::kV + stage * S::kVBytes + (row_in >> 3) * S::kVAtoms + (lane & 7) * 16 + piece * 256;
-            uint4 q[kTile / 16][D / 64]; // all of them on their way before the first is used
+            uint4 q[kTurns][D / 64]; // all of them on their way before the first is used
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
+            for (int k = 0; k < kTurns; ++k)
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                     q[k][c] = lds128(src + k * 8 * D + (((piece + 4 * c) ^ turn) << 4));
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) {
+            for (int k = 0; k < kTurns; ++k) {
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t w[4] = {q[k][c].x, q[k][c].y, q[k][c].z, q[k][c].w};
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
             fence_async_smem();
             mbar_arrive(v_full + stage * 8);
         }
-    } else if (warp == 6) {
+    } else if (warp == S::kLoader) {
         // ---------------------------------------------------------------- the cache's codes and scales
         const int32_t *table = a.block_table + it.b * a.table_stride;
         const int rows_in = min(kTile, a.block_size); // of a block in a tile
@@ -752,11 +765,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
         for (int j = max(0, v_issued - 2); j < v_issued; ++j)
             if (!mbar_wait(c_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
-    } else {
-        // ---------------------------------------------------------------- products
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t q_hi = desc(base + S::kQ, 128, S::kQAtoms);
-        const uint64_t q_lo = desc(base + S::kQ + S::kQBytes, 128, S::kQAtoms);
+    } else if (warp - S::kMma < live_tiles) {
+        // ---------------------------------------------------------------- products of a row tile
+        const int tile = __shfl_sync(0xffffffffu, warp - S::kMma, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + tile * S::kTmem;
+        const uint32_t s_ready = s_full + tile * 16, p_ready = p_full + tile * 16, o_done = v_empty + tile * 16;
+        const uint64_t q_hi = desc(base + S::kQ + tile * 2 * S::kQBytes, 128, S::kQAtoms);
+        const uint64_t q_lo = desc(base + S::kQ + (tile * 2 + 1) * S::kQBytes, 128, S::kQAtoms);
         const auto scores = [&](int j) {
             if (!wait_warp(k_full + (j & 3) * 8, (j >> 2) & 1))
                 return false;
@@ -771,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
                     mma_f8(dst, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
-                commit(s_full + (j & 1) * 8);
+                commit(s_ready + (j & 1) * 8);
                 commit(k_empty + (j & 3) * 8);
             }
             __syncwarp();
@@ -781,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
 #pragma unroll 1
         for (int j = 0; go && j < n; ++j) {
             const int stage = j & 1, phase = (j >> 1) & 1;
-            if (!wait_warp(v_full + stage * 8, phase) || !wait_warp(p_full + stage * 8, phase))
+            if (!wait_warp(v_full + stage * 8, phase) || !wait_warp(p_ready + stage * 8, phase))
                 break;
             fence_after_sync();
             const uint64_t v_d = desc(base + S::kV + stage * S::kVBytes, S::kVAtoms, 128);
@@ -790,45 +805,46 @@ __global__ void __launch_bounds__(kThreads, 2) kv8_tile_kernel(const __grid_cons
                 for (int kk = 0; kk < kTile / 16; ++kk) // 16 positions: 8 columns of P, two atoms of V
                     mma_f16_ts(tm + S::kO, tm + stage * kTile + kk * 8, v_d + (uint64_t)(kk * 2 * S::kVAtoms / 16), S::kIdescO,
                                j > 0 || kk > 0);
-                commit(v_empty + stage * 8);
+                commit(o_done + stage * 8);
             }
             __syncwarp();
             // P lies over its scores: those of two tiles on go there when its product is done
-            if (j + 2 < n && (!wait_warp(v_empty + stage * 8, phase) || !scores(j + 2)))
+            if (j + 2 < n && (!wait_warp(o_done + stage * 8, phase) || !scores(j + 2)))
                 break;
         }
         if (!ok) { // what was issued ends before its memory is given back
             if (elect_one())
-                commit(drained);
-            if (!mbar_wait(drained, 0) && lane == 0)
+                commit(drained + tile * 8);
+            if (!mbar_wait(drained + tile * 8, 0) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
         }
     }
     __syncwarp();
     fence_before_sync();
     __syncthreads();
-    if (warp == 7)
-        dealloc(tmem, S::kTmem);
+    if (warp == S::kMma)
+        dealloc(tmem, NR * S::kTmem);
 }
 
 // Joins the splits of the split items' rows, a warp to a row; the blocks share
 // out the items by eight rows.
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a, const Plan plan)
 {
     constexpr int kD = D / 32;
+    constexpr int kItemRows = NR * kRows, kEights = kItemRows / 8;
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int work = plan.header[1] * a.H_kv * 16; // (partials are fewer than 2^31 / 128)
+    const int work = plan.header[1] * a.H_kv * kEights; // (partials are fewer than 2^31 / 256)
     for (int x = blockIdx.x; x < work; x += gridDim.x) {
-        const int4 info = plan.splits[x / 16 / a.H_kv];
-        const int splits = info.z, h = x / 16 % a.H_kv;
+        const int4 info = plan.splits[x / kEights / a.H_kv];
+        const int splits = info.z, h = x / kEights % a.H_kv;
         const Request rq = request(a, info.x);
-        const int row0 = info.y * kRows;
-        const int rows = min(kRows, rq.qlen * a.G - row0);
-        const int r = warp + 8 * (int)(x & 15);
+        const int row0 = info.y * kItemRows;
+        const int rows = min(kItemRows, rq.qlen * a.G - row0);
+        const int r = warp + 8 * (int)(x % kEights);
         if (r < rows) {
-            auto slot = [&](int s) { return ((int64_t)(info.w + s) * a.H_kv + h) * kRows + r; };
+            auto slot = [&](int s) { return ((int64_t)(info.w + s) * a.H_kv + h) * kItemRows + r; };
             const float2 mine = lane < splits ? plan.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
             const float m = warp_max(mine.x);
             const float f_mine = mine.x == -INFINITY ? 1.f : ex2_approx(mine.x - m);
@@ -874,21 +890,24 @@ struct Sizes {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+int slots_of(int NR, int sm_count) { return (NR == 1 ? 2 : 1) * std::max(sm_count, 1); } // CTAs at a time
+
 // Items: each request's last chunk may be short. Entries: an item, and one more
 // for each whole part of the shares that its length holds. Split items: no more
 // than there are parts; their partials at most twice as many.
-Sizes sizes_of(int64_t B, int64_t T, int G, int H_kv, int D, int sm_count)
+Sizes sizes_of(int64_t B, int64_t T, int G, int H_kv, int D, int NR, int sm_count)
 {
     Sizes z;
-    const int64_t parts = (int64_t)kWaves * 2 * std::max(sm_count, 1) / H_kv + 1;
-    z.items = T * G / kRows + B;
+    const int64_t parts = (int64_t)kWaves * slots_of(NR, sm_count) / H_kv + 1;
+    const int64_t item_rows = NR * kRows;
+    z.items = T * G / item_rows + B;
     z.entries = z.items + parts;
     z.partials = 2 * parts;
     z.entries_at = 256;
     z.splits_at = up256(z.entries_at + (size_t)z.entries * sizeof(int4));
     z.ml_at = up256(z.splits_at + (size_t)parts * sizeof(int4));
-    z.o_at = up256(z.ml_at + (size_t)z.partials * H_kv * kRows * sizeof(float2));
-    z.total = z.o_at + (size_t)z.partials * H_kv * kRows * D * sizeof(float);
+    z.o_at = up256(z.ml_at + (size_t)z.partials * H_kv * item_rows * sizeof(float2));
+    z.total = z.o_at + (size_t)z.partials * H_kv * item_rows * D * sizeof(float);
     return z;
 }
 
@@ -909,41 +928,48 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int s
     return cudaLaunchKernelEx(&cfg, kernel, given...);
 }
 
-template <int D>
+template <int D, int NR>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
-    const Sizes z = sizes_of(a.B, a.T, a.G, a.H_kv, D, sm_count);
+    using S = Shape<D, NR>;
+    const Sizes z = sizes_of(a.B, a.T, a.G, a.H_kv, D, NR, sm_count);
     if (z.entries * a.H_kv > 0x7FFFFFFF)
         return cudaErrorInvalidValue;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Plan plan{reinterpret_cast<int *>(ws), reinterpret_cast<int4 *>(ws + z.entries_at), reinterpret_cast<int4 *>(ws + z.splits_at),
-                    reinterpret_cast<float2 *>(ws + z.ml_at), reinterpret_cast<float *>(ws + z.o_at), (int)z.items};
-    cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+                    reinterpret_cast<float2 *>(ws + z.ml_at), reinterpret_cast<float *>(ws + z.o_at), (int)z.items,
+                    S::kItemRows};
+    cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kTile, maps))
         return cudaErrorInvalidValue;
-    kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, 2 * sm_count);
+    kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, slots_of(NR, sm_count));
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    e = launch_behind(kv8_tile_kernel<D>, dim3((unsigned)(z.entries * a.H_kv)), kThreads, Shape<D>::kSmem, stream, maps[0], maps[1],
-                      a, plan);
+    e = launch_behind(kv8_tile_kernel<D, NR>, dim3((unsigned)(z.entries * a.H_kv)), S::kThreads, S::kSmem, stream, maps[0],
+                      maps[1], a, plan);
     if (e != cudaSuccess)
         return e;
-    return launch_behind(kv8_tile_join_kernel<D>, dim3((unsigned)(16 * sm_count)), 256, 0, stream, a, plan);
+    return launch_behind(kv8_tile_join_kernel<D, NR>, dim3((unsigned)(16 * sm_count)), 256, 0, stream, a, plan);
 }
+
+// Row tiles of a CTA: two where a request's rows may fill more than one.
+int row_tiles(int G, int max_query_len) { return (int64_t)G * max_query_len > kRows ? 2 : 1; }
 
 } // namespace
 
-size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int sm_count)
+size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sm_count)
 {
-    return sizes_of(B, T, H / H_kv, H_kv, D, sm_count).total;
+    return sizes_of(B, T, H / H_kv, H_kv, D, row_tiles(H / H_kv, max_query_len), sm_count).total;
 }
 
-cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, void *workspace, int sm_count, cudaStream_t stream)
+cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream)
 {
-    return D == 128 ? launch<128>(a, workspace, sm_count, stream) : launch<64>(a, workspace, sm_count, stream);
+    if (row_tiles(a.G, max_query_len) == 2)
+        return D == 128 ? launch<128, 2>(a, workspace, sm_count, stream) : launch<64, 2>(a, workspace, sm_count, stream);
+    return D == 128 ? launch<128, 1>(a, workspace, sm_count, stream) : launch<64, 1>(a, workspace, sm_count, stream);
 }
 
 cudaError_t read_kv8_error(int *out, bool reset)

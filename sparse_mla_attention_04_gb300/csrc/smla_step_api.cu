@@ -41,7 +41,7 @@ bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) *
 size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sms)
 {
     return few_rows(H, H_kv, max_query_len) ? smla::kv8_stream_workspace(H / H_kv, D, max_query_len, sms)
-                                            : smla::kv8_tile_workspace(B, T, H, H_kv, D, sms);
+                                            : smla::kv8_tile_workspace(B, T, H, H_kv, D, max_query_len, sms);
 }
 
 smla_status check_kv8_shape(int B, int T, int H, int H_kv, int D, int max_query_len)
@@ -368,7 +368,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     a.out = p->out;
     a.lse = p->lse;
     if (!few_rows(p->H, p->H_kv, p->max_query_len))
-        return cuda_status(smla::launch_kv8_tile(a, p->D, p->workspace, sms, reinterpret_cast<cudaStream_t>(p->stream)));
+        return cuda_status(smla::launch_kv8_tile(a, p->D, p->max_query_len, p->workspace, sms,
+                                                 reinterpret_cast<cudaStream_t>(p->stream)));
     return cuda_status(smla::launch_kv8_stream(a, p->D, p->max_query_len, p->workspace, sms,
                                                reinterpret_cast<cudaStream_t>(p->stream)));
 }
