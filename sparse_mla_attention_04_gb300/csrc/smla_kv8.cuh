@@ -26,6 +26,28 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// A bounded wait of a whole converged warp (as umma::mbar_wait). The warp votes
+// on what it saw, so the control flow stays uniform: where lanes branch on their
+// own, coming together again costs 100 to 200 cycles a wait.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t mbar, uint32_t parity)
+{
+    const auto look = [&] {
+        uint32_t done;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(done)
+                     : "r"(mbar), "r"(parity)
+                     : "memory");
+        return __all_sync(0xffffffffu, done);
+    };
+    if (look())
+        return true;
+    const long long c0 = clock64();
+    while (!look())
+        if (__any_sync(0xffffffffu, clock64() - c0 > (1ll << 32)))
+            return false;
+    return true;
+}
+
 // TMA tile load of the box at (x, y, z) of a 3-D tensor map into shared memory at
 // dst (in the map's swizzle), bytes counted on mbar; out-of-range parts of the box
 // are filled with zeros.

@@ -537,7 +537,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
     bool ok = true;
     // a bounded wait, by whole warps
     auto wait_warp = [&](uint32_t bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
+        ok = ok && mbar_wait_warp(bar, parity);
         if (!ok && lane == 0)
             atomicOr(&g_kv8_error, 1);
         return ok;
