@@ -48,7 +48,7 @@ using namespace umma;
 
 constexpr int kRows = 128;  // of a row tile
 constexpr int kTile = 64;
-constexpr float kSlack = 15.0f;
+constexpr float kSlack = 8.0f;
 constexpr int kMaxSplits = 16; // of an item's positions
 constexpr int kWaves = 2;      // an item is split where it is more than this part of a CTA slot's share
 constexpr int kMinSplit = 16;  // tiles of a split, at least
@@ -274,13 +274,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c)); // a NaN loses, as with fmaxf
-    return r;
-}
-
 // Waits for this thread's tensor-memory loads; x holds what they brought only after it.
 __device__ __forceinline__ void wait_ld32(uint32_t (&x)[32])
 {
@@ -312,93 +305,123 @@ struct Row {
     float m, l; // reference (log2 units), denominator relative to it
 };
 
+// The factors of a tile's 4 groups of 16 positions: of their logits, log2 of
+// their value scales, and its inverse.
+struct Factors {
+    float k[4], vs[4], iv[4];
+    __device__ __forceinline__ Factors(const float *sc, float qs)
+    {
+        const float4 f = *reinterpret_cast<const float4 *>(sc), v = *reinterpret_cast<const float4 *>(sc + 4),
+                     w = *reinterpret_cast<const float4 *>(sc + 8);
+        k[0] = f.x * qs, k[1] = f.y * qs, k[2] = f.z * qs, k[3] = f.w * qs;
+        vs[0] = v.x, vs[1] = v.y, vs[2] = v.z, vs[3] = v.w;
+        iv[0] = w.x, iv[1] = w.y, iv[2] = w.z, iv[3] = w.w;
+    }
+};
+
+// Sixteen logits relative to the reference become weights in binary16; their sum.
+__device__ __forceinline__ float weigh(const uint32_t *x, uint32_t *p)
+{
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const float p0 = ex2_approx(__uint_as_float(x[i])), p1 = ex2_approx(__uint_as_float(x[i + 1]));
+        sum = add2(sum, pair(p0, p1));
+        p[i / 2] = pack_f16x2(p0, p1);
+    }
+    float s0, s1;
+    unpair(sum, s0, s1);
+    return s0 + s1;
+}
+
 // One row's 64 scores (the thread's lane of tensor memory at my) become weights
 // 2^(s + log2(vs) - m) in binary16, over the scores they come from; their sum,
-// each group's divided by vs, joins l. sc: the factors of the 4 groups of 16,
-// log2 of their value scales, 1 / vs. settle() is called, by the whole warp,
-// before O is rescaled: false where its wait gave up. o_cols: O's columns (0
-// before the first product).
-template <typename Settle>
-__device__ __forceinline__ bool row_tile(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row &row, int t0,
-                                         const Sight &see, Settle settle)
+// each group's divided by vs, joins l. False where the reference may have to move
+// (the sum passes 2^15, so a weight may pass what binary16 holds) for some row of
+// the warp: then nothing is changed. For tiles that all rows see.
+__device__ __forceinline__ bool row_tile(uint32_t my, const float *sc, float qs, Row &row)
 {
     uint32_t x[64];
     ld32(my, *reinterpret_cast<uint32_t(*)[32]>(x));
     ld32(my + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-    const float4 f = *reinterpret_cast<const float4 *>(sc), v = *reinterpret_cast<const float4 *>(sc + 4);
-    const float k[4] = {f.x * qs, f.y * qs, f.z * qs, f.w * qs}, vs[4] = {v.x, v.y, v.z, v.w};
+    const Factors f(sc, qs);
+    wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x));
+    wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
+    uint32_t p[32];
+    float l = row.l, all = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float b = f.vs[c] - row.m;
+#pragma unroll
+        for (int i = c * 16; i < c * 16 + 16; i += 2) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pair(f.k[c], f.k[c]), pair(b, b)), e0, e1);
+            x[i] = __float_as_uint(e0);
+            x[i + 1] = __float_as_uint(e1);
+        }
+        const float s = weigh(x + c * 16, p + c * 8);
+        all += s;
+        l = fmaf(s, f.iv[c], l);
+    }
+    // beyond 2^20 the rounding of m alone could pass any bound of the weights
+    if (__any_sync(0xffffffffu, all > 0x1p15f || !(fabsf(row.m) <= 0x1p20f)))
+        return false;
+    row.l = l;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        st16(my + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(p + 16 * i));
+    return true;
+}
+
+// The same for any tile: positions that the row does not see are left out, and the
+// reference moves to the largest logit where that passes it by kSlack. O is at
+// rest. o_cols: O's columns (0 before the first product).
+__device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row row, int t0,
+                                            const Sight see)
+{
+    uint32_t x[64];
+    ld32(my, *reinterpret_cast<uint32_t(*)[32]>(x));
+    ld32(my + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+    const Factors f(sc, qs);
     const float ref = row.m == -INFINITY ? 0.f : row.m;
     wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x));
     wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
-    float now; // the reference that would make the tile's largest weight 1
-    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (fabsf(ref) <= 0x1p20f && see.all(t0) && see.all(t0 + 32)) {
+    // the difference is taken from the rounded logit, as the reference is
+    float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-            float e0, e1;
-            const float b = vs[i >> 4] - ref;
-            unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pair(k[i >> 4], k[i >> 4]), pair(b, b)), e0, e1);
-            x[i] = __float_as_uint(e0);
-            x[i + 1] = __float_as_uint(e1);
-            top[i >> 4] = max3(top[i >> 4], e0, e1);
-        }
-        top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        now = ref + top[0];
-    } else {
-        // Also beyond 2^20, where the difference is taken from the rounded logit, as the
-        // reference is: the rounding of m alone could pass any bound of the weights.
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            const float s = see.sees(t0 + i) ? fmaf(__uint_as_float(x[i]), k[i >> 4], vs[i >> 4]) : -INFINITY;
-            x[i] = __float_as_uint(s - ref);
-            top[i >> 4] = fmaxf(top[i >> 4], s);
-        }
-        now = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        top[0] = now - ref;
+    for (int i = 0; i < 64; ++i) {
+        const float s = see.sees(t0 + i) ? fmaf(__uint_as_float(x[i]), f.k[i >> 4], f.vs[i >> 4]) : -INFINITY;
+        x[i] = __float_as_uint(s - ref);
+        top = fmaxf(top, s); // (a NaN loses)
     }
-    const bool raise = row.m == -INFINITY ? top[0] > -INFINITY : top[0] > kSlack;
+    const bool raise = row.m == -INFINITY ? top > -INFINITY : top - ref > kSlack;
     if (__any_sync(0xffffffffu, raise)) {
         // the row's sums so far and its O under the new reference
-        const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - now)) : 1.f;
-        const float d = raise ? now - ref : 0.f;
-        row.m = raise ? now : row.m;
+        const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - top)) : 1.f;
+        const float d = raise ? top - ref : 0.f;
+        row.m = raise ? top : row.m;
         row.l *= g;
 #pragma unroll
         for (int i = 0; i < 64; ++i)
             x[i] = __float_as_uint(__uint_as_float(x[i]) - d);
-        if (o_cols > 0) {
-            if (!settle())
-                return false;
 #pragma unroll 1
-            for (int o = 0; o < o_cols; o += 16) {
-                uint32_t p[16];
-                ld16(my_o + o, p);
-                wait_ld16(p);
+        for (int o = 0; o < o_cols; o += 16) {
+            uint32_t p[16];
+            ld16(my_o + o, p);
+            wait_ld16(p);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    p[i] = __float_as_uint(__uint_as_float(p[i]) * g);
-                st16(my_o + o, p);
-            }
+            for (int i = 0; i < 16; ++i)
+                p[i] = __float_as_uint(__uint_as_float(p[i]) * g);
+            st16(my_o + o, p);
         }
     }
-    const float4 w = *reinterpret_cast<const float4 *>(sc + 8);
-    const float iv[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint32_t p[8];
-        uint64_t sum = 0;
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float p0 = ex2_approx(__uint_as_float(x[c * 16 + i])), p1 = ex2_approx(__uint_as_float(x[c * 16 + i + 1]));
-            sum = add2(sum, pair(p0, p1));
-            p[i / 2] = pack_f16x2(p0, p1);
-        }
+        row.l = fmaf(weigh(x + c * 16, p), f.iv[c], row.l);
         st8(my + c * 8, p);
-        float s0, s1;
-        unpair(sum, s0, s1);
-        row.l = fmaf(s0 + s1, iv[c], row.l);
     }
-    return true;
+    return row;
 }
 
 // V's codes of a position in a tile that not every row sees whole: nothing where
@@ -581,22 +604,22 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         const uint32_t my = tmem + tile * S::kTmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_ready = s_full + tile * 16, p_ready = p_full + tile * 16, o_done = v_empty + tile * 16;
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
-        Row sums{-INFINITY, 0.f};
+        Row sums{r < rows ? -INFINITY : 0.f, 0.f}; // (a row that is not there, all zeros, moves no reference)
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             // the scales of this tile's blocks, its scores
             if (!wait_warp(sc_full + (j & 7) * 8, (j >> 3) & 1) || !wait_warp(s_ready + (j & 1) * 8, (j >> 1) & 1))
                 break;
             fence_after_sync();
-            // O is at rest once the last tile's product is done: the next one waits for this tile's weights
-            const auto settle = [&] {
-                const bool done = wait_warp(o_done + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1);
+            const int t0 = tb0 + (t_begin + j) * kTile;
+            const float *sc = scales + (j & 7) * 12;
+            if (!(see.all(t0) && see.all(t0 + 32) && row_tile(my + (j & 1) * kTile, sc, qs, sums))) {
+                // O is at rest once the last tile's product is done: the next one waits for this tile's weights
+                if (j > 0 && !wait_warp(o_done + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1))
+                    break;
                 fence_after_sync();
-                return done;
-            };
-            if (!row_tile(my + (j & 1) * kTile, my + S::kO, j > 0 ? D : 0, scales + (j & 7) * 12, qs, sums,
-                          tb0 + (t_begin + j) * kTile, see, settle))
-                break;
+                sums = row_tile_moving(my + (j & 1) * kTile, my + S::kO, j > 0 ? D : 0, sc, qs, sums, t0, see);
+            }
             wait_st();
             fence_before_sync();
             mbar_arrive(p_ready + (j & 1) * 8);
