@@ -67,10 +67,10 @@ template <int D, int NR> struct Shape {
     static constexpr int kCodes = 4 * kTileBytes;   // V as it comes, two stages
     static constexpr int kQ = 6 * kTileBytes;       // of each row tile: hi, lo
     static constexpr int kV = kQ + NR * 2 * kQBytes; // two stages
-    static constexpr int kScales = kV + 2 * kVBytes; // 8 stages x 4 groups x {c, log2 vs, 1 / vs}
-    static constexpr int kBars = kScales + 8 * 4 * 12;
-    static constexpr int kMisc = kBars + 40 * 8;
-    static constexpr int kSmem = kMisc + 16;
+    static constexpr int kScales = kV + 2 * kVBytes; // 2 stages x 8 tiles x {c, log2 vs, 1 / vs} x 4 groups
+    static constexpr int kBars = kScales + 2 * 8 * 4 * 12;
+    static constexpr int kMisc = kBars + 31 * 8;    // the tensor memory's address, a flag
+    static constexpr int kSmem = kMisc + 8;
     static constexpr uint32_t kTmem = 256;          // of a row tile: two S (P over each one's first half) and O
     static constexpr uint32_t kO = 2 * kTile;
     static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
 {
     using S = Shape<D, NR>;
     extern __shared__ __align__(1024) uint8_t smem[]; // (the swizzle goes by address)
-    int *s_any_nan = reinterpret_cast<int *>(smem + S::kMisc + 8);
+    int *s_any_nan = reinterpret_cast<int *>(smem + S::kMisc + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) { // a layout that the swizzle does not fit
@@ -480,11 +480,11 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         return;
     }
     const uint32_t bars = base + S::kBars;
-    // K landed / free (four stages); V's codes landed / free, V ready (two stages); scales written (eight stages);
+    // K landed / free (four stages); V's codes landed / free, V ready (two stages); scales of eight tiles written (two stages);
     // drained (each row tile); Q written; of each row tile, two stages: scores ready, P ready, values done
     const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, v_full = bars + 96,
-                   sc_full = bars + 112, drained = bars + 176, q_full = bars + 192, s_full = bars + 200, p_full = bars + 232,
-                   v_empty = bars + 264;
+                   sc_full = bars + 112, drained = bars + 128, q_full = bars + 144, s_full = bars + 152, p_full = bars + 184,
+                   v_empty = bars + 216;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     grid_wait(); // the plan
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             mbar_init(p_full + 8 * i, kRows);
             mbar_init(v_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2; ++i)
             mbar_init(sc_full + 8 * i, 1);
         mbar_init(q_full, live_tiles * kRows);
         mbar_init_fence();
@@ -607,12 +607,12 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         Row sums{r < rows ? -INFINITY : 0.f, 0.f}; // (a row that is not there, all zeros, moves no reference)
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            // the scales of this tile's blocks, its scores
-            if (!wait_warp(sc_full + (j & 7) * 8, (j >> 3) & 1) || !wait_warp(s_ready + (j & 1) * 8, (j >> 1) & 1))
+            // the scales of the next eight tiles' blocks, this tile's scores
+            if (((j & 7) == 0 && !wait_warp(sc_full + (j >> 3 & 1) * 8, (j >> 4) & 1)) || !wait_warp(s_ready + (j & 1) * 8, (j >> 1) & 1))
                 break;
             fence_after_sync();
             const int t0 = tb0 + (t_begin + j) * kTile;
-            const float *sc = scales + (j & 7) * 12;
+            const float *sc = scales + (j & 15) * 12;
             if (!(see.all(t0) && see.all(t0 + 32) && row_tile(my + (j & 1) * kTile, sc, qs, sums))) {
                 // O is at rest once the last tile's product is done: the next one waits for this tile's weights
                 if (j > 0 && !wait_warp(o_done + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1))
@@ -760,18 +760,20 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             if (lane < pages)
                 tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, k_full + (j & 3) * 8);
             issued = j + 1;
-            if (lane >> 2 == (j & 7)) {
-                // a group outside the pool, past the end, or below what any row sees (where the block may have
-                // gone to another request: a bad scale would reach the sums as 0 * NaN): logits of -inf
-                float *sc = scales + (j & 7) * 12 + (lane & 3);
-                const bool seen = v >= 0 && tb0 + (t_begin + j) * kTile + 16 * (lane & 3) + 15 >= kv_begin;
+            if ((j & 7) == 0) {
+                // the scales of eight tiles, a group to a lane. A group outside the pool, past the end, or below
+                // what any row sees (where the block may have gone to another request: a bad scale would reach
+                // the sums as 0 * NaN): logits of -inf. (The place was last read for tiles up to j - 9, and the
+                // products of j - 6 are done.)
+                float *sc = scales + ((j & 15) + (lane >> 2)) * 12 + (lane & 3);
+                const bool seen = v >= 0 && tb0 + (t_begin + j + (lane >> 2)) * kTile + 16 * (lane & 3) + 15 >= kv_begin;
                 sc[0] = seen ? ks * scale_log2 : 0.f;
                 sc[4] = seen ? lg2_approx(vs) : -INFINITY;
                 sc[8] = seen ? __frcp_rn(vs) : 1.f;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(sc_full + (j >> 3 & 1) * 8);
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(sc_full + (j & 7) * 8);
             if (j > 1 && !wait_warp(c_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
                 break;
             if (lane == 0)
