@@ -56,7 +56,7 @@ constexpr int kMinSplit = 16;  // tiles of a split, at least
 template <int D, int NR> struct Shape {
     static constexpr int kItemRows = NR * kRows;
     static constexpr int kVWarps = 2 * NR;
-    static constexpr int kV0 = 4 * NR, kLoader = kV0 + kVWarps, kMma = kLoader + 1; // the roles' first warps
+    static constexpr int kV0 = 4 * NR, kLoader = kV0 + kVWarps, kMma = kLoader + NR; // the roles' first warps
     static constexpr int kThreads = (kMma + NR) * 32;
     static constexpr int kQBytes = kRows * D;       // one part of a row tile's Q
     static constexpr int kTileBytes = kTile * D;    // one tile of codes
@@ -530,11 +530,11 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
     if (tid == 0) {
         *s_any_nan = 0;
         for (int i = 0; i < 4; ++i) {
-            mbar_init(k_full + 8 * i, 1);
+            mbar_init(k_full + 8 * i, kTile / min(kTile, a.block_size));
             mbar_init(k_empty + 8 * i, live_tiles);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(c_full + 8 * i, 1);
+            mbar_init(c_full + 8 * i, kTile / min(kTile, a.block_size));
             mbar_init(c_empty + 8 * i, S::kVWarps * 32);
             mbar_init(v_full + 8 * i, S::kVWarps * 32);
             mbar_init(drained + 8 * i, 1);
@@ -717,8 +717,10 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             fence_async_smem();
             mbar_arrive(v_full + stage * 8);
         }
-    } else if (warp == S::kLoader) {
+    } else if (warp < S::kMma) {
         // ---------------------------------------------------------------- the cache's codes and scales
+        // One row tile: one warp for K and V; two: a warp for each (one alone held up the rest with small blocks).
+        const bool with_k = NR == 1 || warp == S::kLoader, with_v = NR == 1 || warp != S::kLoader;
         const int32_t *table = a.block_table + it.b * a.table_stride;
         const int rows_in = min(kTile, a.block_size); // of a block in a tile
         const int pages = kTile / rows_in;
@@ -746,21 +748,23 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                 vs_next = scale_of(a.v_scale, v_next);
                 raw = entry((j >> 3) + 2);
             }
-            // lanes p and 16 + p: block p of the tile, for K and for V
-            const int page = __shfl_sync(0xffffffffu, v, (j & 7) * 4 + (((lane & 15) * rows_in >> 4) & 3));
-            // a block outside the pool: rows outside the map, which fills zeros and reads nothing
+            // lane p: block p of the tile. A block outside the pool: rows outside the map, which fills zeros and
+            // reads nothing
+            const int page = __shfl_sync(0xffffffffu, v, (j & 7) * 4 + ((lane * rows_in >> 4) & 3));
             const int y = page >= 0 ? (tb0 + (t_begin + j) * kTile) & (a.block_size - 1) : a.block_size;
             const int z = page >= 0 ? page * a.H_kv + it.h : 0;
-            const uint32_t at = (lane & 15) * rows_in * D;
-            if (j > 3 && !wait_warp(k_empty + (j & 3) * 8, ((j >> 2) - 1) & 1))
-                break;
-            if (lane == 0)
-                mbar_arrive_expect_tx(k_full + (j & 3) * 8, S::kTileBytes);
-            __syncwarp();
-            if (lane < pages)
-                tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, k_full + (j & 3) * 8);
-            issued = j + 1;
-            if ((j & 7) == 0) {
+            const uint32_t at = lane * rows_in * D;
+            if (with_k) {
+                const uint32_t full = k_full + (j & 3) * 8;
+                if (j > 3 && !wait_warp(k_empty + (j & 3) * 8, ((j >> 2) - 1) & 1))
+                    break;
+                if (lane < pages) {
+                    mbar_arrive_expect_tx(full, rows_in * D);
+                    tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, full);
+                }
+                issued = j + 1;
+            }
+            if (with_k && (j & 7) == 0) {
                 // the scales of eight tiles, a group to a lane. A group outside the pool, past the end, or below
                 // what any row sees (where the block may have gone to another request: a bad scale would reach
                 // the sums as 0 * NaN): logits of -inf. (The place was last read for tiles up to j - 9, and the
@@ -774,14 +778,16 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                 if (lane == 0)
                     mbar_arrive(sc_full + (j >> 3 & 1) * 8);
             }
-            if (j > 1 && !wait_warp(c_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
-                break;
-            if (lane == 0)
-                mbar_arrive_expect_tx(c_full + (j & 1) * 8, S::kTileBytes);
-            __syncwarp();
-            if (lane >= 16 && lane - 16 < pages)
-                tma_load_3d(base + S::kCodes + (j & 1) * S::kTileBytes + at, &v_map, 0, y, z, c_full + (j & 1) * 8);
-            v_issued = j + 1;
+            if (with_v) {
+                const uint32_t full = c_full + (j & 1) * 8;
+                if (j > 1 && !wait_warp(c_empty + (j & 1) * 8, ((j >> 1) - 1) & 1))
+                    break;
+                if (lane < pages) {
+                    mbar_arrive_expect_tx(full, rows_in * D);
+                    tma_load_3d(base + S::kCodes + (j & 1) * S::kTileBytes + at, &v_map, 0, y, z, full);
+                }
+                v_issued = j + 1;
+            }
         }
         // no copy outlives the block, also where a wait gave up
         for (int j = max(0, issued - 4); j < issued; ++j)
