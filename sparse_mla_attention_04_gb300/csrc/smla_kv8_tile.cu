@@ -63,9 +63,10 @@ template <int D, int NR> struct Shape {
     static constexpr int kVBytes = kTile * D * 2;   // a tile of V in binary16
     static constexpr int kQAtoms = D / 16 * 128;    // 8 rows of Q: D / 16 core matrices
     static constexpr int kVAtoms = D / 8 * 128;     // 8 rows of V
-    static constexpr int kK = 0;                    // four stages
-    static constexpr int kCodes = 4 * kTileBytes;   // V as it comes, two stages
-    static constexpr int kQ = 6 * kTileBytes;       // of each row tile: hi, lo
+    static constexpr int kKStages = 2 * NR;         // of two tiles (a power of two)
+    static constexpr int kK = 0;
+    static constexpr int kCodes = 2 * kKStages * kTileBytes; // V as it comes, two stages
+    static constexpr int kQ = kCodes + 2 * kTileBytes; // of each row tile: hi, lo
     static constexpr int kV = kQ + NR * 2 * kQBytes; // two stages
     static constexpr int kScales = kV + 2 * kVBytes; // 2 stages x 8 tiles x {c, log2 vs, 1 / vs} x 4 groups
     static constexpr int kBars = kScales + 2 * 8 * 4 * 12;
@@ -480,11 +481,11 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         return;
     }
     const uint32_t bars = base + S::kBars;
-    // K landed / free (four stages); V's codes landed / free, V ready (two stages); scales of eight tiles written (two stages);
-    // drained (each row tile); Q written; of each row tile, two stages: scores ready, P ready, values done
-    const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, v_full = bars + 96,
-                   sc_full = bars + 112, drained = bars + 128, q_full = bars + 144, s_full = bars + 152, p_full = bars + 184,
-                   v_empty = bars + 216;
+    // K landed / free (up to four stages of two tiles); V's codes landed / free (two stages); scales of eight tiles written
+    // (two stages); drained (each row tile); Q written; of each row tile, two stages: scores ready, P and V ready,
+    // values done
+    const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, sc_full = bars + 96,
+                   drained = bars + 112, q_full = bars + 128, s_full = bars + 136, p_full = bars + 168, v_empty = bars + 200;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     grid_wait(); // the plan
@@ -529,23 +530,22 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
 
     if (tid == 0) {
         *s_any_nan = 0;
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(k_full + 8 * i, kTile / min(kTile, a.block_size));
+        const int pages = kTile / min(kTile, a.block_size);
+        for (int i = 0; i < S::kKStages; ++i) {
+            mbar_init(k_full + 8 * i, 2 * pages);
             mbar_init(k_empty + 8 * i, live_tiles);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(c_full + 8 * i, kTile / min(kTile, a.block_size));
-            mbar_init(c_empty + 8 * i, S::kVWarps * 32);
-            mbar_init(v_full + 8 * i, S::kVWarps * 32);
+            mbar_init(c_full + 8 * i, pages);
+            mbar_init(c_empty + 8 * i, S::kVWarps);
+            mbar_init(sc_full + 8 * i, 1);
             mbar_init(drained + 8 * i, 1);
         }
         for (int i = 0; i < 2 * NR; ++i) {
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, kRows);
+            mbar_init(p_full + 8 * i, kRows + S::kVWarps);
             mbar_init(v_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i)
-            mbar_init(sc_full + 8 * i, 1);
         mbar_init(q_full, live_tiles * kRows);
         mbar_init_fence();
     }
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         }
         const float m = sums.m, l = sums.l;
         // (V's last arrival carries the notes of NaN codes)
-        if (ok && wait_warp(v_full + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1) &&
+        if (ok && wait_warp(p_ready + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1) &&
             wait_warp(o_done + ((n - 1) & 1) * 8, ((n - 1) >> 1) & 1)) {
             fence_after_sync();
             const bool live = r < rows;
@@ -713,9 +713,12 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                     sts128(dst + k * S::kVAtoms + c * 1024 + 128, f[4], f[5], f[6], f[7]);
                 }
             }
-            mbar_arrive(c_empty + stage * 8);
             fence_async_smem();
-            mbar_arrive(v_full + stage * 8);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(c_empty + stage * 8);
+            if (lane < live_tiles)
+                mbar_arrive(p_full + lane * 16 + stage * 8);
         }
     } else if (warp < S::kMma) {
         // ---------------------------------------------------------------- the cache's codes and scales
@@ -748,27 +751,29 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                 vs_next = scale_of(a.v_scale, v_next);
                 raw = entry((j >> 3) + 2);
             }
-            // lane p: block p of the tile. A block outside the pool: rows outside the map, which fills zeros and
-            // reads nothing
-            const int page = __shfl_sync(0xffffffffu, v, (j & 7) * 4 + ((lane * rows_in >> 4) & 3));
-            const int y = page >= 0 ? (tb0 + (t_begin + j) * kTile) & (a.block_size - 1) : a.block_size;
+            // lane p: block p of the tile and (of K) of the next one. A block outside the pool: rows outside the map,
+            // which fills zeros and reads nothing
+            const int page = __shfl_sync(0xffffffffu, v, ((j & 7) * 4 + (lane * rows_in >> 4)) & 31);
+            const int y = page >= 0 ? (tb0 + (t_begin + j) * kTile + lane * rows_in) & (a.block_size - 1) : a.block_size;
             const int z = page >= 0 ? page * a.H_kv + it.h : 0;
             const uint32_t at = lane * rows_in * D;
-            if (with_k) {
-                const uint32_t full = k_full + (j & 3) * 8;
-                if (j > 3 && !wait_warp(k_empty + (j & 3) * 8, ((j >> 2) - 1) & 1))
+            if (with_k && !(j & 1)) {
+                const int two = j >> 1;
+                const int stage = two & (S::kKStages - 1);
+                const uint32_t full = k_full + stage * 8;
+                if (two >= S::kKStages && !wait_warp(k_empty + stage * 8, (two / S::kKStages - 1) & 1))
                     break;
-                if (lane < pages) {
+                if (lane < 2 * pages) {
                     mbar_arrive_expect_tx(full, rows_in * D);
-                    tma_load_3d(base + S::kK + (j & 3) * S::kTileBytes + at, &k_map, 0, y, z, full);
+                    tma_load_3d(base + S::kK + stage * 2 * S::kTileBytes + at, &k_map, 0, y, z, full);
                 }
-                issued = j + 1;
+                issued = two + 1;
             }
             if (with_k && (j & 7) == 0) {
                 // the scales of eight tiles, a group to a lane. A group outside the pool, past the end, or below
                 // what any row sees (where the block may have gone to another request: a bad scale would reach
-                // the sums as 0 * NaN): logits of -inf. (The place was last read for tiles up to j - 9, and the
-                // products of j - 6 are done.)
+                // the sums as 0 * NaN): logits of -inf. (The place was last read for tiles up to j - 9; the scores
+                // of j - 7 are there, which waited for the values of j - 9.)
                 float *sc = scales + ((j & 15) + (lane >> 2)) * 12 + (lane & 3);
                 const bool seen = v >= 0 && tb0 + (t_begin + j + (lane >> 2)) * kTile + 16 * (lane & 3) + 15 >= kv_begin;
                 sc[0] = seen ? ks * scale_log2 : 0.f;
@@ -790,8 +795,8 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             }
         }
         // no copy outlives the block, also where a wait gave up
-        for (int j = max(0, issued - 4); j < issued; ++j)
-            if (!mbar_wait(k_full + (j & 3) * 8, (j >> 2) & 1) && lane == 0)
+        for (int j = max(0, issued - S::kKStages); j < issued; ++j)
+            if (!mbar_wait(k_full + (j & (S::kKStages - 1)) * 8, (j / S::kKStages) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
         for (int j = max(0, v_issued - 2); j < v_issued; ++j)
             if (!mbar_wait(c_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
@@ -804,10 +809,11 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         const uint64_t q_hi = desc(base + S::kQ + tile * 2 * S::kQBytes, 128, S::kQAtoms);
         const uint64_t q_lo = desc(base + S::kQ + (tile * 2 + 1) * S::kQBytes, 128, S::kQAtoms);
         const auto scores = [&](int j) {
-            if (!wait_warp(k_full + (j & 3) * 8, (j >> 2) & 1))
+            const int stage = (j >> 1) & (S::kKStages - 1);
+            if (!(j & 1) && !wait_warp(k_full + stage * 8, (j >> 1) / S::kKStages & 1))
                 return false;
             fence_after_sync();
-            const uint32_t k_s = base + S::kK + (j & 3) * S::kTileBytes;
+            const uint32_t k_s = base + S::kK + (stage * 2 + (j & 1)) * S::kTileBytes;
             const uint64_t k_d = D == 128 ? desc_sw128(k_s, 16, 1024) : desc_sw64(k_s, 16, 512);
             const uint32_t dst = tm + (j & 1) * kTile;
             if (elect_one()) {
@@ -818,7 +824,8 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                 for (int kk = 0; kk < D / 32; ++kk)
                     mma_f8(dst, q_lo + kk * 16, k_d + kk * 2, S::kIdescS, 1);
                 commit(s_ready + (j & 1) * 8);
-                commit(k_empty + (j & 3) * 8);
+                if ((j & 1) || j == n - 1)
+                    commit(k_empty + stage * 8);
             }
             __syncwarp();
             return true;
@@ -827,7 +834,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
 #pragma unroll 1
         for (int j = 0; go && j < n; ++j) {
             const int stage = j & 1, phase = (j >> 1) & 1;
-            if (!wait_warp(v_full + stage * 8, phase) || !wait_warp(p_ready + stage * 8, phase))
+            if (!wait_warp(p_ready + stage * 8, phase))
                 break;
             fence_after_sync();
             const uint64_t v_d = desc(base + S::kV + stage * S::kVBytes, S::kVAtoms, 128);
