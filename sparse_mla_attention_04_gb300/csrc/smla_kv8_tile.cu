@@ -80,11 +80,15 @@ template <int D, int NR> struct Shape {
 };
 
 // The plan of a call, in the workspace: how many entries and how many split items
-// there are; the entries {item, split | splits << 16, first partial}, the longest
-// first; the split items {request, chunk, splits, first partial}; their partial sums.
+// there are; the entries, the longest first; the split items {request, chunk,
+// splits, first partial}; their partial sums.
+struct Entry {
+    int b, chunk, split, first;   // split | splits << 16; first partial
+    int q0, qlen, len, none;      // the request
+};
 struct Plan {
     int *header;
-    int4 *entries;
+    Entry *entries;
     int4 *splits;
     float2 *ml; // [partials][H_kv][item_rows]
     float *o;   // [partials][H_kv][item_rows][D]
@@ -222,14 +226,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8At
         const int ns = splits(tiles);
         const int at = atomicAdd(&s_hist[bucket(tiles)], ns);
         int first = 0;
+        Item it;
+        (void)find_item(a, plan.item_rows, n, &it);
         if (ns > 1) {
             first = atomicAdd(&s_parts, ns);
-            Item it;
-            (void)find_item(a, plan.item_rows, n, &it);
             plan.splits[atomicAdd(&s_split_items, 1)] = make_int4(it.b, it.chunk, ns, first);
         }
+        const Request rq = request(a, it.b);
         for (int i = 0; i < ns; ++i)
-            plan.entries[at + i] = make_int4(n, i | ns << 16, first, 0);
+            plan.entries[at + i] = Entry{it.b, it.chunk, i | ns << 16, first, rq.q0, rq.qlen, rq.len, 0};
     };
 #pragma unroll
     for (int i = 0; i < kPlanned; ++i)
@@ -244,6 +249,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8At
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
@@ -380,31 +390,31 @@ __device__ __forceinline__ bool row_tile(uint32_t my, const float *sc, float qs,
 __device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row row, int t0,
                                             const Sight see)
 {
-    uint32_t x[64];
-    ld32(my, *reinterpret_cast<uint32_t(*)[32]>(x));
-    ld32(my + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-    const Factors f(sc, qs);
-    const float ref = row.m == -INFINITY ? 0.f : row.m;
-    wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x));
-    wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32));
-    // the difference is taken from the rounded logit, as the reference is
-    float top = -INFINITY;
+    // sixteen logits at a time, twice: in loops, since what runs seldom is fetched anew
+    const auto logits = [&](int c, uint32_t(&x)[16]) {
+        ld16(my + c * 16, x);
+        const float k = sc[c] * qs, vs = sc[4 + c];
+        const int t = t0 + c * 16;
+        wait_ld16(x);
 #pragma unroll
-    for (int i = 0; i < 64; ++i) {
-        const float s = see.sees(t0 + i) ? fmaf(__uint_as_float(x[i]), f.k[i >> 4], f.vs[i >> 4]) : -INFINITY;
-        x[i] = __float_as_uint(s - ref);
-        top = fmaxf(top, s); // (a NaN loses)
+        for (int i = 0; i < 16; ++i)
+            x[i] = __float_as_uint(see.sees(t + i) ? fmaf(__uint_as_float(x[i]), k, vs) : -INFINITY);
+    };
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t x[16];
+        logits(c, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            top = fmaxf(top, __uint_as_float(x[i])); // (a NaN loses)
     }
-    const bool raise = row.m == -INFINITY ? top > -INFINITY : top - ref > kSlack;
+    const bool raise = row.m == -INFINITY ? top > -INFINITY : top - row.m > kSlack;
     if (__any_sync(0xffffffffu, raise)) {
         // the row's sums so far and its O under the new reference
         const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - top)) : 1.f;
-        const float d = raise ? top - ref : 0.f;
         row.m = raise ? top : row.m;
         row.l *= g;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-            x[i] = __float_as_uint(__uint_as_float(x[i]) - d);
 #pragma unroll 1
         for (int o = 0; o < o_cols; o += 16) {
             uint32_t p[16];
@@ -416,10 +426,15 @@ __device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_co
             st16(my_o + o, p);
         }
     }
+    const float ref = row.m == -INFINITY ? 0.f : row.m;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) { // (the weights lie over scores of groups before)
+        uint32_t x[16], p[8];
+        logits(c, x);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t p[8];
-        row.l = fmaf(weigh(x + c * 16, p), f.iv[c], row.l);
+        for (int i = 0; i < 16; ++i)
+            x[i] = __float_as_uint(__uint_as_float(x[i]) - ref);
+        row.l = fmaf(weigh(x, p), sc[8 + c], row.l);
         st8(my + c * 8, p);
     }
     return row;
@@ -489,17 +504,15 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
 
     grid_wait(); // the plan
-    Item it;
     const int n_entry = (int)(blockIdx.x / a.H_kv);
-    const int4 entry = plan.entries[n_entry]; // (inside the workspace, whatever it holds)
+    const int4 *at = reinterpret_cast<const int4 *>(plan.entries + n_entry); // (inside the workspace, whatever it holds)
+    const int4 e0 = at[0], e1 = at[1];
     if (n_entry >= plan.header[0])
         return;
-    const int split = entry.y & 0xFFFF, splits = entry.y >> 16;
-    if (!find_item(a, S::kItemRows, entry.x, &it))
-        return;
-    it.h = (int)(blockIdx.x % a.H_kv);
-    const int64_t slot0 = ((int64_t)(entry.z + split) * a.H_kv + it.h) * S::kItemRows; // (of a split item)
-    const Request rq = request(a, it.b);
+    const int split = e0.z & 0xFFFF, splits = e0.z >> 16;
+    const Item it{e0.x, e0.y, (int)(blockIdx.x % a.H_kv)};
+    const int64_t slot0 = ((int64_t)(e0.w + split) * a.H_kv + it.h) * S::kItemRows; // (of a split item)
+    const Request rq{e1.x, e1.y, e1.z, 0};
     const Span sp = span_of(a, S::kItemRows, rq, it.chunk);
     const int row0 = sp.row0, rows = sp.rows, p_first = sp.p_first, p_last = sp.p_last, kv_begin = sp.kv_begin,
               kv_end = sp.kv_end, all_from = sp.all_from, tb0 = sp.tb0;
@@ -570,31 +583,50 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         const int tile = warp >> 2; // of rows
         if (tile < live_tiles) {
         // ---------------------------------------------------------------- softmax
-        // this thread's row of Q, in two E4M3 parts; meanwhile the first codes come
+        // Q in two E4M3 parts; meanwhile the first codes come. Four lanes to a row, eight rows to an access (a row to a
+        // lane took 11000 cycles of a 128-column item: 32 cache lines an access).
         const int r = tid;
-        float qs;
+        float qs = 0.f;
         {
-            const bool live = r < rows;
-            const int rr = row0 + (live ? r : 0);
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                               (int64_t)(rq.q0 + rr / a.G) * a.q_st +
-                                                               (int64_t)(it.h * a.G + rr % a.G) * a.q_sh);
-            float amax = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i)
-                amax = fmaxf(amax, live ? amax8(src[i]) : 0.f);
-            float up;
-            split_scale(amax, up, qs);
-            up = a.scale < 0.f ? -up : up;
-            const uint32_t dst = base + S::kQ + tile * 2 * S::kQBytes + ((r & 127) >> 3) * S::kQAtoms + (r & 7) * 16;
-#pragma unroll 2
-            for (int i = 0; i < D / 16; ++i) {
-                uint32_t hi[2][2], lo[2][2];
+            const uint32_t dst = base + S::kQ + tile * 2 * S::kQBytes + (warp & 3) * 4 * S::kQAtoms + (lane >> 2) * 16 +
+                                 (lane >> 1 & 1) * 128 + (lane & 1) * 8;
+#pragma unroll 1
+            for (int g = 0; g < 4; g += 2) {
+                uint4 x[2][D / 32];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    split8(live ? src[2 * i + e] : make_uint4(0, 0, 0, 0), up, hi[e], lo[e]);
-                sts128(dst + i * 128, hi[0][0], hi[0][1], hi[1][0], hi[1][1]);
-                sts128(dst + S::kQBytes + i * 128, lo[0][0], lo[0][1], lo[1][0], lo[1][1]);
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = warp * 32 + (g + i) * 8 + (lane >> 2);
+                    const bool live = rr < rows;
+                    const int row = row0 + (live ? rr : 0);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                                       (int64_t)(rq.q0 + row / a.G) * a.q_st +
+                                                                       (int64_t)(it.h * a.G + row % a.G) * a.q_sh) + (lane & 3);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+                        x[i][c] = live ? src[4 * c] : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c)
+                        amax = fmaxf(amax, amax8(x[i][c]));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                    float up, down;
+                    split_scale(amax, up, down);
+                    up = a.scale < 0.f ? -up : up;
+                    // the row's factor for its own thread
+                    down = __shfl_sync(0xffffffffu, down, (lane & 7) * 4);
+                    qs = (lane >> 3) == g + i ? down : qs;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t hi[2], lo[2];
+                        split8(x[i][c], up, hi, lo);
+                        sts64(dst + (g + i) * S::kQAtoms + c * 256, hi[0], hi[1]);
+                        sts64(dst + (g + i) * S::kQAtoms + c * 256 + S::kQBytes, lo[0], lo[1]);
+                    }
+                }
             }
             fence_async_smem();
             mbar_arrive(q_full);
@@ -638,6 +670,9 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             float lse = 0.f, f = 1.f;
             if (splits == 1)
                 f = finish_row(m, l, a.sinks, head, &lse);
+            // 32 columns of the warp's 32 rows at a time, through what was Q: written a row to a lane, read and stored
+            // in whole rows (16-byte pieces XORed with the row, so that neither meets a bank twice)
+            const uint32_t room = base + S::kQ + tile * 2 * S::kQBytes + (warp & 3) * (2 * S::kQBytes / 4);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
@@ -649,24 +684,39 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                     for (int i = 0; i < 32; ++i)
                         x[i] = (bits >> i & 1) ? 0x7FC00000u : x[i];
                 }
-                if (!live)
-                    continue;
                 if (splits == 1) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + c * 32);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_bf16x2(__uint_as_float(x[i * 8 + 2 * e]) * f, __uint_as_float(x[i * 8 + 2 * e + 1]) * f);
-                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        sts128(room + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4), w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int wr = i * 8 + (lane >> 2), rr = warp * 32 + wr, row = row0 + rr; // four lanes to a row
+                        const uint4 v = lds128(room + wr * 64 + (((lane & 3) ^ (wr >> 1 & 3)) << 4));
+                        if (rr < rows)
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                       ((int64_t)(rq.q0 + row / a.G) * a.H + it.h * a.G + row % a.G) * D + c * 32 +
+                                                       (lane & 3) * 8) = v;
                     }
                 } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(plan.o + slot * D + c * 32);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        sts128(room + lane * 128 + ((i ^ (lane & 7)) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int wr = i * 4 + (lane >> 3), rr = warp * 32 + wr; // eight lanes to a row
+                        const uint4 v = lds128(room + wr * 128 + (((lane & 7) ^ (wr & 7)) << 4));
+                        if (rr < rows)
+                            *reinterpret_cast<uint4 *>(plan.o + (slot0 + rr) * D + c * 32 + (lane & 7) * 4) = v;
+                    }
                 }
+                __syncwarp();
             }
             if (live) {
                 if (splits > 1)
@@ -942,7 +992,7 @@ Sizes sizes_of(int64_t B, int64_t T, int G, int H_kv, int D, int NR, int sm_coun
     z.entries = z.items + parts;
     z.partials = 2 * parts;
     z.entries_at = 256;
-    z.splits_at = up256(z.entries_at + (size_t)z.entries * sizeof(int4));
+    z.splits_at = up256(z.entries_at + (size_t)z.entries * sizeof(Entry));
     z.ml_at = up256(z.splits_at + (size_t)parts * sizeof(int4));
     z.o_at = up256(z.ml_at + (size_t)z.partials * H_kv * item_rows * sizeof(float2));
     z.total = z.o_at + (size_t)z.partials * H_kv * item_rows * D * sizeof(float);
@@ -974,7 +1024,7 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     if (z.entries * a.H_kv > 0x7FFFFFFF)
         return cudaErrorInvalidValue;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const Plan plan{reinterpret_cast<int *>(ws), reinterpret_cast<int4 *>(ws + z.entries_at), reinterpret_cast<int4 *>(ws + z.splits_at),
+    const Plan plan{reinterpret_cast<int *>(ws), reinterpret_cast<Entry *>(ws + z.entries_at), reinterpret_cast<int4 *>(ws + z.splits_at),
                     reinterpret_cast<float2 *>(ws + z.ml_at), reinterpret_cast<float *>(ws + z.o_at), (int)z.items,
                     S::kItemRows};
     cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
