@@ -384,34 +384,53 @@ __device__ __forceinline__ bool row_tile(uint32_t my, const float *sc, float qs,
     return true;
 }
 
-// The same for any tile: positions that the row does not see are left out, and the
-// reference moves to the largest logit where that passes it by kSlack. O is at
-// rest. o_cols: O's columns (0 before the first product).
-__device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row row, int t0,
-                                            const Sight see)
+// Sixteen of the row's logits, -inf where it does not see the position.
+__device__ __forceinline__ void logits(uint32_t my, const float *sc, float qs, int t0, const Sight &see, int c, uint32_t (&x)[16])
 {
-    // sixteen logits at a time, twice: in loops, since what runs seldom is fetched anew
-    const auto logits = [&](int c, uint32_t(&x)[16]) {
-        ld16(my + c * 16, x);
-        const float k = sc[c] * qs, vs = sc[4 + c];
-        const int t = t0 + c * 16;
-        wait_ld16(x);
+    ld16(my + c * 16, x);
+    const float k = sc[c] * qs, vs = sc[4 + c];
+    const int t = t0 + c * 16;
+    wait_ld16(x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            x[i] = __float_as_uint(see.sees(t + i) ? fmaf(__uint_as_float(x[i]), k, vs) : -INFINITY);
-    };
+    for (int i = 0; i < 16; ++i)
+        x[i] = __float_as_uint(see.sees(t + i) ? fmaf(__uint_as_float(x[i]), k, vs) : -INFINITY);
+}
+
+// The largest of the row's 64 logits that it sees.
+__device__ __forceinline__ float largest(uint32_t my, const float *sc, float qs, int t0, const Sight &see)
+{
     float top = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t x[16];
-        logits(c, x);
+        logits(my, sc, qs, t0, see, c, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             top = fmaxf(top, __uint_as_float(x[i])); // (a NaN loses)
     }
+    return top;
+}
+
+// The next two run seldom, so they are short loops: code that is not in the
+// instruction cache costs some 12 cycles an instruction.
+
+// The row's first reference.
+__device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, int t0, const Sight see)
+{
+    return largest(my, sc, qs, t0, see);
+}
+
+// row_tile for any tile and any reference: the reference moves to the tile's largest
+// logit where that passes it by kSlack, and what was added up is rescaled (O is at
+// rest; o_cols: its columns, 0 before the first product); positions that the row
+// does not see are left out; the difference is taken from the rounded logit, as the
+// reference is.
+__device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row row, int t0,
+                                            const Sight see)
+{
+    const float top = largest(my, sc, qs, t0, see);
     const bool raise = row.m == -INFINITY ? top > -INFINITY : top - row.m > kSlack;
     if (__any_sync(0xffffffffu, raise)) {
-        // the row's sums so far and its O under the new reference
         const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - top)) : 1.f;
         row.m = raise ? top : row.m;
         row.l *= g;
@@ -430,7 +449,7 @@ __device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_co
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) { // (the weights lie over scores of groups before)
         uint32_t x[16], p[8];
-        logits(c, x);
+        logits(my, sc, qs, t0, see, c, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             x[i] = __float_as_uint(__uint_as_float(x[i]) - ref);
@@ -516,8 +535,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
     const Span sp = span_of(a, S::kItemRows, rq, it.chunk);
     const int row0 = sp.row0, rows = sp.rows, p_first = sp.p_first, p_last = sp.p_last, kv_begin = sp.kv_begin,
               kv_end = sp.kv_end, all_from = sp.all_from, tb0 = sp.tb0;
-    const int t_begin = (int)((long long)sp.tiles * split / splits);
-    const int t_end = (int)((long long)sp.tiles * (split + 1) / splits);
+    const int t_begin = sp.tiles * split / splits, t_end = sp.tiles * (split + 1) / splits; // (tiles < 2^25, splits <= 16)
     const int n = t_end - t_begin;
     const bool many = p_first != p_last;
     const int live_tiles = NR == 1 || rows <= kRows ? 1 : 2; // (a row tile without rows does nothing)
@@ -590,42 +608,44 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         {
             const uint32_t dst = base + S::kQ + tile * 2 * S::kQBytes + (warp & 3) * 4 * S::kQAtoms + (lane >> 2) * 16 +
                                  (lane >> 1 & 1) * 128 + (lane & 1) * 8;
+            const auto load = [&](int g, uint4(&x)[D / 32]) {
+                const int rr = warp * 32 + g * 8 + (lane >> 2);
+                const bool live = rr < rows;
+                const int row = row0 + (live ? rr : 0);
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                                   (int64_t)(rq.q0 + row / a.G) * a.q_st +
+                                                                   (int64_t)(it.h * a.G + row % a.G) * a.q_sh) + (lane & 3);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    x[c] = live ? src[4 * c] : make_uint4(0, 0, 0, 0);
+            };
+            uint4 x[D / 32], next[D / 32];
+            load(0, next);
 #pragma unroll 1
-            for (int g = 0; g < 4; g += 2) {
-                uint4 x[2][D / 32];
+            for (int g = 0; g < 4; ++g) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rr = warp * 32 + (g + i) * 8 + (lane >> 2);
-                    const bool live = rr < rows;
-                    const int row = row0 + (live ? rr : 0);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                                       (int64_t)(rq.q0 + row / a.G) * a.q_st +
-                                                                       (int64_t)(it.h * a.G + row % a.G) * a.q_sh) + (lane & 3);
+                for (int c = 0; c < D / 32; ++c)
+                    x[c] = next[c];
+                if (g < 3)
+                    load(g + 1, next);
+                float amax = 0.f;
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c)
-                        x[i][c] = live ? src[4 * c] : make_uint4(0, 0, 0, 0);
-                }
+                for (int c = 0; c < D / 32; ++c)
+                    amax = fmaxf(amax, amax8(x[c]));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                float up, down;
+                split_scale(amax, up, down);
+                up = a.scale < 0.f ? -up : up;
+                // the row's factor for its own thread
+                down = __shfl_sync(0xffffffffu, down, (lane & 7) * 4);
+                qs = (lane >> 3) == g ? down : qs;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float amax = 0.f;
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c)
-                        amax = fmaxf(amax, amax8(x[i][c]));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                    float up, down;
-                    split_scale(amax, up, down);
-                    up = a.scale < 0.f ? -up : up;
-                    // the row's factor for its own thread
-                    down = __shfl_sync(0xffffffffu, down, (lane & 7) * 4);
-                    qs = (lane >> 3) == g + i ? down : qs;
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t hi[2], lo[2];
-                        split8(x[i][c], up, hi, lo);
-                        sts64(dst + (g + i) * S::kQAtoms + c * 256, hi[0], hi[1]);
-                        sts64(dst + (g + i) * S::kQAtoms + c * 256 + S::kQBytes, lo[0], lo[1]);
-                    }
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t hi[2], lo[2];
+                    split8(x[c], up, hi, lo);
+                    sts64(dst + g * S::kQAtoms + c * 256, hi[0], hi[1]);
+                    sts64(dst + g * S::kQAtoms + c * 256 + S::kQBytes, lo[0], lo[1]);
                 }
             }
             fence_async_smem();
@@ -637,6 +657,10 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         const uint32_t s_ready = s_full + tile * 16, p_ready = p_full + tile * 16, o_done = v_empty + tile * 16;
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
         Row sums{r < rows ? -INFINITY : 0.f, 0.f}; // (a row that is not there, all zeros, moves no reference)
+        if (wait_warp(sc_full, 0) && wait_warp(s_ready, 0)) {
+            fence_after_sync();
+            sums.m = fmaxf(sums.m, row_first(my, scales, qs, tb0 + t_begin * kTile, see));
+        }
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             // the scales of the next eight tiles' blocks, this tile's scores
@@ -645,12 +669,14 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             fence_after_sync();
             const int t0 = tb0 + (t_begin + j) * kTile;
             const float *sc = scales + (j & 15) * 12;
-            if (!(see.all(t0) && see.all(t0 + 32) && row_tile(my + (j & 1) * kTile, sc, qs, sums))) {
+            const uint32_t my_s = my + (j & 1) * kTile;
+            const bool all = see.all(t0) && see.all(t0 + 32);
+            if (!(all && row_tile(my_s, sc, qs, sums))) {
                 // O is at rest once the last tile's product is done: the next one waits for this tile's weights
                 if (j > 0 && !wait_warp(o_done + ((j - 1) & 1) * 8, ((j - 1) >> 1) & 1))
                     break;
                 fence_after_sync();
-                sums = row_tile_moving(my + (j & 1) * kTile, my + S::kO, j > 0 ? D : 0, sc, qs, sums, t0, see);
+                sums = row_tile_moving(my_s, my + S::kO, j > 0 ? D : 0, sc, qs, sums, t0, see);
             }
             wait_st();
             fence_before_sync();
@@ -673,6 +699,13 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             // 32 columns of the warp's 32 rows at a time, through what was Q: written a row to a lane, read and stored
             // in whole rows (16-byte pieces XORed with the row, so that neither meets a bank twice)
             const uint32_t room = base + S::kQ + tile * 2 * S::kQBytes + (warp & 3) * (2 * S::kQBytes / 4);
+            __nv_bfloat16 *dst[4]; // of the four rows that the lane stores pieces of
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + warp * 32 + i * 8 + (lane >> 2);
+                dst[i] = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)(rq.q0 + row / a.G) * a.H + it.h * a.G + row % a.G) * D +
+                         (lane & 3) * 8;
+            }
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
@@ -696,12 +729,10 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int wr = i * 8 + (lane >> 2), rr = warp * 32 + wr, row = row0 + rr; // four lanes to a row
+                        const int wr = i * 8 + (lane >> 2), rr = warp * 32 + wr; // four lanes to a row
                         const uint4 v = lds128(room + wr * 64 + (((lane & 3) ^ (wr >> 1 & 3)) << 4));
                         if (rr < rows)
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                       ((int64_t)(rq.q0 + row / a.G) * a.H + it.h * a.G + row % a.G) * D + c * 32 +
-                                                       (lane & 3) * 8) = v;
+                            *reinterpret_cast<uint4 *>(dst[i] + c * 32) = v;
                     }
                 } else {
 #pragma unroll
