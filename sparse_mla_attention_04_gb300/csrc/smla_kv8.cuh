@@ -26,6 +26,12 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// Ends an mbarrier's use: its place may be set up anew.
+__device__ __forceinline__ void mbar_inval(uint32_t mbar)
+{
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(mbar) : "memory");
+}
+
 // A bounded wait of a whole converged warp (as umma::mbar_wait). The warp votes
 // on what it saw, so the control flow stays uniform: where lanes branch on their
 // own, coming together again costs 100 to 200 cycles a wait.
@@ -114,23 +120,25 @@ __device__ __forceinline__ float amax8(const uint4 &v)
 }
 
 // Eight bf16 values times `up` as E4M3 codes: hi = E4M3(x) and lo = E4M3(x - hi).
+// Below 2^8 the scaled values are exact in binary16 down to 2^-17, far below lo's
+// smallest step.
 __device__ __forceinline__ void split8(const uint4 &v, float up, uint32_t (&hi)[2], uint32_t (&lo)[2])
 {
+    const __nv_bfloat162 u = __float2bfloat162_rn(up);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), u));
+        const __half2 x = __floats2half2_rn(f.x, f.y);
+        h[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+        const __half2 back = static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[i], __NV_E4M3));
+        l[i] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E4M3);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * i]));
-        float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[2 * i + 1]));
-        a = make_float2(a.x * up, a.y * up);
-        b = make_float2(b.x * up, b.y * up);
-        hi[i] = (__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) & 0xFFFFu) |
-                ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
-        uint32_t f0, f1;
-        e4m3x4_to_f16x4(hi[i], f0, f1);
-        const float2 ha = __half22float2(*reinterpret_cast<const __half2 *>(&f0));
-        const float2 hb = __half22float2(*reinterpret_cast<const __half2 *>(&f1));
-        lo[i] = (__nv_cvt_float2_to_fp8x2(make_float2(a.x - ha.x, a.y - ha.y), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu) |
-                ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(b.x - hb.x, b.y - hb.y), __NV_SATFINITE, __NV_E4M3) << 16);
+        hi[i] = __byte_perm(h[2 * i], h[2 * i + 1], 0x5410);
+        lo[i] = __byte_perm(l[2 * i], l[2 * i + 1], 0x5410);
     }
 }
 

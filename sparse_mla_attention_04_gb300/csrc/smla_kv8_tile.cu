@@ -1,19 +1,22 @@
 // Attention over the block-scaled 8-bit cache for many query rows (prompts and
-// chunks of prompts, sm_103a): 128 query rows to a tile, both products on the
+// chunks of prompts, sm_103a): 128 query rows to a row tile, both products on the
 // tensor cores (tcgen05), scores and sums in tensor memory.
 //
-// A CTA takes 128 rows (token, head of the kv head's group) of one request and
-// kv head and walks over the visible positions in tiles of 64. Scores have two
-// buffers in tensor memory: while a tile's softmax runs, the next one's scores
-// are computed; two CTAs share an SM, so that the tensor cores have the other's
-// products meanwhile. Warps of a CTA:
-//   0-3  softmax, a row to a thread; the epilogue
-//   4-5  V's codes, expanded to binary16
-//   6    the blocks' codes by TMA as they lie in the cache; the blocks' scales
-//   7    issues the tensor-core products
-// (eight warps, so that both CTAs' threads have 128 registers). Their loops are
-// kept short, not unrolled: all run at once, and with long straight code each
-// instruction was fetched again every tile (8 to 20 cycles an instruction).
+// A unit of work is up to 128 or 256 rows (token, head of the kv head's group) of
+// one request and kv head. A CTA walks over its visible positions in tiles of 64.
+// Scores have two buffers in tensor memory for each row tile: while a tile's softmax
+// runs, the next one's scores are computed. Where a request's rows may fill more than
+// one row tile, a CTA has two and an SM one CTA: the row tiles share the copies of K
+// and V and V's expansion. With fewer rows a CTA has one and an SM two CTAs, so that
+// the tensor cores have the other's products meanwhile (with 40 rows to a request
+// the second row tile would have nothing). Warps of a CTA with NR row tiles:
+//   4 NR   softmax, a row to a thread; Q before and the epilogue behind it
+//   2 NR   V's codes, expanded to binary16
+//   NR     the blocks' codes by TMA as they lie in the cache (K and V by a warp each
+//          with two row tiles), the blocks' scales
+//   NR     the tensor-core products of a row tile each
+// The CTAs stay and take unit after unit; a kernel before lays out the work (see
+// Plan), one behind joins the units that several CTAs shared.
 //
 // S = Q K^T runs on the cache's codes as they are. q's bf16 values are carried
 // exactly by two E4M3 parts: scaled by a power of two to below 2^8, hi = E4M3(q)
@@ -24,18 +27,33 @@
 // expanded exactly to binary16: 8-bit weights would lose half of their bits.
 // The block scales enter as in the streaming kernel: K's multiplies the logits,
 // V's is folded into the exponent, p' = 2^(s + log2(vs) - m), and the
-// denominator adds p' / vs. A row's reference m moves, and what was added up
-// so far is rescaled, only when a logit passes it by 15 (p' <= 2^15 is inside
-// binary16, whose precision is relative): the scores are read once, with no
-// pass for the maximum before.
+// denominator adds p' / vs. A row's reference m is its largest logit of the first
+// tile that it sees. The weights of a tile are taken without looking for its maximum;
+// their sum (at most 2^15, so that each is inside binary16, whose precision is
+// relative) says whether m must move, and only then, which is seldom, the tile is
+// gone through again and what was added up so far is rescaled.
 //
 // Shared memory: the codes in TMA's swizzled rows; Q and the expanded V in 8-row
 // x 16-byte core matrices, written so that eight lanes fill one (no bank
 // conflict). Blocks outside the pool are zero-filled and not read.
+//
+// Bound and measured. A prompt of 8192 tokens, 32 heads on 8 kv heads of 128
+// columns: 0.440 ms, 1.25 PFLOP/s (66% of the measured bf16 rate; the products alone
+// keep the tensor pipe busy for two thirds of it, S being bound by what its operands
+// take from shared memory: 49 cycles for 64 columns against 32). Six chunks of 45 to
+// 701 tokens behind 2114 to 32001 positions, 16 heads on 2 kv heads of 64 columns,
+// blocks of 16: 236 us, 0.76 PFLOP/s; there a tile has half the products for the same
+// softmax, whose instructions (some 300 a tile and warp, with four exponentials a
+// cycle of a sub-core) take over half of the issue slots. What counted on the way:
+// short loops (eight to sixteen warps run five different pieces of code, and what is
+// not in the instruction cache costs some 12 cycles an instruction); products issued
+// under uniform control; the table and scales read and handed over eight tiles at a
+// time; K and V copied by a warp each; whole rows of Q and out to an access.
 #include "smla_kv8.cuh"
 #include "smla_umma.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace smla {
 
@@ -48,10 +66,18 @@ using namespace umma;
 
 constexpr int kRows = 128;  // of a row tile
 constexpr int kTile = 64;
-constexpr float kSlack = 8.0f;
-constexpr int kMaxSplits = 16; // of an item's positions
-constexpr int kWaves = 2;      // an item is split where it is more than this part of a CTA slot's share
-constexpr int kMinSplit = 16;  // tiles of a split, at least
+constexpr float kSlack = 8.0f; // (log2) a logit's distance above the reference that moves it, when it is looked at
+constexpr int kPieceCost = 13; // a unit's start and end, in tiles (measured: 14000 to 19000 cycles, a tile 1450 to 1550)
+constexpr int kMinPart = 22;  // a CTA's part of the work, in tiles, before more CTAs share it
+
+// The CTA's place in the work, and what else its warps share.
+struct Misc {
+    long long at, hi, total; // cost: where it is, where its part ends, all
+    int item, parts;
+    int units, next;         // units taken whole (0: the work is cut into parts), the next one
+    uint32_t tmem;
+    int any_nan;
+};
 
 template <int D, int NR> struct Shape {
     static constexpr int kItemRows = NR * kRows;
@@ -70,8 +96,14 @@ template <int D, int NR> struct Shape {
     static constexpr int kV = kQ + NR * 2 * kQBytes; // two stages
     static constexpr int kScales = kV + 2 * kVBytes; // 2 stages x 8 tiles x {c, log2 vs, 1 / vs} x 4 groups
     static constexpr int kBars = kScales + 2 * 8 * 4 * 12;
-    static constexpr int kMisc = kBars + 31 * 8;    // the tensor memory's address, a flag
-    static constexpr int kSmem = kMisc + 8;
+    // K landed / free (each stage); V's codes landed / free (two stages); scales of eight tiles written (two stages);
+    // drained (each row tile); Q written; of each row tile, two stages: scores ready, P and V ready, values done
+    static constexpr int kKFull = 0, kKEmpty = kKFull + kKStages, kCFull = kKEmpty + kKStages, kCEmpty = kCFull + 2,
+                         kScFull = kCEmpty + 2, kDrained = kScFull + 2, kQFull = kDrained + NR, kSFull = kQFull + 1,
+                         kPFull = kSFull + 2 * NR, kVEmpty = kPFull + 2 * NR, kBarriers = kVEmpty + 2 * NR;
+    static_assert(kBarriers <= 32, "a lane sets each up");
+    static constexpr int kMisc = kBars + (kBarriers + 1) / 2 * 16;
+    static constexpr int kSmem = kMisc + (int)sizeof(Misc);
     static constexpr uint32_t kTmem = 256;          // of a row tile: two S (P over each one's first half) and O
     static constexpr uint32_t kO = 2 * kTile;
     static constexpr uint32_t kIdescS = idesc(128, kTile, 0, 0, 0, 0);
@@ -79,19 +111,24 @@ template <int D, int NR> struct Shape {
     static_assert(NR == 2 || 2 * (kSmem + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
-// The plan of a call, in the workspace: how many entries and how many split items
-// there are; the entries, the longest first; the split items {request, chunk,
-// splits, first partial}; their partial sums.
-struct Entry {
-    int b, chunk, split, first;   // split | splits << 16; first partial
-    int q0, qlen, len, none;      // the request
+// The plan of a call, in the workspace. A unit is an item's kv head. Where the
+// longest unit is at most a third of a CTA's share, the CTAs take whole units, the
+// longest first, as they are free (a prompt of 8192 tokens with 8 kv heads: 440 us,
+// cut into equal parts 460); otherwise the units laid end to end are cut into equal
+// parts, one for each CTA, wherever in a unit that falls (ragged chunks: 236 us, in
+// pieces of at most half of a share, the longest first, 276).
+struct PlannedItem {
+    int b, chunk, tiles, none;
+    int q0, qlen, len, none2; // the request
 };
 struct Plan {
-    int *header;
-    Entry *entries;
-    int4 *splits;
-    float2 *ml; // [partials][H_kv][item_rows]
-    float *o;   // [partials][H_kv][item_rows][D]
+    int *head;       // units taken whole (0: cut); how many are taken
+    long long *cost; // [items + 1]: of the items before, for one kv head, in tiles
+    PlannedItem *items;
+    int *order;      // [items]: the longest first
+    int4 *dir;       // [CTAs]: the unit that it begins and others end, {last CTA (-1: none), request, chunk, head}
+    float2 *ml; // [2 CTAs][item_rows]
+    float *o;   // [2 CTAs][item_rows][D]
     int n_items, item_rows;
 };
 
@@ -143,107 +180,93 @@ __device__ __forceinline__ Span span_of(const Kv8AttnArgs &a, int item_rows, con
     return s;
 }
 
-// Plans a call, by one block: items that are longer than their part of a CTA
-// slot's share are split, and the entries are sorted by length (64 classes), so
-// that ragged requests fill the GPU evenly whatever their order. Where an entry
-// or a partial stands does not change what is computed from it. The first
-// kPlanned items of a thread stay in registers.
-constexpr int kPlanThreads = 1024, kPlanned = 4;
-__global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8AttnArgs a, const Plan plan, int slots)
+// Plans a call, by one block. Where a unit stands in the order, and which CTA takes
+// it, does not change what is computed from it.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) kv8_tile_plan_kernel(const Kv8AttnArgs a, const Plan plan, int ctas)
 {
-    __shared__ long long s_total;
-    __shared__ int s_most, s_hist[64], s_parts, s_split_items;
+    __shared__ long long s_warp[kPlanThreads / 32];
+    __shared__ int s_most, s_real, s_class[64];
     grid_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid == 0) {
-        s_total = 0;
-        s_most = 0;
-        s_parts = 0;
-        s_split_items = 0;
-    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < 64)
-        s_hist[tid] = 0;
+        s_class[tid] = 0;
+    if (tid == 0)
+        s_most = s_real = 0;
     __syncthreads();
-    auto tiles_of = [&](int n) { // -1: no such item
+    long long before = 0;
+    for (int n0 = 0; n0 < plan.n_items; n0 += kPlanThreads) {
+        const int n = n0 + tid;
         Item it;
-        return find_item(a, plan.item_rows, n, &it) ? span_of(a, plan.item_rows, request(a, it.b), it.chunk).tiles : -1;
+        long long cost = 0;
+        if (n < plan.n_items && find_item(a, plan.item_rows, n, &it)) {
+            const Request rq = request(a, it.b);
+            const int tiles = span_of(a, plan.item_rows, rq, it.chunk).tiles;
+            cost = max(1, tiles) + kPieceCost;
+            plan.items[n] = PlannedItem{it.b, it.chunk, tiles, 0, rq.q0, rq.qlen, rq.len, 0};
+        }
+        long long to = cost;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, to, d);
+            to += lane >= d ? x : 0;
+        }
+        if (lane == 31)
+            s_warp[warp] = to;
+        __syncthreads();
+        long long all = 0;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const long long x = s_warp[w];
+            to += w < warp ? x : 0;
+            all += x;
+        }
+        if (n < plan.n_items)
+            plan.cost[n] = before + to - cost;
+        const int most = __reduce_max_sync(0xffffffffu, (int)cost), real = __popc(__ballot_sync(0xffffffffu, cost > 0));
+        if (lane == 0 && real > 0) {
+            atomicMax(&s_most, most);
+            atomicAdd(&s_real, real);
+        }
+        before += all;
+        __syncthreads();
+    }
+    const int most = s_most;
+    const bool whole = 3ll * most * ctas <= before * a.H_kv && (long long)s_real * a.H_kv < INT_MAX / 2;
+    if (tid == 0) {
+        plan.cost[plan.n_items] = before;
+        plan.head[0] = whole ? s_real * a.H_kv : 0;
+        plan.head[1] = 0;
+    }
+    if (!whole)
+        return;
+    // sorted by length, in 64 classes (a thread reads what it wrote)
+    const auto class_of = [&](int n) {
+        const int tiles = plan.items[n].tiles;
+        return 63 - (int)((max(1, tiles) + kPieceCost) * 63ll / most);
     };
-    int kept[kPlanned];
-    long long sum = 0;
-    int most = 0;
-#pragma unroll
-    for (int i = 0; i < kPlanned; ++i) {
-        const int n = tid + i * kPlanThreads;
-        kept[i] = n < plan.n_items ? tiles_of(n) : -1;
-        sum += max(kept[i], 0);
-        most = max(most, kept[i]);
-    }
-    for (int n = tid + kPlanned * kPlanThreads; n < plan.n_items; n += kPlanThreads) {
-        const int tiles = tiles_of(n);
-        sum += max(tiles, 0);
-        most = max(most, tiles);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-        atomicAdd(reinterpret_cast<unsigned long long *>(&s_total), (unsigned long long)sum);
-        atomicMax(&s_most, most);
-    }
-    __syncthreads();
-    const int target = (int)max((long long)kMinSplit, (s_total * a.H_kv + (long long)kWaves * slots - 1) / ((long long)kWaves * slots));
-    const int longest = max(1, min(s_most, target));
-    auto splits = [&](int tiles) { return min(kMaxSplits, max(1, (tiles + target - 1) / target)); };
-    auto bucket = [&](int tiles) { return 63 - min(63, (int)((long long)(tiles / splits(tiles)) * 63 / longest)); };
-    auto count = [&](int tiles) {
-        if (tiles >= 0)
-            atomicAdd(&s_hist[bucket(tiles)], splits(tiles));
+    const auto real = [&](int n) {
+        Item it;
+        return find_item(a, plan.item_rows, n, &it);
     };
-#pragma unroll
-    for (int i = 0; i < kPlanned; ++i)
-        count(kept[i]);
-    for (int n = tid + kPlanned * kPlanThreads; n < plan.n_items; n += kPlanThreads)
-        count(tiles_of(n));
+    for (int n = tid; n < plan.n_items; n += kPlanThreads)
+        if (real(n))
+            atomicAdd(&s_class[class_of(n)], 1);
     __syncthreads();
     if (tid < 32) { // the classes' first places
-        const int x0 = s_hist[2 * lane], x1 = s_hist[2 * lane + 1];
+        const int x0 = s_class[2 * lane], x1 = s_class[2 * lane + 1];
         int to = x0 + x1;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, to, d);
             to += lane >= d ? y : 0;
         }
-        s_hist[2 * lane] = to - x0 - x1;
-        s_hist[2 * lane + 1] = to - x1;
-        if (lane == 31)
-            plan.header[0] = to;
+        s_class[2 * lane] = to - x0 - x1;
+        s_class[2 * lane + 1] = to - x1;
     }
     __syncthreads();
-    auto place = [&](int n, int tiles) {
-        if (tiles < 0)
-            return;
-        const int ns = splits(tiles);
-        const int at = atomicAdd(&s_hist[bucket(tiles)], ns);
-        int first = 0;
-        Item it;
-        (void)find_item(a, plan.item_rows, n, &it);
-        if (ns > 1) {
-            first = atomicAdd(&s_parts, ns);
-            plan.splits[atomicAdd(&s_split_items, 1)] = make_int4(it.b, it.chunk, ns, first);
-        }
-        const Request rq = request(a, it.b);
-        for (int i = 0; i < ns; ++i)
-            plan.entries[at + i] = Entry{it.b, it.chunk, i | ns << 16, first, rq.q0, rq.qlen, rq.len, 0};
-    };
-#pragma unroll
-    for (int i = 0; i < kPlanned; ++i)
-        place(tid + i * kPlanThreads, kept[i]);
-    for (int n = tid + kPlanned * kPlanThreads; n < plan.n_items; n += kPlanThreads)
-        place(n, tiles_of(n));
-    __syncthreads();
-    if (tid == 0)
-        plan.header[1] = s_split_items;
+    for (int n = tid; n < plan.n_items; n += kPlanThreads)
+        if (real(n))
+            plan.order[atomicAdd(&s_class[class_of(n)], 1)] = n;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
@@ -417,7 +440,20 @@ __device__ __forceinline__ float largest(uint32_t my, const float *sc, float qs,
 // The row's first reference.
 __device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, int t0, const Sight see)
 {
-    return largest(my, sc, qs, t0, see);
+    if (!see.all(t0) || !see.all(t0 + 32))
+        return largest(my, sc, qs, t0, see);
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t x[16];
+        ld16(my + c * 16, x);
+        const float k = sc[c] * qs, vs = sc[4 + c];
+        wait_ld16(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            top = fmaxf(top, fmaf(__uint_as_float(x[i]), k, vs));
+    }
+    return top;
 }
 
 // row_tile for any tile and any reference: the reference moves to the tile's largest
@@ -499,95 +535,78 @@ __device__ __noinline__ uint32_t nan_columns(const Kv8AttnArgs &a, const Item &i
     return bits;
 }
 
+// A part of a unit, as much of it as a CTA's part of the work holds.
+struct Piece {
+    Item it;
+    Request rq;
+    int t_begin, t_end; // tiles
+    bool whole;
+    int64_t slot0;      // where the partial sums of its rows go
+};
+
+// Works on a piece, by the whole block; false where a wait gave up. The barriers
+// were last used for a piece before (not the first time).
 template <int D, int NR>
-__global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
-                                                               const __grid_constant__ CUtensorMap v_map,
-                                                               const Kv8AttnArgs a, const Plan plan)
+__device__ __forceinline__ bool work_on(const CUtensorMap &k_map, const CUtensorMap &v_map, const Kv8AttnArgs &a, const Plan &plan,
+                                        uint8_t *smem, const Piece &piece, bool first)
 {
     using S = Shape<D, NR>;
-    extern __shared__ __align__(1024) uint8_t smem[]; // (the swizzle goes by address)
-    int *s_any_nan = reinterpret_cast<int *>(smem + S::kMisc + 4);
+    Misc *misc = reinterpret_cast<Misc *>(smem + S::kMisc);
+    int *s_any_nan = &misc->any_nan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t base = smem_u32(smem);
-    if (base & 1023u) { // a layout that the swizzle does not fit
-        if (tid == 0)
-            atomicOr(&g_kv8_error, 1);
-        return;
-    }
-    const uint32_t bars = base + S::kBars;
-    // K landed / free (up to four stages of two tiles); V's codes landed / free (two stages); scales of eight tiles written
-    // (two stages); drained (each row tile); Q written; of each row tile, two stages: scores ready, P and V ready,
-    // values done
-    const uint32_t k_full = bars, k_empty = bars + 32, c_full = bars + 64, c_empty = bars + 80, sc_full = bars + 96,
-                   drained = bars + 112, q_full = bars + 128, s_full = bars + 136, p_full = bars + 168, v_empty = bars + 200;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kMisc);
-
-    grid_wait(); // the plan
-    const int n_entry = (int)(blockIdx.x / a.H_kv);
-    const int4 *at = reinterpret_cast<const int4 *>(plan.entries + n_entry); // (inside the workspace, whatever it holds)
-    const int4 e0 = at[0], e1 = at[1];
-    if (n_entry >= plan.header[0])
-        return;
-    const int split = e0.z & 0xFFFF, splits = e0.z >> 16;
-    const Item it{e0.x, e0.y, (int)(blockIdx.x % a.H_kv)};
-    const int64_t slot0 = ((int64_t)(e0.w + split) * a.H_kv + it.h) * S::kItemRows; // (of a split item)
-    const Request rq{e1.x, e1.y, e1.z, 0};
+    const uint32_t base = smem_u32(smem), bars = base + S::kBars;
+    const uint32_t k_full = bars + 8 * S::kKFull, k_empty = bars + 8 * S::kKEmpty, c_full = bars + 8 * S::kCFull,
+                   c_empty = bars + 8 * S::kCEmpty, sc_full = bars + 8 * S::kScFull, drained = bars + 8 * S::kDrained,
+                   q_full = bars + 8 * S::kQFull, s_full = bars + 8 * S::kSFull, p_full = bars + 8 * S::kPFull,
+                   v_empty = bars + 8 * S::kVEmpty;
+    const Item it = piece.it;
+    const Request rq = piece.rq;
+    const int64_t slot0 = piece.slot0;
     const Span sp = span_of(a, S::kItemRows, rq, it.chunk);
     const int row0 = sp.row0, rows = sp.rows, p_first = sp.p_first, p_last = sp.p_last, kv_begin = sp.kv_begin,
               kv_end = sp.kv_end, all_from = sp.all_from, tb0 = sp.tb0;
-    const int t_begin = sp.tiles * split / splits, t_end = sp.tiles * (split + 1) / splits; // (tiles < 2^25, splits <= 16)
-    const int n = t_end - t_begin;
+    const int t_begin = piece.t_begin, n = piece.t_end - t_begin;
     const bool many = p_first != p_last;
     const int live_tiles = NR == 1 || rows <= kRows ? 1 : 2; // (a row tile without rows does nothing)
 
-    if (n <= 0) { // nothing to see here
+    if (n <= 0) { // nothing to see (a whole unit)
         if (tid < rows) {
             const int64_t t = rq.q0 + (row0 + tid) / a.G;
             const int head = it.h * a.G + (row0 + tid) % a.G;
-            if (splits > 1) {
-                plan.ml[slot0 + tid] = make_float2(-INFINITY, 0.f);
-            } else {
-                float lse;
-                finish_row(-INFINITY, 0.f, a.sinks, head, &lse);
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D);
-                for (int i = 0; i < D / 8; ++i)
-                    dst[i] = make_uint4(0, 0, 0, 0);
-                if (a.lse)
-                    a.lse[t * a.H + head] = lse;
-            }
+            float lse;
+            finish_row(-INFINITY, 0.f, a.sinks, head, &lse);
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D);
+            for (int i = 0; i < D / 8; ++i)
+                dst[i] = make_uint4(0, 0, 0, 0);
+            if (a.lse)
+                a.lse[t * a.H + head] = lse;
         }
-        return;
+        return true;
     }
 
-    if (tid == 0) {
-        *s_any_nan = 0;
+    if (tid < S::kBarriers) { // a barrier to a lane
         const int pages = kTile / min(kTile, a.block_size);
-        for (int i = 0; i < S::kKStages; ++i) {
-            mbar_init(k_full + 8 * i, 2 * pages);
-            mbar_init(k_empty + 8 * i, live_tiles);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(c_full + 8 * i, pages);
-            mbar_init(c_empty + 8 * i, S::kVWarps);
-            mbar_init(sc_full + 8 * i, 1);
-            mbar_init(drained + 8 * i, 1);
-        }
-        for (int i = 0; i < 2 * NR; ++i) {
-            mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, kRows + S::kVWarps);
-            mbar_init(v_empty + 8 * i, 1);
-        }
-        mbar_init(q_full, live_tiles * kRows);
+        const int count = tid < S::kKEmpty    ? 2 * pages
+                          : tid < S::kCFull   ? live_tiles
+                          : tid < S::kCEmpty  ? pages
+                          : tid < S::kScFull  ? S::kVWarps
+                          : tid == S::kQFull  ? live_tiles * kRows
+                          : tid < S::kPFull   ? 1
+                          : tid < S::kVEmpty  ? kRows + S::kVWarps
+                                              : 1;
+        if (!first)
+            mbar_inval(bars + 8 * tid);
+        mbar_init(bars + 8 * tid, count);
         mbar_init_fence();
+        if (tid == 0)
+            *s_any_nan = 0;
     }
-    if (warp == S::kMma)
-        alloc(smem_u32(tmem_slot), NR * S::kTmem);
     const float scale_log2 = fabsf(a.scale) * kLog2e; // the sign goes into q
 
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = misc->tmem;
     bool ok = true;
     // a bounded wait, by whole warps
     auto wait_warp = [&](uint32_t bar, uint32_t parity) {
@@ -597,10 +616,9 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         return ok;
     };
 
-    if (warp < S::kV0) {
-        const int tile = warp >> 2; // of rows
-        if (tile < live_tiles) {
+    if (warp < 4 * live_tiles) {
         // ---------------------------------------------------------------- softmax
+        const int tile = warp >> 2; // of rows
         // Q in two E4M3 parts; meanwhile the first codes come. Four lanes to a row, eight rows to an access (a row to a
         // lane took 11000 cycles of a 128-column item: 32 cache lines an access).
         const int r = tid;
@@ -694,7 +712,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             const int64_t slot = slot0 + r;
             const bool nans = many && *s_any_nan;
             float lse = 0.f, f = 1.f;
-            if (splits == 1)
+            if (piece.whole)
                 f = finish_row(m, l, a.sinks, head, &lse);
             // 32 columns of the warp's 32 rows at a time, through what was Q: written a row to a lane, read and stored
             // in whole rows (16-byte pieces XORed with the row, so that neither meets a bank twice)
@@ -717,7 +735,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                     for (int i = 0; i < 32; ++i)
                         x[i] = (bits >> i & 1) ? 0x7FC00000u : x[i];
                 }
-                if (splits == 1) {
+                if (piece.whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
@@ -750,13 +768,14 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
                 __syncwarp();
             }
             if (live) {
-                if (splits > 1)
+                if (!piece.whole)
                     plan.ml[slot] = make_float2(m, l);
                 else if (a.lse)
                     a.lse[t * a.H + head] = lse;
             }
         }
-        }
+    } else if (warp < S::kV0) {
+        // a row tile without rows
     } else if (warp < S::kLoader) {
         // ---------------------------------------------------------------- V
         constexpr int kTurns = kTile / S::kVWarps / 8;
@@ -879,6 +898,9 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         for (int j = max(0, issued - S::kKStages); j < issued; ++j)
             if (!mbar_wait(k_full + (j & (S::kKStages - 1)) * 8, (j / S::kKStages) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
+        // nor does the news that K is free, which comes from the tensor core and which nobody waits for
+        for (int j = max(0, issued - S::kKStages); ok && j < issued; ++j)
+            (void)wait_warp(k_empty + (j & (S::kKStages - 1)) * 8, (j / S::kKStages) & 1);
         for (int j = max(0, v_issued - 2); j < v_issued; ++j)
             if (!mbar_wait(c_full + (j & 1) * 8, (j >> 1) & 1) && lane == 0)
                 atomicOr(&g_kv8_error, 2);
@@ -940,93 +962,198 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
     }
     __syncwarp();
     fence_before_sync();
-    __syncthreads();
-    if (warp == S::kMma)
-        dealloc(tmem, NR * S::kTmem);
+    return ok;
 }
 
-// Joins the splits of the split items' rows, a warp to a row; the blocks share
-// out the items by eight rows.
 template <int D, int NR>
-__global__ void __launch_bounds__(256) kv8_tile_join_kernel(const Kv8AttnArgs a, const Plan plan)
+__global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
+                                                                                             const __grid_constant__ CUtensorMap v_map,
+                                                                                             const Kv8AttnArgs a, const Plan plan)
 {
-    constexpr int kD = D / 32;
-    constexpr int kItemRows = NR * kRows, kEights = kItemRows / 8;
-    grid_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int work = plan.header[1] * a.H_kv * kEights; // (partials are fewer than 2^31 / 256)
-    for (int x = blockIdx.x; x < work; x += gridDim.x) {
-        const int4 info = plan.splits[x / kEights / a.H_kv];
-        const int splits = info.z, h = x / kEights % a.H_kv;
-        const Request rq = request(a, info.x);
-        const int row0 = info.y * kItemRows;
-        const int rows = min(kItemRows, rq.qlen * a.G - row0);
-        const int r = warp + 8 * (int)(x % kEights);
-        if (r < rows) {
-            auto slot = [&](int s) { return ((int64_t)(info.w + s) * a.H_kv + h) * kItemRows + r; };
-            const float2 mine = lane < splits ? plan.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
-            const float m = warp_max(mine.x);
-            const float f_mine = mine.x == -INFINITY ? 1.f : ex2_approx(mine.x - m);
-            // nothing seen: no sums were written
-            const unsigned seen = __ballot_sync(0xffffffffu, lane < splits && !(mine.x == -INFINITY && mine.y == 0.f));
-            float acc[kD], l = 0.f;
-#pragma unroll
-            for (int i = 0; i < kD; ++i)
-                acc[i] = 0.f;
-#pragma unroll 8
-            for (int s = 0; s < splits; ++s) {
-                float2 v[kD / 2];
-                const float2 *src = reinterpret_cast<const float2 *>(plan.o + slot(s) * D + lane * kD);
-#pragma unroll
-                for (int i = 0; i < kD / 2; ++i)
-                    v[i] = seen >> s & 1 ? src[i] : make_float2(0.f, 0.f);
-                const float sl = __shfl_sync(0xffffffffu, mine.y, s), f = __shfl_sync(0xffffffffu, f_mine, s);
-                l += sl * f;
-#pragma unroll
-                for (int i = 0; i < kD / 2; ++i) {
-                    acc[2 * i] += v[i].x * f;
-                    acc[2 * i + 1] += v[i].y * f;
-                }
-            }
-            const int64_t t = rq.q0 + (row0 + r) / a.G;
-            const int head = h * a.G + (row0 + r) % a.G;
-            float lse;
-            const float f = finish_row(m, l, a.sinks, head, &lse);
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + lane * kD;
-#pragma unroll
-            for (int i = 0; i < kD; i += 2)
-                *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
-            if (a.lse && lane == 0)
-                a.lse[t * a.H + head] = lse;
+    using S = Shape<D, NR>;
+    extern __shared__ __align__(1024) uint8_t smem[]; // (the swizzle goes by address)
+    Misc *misc = reinterpret_cast<Misc *>(smem + S::kMisc);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const bool fits = (smem_u32(smem) & 1023u) == 0; // otherwise a layout that the swizzle does not fit
+    if (!fits && tid == 0)
+        atomicOr(&g_kv8_error, 1);
+    if (warp == S::kMma)
+        alloc(smem_u32(&misc->tmem), NR * S::kTmem);
+    grid_wait(); // the plan
+    if (tid == 0) {
+        plan.dir[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        const long long total = plan.cost[plan.n_items] * a.H_kv;
+        const int parts = (int)min((long long)gridDim.x, max(1ll, (total + kMinPart - 1) / kMinPart));
+        const bool mine = fits && (int)blockIdx.x < parts;
+        misc->total = total;
+        misc->units = fits ? plan.head[0] : 0;
+        misc->next = misc->units > 0 ? atomicAdd(plan.head + 1, 1) : 0;
+        misc->parts = parts;
+        misc->at = mine ? total * blockIdx.x / parts : 0;
+        misc->hi = mine ? total * (blockIdx.x + 1) / parts : 0;
+        int lo = 0, hi = plan.n_items - 1; // the last item that begins at or before: items that are none cost nothing
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (plan.cost[mid] * a.H_kv <= misc->at)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
+        misc->item = lo;
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    bool first = true;
+    const int units = misc->units;
+    while (units > 0 ? misc->next < units : misc->at < misc->hi) {
+        Piece piece;
+        int s0 = 0, s1 = 1, item;
+        int last = -1; // the CTA that ends the unit
+        long long end = 0;
+        if (units > 0) {
+            const int u = misc->next;
+            item = plan.order[u / a.H_kv];
+            piece.it.h = u % a.H_kv;
+        } else {
+            const long long at = misc->at;
+            item = misc->item;
+            long long base = plan.cost[item] * a.H_kv, next = plan.cost[item + 1] * a.H_kv;
+            while (at >= next) {
+                base = next;
+                next = plan.cost[++item + 1] * a.H_kv;
+            }
+            const int cost = (int)((next - base) / a.H_kv);
+            piece.it.h = (int)((at - base) / cost);
+            const long long unit = base + (long long)piece.it.h * cost;
+            end = min(misc->hi, unit + cost);
+            s0 = (int)max(0ll, at - unit - kPieceCost);
+            s1 = (int)max(0ll, end - unit - kPieceCost);
+            last = (int)(((unit + cost) * misc->parts - 1) / misc->total);
+        }
+        const int4 *in = reinterpret_cast<const int4 *>(plan.items + item);
+        const int4 i0 = in[0], i1 = in[1];
+        const int tiles = i0.z;
+        piece.it.b = i0.x;
+        piece.it.chunk = i0.y;
+        piece.rq = Request{i1.x, i1.y, i1.z, 0};
+        if (units > 0)
+            s1 = max(1, tiles);
+        piece.t_begin = s0;
+        piece.t_end = min(s1, tiles);
+        piece.whole = s0 == 0 && s1 == max(1, tiles);
+        piece.slot0 = (2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0)) * S::kItemRows;
+        __syncthreads(); // all have read the place
+        if (tid == 0) {
+            misc->at = end;
+            misc->item = item;
+            if (s0 == 0 && s0 < s1 && !piece.whole) // (the thread that wrote it above)
+                plan.dir[blockIdx.x] = make_int4(last, piece.it.b, piece.it.chunk, piece.it.h);
+        }
+        if (units > 0 && tid == S::kV0 * 32)
+            misc->next = atomicAdd(plan.head + 1, 1);
+        if (s0 < s1) {
+            const bool ok = work_on<D, NR>(k_map, v_map, a, plan, smem, piece, first);
+            first = first && piece.t_end <= s0;
+            if (!ok) { // (every warp that waited on that gives up, too)
+                misc->hi = 0;
+                misc->next = INT_MAX;
+            }
+        }
+        fence_async_smem(); // what was written or read here, before copies land there again
+        __syncthreads();
+        fence_after_sync();
+    }
+    if (warp == S::kMma)
+        dealloc(misc->tmem, NR * S::kTmem);
+}
+
+// Joins the partial sums of the units that several CTAs share: a row to D / 4
+// lanes, four rows of a lane at a time, whose loads are on their way together.
+constexpr int kJoinWarps = 8, kJoinRows = 4;
+template <int D, int NR>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv8_tile_join_kernel(const Kv8AttnArgs a, const Plan plan)
+{
+    constexpr int kItemRows = NR * kRows, kLanes = D / 4, kPer = 32 / kLanes; // lanes to a row, rows to a warp's access
+    grid_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
+    const int4 u = plan.dir[c0];
+    if (u.x <= c0)
+        return;
+    const Request rq = request(a, u.y);
+    const int row0 = u.z * kItemRows, rows = min(kItemRows, rq.qlen * a.G - row0);
+    const int first = (blockIdx.y * kJoinWarps + warp) * kPer * kJoinRows + lane / kLanes, part = lane % kLanes;
+    const auto slot = [&](int c, int k) { // (rows that are not there: another one's, not stored)
+        return (2 * (int64_t)c + (c == c0)) * kItemRows + min(first + k * kPer, rows - 1);
+    };
+    float m[kJoinRows], l[kJoinRows];
+    float4 acc[kJoinRows];
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int c = c0; c <= u.x; ++c)
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k)
+            m[k] = fmaxf(m[k], plan.ml[slot(c, k)].x);
+    for (int c = c0; c <= u.x; ++c) {
+        float2 ml[kJoinRows];
+        float4 v[kJoinRows];
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            ml[k] = plan.ml[slot(c, k)];
+            v[k] = *reinterpret_cast<const float4 *>(plan.o + slot(c, k) * D + part * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            // one that saw nothing has m = -inf; its sums are 0, or NaN from a NaN logit
+            const float f = ml[k].x == -INFINITY ? 1.f : ex2_approx(ml[k].x - m[k]);
+            l[k] += ml[k].y * f;
+            acc[k].x += v[k].x * f;
+            acc[k].y += v[k].y * f;
+            acc[k].z += v[k].z * f;
+            acc[k].w += v[k].w * f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        const int r = first + k * kPer;
+        if (r >= rows)
+            break;
+        const int64_t t = rq.q0 + (row0 + r) / a.G;
+        const int head = u.w * a.G + (row0 + r) % a.G;
+        float lse;
+        const float f = finish_row(m[k], l[k], a.sinks, head, &lse);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D + part * 4) =
+            make_uint2(pack_bf16x2(acc[k].x * f, acc[k].y * f), pack_bf16x2(acc[k].z * f, acc[k].w * f));
+        if (a.lse && part == 0)
+            a.lse[t * a.H + head] = lse;
     }
 }
 
 struct Sizes {
-    int64_t items, entries, partials; // entries and partials: for each kv head
-    size_t entries_at, splits_at, ml_at, o_at, total;
+    int64_t items;
+    size_t cost_at, items_at, order_at, dir_at, ml_at, o_at, total;
 };
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int slots_of(int NR, int sm_count) { return (NR == 1 ? 2 : 1) * std::max(sm_count, 1); } // CTAs at a time
 
-// Items: each request's last chunk may be short. Entries: an item, and one more
-// for each whole part of the shares that its length holds. Split items: no more
-// than there are parts; their partials at most twice as many.
-Sizes sizes_of(int64_t B, int64_t T, int G, int H_kv, int D, int NR, int sm_count)
+Sizes sizes_of(int64_t B, int64_t T, int G, int D, int NR, int sm_count)
 {
     Sizes z;
-    const int64_t parts = (int64_t)kWaves * slots_of(NR, sm_count) / H_kv + 1;
-    const int64_t item_rows = NR * kRows;
-    z.items = T * G / item_rows + B;
-    z.entries = z.items + parts;
-    z.partials = 2 * parts;
-    z.entries_at = 256;
-    z.splits_at = up256(z.entries_at + (size_t)z.entries * sizeof(Entry));
-    z.ml_at = up256(z.splits_at + (size_t)parts * sizeof(int4));
-    z.o_at = up256(z.ml_at + (size_t)z.partials * H_kv * item_rows * sizeof(float2));
-    z.total = z.o_at + (size_t)z.partials * H_kv * item_rows * D * sizeof(float);
+    const size_t rows = NR * kRows, partials = 2 * (size_t)slots_of(NR, sm_count);
+    z.items = T * G / (int64_t)rows + B; // each request's last chunk may be short
+    z.cost_at = 256;
+    z.items_at = up256(z.cost_at + (size_t)(z.items + 1) * sizeof(long long));
+    z.order_at = up256(z.items_at + (size_t)z.items * sizeof(PlannedItem));
+    z.dir_at = up256(z.order_at + (size_t)z.items * sizeof(int));
+    z.ml_at = up256(z.dir_at + (size_t)slots_of(NR, sm_count) * sizeof(int4));
+    z.o_at = up256(z.ml_at + partials * rows * sizeof(float2));
+    z.total = z.o_at + partials * rows * D * sizeof(float);
     return z;
 }
 
@@ -1051,37 +1178,44 @@ template <int D, int NR>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
     using S = Shape<D, NR>;
-    const Sizes z = sizes_of(a.B, a.T, a.G, a.H_kv, D, NR, sm_count);
-    if (z.entries * a.H_kv > 0x7FFFFFFF)
-        return cudaErrorInvalidValue;
+    const Sizes z = sizes_of(a.B, a.T, a.G, D, NR, sm_count);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const Plan plan{reinterpret_cast<int *>(ws), reinterpret_cast<Entry *>(ws + z.entries_at), reinterpret_cast<int4 *>(ws + z.splits_at),
-                    reinterpret_cast<float2 *>(ws + z.ml_at), reinterpret_cast<float *>(ws + z.o_at), (int)z.items,
+    const Plan plan{reinterpret_cast<int *>(ws),
+                    reinterpret_cast<long long *>(ws + z.cost_at),
+                    reinterpret_cast<PlannedItem *>(ws + z.items_at),
+                    reinterpret_cast<int *>(ws + z.order_at),
+                    reinterpret_cast<int4 *>(ws + z.dir_at),
+                    reinterpret_cast<float2 *>(ws + z.ml_at),
+                    reinterpret_cast<float *>(ws + z.o_at),
+                    (int)z.items,
                     S::kItemRows};
+    const int grid = slots_of(NR, sm_count);
     cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kTile, maps))
         return cudaErrorInvalidValue;
-    kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, slots_of(NR, sm_count));
+    kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, grid);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    e = launch_behind(kv8_tile_kernel<D, NR>, dim3((unsigned)(z.entries * a.H_kv)), S::kThreads, S::kSmem, stream, maps[0],
-                      maps[1], a, plan);
+    e = launch_behind(kv8_tile_kernel<D, NR>, dim3((unsigned)grid), S::kThreads, S::kSmem, stream, maps[0], maps[1], a, plan);
     if (e != cudaSuccess)
         return e;
-    return launch_behind(kv8_tile_join_kernel<D, NR>, dim3((unsigned)(16 * sm_count)), 256, 0, stream, a, plan);
+    constexpr int kRowsOfBlock = kJoinWarps * 32 / (D / 4) * kJoinRows;
+    return launch_behind(kv8_tile_join_kernel<D, NR>, dim3((unsigned)grid, S::kItemRows / kRowsOfBlock), kJoinWarps * 32, 0, stream, a,
+                         plan);
 }
 
-// Row tiles of a CTA: two where a request's rows may fill more than one.
+// Row tiles of a CTA: two where a request's rows may fill more than one (a prompt of
+// 8192 tokens: 472 us when this was chosen, 492 with one; the ragged chunks alike).
 int row_tiles(int G, int max_query_len) { return (int64_t)G * max_query_len > kRows ? 2 : 1; }
 
 } // namespace
 
 size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sm_count)
 {
-    return sizes_of(B, T, H / H_kv, H_kv, D, row_tiles(H / H_kv, max_query_len), sm_count).total;
+    return sizes_of(B, T, H / H_kv, D, row_tiles(H / H_kv, max_query_len), sm_count).total;
 }
 
 cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream)
