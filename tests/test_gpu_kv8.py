@@ -283,7 +283,7 @@ def test_infinite_and_nan_queries_stay_in_their_rows():
     assert bool(torch.isnan(lse.cpu()[1, 3])) and bool(torch.isnan(lse.cpu()[2, 0]))
 
 
-@pytest.mark.parametrize("B,max_q", [(300, 1), (70, 20)])
+@pytest.mark.parametrize("B,max_q", [(300, 1), (70, 20), (40, 300), (3, 200), (3, 30)])
 def test_many_requests_and_long_contexts(B, max_q):
     """More units than blocks and units that span many blocks, against a dense binary64 product on the GPU."""
     r = np.random.RandomState(B)
@@ -516,3 +516,12 @@ def test_append_of_nothing_and_of_one_head():
     rows = torch.randn((5, D), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
     k = rows.as_strided((5, 1, D), (D, 7, 1))
     _append_both(k, k, torch.arange(3, 8), codes, scales)
+
+
+@pytest.mark.parametrize("ql", [[1, 400, 3, 0, 1, 64], [200, 1, 1, 1, 33, 129]])
+def test_prompts_and_single_tokens_in_one_call(ql):
+    """A batch that mixes prompts with decoding requests: row tiles without rows beside full ones."""
+    p = _problem(8, 2, 128, 16, [900, 400, 2000, 50, 1, 64] if ql[0] == 1 else [200, 3000, 17, 1, 33, 700], ql, seed=22)
+    _check(p, _run(p))
+    _check(p, _run(p, 100), 100)
+    assert binding.smla_device_error(reset=True) == 0
