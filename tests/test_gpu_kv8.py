@@ -53,7 +53,9 @@ def _append_both(k, v, slots, codes, scales, **kw):
     (1, 64, 16, [(0, 1)]), (2, 128, 64, [(0, 1), (70, 1), (191, 1)]), (8, 128, 64, [(5, 200)]),
     (3, 64, 32, [(31, 1), (40, 17), (96, 64)]), (4, 128, 128, [(0, 128), (255, 2)]), (2, 64, 128, [(1, 383)]),
     (1, 128, 16, [(i * 16 + i % 16, 1) for i in range(40)]), (8, 64, 16, [(3, 1000)]),
-    (5, 128, 32, [(i * 64 + 7, 9) for i in range(60)])])
+    (5, 128, 32, [(i * 64 + 7, 9) for i in range(60)]),
+    (8, 64, 16, [(i * 16 + 3, 1) for i in range(1500)]),       # a large decode step
+    (8, 128, 64, [(i * 64 + i % 60, 1 + i % 4) for i in range(500)] + [(40000, 900)])])   # single tokens, then a prompt
 @pytest.mark.parametrize("loud", [False, True])
 def test_append_bits(hk, D, bs, runs, loud):
     """Runs (first slot, tokens) in whole and part blocks; loud: new values that make the blocks' scales grow."""
