@@ -35,7 +35,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // workspace of smla_build_block_tables: the ring state, then the plan of each request
 size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + up256((size_t)B * sizeof(int32_t)); }
 
-// Rows of a request that the streaming kernel takes in one unit; more go to the tile kernel.
+// Rows of a request that the streaming kernel takes in one unit; more go to the tile
+// kernel. 64 requests of 4096 positions, 4 kv heads of 128 columns: 8 rows 73 us against
+// 88 by the tile kernel, 16 rows 92 against 92 (32 requests of 16384: 156 against 136;
+// one of 32768: 37 against 56); 20 rows, 32 requests of 8192 and 8 kv heads: 288 against
+// 143, since K and V are read twice.
 bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) * max_query_len <= 16; }
 
 size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sms)
