@@ -527,8 +527,9 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
  * out           device, bf16 [T, H, D] contiguous, 16-byte aligned; must not
  *               overlap q. lse device, float [T, H] or NULL.
  * sinks         device, float [H] or NULL, in the units of scale * q . k.
- * workspace     device, >= smla_kv8_attn_workspace_size(...) bytes (for the
- *               current device), 256-byte aligned, need not be initialised.
+ * workspace     device, >= smla_kv8_attn_workspace_size(...) bytes, or
+ *               smla_kv8_attn_workspace_size_of(params) (for the current
+ *               device), 256-byte aligned, need not be initialised.
  *               Calls that overlap in time must not share it.
  * H a multiple of H_kv; B >= 0, T >= 0 (0: a no-op); 0 <= window;
  * num_blocks * H_kv below 2^31, table_width * block_size at most 2^30.
@@ -556,6 +557,9 @@ typedef struct smla_kv8_attn_params {
 
 /* (size_t)-1 on invalid arguments or a failed device query. */
 SMLA_API size_t smla_kv8_attn_workspace_size(int B, int T, int H, int H_kv, int D, int max_query_len);
+/* The bytes that one call needs: its block table's width bounds the work, so they
+ * may be fewer (pointers, strides and the workspace are not looked at). */
+SMLA_API size_t smla_kv8_attn_workspace_size_of(const smla_kv8_attn_params *params);
 SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *params);
 
 /*

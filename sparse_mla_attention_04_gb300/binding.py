@@ -83,6 +83,7 @@ SIGNATURES = {
                          _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
                          _c.c_int64, _c.c_void_p], _c.c_int),
     "smla_kv8_attn_workspace_size": ([_c.c_int] * 6, _c.c_size_t),
+    "smla_kv8_attn_workspace_size_of": ([_c.c_void_p], _c.c_size_t),
     "smla_kv8_attn_fwd": ([_c.c_void_p], _c.c_int),
     "sparse_mla_fwd_no_alloc": ([_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p,
                                  _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int64, _c.c_int,
@@ -692,15 +693,24 @@ def smla_build_block_tables(seq_lens: torch.Tensor, query_lens: torch.Tensor, bl
     with _on(dev, stream) as handle:
         held = blocks_held if blocks_held_out is None else _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
         state = ring_state if ring_state_out is None else _out(ring_state_out, "ring_state_out", (2,), torch.int32, dev)
-        query_start = _out(query_start, "query_start", (B + 1,), torch.int32, dev)
-        positions = _out(positions, "positions", (num_tokens,), torch.int64, dev)
-        slot_mapping = _out(slot_mapping, "slot_mapping", (num_tokens,), torch.int64, dev)
-        token_request = _out(token_request, "token_request", (num_tokens,), torch.int32, dev)
-        counts = _out(counts, "counts", (4,), torch.int32, dev)
         need = _sizes.get(("tables", B))
         if need is None:
             need = _sizes[("tables", B)] = int(L.smla_build_block_tables_workspace_size(B))
-        workspace, ws_bytes = _workspace(workspace, need, dev)
+        if (query_start is None and positions is None and slot_mapping is None and token_request is None
+                and counts is None and workspace is None):
+            # two allocations for all (each is as dear as the kernel's launch); the workspace first, for its alignment
+            positions, slot_mapping = torch.empty((2, num_tokens), dtype=torch.int64, device=dev).unbind(0)
+            ints = need // 4
+            workspace, counts, query_start, token_request = torch.empty(
+                ints + 5 + B + num_tokens, dtype=torch.int32, device=dev).split_with_sizes((ints, 4, B + 1, num_tokens))
+            ws_bytes = need
+        else:
+            query_start = _out(query_start, "query_start", (B + 1,), torch.int32, dev)
+            positions = _out(positions, "positions", (num_tokens,), torch.int64, dev)
+            slot_mapping = _out(slot_mapping, "slot_mapping", (num_tokens,), torch.int64, dev)
+            token_request = _out(token_request, "token_request", (num_tokens,), torch.int32, dev)
+            counts = _out(counts, "counts", (4,), torch.int32, dev)
+            workspace, ws_bytes = _workspace(workspace, need, dev)
         st = L.smla_build_block_tables(
             seq_lens.data_ptr(), query_lens.data_ptr(), blocks_held.data_ptr(), held.data_ptr(), B, block_size,
             block_table.data_ptr(), row_stride, width, free_ring.data_ptr(), free_ring.shape[0], ring_state.data_ptr(),
@@ -901,10 +911,13 @@ def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         out = _out(out, "out", (T, H, D), torch.bfloat16, dev)
         if lse is not None or return_lse:
             lse = _out(lse, "lse", (T, H), torch.float32, dev)
-        sizes = (dev.index, B, T, H, H_kv, D, max_query_len)
+        sizes = (dev.index, B, T, H, H_kv, D, max_query_len, width, block_size)
         need = _sizes.get(sizes)
         if need is None:
-            need = _sizes[sizes] = smla_kv8_attn_workspace_size(B, T, H, H_kv, D, max_query_len)
+            need = L.smla_kv8_attn_workspace_size_of(_KV8_ATTN_PARAMS.pack(
+                _KV8_ATTN_PARAMS.size, *([0] * 10), width, 0, 0, B, T, H, H_kv, D, block_size, max_query_len, 0, 0.0,
+                0, 0, 0, 0, 0, 0))
+            need = _sizes[sizes] = 256 if need == ctypes.c_size_t(-1).value else need  # (the call says what is wrong)
         workspace, ws_bytes = _workspace(workspace, need, dev)
         qs = q.stride()
         st = L.smla_kv8_attn_fwd(_KV8_ATTN_PARAMS.pack(

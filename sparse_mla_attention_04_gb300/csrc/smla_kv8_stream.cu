@@ -148,8 +148,8 @@ template <int D, int NT> struct Layout {
 
 // The workspace: for each block the unit that it begins and others end, {last
 // block (-1: none), request, index in the request}; then a head and a tail
-// partial of each block. Its size follows from the GPU alone, so nothing that the
-// lengths hold leads outside it.
+// partial of each block. Its size follows from the blocks launched, so nothing that
+// the lengths hold leads outside it.
 struct Part {
     int4 *dir;
     float2 *ml;   // [2 blocks][R]
@@ -734,10 +734,20 @@ struct Sizes {
     size_t ml, o, total;
 };
 
-Sizes sizes(int D, int NT, int sm_count)
+// The most work that there can be decides the blocks: one without a part ends at once, but not for nothing.
+int grid_of(int B, int T, int G, int H_kv, int NT, int64_t positions, int sm_count)
+{
+    const double units = ((double)T * G / (8 * NT) + B) * H_kv; // each request's last chunk may be short
+    const double most = units * ((double)positions / kStep + kUnitCost + 1);
+    const int fill = fill_of(NT, sm_count);
+    if (most < (double)fill * kMinPart)
+        return std::max(1, (int)(most / kMinPart) + 1);
+    return most < 24.0 * kMinPart * fill ? fill : fill * (1 + kSmallPerBig); // (small parts only where they are work enough)
+}
+
+Sizes sizes(int D, int NT, size_t blocks)
 {
     const int R = 8 * NT;
-    const size_t blocks = (size_t)fill_of(NT, sm_count) * (1 + kSmallPerBig);
     Sizes s;
     s.ml = up256(blocks * sizeof(int4));
     s.o = up256(s.ml + 2 * blocks * R * sizeof(float2));
@@ -749,7 +759,8 @@ template <int D, int NT>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
     using L = Layout<D, NT>;
-    const Sizes sz = sizes(D, NT, sm_count);
+    const int grid = grid_of(a.B, a.T, a.G, a.H_kv, NT, (int64_t)a.table_width << a.block_shift, sm_count);
+    const Sizes sz = sizes(D, NT, grid);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Part part{reinterpret_cast<int4 *>(ws), reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o),
                     fill_of(NT, sm_count)};
@@ -759,13 +770,6 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kStep, maps))
         return cudaErrorInvalidValue;
-    // the most work that there can be decides the grid: blocks without a part end at once, but not for nothing
-    const double units = ((double)a.T * a.G / (8 * NT) + a.B) * a.H_kv; // each request's last chunk may be short
-    const double most = units * ((double)a.table_width * a.block_size / kStep + kUnitCost + 1);
-    const int fill = part.fill;
-    int grid = fill * (1 + kSmallPerBig);
-    if (most < 24.0 * kMinPart * fill) // no small parts
-        grid = most < (double)fill * kMinPart ? std::max(1, (int)(most / kMinPart) + 1) : fill;
     kv8_stream_kernel<D, NT><<<grid, kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
@@ -789,9 +793,10 @@ int tiles_for(int G, int max_query_len) { return (int64_t)G * max_query_len > 8 
 
 } // namespace
 
-size_t kv8_stream_workspace(int G, int D, int max_query_len, int sm_count)
+size_t kv8_stream_workspace(int B, int T, int G, int H_kv, int D, int max_query_len, int64_t positions, int sm_count)
 {
-    return sizes(D, tiles_for(G, max_query_len), sm_count).total;
+    const int nt = tiles_for(G, max_query_len);
+    return sizes(D, nt, grid_of(B, T, G, H_kv, nt, positions, sm_count)).total;
 }
 
 cudaError_t launch_kv8_stream(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count,

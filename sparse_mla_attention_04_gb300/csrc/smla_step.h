@@ -98,7 +98,8 @@ size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int max_query_le
 cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream);
 cudaError_t read_kv8_error(int *out, bool reset);
 cudaError_t read_kv8_stream_error(int *out, bool reset);
-size_t kv8_stream_workspace(int G, int D, int max_query_len, int sm_count);
+// positions: those that the block table has at most
+size_t kv8_stream_workspace(int B, int T, int G, int H_kv, int D, int max_query_len, int64_t positions, int sm_count);
 cudaError_t launch_kv8_stream(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count,
                               cudaStream_t stream);
 

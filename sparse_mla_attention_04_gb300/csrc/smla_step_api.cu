@@ -42,9 +42,11 @@ size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + 
 // 143, since K and V are read twice.
 bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) * max_query_len <= 16; }
 
-size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sms)
+constexpr int64_t kMostPositions = 1 << 30; // of a block table
+
+size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int64_t positions, int sms)
 {
-    return few_rows(H, H_kv, max_query_len) ? smla::kv8_stream_workspace(H / H_kv, D, max_query_len, sms)
+    return few_rows(H, H_kv, max_query_len) ? smla::kv8_stream_workspace(B, T, H / H_kv, H_kv, D, max_query_len, positions, sms)
                                             : smla::kv8_tile_workspace(B, T, H, H_kv, D, max_query_len, sms);
 }
 
@@ -309,7 +311,19 @@ SMLA_API size_t smla_kv8_attn_workspace_size(int B, int T, int H, int H_kv, int 
     int sms = 0;
     if (check_kv8_shape(B, T, H, H_kv, D, max_query_len) != SMLA_OK || current_sm_count(&sms) != cudaSuccess)
         return (size_t)-1;
-    return kv8_workspace(B, T, H, H_kv, D, max_query_len, sms);
+    return kv8_workspace(B, T, H, H_kv, D, max_query_len, kMostPositions, sms);
+}
+
+SMLA_API size_t smla_kv8_attn_workspace_size_of(const smla_kv8_attn_params *p)
+{
+    int sms = 0;
+    if (p == nullptr || p->size < sizeof(smla_kv8_attn_params) ||
+        check_kv8_shape(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len) != SMLA_OK || p->table_width < 0 ||
+        block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > kMostPositions ||
+        current_sm_count(&sms) != cudaSuccess)
+        return (size_t)-1;
+    return kv8_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len,
+                         (int64_t)p->table_width << block_shift(p->block_size), sms);
 }
 
 SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
@@ -323,7 +337,7 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     if (p->num_blocks < 0 || p->table_width < 0 || p->table_stride < p->table_width || p->window < 0 ||
         p->q_stride_t < 0 || p->q_stride_h < 0 || !std::isfinite(p->scale))
         return SMLA_ERR_BAD_SHAPE;
-    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > 1 << 30 ||
+    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > kMostPositions ||
         p->num_blocks > INT_MAX / p->H_kv)
         return SMLA_ERR_UNSUPPORTED;
     if (p->T == 0 || p->B == 0)
@@ -342,7 +356,8 @@ SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms); e != cudaSuccess)
         return cuda_status(e);
-    if (p->workspace_bytes < kv8_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len, sms))
+    if (p->workspace_bytes < kv8_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len,
+                                           (int64_t)p->table_width << block_shift(p->block_size), sms))
         return SMLA_ERR_WORKSPACE_TOO_SMALL;
     smla::Kv8AttnArgs a;
     a.q = p->q;

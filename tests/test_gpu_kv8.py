@@ -527,3 +527,26 @@ def test_prompts_and_single_tokens_in_one_call(ql):
     _check(p, _run(p))
     _check(p, _run(p, 100), 100)
     assert binding.smla_device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("H,hk,D,B,q", [(16, 2, 128, 1, 1), (32, 8, 128, 64, 1), (8, 8, 64, 3, 2), (8, 1, 64, 5, 300)])
+def test_the_workspace_of_a_call_is_within_the_bound(H, hk, D, B, q):
+    """And a call runs in exactly what it asks for, whatever the table's width."""
+    bound = binding.smla_kv8_attn_workspace_size(B, B * q, H, hk, D, q)
+    for width in (0, 1, 7, 600):
+        kc, vc, ks, vs = binding.new_kv8_cache(4, hk, 16, D, device=DEV)
+        kc.fill_(0x30)
+        vc.fill_(0x38)                                         # 1.0 everywhere
+        table = torch.arange(width, device=DEV).remainder(4).int().repeat(B, 1)
+        lens = torch.full((B,), max(width * 16 - 3, 0), dtype=torch.int32, device=DEV)
+        start = torch.arange(0, B * q + 1, q, dtype=torch.int32, device=DEV)
+        x = torch.randn((B * q, H, D), device=DEV).to(torch.bfloat16)
+        p = binding._KV8_ATTN_PARAMS
+        need = binding.lib().smla_kv8_attn_workspace_size_of(p.pack(p.size, *([0] * 10), width, 0, 0, B, B * q, H, hk, D, 16, q,
+                                                                    0, 0.0, 0, 0, 0, 0, 0, 0))
+        assert 0 < need <= bound
+        room = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        out, _ = binding.smla_kv8_attn_fwd(x, kc, vc, ks, vs, table, lens, start, 0.1, max_query_len=q, workspace=room[:need])
+        seen = (torch.arange(B * q, device=DEV) % q + lens[0] - q >= 0)
+        assert torch.allclose(out.float(), seen[:, None, None].float().expand_as(out), rtol=2.0 ** -7, atol=0)
+        assert bool((room[need:] == 0x5A).all())

@@ -185,3 +185,19 @@ def test_row_strides_that_no_row_uses_and_rows_over_one_another(L):
     assert append(T=(1 << 31) - 1) == b.SMLA_ERR_UNSUPPORTED
     for kw in (dict(T=1, kt=1021, vt=3), dict(H=1, kh=5, vh=7)):
         assert append(**kw) == b.SMLA_ERR_MISALIGNED       # (the slots' address)
+
+
+def test_workspace_of_a_call(L):
+    """-1 for what the call would refuse; on a GPU no more than the bound without the table's width."""
+    def need(**kw):
+        a = dict(size=ctypes.sizeof(b.SmlaKv8AttnParams), q=None, q_stride_t=0, q_stride_h=0, k_cache=None, v_cache=None,
+                 k_scale=None, v_scale=None, num_blocks=0, block_table=None, table_stride=0, table_width=16, seq_lens=None,
+                 query_start=None, B=2, T=2, H=32, H_kv=8, D=128, block_size=64, max_query_len=1, window=0, scale=0.1,
+                 sinks=None, out=None, lse=None, workspace=None, workspace_bytes=0, stream=None)
+        a.update(kw)
+        return L.smla_kv8_attn_workspace_size_of(ctypes.byref(b.SmlaKv8AttnParams(*[a[n] for n, _ in b.SmlaKv8AttnParams._fields_])))
+
+    none = ctypes.c_size_t(-1).value
+    assert L.smla_kv8_attn_workspace_size_of(None) == none
+    for bad in (dict(size=8), dict(B=-1), dict(D=96), dict(block_size=48), dict(table_width=-1), dict(table_width=1 << 26)):
+        assert need(**bad) == none, bad
