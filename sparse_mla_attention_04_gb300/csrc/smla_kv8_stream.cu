@@ -115,7 +115,7 @@ struct Division {
     {
         Division d{total, total, 0, 0};
         const long long parts = max(1ll, (total + kMinPart - 1) / kMinPart);
-        d.big = (int)min((long long)fill, parts);
+        d.big = (int)min((long long)min(fill, grid), parts); // (never more than there are, whatever the starts hold)
         // small parts of a twelfth of a block's share, where that is work enough for one
         if (grid > fill && total / 12 >= (long long)2 * kMinPart * fill) {
             d.small = grid - fill;

@@ -490,7 +490,9 @@ def test_starts_that_overlap_stay_within_the_buffers(ql):
     T = 6 * ql
     p["start"] = torch.tensor([0, T, 0, T, 0, T, 0], dtype=torch.int32)
     out = torch.full((T + 2, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
-    need = binding.smla_kv8_attn_workspace_size(6, T + 2, 8, 2, 128, ql)
+    c = binding._KV8_ATTN_PARAMS
+    need = binding.lib().smla_kv8_attn_workspace_size_of(c.pack(c.size, *([0] * 10), p["table"].shape[1], 0, 0, 6, T + 2, 8, 2, 128,
+                                                                64, ql, 0, 0.0, 0, 0, 0, 0, 0, 0))
     room = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
     _run(p, out=out, workspace=room[:need])
     torch.cuda.synchronize()
