@@ -474,7 +474,7 @@ SMLA_API smla_status smla_rope(const smla_rope_params *params);
  * smla_kv8_append writes the rows of T new tokens at their slots. A run is a
  * maximal stretch of consecutive tokens t whose slots lie in one block. For each
  * run, head and cache, with amax the largest finite |x| of the run's rows there
- * and s_new = max(amax / 448, 2^-60) (1.0 if amax is 0), in binary32:
+ * (0 if there is none) and s_new = max(amax / 448, 2^-60), in binary32:
  *   - if the run's smallest offset o is above 0, the block holds o older tokens:
  *     scale = max(old scale, s_new), and when it grew their codes become
  *     E4M3_RNE(code * old / scale); otherwise scale = s_new;

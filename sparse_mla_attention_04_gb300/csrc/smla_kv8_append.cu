@@ -217,7 +217,8 @@ __device__ __forceinline__ void write_run(const Kv8AppendArgs &a, const Run &run
             m = amax8<true>(m, *reinterpret_cast<const uint4 *>(rows + (int64_t)(r - sub) * st));
         amax = team_max(m);
     }
-    float now = amax == 0.f ? 1.0f : fmaxf(__fdiv_rn(amax, 448.0f), kMinScale);
+    // (rows of zeros, which any scale holds, ask for the smallest: they change no block that has other rows)
+    float now = fmaxf(__fdiv_rn(amax, 448.0f), kMinScale);
     uint8_t *dst = (isv ? a.v_cache : a.k_cache) + (((int64_t)run.block * a.H_kv + h) << a.block_shift) * D;
     if (low > 0) {
         if (now > old) {

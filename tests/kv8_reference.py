@@ -140,7 +140,7 @@ def append(k, slots, cache, scale):
         rows = k[t:e].float()                                  # [n, H_kv, D]
         a = rows.abs()
         amax = torch.where(torch.isfinite(a), a, torch.zeros_like(a)).amax((0, 2))
-        new = torch.where(amax > 0, (amax / 448.0).clamp(min=2.0 ** -60), torch.ones_like(amax))
+        new = (amax / 448.0).clamp(min=2.0 ** -60)
         low = int(offs.min())
         for h in range(hk):
             now = new[h]
