@@ -507,10 +507,15 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
  * With sinks, e^{sinks[h]} joins the denominator and the lse. A row that sees
  * nothing gives out = 0 and lse = -inf (sinks[h] with sinks). Positions whose
  * block_table entry is outside [0, num_blocks) are not read and see no one;
- * nothing beyond seq_lens[b] is read. q keeps its bf16 values (dots in 16 bits
- * or in two 8-bit parts of it, sums in binary32), softmax weights are rounded to
- * binary16. Scales are read of the blocks that a token of the request sees; of
- * one request and head they must be positive, at least 2^-60 (as
+ * nothing beyond seq_lens[b] is read. Sums are in binary32. q is carried by two
+ * E4M3 parts: its bf16 values whole down to 2^-9 of the largest |q| of their row
+ * (token and head), to 2^-17 of that below. Weights are rounded to binary16 with
+ * their block's value scale in them: softmax weight times v_scale is kept to 2^-11
+ * of itself down to 2^-19 of the row's largest such product, to 2^-30 of that
+ * product below; the denominator and lse have every weight in binary32. (So a
+ * block whose scale is 2^19 times the others', but not its values, still leaves
+ * the others theirs.) Scales are read of the blocks that a token of the request
+ * sees; of one request and head they must be positive, at least 2^-60 (as
  * smla_kv8_append gives them) and within a factor of 2^100.
  *
  * q             device, bf16 [T, H, D], element strides (t, h) multiples of 8,

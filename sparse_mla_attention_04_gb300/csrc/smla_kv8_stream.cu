@@ -31,9 +31,11 @@
 // bytes of a K row are two k-steps of its fragment, and its 16 bytes of four V
 // rows are its whole V^T fragment.
 // The block scales: K's multiplies the logits, V's is folded into the exponent,
-// p' = 2^(s + log2(vs) - m), so p' <= 2^8 needs no other range, and the
-// denominator adds p' / vs. The reference m moves only when a logit passes it
-// by 8 (then p' would pass 2^8): one vote a step instead of a reduction.
+// p' = 2^(s + log2(vs) - m), and the denominator adds p' / vs. The reference m is
+// set so that the largest p' is 2^11 and moves only when one would pass 2^15: one
+// vote a step instead of a reduction. Binary16 holds p' to 2^-11 of itself down
+// to 2^-14, a 2^-25th of the largest: with the largest at 1 a value scale 2^-20 of
+// another's, whose block may hold nothing of that size, lost all but a few bits.
 //
 // Measured: 64 requests of up to 32768 positions (1.08 GB of codes, 32 heads on 8 kv
 // heads of 128 columns) in 188 us, 5.7 TB/s, 85% of the copy bandwidth; one request of
@@ -59,7 +61,8 @@ constexpr int kStep = 32;     // positions a warp takes at a time
 constexpr int kStages = 2;
 constexpr int kUnitCost = 2;  // a unit's start and end, in steps
 constexpr int kMinPart = 6;   // a block's part, in steps, before more blocks share the work
-constexpr float kSlack = 8.0f;
+constexpr float kTop = 11.0f;   // (log2) the largest weight where the reference is set,
+constexpr float kSlack = 15.0f; // and what none may pass: binary16 ends at 65504
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
 {
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                                 y = -INFINITY;
                         }
                         sc[x][nt][e] = y;
-                        raise |= y > m[nt][e & 1] + kSlack;
+                        raise |= y > __fadd_rd(m[nt][e & 1], kSlack); // (rounded so that no weight passes it, far out too)
                     }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        const float now = fmaxf(m[nt][e], x);
+                        const float now = fmaxf(m[nt][e], __fadd_ru(x, -kTop));
                         const float f = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - now);
                         m[nt][e] = now;
                         l[nt][e] *= f;

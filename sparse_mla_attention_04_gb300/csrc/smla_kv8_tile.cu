@@ -27,11 +27,15 @@
 // expanded exactly to binary16: 8-bit weights would lose half of their bits.
 // The block scales enter as in the streaming kernel: K's multiplies the logits,
 // V's is folded into the exponent, p' = 2^(s + log2(vs) - m), and the
-// denominator adds p' / vs. A row's reference m is its largest logit of the first
-// tile that it sees. The weights of a tile are taken without looking for its maximum;
-// their sum (at most 2^15, so that each is inside binary16, whose precision is
-// relative) says whether m must move, and only then, which is seldom, the tile is
-// gone through again and what was added up so far is rescaled.
+// denominator adds p' / vs. A row's reference m is set so that the largest p' of the
+// first tile that it sees is 2^5. The weights of a tile are taken without looking for
+// its maximum; their sum (at most 65504, so that each is inside binary16) says whether
+// m must move, and only then, which is seldom, the tile is gone through again and what
+// was added up so far is rescaled. Binary16 holds p' to 2^-11 of itself down to 2^-14,
+// 2^-19 of the largest: with the largest at 1 the values of blocks whose scale is 2^-16
+// of another's, which may hold nothing of its size, lost bits. A larger first weight
+// leaves the sums less to grow: a prompt of 8192 tokens takes 440 us with 2^0 or 2^5,
+// 444 with 2^6, 448 with 2^7.
 //
 // Shared memory: the codes in TMA's swizzled rows; Q and the expanded V in 8-row
 // x 16-byte core matrices, written so that eight lanes fill one (no bank
@@ -66,7 +70,9 @@ using namespace umma;
 
 constexpr int kRows = 128;  // of a row tile
 constexpr int kTile = 64;
-constexpr float kSlack = 8.0f; // (log2) a logit's distance above the reference that moves it, when it is looked at
+constexpr float kTop = 5.0f;     // (log2) the largest weight where the reference is set
+constexpr float kSlack = 9.9f;  // (log2) the largest weight that does not move it, when it is looked at
+constexpr float kMostSum = 65504.0f; // of 64 weights that are not looked at: 64 of 2^kSlack stay below
 constexpr int kPieceCost = 13; // a unit's start and end, in tiles (measured: 14000 to 19000 cycles, a tile 1450 to 1550)
 constexpr int kMinPart = 22;  // a CTA's part of the work, in tiles, before more CTAs share it
 
@@ -371,7 +377,7 @@ __device__ __forceinline__ float weigh(const uint32_t *x, uint32_t *p)
 // One row's 64 scores (the thread's lane of tensor memory at my) become weights
 // 2^(s + log2(vs) - m) in binary16, over the scores they come from; their sum,
 // each group's divided by vs, joins l. False where the reference may have to move
-// (the sum passes 2^15, so a weight may pass what binary16 holds) for some row of
+// (the sum passes what binary16 holds, so a weight may) for some row of
 // the warp: then nothing is changed. For tiles that all rows see.
 __device__ __forceinline__ bool row_tile(uint32_t my, const float *sc, float qs, Row &row)
 {
@@ -398,7 +404,7 @@ __device__ __forceinline__ bool row_tile(uint32_t my, const float *sc, float qs,
         l = fmaf(s, f.iv[c], l);
     }
     // beyond 2^20 the rounding of m alone could pass any bound of the weights
-    if (__any_sync(0xffffffffu, all > 0x1p15f || !(fabsf(row.m) <= 0x1p20f)))
+    if (__any_sync(0xffffffffu, all > kMostSum || !(fabsf(row.m) <= 0x1p20f)))
         return false;
     row.l = l;
 #pragma unroll
@@ -437,11 +443,15 @@ __device__ __forceinline__ float largest(uint32_t my, const float *sc, float qs,
 // The next two run seldom, so they are short loops: code that is not in the
 // instruction cache costs some 12 cycles an instruction.
 
+// The reference of a row whose largest logit is `top` (rounded up, so that far out,
+// where kTop is less than the logits' step, no weight passes 1).
+__device__ __forceinline__ float reference(float top) { return __fadd_ru(top, -kTop); }
+
 // The row's first reference.
 __device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, int t0, const Sight see)
 {
     if (!see.all(t0) || !see.all(t0 + 32))
-        return largest(my, sc, qs, t0, see);
+        return reference(largest(my, sc, qs, t0, see));
     float top = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
@@ -453,11 +463,11 @@ __device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, 
         for (int i = 0; i < 16; ++i)
             top = fmaxf(top, fmaf(__uint_as_float(x[i]), k, vs));
     }
-    return top;
+    return reference(top);
 }
 
-// row_tile for any tile and any reference: the reference moves to the tile's largest
-// logit where that passes it by kSlack, and what was added up is rescaled (O is at
+// row_tile for any tile and any reference: the reference moves where a weight passes
+// 2^kSlack (to 2^kTop), and what was added up is rescaled (O is at
 // rest; o_cols: its columns, 0 before the first product); positions that the row
 // does not see are left out; the difference is taken from the rounded logit, as the
 // reference is.
@@ -467,8 +477,9 @@ __device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_co
     const float top = largest(my, sc, qs, t0, see);
     const bool raise = row.m == -INFINITY ? top > -INFINITY : top - row.m > kSlack;
     if (__any_sync(0xffffffffu, raise)) {
-        const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - top)) : 1.f;
-        row.m = raise ? top : row.m;
+        const float ref = reference(top);
+        const float g = raise ? (row.m == -INFINITY ? 0.f : ex2_approx(row.m - ref)) : 1.f;
+        row.m = raise ? ref : row.m;
         row.l *= g;
 #pragma unroll 1
         for (int o = 0; o < o_cols; o += 16) {
