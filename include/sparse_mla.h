@@ -397,9 +397,11 @@ typedef enum {
 /*
  * The rotary table that smla_rope and smla_fused_qk_rope_cache read: row r
  * holds, for position p = first_position + r and pairs i < n = rot_dim / 2,
- * m cos(p f_i) in column i and m sin(p f_i) in column n + i, in binary32. The
- * angle is carried as a 64-bit fraction of a turn, so it is as exact at
- * position 2^31 as at 1 (the frequencies are rounded to binary64 once).
+ * m cos(p f_i) in column i and m sin(p f_i) in column n + i, in binary32, each to
+ * 6 * 2^-24 of itself for the angle that it is taken at. The angle is carried as a
+ * 64-bit fraction of a turn, and whole turns leave it without a rounding; what moves
+ * it is the frequency's own, in binary64 (some 2^-50 of it, so p f_i 2^-50: 2^-19
+ * radians at position 2^31 for f = 1) and to 2^-65 of a turn a position.
  *
  * table              device, float [num_positions, rot_dim], 4-byte aligned, written.
  * num_positions, first_position  >= 0, first_position + num_positions <= 2^31.

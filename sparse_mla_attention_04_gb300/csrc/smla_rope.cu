@@ -12,14 +12,20 @@ __device__ int g_rope_error = 0; // bit 4: a position out of range
 
 namespace {
 
-// Sine and cosine of a 64-bit fraction of a turn (its high 32 bits: 2^-32 of a
-// turn is 1.5e-9 radians, a fortieth of binary32's step at 1). The nearest
-// quarter turn leaves an angle of at most pi/4, for which the Taylor series to
-// x^9 and x^10 are off by less than 2e-9; the quarter then swaps and negates.
-__device__ __forceinline__ void sincos_turn(unsigned hi, float &s, float &c)
+// Sine and cosine of a 64-bit fraction of a turn, times `factor`. The nearest quarter
+// turn leaves an angle of at most pi/4, all of whose bits go into its rounding to
+// binary32 (the sines of the first positions of a slow pair are as small as the
+// angles), and for which the Taylor series to x^9 and x^10 are off by less than 2e-9
+// of the value; the quarter then swaps and negates. In all below 6 * 2^-24 of each
+// value. `at` is the fraction plus kHalves: half a quarter, so that bits 63 and 62 are
+// the nearest quarter, and half of bit 32, so that the word above is rounded and the
+// word below is what is left of it, with its sign.
+constexpr unsigned long long kHalves = 0x2000000080000000ull;
+__device__ __forceinline__ void sincos_turn(unsigned long long at, float factor, float &s, float &c)
 {
-    const unsigned q = (hi + 0x20000000u) >> 30;
-    const float x = (float)(int)(hi - (q << 30)) * 1.4629180792671596e-9f; // 2 pi 2^-32
+    const unsigned hi = (unsigned)(at >> 32), lo = (unsigned)at;
+    const float x = fmaf((float)(int)(lo ^ 0x80000000u), 0x1p-32f, (float)((int)(hi & 0x3FFFFFFFu) - 0x20000000)) *
+                    1.4629180792671596e-9f; // 2 pi 2^-32
     const float y = x * x;
     float sn = fmaf(y, 2.7557319e-6f, -1.9841270e-4f);
     sn = fmaf(sn, y, 8.3333333e-3f);
@@ -30,9 +36,10 @@ __device__ __forceinline__ void sincos_turn(unsigned hi, float &s, float &c)
     cs = fmaf(cs, y, 4.1666667e-2f);
     cs = fmaf(cs, y, -0.5f);
     cs = fmaf(cs, y, 1.0f);
-    const float a = q & 1 ? cs : sn, b = q & 1 ? sn : cs;
-    s = q & 2 ? -a : a;
-    c = (q + 1) & 2 ? -b : b;
+    const bool odd = hi & 0x40000000u;
+    const unsigned f = __float_as_uint(factor);
+    s = (odd ? cs : sn) * __uint_as_float(f ^ (hi & 0x80000000u));                 // quarters 2 and 3: negative
+    c = (odd ? sn : cs) * __uint_as_float(f ^ ((hi + 0x40000000u) & 0x80000000u)); // quarters 1 and 2
 }
 
 // The table. frac[i] is pair i's frequency as a fraction of a turn, times 2^64:
@@ -40,8 +47,10 @@ __device__ __forceinline__ void sincos_turn(unsigned hi, float &s, float &c)
 // rounding at all however far the position, in integer arithmetic (binary64
 // would run at 1/64 of the binary32 rate here). A thread keeps its kVec pairs
 // and walks down the rows, adding a constant to each angle. Bound: 4 bytes
-// written per value. Measured: 1048576 rows of 64 values (268 MB) in 39.8 us, 6.74
-// TB/s, the copy bandwidth (63.5 us with CUDA's sincospif and 4-byte stores).
+// written per value; the instructions come close to it. Measured: 1048576 rows of 64
+// values (268 MB) in 40.3 us, 6.67 TB/s, 98% of the copy bandwidth (39.8 with the
+// angle cut to 32 bits, 43.0 with the signs chosen instead of set, 59.4 with the
+// angle converted from 64 bits at once, 63.5 with CUDA's sincospif and 4-byte stores).
 template <int kVec>
 __global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ table, int64_t rows, int64_t first,
                                                          const RopeFrequencies f)
@@ -56,7 +65,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ tab
     unsigned long long at[kVec], step[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-        at[e] = (unsigned long long)(first + r) * f.frac[i + e];
+        at[e] = (unsigned long long)(first + r) * f.frac[i + e] + kHalves;
         step[e] = (unsigned long long)stride * f.frac[i + e];
     }
 #pragma unroll 2
@@ -66,9 +75,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ tab
         } c, s;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            sincos_turn((unsigned)(at[e] >> 32), s.v[e], c.v[e]);
-            c.v[e] *= f.factor;
-            s.v[e] *= f.factor;
+            sincos_turn(at[e], f.factor, s.v[e], c.v[e]);
             at[e] += step[e];
         }
         float *row = table + r * 2 * n + i;

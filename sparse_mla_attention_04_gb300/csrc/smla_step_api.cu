@@ -174,7 +174,7 @@ SMLA_API smla_status smla_rope_cos_sin_cache(float *table, int64_t num_positions
             const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
             w = w / factor * ramp + w * (1.0 - ramp);
         }
-        f.frac[i] = (unsigned long long)(w / two_pi * 18446744073709551616.0); // below 2^62: w <= 1
+        f.frac[i] = (unsigned long long)std::nearbyint(w / two_pi * 18446744073709551616.0); // below 2^62: w <= 1
     }
     const double m = attention_factor > 0.0 ? attention_factor
                                             : (scaling == SMLA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0);
