@@ -341,8 +341,9 @@ SMLA_API smla_status sparse_mla_fwd_no_alloc(const void *q, const void *kv_cache
  * If a request needs more than table_width blocks, or the ring holds fewer than
  * the batch needs, nothing is taken or given back (tables, ring, held counts
  * and ring state keep their values), counts[3] is the number of blocks lacking
- * and tokens in blocks not held get slot -1: the caller can free requests and
- * call again.
+ * (those beyond the rows' width, plus those that the ring holds too few) and
+ * tokens in blocks not held get slot -1: the caller can free requests and call
+ * again.
  *
  * seq_lens, query_lens   device, int32 [B].
  * blocks_held            device, int32 [B]: blocks each request has in its row.

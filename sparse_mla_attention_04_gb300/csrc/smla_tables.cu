@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) tables_small_kernel(const TablesArgs
     __shared__ Sums warp_sums[32];
     __shared__ int4 s_plan[kThreads];
     __shared__ int s_start[kThreads + 1], s_give[kThreads];
-    __shared__ int s_wide;
+    __shared__ unsigned long long s_wide; // blocks that rows have no room for
     const int tid = threadIdx.x;
     const int2 ring = ring_state(a);
     const int head = ring.x, count = ring.y;
@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(kThreads) tables_small_kernel(const TablesArgs
     Sums all;
     const Sums x = block_exclusive(v, &all, warp_sums);
     if (r.need > a.table_width)
-        atomicAdd(&s_wide, min(r.need - a.table_width, INT_MAX / kThreads)); // (whole numbers: any order)
+        atomicAdd(&s_wide, (unsigned long long)(r.need - a.table_width)); // (whole numbers: any order)
     __syncthreads();
-    const long long lacking = s_wide + max(all.take - count, 0ll);
+    const long long lacking = (long long)s_wide + max(all.take - count, 0ll);
     const bool ok = lacking == 0;
     if (tid < a.B) {
         const int after = ok ? r.need : r.held;
