@@ -11,6 +11,7 @@ raises — there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -693,9 +694,7 @@ def smla_build_block_tables(seq_lens: torch.Tensor, query_lens: torch.Tensor, bl
     with _on(dev, stream) as handle:
         held = blocks_held if blocks_held_out is None else _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
         state = ring_state if ring_state_out is None else _out(ring_state_out, "ring_state_out", (2,), torch.int32, dev)
-        need = _sizes.get(("tables", B))
-        if need is None:
-            need = _sizes[("tables", B)] = int(L.smla_build_block_tables_workspace_size(B))
+        need = _tables_workspace(B)
         if (query_start is None and positions is None and slot_mapping is None and token_request is None
                 and counts is None and workspace is None):
             # two allocations for all (each is as dear as the kernel's launch); the workspace first, for its alignment
@@ -721,8 +720,24 @@ def smla_build_block_tables(seq_lens: torch.Tensor, query_lens: torch.Tensor, bl
     return BlockTables(query_start, positions, slot_mapping, token_request, counts, held, state)
 
 
-# workspace bytes by the sizes they follow from (and the device, whose SM count they follow too)
-_sizes = {}
+# Workspace bytes of recent sizes: a call to the library for each costs more than the rest of the binding's checks,
+# but a server's sizes have no end.
+@functools.lru_cache(maxsize=1024)
+def _tables_workspace(B: int) -> int:
+    return int((_lib or lib()).smla_build_block_tables_workspace_size(B))
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv8_attn_workspace(device: int, B: int, T: int, H: int, H_kv: int, D: int, max_query_len: int, width: int,
+                        block_size: int) -> int:
+    """For `device`, which is the current one (its SM count decides). Raises where the library has no answer, which
+    is not kept: a device query may have failed in passing."""
+    need = (_lib or lib()).smla_kv8_attn_workspace_size_of(_KV8_ATTN_PARAMS.pack(
+        _KV8_ATTN_PARAMS.size, *([0] * 10), width, 0, 0, B, T, H, H_kv, D, block_size, max_query_len, 0, 0.0, 0, 0, 0, 0,
+        0, 0))
+    if need == ctypes.c_size_t(-1).value:
+        raise SmlaError(SMLA_ERR_BAD_SHAPE, "smla_kv8_attn_workspace_size_of")
+    return int(need)
 
 
 def smla_rope_cos_sin_cache(num_positions: int, rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
@@ -911,13 +926,10 @@ def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         out = _out(out, "out", (T, H, D), torch.bfloat16, dev)
         if lse is not None or return_lse:
             lse = _out(lse, "lse", (T, H), torch.float32, dev)
-        sizes = (dev.index, B, T, H, H_kv, D, max_query_len, width, block_size)
-        need = _sizes.get(sizes)
-        if need is None:
-            need = L.smla_kv8_attn_workspace_size_of(_KV8_ATTN_PARAMS.pack(
-                _KV8_ATTN_PARAMS.size, *([0] * 10), width, 0, 0, B, T, H, H_kv, D, block_size, max_query_len, 0, 0.0,
-                0, 0, 0, 0, 0, 0))
-            need = _sizes[sizes] = 256 if need == ctypes.c_size_t(-1).value else need  # (the call says what is wrong)
+        try:
+            need = _kv8_attn_workspace(dev.index, B, T, H, H_kv, D, max_query_len, width, block_size)
+        except SmlaError:
+            need = 256  # (the call says what is wrong)
         workspace, ws_bytes = _workspace(workspace, need, dev)
         qs = q.stride()
         st = L.smla_kv8_attn_fwd(_KV8_ATTN_PARAMS.pack(
