@@ -410,7 +410,8 @@ typedef enum {
  * base               > 1 and finite.
  * scaling            smla_rope_scaling; factor >= 1 (ignored for NONE);
  *                    original_max_position >= 1, beta_fast > beta_slow > 0 (YARN).
- * attention_factor   m; 0 = the scaling's own: 0.1 ln(factor) + 1 for YARN, else 1.
+ * attention_factor   m, finite in binary32; 0 = the scaling's own:
+ *                    0.1 ln(factor) + 1 for YARN, else 1.
  */
 SMLA_API smla_status smla_rope_cos_sin_cache(float *table, int64_t num_positions, int64_t first_position,
                                              int rot_dim, double base, int scaling, double factor,

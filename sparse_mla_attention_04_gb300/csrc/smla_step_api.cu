@@ -3,6 +3,7 @@
 // Declared and documented in include/sparse_mla.h.
 #include "smla_step.h"
 
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -137,7 +138,7 @@ SMLA_API smla_status smla_rope_cos_sin_cache(float *table, int64_t num_positions
         return SMLA_ERR_BAD_SHAPE;
     if (scaling < SMLA_ROPE_NONE || scaling > SMLA_ROPE_YARN)
         return SMLA_ERR_BAD_DTYPE;
-    if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(attention_factor) || attention_factor < 0.0)
+    if (!(base > 1.0) || !std::isfinite(base) || !(attention_factor >= 0.0 && attention_factor <= FLT_MAX))
         return SMLA_ERR_BAD_SHAPE;
     if (scaling != SMLA_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
         return SMLA_ERR_BAD_SHAPE;
