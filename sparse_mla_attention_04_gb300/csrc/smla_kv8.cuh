@@ -174,8 +174,8 @@ __device__ __forceinline__ float finish_row(float m, float l, const float *sinks
     if (sinks) {
         const float s = sinks[head] * kLog2e;
         const float top = fmaxf(m, s);
-        if (top == -INFINITY) { // nothing seen and a sink of -inf
-            *lse = -INFINITY;
+        if (fabsf(top) == INFINITY) { // a sink beside which nothing is left, or nothing seen and a sink of -inf
+            *lse = sinks[head] + l;   // (a NaN among the sums stays)
             return 0.0f;
         }
         f = ex2_approx(m - top); // m = -inf: 0

@@ -584,13 +584,11 @@ __device__ __forceinline__ bool work_on(const CUtensorMap &k_map, const CUtensor
         if (tid < rows) {
             const int64_t t = rq.q0 + (row0 + tid) / a.G;
             const int head = it.h * a.G + (row0 + tid) % a.G;
-            float lse;
-            finish_row(-INFINITY, 0.f, a.sinks, head, &lse);
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (t * a.H + head) * D);
             for (int i = 0; i < D / 8; ++i)
                 dst[i] = make_uint4(0, 0, 0, 0);
             if (a.lse)
-                a.lse[t * a.H + head] = lse;
+                a.lse[t * a.H + head] = a.sinks ? a.sinks[head] : -INFINITY;
         }
         return true;
     }
