@@ -776,9 +776,18 @@ def smla_rope_cos_sin_cache(num_positions: int, rot_dim: int, *, base: float = 1
     return out
 
 
-# the C structures, packed (native sizes and alignment) instead of built field by field
-_ROPE_PARAMS = struct.Struct("@NiPqqPqqPqqPqqPPqiiiiiiiiP")
-_KV8_ATTN_PARAMS = struct.Struct("@NPqqPPPPqPqiPPiiiiiiiifPPPPNP")
+_LETTERS = {_c.c_size_t: "N", _c.c_int: "i", _c.c_int64: "q", _c.c_float: "f", _c.c_void_p: "P"}
+
+
+def _packed(structure) -> struct.Struct:
+    """A C structure packed in one call (native sizes and alignment) instead of built field by field."""
+    packed = struct.Struct("@" + "".join(_LETTERS[t] for _, t in structure._fields_))
+    assert packed.size == ctypes.sizeof(structure)
+    return packed
+
+
+_ROPE_PARAMS = _packed(SmlaRopeParams)
+_KV8_ATTN_PARAMS = _packed(SmlaKv8AttnParams)
 
 
 def smla_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, cos_sin_cache: torch.Tensor, *,
