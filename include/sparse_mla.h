@@ -366,6 +366,7 @@ SMLA_API smla_status sparse_mla_fwd_no_alloc(const void *q, const void *kv_cache
  * workspace              device, smla_build_block_tables_workspace_size(B)
  *                        bytes, 16-byte aligned; need not be initialised.
  *                        Calls that overlap in time must not share it.
+ * B and table_width at most 2^30, B * table_width and num_tokens below 2^31.
  */
 SMLA_API size_t smla_build_block_tables_workspace_size(int B);
 SMLA_API smla_status smla_build_block_tables(const int32_t *seq_lens, const int32_t *query_lens,
@@ -541,7 +542,7 @@ SMLA_API smla_status smla_kv8_append(const void *k, int64_t k_stride_t, int64_t 
  *               device), 256-byte aligned, need not be initialised.
  *               Calls that overlap in time must not share it.
  * H a multiple of H_kv; B >= 0, T >= 0 (0: a no-op); 0 <= window;
- * num_blocks * H_kv below 2^31, table_width * block_size at most 2^30.
+ * num_blocks * H_kv below 2^31, B and table_width * block_size at most 2^30.
  */
 typedef struct smla_kv8_attn_params {
     size_t size; /* sizeof(smla_kv8_attn_params) */

@@ -44,6 +44,7 @@ size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + 
 bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) * max_query_len <= 16; }
 
 constexpr int64_t kMostPositions = 1 << 30; // of a block table
+constexpr int kMostRequests = 1 << 30, kMostWidth = 1 << 30; // loops over them step past their ends in 31 bits
 
 size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int64_t positions, int sms)
 {
@@ -58,7 +59,7 @@ smla_status check_kv8_shape(int B, int T, int H, int H_kv, int D, int max_query_
     if (D != 64 && D != 128)
         return SMLA_ERR_UNSUPPORTED;
     // row and unit counts stay in 31 bits
-    if ((int64_t)T * (H / H_kv) > INT_MAX / 2 || ((int64_t)T * (H / H_kv) / 8 + B) * H_kv > INT_MAX)
+    if (B > kMostRequests || (int64_t)T * (H / H_kv) > INT_MAX / 2 || ((int64_t)T * (H / H_kv) / 8 + B) * H_kv > INT_MAX)
         return SMLA_ERR_UNSUPPORTED;
     return SMLA_OK;
 }
@@ -67,7 +68,10 @@ smla_status check_kv8_shape(int B, int T, int H, int H_kv, int D, int max_query_
 
 extern "C" {
 
-SMLA_API size_t smla_build_block_tables_workspace_size(int B) { return B < 0 ? (size_t)-1 : tables_workspace(B); }
+SMLA_API size_t smla_build_block_tables_workspace_size(int B)
+{
+    return B < 0 || B > kMostRequests ? (size_t)-1 : tables_workspace(B);
+}
 
 SMLA_API smla_status smla_build_block_tables(const int32_t *seq_lens, const int32_t *query_lens,
                                              const int32_t *blocks_held, int32_t *blocks_held_out, int B,
@@ -80,7 +84,8 @@ SMLA_API smla_status smla_build_block_tables(const int32_t *seq_lens, const int3
 {
     if (B < 0 || num_tokens < 0 || num_tokens > INT_MAX || table_width < 0 || table_stride < table_width || ring_size < 1)
         return SMLA_ERR_BAD_SHAPE;
-    if (block_shift(block_size) < 0)
+    // (with B * table_width, what is given back stays in 31 bits whatever blocks_held says)
+    if (block_shift(block_size) < 0 || B > kMostRequests || table_width > kMostWidth || (int64_t)B * table_width > INT_MAX)
         return SMLA_ERR_UNSUPPORTED;
     if (ring_state == nullptr || ring_state_out == nullptr || query_start == nullptr || counts == nullptr ||
         free_ring == nullptr || workspace == nullptr ||
