@@ -260,7 +260,7 @@ cudaError_t launch_vec(const RopeArgs &a, int sm_count, cudaStream_t stream)
         y = std::max(1, std::min(std::min(128 / x, 64), (heads + batch - 1) / batch));
         groups = std::min<int64_t>((heads + y - 1) / y, std::max<int64_t>(1, (int64_t)8 * sm_count / a.T));
     }
-    const dim3 grid((unsigned)((a.T + z - 1) / z), (unsigned)std::min<int64_t>(groups, 65535)), block(x, y, z);
+    const dim3 grid((unsigned)(((int64_t)a.T + z - 1) / z), (unsigned)std::min<int64_t>(groups, 65535)), block(x, y, z);
     if (a.neox)
         rope_kernel<E, kVec, true><<<grid, block, 0, stream>>>(a);
     else
