@@ -482,7 +482,8 @@ SMLA_API smla_status smla_rope(const smla_rope_params *params);
  * (0 if there is none) and s_new = max(amax / 448, 2^-60), in binary32:
  *   - if the run's smallest offset o is above 0, the block holds o older tokens:
  *     scale = max(old scale, s_new), and when it grew their codes become
- *     E4M3_RNE(code * old / scale); otherwise scale = s_new;
+ *     E4M3_RNE(code * old / scale); otherwise scale = s_new (so rows of zeros
+ *     change no block that holds other rows);
  *   - the run's codes are E4M3_RNE_satfinite(x / scale) (infinities saturate,
  *     NaN is the NaN code).
  * A negative slot skips its token (and ends a run); a slot >= num_blocks *

@@ -8,9 +8,10 @@
 // lane reads of a run (kHeld 16-byte pieces) stays in registers between the two
 // passes; what is beyond is read again (from L2). Bound: 2 bytes read and 1
 // written per element. Measured: a prompt of 8192 tokens, 8 kv heads of 128 columns
-// (50 MB) in 20.5 us on the device, 2.4 TB/s, bound by instructions (0.6 of the issue
-// slots: four values take some ten, two conversions to bracket each quotient among
-// them); one token for each of 64 requests in 4.5 us on the device, in an 11 us call.
+// (50 MB) in 20.5 us on the device, 2.4 TB/s: 2048 blocks in 2.7 waves, each with its
+// slots' scan, loads, two meetings, quotients and stores one after another (0.6 of the
+// issue slots: four values take some ten, two conversions to bracket each quotient among
+// them); one token for each of 64 requests in 4.5 us on the device, in a 17 us call.
 #include "smla_device.cuh"
 #include "smla_step.h"
 

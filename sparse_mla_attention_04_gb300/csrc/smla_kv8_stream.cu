@@ -38,7 +38,7 @@
 // another's, whose block may hold nothing of that size, lost all but a few bits.
 //
 // Measured: 64 requests of up to 32768 positions (1.08 GB of codes, 32 heads on 8 kv
-// heads of 128 columns) in 188 us, 5.7 TB/s, 85% of the copy bandwidth; one request of
+// heads of 128 columns) in 189 us, 5.7 TB/s, 84% of the copy bandwidth; one request of
 // 509 positions in 23 us a call, of which the two kernels take about 10. Steps of 64
 // positions, cp.async copies and binary16 products for S took 253 us; equal parts
 // without the small ones 196.

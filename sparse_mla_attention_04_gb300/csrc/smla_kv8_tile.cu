@@ -42,11 +42,11 @@
 // conflict). Blocks outside the pool are zero-filled and not read.
 //
 // Bound and measured. A prompt of 8192 tokens, 32 heads on 8 kv heads of 128
-// columns: 0.440 ms, 1.25 PFLOP/s (66% of the measured bf16 rate; the products alone
-// keep the tensor pipe busy for 53% of it, S being bound by what its operands
+// columns: 0.442 ms, 1.24 PFLOP/s (65% of the measured bf16 rate; the products alone
+// keep the tensor pipe busy for 55% of it, S being bound by what its operands
 // take from shared memory: 49 cycles for 64 columns against 32). Six chunks of 45 to
 // 701 tokens behind 2114 to 32001 positions, 16 heads on 2 kv heads of 64 columns,
-// blocks of 16: 236 us, 0.76 PFLOP/s; there a tile has half the products for the same
+// blocks of 16: 238 us, 0.76 PFLOP/s; there a tile has half the products for the same
 // softmax, whose instructions (some 300 a tile and warp, with four exponentials a
 // cycle of a sub-core) take over half of the issue slots. What counted on the way:
 // short loops (eight to sixteen warps run five different pieces of code, and what is

@@ -71,7 +71,7 @@ struct Kv8AppendArgs {
     uint8_t *k_cache, *v_cache; // [num_blocks, H_kv, block_size, D]
     float *k_scale, *v_scale;   // [num_blocks, H_kv]
     int64_t num_blocks;
-    int window; // tokens whose runs one warp takes (set by the launch)
+    int window; // tokens whose runs one block takes (set by the launch)
 };
 cudaError_t launch_kv8_append(const Kv8AppendArgs &a, int D, int sm_count, cudaStream_t stream);
 cudaError_t read_append_error(int *out, bool reset);

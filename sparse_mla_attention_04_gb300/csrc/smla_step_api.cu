@@ -38,9 +38,11 @@ size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + 
 
 // Rows of a request that the streaming kernel takes in one unit; more go to the tile
 // kernel. 64 requests of 4096 positions, 4 kv heads of 128 columns: 8 rows 73 us against
-// 88 by the tile kernel, 16 rows 92 against 92 (32 requests of 16384: 156 against 136;
-// one of 32768: 37 against 56); 20 rows, 32 requests of 8192 and 8 kv heads: 288 against
-// 143, since K and V are read twice.
+// 88 by the tile kernel, 16 rows 92 against 92 (one of 32768: 37 against 56; but 32
+// requests of 16384: 156 against 136); 20 rows, 32 requests of 8192 and 8 kv heads: 288
+// against 143, since K and V are read twice and the second unit, of 4 rows, is not full.
+// By the bound alone: requests with fewer rows than it says have units that are not full,
+// whose steps all go through the masks (8 rows under a bound of 16: 293 against 141).
 bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) * max_query_len <= 16; }
 
 constexpr int64_t kMostPositions = 1 << 30; // of a block table
