@@ -155,3 +155,21 @@ def test_large_and_tiny_queries_row_by_row(T):
     q[:, 4] *= 30.0
     q[:, 5, 1:] *= 2.0 ** -12                                  # one element alone
     _check(p, q.to(torch.bfloat16), n, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("T", [1, 7, 60, 200])
+def test_a_context_without_values(T):
+    """Blocks of zeros at the smallest scale: out 0, and the lse as ever. There the logits in log2 units have -60
+    added and the denominator is about 2^66: a rounding of 2^-19 and a logarithm of 2^-22 times 66, times ln 2."""
+    H, hk, D, bs, n = 4, 2, 64, 16, 200
+    g = torch.Generator().manual_seed(T)
+    k = torch.randn((n, hk, D), generator=g).to(torch.bfloat16)
+    cache = binding.new_kv8_cache(14, hk, bs, D)
+    binding.smla_kv8_append(k.to(DEV), torch.zeros_like(k).to(DEV), torch.arange(n, device=DEV), *cache)
+    p = dict(zip(("kc", "vc", "ks", "vs"), (x.cpu() for x in cache)), table=torch.arange(14, dtype=torch.int32)[None])
+    q = torch.randn((T, H, D), generator=g).to(torch.bfloat16)
+    out, lse = _run(p, q, n, 0.125)
+    assert bool((out == 0).all())
+    p["table"] = p["table"][:, :-(-n // bs)]
+    _, z, _, ztol = _expect(p, q, n, 0.125)
+    assert bool(((lse - z).abs() <= ztol + 2.0 ** -16).all()), float((lse - z).abs().max())
