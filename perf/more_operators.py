@@ -212,6 +212,9 @@ def prepare(case, seed):
         count = np.where(r.rand(c["B"]) < 0.05, 0, count)
         for b in range(c["B"]):
             kept[b, :count[b]] = np.sort(r.choice(int(ql[b]), int(count[b]), replace=False))
+        if own:  # what a program keeps beside its caches
+            from sparse_mla_attention_04_gb300 import binding
+            s["handle"] = binding.TokenPools(s["caches"], c["bs"])
         s.update(table=table, lens=_up(lens), ql=_up(ql), kept=_up(kept), count=_up(count), lens_out=torch.empty(c["B"], dtype=torch.int32, device=DEV))
     elif c["op"] == "fork":
         s.update(_fork_inputs(c, r))
@@ -228,6 +231,9 @@ def prepare(case, seed):
         same = r.rand(c["n"]) < 0.3  # one block is often copied several times
         src = np.where(same & ~none, perm[0], src)
         s.update(src=_up(src), dst=_up(dst))
+        if own:
+            from sparse_mla_attention_04_gb300 import binding
+            s["handle"] = binding.BlockPools(s["pools"])
     return s
 
 
@@ -296,13 +302,13 @@ def _own(s):
         q, k = b.smla_qk_norm_rope(s["q"], s["k"], s["wq"], s["wk"], s["pos"], s["cs"], eps=1e-6, weight_offset=c["plus"], rot_offset=c["off"], is_neox=c["half"])
         return {"q": q, "k": k}
     if c["op"] == "keep":
-        b.smla_keep_tokens(s["caches"], s["table"], s["lens"], s["ql"], s["kept"], s["count"], block_size=c["bs"], seq_lens_out=s["lens_out"])
+        b.smla_keep_tokens(s["handle"], s["table"], s["lens"], s["ql"], s["kept"], s["count"], seq_lens_out=s["lens_out"])
         return _kept(s, s["lens_out"])
     if c["op"] == "fork":
         f = b.smla_fork_block_tables(s["source"], s["keep"], s["held"], s["table"], s["ring"], s["state"], block_size=c["bs"], num_blocks=s["cap"], block_table_out=s["table_out"],
                                      blocks_held_out=s["held_out"], ring_state_out=s["state_out"], copy_from=s["src"], copy_to=s["dst"], counts=s["counts"])
         return {"table": f.block_table, "held": f.blocks_held, "ring": s["ring"], "state": f.ring_state, "src": f.copy_from, "dst": f.copy_to, "counts": f.counts}
-    b.smla_copy_blocks(s["pools"], s["src"], s["dst"])
+    b.smla_copy_blocks(s["handle"], s["src"], s["dst"])
     return _copied(s)
 
 
