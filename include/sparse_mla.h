@@ -574,15 +574,252 @@ SMLA_API size_t smla_kv8_attn_workspace_size_of(const smla_kv8_attn_params *para
 SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *params);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Steps that draft and branch: norms of queries and keys with their rotation, trees
+ * of drafted tokens verified at once, their accepted tokens kept, and requests whose
+ * block tables go on from one another (samples of one prompt, beams).
+ * ---------------------------------------------------------------------------
+ *
+ * Root-mean-square norms of each query and key head, and smla_rope's rotation behind
+ * them, in one pass. For token t and head h of q (and of k with k_weight):
+ *   y_d = x_d r (weight_d + weight_offset), r = (mean over the head's D columns of
+ *   x^2 + eps)^-1/2, then the columns [rot_offset, rot_offset + rot_dim) turned as
+ * smla_rope turns them, in binary32 (squares that pass it are taken of the row scaled
+ * by a power of two), rounded once to the type. A head with an infinity has zeros
+ * beside it and NaN in its place, one with a NaN is all NaN, and what is rotated with
+ * a NaN is one.
+ *
+ * q, k, q_out, k_out, positions, cos_sin_cache, T, H, H_k, D, rot_dim, rot_offset,
+ *              is_neox: as for smla_rope (strided, in place, q alone, tokens out of
+ *              range not written and bit 4 of smla_device_error set).
+ * q_weight, k_weight  device, of weight_dtype (dtype, or SMLA_F32): [D] for all heads
+ *              (stride_h 0) or a row of D to a head, stride_h elements apart; NULL:
+ *              factors of 1 (weight_offset is not added).
+ * weight_offset  finite; 1 for weights that are held less one.
+ * eps          finite, at least 2^-100.
+ */
+typedef struct smla_qk_norm_rope_params {
+    size_t size; /* sizeof(smla_qk_norm_rope_params) */
+    int dtype, weight_dtype;
+    const void *q;
+    int64_t q_stride_t, q_stride_h;
+    void *q_out;
+    int64_t q_out_stride_t, q_out_stride_h;
+    const void *k;
+    int64_t k_stride_t, k_stride_h;
+    void *k_out;
+    int64_t k_out_stride_t, k_out_stride_h;
+    const void *q_weight;
+    int64_t q_weight_stride_h;
+    const void *k_weight;
+    int64_t k_weight_stride_h;
+    float weight_offset, eps;
+    const int64_t *positions;
+    const float *cos_sin_cache;
+    int64_t max_position;
+    int T, H, H_k, D, rot_dim, rot_offset, is_neox;
+    smla_stream_t stream;
+} smla_qk_norm_rope_params;
+
+SMLA_API smla_status smla_qk_norm_rope(const smla_qk_norm_rope_params *params);
+
+/*
+ * Masks and positions of drafted trees. A request's new tokens are the nodes of its
+ * tree, in the order of the flat tokens [query_start[b], query_start[b + 1]); they lie
+ * in the cache behind its context as any new tokens do, at ctx + i with ctx =
+ * seq_lens[b] - (their number). parents[t] is the number in the tree of the node that
+ * token t follows, -1 where it follows the context; it is below its own. Token t's
+ * mask has the bits of itself and of the nodes that it descends from (bit i % 64 of
+ * word i / 64 for node i), with window > 0 only of those fewer than `window`
+ * generations up; its position is ctx + the number of nodes that it descends from (0
+ * if that is negative).
+ *
+ * parents      device, int32 [T]. One that is not in [-1, its own number) counts as
+ *              -1, and sets bit 16 of smla_device_error.
+ * seq_lens     device, int32 [B]; query_start int32 [B + 1], ascending, within [0, T].
+ * tree_words   1..16: 64-bit words of a mask. Nodes from 64 tree_words on have an empty
+ *              mask and position ctx, and set bit 16 of smla_device_error.
+ * tree_mask    device, uint64 [T, tree_words], 8-byte aligned; positions device, int64
+ *              [T]; both written, with 0 for rows behind the last request.
+ */
+SMLA_API smla_status smla_build_tree_masks(const int32_t *parents, const int32_t *seq_lens,
+                                           const int32_t *query_start, int B, int T, int tree_words, int window,
+                                           uint64_t *tree_mask, int64_t *positions, smla_stream_t stream);
+
+/*
+ * smla_kv8_attn_fwd for trees of drafted tokens: token t of request b sees the context
+ * [0, ctx) (ctx = seq_lens[b] - its number of new tokens; with window > 0 the
+ * positions above positions[t] - window of it) and those of its request's new tokens
+ * whose bits are set in its row of tree_mask: position ctx + i for bit i % 64 of word
+ * i / 64, whether before or behind it, itself included only by its own bit; the window
+ * does not apply to them. Bits of nodes that the request does not have are not looked
+ * at, nodes without a bit are seen by none. Everything else (masked rows, sinks, pages
+ * outside the pool, precision, workspace) is as for smla_kv8_attn_fwd, whose causal
+ * mask is that of trees without branches.
+ *
+ * attn         the call; its `size` is sizeof(smla_kv8_attn_params), its workspace by
+ *              smla_kv8_attn_workspace_size(_of).
+ * tree_mask    device, uint64 [T, tree_words], 8-byte aligned; tree_words 1..2^20.
+ * positions    device, int64 [T], or NULL without a window: the tokens' positions in
+ *              their branches. One outside [ctx, seq_lens[b]) counts as the nearest.
+ */
+typedef struct smla_kv8_tree_attn_params {
+    size_t size; /* sizeof(smla_kv8_tree_attn_params) */
+    smla_kv8_attn_params attn;
+    const uint64_t *tree_mask;
+    int tree_words;
+    const int64_t *positions;
+} smla_kv8_tree_attn_params;
+
+SMLA_API smla_status smla_kv8_tree_attn_fwd(const smla_kv8_tree_attn_params *params);
+
+/*
+ * Keeps some of each request's new tokens (the accepted path of a drafted tree): the
+ * cache rows of the kept ones move together behind the context, in every layer's pools
+ * at once and in place, and seq_lens_out[b] = ctx + their number is the request's new
+ * length, ctx = seq_lens[b] - query_lens[b] (query_lens clamped to [0, seq_lens]). Kept
+ * token i of request b is its new token kept[b, i]: the row of position ctx + kept[b, i]
+ * goes to position ctx + i, both found through block_table. The numbers ascend strictly
+ * and lie below query_lens[b]; the first that does not ends the list and sets bit 16 of
+ * smla_device_error, as does a kept_lens[b] above the most there can be (which is cut).
+ * Rows whose old or new block is outside the pool do not move. The blocks written to
+ * must be this request's alone (see smla_fork_block_tables), and no block may stand
+ * twice in its row.
+ *
+ * scales NULL: rows of row_bytes bytes as they are (a multiple of 8, at most 65536), in
+ * pools [num_blocks, heads, block_size, row_bytes]: the latent cache with heads = 1.
+ * Otherwise the block-scaled cache: each K and each V is a pool of codes
+ * [num_blocks, heads, block_size, D] with row_bytes = D = 64 or 128, and its scales
+ * [num_blocks, heads]. There the scale of a block that rows go to becomes the largest
+ * of its own and of those of the blocks that they come from; if that is larger, the
+ * older codes in it (below the first row that is moved there) become
+ * E4M3_RNE(code * old / scale), as do all moved ones whose block's scale was another:
+ * codes under the same scale are copied. (Two operations in binary32, then the
+ * rounding; positive scales.) Rows of the block behind the kept ones are left as they
+ * are.
+ *
+ * block_table  device, int32 [B, table_width], row stride table_stride; positions past
+ *              it do not move.
+ * seq_lens, query_lens, kept_lens  device, int32 [B]; kept int32 [B, kept_width], row
+ *              stride kept_stride.
+ * seq_lens_out device, int32 [B], or NULL; none of the other lengths.
+ * pools, scales  arrays on the HOST, [num_pools], of device pointers: 16-byte aligned
+ *              (rows as they are: 8), scales 4-byte. Read during the call only.
+ * B * heads below 2^24, table_width * block_size at most 2^30.
+ */
+typedef struct smla_keep_tokens_params {
+    size_t size; /* sizeof(smla_keep_tokens_params) */
+    const int32_t *block_table;
+    int64_t table_stride;
+    int table_width;
+    const int32_t *seq_lens, *query_lens, *kept;
+    int64_t kept_stride;
+    int kept_width;
+    const int32_t *kept_lens;
+    int32_t *seq_lens_out;
+    int B, heads, block_size, row_bytes;
+    int64_t num_blocks;
+    int num_pools;
+    void *const *pools;
+    float *const *scales;
+    smla_stream_t stream;
+} smla_keep_tokens_params;
+
+SMLA_API smla_status smla_keep_tokens(const smla_keep_tokens_params *params);
+
+/*
+ * Block tables that go on from others: new row b holds the first blocks of old row
+ * source_rows[b] (shared with it and with whatever other rows hold them), as many as
+ * its first n = seq_lens[b] tokens need (at most those that blocks_held says are
+ * there); source_rows[b] outside [0, B_old) makes an empty row. One call forks requests
+ * (several rows from one), reorders beams, cuts requests back, ends them:
+ *   - a last block that is not full will be written to, so it must be its row's alone.
+ *     Where other new rows hold it as well, one that holds it full keeps it, else the
+ *     first row that ends in it; every other row that ends in it gets a new block, the
+ *     free ring's next (rows in order), and copy_from[b], copy_to[b] name both blocks
+ *     for smla_copy_blocks (-1, -1 for rows that need no copy);
+ *   - blocks of the old rows that no new row holds go back to the ring, behind its end,
+ *     each once, in the order of their first places (old rows in order, then entries).
+ * The ring is that of smla_build_block_tables. Nothing is counted between calls: every
+ * row that holds blocks is among the old rows, and every old row that is to live on is
+ * some new row's source. Rows that share blocks end and shrink by this call;
+ * smla_build_block_tables may then let all rows grow (but would give a shared block back
+ * while others hold it). If the ring holds too few blocks, counts[3] says how many lack,
+ * the copies are all -1 and nothing else changes (block_table_out and blocks_held_out
+ * are not written).
+ *
+ * source_rows, seq_lens  device, int32 [B].
+ * blocks_held  device, int32 [B_old]; block_table device, int32 [B_old, table_width],
+ *              row stride table_stride.
+ * blocks_held_out  device, int32 [B], block_table_out device, int32 [B, table_width],
+ *              row stride table_out_stride: written (the entries of blocks held; others
+ *              keep what they hold). They must not overlap the old ones.
+ * num_blocks   of the pool: entries outside [0, num_blocks) are carried on, never
+ *              copied and never given back.
+ * free_ring, ring_size, ring_state, ring_state_out  as for smla_build_block_tables.
+ * copy_from, copy_to  device, int32 [B], written.
+ * counts       device, int32 [4], written: tokens that the new rows hold, blocks taken,
+ *              given back, lacking.
+ * workspace    device, smla_fork_block_tables_workspace_size(...) bytes, 16-byte
+ *              aligned; need not be initialised. Calls that overlap in time must not
+ *              share it.
+ * B, B_old and table_width at most 2^30, their products with table_width below 2^31,
+ * table_width * block_size at most 2^30, num_blocks below 2^31.
+ */
+typedef struct smla_fork_block_tables_params {
+    size_t size; /* sizeof(smla_fork_block_tables_params) */
+    const int32_t *source_rows, *seq_lens;
+    int B;
+    const int32_t *blocks_held;
+    int B_old;
+    const int32_t *block_table;
+    int64_t table_stride;
+    int32_t *blocks_held_out;
+    int32_t *block_table_out;
+    int64_t table_out_stride;
+    int table_width, block_size;
+    int64_t num_blocks;
+    int32_t *free_ring;
+    int ring_size;
+    const int32_t *ring_state;
+    int32_t *ring_state_out;
+    int32_t *copy_from, *copy_to, *counts;
+    void *workspace;
+    size_t workspace_bytes;
+    smla_stream_t stream;
+} smla_fork_block_tables_params;
+
+/* (size_t)-1 on invalid arguments. */
+SMLA_API size_t smla_fork_block_tables_workspace_size(int B_old, int B, int table_width, int64_t num_blocks);
+SMLA_API smla_status smla_fork_block_tables(const smla_fork_block_tables_params *params);
+
+/*
+ * Copies blocks within each of several pools (every layer's keys, values and scales in
+ * one call): block copy_from[i] to block copy_to[i], i < n. A pair with a number outside
+ * [0, num_blocks), or the same twice, copies nothing. A block that is copied to must not
+ * stand among the others of either list that copy (a block may be copied from many
+ * times).
+ *
+ * pools, block_bytes  arrays on the HOST, [num_pools]: the device pointer to a pool and
+ *              the bytes of one of its blocks (any; whole 16-byte pieces move fastest).
+ *              Read during the call only.
+ * copy_from, copy_to  device, int32 [n].
+ */
+SMLA_API smla_status smla_copy_blocks(void *const *pools, const int64_t *block_bytes, int num_pools,
+                                      const int32_t *copy_from, const int32_t *copy_to, int n, int64_t num_blocks,
+                                      smla_stream_t stream);
+
+/*
  * Error word of the device-side checks (0 = none). The tcgen05 kernels wait on
  * the tensor core and on their own warps with a time limit (about 2 s); a wait
  * that gives up sets a bit here (1 = an awaited barrier never completed,
  * 2 = the copies or MMAs in flight did not drain), abandons the call's
  * arithmetic, frees its tensor memory and returns, leaving the context usable.
- * smla_fused_qk_rope_cache and smla_rope set 4 for a position outside
- * [0, max_position); smla_fused_qk_rope_cache and smla_kv8_append set 8 for a
- * slot past the pool. smla_kv8_attn_fwd's waits for its copies and products have
- * the same limit and bits. Synchronous (copies the word from the device):
+ * smla_fused_qk_rope_cache, smla_rope and smla_qk_norm_rope set 4 for a position
+ * outside [0, max_position); smla_fused_qk_rope_cache and smla_kv8_append set 8 for a
+ * slot past the pool; smla_build_tree_masks and smla_keep_tokens set 16 for trees and
+ * lists of kept tokens that are none. The waits of smla_kv8_attn_fwd and
+ * smla_kv8_tree_attn_fwd for their copies and products have the same limit and bits. Synchronous (copies the word from the device):
  * unlike every other entry point it waits for the device, since the word is
  * read on the host. reset != 0 clears it.
  */

@@ -15,7 +15,7 @@ import functools
 import os
 import struct
 import threading
-from typing import NamedTuple, Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -86,6 +86,14 @@ SIGNATURES = {
     "smla_kv8_attn_workspace_size": ([_c.c_int] * 6, _c.c_size_t),
     "smla_kv8_attn_workspace_size_of": ([_c.c_void_p], _c.c_size_t),
     "smla_kv8_attn_fwd": ([_c.c_void_p], _c.c_int),
+    "smla_qk_norm_rope": ([_c.c_void_p], _c.c_int),
+    "smla_build_tree_masks": ([_c.c_void_p] * 3 + [_c.c_int] * 4 + [_c.c_void_p] * 3, _c.c_int),
+    "smla_kv8_tree_attn_fwd": ([_c.c_void_p], _c.c_int),
+    "smla_keep_tokens": ([_c.c_void_p], _c.c_int),
+    "smla_fork_block_tables_workspace_size": ([_c.c_int] * 3 + [_c.c_int64], _c.c_size_t),
+    "smla_fork_block_tables": ([_c.c_void_p], _c.c_int),
+    "smla_copy_blocks": ([_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64,
+                          _c.c_void_p], _c.c_int),
     "sparse_mla_fwd_no_alloc": ([_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_void_p,
                                  _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int64, _c.c_int,
                                  _c.c_float, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_int,
@@ -137,6 +145,48 @@ class SmlaKv8AttnParams(ctypes.Structure):
                 ("D", _c.c_int), ("block_size", _c.c_int), ("max_query_len", _c.c_int), ("window", _c.c_int),
                 ("scale", _c.c_float), ("sinks", _c.c_void_p), ("out", _c.c_void_p), ("lse", _c.c_void_p),
                 ("workspace", _c.c_void_p), ("workspace_bytes", _c.c_size_t), ("stream", _c.c_void_p)]
+
+
+class SmlaQkNormRopeParams(ctypes.Structure):
+    """smla_qk_norm_rope_params of include/sparse_mla.h."""
+    _fields_ = [("size", _c.c_size_t), ("dtype", _c.c_int), ("weight_dtype", _c.c_int), ("q", _c.c_void_p),
+                ("q_stride_t", _c.c_int64), ("q_stride_h", _c.c_int64), ("q_out", _c.c_void_p),
+                ("q_out_stride_t", _c.c_int64), ("q_out_stride_h", _c.c_int64), ("k", _c.c_void_p),
+                ("k_stride_t", _c.c_int64), ("k_stride_h", _c.c_int64), ("k_out", _c.c_void_p),
+                ("k_out_stride_t", _c.c_int64), ("k_out_stride_h", _c.c_int64), ("q_weight", _c.c_void_p),
+                ("q_weight_stride_h", _c.c_int64), ("k_weight", _c.c_void_p), ("k_weight_stride_h", _c.c_int64),
+                ("weight_offset", _c.c_float), ("eps", _c.c_float), ("positions", _c.c_void_p),
+                ("cos_sin_cache", _c.c_void_p), ("max_position", _c.c_int64), ("T", _c.c_int), ("H", _c.c_int),
+                ("H_k", _c.c_int), ("D", _c.c_int), ("rot_dim", _c.c_int), ("rot_offset", _c.c_int),
+                ("is_neox", _c.c_int), ("stream", _c.c_void_p)]
+
+
+class SmlaKv8TreeAttnParams(ctypes.Structure):
+    """smla_kv8_tree_attn_params of include/sparse_mla.h."""
+    _fields_ = [("size", _c.c_size_t), ("attn", SmlaKv8AttnParams), ("tree_mask", _c.c_void_p), ("tree_words", _c.c_int),
+                ("positions", _c.c_void_p)]
+
+
+class SmlaKeepTokensParams(ctypes.Structure):
+    """smla_keep_tokens_params of include/sparse_mla.h."""
+    _fields_ = [("size", _c.c_size_t), ("block_table", _c.c_void_p), ("table_stride", _c.c_int64),
+                ("table_width", _c.c_int), ("seq_lens", _c.c_void_p), ("query_lens", _c.c_void_p), ("kept", _c.c_void_p),
+                ("kept_stride", _c.c_int64), ("kept_width", _c.c_int), ("kept_lens", _c.c_void_p),
+                ("seq_lens_out", _c.c_void_p), ("B", _c.c_int), ("heads", _c.c_int), ("block_size", _c.c_int),
+                ("row_bytes", _c.c_int), ("num_blocks", _c.c_int64), ("num_pools", _c.c_int), ("pools", _c.c_void_p),
+                ("scales", _c.c_void_p), ("stream", _c.c_void_p)]
+
+
+class SmlaForkBlockTablesParams(ctypes.Structure):
+    """smla_fork_block_tables_params of include/sparse_mla.h."""
+    _fields_ = [("size", _c.c_size_t), ("source_rows", _c.c_void_p), ("seq_lens", _c.c_void_p), ("B", _c.c_int),
+                ("blocks_held", _c.c_void_p), ("B_old", _c.c_int), ("block_table", _c.c_void_p),
+                ("table_stride", _c.c_int64), ("blocks_held_out", _c.c_void_p), ("block_table_out", _c.c_void_p),
+                ("table_out_stride", _c.c_int64), ("table_width", _c.c_int), ("block_size", _c.c_int),
+                ("num_blocks", _c.c_int64), ("free_ring", _c.c_void_p), ("ring_size", _c.c_int),
+                ("ring_state", _c.c_void_p), ("ring_state_out", _c.c_void_p), ("copy_from", _c.c_void_p),
+                ("copy_to", _c.c_void_p), ("counts", _c.c_void_p), ("workspace", _c.c_void_p),
+                ("workspace_bytes", _c.c_size_t), ("stream", _c.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -779,15 +829,23 @@ def smla_rope_cos_sin_cache(num_positions: int, rot_dim: int, *, base: float = 1
 _LETTERS = {_c.c_size_t: "N", _c.c_int: "i", _c.c_int64: "q", _c.c_float: "f", _c.c_void_p: "P"}
 
 
+def _letters(structure) -> str:
+    return "".join(_letters(t) if hasattr(t, "_fields_") else _LETTERS[t] for _, t in structure._fields_)
+
+
 def _packed(structure) -> struct.Struct:
     """A C structure packed in one call (native sizes and alignment) instead of built field by field."""
-    packed = struct.Struct("@" + "".join(_LETTERS[t] for _, t in structure._fields_))
+    packed = struct.Struct("@" + _letters(structure))
     assert packed.size == ctypes.sizeof(structure)
     return packed
 
 
 _ROPE_PARAMS = _packed(SmlaRopeParams)
 _KV8_ATTN_PARAMS = _packed(SmlaKv8AttnParams)
+_KV8_TREE_ATTN_PARAMS = _packed(SmlaKv8TreeAttnParams)
+_QK_NORM_ROPE_PARAMS = _packed(SmlaQkNormRopeParams)
+_KEEP_TOKENS_PARAMS = _packed(SmlaKeepTokensParams)
+_FORK_PARAMS = _packed(SmlaForkBlockTablesParams)
 
 
 def smla_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, cos_sin_cache: torch.Tensor, *,
@@ -895,22 +953,8 @@ def smla_kv8_attn_workspace_size(B: int, T: int, H: int, H_kv: int, D: int, max_
     return int(n)
 
 
-def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
-                      v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
-                      query_start: torch.Tensor, scale: float, *, max_query_len: int, window: int = 0,
-                      sinks: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                      lse: Optional[torch.Tensor] = None, return_lse: bool = True,
-                      workspace: Optional[torch.Tensor] = None,
-                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """Causal attention of each request's last tokens over its pages of the
-    block-scaled cache: out [T, H, D] (bf16) and lse [T, H] (fp32).
-
-    q bf16 [T, H, D] (rows may be strided); the caches and scales as for
-    smla_kv8_append, H a multiple of H_kv; block_table int32 [B, width] (rows
-    may be strided); seq_lens int32 [B]; query_start int32 [B + 1] (rows of q
-    past query_start[B] are left alone); max_query_len: a bound of the requests'
-    tokens in q; window > 0: each token sees its last `window` positions; sinks
-    fp32 [H]: logits that join the denominator."""
+def _kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, scale, max_query_len, window, sinks,
+              out, lse, return_lse, workspace, stream, tree_mask, positions):
     num_blocks, H_kv, block_size, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     dev = k_cache.device
     _rows(q, "q", torch.bfloat16, 3, dev)
@@ -930,6 +974,16 @@ def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         _fits(sinks, "sinks", torch.float32, 1, dev)
         if sinks.shape[0] != H:
             raise ValueError("sinks must be [H]")
+    if tree_mask is not None:
+        _fits(tree_mask, "tree_mask", torch.int64, 2, dev)
+        if tree_mask.shape[0] != T:
+            raise ValueError("tree_mask must be [T, words], T = %d" % T)
+        if positions is not None:
+            _fits(positions, "positions", torch.int64, 1, dev)
+            if positions.shape[0] != T:
+                raise ValueError("positions must be [T] = [%d]" % T)
+        elif window > 0:
+            raise ValueError("a window needs the tokens' positions")
     L = _lib or lib()
     with _on(dev, stream) as handle:
         out = _out(out, "out", (T, H, D), torch.bfloat16, dev)
@@ -941,15 +995,41 @@ def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
             need = 256  # (the call says what is wrong)
         workspace, ws_bytes = _workspace(workspace, need, dev)
         qs = q.stride()
-        st = L.smla_kv8_attn_fwd(_KV8_ATTN_PARAMS.pack(
+        attn = (
             _KV8_ATTN_PARAMS.size, q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(),
             k_scale.data_ptr(), v_scale.data_ptr(), num_blocks, block_table.data_ptr(), row_stride, width,
             seq_lens.data_ptr(), query_start.data_ptr(), B, T, H, H_kv, D, block_size, max_query_len, window, scale,
             0 if sinks is None else sinks.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), ws_bytes, handle))
+            workspace.data_ptr(), ws_bytes, handle)
+        if tree_mask is None:
+            st = L.smla_kv8_attn_fwd(_KV8_ATTN_PARAMS.pack(*attn))
+        else:
+            st = L.smla_kv8_tree_attn_fwd(_KV8_TREE_ATTN_PARAMS.pack(
+                _KV8_TREE_ATTN_PARAMS.size, *attn, tree_mask.data_ptr(), tree_mask.shape[1],
+                0 if positions is None else positions.data_ptr()))
     if st:
-        _check(st, "smla_kv8_attn_fwd")
+        _check(st, "smla_kv8_attn_fwd" if tree_mask is None else "smla_kv8_tree_attn_fwd")
     return out, lse
+
+
+def smla_kv8_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                      v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      query_start: torch.Tensor, scale: float, *, max_query_len: int, window: int = 0,
+                      sinks: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal attention of each request's last tokens over its pages of the
+    block-scaled cache: out [T, H, D] (bf16) and lse [T, H] (fp32).
+
+    q bf16 [T, H, D] (rows may be strided); the caches and scales as for
+    smla_kv8_append, H a multiple of H_kv; block_table int32 [B, width] (rows
+    may be strided); seq_lens int32 [B]; query_start int32 [B + 1] (rows of q
+    past query_start[B] are left alone); max_query_len: a bound of the requests'
+    tokens in q; window > 0: each token sees its last `window` positions; sinks
+    fp32 [H]: logits that join the denominator."""
+    return _kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, scale, max_query_len,
+                     window, sinks, out, lse, return_lse, workspace, stream, None, None)
 
 
 def new_kv8_cache(num_blocks: int, H_kv: int, block_size: int, D: int, device="cuda"):
@@ -958,3 +1038,336 @@ def new_kv8_cache(num_blocks: int, H_kv: int, block_size: int, D: int, device="c
     return (torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device),
             torch.ones((num_blocks, H_kv), dtype=torch.float32, device=device),
             torch.ones((num_blocks, H_kv), dtype=torch.float32, device=device))
+
+
+# ---- steps that draft and branch: norms with the rotation, tree masks, kept tokens, forked tables, block copies
+
+
+def smla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
+                      k_weight: Optional[torch.Tensor], positions: torch.Tensor, cos_sin_cache: torch.Tensor, *,
+                      eps: float = 1e-6, weight_offset: float = 0.0, rot_offset: int = 0, is_neox: bool = True,
+                      q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Root-mean-square norm of each head of q [T, H, D] and k [T, H_k, D] (or
+    None), then smla_rope's rotation of its columns [rot_offset, rot_offset +
+    rot_dim), rounded once: x * (mean(x^2) + eps)^-1/2 * (weight + weight_offset).
+    q_weight, k_weight: [D] for all heads or a row to a head ([H, D], [H_k, D]),
+    of the tensors' type or fp32, both of one; None: no factors. The other
+    arguments are smla_rope's; q_out / k_out may be q / k: done in place."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPE:
+        raise TypeError("q must be a bf16, fp16 or fp32 tensor")
+    dtype, dev = q.dtype, q.device
+    _rows(q, "q", dtype, 3)
+    T, H, D = q.shape
+    if k is not None:
+        _rows(k, "k", dtype, 3, dev)
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("k must be [T, H_k, D] = [%d, *, %d], got %s" % (T, D, tuple(k.shape)))
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out or k_weight without k")
+    wtype = dtype
+    weights = []
+    for name, w, x in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
+        if w is None:
+            weights += [0, 0]
+            continue
+        if not isinstance(w, torch.Tensor) or (w.dtype != dtype and w.dtype != torch.float32):
+            raise TypeError("%s must be a tensor of %s or torch.float32" % (name, dtype))
+        if not weights or weights[0] == 0:
+            wtype = w.dtype
+        elif w.dtype != wtype:
+            raise TypeError("q_weight is %s, k_weight %s" % (wtype, w.dtype))
+        _rows(w, name, wtype, w.dim(), dev)
+        if w.shape != (D,) and w.shape != (x.shape[1], D):
+            raise ValueError("%s must be [%d] or [%d, %d], got %s" % (name, D, x.shape[1], D, tuple(w.shape)))
+        weights += [w.data_ptr(), w.stride(0) if w.dim() == 2 else 0]
+    _fits(positions, "positions", torch.int64, 1, dev)
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [T] = [%d]" % T)
+    _fits(cos_sin_cache, "cos_sin_cache", torch.float32, 2, dev)
+    for name, x, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if x is not None and x is not like:
+            _rows(x, name, dtype, 3, dev)
+            if x.shape != like.shape:
+                raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(x.shape)))
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=dtype, device=dev)
+        qs, os = q.stride(), q_out.stride()
+        if k is None:
+            ks = (0, 0, 0, 0, 0, 0)
+            Hk = 0
+        else:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+            Hk = k.shape[1]
+            a, b = k.stride(), k_out.stride()
+            ks = (k.data_ptr(), a[0], a[1], k_out.data_ptr(), b[0], b[1])
+        P, rot = cos_sin_cache.shape
+        st = L.smla_qk_norm_rope(_QK_NORM_ROPE_PARAMS.pack(
+            _QK_NORM_ROPE_PARAMS.size, _DTYPE[dtype], _DTYPE[wtype], q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os[0],
+            os[1], *ks, *weights, weight_offset, eps, positions.data_ptr(), cos_sin_cache.data_ptr(), P, T, H, Hk, D, rot,
+            rot_offset, 1 if is_neox else 0, handle))
+    if st:
+        _check(st, "smla_qk_norm_rope")
+    return q_out, k_out
+
+
+class TreeMasks(NamedTuple):
+    """What smla_build_tree_masks returns (device tensors)."""
+    tree_mask: torch.Tensor  # int64 [T, words]: bit i % 64 of word i / 64 for the tree's node i
+    positions: torch.Tensor  # int64 [T]
+
+
+def smla_build_tree_masks(parents: torch.Tensor, seq_lens: torch.Tensor, query_start: torch.Tensor, *, max_query_len: int,
+                          window: int = 0, tree_mask: Optional[torch.Tensor] = None,
+                          positions: Optional[torch.Tensor] = None, stream=None) -> TreeMasks:
+    """Masks and positions of drafted trees, for smla_kv8_tree_attn_fwd and the
+    rotation. parents int32 [T]: the number (in its request's new tokens) of the
+    node that each token follows, below its own, -1 for the context's end;
+    seq_lens int32 [B] with the new tokens; query_start int32 [B + 1];
+    max_query_len: a bound of a tree's nodes, at most 1024. A token's mask has
+    itself and the nodes that it descends from, with a window only those fewer
+    than `window` generations up."""
+    _need(parents, "parents", torch.int32, 1)
+    dev = parents.device
+    T = parents.shape[0]
+    _fits(seq_lens, "seq_lens", torch.int32, 1, dev)
+    _fits(query_start, "query_start", torch.int32, 1, dev)
+    B = seq_lens.shape[0]
+    if query_start.shape[0] != B + 1:
+        raise ValueError("query_start must be [B + 1] = [%d]" % (B + 1))
+    if max_query_len < 0:
+        raise ValueError("max_query_len must not be negative")
+    words = max(1, (max_query_len + 63) // 64)
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
+        if tree_mask is None and positions is None:
+            both = torch.empty(T * (words + 1), dtype=torch.int64, device=dev)
+            tree_mask, positions = both[:T * words].view(T, words), both[T * words:]
+        else:
+            tree_mask = _out(tree_mask, "tree_mask", (T, words), torch.int64, dev)
+            positions = _out(positions, "positions", (T,), torch.int64, dev)
+        st = L.smla_build_tree_masks(parents.data_ptr(), seq_lens.data_ptr(), query_start.data_ptr(), B, T, words, window,
+                                     tree_mask.data_ptr(), positions.data_ptr(), handle)
+    if st:
+        _check(st, "smla_build_tree_masks")
+    return TreeMasks(tree_mask, positions)
+
+
+def smla_kv8_tree_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                           v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                           query_start: torch.Tensor, tree_mask: torch.Tensor, scale: float, *, max_query_len: int,
+                           window: int = 0, positions: Optional[torch.Tensor] = None,
+                           sinks: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                           workspace: Optional[torch.Tensor] = None,
+                           stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """smla_kv8_attn_fwd for trees of drafted tokens: each of a request's new
+    tokens sees the context before them and, of them, those whose bits are set in
+    its row of tree_mask (int64 [T, words], bit i % 64 of word i / 64 for the
+    request's new token i; smla_build_tree_masks makes it). With a window, a token
+    sees the context's positions above positions[t] - window (int64 [T])."""
+    if tree_mask is None:
+        raise ValueError("tree_mask is needed")
+    return _kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, scale, max_query_len,
+                     window, sinks, out, lse, return_lse, workspace, stream, tree_mask, positions)
+
+
+class TokenPools:
+    """The caches of all layers for smla_keep_tokens, looked at once (an engine's
+    caches live as long as it does). caches: block-scaled caches (k_cache, v_cache,
+    k_scale, v_scale), all of one shape; or latent pools [num_slots, D] of one shape
+    and type, then with block_size."""
+
+    __slots__ = ("tensors", "device", "heads", "block_size", "row_bytes", "num_blocks", "count", "pools", "scales")
+
+    def __init__(self, caches: Sequence, block_size: Optional[int] = None):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("no caches")
+        if isinstance(caches[0], torch.Tensor):
+            first = caches[0]
+            _need(first, "caches[0]", first.dtype, 2)
+            if block_size is None:
+                raise ValueError("latent pools need block_size")
+            slots, D = first.shape
+            if slots % block_size != 0:
+                raise ValueError("%d slots are no whole blocks of %d" % (slots, block_size))
+            for i, x in enumerate(caches):
+                _fits(x, "caches[%d]" % i, first.dtype, 2, first.device)
+                if x.shape != first.shape:
+                    raise ValueError("caches[%d] is %s, caches[0] %s" % (i, tuple(x.shape), tuple(first.shape)))
+            self.heads, self.block_size, self.num_blocks = 1, block_size, slots // block_size
+            self.row_bytes = D * first.element_size()
+            codes, scales = caches, None
+            self.device = first.device
+        else:
+            shape = _kv8_cache(*caches[0])
+            self.device = caches[0][0].device
+            codes, scales = [], []
+            for i, (kc, vc, ks, vs) in enumerate(caches):
+                if _kv8_cache(kc, vc, ks, vs) != shape or kc.device != self.device:
+                    raise ValueError("caches[%d] is %s on %s, caches[0] %s on %s"
+                                     % (i, tuple(kc.shape), kc.device, tuple(shape), self.device))
+                codes += [kc, vc]
+                scales += [ks, vs]
+            self.num_blocks, self.heads, self.block_size, self.row_bytes = shape
+            if block_size is not None and block_size != self.block_size:
+                raise ValueError("block_size is %d, the caches' %d" % (block_size, self.block_size))
+        self.tensors = (codes, scales)
+        self.count = len(codes)
+        self.pools = (_c.c_void_p * self.count)(*[x.data_ptr() for x in codes])
+        self.scales = None if scales is None else (_c.c_void_p * self.count)(*[x.data_ptr() for x in scales])
+
+
+def smla_keep_tokens(caches, block_table: torch.Tensor, seq_lens: torch.Tensor, query_lens: torch.Tensor,
+                     kept: torch.Tensor, kept_lens: torch.Tensor, *, block_size: Optional[int] = None,
+                     seq_lens_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Keeps some of each request's new tokens (the accepted path of a drafted
+    tree): their cache rows move together behind the context, in place, in every
+    layer at once. caches: a TokenPools, or what one is made of (block_size for
+    latent pools). seq_lens int32 [B] with the new tokens, query_lens int32 [B];
+    kept int32 [B, width]: the numbers of the kept ones, ascending, kept_lens int32
+    [B] of them. Returns the requests' new lengths (not in place of the old)."""
+    pools = caches if isinstance(caches, TokenPools) else TokenPools(caches, block_size)
+    if block_size is not None and block_size != pools.block_size:
+        raise ValueError("block_size is %d, the caches' %d" % (block_size, pools.block_size))
+    dev = pools.device
+    _rows(block_table, "block_table", torch.int32, 2, dev)
+    B, width = block_table.shape
+    _fits(seq_lens, "seq_lens", torch.int32, 1, dev)
+    _fits(query_lens, "query_lens", torch.int32, 1, dev)
+    _fits(kept_lens, "kept_lens", torch.int32, 1, dev)
+    _rows(kept, "kept", torch.int32, 2, dev)
+    if seq_lens.shape[0] != B or query_lens.shape[0] != B or kept_lens.shape[0] != B or kept.shape[0] != B:
+        raise ValueError("seq_lens, query_lens, kept and kept_lens must have %d rows" % B)
+    row_stride = max(block_table.stride(0), width) if B <= 1 else block_table.stride(0)
+    kept_stride = max(kept.stride(0), kept.shape[1]) if B <= 1 else kept.stride(0)
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
+        seq_lens_out = _out(seq_lens_out, "seq_lens_out", (B,), torch.int32, dev)
+        st = L.smla_keep_tokens(_KEEP_TOKENS_PARAMS.pack(
+            _KEEP_TOKENS_PARAMS.size, block_table.data_ptr(), row_stride, width, seq_lens.data_ptr(),
+            query_lens.data_ptr(), kept.data_ptr(), kept_stride, kept.shape[1], kept_lens.data_ptr(),
+            seq_lens_out.data_ptr(), B, pools.heads, pools.block_size, pools.row_bytes, pools.num_blocks, pools.count,
+            ctypes.addressof(pools.pools), 0 if pools.scales is None else ctypes.addressof(pools.scales), handle))
+    if st:
+        _check(st, "smla_keep_tokens")
+    return seq_lens_out
+
+
+class ForkedTables(NamedTuple):
+    """What smla_fork_block_tables returns (device tensors)."""
+    block_table: torch.Tensor  # int32 [B, width]
+    blocks_held: torch.Tensor  # int32 [B]
+    ring_state: torch.Tensor   # int32 [2]: head, count
+    copy_from: torch.Tensor    # int32 [B], -1 where there is nothing to copy
+    copy_to: torch.Tensor      # int32 [B]
+    counts: torch.Tensor       # int32 [4]: tokens held, blocks taken, blocks given back, blocks lacking
+
+
+@functools.lru_cache(maxsize=1024)
+def _fork_workspace(B_old: int, B: int, width: int, num_blocks: int) -> int:
+    need = (_lib or lib()).smla_fork_block_tables_workspace_size(B_old, B, width, num_blocks)
+    return 256 if need == ctypes.c_size_t(-1).value else int(need)  # (the call says what is wrong)
+
+
+def smla_fork_block_tables(source_rows: torch.Tensor, seq_lens: torch.Tensor, blocks_held: torch.Tensor,
+                           block_table: torch.Tensor, free_ring: torch.Tensor, ring_state: torch.Tensor, *,
+                           block_size: int, num_blocks: int, block_table_out: Optional[torch.Tensor] = None,
+                           blocks_held_out: Optional[torch.Tensor] = None,
+                           ring_state_out: Optional[torch.Tensor] = None, copy_from: Optional[torch.Tensor] = None,
+                           copy_to: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> ForkedTables:
+    """Block tables that go on from others, all on the device (include/sparse_mla.h):
+    new row b shares the blocks of old row source_rows[b] (int32 [B]; -1: an empty
+    row) that its first seq_lens[b] tokens (int32 [B]) lie in; a last block that is
+    not full and that other new rows hold too is replaced by one from the ring, to be
+    copied by smla_copy_blocks(pools, copy_from, copy_to); blocks that no new row
+    holds go back to the ring. blocks_held int32 [B_old] and block_table int32
+    [B_old, width] (rows may be strided) stay; free_ring and ring_state as for
+    smla_build_block_tables (ring_state updated in place unless ring_state_out is
+    given). Fresh outputs' entries past a row's blocks are -1. Nothing changes when
+    blocks lack: counts[3] says how many."""
+    _need(source_rows, "source_rows", torch.int32, 1)
+    dev = source_rows.device
+    B = source_rows.shape[0]
+    _fits(seq_lens, "seq_lens", torch.int32, 1, dev)
+    _fits(blocks_held, "blocks_held", torch.int32, 1, dev)
+    _rows(block_table, "block_table", torch.int32, 2, dev)
+    B_old, width = block_table.shape
+    if seq_lens.shape[0] != B or blocks_held.shape[0] != B_old:
+        raise ValueError("seq_lens must be [%d], blocks_held [%d]" % (B, B_old))
+    _fits(free_ring, "free_ring", torch.int32, 1, dev)
+    _fits(ring_state, "ring_state", torch.int32, 1, dev)
+    if ring_state.shape[0] != 2:
+        raise ValueError("ring_state must be [2]: head, count")
+    if block_table_out is not None:
+        _rows(block_table_out, "block_table_out", torch.int32, 2, dev)
+        if block_table_out.shape != (B, width):
+            raise ValueError("block_table_out must be [%d, %d], got %s" % (B, width, tuple(block_table_out.shape)))
+    L = _lib or lib()
+    with _on(dev, stream) as handle:
+        if block_table_out is None:
+            block_table_out = torch.full((B, width), -1, dtype=torch.int32, device=dev)
+        state = ring_state if ring_state_out is None else _out(ring_state_out, "ring_state_out", (2,), torch.int32, dev)
+        held = _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
+        copy_from = _out(copy_from, "copy_from", (B,), torch.int32, dev)
+        copy_to = _out(copy_to, "copy_to", (B,), torch.int32, dev)
+        counts = _out(counts, "counts", (4,), torch.int32, dev)
+        workspace, ws_bytes = _workspace(workspace, _fork_workspace(B_old, B, width, num_blocks), dev)
+        old_stride, new_stride = (max(x.stride(0), width) if x.shape[0] <= 1 else x.stride(0)
+                                  for x in (block_table, block_table_out))
+        st = L.smla_fork_block_tables(_FORK_PARAMS.pack(
+            _FORK_PARAMS.size, source_rows.data_ptr(), seq_lens.data_ptr(), B, blocks_held.data_ptr(), B_old,
+            block_table.data_ptr(), old_stride, held.data_ptr(), block_table_out.data_ptr(), new_stride, width, block_size,
+            num_blocks, free_ring.data_ptr(), free_ring.shape[0], ring_state.data_ptr(), state.data_ptr(),
+            copy_from.data_ptr(), copy_to.data_ptr(), counts.data_ptr(), workspace.data_ptr(), ws_bytes, handle))
+    if st:
+        _check(st, "smla_fork_block_tables")
+    return ForkedTables(block_table_out, held, state, copy_from, copy_to, counts)
+
+
+class BlockPools:
+    """Pools for smla_copy_blocks, looked at once: contiguous tensors of any type
+    whose first dimension is the blocks (every layer's codes and scales; a latent pool
+    as view(num_blocks, -1))."""
+
+    __slots__ = ("tensors", "device", "num_blocks", "count", "pools", "block_bytes")
+
+    def __init__(self, pools: Sequence[torch.Tensor]):
+        self.tensors = list(pools)
+        if not self.tensors:
+            raise ValueError("no pools")
+        first = self.tensors[0]
+        for i, x in enumerate(self.tensors):
+            if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1 or not x.is_contiguous():
+                raise ValueError("pools[%d] must be a contiguous CUDA tensor" % i)
+            if x.device != first.device or x.shape[0] != first.shape[0]:
+                raise ValueError("pools[%d] has %d blocks on %s, pools[0] %d on %s"
+                                 % (i, x.shape[0], x.device, first.shape[0], first.device))
+        self.device, self.num_blocks, self.count = first.device, first.shape[0], len(self.tensors)
+        self.pools = (_c.c_void_p * self.count)(*[x.data_ptr() for x in self.tensors])
+        self.block_bytes = (_c.c_int64 * self.count)(*[x.numel() * x.element_size() // max(1, self.num_blocks)
+                                                       for x in self.tensors])
+
+
+def smla_copy_blocks(pools, copy_from: torch.Tensor, copy_to: torch.Tensor, stream=None) -> None:
+    """Copies block copy_from[i] to block copy_to[i] (int32 [n]; a number outside the
+    pool: nothing) in each of the pools: a BlockPools, or the tensors one is made of.
+    No block that is copied to may stand elsewhere in either list."""
+    if not isinstance(pools, BlockPools):
+        pools = BlockPools(pools)
+    _fits(copy_from, "copy_from", torch.int32, 1, pools.device)
+    _fits(copy_to, "copy_to", torch.int32, 1, pools.device)
+    n = copy_from.shape[0]
+    if copy_to.shape[0] != n:
+        raise ValueError("copy_from has %d entries, copy_to %d" % (n, copy_to.shape[0]))
+    L = _lib or lib()
+    with _on(pools.device, stream) as handle:
+        st = L.smla_copy_blocks(pools.pools, pools.block_bytes, pools.count, copy_from.data_ptr(), copy_to.data_ptr(), n,
+                                pools.num_blocks, handle)
+    if st:
+        _check(st, "smla_copy_blocks")

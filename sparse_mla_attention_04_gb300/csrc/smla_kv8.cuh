@@ -97,6 +97,47 @@ __device__ __forceinline__ Request request(const Kv8AttnArgs &a, int b)
     return r;
 }
 
+// What a token of a drafted tree sees: of the context [0, ctx) the positions from lo on, and of its request's
+// new tokens, at [ctx, len), those whose bits are set in its row of the mask.
+struct TreeRow {
+    int ctx, len, lo;
+    const uint64_t *bits;
+    int words;
+
+    // token t of the batch; `there` is false for a row that is none: it sees nothing
+    __device__ __forceinline__ TreeRow(const Kv8AttnArgs &a, const Request &r, int t, bool there)
+        : ctx(there ? r.len - r.qlen : 0), len(there ? r.len : 0), lo(0), bits(a.tree_mask + (int64_t)(there ? t : 0) * a.tree_words),
+          words(a.tree_words)
+    {
+        if (a.window > 0 && there) // (a position that no new token can have is taken as the nearest)
+            lo = (int)max((long long)ctx, min((long long)a.tree_positions[t], (long long)len - 1)) - a.window + 1;
+    }
+    __device__ __forceinline__ bool sees(int j) const
+    {
+        if (j < ctx)
+            return j >= lo;
+        const int i = j - ctx;
+        return j < len && i < words * 64 && (__ldg(bits + (i >> 6)) >> (i & 63) & 1);
+    }
+    // Of sixteen positions from j on (j >= 0): bit i is whether j + i is seen.
+    __device__ __forceinline__ uint32_t sees16(int j) const
+    {
+        const auto below = [](int n) { return (1u << min(max(n, 0), 16)) - 1; };
+        uint32_t see = below(ctx - j) & ~below(lo - j);
+        if (j + 16 > ctx) {
+            const int i = max(j - ctx, 0), skip = max(ctx - j, 0); // the first node among them, its place
+            uint64_t w = 0;
+            if (i < words * 64) {
+                w = __ldg(bits + (i >> 6)) >> (i & 63);
+                if ((i & 63) > 48 && (i >> 6) + 1 < words)
+                    w |= __ldg(bits + (i >> 6) + 1) << (64 - (i & 63));
+            }
+            see |= ((uint32_t)w << skip) & below(len - j) & ~below(ctx - j);
+        }
+        return see;
+    }
+};
+
 // q's rows as two E4M3 parts: the power of two that brings a row below 2^8, and
 // its inverse (NaN for a row with an infinity, which has no finite logit).
 __device__ __forceinline__ void split_scale(float amax, float &up, float &down)

@@ -13,6 +13,7 @@
 // issue slots: four values take some ten, two conversions to bracket each quotient among
 // them); one token for each of 64 requests in 4.5 us on the device, in a 17 us call.
 #include "smla_device.cuh"
+#include "smla_kv8_codes.cuh"
 #include "smla_step.h"
 
 #include <algorithm>
@@ -97,20 +98,6 @@ __device__ __forceinline__ uint2 quant8(const uint4 v, float s, const E4m3Recip 
     if (!r.ok || a.x != b.x || a.y != b.y)
         return divide8(v, s);
     return a;
-}
-
-// Four older codes under a grown scale: E4M3(code * old / now), each operation rounded in binary32.
-__device__ __noinline__ uint32_t requant4(uint32_t w, float old, float now)
-{
-    uint32_t lo, hi;
-    e4m3x4_to_f16x4(w, lo, hi);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    const float2 qa = make_float2(__fdiv_rn(__fmul_rn(a.x, old), now), __fdiv_rn(__fmul_rn(a.y, old), now));
-    const float2 qb = make_float2(__fdiv_rn(__fmul_rn(b.x, old), now), __fdiv_rn(__fmul_rn(b.y, old), now));
-    const uint32_t ca = __nv_cvt_float2_to_fp8x2(qa, __NV_SATFINITE, __NV_E4M3);
-    const uint32_t cb = __nv_cvt_float2_to_fp8x2(qb, __NV_SATFINITE, __NV_E4M3);
-    return (ca & 0xFFFFu) | (cb << 16);
 }
 
 __device__ __forceinline__ float warp_amax(uint32_t m)
@@ -327,7 +314,13 @@ cudaError_t launch_kv8_append(const Kv8AppendArgs &args, int D, int sm_count, cu
 
 cudaError_t read_append_error(int *out, bool reset)
 {
+    int tree = 0, keep = 0;
+    if (const cudaError_t e = read_tree_error(&tree, reset); e != cudaSuccess)
+        return e;
+    if (const cudaError_t e = read_keep_error(&keep, reset); e != cudaSuccess)
+        return e;
     cudaError_t e = cudaMemcpyFromSymbol(out, g_append_error, sizeof(int));
+    *out |= tree | keep;
     if (e == cudaSuccess && reset) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(g_append_error, &zero, sizeof(int));

@@ -149,6 +149,24 @@ template <int D, int NT> struct Layout {
     static constexpr int kSmem = kBig + kWarps * R * 8 + kWarps * kStages * 32 + kNanWords * 4 + kWarps * kStages * 8;
 };
 
+// What a lane's rows of a drafted tree (by their tokens, -1: none) see of its positions j, j + 8, j + 16 and
+// j + 24 of a step: bit 8 nt + 4 x + e for row (nt, e & 1) and position 16 x + 4 (e & 2).
+template <int NT>
+__device__ __forceinline__ uint32_t tree_sight(const Kv8AttnArgs &a, const Request rq, const int (&token)[NT][2], int j)
+{
+    uint32_t see = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+            const TreeRow row(a, rq, token[nt][e2], token[nt][e2] >= 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                see |= (uint32_t)row.sees(j + 8 * k) << (8 * nt + 4 * (k >> 1) + 2 * (k & 1) + e2);
+        }
+    return see;
+}
+
 // The workspace: for each block the unit that it begins and others end, {last
 // block (-1: none), request, index in the request}; then a head and a tail
 // partial of each block. Its size follows from the blocks launched, so nothing that
@@ -160,7 +178,7 @@ struct Part {
     int fill;     // blocks that the GPU holds at a time
 };
 
-template <int D, int NT>
+template <int D, int NT, bool kTree>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                                 const __grid_constant__ CUtensorMap v_map,
                                                                                 const Kv8AttnArgs a, const Part part)
@@ -284,10 +302,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
         const int h = (int)(ui % a.H_kv);
         const int row0 = (int)(ui / a.H_kv) * R;
         const int rows = min(R, rq.qlen * a.G - row0);
-        // the chunk's tokens and what its rows see
-        const int p_first = rq.pos(row0 / a.G), p_last = rq.pos((row0 + rows - 1) / a.G);
+        // the chunk's tokens and what its rows see (of a drafted tree: positions up to p_first, the context's
+        // last, are seen by all)
+        const int p_first = kTree ? rq.pos(-1) : rq.pos(row0 / a.G);
+        const int p_last = kTree ? rq.len - 1 : rq.pos((row0 + rows - 1) / a.G);
         const int kv_end = min(rq.len, p_last + 1);                                    // beyond: seen by none
-        const int kv_begin = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+        const int kv_begin = a.window > 0 ? max(0, p_first - a.window + (kTree ? 2 : 1)) : 0;
         const int all_from = a.window > 0 ? p_last - a.window + 1 : 0;                 // [all_from, p_first]: seen by all
         const bool many = p_first != p_last;
 
@@ -386,7 +406,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             for (int e2 = 0; e2 < 2; ++e2) {
                 cscale[nt][e2] = __shfl_sync(0xffffffffu, qscale[nt], 4 * (2 * t4 + e2));
                 const int rc = nt * 8 + 2 * t4 + e2;
-                pos[nt][e2] = rc < rows ? rq.pos((row0 + rc) / a.G) : -1;
+                if (kTree)
+                    pos[nt][e2] = rc < rows ? rq.q0 + (row0 + rc) / a.G : -1; // (the token)
+                else
+                    pos[nt][e2] = rc < rows ? rq.pos((row0 + rc) / a.G) : -1;
             }
         }
 
@@ -454,6 +477,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
             const float4 mt[2] = {meta[stage * 2], meta[stage * 2 + 1]};
             const bool clear = tb + kStep - 1 <= p_first && tb >= all_from && rows == R;
             bool raise = false;
+            uint32_t sight = 0; // of a drafted tree: bit 8 nt + 4 x + e
+            if (kTree && !clear)
+                sight = tree_sight<NT>(a, rq, pos, tb + tau_g);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -461,7 +487,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float y = fmaf(sc[x][nt][e], mt[x].x * cscale[nt][e & 1], mt[x].y);
-                        if (!clear) {
+                        if (kTree && !clear) {
+                            if (!(sight >> (8 * nt + 4 * x + e) & 1))
+                                y = -INFINITY;
+                        } else if (!clear) {
                             const int j = tb + 16 * x + tau_g + 4 * (e & 2);
                             const int p = pos[nt][e & 1];
                             if (!(j <= p && (a.window <= 0 || j > p - a.window)))
@@ -543,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_stream_kernel(c
                                         const int d = kV * g + 4 * w + z;
                                         for (int r = 0; r < rows; ++r) {
                                             const int p = rq.pos((row0 + r) / a.G);
-                                            if (j <= p && (a.window <= 0 || j > p - a.window))
+                                            if (kTree ? TreeRow(a, rq, rq.q0 + (row0 + r) / a.G, true).sees(j)
+                                                      : j <= p && (a.window <= 0 || j > p - a.window))
                                                 atomicOr(&s_nan[(r * D + d) >> 5], 1u << (d & 31));
                                         }
                                     }
@@ -729,8 +759,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
         a.lse[t * a.H + head] = lse;
 }
 
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
 int fill_of(int NT, int sm_count) { return sm_count * (NT == 1 ? 3 : 2); }
 
 struct Sizes {
@@ -758,7 +786,7 @@ Sizes sizes(int D, int NT, size_t blocks)
     return s;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kTree>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
     using L = Layout<D, NT>;
@@ -767,13 +795,13 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const Part part{reinterpret_cast<int4 *>(ws), reinterpret_cast<float2 *>(ws + sz.ml), reinterpret_cast<float *>(ws + sz.o),
                     fill_of(NT, sm_count)};
-    cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv8_stream_kernel<D, NT, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kStep, maps))
         return cudaErrorInvalidValue;
-    kv8_stream_kernel<D, NT><<<grid, kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
+    kv8_stream_kernel<D, NT, kTree><<<grid, kThreads, L::kSmem, stream>>>(maps[0], maps[1], a, part);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     if (grid == 1)
@@ -794,6 +822,15 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
 // Query rows to a unit: 8, or 16 where the requests' rows fill more than 8.
 int tiles_for(int G, int max_query_len) { return (int64_t)G * max_query_len > 8 ? 2 : 1; }
 
+template <bool kTree>
+cudaError_t launch_rows(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream)
+{
+    const int nt = tiles_for(a.G, max_query_len);
+    if (D == 128)
+        return nt == 1 ? launch<128, 1, kTree>(a, workspace, sm_count, stream) : launch<128, 2, kTree>(a, workspace, sm_count, stream);
+    return nt == 1 ? launch<64, 1, kTree>(a, workspace, sm_count, stream) : launch<64, 2, kTree>(a, workspace, sm_count, stream);
+}
+
 } // namespace
 
 size_t kv8_stream_workspace(int B, int T, int G, int H_kv, int D, int max_query_len, int64_t positions, int sm_count)
@@ -805,10 +842,8 @@ size_t kv8_stream_workspace(int B, int T, int G, int H_kv, int D, int max_query_
 cudaError_t launch_kv8_stream(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count,
                               cudaStream_t stream)
 {
-    const int nt = tiles_for(a.G, max_query_len);
-    if (D == 128)
-        return nt == 1 ? launch<128, 1>(a, workspace, sm_count, stream) : launch<128, 2>(a, workspace, sm_count, stream);
-    return nt == 1 ? launch<64, 1>(a, workspace, sm_count, stream) : launch<64, 2>(a, workspace, sm_count, stream);
+    return a.tree_mask ? launch_rows<true>(a, D, max_query_len, workspace, sm_count, stream)
+                       : launch_rows<false>(a, D, max_query_len, workspace, sm_count, stream);
 }
 
 cudaError_t read_kv8_stream_error(int *out, bool reset)

@@ -176,10 +176,11 @@ __device__ __forceinline__ Span span_of(const Kv8AttnArgs &a, int item_rows, con
     Span s;
     s.row0 = chunk * item_rows;
     s.rows = min(item_rows, rq.qlen * a.G - s.row0);
-    s.p_first = rq.pos(s.row0 / a.G);
-    s.p_last = rq.pos((s.row0 + s.rows - 1) / a.G);
+    const bool tree = a.tree_mask != nullptr; // the context's positions are seen by all rows, those behind by some
+    s.p_first = tree ? rq.pos(-1) : rq.pos(s.row0 / a.G);
+    s.p_last = tree ? rq.len - 1 : rq.pos((s.row0 + s.rows - 1) / a.G);
     s.kv_end = min(rq.len, s.p_last + 1);
-    s.kv_begin = a.window > 0 ? max(0, s.p_first - a.window + 1) : 0;
+    s.kv_begin = a.window > 0 ? max(0, s.p_first - a.window + (tree ? 2 : 1)) : 0;
     s.all_from = a.window > 0 ? s.p_last - a.window + 1 : 0;
     s.tb0 = s.kv_begin & ~(kTile - 1);
     s.tiles = s.kv_end > s.tb0 ? (s.kv_end - s.tb0 + kTile - 1) / kTile : 0;
@@ -333,11 +334,31 @@ __device__ __forceinline__ void wait_ld16(uint32_t (&x)[16])
 }
 
 // What the rows of a tile see of 32 positions.
-struct Sight {
+template <bool kTree> struct Sight;
+template <> struct Sight<false> {
     int p_first, all_from; // the tile's: see Span
     int pos, pos_lo;       // this row: pos_lo <= t <= pos
+    __device__ __forceinline__ Sight(const Kv8AttnArgs &a, const Span &sp, const Request &rq, int r)
+        : p_first(sp.p_first), all_from(sp.all_from), pos(r < sp.rows ? rq.pos((sp.row0 + r) / a.G) : -1),
+          pos_lo(a.window > 0 ? pos - a.window + 1 : 0)
+    {
+    }
     __device__ bool all(int t) const { return t + 31 <= p_first && t >= all_from; }
     __device__ bool sees(int t) const { return t <= pos && t >= pos_lo; }
+    __device__ int first() const { return pos_lo; }
+    __device__ int last() const { return pos; }
+};
+template <> struct Sight<true> {
+    int p_first, all_from;
+    TreeRow row;
+    __device__ __forceinline__ Sight(const Kv8AttnArgs &a, const Span &sp, const Request &rq, int r)
+        : p_first(sp.p_first), all_from(sp.all_from), row(a, rq, rq.q0 + (sp.row0 + r) / a.G, r < sp.rows)
+    {
+    }
+    __device__ bool all(int t) const { return t + 31 <= p_first && t >= all_from; }
+    __device__ bool sees(int t) const { return row.sees(t); }
+    __device__ int first() const { return max(row.lo, 0); }
+    __device__ int last() const { return row.len - 1; }
 };
 
 // A row's running sums.
@@ -414,19 +435,25 @@ __device__ __forceinline__ bool row_tile(uint32_t my, const float *sc, float qs,
 }
 
 // Sixteen of the row's logits, -inf where it does not see the position.
-__device__ __forceinline__ void logits(uint32_t my, const float *sc, float qs, int t0, const Sight &see, int c, uint32_t (&x)[16])
+template <bool kTree>
+__device__ __forceinline__ void logits(uint32_t my, const float *sc, float qs, int t0, const Sight<kTree> &see, int c,
+                                       uint32_t (&x)[16])
 {
     ld16(my + c * 16, x);
     const float k = sc[c] * qs, vs = sc[4 + c];
     const int t = t0 + c * 16;
+    uint32_t bits = 0;
+    if constexpr (kTree)
+        bits = see.row.sees16(t);
     wait_ld16(x);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        x[i] = __float_as_uint(see.sees(t + i) ? fmaf(__uint_as_float(x[i]), k, vs) : -INFINITY);
+        x[i] = __float_as_uint((kTree ? bits >> i & 1 : see.sees(t + i)) ? fmaf(__uint_as_float(x[i]), k, vs) : -INFINITY);
 }
 
 // The largest of the row's 64 logits that it sees.
-__device__ __forceinline__ float largest(uint32_t my, const float *sc, float qs, int t0, const Sight &see)
+template <bool kTree>
+__device__ __forceinline__ float largest(uint32_t my, const float *sc, float qs, int t0, const Sight<kTree> &see)
 {
     float top = -INFINITY;
 #pragma unroll 1
@@ -448,7 +475,8 @@ __device__ __forceinline__ float largest(uint32_t my, const float *sc, float qs,
 __device__ __forceinline__ float reference(float top) { return __fadd_ru(top, -kTop); }
 
 // The row's first reference.
-__device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, int t0, const Sight see)
+template <bool kTree>
+__device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, int t0, const Sight<kTree> see)
 {
     if (!see.all(t0) || !see.all(t0 + 32))
         return reference(largest(my, sc, qs, t0, see));
@@ -471,8 +499,9 @@ __device__ __noinline__ float row_first(uint32_t my, const float *sc, float qs, 
 // rest; o_cols: its columns, 0 before the first product); positions that the row
 // does not see are left out; the difference is taken from the rounded logit, as the
 // reference is.
+template <bool kTree>
 __device__ __noinline__ Row row_tile_moving(uint32_t my, uint32_t my_o, int o_cols, const float *sc, float qs, Row row, int t0,
-                                            const Sight see)
+                                            const Sight<kTree> see)
 {
     const float top = largest(my, sc, qs, t0, see);
     const bool raise = row.m == -INFINITY ? top > -INFINITY : top - row.m > kSlack;
@@ -526,14 +555,14 @@ __device__ __noinline__ void visible_codes(uint32_t (&w)[4], bool in, bool many,
 // Which of the 32 value columns from 32 c on hold a NaN code at a position that
 // the row sees, in the tiles where some rows see positions that others do not
 // (there the codes were taken out, so that 0 * NaN does not reach the others).
-template <int D>
-__device__ __noinline__ uint32_t nan_columns(const Kv8AttnArgs &a, const Item &it, const Sight &see, int tb0, int t_begin, int n,
-                                             int c)
+template <int D, bool kTree>
+__device__ __noinline__ uint32_t nan_columns(const Kv8AttnArgs &a, const Item &it, const Sight<kTree> &see, int tb0, int t_begin,
+                                             int n, int c)
 {
     uint32_t bits = 0;
-    for (int t = max(see.pos_lo, tb0 + t_begin * kTile); t <= see.pos && t < tb0 + (t_begin + n) * kTile; ++t) {
+    for (int t = max(see.first(), tb0 + t_begin * kTile); t <= see.last() && t < tb0 + (t_begin + n) * kTile; ++t) {
         const int tile = t & ~(kTile - 1); // (tb0 is a multiple of it)
-        if (tile + kTile - 1 <= see.p_first && tile >= see.all_from)
+        if ((tile + kTile - 1 <= see.p_first && tile >= see.all_from) || (kTree && !see.sees(t)))
             continue;
         const int e = t >> a.block_shift;
         const int v = e < a.table_width ? a.block_table[it.b * a.table_stride + e] : -1;
@@ -557,7 +586,7 @@ struct Piece {
 
 // Works on a piece, by the whole block; false where a wait gave up. The barriers
 // were last used for a piece before (not the first time).
-template <int D, int NR>
+template <int D, int NR, bool kTree>
 __device__ __forceinline__ bool work_on(const CUtensorMap &k_map, const CUtensorMap &v_map, const Kv8AttnArgs &a, const Plan &plan,
                                         uint8_t *smem, const Piece &piece, bool first)
 {
@@ -678,8 +707,7 @@ __device__ __forceinline__ bool work_on(const CUtensorMap &k_map, const CUtensor
             fence_async_smem();
             mbar_arrive(q_full);
         }
-        const int pos = r < rows ? rq.pos((row0 + r) / a.G) : -1;
-        const Sight see{p_first, all_from, pos, a.window > 0 ? pos - a.window + 1 : 0};
+        const Sight<kTree> see(a, sp, rq, r);
         const uint32_t my = tmem + tile * S::kTmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_ready = s_full + tile * 16, p_ready = p_full + tile * 16, o_done = v_empty + tile * 16;
         const float *scales = reinterpret_cast<const float *>(smem + S::kScales);
@@ -739,7 +767,7 @@ __device__ __forceinline__ bool work_on(const CUtensorMap &k_map, const CUtensor
                 ld32(my + S::kO + c * 32, x);
                 wait_ld32(x);
                 if (nans) {
-                    const uint32_t bits = live ? nan_columns<D>(a, it, see, tb0, t_begin, n, c) : 0;
+                    const uint32_t bits = live ? nan_columns<D, kTree>(a, it, see, tb0, t_begin, n, c) : 0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         x[i] = (bits >> i & 1) ? 0x7FC00000u : x[i];
@@ -974,7 +1002,7 @@ __device__ __forceinline__ bool work_on(const CUtensorMap &k_map, const CUtensor
     return ok;
 }
 
-template <int D, int NR>
+template <int D, int NR, bool kTree>
 __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8_tile_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                                              const __grid_constant__ CUtensorMap v_map,
                                                                                              const Kv8AttnArgs a, const Plan plan)
@@ -1062,7 +1090,7 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         if (units > 0 && tid == S::kV0 * 32)
             misc->next = atomicAdd(plan.head + 1, 1);
         if (s0 < s1) {
-            const bool ok = work_on<D, NR>(k_map, v_map, a, plan, smem, piece, first);
+            const bool ok = work_on<D, NR, kTree>(k_map, v_map, a, plan, smem, piece, first);
             first = first && piece.t_end <= s0;
             if (!ok) { // (every warp that waited on that gives up, too)
                 misc->hi = 0;
@@ -1147,8 +1175,6 @@ struct Sizes {
     size_t cost_at, items_at, order_at, dir_at, ml_at, o_at, total;
 };
 
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
 int slots_of(int NR, int sm_count) { return (NR == 1 ? 2 : 1) * std::max(sm_count, 1); } // CTAs at a time
 
 Sizes sizes_of(int64_t B, int64_t T, int G, int D, int NR, int sm_count)
@@ -1183,7 +1209,7 @@ cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, int s
     return cudaLaunchKernelEx(&cfg, kernel, given...);
 }
 
-template <int D, int NR>
+template <int D, int NR, bool kTree>
 cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStream_t stream)
 {
     using S = Shape<D, NR>;
@@ -1199,7 +1225,7 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
                     (int)z.items,
                     S::kItemRows};
     const int grid = slots_of(NR, sm_count);
-    cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv8_tile_kernel<D, NR, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap maps[2];
@@ -1208,7 +1234,7 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, grid);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    e = launch_behind(kv8_tile_kernel<D, NR>, dim3((unsigned)grid), S::kThreads, S::kSmem, stream, maps[0], maps[1], a, plan);
+    e = launch_behind(kv8_tile_kernel<D, NR, kTree>, dim3((unsigned)grid), S::kThreads, S::kSmem, stream, maps[0], maps[1], a, plan);
     if (e != cudaSuccess)
         return e;
     constexpr int kRowsOfBlock = kJoinWarps * 32 / (D / 4) * kJoinRows;
@@ -1221,6 +1247,14 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
 // rows 134 (150); 128 rows 120 (92), 40 rows 118 (90).
 int row_tiles(int G, int max_query_len) { return (int64_t)G * max_query_len > kRows ? 2 : 1; }
 
+template <bool kTree>
+cudaError_t launch_rows(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream)
+{
+    if (row_tiles(a.G, max_query_len) == 2)
+        return D == 128 ? launch<128, 2, kTree>(a, workspace, sm_count, stream) : launch<64, 2, kTree>(a, workspace, sm_count, stream);
+    return D == 128 ? launch<128, 1, kTree>(a, workspace, sm_count, stream) : launch<64, 1, kTree>(a, workspace, sm_count, stream);
+}
+
 } // namespace
 
 size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sm_count)
@@ -1230,9 +1264,8 @@ size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int max_query_le
 
 cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream)
 {
-    if (row_tiles(a.G, max_query_len) == 2)
-        return D == 128 ? launch<128, 2>(a, workspace, sm_count, stream) : launch<64, 2>(a, workspace, sm_count, stream);
-    return D == 128 ? launch<128, 1>(a, workspace, sm_count, stream) : launch<64, 1>(a, workspace, sm_count, stream);
+    return a.tree_mask ? launch_rows<true>(a, D, max_query_len, workspace, sm_count, stream)
+                       : launch_rows<false>(a, D, max_query_len, workspace, sm_count, stream);
 }
 
 cudaError_t read_kv8_error(int *out, bool reset)

@@ -1,6 +1,7 @@
 // Rotary positions (sm_103a): the cos/sin table of a scaled frequency set, and
 // the rotation of part of each head.
 #include "smla_device.cuh"
+#include "smla_rope.cuh"
 #include "smla_step.h"
 
 #include <algorithm>
@@ -11,6 +12,8 @@ namespace smla {
 __device__ int g_rope_error = 0; // bit 4: a position out of range
 
 namespace {
+
+using namespace rope;
 
 // Sine and cosine of a 64-bit fraction of a turn, times `factor`. The nearest quarter
 // turn leaves an angle of at most pi/4, all of whose bits go into its rounding to
@@ -84,36 +87,6 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float *__restrict__ tab
     }
 }
 
-__device__ __forceinline__ float rot_a(float a, float b, float c, float s)
-{
-    return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-}
-__device__ __forceinline__ float rot_b(float a, float b, float c, float s)
-{
-    return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-}
-
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f(float x) { return x; }
-template <typename E> __device__ __forceinline__ E from_f(float x);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
-template <> __device__ __forceinline__ float from_f(float x) { return x; }
-
-// kVec elements moved as one access: as one word, whose elements are looked at in
-// place (a structure of elements would be copied element by element).
-template <int kBytes> struct Word;
-template <> struct Word<16> { using type = uint4; };
-template <> struct Word<4> { using type = uint32_t; };
-template <> struct Word<2> { using type = uint16_t; };
-template <typename E, int kVec> struct Pack {
-    typename Word<sizeof(E) * kVec>::type w;
-    __device__ __forceinline__ void load(const E *p) { w = *reinterpret_cast<const decltype(w) *>(p); }
-    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<decltype(w) *>(p) = w; }
-    __device__ __forceinline__ E &at(int i) { return reinterpret_cast<E *>(&w)[i]; }
-};
-
 // A unit is what one thread turns or copies of one head: with halves, kVec
 // elements of each half (kVec pairs); interleaved, kVec elements (kVec / 2
 // pairs; two for kVec = 1); or kVec plain columns. A thread keeps its unit, so
@@ -126,26 +99,6 @@ template <typename E, int kVec> struct Pack {
 // the device, 5.5 TB/s (the device's own copy of as many bytes: 31 us); 64 tokens in a
 // 10 us call.
 template <int kVec, bool kNeox> constexpr int kBatch = kNeox || kVec == 1 ? 2 : 4;
-
-// kPairs consecutive floats of a table row, by 16 bytes where they are aligned.
-template <int kPairs>
-__device__ __forceinline__ void load_angles(const float *p, float (&v)[kPairs])
-{
-    if (kPairs % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-        for (int e = 0; e < kPairs / 4; ++e) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + e);
-            v[4 * e] = f.x;
-            v[(4 * e + 1) % kPairs] = f.y;
-            v[(4 * e + 2) % kPairs] = f.z;
-            v[(4 * e + 3) % kPairs] = f.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e)
-            v[e] = __ldg(p + e);
-    }
-}
 
 template <typename E, int kVec, bool kNeox>
 __global__ void __launch_bounds__(256, 4) rope_kernel(const RopeArgs a)
@@ -315,7 +268,11 @@ cudaError_t launch_rope(const RopeArgs &a, int dtype, int sm_count, cudaStream_t
 
 cudaError_t read_rope_error(int *out, bool reset)
 {
+    int norm = 0;
+    if (const cudaError_t e = read_norm_rope_error(&norm, reset); e != cudaSuccess)
+        return e;
     cudaError_t e = cudaMemcpyFromSymbol(out, g_rope_error, sizeof(int));
+    *out |= norm;
     if (e == cudaSuccess && reset) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(g_rope_error, &zero, sizeof(int));

@@ -9,29 +9,14 @@
 
 namespace {
 
+using smla::aligned;
+using smla::block_shift;
 using smla::cuda_status;
 using smla::current_sm_count;
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// log2 of a supported block size, -1 otherwise
-int block_shift(int block_size)
-{
-    switch (block_size) {
-    case 16:
-        return 4;
-    case 32:
-        return 5;
-    case 64:
-        return 6;
-    case 128:
-        return 7;
-    default:
-        return -1;
-    }
-}
-
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+using smla::kMostPositions;
+using smla::kMostRequests;
+using smla::kMostWidth;
+using smla::up256;
 
 // workspace of smla_build_block_tables: the ring state, then the plan of each request
 size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + up256((size_t)B * sizeof(int32_t)); }
@@ -44,9 +29,6 @@ size_t tables_workspace(int B) { return 256 + up256((size_t)B * sizeof(int4)) + 
 // By the bound alone: requests with fewer rows than it says have units that are not full,
 // whose steps all go through the masks (8 rows under a bound of 16: 293 against 141).
 bool few_rows(int H, int H_kv, int max_query_len) { return (int64_t)(H / H_kv) * max_query_len <= 16; }
-
-constexpr int64_t kMostPositions = 1 << 30; // of a block table
-constexpr int kMostRequests = 1 << 30, kMostWidth = 1 << 30; // loops over them step past their ends in 31 bits
 
 size_t kv8_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int64_t positions, int sms)
 {
@@ -64,6 +46,82 @@ smla_status check_kv8_shape(int B, int T, int H, int H_kv, int D, int max_query_
     if (B > kMostRequests || (int64_t)T * (H / H_kv) > INT_MAX / 2 || ((int64_t)T * (H / H_kv) / 8 + B) * H_kv > INT_MAX)
         return SMLA_ERR_UNSUPPORTED;
     return SMLA_OK;
+}
+
+// The masks of drafted trees, for smla_kv8_tree_attn_fwd (mask NULL: none).
+struct Tree {
+    const uint64_t *mask;
+    int words;
+    const int64_t *positions;
+};
+
+smla_status kv8_attn(const smla_kv8_attn_params *p, const Tree *tree)
+{
+    if (p->size < sizeof(smla_kv8_attn_params))
+        return SMLA_ERR_BAD_SHAPE;
+    if (const smla_status s = check_kv8_shape(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len); s != SMLA_OK)
+        return s;
+    if (p->num_blocks < 0 || p->table_width < 0 || p->table_stride < p->table_width || p->window < 0 ||
+        p->q_stride_t < 0 || p->q_stride_h < 0 || !std::isfinite(p->scale))
+        return SMLA_ERR_BAD_SHAPE;
+    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > kMostPositions ||
+        p->num_blocks > INT_MAX / p->H_kv)
+        return SMLA_ERR_UNSUPPORTED;
+    if (p->T == 0 || p->B == 0)
+        return SMLA_OK;
+    if (p->q == nullptr || p->out == nullptr || p->seq_lens == nullptr || p->query_start == nullptr ||
+        (p->table_width > 0 && p->block_table == nullptr) ||
+        (p->num_blocks > 0 && (p->k_cache == nullptr || p->v_cache == nullptr || p->k_scale == nullptr || p->v_scale == nullptr)) ||
+        p->workspace == nullptr || (tree && (tree->mask == nullptr || (p->window > 0 && tree->positions == nullptr))))
+        return SMLA_ERR_NULL_POINTER;
+    const int64_t q_st = p->T > 1 ? p->q_stride_t : 0, q_sh = p->H > 1 ? p->q_stride_h : 0; // (of one row none is used)
+    if (q_st % 8 != 0 || q_sh % 8 != 0 || !aligned(p->q, 16) || !aligned(p->out, 16) ||
+        !aligned(p->k_cache, 16) || !aligned(p->v_cache, 16) || !aligned(p->k_scale, 4) || !aligned(p->v_scale, 4) ||
+        !aligned(p->block_table, 4) || !aligned(p->seq_lens, 4) || !aligned(p->query_start, 4) || !aligned(p->lse, 4) ||
+        !aligned(p->sinks, 4) || !aligned(p->workspace, 256) ||
+        (tree && (!aligned(tree->mask, 8) || !aligned(tree->positions, 8))))
+        return SMLA_ERR_MISALIGNED;
+    int sms = 0;
+    if (const cudaError_t e = current_sm_count(&sms); e != cudaSuccess)
+        return cuda_status(e);
+    if (p->workspace_bytes < kv8_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len,
+                                           (int64_t)p->table_width << block_shift(p->block_size), sms))
+        return SMLA_ERR_WORKSPACE_TOO_SMALL;
+    smla::Kv8AttnArgs a;
+    a.q = p->q;
+    a.q_st = q_st;
+    a.q_sh = q_sh;
+    a.k_cache = static_cast<const uint8_t *>(p->k_cache);
+    a.v_cache = static_cast<const uint8_t *>(p->v_cache);
+    a.k_scale = p->k_scale;
+    a.v_scale = p->v_scale;
+    a.num_blocks = p->num_blocks;
+    a.block_table = p->block_table;
+    a.table_stride = p->table_stride;
+    a.table_width = p->table_width;
+    a.seq_lens = p->seq_lens;
+    a.query_start = p->query_start;
+    a.B = p->B;
+    a.T = p->T;
+    a.H = p->H;
+    a.H_kv = p->H_kv;
+    a.G = p->H / p->H_kv;
+    a.block_size = p->block_size;
+    a.block_shift = block_shift(p->block_size);
+    // a window of all positions that the table has is none, and sums with others stay in 31 bits
+    a.window = p->window < (int64_t)p->table_width << a.block_shift ? p->window : 0;
+    a.scale = p->scale;
+    a.sinks = p->sinks;
+    a.out = p->out;
+    a.lse = p->lse;
+    a.tree_mask = tree ? tree->mask : nullptr;
+    a.tree_words = tree ? tree->words : 0;
+    a.tree_positions = tree ? tree->positions : nullptr;
+    if (!few_rows(p->H, p->H_kv, p->max_query_len))
+        return cuda_status(smla::launch_kv8_tile(a, p->D, p->max_query_len, p->workspace, sms,
+                                                 reinterpret_cast<cudaStream_t>(p->stream)));
+    return cuda_status(smla::launch_kv8_stream(a, p->D, p->max_query_len, p->workspace, sms,
+                                               reinterpret_cast<cudaStream_t>(p->stream)));
 }
 
 } // namespace
@@ -223,15 +281,8 @@ SMLA_API smla_status smla_rope(const smla_rope_params *p)
     if ((p->H > 0 && p->q == p->q_out && (p->q_stride_t != p->q_out_stride_t || p->q_stride_h != p->q_out_stride_h)) ||
         (p->H_k > 0 && p->k == p->k_out && (p->k_stride_t != p->k_out_stride_t || p->k_stride_h != p->k_out_stride_h)))
         return SMLA_ERR_BAD_SHAPE;
-    // Rows over one another would be written by several threads: heads lie within a token's row, or tokens within a
-    // head's (any other order of rows apart is refused with those that overlap).
-    const auto overlapping = [&](int heads, int64_t st, int64_t sh) {
-        if ((heads > 1 && sh < p->D) || (p->T > 1 && st < p->D))
-            return true;
-        return heads > 1 && p->T > 1 && st < (heads - 1) * sh + p->D && sh < (p->T - 1) * st + p->D;
-    };
-    if ((p->H > 0 && overlapping(p->H, p->q_out_stride_t, p->q_out_stride_h)) ||
-        (p->H_k > 0 && overlapping(p->H_k, p->k_out_stride_t, p->k_out_stride_h)))
+    if ((p->H > 0 && smla::rows_overlap(p->T, p->H, p->D, p->q_out_stride_t, p->q_out_stride_h)) ||
+        (p->H_k > 0 && smla::rows_overlap(p->T, p->H_k, p->D, p->k_out_stride_t, p->k_out_stride_h)))
         return SMLA_ERR_BAD_SHAPE;
     smla::RopeArgs a{};
     if (p->H > 0) {
@@ -336,69 +387,17 @@ SMLA_API size_t smla_kv8_attn_workspace_size_of(const smla_kv8_attn_params *p)
 
 SMLA_API smla_status smla_kv8_attn_fwd(const smla_kv8_attn_params *p)
 {
+    return p == nullptr ? SMLA_ERR_NULL_POINTER : kv8_attn(p, nullptr);
+}
+
+SMLA_API smla_status smla_kv8_tree_attn_fwd(const smla_kv8_tree_attn_params *p)
+{
     if (p == nullptr)
         return SMLA_ERR_NULL_POINTER;
-    if (p->size < sizeof(smla_kv8_attn_params))
+    if (p->size < sizeof(smla_kv8_tree_attn_params) || p->tree_words < 1 || p->tree_words > (1 << 20))
         return SMLA_ERR_BAD_SHAPE;
-    if (const smla_status s = check_kv8_shape(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len); s != SMLA_OK)
-        return s;
-    if (p->num_blocks < 0 || p->table_width < 0 || p->table_stride < p->table_width || p->window < 0 ||
-        p->q_stride_t < 0 || p->q_stride_h < 0 || !std::isfinite(p->scale))
-        return SMLA_ERR_BAD_SHAPE;
-    if (block_shift(p->block_size) < 0 || ((int64_t)p->table_width << block_shift(p->block_size)) > kMostPositions ||
-        p->num_blocks > INT_MAX / p->H_kv)
-        return SMLA_ERR_UNSUPPORTED;
-    if (p->T == 0 || p->B == 0)
-        return SMLA_OK;
-    if (p->q == nullptr || p->out == nullptr || p->seq_lens == nullptr || p->query_start == nullptr ||
-        (p->table_width > 0 && p->block_table == nullptr) ||
-        (p->num_blocks > 0 && (p->k_cache == nullptr || p->v_cache == nullptr || p->k_scale == nullptr || p->v_scale == nullptr)) ||
-        p->workspace == nullptr)
-        return SMLA_ERR_NULL_POINTER;
-    const int64_t q_st = p->T > 1 ? p->q_stride_t : 0, q_sh = p->H > 1 ? p->q_stride_h : 0; // (of one row none is used)
-    if (q_st % 8 != 0 || q_sh % 8 != 0 || !aligned(p->q, 16) || !aligned(p->out, 16) ||
-        !aligned(p->k_cache, 16) || !aligned(p->v_cache, 16) || !aligned(p->k_scale, 4) || !aligned(p->v_scale, 4) ||
-        !aligned(p->block_table, 4) || !aligned(p->seq_lens, 4) || !aligned(p->query_start, 4) || !aligned(p->lse, 4) ||
-        !aligned(p->sinks, 4) || !aligned(p->workspace, 256))
-        return SMLA_ERR_MISALIGNED;
-    int sms = 0;
-    if (const cudaError_t e = current_sm_count(&sms); e != cudaSuccess)
-        return cuda_status(e);
-    if (p->workspace_bytes < kv8_workspace(p->B, p->T, p->H, p->H_kv, p->D, p->max_query_len,
-                                           (int64_t)p->table_width << block_shift(p->block_size), sms))
-        return SMLA_ERR_WORKSPACE_TOO_SMALL;
-    smla::Kv8AttnArgs a;
-    a.q = p->q;
-    a.q_st = q_st;
-    a.q_sh = q_sh;
-    a.k_cache = static_cast<const uint8_t *>(p->k_cache);
-    a.v_cache = static_cast<const uint8_t *>(p->v_cache);
-    a.k_scale = p->k_scale;
-    a.v_scale = p->v_scale;
-    a.num_blocks = p->num_blocks;
-    a.block_table = p->block_table;
-    a.table_stride = p->table_stride;
-    a.table_width = p->table_width;
-    a.seq_lens = p->seq_lens;
-    a.query_start = p->query_start;
-    a.B = p->B;
-    a.T = p->T;
-    a.H = p->H;
-    a.H_kv = p->H_kv;
-    a.G = p->H / p->H_kv;
-    a.block_size = p->block_size;
-    a.block_shift = block_shift(p->block_size);
-    // a window of all positions that the table has is none, and sums with others stay in 31 bits
-    a.window = p->window < (int64_t)p->table_width << a.block_shift ? p->window : 0;
-    a.scale = p->scale;
-    a.sinks = p->sinks;
-    a.out = p->out;
-    a.lse = p->lse;
-    if (!few_rows(p->H, p->H_kv, p->max_query_len))
-        return cuda_status(smla::launch_kv8_tile(a, p->D, p->max_query_len, p->workspace, sms,
-                                                 reinterpret_cast<cudaStream_t>(p->stream)));
-    return cuda_status(smla::launch_kv8_stream(a, p->D, p->max_query_len, p->workspace, sms,
-                                               reinterpret_cast<cudaStream_t>(p->stream)));
+    const Tree tree{p->tree_mask, p->tree_words, p->positions};
+    return kv8_attn(&p->attn, &tree);
 }
 
 } // extern "C"
