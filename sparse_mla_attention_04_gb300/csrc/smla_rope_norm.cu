@@ -4,10 +4,14 @@
 // y = x r (w + offset), r = (mean of x^2 over the head's D columns + eps)^-1/2, then the
 // rotated columns turned, all in binary32, and one rounding at the end: the split
 // chain (norm, store, rotation) rounds twice and moves every element twice.
-// Bound: the bytes in and out. Two lanes' worth of a row never meet in memory: a
-// row is a group of up to 32 lanes, each with two 16-byte chunks of it (with
-// halves, those that a rotation pairs), so a row is read once, its sum goes through
-// shuffles, and it may be written where it was.
+// A row is a group of up to 32 lanes, each with two 16-byte chunks of it (with halves,
+// those that a rotation pairs): it is read once, its sum goes through shuffles, and it
+// may be written where it was. Bound: the bytes in and out. Measured: 8192 tokens, 32 + 8
+// heads of 128 columns in bf16 (168 MB) in 36.2 us, 4.6 TB/s (the device's own copy of
+// as many bytes: 31), in 38.1 with binary32 weights of their own for each head; 64 tokens
+// 2.9 us. Two heads at a time instead of the next one read ahead: 45 to 47 us, since
+// registers leave fewer warps; 16 heads to a group 41, 4 38; arithmetic by single
+// elements and weights by single words 60.
 #include "smla_device.cuh"
 #include "smla_rope.cuh"
 #include "smla_step.h"
@@ -24,23 +28,118 @@ namespace {
 
 using namespace rope;
 
-constexpr int kBatch = 2;    // heads of a group on their way at a time
-constexpr int kThreads = 256;
+constexpr int kMostPer = 8; // heads that a group takes
+constexpr int kThreads = 128;
 
 // r of a row from the sum of its squares. Where that passes binary32 the row's
 // elements are to be taken 2^-70 times (`small`), and the sum is one of those: finite
-// for every finite row of up to 2^17 columns.
+// for every finite row of up to 2^17 columns. (rsqrtf: 2 units in the last place.)
 constexpr float kSmall = 0x1p-70f;
-__device__ __forceinline__ float inverse_rms(float sum, int D, float eps, bool small)
+__device__ __forceinline__ float inverse_rms(float sum, float inv_D, float eps, bool small)
 {
-    const float mean = __fdiv_rn(sum, (float)D);
-    return __frsqrt_rn(mean + (small ? eps * kSmall * kSmall : eps));
+    return rsqrtf(fmaf(sum, inv_D, small ? eps * kSmall * kSmall : eps));
 }
 
-template <typename Wt>
-__device__ __forceinline__ float weight_at(const void *w, int64_t i)
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y)
 {
-    return to_f(static_cast<const Wt *>(w)[i]);
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t r)
+{
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The values of a chunk in pairs, and pairs as a chunk.
+template <typename E> struct Chunk;
+template <> struct Chunk<__nv_bfloat16> {
+    static __device__ __forceinline__ void open(const uint4 &w, uint64_t (&v)[4])
+    {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = pair(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t word(uint64_t v)
+    {
+        const float2 f = unpair(v);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static __device__ __forceinline__ uint4 close(const uint64_t (&v)[4])
+    {
+        return make_uint4(word(v[0]), word(v[1]), word(v[2]), word(v[3]));
+    }
+};
+template <> struct Chunk<__half> {
+    static __device__ __forceinline__ void open(const uint4 &w, uint64_t (&v)[4])
+    {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[i]));
+            v[i] = pair(f.x, f.y);
+        }
+    }
+    static __device__ __forceinline__ uint32_t word(uint64_t v)
+    {
+        const float2 f = unpair(v);
+        const __half2 b = __floats2half2_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static __device__ __forceinline__ uint4 close(const uint64_t (&v)[4])
+    {
+        return make_uint4(word(v[0]), word(v[1]), word(v[2]), word(v[3]));
+    }
+};
+template <> struct Chunk<float> {
+    static __device__ __forceinline__ void open(const uint4 &w, uint64_t (&v)[2])
+    {
+        v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+        v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ uint4 close(const uint64_t (&v)[2])
+    {
+        const float2 a = unpair(v[0]), b = unpair(v[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+};
+
+// kVec weights from column col on, by 16 bytes where they are aligned (`whole`).
+template <typename Wt, int kVec>
+__device__ __forceinline__ void load_weights(const Wt *w, bool whole, float offset, float (&v)[kVec])
+{
+    if (whole) {
+        constexpr int kPer = 16 / sizeof(Wt);
+#pragma unroll
+        for (int i = 0; i < kVec / kPer; ++i) {
+            Pack<Wt, kPer> p;
+            p.w = __ldg(reinterpret_cast<const uint4 *>(w) + i);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                v[i * kPer + e] = to_f(p.at(e)) + offset;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            v[e] = to_f(w[e]) + offset;
+    }
 }
 
 // Where a group's lane stands: its two chunks' columns (-1: none) and whether they turn.
@@ -87,158 +186,145 @@ template <int kVec, bool kNeox> struct Place {
     }
 };
 
-// A group of blockDim.x lanes takes heads y, y + spread, ... of a token's queries, then of its keys.
+// A group of blockDim.x lanes takes `per` heads of a token's queries or keys one after another, the next one on its way
+// meanwhile.
 template <typename E, typename Wt, bool kNeox>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a, int spread)
+__global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeArgs a, int per, int q_groups, int groups)
 {
-    constexpr int kVec = 16 / sizeof(E);
-    using P = Pack<E, kVec>;
+    constexpr int kVec = 16 / sizeof(E), kPairs = kVec / 2;
+    using C = Chunk<E>;
     const int64_t item = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t t = item / spread;
-    const int y = (int)(item - t * spread);
+    const int64_t t = item / groups;
+    int y = (int)(item - t * groups);
     const bool live = t < a.T;
     const int64_t pos = live ? a.positions[t] : 0;
+    const bool side = y >= q_groups, reports = threadIdx.x == 0 && y == 0;
+    y -= side ? q_groups : 0;
     const Place<kVec, kNeox> at(a, threadIdx.x);
-    bool first = true, ok = live;
+    const int h0 = y * per, count = live ? min(per, (side ? a.H_k : a.H) - h0) : 0;
+    const int64_t sh = side ? a.k_sh : a.q_sh, oh = side ? a.ko_sh : a.qo_sh, wh = side ? a.kw_sh : a.qw_sh;
+    const E *src = static_cast<const E *>(side ? a.k : a.q) + t * (side ? a.k_st : a.q_st) + h0 * sh;
+    E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * (side ? a.ko_st : a.qo_st) + h0 * oh;
+    const Wt *w = static_cast<const Wt *>(side ? a.k_weight : a.q_weight);
+    const bool whole = ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(wh * sizeof(Wt))) & 15) == 0;
+    uint4 xa, xb; // the next head
+    const auto ask = [&](int i) {
+        xa = xb = make_uint4(0, 0, 0, 0);
+        if (i < count) {
+            const E *row = src + i * sh;
+            if (at.ca >= 0)
+                xa = __ldcs(reinterpret_cast<const uint4 *>(row + at.ca));
+            if (at.cb >= 0)
+                xb = __ldcs(reinterpret_cast<const uint4 *>(row + at.cb));
+        }
+    };
+    ask(0);
+    float wa[kVec], wb[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+        wa[e] = wb[e] = 1.f;
+    const auto weights = [&](int h) {
+        if (w && at.ca >= 0)
+            load_weights<Wt, kVec>(w + h * wh + at.ca, whole, a.weight_offset, wa);
+        if (w && at.cb >= 0)
+            load_weights<Wt, kVec>(w + h * wh + at.cb, whole, a.weight_offset, wb);
+    };
+    if (wh == 0)
+        weights(0);
+    const bool ok = live && pos >= 0 && pos < a.max_position;
+    if (live && !ok && reports)
+        atomicOr(&g_norm_rope_error, 4);
     float c[kVec], s[kVec]; // halves: of the pairs; interleaved: of chunk A's pairs, then of B's
 #pragma unroll
     for (int e = 0; e < kVec; ++e)
         c[e] = 1.f, s[e] = 0.f;
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-        const int count = side ? a.H_k : a.H;
-        if (count == 0)
-            continue;
-        const int64_t sh = side ? a.k_sh : a.q_sh, oh = side ? a.ko_sh : a.qo_sh, wh = side ? a.kw_sh : a.qw_sh;
-        const E *src = static_cast<const E *>(side ? a.k : a.q) + t * (side ? a.k_st : a.q_st);
-        E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * (side ? a.ko_st : a.qo_st);
-        const void *w = side ? a.k_weight : a.q_weight;
-        float wa[kVec], wb[kVec];
-        const auto weights = [&](int h) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                wa[e] = w && at.ca >= 0 ? weight_at<Wt>(w, h * wh + at.ca + e) + a.weight_offset : 1.f;
-                wb[e] = w && at.cb >= 0 ? weight_at<Wt>(w, h * wh + at.cb + e) + a.weight_offset : 1.f;
+    if (ok) {
+        const float *row = a.cos_sin + pos * a.rot_dim;
+        const int n = a.rot_dim / 2;
+        if (kNeox) {
+            if (at.ta) {
+                load_angles<kVec>(row + at.pair_a, c);
+                load_angles<kVec>(row + n + at.pair_a, s);
             }
-        };
-#pragma unroll 1
-        for (int h0 = y; h0 - y < count; h0 += kBatch * spread) { // (the same rounds for all groups of a warp)
-            P xa[kBatch], xb[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int h = h0 + i * spread;
-                xa[i].w = xb[i].w = make_uint4(0, 0, 0, 0);
-                if (live && h < count && at.ca >= 0)
-                    xa[i].load(src + h * sh + at.ca);
-                if (live && h < count && at.cb >= 0)
-                    xb[i].load(src + h * sh + at.cb);
+        } else {
+            if (at.ta) {
+                load_angles<kPairs>(row + at.pair_a, *reinterpret_cast<float(*)[kPairs]>(c));
+                load_angles<kPairs>(row + n + at.pair_a, *reinterpret_cast<float(*)[kPairs]>(s));
             }
-            if (wh == 0 && h0 == y)
-                weights(0);
-            if (first) {
-                first = false;
-                if (live && (pos < 0 || pos >= a.max_position)) {
-                    if (threadIdx.x == 0 && y == 0)
-                        atomicOr(&g_norm_rope_error, 4);
-                    ok = false;
-                }
-                if (ok) {
-                    const float *row = a.cos_sin + pos * a.rot_dim;
-                    const int n = a.rot_dim / 2;
-                    if (kNeox) {
-                        if (at.ta) {
-                            load_angles<kVec>(row + at.pair_a, c);
-                            load_angles<kVec>(row + n + at.pair_a, s);
-                        }
-                    } else {
-                        float(&ca)[kVec / 2] = *reinterpret_cast<float(*)[kVec / 2]>(c);
-                        float(&sa)[kVec / 2] = *reinterpret_cast<float(*)[kVec / 2]>(s);
-                        float(&cb)[kVec / 2] = *reinterpret_cast<float(*)[kVec / 2]>(c + kVec / 2);
-                        float(&sb)[kVec / 2] = *reinterpret_cast<float(*)[kVec / 2]>(s + kVec / 2);
-                        if (at.ta) {
-                            load_angles<kVec / 2>(row + at.pair_a, ca);
-                            load_angles<kVec / 2>(row + n + at.pair_a, sa);
-                        }
-                        if (at.tb) {
-                            load_angles<kVec / 2>(row + at.pair_b, cb);
-                            load_angles<kVec / 2>(row + n + at.pair_b, sb);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int h = h0 + i * spread;
-                float va[kVec], vb[kVec];
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    va[e] = to_f(xa[i].at(e));
-                    vb[e] = to_f(xb[i].at(e));
-                    sum = fmaf(va[e], va[e], sum);
-                    sum = fmaf(vb[e], vb[e], sum);
-                }
-                for (int d = 1; d < (int)blockDim.x; d <<= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const bool small = !(sum <= FLT_MAX);
-                if (__any_sync(0xffffffffu, small)) { // (seldom)
-                    float again = 0.f;
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        va[e] *= small ? kSmall : 1.f;
-                        vb[e] *= small ? kSmall : 1.f;
-                        again = fmaf(va[e], va[e], again);
-                        again = fmaf(vb[e], vb[e], again);
-                    }
-                    for (int d = 1; d < (int)blockDim.x; d <<= 1)
-                        again += __shfl_xor_sync(0xffffffffu, again, d);
-                    sum = small ? again : sum;
-                }
-                const float r = inverse_rms(sum, a.D, a.eps, small);
-                if (!ok || h >= count)
-                    continue; // (no shuffles below)
-                if (wh != 0)
-                    weights(h);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    va[e] = va[e] * r * wa[e];
-                    vb[e] = vb[e] * r * wb[e];
-                }
-                if (kNeox) {
-                    if (at.ta) {
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) {
-                            const float p = va[e], q = vb[e];
-                            va[e] = rot_a(p, q, c[e], s[e]);
-                            vb[e] = rot_b(p, q, c[e], s[e]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kVec / 2; ++e) {
-                        float p = va[2 * e], q = va[2 * e + 1];
-                        if (at.ta) {
-                            va[2 * e] = rot_a(p, q, c[e], s[e]);
-                            va[2 * e + 1] = rot_b(p, q, c[e], s[e]);
-                        }
-                        p = vb[2 * e], q = vb[2 * e + 1];
-                        if (at.tb) {
-                            vb[2 * e] = rot_a(p, q, c[kVec / 2 + e], s[kVec / 2 + e]);
-                            vb[2 * e + 1] = rot_b(p, q, c[kVec / 2 + e], s[kVec / 2 + e]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    xa[i].at(e) = from_f<E>(va[e]);
-                    xb[i].at(e) = from_f<E>(vb[e]);
-                }
-                if (at.ca >= 0)
-                    xa[i].store(dst + h * oh + at.ca);
-                if (at.cb >= 0)
-                    xb[i].store(dst + h * oh + at.cb);
+            if (at.tb) {
+                load_angles<kPairs>(row + at.pair_b, *reinterpret_cast<float(*)[kPairs]>(c + kPairs));
+                load_angles<kPairs>(row + n + at.pair_b, *reinterpret_cast<float(*)[kPairs]>(s + kPairs));
             }
         }
+    }
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) { // (the same rounds for all groups of a warp)
+        uint64_t va[kPairs], vb[kPairs], sums = 0;
+        C::open(xa, va);
+        C::open(xb, vb);
+        ask(i + 1);
+        if (wh != 0 && i < count)
+            weights(h0 + i);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e)
+            sums = fma2(vb[e], vb[e], fma2(va[e], va[e], sums));
+        const float2 both = unpair(sums);
+        float sum = both.x + both.y;
+        for (int d = 1; d < (int)blockDim.x; d <<= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const bool small = !(sum <= FLT_MAX);
+        if (__any_sync(0xffffffffu, small)) { // (seldom)
+            const uint64_t f = pair(small ? kSmall : 1.f, small ? kSmall : 1.f);
+            sums = 0;
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                va[e] = mul2(va[e], f);
+                vb[e] = mul2(vb[e], f);
+                sums = fma2(vb[e], vb[e], fma2(va[e], va[e], sums));
+            }
+            const float2 again = unpair(sums);
+            float x = again.x + again.y;
+            for (int d = 1; d < (int)blockDim.x; d <<= 1)
+                x += __shfl_xor_sync(0xffffffffu, x, d);
+            sum = small ? x : sum;
+        }
+        if (!ok || i >= count)
+            continue; // (no shuffles below)
+        const float r = inverse_rms(sum, a.inv_D, a.eps, small);
+        const uint64_t rr = pair(r, r);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            va[e] = mul2(mul2(va[e], rr), pair(wa[2 * e], wa[2 * e + 1]));
+            vb[e] = mul2(mul2(vb[e], rr), pair(wb[2 * e], wb[2 * e + 1]));
+        }
+        if (kNeox) {
+            if (at.ta) {
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) {
+                    const uint64_t p = va[e], q = vb[e], cc = pair(c[2 * e], c[2 * e + 1]);
+                    va[e] = fma2(p, cc, mul2(q, pair(-s[2 * e], -s[2 * e + 1])));
+                    vb[e] = fma2(q, cc, mul2(p, pair(s[2 * e], s[2 * e + 1])));
+                }
+            }
+        } else {
+            const auto turn = [](uint64_t v, float c, float s) {
+                const float2 x = unpair(v);
+                return pair(fmaf(x.x, c, -(x.y * s)), fmaf(x.y, c, x.x * s));
+            };
+            if (at.ta)
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    va[e] = turn(va[e], c[e], s[e]);
+            if (at.tb)
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    vb[e] = turn(vb[e], c[kPairs + e], s[kPairs + e]);
+        }
+        E *row = dst + i * oh;
+        if (at.ca >= 0)
+            __stcs(reinterpret_cast<uint4 *>(row + at.ca), C::close(va));
+        if (at.cb >= 0)
+            __stcs(reinterpret_cast<uint4 *>(row + at.cb), C::close(vb));
     }
 }
 
@@ -265,8 +351,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRopeA
     }
     const E *src = static_cast<const E *>(side ? a.k : a.q) + t * (side ? a.k_st : a.q_st) + h * (side ? a.k_sh : a.q_sh);
     E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * (side ? a.ko_st : a.qo_st) + h * (side ? a.ko_sh : a.qo_sh);
-    const void *w = side ? a.k_weight : a.q_weight;
-    const int64_t w0 = h * (side ? a.kw_sh : a.qw_sh);
+    const Wt *w = static_cast<const Wt *>(side ? a.k_weight : a.q_weight);
+    if (w)
+        w += h * (side ? a.kw_sh : a.qw_sh);
     float f = 1.f, sum = 0.f;
     for (int pass = 0; pass < 2; ++pass) {
         sum = 0.f;
@@ -281,9 +368,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRopeA
             break;
         f = kSmall;
     }
-    const float r = inverse_rms(sum, a.D, a.eps, f != 1.f);
+    const float r = inverse_rms(sum, a.inv_D, a.eps, f != 1.f);
     const auto value = [&](int i) {
-        return to_f(src[i]) * f * r * (w ? weight_at<Wt>(w, w0 + i) + a.weight_offset : 1.f);
+        return to_f(src[i]) * f * r * (w ? to_f(w[i]) + a.weight_offset : 1.f);
     };
     for (int i = lane; i < a.D - a.rot_dim; i += 32) {
         const int col = i < a.rot_offset ? i : i + a.rot_dim;
@@ -319,27 +406,20 @@ cudaError_t launch(const NormRopeArgs &a, int sm_count, cudaStream_t stream)
     int lanes = 1;
     while (lanes < units)
         lanes *= 2;
-    // Few tokens: a head to a group, so that all SMs have some. Many: as many groups to a token as leave each at least
-    // three rounds of heads (positions and angles are read once for them) and waste least of the rounds.
-    int spread = heads;
-    if ((int64_t)a.T * heads * lanes > (int64_t)sm_count * 2048) {
-        const auto rounds = [&](int y) {
-            return (a.H + kBatch * y - 1) / (kBatch * y) + (a.H_k + kBatch * y - 1) / (kBatch * y);
-        };
-        spread = 1;
-        for (int y = 2; y <= heads && rounds(y) >= 3; ++y)
-            if (rounds(y) * y <= rounds(spread) * spread)
-                spread = y;
-    }
+    // Few tokens: a head to a group, so that all SMs have some. Many: up to eight, so that positions and angles are read
+    // once for them.
+    const bool many = (int64_t)a.T * heads * lanes > (int64_t)sm_count * 2048;
+    const int per = many ? std::min(kMostPer, std::max(a.H, a.H_k)) : 1;
+    const int q_groups = (a.H + per - 1) / per, token_groups = q_groups + (a.H_k + per - 1) / per;
     const int groups = kThreads / lanes;
-    const int64_t blocks = ((int64_t)a.T * spread + groups - 1) / groups;
+    const int64_t blocks = ((int64_t)a.T * token_groups + groups - 1) / groups;
     if (blocks > INT_MAX)
         return cudaErrorInvalidValue;
     const dim3 block(lanes, groups);
     if (a.neox)
-        norm_rope_kernel<E, Wt, true><<<(unsigned)blocks, block, 0, stream>>>(a, spread);
+        norm_rope_kernel<E, Wt, true><<<(unsigned)blocks, block, 0, stream>>>(a, per, q_groups, token_groups);
     else
-        norm_rope_kernel<E, Wt, false><<<(unsigned)blocks, block, 0, stream>>>(a, spread);
+        norm_rope_kernel<E, Wt, false><<<(unsigned)blocks, block, 0, stream>>>(a, per, q_groups, token_groups);
     return cudaGetLastError();
 }
 

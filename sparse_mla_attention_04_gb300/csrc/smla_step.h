@@ -99,7 +99,7 @@ struct NormRopeArgs {
     int64_t q_st, q_sh, qo_st, qo_sh, k_st, k_sh, ko_st, ko_sh;
     const void *q_weight, *k_weight; // [D] (stride 0) or a row to a head; nullptr: ones
     int64_t qw_sh, kw_sh;
-    float weight_offset, eps;
+    float weight_offset, eps, inv_D;
     const int64_t *positions;
     const float *cos_sin;
     int64_t max_position;
@@ -216,7 +216,11 @@ struct Kv8AttnArgs {
 };
 size_t kv8_tile_workspace(int B, int T, int H, int H_kv, int D, int max_query_len, int sm_count);
 cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, int max_query_len, void *workspace, int sm_count, cudaStream_t stream);
-cudaError_t read_kv8_error(int *out, bool reset);
+cudaError_t read_kv8_error(int *out, bool reset); // and that of the rows kernel
+// for drafted trees of some dozens of rows to a request
+size_t kv8_rows_workspace(int D, int sm_count);
+cudaError_t launch_kv8_rows(const Kv8AttnArgs &a, int D, void *workspace, int sm_count, cudaStream_t stream);
+cudaError_t read_kv8_rows_error(int *out, bool reset);
 cudaError_t read_kv8_stream_error(int *out, bool reset);
 // positions: those that the block table has at most
 size_t kv8_stream_workspace(int B, int T, int G, int H_kv, int D, int max_query_len, int64_t positions, int sm_count);

@@ -102,6 +102,7 @@ SMLA_API smla_status smla_qk_norm_rope(const smla_qk_norm_rope_params *p)
     }
     a.weight_offset = p->weight_offset;
     a.eps = p->eps;
+    a.inv_D = 1.0f / (float)p->D;
     a.positions = p->positions;
     a.cos_sin = p->cos_sin_cache;
     a.max_position = p->max_position;

@@ -22,8 +22,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kLanes = 32, kUnit = kForkUnit, kPer = kUnit / kLanes;
-// Up to this many entries of the old and new rows one block does it all.
-constexpr int64_t kOneBlockEntries = 16384;
+// Up to this many entries of the old and new rows one block does it all, without the launches of the five phases:
+// 264 entries 6.6 us by one block and 9.5 by launches, 4000 7.7 and 10.9, 16000 12.5 and 11.1, 131584 (256 old and 256
+// new rows of 257) 114 and 11.9. (A cluster of eight blocks: 9.6, 11.0, 13.6, 23.)
+constexpr int64_t kOneBlockEntries = 8192;
 
 // A new row: the old one that it goes on from (-1: none), what it keeps.
 struct NewRow {
@@ -64,15 +66,46 @@ __device__ __forceinline__ unsigned ring_place(const ForkArgs &a, unsigned head,
 // The units of rows: row u / units, entries from u % units * kUnit on.
 __device__ __forceinline__ int units_of(const ForkArgs &a) { return max(1, (a.table_width + kUnit - 1) / kUnit); }
 
+// A lane's entries of a unit, all on their way at once: -1 where there is none, or none of the pool's.
+__device__ __forceinline__ void load_unit(const ForkArgs &a, const int32_t *row, int j0, int end, int lane, int (&e)[kPer])
+{
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int j = j0 + k * kLanes + lane;
+        e[k] = j < end ? row[j] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        e[k] = in_pool(a, e[k]) ? e[k] : -1;
+}
+
+// A bit to each of the lane's entries that gives its block back.
+__device__ __forceinline__ unsigned giving(const ForkArgs &a, int r, int j0, int lane, const int (&e)[kPer])
+{
+    uint32_t m[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        m[k] = e[k] >= 0 ? mark_of(a, e[k]) : 0;
+    unsigned bits = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        bits |= (unsigned)(e[k] >= 0 && m[k] == place(a, r, j0 + k * kLanes + lane)) << k;
+    return bits;
+}
+
 __device__ __forceinline__ void clear_marks(const ForkArgs &a, int64_t warp, int64_t warps, int lane)
 {
     const int units = units_of(a);
     for (int64_t u = warp; u < (int64_t)a.B_old * units; u += warps) {
         const int r = (int)(u / units), j0 = (int)(u % units) * kUnit, end = min(held_of(a, r), j0 + kUnit);
-        const int32_t *row = old_row(a, r);
-        for (int j = j0 + lane; j < end; j += kLanes)
-            if (const int e = row[j]; in_pool(a, e))
-                a.marks[e] = 0xFFFFFFFFu;
+        if (j0 >= end)
+            continue;
+        int e[kPer];
+        load_unit(a, old_row(a, r), j0, end, lane, e);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (e[k] >= 0)
+                a.marks[e[k]] = 0xFFFFFFFFu;
     }
 }
 
@@ -90,10 +123,14 @@ __device__ __forceinline__ void set_marks(const ForkArgs &a, int64_t warp, int64
         const int end = min(is_new ? x.blocks : held_of(a, b), j0 + kUnit);
         if (j0 >= end)
             continue;
-        const int32_t *row = old_row(a, x.source);
-        for (int j = j0 + lane; j < end; j += kLanes)
-            if (const int e = row[j]; in_pool(a, e))
-                atomicMin(a.marks + e, !is_new ? place(a, b, j) : x.tail && j == x.blocks - 1 ? 1u + (uint32_t)b : 0u);
+        int e[kPer];
+        load_unit(a, old_row(a, x.source), j0, end, lane, e);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int j = j0 + k * kLanes + lane;
+            if (e[k] >= 0)
+                atomicMin(a.marks + e[k], !is_new ? place(a, b, j) : x.tail && j == x.blocks - 1 ? 1u + (uint32_t)b : 0u);
+        }
     }
 }
 
@@ -103,12 +140,12 @@ __device__ __forceinline__ void count_gives(const ForkArgs &a, int64_t warp, int
     const int units = units_of(a);
     for (int64_t u = warp; u < (int64_t)a.B_old * units; u += warps) {
         const int r = (int)(u / units), j0 = (int)(u % units) * kUnit, end = min(held_of(a, r), j0 + kUnit);
-        const int32_t *row = old_row(a, r);
         int n = 0;
-        for (int j = j0 + lane; j < end; j += kLanes)
-            if (const int e = row[j]; in_pool(a, e))
-                n += mark_of(a, e) == place(a, r, j);
-        n = __reduce_add_sync(0xffffffffu, n);
+        if (j0 < end) {
+            int e[kPer];
+            load_unit(a, old_row(a, r), j0, end, lane, e);
+            n = __reduce_add_sync(0xffffffffu, __popc(giving(a, r, j0, lane, e)));
+        }
         if (lane == 0)
             a.gives[u] = n;
     }
@@ -218,26 +255,33 @@ __device__ __forceinline__ void fill(const ForkArgs &a, int64_t warp, int64_t wa
                 continue;
             const int32_t *row = old_row(a, p.x);
             int32_t *out = a.block_table_out + b * a.out_stride;
+            int e[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int j = j0 + k * kLanes + lane;
+                e[k] = j < p.y ? row[j] : 0;
+            }
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int j = j0 + k * kLanes + lane;
                 if (j < p.y)
-                    out[j] = p.z >= 0 && j == p.y - 1 ? own : row[j];
+                    out[j] = p.z >= 0 && j == p.y - 1 ? own : e[k];
             }
         } else if (ok) {
             const int64_t v = u - new_units;
             const int r = (int)(v / units), j0 = (int)(v % units) * kUnit, end = min(held_of(a, r), j0 + kUnit);
             if (j0 >= end)
                 continue;
-            const int32_t *row = old_row(a, r);
             unsigned at = a.gives[v];
-            for (int j1 = j0; j1 < end; j1 += kLanes) {
-                const int j = j1 + lane;
-                const int e = j < end ? row[j] : -1;
-                const bool gives = j < end && in_pool(a, e) && mark_of(a, e) == place(a, r, j);
+            int e[kPer];
+            load_unit(a, old_row(a, r), j0, end, lane, e);
+            const unsigned bits = giving(a, r, j0, lane, e);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const bool gives = bits >> k & 1;
                 const unsigned votes = __ballot_sync(0xffffffffu, gives);
                 if (gives)
-                    a.free_ring[ring_place(a, end_place, at + __popc(votes & ((1u << lane) - 1)))] = e;
+                    a.free_ring[ring_place(a, end_place, at + __popc(votes & ((1u << lane) - 1)))] = e[k];
                 at += __popc(votes);
             }
         }
