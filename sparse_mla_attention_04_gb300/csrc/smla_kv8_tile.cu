@@ -1270,11 +1270,7 @@ cudaError_t launch_kv8_tile(const Kv8AttnArgs &a, int D, int max_query_len, void
 
 cudaError_t read_kv8_error(int *out, bool reset)
 {
-    int rows = 0;
-    if (const cudaError_t e = read_kv8_rows_error(&rows, reset); e != cudaSuccess)
-        return e;
     cudaError_t e = cudaMemcpyFromSymbol(out, g_kv8_error, sizeof(int));
-    *out |= rows;
     if (e == cudaSuccess && reset) {
         const int zero = 0;
         e = cudaMemcpyToSymbol(g_kv8_error, &zero, sizeof(int));

@@ -48,14 +48,6 @@ smla_status check_kv8_shape(int B, int T, int H, int H_kv, int D, int max_query_
     return SMLA_OK;
 }
 
-// Rows of a request's tree that the rows kernel takes, in units of 64 (its workspace is smaller than the tile
-// kernel's, which calls are asked for).
-bool some_rows(int H, int H_kv, int max_query_len)
-{
-    const int64_t rows = (int64_t)(H / H_kv) * max_query_len;
-    return rows > 16 && rows <= 128;
-}
-
 // The masks of drafted trees, for smla_kv8_tree_attn_fwd (mask NULL: none).
 struct Tree {
     const uint64_t *mask;
@@ -125,8 +117,6 @@ smla_status kv8_attn(const smla_kv8_attn_params *p, const Tree *tree)
     a.tree_mask = tree ? tree->mask : nullptr;
     a.tree_words = tree ? tree->words : 0;
     a.tree_positions = tree ? tree->positions : nullptr;
-    if (tree && some_rows(p->H, p->H_kv, p->max_query_len))
-        return cuda_status(smla::launch_kv8_rows(a, p->D, p->workspace, sms, reinterpret_cast<cudaStream_t>(p->stream)));
     if (!few_rows(p->H, p->H_kv, p->max_query_len))
         return cuda_status(smla::launch_kv8_tile(a, p->D, p->max_query_len, p->workspace, sms,
                                                  reinterpret_cast<cudaStream_t>(p->stream)));
