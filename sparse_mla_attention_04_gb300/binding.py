@@ -1043,6 +1043,19 @@ def new_kv8_cache(num_blocks: int, H_kv: int, block_size: int, D: int, device="c
 # ---- steps that draft and branch: norms with the rotation, tree masks, kept tokens, forked tables, block copies
 
 
+def _head_weight(w: Optional[torch.Tensor], name: str, heads: int, D: int, dtype, device: torch.device):
+    """A norm's weights: their address and the stride from head to head (0: one row for all; no weights: 0, 0)."""
+    if w is None:
+        return 0, 0
+    if not isinstance(w, torch.Tensor) or (w.dtype is not dtype and w.dtype is not torch.float32):
+        raise TypeError("%s must be a tensor of %s or torch.float32" % (name, dtype))
+    ndim = w.dim()
+    if (ndim != 1 or w.shape[0] != D) and w.shape != (heads, D):
+        raise ValueError("%s must be [%d] or [%d, %d], got %s" % (name, D, heads, D, tuple(w.shape)))
+    _rows(w, name, w.dtype, ndim, device)
+    return w.data_ptr(), w.stride(0) if ndim == 2 else 0
+
+
 def smla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor],
                       k_weight: Optional[torch.Tensor], positions: torch.Tensor, cos_sin_cache: torch.Tensor, *,
                       eps: float = 1e-6, weight_offset: float = 0.0, rot_offset: int = 0, is_neox: bool = True,
@@ -1065,31 +1078,21 @@ def smla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Opti
             raise ValueError("k must be [T, H_k, D] = [%d, *, %d], got %s" % (T, D, tuple(k.shape)))
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out or k_weight without k")
-    wtype = dtype
-    weights = []
-    for name, w, x in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
-        if w is None:
-            weights += [0, 0]
-            continue
-        if not isinstance(w, torch.Tensor) or (w.dtype != dtype and w.dtype != torch.float32):
-            raise TypeError("%s must be a tensor of %s or torch.float32" % (name, dtype))
-        if not weights or weights[0] == 0:
-            wtype = w.dtype
-        elif w.dtype != wtype:
-            raise TypeError("q_weight is %s, k_weight %s" % (wtype, w.dtype))
-        _rows(w, name, wtype, w.dim(), dev)
-        if w.shape != (D,) and w.shape != (x.shape[1], D):
-            raise ValueError("%s must be [%d] or [%d, %d], got %s" % (name, D, x.shape[1], D, tuple(w.shape)))
-        weights += [w.data_ptr(), w.stride(0) if w.dim() == 2 else 0]
+    qw, qw_stride = _head_weight(q_weight, "q_weight", H, D, dtype, dev)
+    kw, kw_stride = _head_weight(k_weight, "k_weight", 0 if k is None else k.shape[1], D, dtype, dev)
+    wtype = dtype if q_weight is None and k_weight is None else (k_weight if q_weight is None else q_weight).dtype
+    if k_weight is not None and k_weight.dtype is not wtype:
+        raise TypeError("q_weight is %s, k_weight %s" % (wtype, k_weight.dtype))
     _fits(positions, "positions", torch.int64, 1, dev)
     if positions.shape[0] != T:
         raise ValueError("positions must be [T] = [%d]" % T)
     _fits(cos_sin_cache, "cos_sin_cache", torch.float32, 2, dev)
-    for name, x, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if x is not None and x is not like:
-            _rows(x, name, dtype, 3, dev)
-            if x.shape != like.shape:
-                raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(x.shape)))
+    if q_out is not None or k_out is not None:
+        for name, x, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if x is not None and x is not like:
+                _rows(x, name, dtype, 3, dev)
+                if x.shape != like.shape:
+                    raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(x.shape)))
     L = _lib or lib()
     with _on(dev, stream) as handle:
         if q_out is None:
@@ -1107,7 +1110,7 @@ def smla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Opti
         P, rot = cos_sin_cache.shape
         st = L.smla_qk_norm_rope(_QK_NORM_ROPE_PARAMS.pack(
             _QK_NORM_ROPE_PARAMS.size, _DTYPE[dtype], _DTYPE[wtype], q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os[0],
-            os[1], *ks, *weights, weight_offset, eps, positions.data_ptr(), cos_sin_cache.data_ptr(), P, T, H, Hk, D, rot,
+            os[1], *ks, qw, qw_stride, kw, kw_stride, weight_offset, eps, positions.data_ptr(), cos_sin_cache.data_ptr(), P, T, H, Hk, D, rot,
             rot_offset, 1 if is_neox else 0, handle))
     if st:
         _check(st, "smla_qk_norm_rope")
@@ -1143,12 +1146,8 @@ def smla_build_tree_masks(parents: torch.Tensor, seq_lens: torch.Tensor, query_s
     words = max(1, (max_query_len + 63) // 64)
     L = _lib or lib()
     with _on(dev, stream) as handle:
-        if tree_mask is None and positions is None:
-            both = torch.empty(T * (words + 1), dtype=torch.int64, device=dev)
-            tree_mask, positions = both[:T * words].view(T, words), both[T * words:]
-        else:
-            tree_mask = _out(tree_mask, "tree_mask", (T, words), torch.int64, dev)
-            positions = _out(positions, "positions", (T,), torch.int64, dev)
+        tree_mask = _out(tree_mask, "tree_mask", (T, words), torch.int64, dev)
+        positions = _out(positions, "positions", (T,), torch.int64, dev)
         st = L.smla_build_tree_masks(parents.data_ptr(), seq_lens.data_ptr(), query_start.data_ptr(), B, T, words, window,
                                      tree_mask.data_ptr(), positions.data_ptr(), handle)
     if st:

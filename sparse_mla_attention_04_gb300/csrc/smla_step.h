@@ -174,7 +174,7 @@ struct ForkArgs {
     uint32_t *marks;     // [num_blocks]
     int32_t *gives;      // [B_old * units] blocks that the unit gives back, then where its first one goes
     int4 *plan;          // [B] source row, blocks, the number of its new last block (-1: none)
-    int32_t *state;      // [3] ring head and count before the call, whether blocks lack
+    int32_t *state;      // [4] ring head and count before the call, whether blocks lack, blocks done
 };
 cudaError_t launch_fork_tables(const ForkArgs &a, int sm_count, cudaStream_t stream);
 

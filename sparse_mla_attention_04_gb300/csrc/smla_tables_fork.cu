@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kLanes = 32, kUnit = kForkUnit, kPer = kUnit / kLanes;
-// Up to this many entries of the old and new rows one block does it all, without the launches of the five phases:
+// Up to this many entries of the old and new rows one block does it all, without the launches of the phases:
 // 264 entries 6.6 us by one block and 9.5 by launches, 4000 7.7 and 10.9, 16000 12.5 and 11.1, 131584 (256 old and 256
 // new rows of 257) 114 and 11.9. (A cluster of eight blocks: 9.6, 11.0, 13.6, 23.)
 constexpr int64_t kOneBlockEntries = 8192;
@@ -190,7 +190,7 @@ __device__ __forceinline__ void sum_up(const ForkArgs &a)
     long long given = 0, taken = 0, tokens = 0, total;
     for (int64_t u0 = 0; u0 < units; u0 += kThreads) {
         const int64_t u = u0 + tid;
-        const long long n = u < units ? a.gives[u] : 0;
+        const long long n = u < units ? __ldcg(a.gives + u) : 0; // (other blocks' writes)
         const long long at = given + block_exclusive(n, &total, warp_sums);
         if (u < units)
             a.gives[u] = (int)at;
@@ -303,27 +303,39 @@ __global__ void __launch_bounds__(kThreads) fork_one_kernel(const ForkArgs a)
     fill(a, warp, warps, lane);
 }
 
-enum class Phase { kClear, kSet, kCount, kFill };
+enum class Phase { kClear, kSet, kFill };
 template <Phase kPhase> __global__ void __launch_bounds__(256) fork_phase_kernel(const ForkArgs a)
 {
     umma::grid_launch_dependents();
     umma::grid_wait(); // the phase before
     const int lane = threadIdx.x & 31;
     const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    if (kPhase == Phase::kClear)
+    if (kPhase == Phase::kClear) {
+        if (warp == 0 && lane == 0)
+            a.state[3] = 0; // the counting blocks that are done
         clear_marks(a, warp, warps, lane);
-    else if (kPhase == Phase::kSet)
+    } else if (kPhase == Phase::kSet) {
         set_marks(a, warp, warps, lane);
-    else if (kPhase == Phase::kCount)
-        count_gives(a, warp, warps, lane);
-    else
+    } else {
         fill(a, warp, warps, lane);
+    }
 }
 
-__global__ void __launch_bounds__(kThreads) fork_sum_kernel(const ForkArgs a)
+// Counts, and by the block that is done last the sums.
+__global__ void __launch_bounds__(kThreads) fork_count_kernel(const ForkArgs a)
 {
+    __shared__ bool s_last;
     umma::grid_launch_dependents();
     umma::grid_wait();
+    count_gives(a, (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), (int64_t)gridDim.x * (kThreads / 32), threadIdx.x & 31);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = atomicAdd(a.state + 3, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!s_last)
+        return;
+    __threadfence();
     sum_up(a);
 }
 
@@ -353,9 +365,7 @@ cudaError_t launch_fork_tables(const ForkArgs &a, int sm_count, cudaStream_t str
     if (e == cudaSuccess)
         e = go(fork_phase_kernel<Phase::kSet>, blocks, 256);
     if (e == cudaSuccess)
-        e = go(fork_phase_kernel<Phase::kCount>, blocks, 256);
-    if (e == cudaSuccess)
-        e = go(fork_sum_kernel, 1, kThreads);
+        e = go(fork_count_kernel, (blocks + 3) / 4, kThreads);
     if (e == cudaSuccess)
         e = go(fork_phase_kernel<Phase::kFill>, blocks, 256);
     return e;
