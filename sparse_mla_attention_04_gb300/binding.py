@@ -1215,6 +1215,8 @@ class TokenPools:
             self.num_blocks, self.heads, self.block_size, self.row_bytes = shape
             if block_size is not None and block_size != self.block_size:
                 raise ValueError("block_size is %d, the caches' %d" % (block_size, self.block_size))
+        if len({x.data_ptr() for x in codes}) != len(codes) and self.num_blocks > 0:
+            raise ValueError("a pool stands twice among the caches (its rows would move twice)")
         self.tensors = (codes, scales)
         self.count = len(codes)
         self.pools = (_c.c_void_p * self.count)(*[x.data_ptr() for x in codes])

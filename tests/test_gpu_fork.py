@@ -139,6 +139,13 @@ def test_strided_tables_streams_and_replay(W):
     with pytest.raises(ValueError):
         binding.smla_fork_block_tables(src, kp, hd, buffers[0, :, :W], rg, st, block_size=bs, num_blocks=nb,
                                        block_table_out=buffers[1])
+    with pytest.raises(binding.SmlaError):
+        binding.smla_fork_block_tables(src, kp, hd, buffers[0, :, :W], rg, st, block_size=bs, num_blocks=nb,
+                                       block_table_out=buffers[1, :, :W], workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(binding.SmlaError):
+        binding.smla_fork_block_tables(src, kp, hd, buffers[0, :, :W], rg, st, block_size=24, num_blocks=nb)
+    with pytest.raises(ValueError):
+        binding.smla_fork_block_tables(src, kp[:3], hd, buffers[0, :, :W], rg, st, block_size=bs, num_blocks=nb)
     side = torch.cuda.Stream()
     rg, st = _up(ring), _up(state)
     torch.cuda.synchronize()

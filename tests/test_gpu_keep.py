@@ -158,6 +158,10 @@ def test_strided_tables_many_layers_and_replay():
         binding.smla_keep_tokens(handle, wide, n, q, list_wide, c, block_size=32)
     with pytest.raises(ValueError):
         binding.TokenPools([got[0], tuple(x[:1] for x in got[1])])
+    with pytest.raises(ValueError):
+        binding.TokenPools([got[0], got[1], got[0]])                 # its rows would move twice
+    with pytest.raises(ValueError):
+        binding.TokenPools([got[0][0].view(-1, 64), got[1][0].view(-1, 64)])                   # latent pools without block_size
 
 
 def test_pools_past_32_bits():
