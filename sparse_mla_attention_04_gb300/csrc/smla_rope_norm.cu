@@ -6,12 +6,14 @@
 // chain (norm, store, rotation) rounds twice and moves every element twice.
 // A row is a group of up to 32 lanes, each with two 16-byte chunks of it (with halves,
 // those that a rotation pairs): it is read once, its sum goes through shuffles, and it
-// may be written where it was. Bound: the bytes in and out. Measured: 8192 tokens, 32 + 8
-// heads of 128 columns in bf16 (168 MB) in 36.2 us, 4.6 TB/s (the device's own copy of
-// as many bytes: 31), in 38.1 with binary32 weights of their own for each head; 64 tokens
-// 2.9 us. Two heads at a time instead of the next one read ahead: 45 to 47 us, since
-// registers leave fewer warps; 16 heads to a group 41, 4 38; arithmetic by single
-// elements and weights by single words 60.
+// may be written where it was. Bound: the bytes in and out. Measured on the device: 8192
+// tokens, 32 + 8 heads of 128 columns in bf16 (168 MB) in 29.0 us, 5.8 TB/s (the
+// device's own copy of as many bytes: 31), in 40.5 with binary32 weights of their own for
+// each head, which are read again for each row (from L1, twice the row's own bytes); 64
+// tokens 2.6 us. What counted: arithmetic on pairs of elements and weights by 16 bytes (60 us
+// by single ones), more warps (two heads at a time in registers 45, one and the next
+// 36), three heads on their way in shared memory (29; with weights for each head 44,
+// since the L1 cache gets smaller), eight heads to a group (four 32, sixteen 33).
 #include "smla_device.cuh"
 #include "smla_rope.cuh"
 #include "smla_step.h"
@@ -29,6 +31,7 @@ namespace {
 using namespace rope;
 
 constexpr int kMostPer = 8; // heads that a group takes
+constexpr int kDepth = 4;   // and that are on their way at a time, with the one in hand (a power of two)
 constexpr int kThreads = 128;
 
 // r of a row from the sum of its squares. Where that passes binary32 the row's
@@ -63,6 +66,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -186,9 +196,15 @@ template <int kVec, bool kNeox> struct Place {
     }
 };
 
+// Sixteen bytes to shared memory, without waiting.
+__device__ __forceinline__ void copy16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // A group of blockDim.x lanes takes `per` heads of a token's queries or keys one after another, the next one on its way
 // meanwhile.
-template <typename E, typename Wt, bool kNeox>
+template <typename E, typename Wt, bool kNeox, bool kHeads>
 __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeArgs a, int per, int q_groups, int groups)
 {
     constexpr int kVec = 16 / sizeof(E), kPairs = kVec / 2;
@@ -207,30 +223,44 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeAr
     E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * (side ? a.ko_st : a.qo_st) + h0 * oh;
     const Wt *w = static_cast<const Wt *>(side ? a.k_weight : a.q_weight);
     const bool whole = ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(wh * sizeof(Wt))) & 15) == 0;
-    uint4 xa, xb; // the next head
+    // The next heads' chunks come to the thread's own places in shared memory, which hold no registers meanwhile; with
+    // weights for each head, which want the L1 cache, the next one's to registers.
+    __shared__ uint4 s_ring[kHeads ? 1 : kDepth][2][kHeads ? 1 : kThreads];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint4 xa = none, xb = none;
     const auto ask = [&](int i) {
-        xa = xb = make_uint4(0, 0, 0, 0);
-        if (i < count) {
-            const E *row = src + i * sh;
-            if (at.ca >= 0)
-                xa = __ldcs(reinterpret_cast<const uint4 *>(row + at.ca));
-            if (at.cb >= 0)
-                xb = __ldcs(reinterpret_cast<const uint4 *>(row + at.cb));
+        const E *row = src + i * sh;
+        const bool in_a = i < count && at.ca >= 0, in_b = i < count && at.cb >= 0;
+        if (kHeads) {
+            xa = in_a ? __ldcs(reinterpret_cast<const uint4 *>(row + at.ca)) : none;
+            xb = in_b ? __ldcs(reinterpret_cast<const uint4 *>(row + at.cb)) : none;
+        } else {
+            if (in_a)
+                copy16(&s_ring[i % kDepth][0][tid], row + at.ca);
+            if (in_b)
+                copy16(&s_ring[i % kDepth][1][tid], row + at.cb);
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
     };
     ask(0);
+    if (!kHeads)
+#pragma unroll
+        for (int i = 1; i < kDepth - 1; ++i)
+            ask(i);
     float wa[kVec], wb[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e)
         wa[e] = wb[e] = 1.f;
     const auto weights = [&](int h) {
         if (w && at.ca >= 0)
-            load_weights<Wt, kVec>(w + h * wh + at.ca, whole, a.weight_offset, wa);
+            load_weights<Wt, kVec>(w + h * wh + at.ca, whole, kHeads ? 0.f : a.weight_offset, wa);
         if (w && at.cb >= 0)
-            load_weights<Wt, kVec>(w + h * wh + at.cb, whole, a.weight_offset, wb);
+            load_weights<Wt, kVec>(w + h * wh + at.cb, whole, kHeads ? 0.f : a.weight_offset, wb);
     };
-    if (wh == 0)
+    if (!kHeads)
         weights(0);
+    const uint64_t offset = w ? pair(a.weight_offset, a.weight_offset) : 0; // (of weights for each head)
     const bool ok = live && pos >= 0 && pos < a.max_position;
     if (live && !ok && reports)
         atomicOr(&g_norm_rope_error, 4);
@@ -260,11 +290,18 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeAr
 #pragma unroll 1
     for (int i = 0; i < per; ++i) { // (the same rounds for all groups of a warp)
         uint64_t va[kPairs], vb[kPairs], sums = 0;
-        C::open(xa, va);
-        C::open(xb, vb);
-        ask(i + 1);
-        if (wh != 0 && i < count)
-            weights(h0 + i);
+        if (kHeads) {
+            if (i < count) // asked for before the head is waited for
+                weights(h0 + i);
+            C::open(xa, va);
+            C::open(xb, vb);
+            ask(i + 1);
+        } else {
+            ask(i + kDepth - 1);
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
+            C::open(at.ca >= 0 && i < count ? s_ring[i % kDepth][0][tid] : none, va);
+            C::open(at.cb >= 0 && i < count ? s_ring[i % kDepth][1][tid] : none, vb);
+        }
 #pragma unroll
         for (int e = 0; e < kPairs; ++e)
             sums = fma2(vb[e], vb[e], fma2(va[e], va[e], sums));
@@ -294,8 +331,13 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeAr
         const uint64_t rr = pair(r, r);
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) {
-            va[e] = mul2(mul2(va[e], rr), pair(wa[2 * e], wa[2 * e + 1]));
-            vb[e] = mul2(mul2(vb[e], rr), pair(wb[2 * e], wb[2 * e + 1]));
+            uint64_t fa = pair(wa[2 * e], wa[2 * e + 1]), fb = pair(wb[2 * e], wb[2 * e + 1]);
+            if (kHeads) {
+                fa = add2(fa, offset);
+                fb = add2(fb, offset);
+            }
+            va[e] = mul2(mul2(va[e], rr), fa);
+            vb[e] = mul2(mul2(vb[e], rr), fb);
         }
         if (kNeox) {
             if (at.ta) {
@@ -416,10 +458,10 @@ cudaError_t launch(const NormRopeArgs &a, int sm_count, cudaStream_t stream)
     if (blocks > INT_MAX)
         return cudaErrorInvalidValue;
     const dim3 block(lanes, groups);
-    if (a.neox)
-        norm_rope_kernel<E, Wt, true><<<(unsigned)blocks, block, 0, stream>>>(a, per, q_groups, token_groups);
-    else
-        norm_rope_kernel<E, Wt, false><<<(unsigned)blocks, block, 0, stream>>>(a, per, q_groups, token_groups);
+    const bool each = a.qw_sh != 0 || a.kw_sh != 0; // weights of their own for each head
+    const auto kernel = a.neox ? (each ? norm_rope_kernel<E, Wt, true, true> : norm_rope_kernel<E, Wt, true, false>)
+                               : (each ? norm_rope_kernel<E, Wt, false, true> : norm_rope_kernel<E, Wt, false, false>);
+    kernel<<<(unsigned)blocks, block, 0, stream>>>(a, per, q_groups, token_groups);
     return cudaGetLastError();
 }
 
