@@ -79,6 +79,9 @@ constexpr int kMinPart = 22;  // a CTA's part of the work, in tiles, before more
 // The CTA's place in the work, and what else its warps share.
 struct Misc {
     long long at, hi, total; // cost: where it is, where its part ends, all
+    long long base;          // without a plan: before the request `item`,
+    int q0, qlen, len;       // that request,
+    int tiles, count;        // and its units
     int item, parts;
     int units, next;         // units taken whole (0: the work is cut into parts), the next one
     uint32_t tmem;
@@ -138,6 +141,17 @@ struct Plan {
     int n_items, item_rows;
 };
 
+// Drafted trees of few requests go without that kernel and its launch: all rows of a request see the same tiles, so
+// the CTAs find their parts by the requests alone (as the streaming kernel does), where units are too few to be taken
+// whole (`items` is NULL). 16 requests of 8192 positions with 16 nodes 75.6 us, planned 79.5; one of 509 with 8 17.8 and
+// 19.6.
+
+// The units of a request with drafted trees and the cost of each.
+struct Units {
+    int tiles, count, cost;
+    __device__ long long all() const { return (long long)count * cost; }
+};
+
 // A tile's item: request, chunk of rows, kv head.
 struct Item {
     int b, chunk, h;
@@ -185,6 +199,80 @@ __device__ __forceinline__ Span span_of(const Kv8AttnArgs &a, int item_rows, con
     s.tb0 = s.kv_begin & ~(kTile - 1);
     s.tiles = s.kv_end > s.tb0 ? (s.kv_end - s.tb0 + kTile - 1) / kTile : 0;
     return s;
+}
+
+__device__ __forceinline__ Units units_of(const Kv8AttnArgs &a, int item_rows, const Request &rq)
+{
+    Units u;
+    u.tiles = rq.qlen > 0 ? span_of(a, item_rows, rq, 0).tiles : 0;
+    u.count = (int)(((long long)rq.qlen * a.G + item_rows - 1) / item_rows * a.H_kv); // (checked on the host)
+    u.cost = max(1, u.tiles) + kPieceCost;
+    return u;
+}
+
+// This CTA's part of the work without a plan, by the whole block: each thread adds up its requests, the block scans the
+// sums, and the thread whose requests hold the part's begin finds the request. `sums`: two words to a warp, free by now.
+template <int kThreads>
+__device__ __forceinline__ void find_part(const Kv8AttnArgs &a, int item_rows, bool fits, Misc *misc, long long *sums)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    long long cost = 0;
+    int count = 0; // (fewer than three to a CTA)
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < a.B) {
+            const Units u = units_of(a, item_rows, request(a, b));
+            cost += u.all();
+            count += u.count;
+        }
+    }
+    long long to = cost; // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, to, d);
+        to += lane >= d ? x : 0;
+    }
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 31) {
+        sums[2 * warp] = to;
+        sums[2 * warp + 1] = count;
+    }
+    if (tid == 0)
+        misc->at = misc->hi = 0;
+    __syncthreads();
+    long long total = 0, before = to - cost, units = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? sums[2 * w] : 0;
+        total += sums[2 * w];
+        units += sums[2 * w + 1];
+    }
+    // (at least a CTA to a unit: eight units of one tile 16 us, in five parts 20)
+    const int parts = (int)min((long long)gridDim.x, max(max(1ll, units), (total + kMinPart - 1) / kMinPart));
+    if (fits && (int)blockIdx.x < parts) {
+        const long long lo = total * blockIdx.x / parts, hi = total * (blockIdx.x + 1) / parts;
+        if (lo < hi && lo >= before && lo < before + cost) {
+            int b = tid * per;
+            Request rq = request(a, b);
+            Units u = units_of(a, item_rows, rq);
+            while (lo >= before + u.all()) {
+                before += u.all();
+                rq = request(a, ++b);
+                u = units_of(a, item_rows, rq);
+            }
+            misc->at = lo;
+            misc->hi = hi;
+            misc->base = before;
+            misc->q0 = rq.q0;
+            misc->qlen = rq.qlen;
+            misc->len = rq.len;
+            misc->tiles = u.tiles;
+            misc->count = u.count;
+            misc->item = b;
+            misc->total = total;
+            misc->parts = parts;
+        }
+    }
 }
 
 // Plans a call, by one block. Where a unit stands in the order, and which CTA takes
@@ -1016,9 +1104,14 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         atomicOr(&g_kv8_error, 1);
     if (warp == S::kMma)
         alloc(smem_u32(&misc->tmem), NR * S::kTmem);
-    grid_wait(); // the plan
-    if (tid == 0) {
+    const bool planned = !kTree || plan.items != nullptr;
+    if (planned)
+        grid_wait(); // the plan
+    if (tid == 0)
         plan.dir[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (!planned)
+        find_part<S::kThreads>(a, S::kItemRows, fits, misc, reinterpret_cast<long long *>(smem + S::kQ));
+    else if (tid == 0) {
         const long long total = plan.cost[plan.n_items] * a.H_kv;
         const int parts = (int)min((long long)gridDim.x, max(1ll, (total + kMinPart - 1) / kMinPart));
         const bool mine = fits && (int)blockIdx.x < parts;
@@ -1042,20 +1135,46 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
     __syncthreads();
     fence_after_sync();
     bool first = true;
-    const int units = misc->units;
+    const int units = planned ? misc->units : 0;
     while (units > 0 ? misc->next < units : misc->at < misc->hi) {
         Piece piece;
         int s0 = 0, s1 = 1, item;
         int last = -1; // the CTA that ends the unit
         long long end = 0;
-        if (units > 0) {
+        int tiles;
+        long long base = 0;
+        Units un{0, 0, 0};
+        if (!planned) {
+            const long long at = misc->at;
+            base = misc->base;
+            item = misc->item; // (the request)
+            piece.rq = Request{misc->q0, misc->qlen, misc->len, 0};
+            un.tiles = misc->tiles;
+            un.count = misc->count;
+            un.cost = max(1, un.tiles) + kPieceCost;
+            while (at >= base + un.all()) { // requests without tokens have no units
+                base += un.all();
+                piece.rq = request(a, ++item);
+                un = units_of(a, S::kItemRows, piece.rq);
+            }
+            const long long x = at - base;
+            const int u = x < INT_MAX ? (int)x / un.cost : (int)(x / un.cost);
+            const long long unit = base + (long long)u * un.cost;
+            end = min(misc->hi, unit + un.cost);
+            s0 = (int)max(0ll, at - unit - kPieceCost);
+            s1 = (int)max(0ll, end - unit - kPieceCost);
+            last = (int)(((unit + un.cost) * misc->parts - 1) / misc->total);
+            piece.it = Item{item, u / a.H_kv, u % a.H_kv};
+            tiles = un.tiles;
+        } else if (units > 0) {
             const int u = misc->next;
             item = plan.order[u / a.H_kv];
             piece.it.h = u % a.H_kv;
         } else {
             const long long at = misc->at;
             item = misc->item;
-            long long base = plan.cost[item] * a.H_kv, next = plan.cost[item + 1] * a.H_kv;
+            base = plan.cost[item] * a.H_kv;
+            long long next = plan.cost[item + 1] * a.H_kv;
             while (at >= next) {
                 base = next;
                 next = plan.cost[++item + 1] * a.H_kv;
@@ -1068,12 +1187,14 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
             s1 = (int)max(0ll, end - unit - kPieceCost);
             last = (int)(((unit + cost) * misc->parts - 1) / misc->total);
         }
-        const int4 *in = reinterpret_cast<const int4 *>(plan.items + item);
-        const int4 i0 = in[0], i1 = in[1];
-        const int tiles = i0.z;
-        piece.it.b = i0.x;
-        piece.it.chunk = i0.y;
-        piece.rq = Request{i1.x, i1.y, i1.z, 0};
+        if (planned) {
+            const int4 *in = reinterpret_cast<const int4 *>(plan.items + item);
+            const int4 i0 = in[0], i1 = in[1];
+            tiles = i0.z;
+            piece.it.b = i0.x;
+            piece.it.chunk = i0.y;
+            piece.rq = Request{i1.x, i1.y, i1.z, 0};
+        }
         if (units > 0)
             s1 = max(1, tiles);
         piece.t_begin = s0;
@@ -1084,6 +1205,14 @@ __global__ void __launch_bounds__((Shape<D, NR>::kThreads), NR == 1 ? 2 : 1) kv8
         if (tid == 0) {
             misc->at = end;
             misc->item = item;
+            if (!planned) {
+                misc->base = base;
+                misc->q0 = piece.rq.q0;
+                misc->qlen = piece.rq.qlen;
+                misc->len = piece.rq.len;
+                misc->tiles = un.tiles;
+                misc->count = un.count;
+            }
             if (s0 == 0 && s0 < s1 && !piece.whole) // (the thread that wrote it above)
                 plan.dir[blockIdx.x] = make_int4(last, piece.it.b, piece.it.chunk, piece.it.h);
         }
@@ -1215,7 +1344,7 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     using S = Shape<D, NR>;
     const Sizes z = sizes_of(a.B, a.T, a.G, D, NR, sm_count);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const Plan plan{reinterpret_cast<int *>(ws),
+    Plan plan{reinterpret_cast<int *>(ws),
                     reinterpret_cast<long long *>(ws + z.cost_at),
                     reinterpret_cast<PlannedItem *>(ws + z.items_at),
                     reinterpret_cast<int *>(ws + z.order_at),
@@ -1231,10 +1360,17 @@ cudaError_t launch(const Kv8AttnArgs &a, void *workspace, int sm_count, cudaStre
     CUtensorMap maps[2];
     if (!kv8_tensor_maps(a, D, kTile, maps))
         return cudaErrorInvalidValue;
-    kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, grid);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
-    e = launch_behind(kv8_tile_kernel<D, NR, kTree>, dim3((unsigned)grid), S::kThreads, S::kSmem, stream, maps[0], maps[1], a, plan);
+    // (units that are taken whole are at least three to a CTA)
+    if (kTree && z.items * a.H_kv < 3ll * grid) {
+        plan.items = nullptr;
+        kv8_tile_kernel<D, NR, kTree><<<grid, S::kThreads, S::kSmem, stream>>>(maps[0], maps[1], a, plan);
+        e = cudaGetLastError();
+    } else {
+        kv8_tile_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, grid);
+        if ((e = cudaGetLastError()) != cudaSuccess)
+            return e;
+        e = launch_behind(kv8_tile_kernel<D, NR, kTree>, dim3((unsigned)grid), S::kThreads, S::kSmem, stream, maps[0], maps[1], a, plan);
+    }
     if (e != cudaSuccess)
         return e;
     constexpr int kRowsOfBlock = kJoinWarps * 32 / (D / 4) * kJoinRows;

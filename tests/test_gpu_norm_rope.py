@@ -151,3 +151,15 @@ def test_refusals_graph_and_stream():
     _close(got[0], q, wq, 0.0, 1e-6, pos, cs, 0, True)
     empty = binding.smla_qk_norm_rope(q[:0], k[:0], wq, wk, pos[:0], cs)
     assert empty[0].shape == (0, 8, 128)
+
+
+def test_rows_past_32_bits():
+    """Rows whose offsets pass 2^31 elements."""
+    H, D, st = 3, 128, (1 << 30) + 128
+    room = torch.empty(2 * st + H * D, dtype=torch.bfloat16, device=DEV)
+    q = room.as_strided((3, H, D), (st, D, 1))
+    (small, _), (wq, _), pos, cs = _problem(3, H, 1, D, 64, "bf16", 13)
+    q.copy_(small)
+    want = binding.smla_qk_norm_rope(small, None, wq, None, pos, cs)[0]
+    binding.smla_qk_norm_rope(q, None, wq, None, pos, cs, q_out=q)
+    assert torch.equal(q, want)

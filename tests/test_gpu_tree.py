@@ -213,6 +213,27 @@ def test_split_over_many_blocks_streams_and_replay():
     _check(p, mask2, got)
 
 
+@pytest.mark.parametrize("bound", [20, 100])
+def test_many_requests(bound):
+    """So many units that they are planned and taken whole, by one and by two row tiles to a CTA."""
+    r = np.random.RandomState(bound)
+    ql = [int(x) for x in r.randint(0, 4, 130)]
+    lens = [n + int(x) for n, x in zip(ql, r.randint(0, 60, 130))]
+    p = _problem(16, 8, 64, 16, lens, ql, seed=bound)
+    mask, pos = _trees(p, ql, 7)
+    _check(p, mask, _run(p, mask, max_query_len=bound))
+
+
+@pytest.mark.parametrize("H,hk,D", [(8, 2, 128), (4, 1, 64)])
+def test_requests_without_tokens_among_cut_units(H, hk, D):
+    """Units that several CTAs share, with requests between them that have no tokens, or no context."""
+    ql = [0, 20, 0, 0, 7, 33, 0, 1, 40, 0]
+    lens = [50, 3000, 0, 700, 1500, 33, 9, 2000, 900, 5]
+    p = _problem(H, hk, D, 64, lens, ql, seed=D)
+    mask, pos = _trees(p, ql, 8)
+    _check(p, mask, _run(p, mask))
+
+
 def test_refusals():
     p = _problem(4, 1, 64, 16, [20], [4], seed=1)
     mask, pos = _trees(p, [4], 1)
