@@ -6,14 +6,14 @@
 // chain (norm, store, rotation) rounds twice and moves every element twice.
 // A row is a group of up to 32 lanes, each with two 16-byte chunks of it (with halves,
 // those that a rotation pairs): it is read once, its sum goes through shuffles, and it
-// may be written where it was. Bound: the bytes in and out. Measured on the device: 8192
-// tokens, 32 + 8 heads of 128 columns in bf16 (168 MB) in 29.0 us, 5.8 TB/s (the
-// device's own copy of as many bytes: 31), in 40.5 with binary32 weights of their own for
-// each head, which are read again for each row (from L1, twice the row's own bytes); 64
-// tokens 2.6 us. What counted: arithmetic on pairs of elements and weights by 16 bytes (60 us
-// by single ones), more warps (two heads at a time in registers 45, one and the next
-// 36), three heads on their way in shared memory (29; with weights for each head 44,
-// since the L1 cache gets smaller), eight heads to a group (four 32, sixteen 33).
+// may be written where it was. A group takes up to eight rows and keeps what they share:
+// a token's angles, or a head's weights where each head has its own. Bound: the bytes in
+// and out. Measured on the device: 8192 tokens, 32 + 8 heads of 128 columns in bf16 (168
+// MB) in 29.0 us, 5.8 TB/s (the device's own copy of as many bytes: 31), in 32.7 with
+// binary32 weights for each head (40.5 with the weights read for each row); 64 tokens 2.7
+// us. What counted: arithmetic on pairs of elements and weights by 16 bytes (60 us by single
+// ones), more warps (two rows at a time in registers 45, one and the next 36), three rows
+// on their way in shared memory (29), eight rows to a group (four 32, sixteen 31).
 #include "smla_device.cuh"
 #include "smla_rope.cuh"
 #include "smla_step.h"
@@ -30,7 +30,7 @@ namespace {
 
 using namespace rope;
 
-constexpr int kMostPer = 8; // heads that a group takes
+constexpr int kMostPer = 8; // rows that a group takes
 constexpr int kDepth = 4;   // and that are on their way at a time, with the one in hand (a power of two)
 constexpr int kThreads = 128;
 
@@ -66,13 +66,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -202,106 +195,101 @@ __device__ __forceinline__ void copy16(void *dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// A group of blockDim.x lanes takes `per` heads of a token's queries or keys one after another, the next one on its way
-// meanwhile.
+// A group of blockDim.x lanes takes `per` rows one after another, the next ones on their way meanwhile: heads of one
+// token's queries or keys, whose angles it keeps, or (kHeads: weights of their own for each head) one head of as many
+// tokens, whose weights it keeps; the groups of a block are then heads of the same tokens, which find the angles in L1.
 template <typename E, typename Wt, bool kNeox, bool kHeads>
 __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeArgs a, int per, int q_groups, int groups)
 {
     constexpr int kVec = 16 / sizeof(E), kPairs = kVec / 2;
     using C = Chunk<E>;
     const int64_t item = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t t = item / groups;
-    int y = (int)(item - t * groups);
+    const int64_t t = item / groups * (kHeads ? per : 1); // the (first) token
+    int y = (int)(item % groups);
     const bool live = t < a.T;
-    const int64_t pos = live ? a.positions[t] : 0;
+    int64_t pos = live ? a.positions[t] : 0;
     const bool side = y >= q_groups, reports = threadIdx.x == 0 && y == 0;
     y -= side ? q_groups : 0;
     const Place<kVec, kNeox> at(a, threadIdx.x);
-    const int h0 = y * per, count = live ? min(per, (side ? a.H_k : a.H) - h0) : 0;
-    const int64_t sh = side ? a.k_sh : a.q_sh, oh = side ? a.ko_sh : a.qo_sh, wh = side ? a.kw_sh : a.qw_sh;
-    const E *src = static_cast<const E *>(side ? a.k : a.q) + t * (side ? a.k_st : a.q_st) + h0 * sh;
-    E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * (side ? a.ko_st : a.qo_st) + h0 * oh;
-    const Wt *w = static_cast<const Wt *>(side ? a.k_weight : a.q_weight);
-    const bool whole = ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(wh * sizeof(Wt))) & 15) == 0;
-    // The next heads' chunks come to the thread's own places in shared memory, which hold no registers meanwhile; with
-    // weights for each head, which want the L1 cache, the next one's to registers.
-    __shared__ uint4 s_ring[kHeads ? 1 : kDepth][2][kHeads ? 1 : kThreads];
+    const int h0 = kHeads ? y : y * per;
+    const int count = !live ? 0 : (int)(kHeads ? min((int64_t)per, a.T - t) : (int64_t)min(per, (side ? a.H_k : a.H) - h0));
+    const int64_t sh = side ? a.k_sh : a.q_sh, oh = side ? a.ko_sh : a.qo_sh;
+    const int64_t st = side ? a.k_st : a.q_st, ot = side ? a.ko_st : a.qo_st;
+    const int64_t src_step = kHeads ? st : sh, dst_step = kHeads ? ot : oh; // from row to row
+    const E *src = static_cast<const E *>(side ? a.k : a.q) + t * st + h0 * sh;
+    E *dst = static_cast<E *>(side ? a.k_out : a.q_out) + t * ot + h0 * oh;
+    // the next rows' chunks come to the thread's own places in shared memory, which hold no registers meanwhile
+    __shared__ uint4 s_ring[kDepth][2][kThreads];
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
     const uint4 none = make_uint4(0, 0, 0, 0);
-    uint4 xa = none, xb = none;
     const auto ask = [&](int i) {
-        const E *row = src + i * sh;
-        const bool in_a = i < count && at.ca >= 0, in_b = i < count && at.cb >= 0;
-        if (kHeads) {
-            xa = in_a ? __ldcs(reinterpret_cast<const uint4 *>(row + at.ca)) : none;
-            xb = in_b ? __ldcs(reinterpret_cast<const uint4 *>(row + at.cb)) : none;
-        } else {
-            if (in_a)
+        if (i < count) {
+            const E *row = src + i * src_step;
+            if (at.ca >= 0)
                 copy16(&s_ring[i % kDepth][0][tid], row + at.ca);
-            if (in_b)
+            if (at.cb >= 0)
                 copy16(&s_ring[i % kDepth][1][tid], row + at.cb);
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
         }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-    ask(0);
-    if (!kHeads)
 #pragma unroll
-        for (int i = 1; i < kDepth - 1; ++i)
-            ask(i);
+    for (int i = 0; i < kDepth - 1; ++i)
+        ask(i);
     float wa[kVec], wb[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e)
         wa[e] = wb[e] = 1.f;
-    const auto weights = [&](int h) {
-        if (w && at.ca >= 0)
-            load_weights<Wt, kVec>(w + h * wh + at.ca, whole, kHeads ? 0.f : a.weight_offset, wa);
-        if (w && at.cb >= 0)
-            load_weights<Wt, kVec>(w + h * wh + at.cb, whole, kHeads ? 0.f : a.weight_offset, wb);
+    if (const Wt *w = static_cast<const Wt *>(side ? a.k_weight : a.q_weight)) {
+        const int64_t wh = side ? a.kw_sh : a.qw_sh;
+        const bool whole = ((reinterpret_cast<uintptr_t>(w) | (uintptr_t)(wh * sizeof(Wt))) & 15) == 0;
+        w += kHeads ? h0 * wh : 0;
+        if (at.ca >= 0)
+            load_weights<Wt, kVec>(w + at.ca, whole, a.weight_offset, wa);
+        if (at.cb >= 0)
+            load_weights<Wt, kVec>(w + at.cb, whole, a.weight_offset, wb);
+    }
+    bool ok = false; // the token's position is one
+    float c[kVec], s[kVec]; // halves: of the pairs; interleaved: of chunk A's pairs, then of B's
+    const auto angles = [&](bool there) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            c[e] = 1.f, s[e] = 0.f;
+        ok = there && pos >= 0 && pos < a.max_position;
+        if (there && !ok && reports)
+            atomicOr(&g_norm_rope_error, 4);
+        if (ok) {
+            const float *row = a.cos_sin + pos * a.rot_dim;
+            const int n = a.rot_dim / 2;
+            if (kNeox) {
+                if (at.ta) {
+                    load_angles<kVec>(row + at.pair_a, c);
+                    load_angles<kVec>(row + n + at.pair_a, s);
+                }
+            } else {
+                if (at.ta) {
+                    load_angles<kPairs>(row + at.pair_a, *reinterpret_cast<float(*)[kPairs]>(c));
+                    load_angles<kPairs>(row + n + at.pair_a, *reinterpret_cast<float(*)[kPairs]>(s));
+                }
+                if (at.tb) {
+                    load_angles<kPairs>(row + at.pair_b, *reinterpret_cast<float(*)[kPairs]>(c + kPairs));
+                    load_angles<kPairs>(row + n + at.pair_b, *reinterpret_cast<float(*)[kPairs]>(s + kPairs));
+                }
+            }
+        }
     };
     if (!kHeads)
-        weights(0);
-    const uint64_t offset = w ? pair(a.weight_offset, a.weight_offset) : 0; // (of weights for each head)
-    const bool ok = live && pos >= 0 && pos < a.max_position;
-    if (live && !ok && reports)
-        atomicOr(&g_norm_rope_error, 4);
-    float c[kVec], s[kVec]; // halves: of the pairs; interleaved: of chunk A's pairs, then of B's
-#pragma unroll
-    for (int e = 0; e < kVec; ++e)
-        c[e] = 1.f, s[e] = 0.f;
-    if (ok) {
-        const float *row = a.cos_sin + pos * a.rot_dim;
-        const int n = a.rot_dim / 2;
-        if (kNeox) {
-            if (at.ta) {
-                load_angles<kVec>(row + at.pair_a, c);
-                load_angles<kVec>(row + n + at.pair_a, s);
-            }
-        } else {
-            if (at.ta) {
-                load_angles<kPairs>(row + at.pair_a, *reinterpret_cast<float(*)[kPairs]>(c));
-                load_angles<kPairs>(row + n + at.pair_a, *reinterpret_cast<float(*)[kPairs]>(s));
-            }
-            if (at.tb) {
-                load_angles<kPairs>(row + at.pair_b, *reinterpret_cast<float(*)[kPairs]>(c + kPairs));
-                load_angles<kPairs>(row + n + at.pair_b, *reinterpret_cast<float(*)[kPairs]>(s + kPairs));
-            }
-        }
-    }
+        angles(live);
 #pragma unroll 1
     for (int i = 0; i < per; ++i) { // (the same rounds for all groups of a warp)
-        uint64_t va[kPairs], vb[kPairs], sums = 0;
-        if (kHeads) {
-            if (i < count) // asked for before the head is waited for
-                weights(h0 + i);
-            C::open(xa, va);
-            C::open(xb, vb);
-            ask(i + 1);
-        } else {
-            ask(i + kDepth - 1);
-            asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
-            C::open(at.ca >= 0 && i < count ? s_ring[i % kDepth][0][tid] : none, va);
-            C::open(at.cb >= 0 && i < count ? s_ring[i % kDepth][1][tid] : none, vb);
+        if (kHeads) { // asked for before the row is waited for
+            angles(i < count);
+            pos = i + 1 < count ? a.positions[t + i + 1] : 0;
         }
+        ask(i + kDepth - 1);
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
+        uint64_t va[kPairs], vb[kPairs], sums = 0;
+        C::open(at.ca >= 0 && i < count ? s_ring[i % kDepth][0][tid] : none, va);
+        C::open(at.cb >= 0 && i < count ? s_ring[i % kDepth][1][tid] : none, vb);
 #pragma unroll
         for (int e = 0; e < kPairs; ++e)
             sums = fma2(vb[e], vb[e], fma2(va[e], va[e], sums));
@@ -331,13 +319,8 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeAr
         const uint64_t rr = pair(r, r);
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) {
-            uint64_t fa = pair(wa[2 * e], wa[2 * e + 1]), fb = pair(wb[2 * e], wb[2 * e + 1]);
-            if (kHeads) {
-                fa = add2(fa, offset);
-                fb = add2(fb, offset);
-            }
-            va[e] = mul2(mul2(va[e], rr), fa);
-            vb[e] = mul2(mul2(vb[e], rr), fb);
+            va[e] = mul2(mul2(va[e], rr), pair(wa[2 * e], wa[2 * e + 1]));
+            vb[e] = mul2(mul2(vb[e], rr), pair(wb[2 * e], wb[2 * e + 1]));
         }
         if (kNeox) {
             if (at.ta) {
@@ -362,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeAr
                 for (int e = 0; e < kPairs; ++e)
                     vb[e] = turn(vb[e], c[kPairs + e], s[kPairs + e]);
         }
-        E *row = dst + i * oh;
+        E *row = dst + i * dst_step;
         if (at.ca >= 0)
             __stcs(reinterpret_cast<uint4 *>(row + at.ca), C::close(va));
         if (at.cb >= 0)
@@ -448,17 +431,18 @@ cudaError_t launch(const NormRopeArgs &a, int sm_count, cudaStream_t stream)
     int lanes = 1;
     while (lanes < units)
         lanes *= 2;
-    // Few tokens: a head to a group, so that all SMs have some. Many: up to eight, so that positions and angles are read
-    // once for them.
+    // Few tokens: a row to a group, so that all SMs have some. Many: up to eight, so that positions and angles (or
+    // weights) are read once for them.
     const bool many = (int64_t)a.T * heads * lanes > (int64_t)sm_count * 2048;
-    const int per = many ? std::min(kMostPer, std::max(a.H, a.H_k)) : 1;
-    const int q_groups = (a.H + per - 1) / per, token_groups = q_groups + (a.H_k + per - 1) / per;
+    const bool each = a.qw_sh != 0 || a.kw_sh != 0; // weights of their own for each head
+    const int per = !many ? 1 : std::min(kMostPer, each ? a.T : std::max(a.H, a.H_k));
+    const int q_groups = each ? a.H : (a.H + per - 1) / per;
+    const int token_groups = q_groups + (each ? a.H_k : (a.H_k + per - 1) / per); // of one token, or of `per` tokens
     const int groups = kThreads / lanes;
-    const int64_t blocks = ((int64_t)a.T * token_groups + groups - 1) / groups;
+    const int64_t blocks = ((each ? ((int64_t)a.T + per - 1) / per : (int64_t)a.T) * token_groups + groups - 1) / groups;
     if (blocks > INT_MAX)
         return cudaErrorInvalidValue;
     const dim3 block(lanes, groups);
-    const bool each = a.qw_sh != 0 || a.kw_sh != 0; // weights of their own for each head
     const auto kernel = a.neox ? (each ? norm_rope_kernel<E, Wt, true, true> : norm_rope_kernel<E, Wt, true, false>)
                                : (each ? norm_rope_kernel<E, Wt, false, true> : norm_rope_kernel<E, Wt, false, false>);
     kernel<<<(unsigned)blocks, block, 0, stream>>>(a, per, q_groups, token_groups);
