@@ -681,7 +681,8 @@ SMLA_API smla_status smla_kv8_tree_attn_fwd(const smla_kv8_tree_attn_params *par
  * token i of request b is its new token kept[b, i]: the row of position ctx + kept[b, i]
  * goes to position ctx + i, both found through block_table. The numbers ascend strictly
  * and lie below query_lens[b]; the first that does not ends the list and sets bit 16 of
- * smla_device_error, as does a kept_lens[b] above the most there can be (which is cut).
+ * smla_device_error, as does a kept_lens[b] above the most there can be (which is cut; one
+ * below 0 keeps none).
  * Rows whose old or new block is outside the pool do not move. The blocks written to
  * must be this request's alone (see smla_fork_block_tables), and no block may stand
  * twice in its row.

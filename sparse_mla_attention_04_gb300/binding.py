@@ -901,7 +901,20 @@ def smla_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
     return q_out, k_out
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
+    try:  # the usual call, in one look
+        shape, dev, scales = k_cache.shape, k_cache.device, k_scale.shape
+        if (k_cache.dtype in _CODES and v_cache.dtype in _CODES and k_scale.dtype is torch.float32 is v_scale.dtype
+                and len(shape) == 4 and v_cache.shape == shape and scales == shape[:2] and v_scale.shape == scales
+                and k_cache.is_cuda and v_cache.device == dev and k_scale.device == dev and v_scale.device == dev
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous()):
+            return shape
+    except AttributeError:
+        pass  # (said below)
     for name, x in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(x, torch.Tensor) or x.dtype not in (torch.uint8, torch.float8_e4m3fn):
             raise TypeError("%s must be E4M3 codes (uint8 / float8_e4m3fn)" % name)

@@ -47,7 +47,8 @@ def _problem(T, H, Hk, D, rot, dtype, seed, wide=False, per_head=False, P=200):
     (40, 3, 1, 72, 16, 24), (11, 2, 1, 65, 22, 7), (6, 1, 1, 2, 2, 0), (4, 2, 1, 1000, 100, 300), (3, 130, 17, 64, 32, 16)])
 @pytest.mark.parametrize("neox", [True, False])
 @pytest.mark.parametrize("dtype,wide,per_head,plus", [("bf16", False, False, 0.0), ("bf16", True, True, 1.0), ("f16", False, True, 0.0),
-                                                      ("f32", True, False, -0.5)])
+                                                      ("f16", True, False, 1.0), ("f32", True, False, -0.5),
+                                                      ("f32", True, True, 0.0)])
 def test_values(T, H, Hk, D, rot, off, neox, dtype, wide, per_head, plus):
     (q, k), (wq, wk), pos, cs = _problem(T, H, Hk, D, rot, dtype, D + T, wide, per_head)
     qo, ko = binding.smla_qk_norm_rope(q, k, wq, wk, pos, cs, eps=1e-5, weight_offset=plus, rot_offset=off, is_neox=neox)
@@ -116,6 +117,26 @@ def test_positions_out_of_range(D):
         assert bool((o[[1, 4]] == 7.0).all())
         keep = [0, 2, 3, 5]
         _close(o[keep], x[keep], w, 0.0, 1e-6, pos[keep], cs, 0, True)
+
+
+@pytest.mark.parametrize("T", [3, 2000])
+def test_weights_for_each_head_beside_one_row(T):
+    """Queries with weights for each head, keys with one row for all, or none; bad positions among eight tokens of a head."""
+    binding.smla_device_error(reset=True)
+    (q, k), (wq, _), pos, cs = _problem(T, 9, 4, 128, 64, "bf16", 21, True, True)
+    wk = torch.rand(128, device=DEV) + 0.5
+    for w in (wk, None):
+        qo, ko = binding.smla_qk_norm_rope(q, k, wq, w, pos, cs, weight_offset=0.5)
+        _close(qo, q, wq, 0.5, 1e-6, pos, cs, 0, True)
+        _close(ko, k, w, 0.5, 1e-6, pos, cs, 0, True)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[1::7] = True
+    at = torch.where(bad, 1 << 40, pos)
+    q2, k2 = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    binding.smla_qk_norm_rope(q, k, wq, None, at, cs, weight_offset=0.5, q_out=q2, k_out=k2)
+    assert binding.smla_device_error(reset=True) == 4
+    for x, y in ((q2, qo), (k2, ko)):
+        assert torch.equal(x[~bad], y[~bad]) and bool((x[bad] == 7.0).all())
 
 
 def test_refusals_graph_and_stream():

@@ -111,7 +111,8 @@ def _check(p, mask, got, pos=None, window=0, sinks=None):
     (8, 8, 64, 32, [129, 128, 127], [100, 128, 1]),
     (12, 4, 64, 128, [500, 90, 260], [70, 90, 33]),                # two row tiles
     (16, 1, 128, 64, [310], [130]),                                # masks of three words
-    (5, 1, 64, 16, [37, 0, 600], [37, 0, 20])])                    # no context; no tokens
+    (5, 1, 64, 16, [37, 0, 600], [37, 0, 20]),                     # no context; no tokens
+    (2, 2, 64, 16, [3, 40], [8, 3]), (4, 1, 128, 64, [5, 40], [20, 3])])   # more new tokens than there are positions
 @pytest.mark.parametrize("kind", ["tree", "any"])
 def test_attention(H, hk, D, bs, lens, ql, kind):
     p = _problem(H, hk, D, bs, lens, ql, seed=H * D + len(lens), pad=3)
@@ -232,6 +233,20 @@ def test_requests_without_tokens_among_cut_units(H, hk, D):
     p = _problem(H, hk, D, 64, lens, ql, seed=D)
     mask, pos = _trees(p, ql, 8)
     _check(p, mask, _run(p, mask))
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with outputs and a workspace of its own: the bits of one call at a time."""
+    problems = [_problem(8, 2, 128, 64, [3000, 500], ql, seed=len(ql) + ql[0]) for ql in ([20, 9], [2, 1])]
+    masks = [_trees(p, [int(x) for x in p["start"].diff()], 3)[0] for p in problems]
+    want = [_run(p, m) for p, m in zip(problems, masks)]
+    streams = [torch.cuda.Stream() for _ in problems]
+    torch.cuda.synchronize()
+    got = [[_run(p, m, stream=s) for p, m, s in zip(problems, masks, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for x, y in zip(pair, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
 
 
 def test_refusals():
