@@ -1196,14 +1196,16 @@ class TokenPools:
     __slots__ = ("tensors", "device", "heads", "block_size", "row_bytes", "num_blocks", "count", "pools", "scales")
 
     def __init__(self, caches: Sequence, block_size: Optional[int] = None):
+        if isinstance(caches, torch.Tensor):
+            raise TypeError("caches must be a sequence of caches, not one tensor")
         caches = list(caches)
         if not caches:
             raise ValueError("no caches")
         if isinstance(caches[0], torch.Tensor):
             first = caches[0]
             _need(first, "caches[0]", first.dtype, 2)
-            if block_size is None:
-                raise ValueError("latent pools need block_size")
+            if block_size is None or block_size < 1:
+                raise ValueError("latent pools need block_size, got %s" % (block_size,))
             slots, D = first.shape
             if slots % block_size != 0:
                 raise ValueError("%d slots are no whole blocks of %d" % (slots, block_size))
@@ -1304,7 +1306,7 @@ def smla_fork_block_tables(source_rows: torch.Tensor, seq_lens: torch.Tensor, bl
     [B_old, width] (rows may be strided) stay; free_ring and ring_state as for
     smla_build_block_tables (ring_state updated in place unless ring_state_out is
     given). Fresh outputs' entries past a row's blocks are -1. Nothing changes when
-    blocks lack: counts[3] says how many."""
+    blocks lack (fresh rows and blocks_held are -1 throughout): counts[3] says how many."""
     _need(source_rows, "source_rows", torch.int32, 1)
     dev = source_rows.device
     B = source_rows.shape[0]
@@ -1324,10 +1326,15 @@ def smla_fork_block_tables(source_rows: torch.Tensor, seq_lens: torch.Tensor, bl
             raise ValueError("block_table_out must be [%d, %d], got %s" % (B, width, tuple(block_table_out.shape)))
     L = _lib or lib()
     with _on(dev, stream) as handle:
-        if block_table_out is None:
-            block_table_out = torch.full((B, width), -1, dtype=torch.int32, device=dev)
+        # fresh rows and what they hold are -1 (none) where the call leaves them as they are, by one fill
+        fresh_table, fresh_held = block_table_out is None, blocks_held_out is None
+        if fresh_table or fresh_held:
+            cut = B * width if fresh_table else 0
+            room = torch.full((cut + (B if fresh_held else 0),), -1, dtype=torch.int32, device=dev)
+            if fresh_table:
+                block_table_out = room[:cut].view(B, width)
         state = ring_state if ring_state_out is None else _out(ring_state_out, "ring_state_out", (2,), torch.int32, dev)
-        held = _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
+        held = room[cut:] if fresh_held else _out(blocks_held_out, "blocks_held_out", (B,), torch.int32, dev)
         copy_from = _out(copy_from, "copy_from", (B,), torch.int32, dev)
         copy_to = _out(copy_to, "copy_to", (B,), torch.int32, dev)
         counts = _out(counts, "counts", (4,), torch.int32, dev)
@@ -1352,6 +1359,8 @@ class BlockPools:
     __slots__ = ("tensors", "device", "num_blocks", "count", "pools", "block_bytes")
 
     def __init__(self, pools: Sequence[torch.Tensor]):
+        if isinstance(pools, torch.Tensor):
+            raise TypeError("pools must be a sequence of tensors, not one (its blocks would be taken for pools)")
         self.tensors = list(pools)
         if not self.tensors:
             raise ValueError("no pools")

@@ -197,3 +197,11 @@ def test_binding_refuses_wrong_tensors():
         b.smla_copy_blocks([], i32, i32)
     with pytest.raises(ValueError):
         b.smla_copy_blocks([torch.zeros((4, 4))], i32, i32)
+
+
+def test_one_tensor_is_not_a_sequence_of_pools():
+    pool, i32 = torch.zeros((4, 4, 8)), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: b.BlockPools(pool), lambda: b.smla_copy_blocks(pool, i32, i32), lambda: b.TokenPools(pool[0], 2),
+                 lambda: b.smla_keep_tokens(pool[0], i32, i32, i32, i32, i32, block_size=2)):
+        with pytest.raises(TypeError, match="sequence"):
+            call()

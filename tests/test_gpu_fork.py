@@ -155,6 +155,31 @@ def test_strided_tables_streams_and_replay(W):
     assert np.array_equal(got.block_table.cpu().numpy(), fresh)
 
 
+@pytest.mark.parametrize("table_out", [False, True])
+@pytest.mark.parametrize("held_out", [False, True])
+def test_fresh_outputs_where_blocks_lack(table_out, held_out):
+    """Two rows from one whose last block is partly full, and an empty ring: nothing is written, and what is fresh says so."""
+    table, held = _up([[4, 2, -1]]), _up([2])
+    ring, state = _up([0] * 6), _up([3, 0])
+    given = {}
+    if table_out:
+        given["block_table_out"] = _up(np.full((2, 3), -7))
+    if held_out:
+        given["blocks_held_out"] = _up([-7, -7])
+    torch.empty(4096, dtype=torch.uint8, device=DEV).fill_(0x5A)      # (the allocator hands it out again)
+    got = binding.smla_fork_block_tables(_up([0, 0]), _up([20, 20]), held, table, ring, state, block_size=16, num_blocks=6, **given)
+    assert got.counts.tolist()[1:] == [0, 0, 1]
+    assert got.block_table.tolist() == [[-7 if table_out else -1] * 3] * 2
+    assert got.blocks_held.tolist() == [-7 if held_out else -1] * 2
+    assert got.copy_from.tolist() == got.copy_to.tolist() == [-1, -1] and state.tolist() == [3, 0]
+    ring.fill_(5)
+    state[1] = 1
+    got = binding.smla_fork_block_tables(_up([0, 0]), _up([20, 20]), held, table, ring, state, block_size=16, num_blocks=6, **given)
+    rest = -7 if table_out else -1
+    assert got.block_table.tolist() == [[4, 2, rest], [4, 5, rest]] and got.blocks_held.tolist() == [2, 2]
+    assert got.copy_from.tolist() == [-1, 2] and got.copy_to.tolist() == [-1, 5]
+
+
 # ------------------------------------------------------------------ copies
 def test_copies():
     r = np.random.RandomState(1)

@@ -162,6 +162,8 @@ def test_strided_tables_many_layers_and_replay():
         binding.TokenPools([got[0], got[1], got[0]])                 # its rows would move twice
     with pytest.raises(ValueError):
         binding.TokenPools([got[0][0].view(-1, 64), got[1][0].view(-1, 64)])                   # latent pools without block_size
+    with pytest.raises(ValueError, match="block_size"):
+        binding.TokenPools([got[0][0].view(-1, 64)], block_size=0)
 
 
 def test_pools_past_32_bits():
