@@ -447,7 +447,7 @@ def ceiling_configs(row_bytes: int):
     as the first forward kernels did (issue warps 0) and spread evenly over
     more warps (a warp issues its lanes' copies one after another), or by
     16-byte cp.async copies from eight warps (copy mode 1); and CTA pairs that
-    share each tile (1: cluster multicast, 2: bulk copy into the peer)."""
+    share each tile (1: stores into the peer's shared memory, 2: a bulk copy there)."""
     boxes = (row_bytes + 127) // 128
     tile = 64 * 128 * boxes
     copies = 16 * boxes

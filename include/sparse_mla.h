@@ -925,8 +925,8 @@ SMLA_API smla_status smla_fused_qk_rope_cache(const void *ql_nope, int64_t ql_st
  * pair_mode (with ctas_per_sm = 1): 0 = single CTAs; 1 or 2 = CTAs in pairs,
  * each pair a thread-block cluster of two that takes the tiles one CTA would:
  * each CTA gathers half of every tile's rows (so every row is read once) and
- * delivers it to both CTAs, by cluster multicast of its gathers (1) or by a
- * bulk copy of its landed half into the peer's ring (2); a stage is refilled
+ * delivers it to both CTAs: its landed half goes into the peer's ring by a
+ * warp's 16-byte stores (1) or by a bulk copy (2); a stage is refilled
  * once both consumers released it (the patterns of a pair that shares its key
  * rows). Only the first CTA of a pair writes its checksum (the second writes
  * 0). 3 = single CTAs launched in clusters of two (a control for 1 and 2).

@@ -425,7 +425,7 @@ def smla_gather_probe(pool: torch.Tensor, indices: torch.Tensor, *, ctas_per_sm:
     gathered into shared memory (copy_mode 0: TMA gather4, 1: 16-byte cp.async)
     and folded into per-CTA checksums (uint32 device tensor
     [sm_count * ctas_per_sm], returned); pair_mode 1 / 2: CTA pairs sharing
-    each tile by cluster multicast / by a bulk copy into the peer;
+    each tile by stores / by a bulk copy into the peer's shared memory;
     issue_warps > 0: a tile's copies spread evenly over that many producer
     warps."""
     if pool.dim() != 2 or not pool.is_contiguous() or not pool.is_cuda:

@@ -48,7 +48,7 @@ struct ProbeArgs {
     int stages;
     int hold_ns;
     int pair_mode;      // 0: single CTAs; CTA pairs in clusters, each gathering half of every tile and
-                        // delivering it to both: 1 by TMA multicast, 2 by a bulk copy into the peer;
+                        // delivering it to both: 1 by stores into the peer's shared memory, 2 by a bulk copy there;
                         // 3: single CTAs launched in clusters of two
     int issue_warps;    // 0: copy c issued by producer thread c; k (1..8): the copies spread evenly
                         // over warps 0..k-1, ceil(copies / k) lanes each
@@ -70,16 +70,16 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
     int *abort_s = const_cast<int *>(go_s) + 2;
     auto full = [&](int st) { return bar0 + 8 * st; };                   // this CTA's gathers
     auto empty = [&](int st) { return bar0 + 8 * (kMaxStages + st); };
-    auto xfull = [&](int st) { return bar0 + 8 * (2 * kMaxStages + st); }; // the peer's half (pair_mode 2)
+    auto xfull = [&](int st) { return bar0 + 8 * (2 * kMaxStages + st); }; // the peer's half (pair_mode 1, 2)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // pair_mode 3: independent CTAs, launched in clusters of two (a control)
-    const bool mc = a.pair_mode == 1 || a.pair_mode == 2, xc = a.pair_mode == 2;
+    const bool pair = a.pair_mode == 1 || a.pair_mode == 2, bulk = a.pair_mode == 2;
     const bool async = a.copy_mode == 1;
-    const uint32_t rank = mc ? umma::cluster_rank() : 0u;
+    const uint32_t rank = pair ? umma::cluster_rank() : 0u;
     const int half_bytes = tile_bytes / 2;
-    // tiles are split over CTAs, or over CTA pairs in the multicast mode
-    const int64_t units = mc ? gridDim.x / 2 : gridDim.x, unit = mc ? blockIdx.x / 2 : blockIdx.x;
+    // tiles are split over CTAs, or over CTA pairs that share them
+    const int64_t units = pair ? gridDim.x / 2 : gridDim.x, unit = pair ? blockIdx.x / 2 : blockIdx.x;
     const int64_t ntiles_all = (a.n_indices + kRows - 1) / kRows;
     const int64_t j0 = ntiles_all * unit / units;
     const int64_t j1 = ntiles_all * (unit + 1) / units;
@@ -89,14 +89,14 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
         for (int st = 0; st < a.stages; ++st) {
             // cp.async: every producer thread arrives once its own copies of the tile land
             umma::mbar_init(full(st), async ? kProducerThreads : 1);
-            umma::mbar_init(empty(st), mc ? 2 : 1); // a pair's stage is refilled once both consumers are done
-            umma::mbar_init(xfull(st), 1);
+            umma::mbar_init(empty(st), pair ? 2 : 1); // a pair's stage is refilled once both consumers are done
+            umma::mbar_init(xfull(st), bulk ? 1 : 32);
         }
         umma::mbar_init_fence();
         *abort_s = 0;
     }
     __syncthreads();
-    if (mc) // both CTAs' barriers are initialised before either sends to the other
+    if (pair) // both CTAs' barriers are initialised before either sends to the other
         umma::cluster_barrier();
 
     auto wait_bar = [&](uint32_t mbar, uint32_t parity) {
@@ -109,13 +109,13 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
     };
 
     if (warp < kProducerWarps) {
-        // copy `tid`: key quad qd (rows 4qd..4qd+3 of the tile), box cb; in the
-        // multicast mode each CTA of the pair issues half of the 16 quads
-        const int copies = (mc ? 8 : 16) * a.boxes;
+        // copy `tid`: key quad qd (rows 4qd..4qd+3 of the tile), box cb; of a
+        // pair's tile each CTA issues half of the 16 quads
+        const int copies = (pair ? 8 : 16) * a.boxes;
         const int per_warp = a.issue_warps > 0 ? (copies + a.issue_warps - 1) / a.issue_warps : 32;
         const int cid = a.issue_warps > 0 ? warp * per_warp + lane : tid;
         const bool copier = (a.issue_warps == 0 || (warp < a.issue_warps && lane < per_warp)) && cid < copies;
-        const int qd = (mc ? 8 * (int)rank : 0) + cid / a.boxes, cb = cid % a.boxes;
+        const int qd = (pair ? 8 * (int)rank : 0) + cid / a.boxes, cb = cid % a.boxes;
         auto fetch = [&](int j, int (&r)[4]) {
             if (async) { // lane k < 8 holds row 8 warp + k of the tile
                 const int64_t p = (j0 + j) * kRows + 8 * warp + lane;
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
                 if (j >= a.stages)
                     wait_bar(empty(st), (uint32_t)((j / a.stages - 1) & 1));
                 const int go = !*(volatile int *)abort_s;
-                if (go && !async) // the whole tile, or (pair_mode 2) this CTA's half
-                    umma::mbar_arrive_expect_tx(full(st), (uint32_t)(xc ? half_bytes : tile_bytes));
+                if (go && !async) // the whole tile, or of a pair's this CTA's half
+                    umma::mbar_arrive_expect_tx(full(st), (uint32_t)(pair ? half_bytes : tile_bytes));
                 go_s[j & 1] = go;
             }
             umma::named_bar(1, kProducerThreads);
@@ -165,10 +165,7 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
                                     src + c * 16, x < 0 ? 0u : 16u);
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full(st)) : "memory");
-            } else if (copier && mc && !xc)
-                umma::tma_gather4_multicast(ring + st * tile_bytes + cb * (kRows * 128) + qd * 512, &map, 128 * cb,
-                                            row(r[0]), row(r[1]), row(r[2]), row(r[3]), full(st), (uint16_t)3);
-            else if (copier)
+            } else if (copier)
                 umma::tma_gather4(ring + st * tile_bytes + cb * (kRows * 128) + qd * 512, &map, 128 * cb,
                                   row(r[0]), row(r[1]), row(r[2]), row(r[3]), full(st));
             issued = j + 1;
@@ -187,11 +184,12 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
                     atomicOr(&g_probe_error, 2);
         }
     } else if (warp == kProducerWarps + 1) {
-        // relay (pair_mode 2): once this CTA's half of a tile has landed, copy it
-        // into the same place of the peer's ring (one bulk copy per 128-byte
-        // column block: 8 key quads x 512 B), counted on the peer's xfull; the
-        // peer's stage is free once both consumers released the tile before
-        if (xc && lane == 0) {
+        // relay: once this CTA's half of a tile has landed, copy it into the same
+        // place of the peer's ring (for each 128-byte column block 8 key quads x
+        // 512 B), counted on the peer's xfull: a bulk copy to a column block, or
+        // 16-byte stores of all lanes, each of which then arrives. The peer's
+        // stage is free once both consumers released the tile before
+        if (pair && (lane == 0 || !bulk)) {
             const uint32_t peer = rank ^ 1u;
             for (int j = 0; j < ntiles; ++j) {
                 const int st = j % a.stages;
@@ -199,14 +197,27 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
                     wait_bar(empty(st), (uint32_t)((j / a.stages - 1) & 1));
                 if (*(volatile int *)abort_s)
                     break;
-                umma::mbar_arrive_expect_tx(xfull(st), (uint32_t)half_bytes); // the peer's half, into this CTA
+                if (bulk)
+                    umma::mbar_arrive_expect_tx(xfull(st), (uint32_t)half_bytes); // the peer's half, into this CTA
                 wait_bar(full(st), (uint32_t)((j / a.stages) & 1));
                 if (*(volatile int *)abort_s)
                     break;
                 for (int cb = 0; cb < a.boxes; ++cb) {
                     const uint32_t off = ring + st * tile_bytes + cb * (kRows * 128) + rank * 8 * 512;
-                    umma::bulk_copy_s2peer(off, off, 8 * 512, xfull(st), peer);
+                    if (bulk) {
+                        umma::bulk_copy_s2peer(off, off, 8 * 512, xfull(st), peer);
+                    } else {
+                        uint4 v[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            v[x] = umma::lds128(off + x * 512 + lane * 16);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            umma::sts128_peer(off + x * 512 + lane * 16, v[x], peer);
+                    }
                 }
+                if (!bulk)
+                    umma::mbar_arrive_cluster(xfull(st), peer);
             }
         }
     } else if (lane == 0) {
@@ -216,8 +227,10 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % a.stages;
             wait_bar(full(st), (uint32_t)((j / a.stages) & 1));
-            if (xc)
+            if (pair)
                 wait_bar(xfull(st), (uint32_t)((j / a.stages) & 1));
+            if (pair && !bulk) // the peer's stores, released at the cluster's scope
+                asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
             if (*(volatile int *)abort_s)
                 break;
             const uint32_t base = ring + st * tile_bytes;
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
             if (a.hold_ns > 0)
                 while (umma::globaltimer() - t_land < (uint64_t)a.hold_ns) {
                 }
-            if (mc) {
+            if (pair) {
                 umma::mbar_arrive_cluster(empty(st), rank);
                 umma::mbar_arrive_cluster(empty(st), rank ^ 1u);
             } else {
@@ -237,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) smla_gather_probe_kernel(const Probe
         a.checksum[blockIdx.x] = rank == 0 ? x : 0u; // a pair's two CTAs see the same rows
     }
     __syncthreads();
-    if (mc) // the peer may still send to this CTA's ring and barriers
+    if (pair) // the peer may still send to this CTA's ring and barriers
         umma::cluster_barrier();
 }
 

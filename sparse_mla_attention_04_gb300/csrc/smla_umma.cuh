@@ -69,16 +69,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
                  "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-// Arrive once on the mbarrier at shared-memory offset `mbar` of every CTA of
-// the cluster in `cta_mask` when every tcgen05 op issued so far by this
-// thread is done.
-__device__ __forceinline__ void commit_multicast(uint32_t mbar, uint16_t cta_mask)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(mbar),
-                 "h"(cta_mask)
-                 : "memory");
-}
-
 // Arrive once on `mbar` when every tcgen05 op issued so far by this thread is done.
 __device__ __forceinline__ void commit(uint32_t mbar)
 {
@@ -200,18 +190,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void *tmap, int 
                  : "memory");
 }
 
-// tma_gather4 delivered to the same shared-memory offset (dst) in every CTA
-// of the cluster in `cta_mask`; each destination CTA counts the bytes on its
-// own mbarrier at offset `mbar`.
-__device__ __forceinline__ void tma_gather4_multicast(uint32_t dst, const void *tmap, int x, int r0, int r1, int r2,
-                                                      int r3, uint32_t mbar, uint16_t cta_mask)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster"
-                 " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
-                 "l"(tmap), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(mbar), "h"(cta_mask)
-                 : "memory");
-}
-
 // TMA tile load of the box at (x, y) of a 2-D tensor map into shared memory at
 // dst (in the map's swizzle), bytes counted on mbar; out-of-range parts of the
 // box are filled with zeros.
@@ -250,6 +228,25 @@ __device__ __forceinline__ void bulk_copy_s2peer(uint32_t dst, uint32_t src, uin
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(rbar) : "r"(mbar), "r"(rank));
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(rdst),
                  "r"(src), "r"(bytes), "r"(rbar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Sixteen bytes into the shared memory of cluster CTA `rank`, at offset dst.
+__device__ __forceinline__ void sts128_peer(uint32_t dst, const uint4 &v, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(remote) : "r"(dst), "r"(rank));
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(remote), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
 
