@@ -34,13 +34,16 @@ constexpr int kMostPer = 8; // rows that a group takes
 constexpr int kDepth = 4;   // and that are on their way at a time, with the one in hand (a power of two)
 constexpr int kThreads = 128;
 
-// r of a row from the sum of its squares. Where that passes binary32 the row's
-// elements are to be taken 2^-70 times (`small`), and the sum is one of those: finite
-// for every finite row of up to 2^17 columns. (rsqrtf: 2 units in the last place.)
-constexpr float kSmall = 0x1p-70f;
+// r of a row from the sum of its squares. Where that passes binary32 (`small`) the sum is
+// one of the row taken 2^-74 times: below 2^(2 (128 - 74)) 2^16 = 2^124 for every finite
+// row of up to 65536 columns. The row's elements themselves are not scaled: those of less
+// than 2^-52 would lose bits. r may then be below the normals, where its rounding is at
+// most 2^-22 of it (r > 2^-128). (rsqrtf: 2 units in the last place.)
+constexpr float kSmall = 0x1p-74f;
 __device__ __forceinline__ float inverse_rms(float sum, float inv_D, float eps, bool small)
 {
-    return rsqrtf(fmaf(sum, inv_D, small ? eps * kSmall * kSmall : eps));
+    const float r = rsqrtf(fmaf(sum, inv_D, small ? eps * kSmall * kSmall : eps));
+    return small ? r * kSmall : r;
 }
 
 // Two binary32 operations in one instruction.
@@ -303,9 +306,8 @@ __global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeAr
             sums = 0;
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
-                va[e] = mul2(va[e], f);
-                vb[e] = mul2(vb[e], f);
-                sums = fma2(vb[e], vb[e], fma2(va[e], va[e], sums));
+                const uint64_t p = mul2(va[e], f), q = mul2(vb[e], f);
+                sums = fma2(q, q, fma2(p, p, sums));
             }
             const float2 again = unpair(sums);
             float x = again.x + again.y;
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRopeA
     }
     const float r = inverse_rms(sum, a.inv_D, a.eps, f != 1.f);
     const auto value = [&](int i) {
-        return to_f(src[i]) * f * r * (w ? to_f(w[i]) + a.weight_offset : 1.f);
+        return to_f(src[i]) * r * (w ? to_f(w[i]) + a.weight_offset : 1.f);
     };
     for (int i = lane; i < a.D - a.rot_dim; i += 32) {
         const int col = i < a.rot_offset ? i : i + a.rot_dim;
