@@ -40,6 +40,13 @@ size_t fork_workspace(int B_old, int B, int table_width, int64_t num_blocks)
            up256((size_t)num_blocks * sizeof(uint32_t));
 }
 
+// Whether x[0, n) and y[0, m) have words in common.
+bool overlap(const int32_t *x, int64_t n, const int32_t *y, int64_t m)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return a < b + (uintptr_t)m * 4 && b < a + (uintptr_t)n * 4;
+}
+
 } // namespace
 
 extern "C" {
@@ -286,12 +293,10 @@ SMLA_API smla_status smla_fork_block_tables(const smla_fork_block_tables_params 
         return SMLA_ERR_WORKSPACE_TOO_SMALL;
     // Rows are read while others are written: the old tables and the new ones are apart.
     if (p->B > 0 && p->B_old > 0) {
-        if (p->blocks_held_out == p->blocks_held)
-            return SMLA_ERR_BAD_SHAPE;
         const int64_t old_end = (p->B_old - 1) * p->table_stride + p->table_width,
                       new_end = (p->B - 1) * p->table_out_stride + p->table_width;
-        const uintptr_t o = reinterpret_cast<uintptr_t>(p->block_table), w = reinterpret_cast<uintptr_t>(p->block_table_out);
-        if (p->table_width > 0 && o < w + (uintptr_t)new_end * 4 && w < o + (uintptr_t)old_end * 4)
+        if (overlap(p->blocks_held, p->B_old, p->blocks_held_out, p->B) ||
+            (p->table_width > 0 && overlap(p->block_table, old_end, p->block_table_out, new_end)))
             return SMLA_ERR_BAD_SHAPE;
     }
     smla::ForkArgs a;

@@ -1,0 +1,39 @@
+"""Arrays that are read while others are written must be apart: refused on the host wherever they meet, not only where they
+begin together (CPU only: the fake addresses are never dereferenced)."""
+import ctypes
+
+import pytest
+
+from sparse_mla_attention_04_gb300 import binding as b
+
+P = 0x100000
+
+
+@pytest.fixture(scope="module")
+def L():
+    from sparse_mla_attention_04_gb300 import build
+    build.build()
+    return b.lib()
+
+
+def _call(fn, structure, base, **kw):
+    a = dict(base, size=ctypes.sizeof(structure))
+    a.update(kw)
+    return fn(ctypes.byref(structure(*[a[n] for n, _ in structure._fields_])))
+
+
+def test_fork_held_counts(L):
+    """Five old rows' counts and four new rows': every place of the new ones that meets the old. Those apart go on to the
+    last check, of the workspace's size."""
+    base = dict(source_rows=P, seq_lens=P, B=4, blocks_held=8 * P, B_old=5, block_table=2 * P, table_stride=8, blocks_held_out=9 * P,
+                block_table_out=3 * P, table_out_stride=8, table_width=8, block_size=64, num_blocks=100, free_ring=4 * P,
+                ring_size=100, ring_state=P, ring_state_out=P, copy_from=5 * P, copy_to=6 * P, counts=7 * P, workspace=10 * P,
+                workspace_bytes=1 << 20, stream=None)
+
+    def call(**kw):
+        return _call(L.smla_fork_block_tables, b.SmlaForkBlockTablesParams, base, **kw)
+
+    for words in range(-8, 10):
+        meets = -4 < words < 5
+        got = call(blocks_held_out=8 * P + 4 * words, workspace_bytes=1 << 20 if meets else 8)
+        assert got == (b.SMLA_ERR_BAD_SHAPE if meets else b.SMLA_ERR_WORKSPACE_TOO_SMALL), words
