@@ -703,7 +703,8 @@ SMLA_API smla_status smla_kv8_tree_attn_fwd(const smla_kv8_tree_attn_params *par
  *              it do not move.
  * seq_lens, query_lens, kept_lens  device, int32 [B]; kept int32 [B, kept_width], row
  *              stride kept_stride.
- * seq_lens_out device, int32 [B], or NULL; none of the other lengths.
+ * seq_lens_out device, int32 [B], or NULL; apart from the other lengths, the lists and
+ *              the tables.
  * pools, scales  arrays on the HOST, [num_pools], of device pointers: 16-byte aligned
  *              (rows as they are: 8), scales 4-byte. Read during the call only. No pool
  *              stands there twice.

@@ -179,9 +179,14 @@ SMLA_API smla_status smla_keep_tokens(const smla_keep_tokens_params *p)
         if (!aligned(p->pools[i], scaled ? 16 : 8) || (scaled && !aligned(p->scales[i], 4)))
             return SMLA_ERR_MISALIGNED;
     }
-    // (the lengths are read by every team of the launch, and written by one)
+    if ((int64_t)p->B * p->heads > INT_MAX / smla::kMostPools)
+        return SMLA_ERR_UNSUPPORTED;
+    // (lengths, lists and tables are read by every team of the launch, the new lengths written by one)
+    const auto meets_out = [&](const int32_t *x, int64_t n) { return overlap(x, n, p->seq_lens_out, p->B); };
     if (p->seq_lens_out != nullptr &&
-        (p->seq_lens_out == p->seq_lens || p->seq_lens_out == p->query_lens || p->seq_lens_out == p->kept_lens))
+        (meets_out(p->seq_lens, p->B) || meets_out(p->query_lens, p->B) || meets_out(p->kept_lens, p->B) ||
+         (p->kept_width > 0 && meets_out(p->kept, (p->B - 1) * p->kept_stride + p->kept_width)) ||
+         (p->table_width > 0 && meets_out(p->block_table, (p->B - 1) * p->table_stride + p->table_width))))
         return SMLA_ERR_BAD_SHAPE;
     smla::KeepArgs a;
     a.block_table = p->block_table;
@@ -199,8 +204,6 @@ SMLA_API smla_status smla_keep_tokens(const smla_keep_tokens_params *p)
     a.block_shift = shift;
     a.row_bytes = p->row_bytes;
     a.num_blocks = p->num_blocks;
-    if ((int64_t)p->B * p->heads > INT_MAX / smla::kMostPools)
-        return SMLA_ERR_UNSUPPORTED;
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms); e != cudaSuccess)
         return cuda_status(e);

@@ -37,3 +37,19 @@ def test_fork_held_counts(L):
         meets = -4 < words < 5
         got = call(blocks_held_out=8 * P + 4 * words, workspace_bytes=1 << 20 if meets else 8)
         assert got == (b.SMLA_ERR_BAD_SHAPE if meets else b.SMLA_ERR_WORKSPACE_TOO_SMALL), words
+
+
+@pytest.mark.parametrize("name", ["seq_lens", "query_lens", "kept_lens", "kept", "block_table"])
+def test_kept_tokens_lengths(L, name):
+    """Three requests: every place of the new lengths that meets an array of theirs. Apart from it the call is fine but for
+    the pool's address, 4 bytes past a multiple of 8."""
+    pools = (ctypes.c_void_p * 1)(20 * P)
+    base = dict(block_table=P, table_stride=6, table_width=4, seq_lens=2 * P, query_lens=3 * P, kept=4 * P, kept_stride=9,
+                kept_width=8, kept_lens=5 * P, seq_lens_out=6 * P, B=3, heads=1, block_size=64, row_bytes=128, num_blocks=10,
+                num_pools=1, pools=ctypes.addressof(pools), scales=None, stream=None)
+    words = {"kept": 2 * 9 + 8, "block_table": 2 * 6 + 4}.get(name, 3)
+    for at in range(-6, words + 4):
+        meets = -3 < at < words
+        pools[0] = 20 * P + (0 if meets else 4)
+        got = _call(L.smla_keep_tokens, b.SmlaKeepTokensParams, base, seq_lens_out=base[name] + 4 * at)
+        assert got == (b.SMLA_ERR_BAD_SHAPE if meets else b.SMLA_ERR_MISALIGNED), at
