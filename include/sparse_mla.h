@@ -706,8 +706,8 @@ SMLA_API smla_status smla_kv8_tree_attn_fwd(const smla_kv8_tree_attn_params *par
  * seq_lens_out device, int32 [B], or NULL; apart from the other lengths, the lists and
  *              the tables.
  * pools, scales  arrays on the HOST, [num_pools], of device pointers: 16-byte aligned
- *              (rows as they are: 8), scales 4-byte. Read during the call only. No pool
- *              stands there twice.
+ *              (rows as they are: 8), scales 4-byte. Read during the call only. No two
+ *              of the pools and scales share memory.
  * B * heads below 2^24, table_width * block_size at most 2^30.
  */
 typedef struct smla_keep_tokens_params {

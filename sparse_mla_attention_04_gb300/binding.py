@@ -1187,11 +1187,21 @@ def smla_kv8_tree_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                      window, sinks, out, lse, return_lse, workspace, stream, tree_mask, positions)
 
 
+def _meet(ranges) -> bool:
+    """Whether two of the (address, bytes) have a byte in common."""
+    end = 0
+    for at, size in sorted(r for r in ranges if r[1] > 0):
+        if at < end:
+            return True
+        end = at + size
+    return False
+
+
 class TokenPools:
     """The caches of all layers for smla_keep_tokens, looked at once (an engine's
     caches live as long as it does). caches: block-scaled caches (k_cache, v_cache,
     k_scale, v_scale), all of one shape; or latent pools [num_slots, D] of one shape
-    and type, then with block_size."""
+    and type, then with block_size. No two of their tensors may share memory."""
 
     __slots__ = ("tensors", "device", "heads", "block_size", "row_bytes", "num_blocks", "count", "pools", "scales")
 
@@ -1230,8 +1240,8 @@ class TokenPools:
             self.num_blocks, self.heads, self.block_size, self.row_bytes = shape
             if block_size is not None and block_size != self.block_size:
                 raise ValueError("block_size is %d, the caches' %d" % (block_size, self.block_size))
-        if len({x.data_ptr() for x in codes}) != len(codes) and self.num_blocks > 0:
-            raise ValueError("a pool stands twice among the caches (its rows would move twice)")
+        if _meet((x.data_ptr(), x.numel() * x.element_size()) for x in codes + (scales or [])):
+            raise ValueError("pools or scales share memory (a row would move twice, or a scale grow twice)")
         self.tensors = (codes, scales)
         self.count = len(codes)
         self.pools = (_c.c_void_p * self.count)(*[x.data_ptr() for x in codes])

@@ -53,3 +53,10 @@ def test_kept_tokens_lengths(L, name):
         pools[0] = 20 * P + (0 if meets else 4)
         got = _call(L.smla_keep_tokens, b.SmlaKeepTokensParams, base, seq_lens_out=base[name] + 4 * at)
         assert got == (b.SMLA_ERR_BAD_SHAPE if meets else b.SMLA_ERR_MISALIGNED), at
+
+
+def test_memory_that_meets():
+    for apart in ([], [(5, 3)], [(8, 4), (0, 8), (12, 1)], [(3, 0), (0, 8), (3, 0), (8, 0), (8, 2)], [(1 << 60, 5), (7, (1 << 60) - 7)]):
+        assert not b._meet(apart), apart
+    for meet in ([(0, 8), (0, 8)], [(8, 4), (0, 9)], [(0, 100), (200, 5), (40, 2)], [(5, 1), (0, 6)], [(0, 10), (2, 2), (11, 3), (13, 9)]):
+        assert b._meet(meet), meet
