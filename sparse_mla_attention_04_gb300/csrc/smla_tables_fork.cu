@@ -25,10 +25,6 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kLanes = 32, kUnit = kForkUnit, kPer = kUnit / kLanes;
-// Up to this many entries of the old and new rows one block does it all, without the launches of the phases:
-// 264 entries 6.6 us by one block and 9.5 by launches, 4000 7.7 and 10.9, 16000 12.5 and 11.1, 131584 (256 old and 256
-// new rows of 257) 114 and 11.9. (A cluster of eight blocks: 9.6, 11.0, 13.6, 23.)
-constexpr int64_t kOneBlockEntries = 8192;
 
 // A new row: the old one that it goes on from (-1: none), what it keeps.
 struct NewRow {
@@ -346,11 +342,11 @@ __global__ void __launch_bounds__(kThreads) fork_count_kernel(const ForkArgs a)
 
 cudaError_t launch_fork_tables(const ForkArgs &a, int sm_count, cudaStream_t stream)
 {
-    if ((int64_t)(a.B + a.B_old) * std::max(a.table_width, 1) <= kOneBlockEntries) {
+    if (fork_by_one_block(a.B_old, a.B, a.table_width)) {
         fork_one_kernel<<<1, kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    const int64_t units = (int64_t)(a.B + a.B_old) * std::max(1, (a.table_width + kUnit - 1) / kUnit);
+    const int64_t units = ((int64_t)a.B + a.B_old) * std::max(1, (a.table_width + kUnit - 1) / kUnit);
     const unsigned blocks = (unsigned)std::min<int64_t>((units + 7) / 8, (int64_t)std::max(sm_count, 1) * 8);
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
