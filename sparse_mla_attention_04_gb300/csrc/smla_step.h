@@ -152,13 +152,19 @@ cudaError_t launch_copy_blocks(const CopyArgs &a, int sm_count, cudaStream_t str
 
 // Forked block tables, validated by the ABI layer.
 constexpr int kForkUnit = 256; // entries of a row that a warp takes
-// Up to this many entries of the old and new rows one block does it all, without the launches of the phases:
-// 264 entries 6.6 us by one block and 9.5 by launches, 4000 7.7 and 10.9, 16000 12.5 and 11.1, 131584 (256 old and 256
-// new rows of 257) 114 and 11.9. (A cluster of eight blocks: 9.6, 11.0, 13.6, 23.)
-constexpr int64_t kForkOneBlockEntries = 8192;
+// Units of the old and new rows: at least one to a row, however narrow.
+constexpr int64_t fork_units(int64_t rows, int table_width)
+{
+    return rows * (table_width > kForkUnit ? ((int64_t)table_width + kForkUnit - 1) / kForkUnit : 1);
+}
+// Up to this many units one block does it all, a warp to a unit, without the launches of the phases: its rounds of 32 units
+// take 3 us each, the launches as good as nothing. By one block and by launches, rows being old and new ones together: 5 rows
+// of 32 entries 6.5 us and 9.9, 32 of 8 7.6 and 10.4, 2 of 4000 15.6 and 14.6; 64 of 2 10.2 and 10.7, 64 of 100 14.9 and 12.4,
+// 128 of 8 15.6 and 10.4, 512 of 8 48 and 10.9, 2000 of 2 175 and 13.5. (A cluster of eight blocks: 264 entries 9.6, 4000 11.0.)
+constexpr int64_t kForkOneBlockUnits = 32;
 constexpr bool fork_by_one_block(int B_old, int B, int table_width)
 {
-    return ((int64_t)B + B_old) * (table_width > 1 ? table_width : 1) <= kForkOneBlockEntries;
+    return fork_units((int64_t)B + B_old, table_width) <= kForkOneBlockUnits;
 }
 struct ForkArgs {
     const int32_t *source_rows, *seq_lens; // [B]

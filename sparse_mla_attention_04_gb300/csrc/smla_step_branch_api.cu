@@ -15,13 +15,6 @@ using smla::cuda_status;
 using smla::current_sm_count;
 using smla::up256;
 
-// Units of an old row (see kForkUnit).
-int64_t fork_units(int B_old, int table_width)
-{
-    const int64_t units = ((int64_t)table_width + smla::kForkUnit - 1) / smla::kForkUnit;
-    return (int64_t)B_old * (units > 0 ? units : 1);
-}
-
 bool fork_sizes(int B_old, int B, int table_width, int64_t num_blocks)
 {
     return B_old >= 0 && B >= 0 && table_width >= 0 && num_blocks >= 0;
@@ -36,7 +29,7 @@ bool fork_supported(int B_old, int B, int table_width, int64_t num_blocks)
 // workspace of smla_fork_block_tables: state, the rows' plans, the units' sums, the marks
 size_t fork_workspace(int B_old, int B, int table_width, int64_t num_blocks)
 {
-    return 256 + up256((size_t)B * sizeof(int4)) + up256((size_t)fork_units(B_old, table_width) * sizeof(int32_t)) +
+    return 256 + up256((size_t)B * sizeof(int4)) + up256((size_t)smla::fork_units(B_old, table_width) * sizeof(int32_t)) +
            up256((size_t)num_blocks * sizeof(uint32_t));
 }
 
@@ -329,7 +322,7 @@ SMLA_API smla_status smla_fork_block_tables(const smla_fork_block_tables_params 
     a.plan = reinterpret_cast<int4 *>(ws);
     ws += up256((size_t)p->B * sizeof(int4));
     a.gives = reinterpret_cast<int32_t *>(ws);
-    ws += up256((size_t)fork_units(p->B_old, p->table_width) * sizeof(int32_t));
+    ws += up256((size_t)smla::fork_units(p->B_old, p->table_width) * sizeof(int32_t));
     a.marks = reinterpret_cast<uint32_t *>(ws);
     int sms = 0;
     if (const cudaError_t e = current_sm_count(&sms); e != cudaSuccess)

@@ -346,7 +346,7 @@ cudaError_t launch_fork_tables(const ForkArgs &a, int sm_count, cudaStream_t str
         fork_one_kernel<<<1, kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    const int64_t units = ((int64_t)a.B + a.B_old) * std::max(1, (a.table_width + kUnit - 1) / kUnit);
+    const int64_t units = fork_units((int64_t)a.B + a.B_old, a.table_width);
     const unsigned blocks = (unsigned)std::min<int64_t>((units + 7) / 8, (int64_t)std::max(sm_count, 1) * 8);
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;

@@ -40,3 +40,11 @@ def test_rows_up_to_the_limits(by_one_block):
     large = [(most, most, 0), (most, most, 1), (most, most - 1, 1), (most, 0, 1), (0, most, 0), (1, 1, most), (7, 5, 100000000)]
     assert by_one_block(*large) == [False] * len(large)
     assert by_one_block((0, 0, 0), (1, 4, 8), (0, 3, 4), (3, 0, 4), (1, 1, 1)) == [True] * 5
+
+
+def test_a_row_is_a_unit_however_narrow(by_one_block):
+    """One block has 32 warps, a unit of up to 256 entries of one row to each: more units than that go to the phases."""
+    for few in ((16, 16, 256), (1, 31, 1), (31, 1, 0), (1, 1, 4096), (1, 4, 600), (3, 5, 700)):
+        assert by_one_block(few) == [True], few
+    for many in ((16, 17, 1), (16, 16, 257), (256, 256, 2), (1000, 1000, 2), (4000, 4000, 1), (1, 1, 4097), (64, 64, 8)):
+        assert by_one_block(many) == [False], many
