@@ -820,10 +820,11 @@ SMLA_API smla_status smla_copy_blocks(void *const *pools, const int64_t *block_b
  * arithmetic, frees its tensor memory and returns, leaving the context usable.
  * smla_fused_qk_rope_cache, smla_rope and smla_qk_norm_rope set 4 for a position
  * outside [0, max_position); smla_fused_qk_rope_cache and smla_kv8_append set 8 for a
- * slot past the pool; smla_build_tree_masks and smla_keep_tokens set 16 for trees and
- * lists of kept tokens that are none. The waits of smla_kv8_attn_fwd and
- * smla_kv8_tree_attn_fwd for their copies and products have the same limit and bits. Synchronous (copies the word from the device):
- * unlike every other entry point it waits for the device, since the word is
+ * slot past the pool; smla_build_tree_masks and smla_keep_tokens both set 16, for trees
+ * and for lists of kept tokens that are none (a caller that has to tell them apart reads
+ * the word between the two). The waits of smla_kv8_attn_fwd and smla_kv8_tree_attn_fwd
+ * for their copies and products have the same limit and bits as the forward's.
+ * Synchronous (copies the word from the device): unlike every other entry point it waits for the device, since the word is
  * read on the host. reset != 0 clears it.
  */
 SMLA_API smla_status smla_device_error(int *code, int reset);
