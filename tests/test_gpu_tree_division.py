@@ -56,3 +56,11 @@ def test_long_contexts(H, hk, D, ql, window):
     _check(p, mask, got, pos if window else None, window)
     again = _run(p, mask, pos if window else None, window)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("H,D,ql,kind", [(1, 64, [1000, 3], "tree"), (1, 128, [1024], "any"), (2, 64, [513, 64], "chain")])
+def test_the_largest_trees(H, D, ql, kind):
+    """Masks of up to sixteen words, trees that span many tiles of positions."""
+    p = _problem(H, 1, D, 16, [n + 90 for n in ql], ql, seed=ql[0])
+    mask, _ = _trees(p, ql, 5, kind=kind)
+    _check(p, mask, _run(p, mask))
